@@ -12,6 +12,8 @@ Entry points (same names as the C ABI):
 * ``msa_bwd(shape, Q, K, V, O, dO, LSE, q_idx, k_idx, block_idx, kl_weight,
   dQ, dK, dV, dq_idx, dk_idx, KL, workspace, stream=None)``
 * ``msa_workspace_size(shape, which)``, ``msa_check_device_status(workspace, stream)``
+* serving, over a ``PagedCache``: ``msa_paged_append``, ``msa_paged_sparse_attn``,
+  ``msa_paged_dense_attn`` (see ``paged.py``)
 
 Tensors are torch CUDA tensors (bf16 / int32 / fp32, contiguous, layouts as
 in the header) or raw device addresses (int). ``stream`` is a
@@ -29,12 +31,14 @@ LIB_PATH = os.path.join(_HERE, "libmsa_gb300.so")
 
 MSA_OK, MSA_ERR_INVALID_ARG, MSA_ERR_UNSUPPORTED, MSA_ERR_WORKSPACE, MSA_ERR_CUDA, MSA_ERR_DEVICE = range(6)
 MSA_WS_TOPK, MSA_WS_FWD, MSA_WS_BWD, MSA_WS_TOPK_FP8, MSA_WS_DENSE = 0, 1, 2, 3, 4
+MSA_WS_PAGED_APPEND, MSA_WS_PAGED_SPARSE, MSA_WS_PAGED_DENSE = 0, 1, 2
 MSA_TIME_INDEX_TOPK, MSA_TIME_SPARSE_FWD, MSA_TIME_BWD, MSA_TIME_DENSE_FWD, MSA_TIME_DENSE_BWD = 0, 1, 2, 3, 4
 
 EXPORTED = ("msa_workspace_size", "msa_index_topk", "msa_sparse_fwd", "msa_bwd", "msa_last_error",
             "msa_check_device_status", "msa_selftest_wait_timeout", "msa_kernel_launches", "msa_version",
             "msa_index_topk_noalloc", "msa_index_topk_fp8", "msa_block_map", "msa_sparse_fwd_mapped", "msa_bwd_mapped",
-            "msa_warmup_block_idx", "msa_set_timing_events", "msa_dense_fwd", "msa_dense_bwd")
+            "msa_warmup_block_idx", "msa_set_timing_events", "msa_dense_fwd", "msa_dense_bwd",
+            "msa_paged_workspace_size", "msa_paged_append", "msa_paged_sparse_attn", "msa_paged_dense_attn")
 
 
 class MsaError(RuntimeError):
@@ -106,6 +110,14 @@ def load_library():
     lib.msa_dense_fwd.restype = ctypes.c_int
     lib.msa_dense_bwd.argtypes = [S, P, P, P, P, P, P, P, P, ctypes.c_float, P, P, P, P, P, P, P, ctypes.c_size_t, P]
     lib.msa_dense_bwd.restype = ctypes.c_int
+    R = ctypes.c_void_p  # the paged calls' structs, by address
+    lib.msa_paged_workspace_size.argtypes = [R, ctypes.c_int]
+    lib.msa_paged_workspace_size.restype = ctypes.c_size_t
+    lib.msa_paged_append.argtypes = [R, R, R, R, P, P, P, ctypes.c_size_t, P]
+    lib.msa_paged_sparse_attn.argtypes = [R, R, P, P, P, P, P, P, ctypes.c_size_t, P]
+    lib.msa_paged_dense_attn.argtypes = [R, R, P, P, P, P, ctypes.c_size_t, P]
+    for f in (lib.msa_paged_append, lib.msa_paged_sparse_attn, lib.msa_paged_dense_attn):
+        f.restype = ctypes.c_int
     lib.msa_selftest_wait_timeout.argtypes = [P, ctypes.c_int32, P]
     lib.msa_selftest_wait_timeout.restype = ctypes.c_int
     _lib = lib
@@ -333,3 +345,7 @@ def dense_bwd(shape: Shape, Q, K, V, O, dO, LSE, q_idx, k_idx, kl_weight=1.0, wo
     msa_dense_bwd(shape, Q, K, V, O, dO, LSE, q_idx, k_idx, kl_weight, out["dQ"], out["dK"], out["dV"],
                   out["dq_idx"], out["dk_idx"], out["KL"], ws, stream)
     return out
+
+
+from .paged import (PagedCache, PagedShape, Rope, alloc_paged_workspace, msa_paged_append, msa_paged_dense_attn,  # noqa: E402,F401
+                    msa_paged_sparse_attn, msa_paged_workspace_size, paged_append, paged_dense_attn, paged_sparse_attn)

@@ -15,7 +15,7 @@ namespace msa {
 
 static thread_local char g_err[512];
 
-static msa_status fail(msa_status s, const char* fmt, ...) {
+msa_status fail(msa_status s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(g_err, sizeof g_err, fmt, ap);
@@ -211,7 +211,7 @@ static msa_status check_topk_k(const Prob& p) {
   return MSA_OK;
 }
 
-static msa_status check_ptr(const void* ptr, const char* name, size_t align) {
+msa_status check_ptr(const void* ptr, const char* name, size_t align) {
   if (!ptr) return fail(MSA_ERR_INVALID_ARG, "%s is NULL", name);
   if (reinterpret_cast<uintptr_t>(ptr) % align)
     return fail(MSA_ERR_INVALID_ARG, "%s is not %zu-byte aligned", name, align);
@@ -227,7 +227,7 @@ static msa_status check_ws(const Prob& p, int which, void* ws, size_t bytes, WsL
   return MSA_OK;
 }
 
-static msa_status check_device() {
+msa_status check_device() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return fail(MSA_ERR_UNSUPPORTED, "no CUDA device");
   int major = 0;
@@ -236,7 +236,7 @@ static msa_status check_device() {
   return MSA_OK;
 }
 
-static msa_status cuda_status(cudaError_t e, const char* what) {
+msa_status cuda_status(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return MSA_OK;
   cudaGetLastError();
   return fail(MSA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
@@ -257,7 +257,7 @@ using namespace msa;
 
 extern "C" {
 
-int32_t msa_version(void) { return (1 << 16) | 4; }
+int32_t msa_version(void) { return (1 << 16) | 5; }
 
 int64_t msa_kernel_launches(void) { return g_launches.load(std::memory_order_relaxed); }
 

@@ -132,6 +132,12 @@ cudaError_t launch_bwd_dense(const Prob& p, const void* Q, const void* K, const 
                              float* dQ, float* dK, float* dV, float* dq_idx, float* dk_idx, float* KL, uint8_t* ws,
                              const WsLayout& L, const DenseSchedule& ds, cudaStream_t st);
 
+// Checks shared by the entry points (msa_api.cu).
+msa_status fail(msa_status s, const char* fmt, ...);
+msa_status check_ptr(const void* ptr, const char* name, size_t align);
+msa_status check_device();
+msa_status cuda_status(cudaError_t e, const char* what);
+
 cudaError_t launch_selftest_wait_timeout(int* err, long long limit_ns, cudaStream_t st);
 
 }  // namespace msa

@@ -1,0 +1,76 @@
+// Host-side internals of the paged-cache entry points: the validated batch,
+// the workspace layout, and the launchers.
+#pragma once
+
+#include "msa_internal.h"
+
+namespace msa {
+
+// SMs the work is cut for. A constant, so that a workspace's size does not
+// depend on the machine that asks for it (any SM count runs the same cuts).
+constexpr int kCutSms = 152;
+
+struct PagedProb {
+  int S, N, Hq, G, hg, k;
+  int num_pages, max_blocks, prefix;
+  float scale;
+};
+
+// Workspace regions (byte offsets, 256-aligned) and how the work is cut.
+struct PagedWs {
+  size_t rows = 0;      // int4 [N]  per new row: sequence (-1: none), position, rows of its sequence before it, and from it on
+  size_t pooled = 0;    // fp32 [N, G, max_blocks] block maxima of the index scores
+  size_t amax = 0;      // fp32 [S, max_blocks]    largest |index key| value of a block
+  size_t part_o = 0;    // fp32 [pslots + splits, N, Hq, d] partial outputs (normalised)
+  size_t part_lse = 0;  // fp32 [pslots + splits, N, Hq]    their log2-sum-exp2
+  size_t total = 256;
+  int splits = 1;       // partials a row's own pages are cut into ...
+  int per_split = 1;    // ... of this many pages
+  int tile_rows = 1;    // new rows of one sequence that share the key tiles (mma.sync path)
+  int pairs = 0;        // shared prefix: pairs of 128-row query tiles
+  int teams = 0;        // shared prefix: runs of pages, each walked by `pairs` CTAs
+  int pslots = 0;       // shared prefix: partials per row
+};
+
+PagedWs paged_ws_layout(const PagedProb& p, int which);
+
+// Units (group, page) of the shared prefix, cut into `teams` runs of nearly
+// equal length: run j holds [j U / teams, (j + 1) U / teams).
+__host__ __device__ inline int team_start(int j, int units, int teams) { return (int)((long long)j * units / teams); }
+__host__ __device__ inline int team_of(int u, int units, int teams) {
+  return (int)((((long long)u + 1) * teams - 1) / units);
+}
+
+struct PagedCachePtrs {
+  void *K, *V, *k_idx;
+  const int32_t *page_table, *row_start, *seq_len;
+};
+
+struct RopeRows {
+  const void *Q, *K, *V, *q_idx, *k_idx;
+  long long ld_Q, ld_K, ld_V, ld_q_idx, ld_k_idx;  // elements between consecutive rows
+  void *Q_out, *q_idx_out;
+  const float *inv_freq, *inv_freq_idx;
+  int rot, rot_idx, interleaved;
+};
+
+cudaError_t launch_paged_append(const PagedProb& p, const PagedCachePtrs& c, const RopeRows& r, uint8_t* ws,
+                                cudaStream_t st);
+// Sequence and position of every new row; checks of the batch description.
+cudaError_t launch_paged_rows(const PagedProb& p, const PagedCachePtrs& c, uint8_t* ws, const PagedWs& L,
+                              cudaStream_t st);
+cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, const void* q_idx, int32_t* block_idx,
+                               uint8_t* ws, const PagedWs& L, cudaStream_t st);
+// Attention of every new row over its selected pages (block_idx) or, with
+// block_idx null, over its sequence's pages behind the shared prefix.
+cudaError_t launch_paged_attn(const PagedProb& p, const PagedCachePtrs& c, const void* Q, const int32_t* block_idx,
+                              void* O, float* LSE, uint8_t* ws, const PagedWs& L, cudaStream_t st);
+cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, const void* Q, uint8_t* ws,
+                                const PagedWs& L, cudaStream_t st);
+cudaError_t launch_paged_merge(const PagedProb& p, const int32_t* block_idx, void* O, float* LSE, uint8_t* ws,
+                               const PagedWs& L, cudaStream_t st);
+
+// Tensor map over a K or V pool as rows of 128 values: box of 64 columns x 128 rows (half a page of one group).
+bool encode_pool_map(CUtensorMap* m, const PagedProb& p, void* pool);
+
+}  // namespace msa

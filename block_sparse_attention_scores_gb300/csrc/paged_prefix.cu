@@ -1,0 +1,360 @@
+// Full attention of a batch's new rows over the pages that all its sequences
+// share: one pass over those pages for the whole batch.
+//
+// The rows of every sequence times the heads of a group fill 128-row tiles
+// (128 / h_g rows each), so the shared part is a matrix product with as many
+// rows as the batch has, whatever the sequences' lengths: tcgen05, two tiles
+// per CTA against each K/V page, which arrives once for both.
+//   S_t = Q_t K^T (TMEM);  P_t = exp2(S_t scale log2 e - m), bf16 over S_t's
+//   columns;  O_t += P_t V (P_t from TMEM, O_t in TMEM)
+// for the tiles t = 0, 1 in turn, so that the tensor core computes one tile's
+// products while the softmax warps of the other work (the scheme of the full
+// causal forward, without masks: every row sees every shared token). P is
+// rounded to bf16 as there: the MMA takes both operands in V's type, and the
+// row sum is taken before the rounding. The running maximum moves only when a
+// page raises it by more than 2^8 (an O_t rescale is a TMEM round trip).
+//
+// Work: all (group, page) pairs in a line, cut into `teams` runs of equal
+// length; a run is walked by `pairs` CTAs at once, one per pair of tiles, so
+// that a page is read from HBM once and from L2 by the others. A run leaves
+// one partial O (fp32, normalised) and log-sum-exp per row and group.
+#include "paged.h"
+#include "sm100.cuh"
+
+namespace msa {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kHeadroom = 8.f;  // P = exp2(s - m) stays <= 2^kHeadroom
+constexpr int kThreads = 320;     // warp 0 TMA, warp 1 UMMA + TMEM, warps 2-5 and 6-9 softmax of tiles 0 and 1
+constexpr int kTile = 32768;      // 128 rows x 128 bf16, two 64-column SW128 chunks
+constexpr int kChunk = 16384;
+constexpr int kStages = 2;        // K/V ring
+constexpr int oQ = 0, oK = 2 * kTile, oV = oK + kStages * kTile;
+constexpr int kSmem = oV + kStages * kTile + 1024;
+
+struct PrefixArgs {
+  const int4* rows;
+  const int32_t* page_table;
+  float *part_o, *part_lse;
+  int N, Hq, G, hg, prefix, pairs, teams, num_pages, max_blocks;
+  float scale_log2;
+  int* err;
+};
+
+struct PrefixShared {
+  uint64_t q_full, q_empty;
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_prefix_kernel(PrefixArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_v) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ PrefixShared sh;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int team = blockIdx.x / a.pairs, pair = blockIdx.x % a.pairs;
+  const int units = a.G * a.prefix;
+  const int u_begin = team_start(team, units, a.teams), u_end = team_start(team + 1, units, a.teams);
+  const int tile_rows = 128 / a.hg;
+  const int ref = __ldg(a.rows).x;  // the first sequence with rows; its table holds the shared pages
+  if (ref < 0) return;              // no rows at all, or the first one was refused
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.o_full[i], 1);
+      mbar_init(&sh.o_free[i], 4);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.v_full[i], 1);
+      mbar_init(&sh.v_empty[i], 1);
+    }
+    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_empty, 1);
+    sh.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sh.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;  // S_0 [0,128), S_1 [128,256), O_0 [256,384), O_1 [384,512)
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer
+    tma_prefetch_desc(&map_q);
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+    uint32_t kc = 0;
+    bool ok = true;
+    int seg = 0;
+    for (int u = u_begin; u < u_end && ok; ++seg) {
+      const int g = u / a.prefix, stop = min(u_end, (g + 1) * a.prefix);
+      if (!mbar_wait(&sh.q_empty, (seg & 1) ^ 1, a.err, 1502)) { ok = false; break; }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sh.q_full, 2 * kTile);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int row0 = (2 * pair + t) * tile_rows;  // rows past N arrive as zeros
+          tma_load_3d(smem + oQ + t * kTile, &map_q, &sh.q_full, 0, g * a.hg, row0);
+          tma_load_3d(smem + oQ + t * kTile + kChunk, &map_q, &sh.q_full, 64, g * a.hg, row0);
+        }
+      }
+      __syncwarp();
+      for (int u0 = u; u0 < stop && ok; u0 += 32) {
+        int page = 0;
+        if (u0 + lane < stop) {
+          page = __ldg(a.page_table + (size_t)ref * a.max_blocks + (u0 + lane - g * a.prefix));
+          if (page < 0 || page >= a.num_pages) {
+            dev_fail(a.err, kDevBadIndex, 1511);
+            page = 0;
+          }
+        }
+        const int here = min(32, stop - u0);
+        for (int i = 0; i < here; ++i, ++kc) {
+          const int st = kc % kStages;
+          const uint32_t par = ((kc / kStages) & 1) ^ 1;
+          const int y = (__shfl_sync(0xffffffffu, page, i) * a.G + g) * 128;
+          if (!mbar_wait(&sh.k_empty[st], par, a.err, 1503)) { ok = false; break; }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sh.k_full[st], kTile);
+            tma_load_2d(smem + oK + st * kTile, &map_k, &sh.k_full[st], 0, y);
+            tma_load_2d(smem + oK + st * kTile + kChunk, &map_k, &sh.k_full[st], 64, y);
+          }
+          __syncwarp();
+          if (!mbar_wait(&sh.v_empty[st], par, a.err, 1504)) { ok = false; break; }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sh.v_full[st], kTile);
+            tma_load_2d(smem + oV + st * kTile, &map_v, &sh.v_full[st], 0, y);
+            tma_load_2d(smem + oV + st * kTile + kChunk, &map_v, &sh.v_full[st], 64, y);
+          }
+          __syncwarp();
+        }
+      }
+      u = stop;
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- UMMA issuer
+    if (lane == 0) {
+      constexpr uint32_t id_s = make_idesc_bf16(128, 128, false, false);  // Q, K both K-major
+      constexpr uint32_t id_o = make_idesc_bf16(128, 128, false, true);   // P from TMEM, V MN-major
+      const uint32_t q0 = smem_u32(smem + oQ);
+      uint32_t kc = 0;
+      bool ok = true;
+      auto issue_s = [&](int t, int st) {
+        const uint32_t qa = q0 + t * kTile, ka = smem_u32(smem + oK + st * kTile);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          const uint32_t off = (ks >> 2) * kChunk + (ks & 3) * 32;
+          umma_bf16_ss(tmem + t * 128, make_sdesc(qa + off, 16, 1024, kSw128), make_sdesc(ka + off, 16, 1024, kSw128),
+                       id_s, ks > 0);
+        }
+        umma_commit(&sh.s_full[t]);
+      };
+      auto issue_o = [&](int t, int st, bool acc) {
+        const uint32_t va = smem_u32(smem + oV + st * kTile);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          umma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + ks * 8, make_sdesc(va + ks * 2048, kChunk, 1024, kSw128),
+                       id_o, acc || ks > 0);
+      };
+      int seg = 0;
+      for (int u = u_begin; u < u_end && ok; ++seg) {
+        const int g = u / a.prefix, stop = min(u_end, (g + 1) * a.prefix), pages = stop - u;
+        if (!mbar_wait(&sh.q_full, seg & 1, a.err, 1512)) { ok = false; break; }
+        {
+          const int st = kc % kStages;
+          if (!mbar_wait(&sh.k_full[st], (kc / kStages) & 1, a.err, 1513)) { ok = false; break; }
+          tc_fence_after();
+          issue_s(0, st);
+          issue_s(1, st);
+          umma_commit(&sh.k_empty[st]);
+          if (pages == 1) umma_commit(&sh.q_empty);
+        }
+        for (int c = 0; c < pages && ok; ++c, ++kc) {
+          const int st = kc % kStages, st1 = (kc + 1) % kStages;
+          const uint32_t par = (kc / kStages) & 1, par1 = ((kc + 1) / kStages) & 1;
+          const bool last = c == pages - 1;
+#pragma unroll 1
+          for (int t = 0; t < 2; ++t) {
+            // P_t of this page written (and O_t rescaled if its row maximum moved)
+            if (!mbar_wait(&sh.p_full[t], kc & 1, a.err, 1514 + t)) { ok = false; break; }
+            if (c == 0 && !mbar_wait(&sh.o_free[t], (seg & 1) ^ 1, a.err, 1516 + t)) { ok = false; break; }
+            if (t == 0 && !mbar_wait(&sh.v_full[st], par, a.err, 1518)) { ok = false; break; }
+            tc_fence_after();
+            issue_o(t, st, c > 0);
+            if (t == 1) umma_commit(&sh.v_empty[st]);
+            if (!last) {
+              // the next page's S_t: after this PV_t in issue order, so it overwrites P_t only once read
+              if (t == 0 && !mbar_wait(&sh.k_full[st1], par1, a.err, 1519)) { ok = false; break; }
+              tc_fence_after();
+              issue_s(t, st1);
+              if (t == 1) {
+                umma_commit(&sh.k_empty[st1]);
+                if (c + 1 == pages - 1) umma_commit(&sh.q_empty);
+              }
+            } else {
+              umma_commit(&sh.o_full[t]);
+            }
+          }
+        }
+        u = stop;
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax (thread = one head of one new row)
+    const int t = (warp - 2) >> 2;
+    const int quarter = warp & 3;
+    const int lrow = quarter * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t s_col = t * 128, o_col = 256 + t * 128;
+    const int row = (2 * pair + t) * tile_rows + lrow / a.hg;
+    uint32_t kc = 0;
+    bool ok = true;
+    int seg = 0;
+    for (int u = u_begin; u < u_end && ok; ++seg) {
+      const int g = u / a.prefix, stop = min(u_end, (g + 1) * a.prefix), pages = stop - u;
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int c = 0; c < pages; ++c, ++kc) {
+        if (!mbar_wait(&sh.s_full[t], kc & 1, a.err, 1522 + t)) { ok = false; break; }
+        tc_fence_after();
+        float sv[128], mq[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          tmem_ld32_max(tmem + lane_off + s_col + z * 32, *reinterpret_cast<float(*)[32]>(sv + 32 * z), mq[z]);
+        tmem_wait_ld();
+        const float m_blk = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * a.scale_log2;
+        const bool need = m_blk > m_run + kHeadroom;
+        if (__any_sync(0xffffffffu, need)) {
+          const float alpha = need ? fast_exp2(m_run - m_blk) : 1.f;
+          if (need) m_run = m_blk;
+          l_run *= alpha;
+          if (c > 0) {
+#pragma unroll 1
+            for (int z = 0; z < 4; ++z) {
+              float o[32];
+              tmem_ld32(tmem + lane_off + o_col + z * 32, o);
+              tmem_wait_ld();
+              uint32_t ob[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) ob[i] = __float_as_uint(o[i] * alpha);
+              tmem_st32(tmem + lane_off + o_col + z * 32, ob);
+            }
+            tmem_wait_st();
+          }
+        }
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int z = 0; z < 32; ++z) {
+            const float p0 = fast_exp2(fmaf(sv[64 * h + 2 * z], a.scale_log2, -m_run));
+            const float p1 = fast_exp2(fmaf(sv[64 * h + 2 * z + 1], a.scale_log2, -m_run));
+            l4[(2 * z) & 3] += p0;
+            l4[(2 * z + 1) & 3] += p1;
+            pk[z] = pack_bf16(p0, p1);
+          }
+          tmem_st32(tmem + lane_off + s_col + 32 * h, pk);
+        }
+        tmem_wait_st();
+        l_run += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[t]);
+      }
+      if (!ok) break;
+      // ---- the run's end in this group: the row's partial
+      if (!mbar_wait(&sh.o_full[t], seg & 1, a.err, 1524 + t)) { ok = false; break; }
+      tc_fence_after();
+      const int slot = team - team_of(g * a.prefix, units, a.teams);
+      const size_t at = ((size_t)slot * a.N + row) * a.Hq + g * a.hg + lrow % a.hg;
+      const float inv = 1.f / l_run;
+      float4* dst = reinterpret_cast<float4*>(a.part_o + at * 128);
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        float o[32];
+        tmem_ld32(tmem + lane_off + o_col + z * 32, o);
+        tmem_wait_ld();
+        if (row < a.N) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[8 * z + i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+        }
+      }
+      if (row < a.N) a.part_lse[at] = m_run + log2f(l_run);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.o_free[t]);
+      u = stop;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, const void* Q, uint8_t* ws,
+                                const PagedWs& L, cudaStream_t st) {
+  CUtensorMap mq, mk, mv;
+  {
+    // a tile's rows times the heads of one group: box {64 d, h_g heads, 128 / h_g rows}
+    const uint64_t dims[3] = {128, (uint64_t)p.Hq, (uint64_t)p.N};
+    const uint64_t strides[2] = {256, (uint64_t)p.Hq * 256};
+    const uint32_t box[3] = {64, (uint32_t)p.hg, (uint32_t)(128 / p.hg)};
+    if (!encode_tmap(&mq, const_cast<void*>(Q), 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
+  if (!encode_pool_map(&mk, p, c.K) || !encode_pool_map(&mv, p, c.V)) return cudaErrorInvalidValue;
+  PrefixArgs a;
+  a.rows = reinterpret_cast<const int4*>(ws + L.rows);
+  a.page_table = c.page_table;
+  a.part_o = reinterpret_cast<float*>(ws + L.part_o);
+  a.part_lse = reinterpret_cast<float*>(ws + L.part_lse);
+  a.N = p.N;
+  a.Hq = p.Hq;
+  a.G = p.G;
+  a.hg = p.hg;
+  a.prefix = p.prefix;
+  a.pairs = L.pairs;
+  a.teams = L.teams;
+  a.num_pages = p.num_pages;
+  a.max_blocks = p.max_blocks;
+  a.scale_log2 = p.scale * kLog2e;
+  a.err = reinterpret_cast<int*>(ws);
+  static bool attr[kMaxDevices] = {};
+  const int dslot = device_slot();
+  if (!attr[dslot]) {
+    cudaError_t e = cudaFuncSetAttribute(paged_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    attr[dslot] = true;
+  }
+  paged_prefix_kernel<<<L.teams * L.pairs, kThreads, kSmem, st>>>(a, mq, mk, mv);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace msa

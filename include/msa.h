@@ -294,6 +294,141 @@ MSA_API msa_status msa_dense_bwd(const msa_shape *shape, const void *Q, const vo
                                  float kl_weight, float *dQ, float *dK, float *dV, float *dq_idx, float *dk_idx,
                                  float *KL, void *workspace, size_t workspace_bytes, msa_stream_t stream);
 
+/*
+ * Serving: the layer's new tokens over a paged cache.
+ *
+ * The method's description stops at training; a model trained with it is
+ * decoded with the three calls below. A page holds one KV block (Bk tokens) of
+ * every group, so the block ids of the selection (itinai.ru "How the indexer
+ * works") are columns of the page table, and a selected block is one
+ * contiguous run of K and of V per group.
+ *
+ * A batch is S sequences with N rows (new tokens) in all, in sequence order:
+ * sequence s has the rows row_start[s] .. row_start[s+1] - 1 (any count, none
+ * included), and row r of it the position
+ *   t = seq_len[s] - (row_start[s+1] - r),
+ * seq_len[s] being the sequence's tokens with its new ones. Rows from
+ * row_start[S] on (a padded batch) are left alone: nothing of theirs is read
+ * into a result, and their outputs stay as they were.
+ *
+ * The batch description (row_start, seq_len, page_table, block_idx) is read on
+ * the device when the kernels run; a call's launches depend on `shape` and on
+ * which pointers are NULL only, so a captured call can be replayed on another
+ * batch of the same shape. Kernels check it: a position outside the page table
+ * (or, with a shared prefix, inside the prefix), a page id outside
+ * [0, num_pages), prefix pages that differ between sequences, or a block list
+ * that is not ascending ids up to the row's own block sets the error word, and
+ * the outputs of the rows concerned (of every row, for the prefix) are
+ * unspecified; nothing is read or written out of range.
+ *
+ * Supported: d = 128, d_idx = 64, Bk = 128, Hq / G in {1, 2, 4, 8},
+ * 1 <= k <= 128, S <= 65535, N <= 2^20 (N * Hq <= 2^28), max_blocks <= 8192
+ * (2^20 tokens), num_pages * G < 2^24. Two calls may run at the same time if
+ * they have workspaces of their own. All results are the same bits in every
+ * run on the same inputs.
+ */
+typedef struct msa_paged_shape {
+  int32_t S;             /* sequences                                            */
+  int32_t N;             /* rows the tensors of new tokens have                  */
+  int32_t Hq;            /* query heads                                          */
+  int32_t G;             /* GQA groups = KV heads = index queries per row        */
+  int32_t d;             /* head dim                                             */
+  int32_t d_idx;         /* index dim                                            */
+  int32_t Bk;            /* tokens per page                                      */
+  int32_t k;             /* blocks kept per (row, group), own block included     */
+  int32_t num_pages;     /* pages of the pools                                   */
+  int32_t max_blocks;    /* columns of the page table                            */
+  int32_t prefix_blocks; /* msa_paged_dense_attn: leading pages that all
+                            sequences share (0: none); ignored by the others     */
+  float scale;           /* softmax scale; <= 0 selects 1/sqrt(d)                */
+} msa_paged_shape;
+
+/* The cache and the batch's description, all in device memory. */
+typedef struct msa_paged_cache {
+  void *K, *V;               /* pools [num_pages, G, Bk, d] bf16                 */
+  void *k_idx;               /* pool  [num_pages, Bk, d_idx] bf16; NULL in a
+                                layer without an index branch of its own         */
+  const int32_t *page_table; /* [S, max_blocks] pages of block 0, 1, ...; columns
+                                past a sequence's last block are not read        */
+  const int32_t *row_start;  /* [S + 1], row_start[0] = 0, non-decreasing        */
+  const int32_t *seq_len;    /* [S]                                              */
+} msa_paged_cache;
+
+/* Which entry point a workspace is sized for. */
+enum { MSA_WS_PAGED_APPEND = 0, MSA_WS_PAGED_SPARSE = 1, MSA_WS_PAGED_DENSE = 2 };
+
+/* Bytes of device workspace the entry point `which` needs for `shape` (0 if
+ * the shape is invalid or unsupported). */
+MSA_API size_t msa_paged_workspace_size(const msa_paged_shape *shape, int which);
+
+/* Position rotation: pair i of a vector at position t turns by the angle
+ * t * inv_freq[i]. The pairs are (i, i + rot_dim / 2), or (2 i, 2 i + 1) with
+ * `interleaved` != 0; values from rot_dim on stay as they are. */
+typedef struct msa_rope {
+  const float *inv_freq;     /* [rot_dim / 2] radians per position (device)      */
+  const float *inv_freq_idx; /* [rot_dim_idx / 2]                                */
+  int32_t rot_dim;           /* of Q and K: a multiple of 16 up to d; 0: none    */
+  int32_t rot_dim_idx;       /* of q_idx and k_idx: a multiple of 16 up to d_idx */
+  int32_t interleaved;
+} msa_rope;
+
+/* New rows as the projections leave them. ld_*: elements between consecutive
+ * rows (0: packed), so the pieces of one fused projection can be given as they
+ * lie; each row is packed, starts on a 16-byte boundary, and ld is a multiple
+ * of 8. */
+typedef struct msa_new_rows {
+  const void *Q;     /* [N, Hq, d] bf16, or NULL with Q_out          */
+  const void *K, *V; /* [N, G, d] bf16                               */
+  const void *q_idx; /* [N, G, d_idx] bf16, or NULL with q_idx_out   */
+  const void *k_idx; /* [N, d_idx] bf16, or NULL                     */
+  int64_t ld_Q, ld_K, ld_V, ld_q_idx, ld_k_idx;
+} msa_new_rows;
+
+/*
+ * Appends new tokens: row r of sequence s, position t, goes to slot t % Bk of
+ * page page_table[s][t / Bk], K and k_idx rotated by their position, V as it
+ * is; Q_out [N, Hq, d] and q_idx_out [N, G, d_idx] (packed) get the rotated
+ * queries. The rotation is computed in fp32 from angles that are exact to fp32
+ * at any position, and rounded once. Q_out may be Q, and q_idx_out q_idx, when
+ * they are packed. A page that receives rows must belong to one sequence.
+ */
+MSA_API msa_status msa_paged_append(const msa_paged_shape *shape, const msa_paged_cache *cache, const msa_rope *rope,
+                                    const msa_new_rows *rows, void *Q_out, void *q_idx_out, void *workspace,
+                                    size_t workspace_bytes, msa_stream_t stream);
+
+/*
+ * The MSA layer for new tokens: msa_index_topk's selection and msa_sparse_fwd's
+ * attention for each row over its sequence's pages, for a row at position t
+ * with own block c_t = t / Bk:
+ *   pool[c] = max_{j in block c} <q_idx[r,g,:], k_idx[j,:]>,  c < c_t,
+ *   block_idx[r,g,:] = {c_t} U top-(k-1) of pool under (score descending, id
+ *     ascending), written in ascending order, then -1;
+ *   s_j = scale <Q[r,h,:], K[j,g,:]> over the tokens j <= t of those blocks,
+ *   LSE = ln sum_j exp(s_j),  O[r,h,:] = sum_j exp(s_j - LSE) V[j,g,:].
+ * The selection is that of the exact scores (blocks that fp32 sums cannot tell
+ * apart are compared in 64 bits); a NaN score counts as -infinity. What lies in
+ * the pages behind a row's position reaches no result.
+ *
+ * Q [N, Hq, d], q_idx [N, G, d_idx] bf16 -> block_idx [N, G, k] int32, O
+ * [N, Hq, d] bf16, LSE [N, Hq] fp32. With q_idx NULL the layer reuses a
+ * selection (IndexShare): block_idx is read, not written, and may come from
+ * anywhere; a row whose list is empty (all -1) gives O = 0, LSE = -infinity.
+ */
+MSA_API msa_status msa_paged_sparse_attn(const msa_paged_shape *shape, const msa_paged_cache *cache, const void *Q,
+                                         const void *q_idx, int32_t *block_idx, void *O, float *LSE, void *workspace,
+                                         size_t workspace_bytes, msa_stream_t stream);
+
+/*
+ * Full attention for new tokens (msa_dense_fwd's result for each row, over all
+ * tokens j <= t): the layers and training stages without a selection. The
+ * first shape->prefix_blocks pages of every sequence must be the same (a
+ * prompt that the batch shares); they are read once for the whole batch, and
+ * every row's position must lie behind them. prefix_blocks = 0 shares nothing.
+ */
+MSA_API msa_status msa_paged_dense_attn(const msa_paged_shape *shape, const msa_paged_cache *cache, const void *Q,
+                                        void *O, float *LSE, void *workspace, size_t workspace_bytes,
+                                        msa_stream_t stream);
+
 /* Message describing the last non-OK status returned on this thread. */
 MSA_API const char *msa_last_error(void);
 

@@ -1,0 +1,195 @@
+"""The paged-cache calls check their arguments before any device work (no GPU needed)."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def msa():
+    import __graft_entry__
+
+    __graft_entry__.build_library()
+    import block_sparse_attention_scores_gb300 as m
+
+    return m
+
+
+BASE = dict(S=2, N=3, Hq=8, G=2, num_pages=10, max_blocks=4, k=4)
+P = 4096  # an aligned address that is never followed: every case here is refused on the host
+
+
+def _shape(msa, **kw):
+    return msa.PagedShape(**{**BASE, **kw})
+
+
+def _cache(msa, **kw):
+    from block_sparse_attention_scores_gb300.paged import MsaPagedCache
+
+    return MsaPagedCache(**{**dict(K=P, V=P, k_idx=P, page_table=P, row_start=P, seq_len=P), **kw})
+
+
+def _rope(msa, **kw):
+    from block_sparse_attention_scores_gb300.paged import MsaRope
+
+    return MsaRope(**{**dict(inv_freq=P, inv_freq_idx=P, rot_dim=128, rot_dim_idx=64, interleaved=0), **kw})
+
+
+def _rows(msa, **kw):
+    from block_sparse_attention_scores_gb300.paged import MsaNewRows
+
+    return MsaNewRows(**{**dict(Q=P, K=P, V=P, q_idx=P, k_idx=P), **kw})
+
+
+def _status(msa, f):
+    with pytest.raises(msa.MsaError) as e:
+        msa._check(f())
+    return e.value.status, str(e.value)
+
+
+def _append(msa, shape=None, cache=None, rope=None, rows=None, Q_out=P, q_idx_out=P, ws=P, n=1 << 40):
+    lib, a = msa.load_library(), ctypes.addressof
+    shape, cache = shape or _shape(msa).c(), cache or _cache(msa)
+    rope, rows = rope or _rope(msa), rows or _rows(msa)
+    return _status(msa, lambda: lib.msa_paged_append(a(shape), a(cache), a(rope), a(rows), Q_out, q_idx_out, ws, n, 0))
+
+
+def _sparse(msa, shape=None, cache=None, Q=P, q_idx=P, block_idx=P, O=P, LSE=P, ws=P, n=1 << 40):
+    lib, a = msa.load_library(), ctypes.addressof
+    shape, cache = shape or _shape(msa).c(), cache or _cache(msa)
+    return _status(msa, lambda: lib.msa_paged_sparse_attn(a(shape), a(cache), Q, q_idx, block_idx, O, LSE, ws, n, 0))
+
+
+def _dense(msa, shape=None, cache=None, Q=P, O=P, LSE=P, ws=P, n=1 << 40):
+    lib, a = msa.load_library(), ctypes.addressof
+    shape, cache = shape or _shape(msa).c(), cache or _cache(msa)
+    return _status(msa, lambda: lib.msa_paged_dense_attn(a(shape), a(cache), Q, O, LSE, ws, n, 0))
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(S=0), "INVALID_ARG"), (dict(N=0), "INVALID_ARG"), (dict(Hq=0), "INVALID_ARG"), (dict(G=0), "INVALID_ARG"),
+    (dict(k=0), "INVALID_ARG"), (dict(num_pages=0), "INVALID_ARG"), (dict(max_blocks=0), "INVALID_ARG"),
+    (dict(prefix_blocks=-1), "INVALID_ARG"), (dict(prefix_blocks=4), "INVALID_ARG"), (dict(Hq=7), "INVALID_ARG"),
+    (dict(scale=float("inf")), "INVALID_ARG"), (dict(d=64), "UNSUPPORTED"), (dict(d_idx=32), "UNSUPPORTED"),
+    (dict(Bk=64), "UNSUPPORTED"), (dict(Hq=32), "UNSUPPORTED"), (dict(Hq=6), "UNSUPPORTED"),
+    (dict(k=129), "UNSUPPORTED"), (dict(S=65536), "UNSUPPORTED"), (dict(max_blocks=8193), "UNSUPPORTED"),
+    (dict(N=(1 << 20) + 1), "UNSUPPORTED"), (dict(num_pages=1 << 23), "UNSUPPORTED"),
+    (dict(N=1 << 20, Hq=1024, G=128), "UNSUPPORTED"),
+])
+def test_shapes_outside_the_contract(msa, kw, status):
+    s = _shape(msa, **kw)
+    want = getattr(msa, "MSA_ERR_" + status)
+    for which in (msa.MSA_WS_PAGED_APPEND, msa.MSA_WS_PAGED_SPARSE, msa.MSA_WS_PAGED_DENSE):
+        assert msa.msa_paged_workspace_size(s, which) == 0
+    assert _append(msa, shape=s.c())[0] == want
+    assert _sparse(msa, shape=s.c())[0] == want
+    assert _dense(msa, shape=s.c())[0] == want
+
+
+def test_workspace_sizes(msa):
+    s = _shape(msa)
+    sizes = [msa.msa_paged_workspace_size(s, w) for w in range(3)]
+    assert sizes[0] == 256 and sizes[1] > 256 and sizes[2] > 256
+    assert msa.msa_paged_workspace_size(s, 3) == 0 and msa.msa_paged_workspace_size(s, -1) == 0
+    # the prefix belongs to the dense call alone
+    p = _shape(msa, prefix_blocks=3)
+    assert msa.msa_paged_workspace_size(p, msa.MSA_WS_PAGED_SPARSE) == sizes[1]
+    # the scores of every row and block
+    big = _shape(msa, N=64, max_blocks=8192, num_pages=1 << 20, G=8, Hq=32)
+    assert msa.msa_paged_workspace_size(big, msa.MSA_WS_PAGED_SPARSE) > 64 * 8 * 8192 * 4
+
+
+@pytest.mark.parametrize("name", ["K", "V", "page_table", "row_start", "seq_len"])
+def test_cache_pointers(msa, name):
+    for bad, what in ((None, "NULL"), (P + 2, "aligned")):
+        c = _cache(msa, **{name: bad})
+        for call in (_append, _sparse, _dense):
+            st, msg = call(msa, cache=c)
+            assert st == msa.MSA_ERR_INVALID_ARG and name in msg and what in msg
+
+
+def test_index_keys_are_needed_with_an_index_branch_only(msa):
+    c = _cache(msa, k_idx=None)
+    assert "k_idx" in _sparse(msa, cache=c)[1]
+    assert "k_idx" in _append(msa, cache=c)[1]
+    assert _sparse(msa, cache=c, q_idx=None, ws=None)[0] == msa.MSA_ERR_WORKSPACE  # past the pointer checks
+    assert _append(msa, cache=c, rows=_rows(msa, k_idx=None), ws=None)[0] == msa.MSA_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("name", ["Q", "block_idx", "O", "LSE"])
+def test_sparse_pointers(msa, name):
+    st, msg = _sparse(msa, **{name: None})
+    assert st == msa.MSA_ERR_INVALID_ARG and name in msg
+    st, msg = _sparse(msa, **{name: P + 1})
+    assert st == msa.MSA_ERR_INVALID_ARG and "aligned" in msg
+    if name != "block_idx":
+        assert name in _dense(msa, **{name: None})[1]
+
+
+def test_append_arguments(msa):
+    inv = msa.MSA_ERR_INVALID_ARG
+    for name in ("K", "V"):
+        st, msg = _append(msa, rows=_rows(msa, **{name: None}))
+        assert st == inv and name in msg
+    for name in ("Q", "K", "V", "q_idx", "k_idx"):
+        assert "aligned" in _append(msa, rows=_rows(msa, **{name: P + 8}))[1]
+        for ld in (8, 2052, -2048):  # shorter than a row, not a multiple of 16 bytes, negative
+            if name == "k_idx" and ld == 8:
+                ld = 56
+            st, msg = _append(msa, rows=_rows(msa, **{"ld_" + name: ld}))
+            assert st == inv and "stride of " + name in msg
+    # an input and its output come together
+    assert "Q_out" in _append(msa, Q_out=None)[1]
+    assert "Q_out" in _append(msa, rows=_rows(msa, Q=None))[1]
+    assert "q_idx_out" in _append(msa, q_idx_out=None)[1]
+    assert "q_idx_out" in _append(msa, rows=_rows(msa, q_idx=None))[1]
+    for kw in (dict(rot_dim=144), dict(rot_dim=-16), dict(rot_dim=24), dict(rot_dim_idx=80), dict(rot_dim_idx=8)):
+        st, msg = _append(msa, rope=_rope(msa, **kw))
+        assert st == inv and "rot_dim" in msg
+    assert "inv_freq " in _append(msa, rope=_rope(msa, inv_freq=None))[1]
+    assert "inv_freq_idx" in _append(msa, rope=_rope(msa, inv_freq_idx=None))[1]
+    # no index vectors: their rotation is not looked at
+    r = _rows(msa, q_idx=None, k_idx=None)
+    assert _append(msa, rope=_rope(msa, inv_freq_idx=None, rot_dim_idx=8), rows=r, q_idx_out=None, ws=None)[0] == \
+        msa.MSA_ERR_WORKSPACE
+
+
+def test_null_structs(msa):
+    lib, a = msa.load_library(), ctypes.addressof
+    s, c, r, n = _shape(msa).c(), _cache(msa), _rope(msa), _rows(msa)
+    for args in ((None, a(c), a(r), a(n)), (a(s), None, a(r), a(n)), (a(s), a(c), None, a(n)), (a(s), a(c), a(r), None)):
+        assert _status(msa, lambda: lib.msa_paged_append(*args, P, P, P, 1 << 20, 0))[0] == msa.MSA_ERR_INVALID_ARG
+    assert _status(msa, lambda: lib.msa_paged_sparse_attn(a(s), None, P, P, P, P, P, P, 1 << 20, 0))[0] == \
+        msa.MSA_ERR_INVALID_ARG
+    assert _status(msa, lambda: lib.msa_paged_dense_attn(None, a(c), P, P, P, P, 1 << 20, 0))[0] == \
+        msa.MSA_ERR_INVALID_ARG
+
+
+def test_workspace_is_checked(msa):
+    for call in (_append, _sparse, _dense):
+        assert call(msa, ws=None)[0] == msa.MSA_ERR_WORKSPACE
+        assert "aligned" in call(msa, ws=P + 128)[1]
+        st, msg = call(msa, n=255)
+        assert st == msa.MSA_ERR_WORKSPACE and "needed" in msg
+
+
+def test_binding_refuses_tensors_of_another_kind(msa):
+    import torch
+
+    from block_sparse_attention_scores_gb300.paged import _rows as rows
+
+    with pytest.raises(ValueError, match="GPU"):
+        msa.PagedCache(*[torch.zeros(2, 2, 128, 128, dtype=torch.bfloat16)] * 2, None,
+                       torch.zeros(2, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32),
+                       torch.zeros(2, dtype=torch.int32))
+    cpu = torch.device("cpu")
+    x = torch.zeros(3, 2, 128, dtype=torch.bfloat16)
+    assert rows("K", x, (3, 2, 128), cpu)[1] == 256
+    fused = torch.zeros(3, 640, dtype=torch.bfloat16)[:, 128:384].unflatten(1, (2, 128))
+    assert rows("K", fused, (3, 2, 128), cpu)[1] == 640
+    with pytest.raises(ValueError, match="packed"):
+        rows("K", torch.zeros(2, 3, 128, dtype=torch.bfloat16).transpose(0, 1), (3, 2, 128), cpu)[1] and rows(
+            "K", torch.zeros(3, 128, 2, dtype=torch.bfloat16).transpose(1, 2), (3, 2, 128), cpu)
+    with pytest.raises(ValueError, match="shape"):
+        rows("K", x, (3, 4, 128), cpu)
+    with pytest.raises(ValueError, match="bfloat16"):
+        rows("K", x.float(), (3, 2, 128), cpu)

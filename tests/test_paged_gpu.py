@@ -1,0 +1,540 @@
+"""The paged-cache operators on the GPU against their 64-bit forms (tests/paged_ref.py, bounds derived there)."""
+import math
+
+import numpy as np
+import pytest
+
+import paged_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def msa():
+    import __graft_entry__
+
+    __graft_entry__.build_library()
+    import block_sparse_attention_scores_gb300 as m
+
+    return m
+
+
+def _freq(rot, base=500000.0):
+    import torch
+
+    return 1.0 / base ** (torch.arange(0, rot, 2, dtype=torch.float32) / max(rot, 1))
+
+
+# ----------------------------------------------------------------- append
+APPEND = {
+    "one": dict(counts=[1], lens=[1], Hq=8, G=2, rot=128, rot_idx=64),
+    "page_ends": dict(counts=[1, 1, 1, 2, 128, 129, 3], lens=[127, 128, 129, 129, 256, 300, 3], Hq=4, G=4, rot=64, rot_idx=32),
+    "idle_and_padding": dict(counts=[0, 5, 0, 0, 1, 0], lens=[7, 133, 0, 128, 500, 64], pad=3, Hq=16, G=2, rot=128, rot_idx=64),
+    "interleaved": dict(counts=[3, 130], lens=[1000, 130], Hq=8, G=1, rot=128, rot_idx=64, interleaved=True),
+    "partial_interleaved": dict(counts=[9], lens=[200], Hq=6, G=3, rot=48, rot_idx=16, interleaved=True),
+    "partial_strided": dict(counts=[9, 4], lens=[200, 77], Hq=6, G=3, rot=96, rot_idx=48, fused=True),
+    "no_rotation": dict(counts=[6], lens=[6], Hq=2, G=2, rot=0, rot_idx=0, fused=True),
+    "no_index": dict(counts=[2, 2], lens=[140, 129], Hq=64, G=8, rot=128, rot_idx=0, index=False),
+    "many_sequences": dict(counts=[1] * 70, lens=list(range(1, 141, 2)), Hq=2, G=1, rot=32, rot_idx=64),
+    "in_place": dict(counts=[5], lens=[5], Hq=8, G=2, rot=128, rot_idx=64, in_place=True),
+}
+
+
+@pytest.mark.parametrize("name", APPEND)
+def test_append(msa, name):
+    import torch
+
+    kw = dict(APPEND[name])
+    rot, rot_idx, how = kw.pop("rot"), kw.pop("rot_idx"), kw.pop("interleaved", False)
+    fused, in_place = kw.pop("fused", False), kw.pop("in_place", False)
+    b = ref.Batch(stale=7.0, **kw)
+    shape, cache, t = b.gpu()
+    index = b.k_idx is not None
+    gen = torch.Generator().manual_seed(5)
+    widths = [b.Hq * 128, b.G * 128, b.G * 128] + ([b.G * 64, 64] if index else [])
+    lines = torch.randn(b.N, sum(widths) + 8, generator=gen).to(torch.bfloat16).cuda()[:, :sum(widths)]
+    parts = list(lines.split(widths, dim=1)) if fused else [x.contiguous() for x in lines.split(widths, dim=1)]
+    x = dict(zip(("Q", "K", "V", "q_idx", "k_idx"),
+                 [p.unflatten(1, s) for p, s in zip(parts, [(b.Hq, 128), (b.G, 128), (b.G, 128), (b.G, 64), (64,)])]))
+    was = {n: v.clone() for n, v in x.items()}
+    f, fi = _freq(rot), _freq(rot_idx)
+    rope = msa.Rope(f.cuda(), fi.cuda() if index else None, interleaved=how)
+    out = x["Q"] if in_place else torch.full((b.N, b.Hq, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    qi_out = None
+    if index:
+        qi_out = x["q_idx"] if in_place else torch.full((b.N, b.G, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    ws = msa.alloc_paged_workspace(shape, msa.MSA_WS_PAGED_APPEND)
+    msa.msa_paged_append(shape, cache, rope, x["K"], x["V"], x.get("k_idx"), x["Q"], x.get("q_idx"), out, qi_out, ws)
+    msa.msa_check_device_status(ws)
+
+    # a result is a rounding of sums of two products with fp32 sin and cos: 2^-8 of it and 2^-20 of |a| + |b|
+    def close(got, y, mag, what):
+        assert bool(((got.double() - y).abs() <= 2.0 ** -8 * y.abs() + 2.0 ** -20 * mag).all()), what
+
+    want = {n: getattr(b, n).clone() for n in ("K", "V", "k_idx") if getattr(b, n) is not None}
+    got = {n: t[n].cpu() for n in want}
+    src = {n: v.cpu() for n, v in was.items()}
+    for r in range(b.n):
+        page, slot = int(b.table[b.row_seq[r], b.row_pos[r] // 128]), b.row_pos[r] % 128
+        for n in ("K", "V", "k_idx"):
+            if n not in want:
+                continue
+            here = (page, slice(None), slot) if n != "k_idx" else (page, slot)
+            y, mag = ref.rotated(src[n][r].double(), b.row_pos[r], fi if n == "k_idx" else f, how)
+            if n == "V":
+                y, mag = src[n][r].double(), 0.0 * mag
+            close(got[n][here], y, mag, (n, r))
+            got[n][here] = want[n][here]
+        close(out[r].cpu(), *ref.rotated(src["Q"][r].double(), b.row_pos[r], f, how), ("Q", r))
+        if index:
+            close(qi_out[r].cpu(), *ref.rotated(src["q_idx"][r].double(), b.row_pos[r], fi, how), ("q_idx", r))
+    for n in want:  # nothing else of the pools was touched
+        assert torch.equal(got[n], want[n]), n
+    rest = src["Q"][b.n:] if in_place else torch.full_like(src["Q"][b.n:], 3.0)
+    assert torch.equal(out[b.n:].cpu(), rest)
+
+
+def test_append_far_positions(msa):
+    """Angles at positions up to 2^20 - 1, where a product in fp32 would be off by 0.06 radians."""
+    import torch
+
+    pos = [0, 1, 4095, 99999, 524287, 1048574, 1048575]
+    S, G, Hq = len(pos), 1, 1
+    table = torch.arange(S, dtype=torch.int32).repeat_interleave(8192).view(S, 8192).cuda()
+    K, V = (torch.zeros(S, G, 128, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cache = msa.PagedCache(K, V, None, table, torch.arange(S + 1, dtype=torch.int32, device="cuda"),
+                           torch.tensor([p + 1 for p in pos], dtype=torch.int32, device="cuda"))
+    shape = msa.PagedShape(S=S, N=S, Hq=Hq, G=G, num_pages=S, max_blocks=8192)
+    new = torch.randn(S, 1, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    for f in (_freq(128), torch.linspace(-3.0, 40.0, 64)):  # frequencies past one turn, and backward ones, too
+        ws = msa.alloc_paged_workspace(shape, msa.MSA_WS_PAGED_APPEND)
+        Q, _ = msa.paged_append(shape, cache, msa.Rope(f.cuda()), new, new, Q=new, workspace=ws)
+        msa.msa_check_device_status(ws)
+        for r, p in enumerate(pos):
+            y, mag = ref.rotated(new[r].cpu().double(), p, f, False)
+            # the phase is kept to 2^-32 turns and rounded to fp32 (pi 2^-24), sin and cos to fp32
+            bound = 2.0 ** -8 * y.abs() + 2.0 ** -20 * mag
+            assert bool(((Q[r].cpu().double() - y).abs() <= bound).all()), p
+            assert bool(((K[r, :, p % 128].cpu().double() - y).abs() <= bound).all()), p
+
+
+# ----------------------------------------------------------------- sparse
+SPARSE = {
+    "first_token": dict(counts=[1], lens=[1], Hq=8, G=2, k=4),
+    "page_ends": dict(counts=[1, 1, 1, 1, 1, 1], lens=[2, 127, 128, 129, 256, 257], Hq=8, G=2, k=2),
+    "k1": dict(counts=[1, 2], lens=[700, 1300], Hq=4, G=2, k=1),
+    "hg1_g3": dict(counts=[2, 1], lens=[1500, 2000], Hq=3, G=3, k=5),
+    "hg2_idle_padding": dict(counts=[0, 3, 0, 1], lens=[50, 1027, 0, 4000], Hq=4, G=2, k=7, pad=2),
+    "hg8_rows": dict(counts=[5, 1, 9], lens=[5000, 640, 900], Hq=16, G=2, k=16),
+    "g8": dict(counts=[1, 1, 2], lens=[3000, 2999, 5111], Hq=32, G=8, k=16),
+    "all_blocks_kept": dict(counts=[1, 4], lens=[1000, 260], Hq=8, G=1, k=40),
+    "k33": dict(counts=[1, 1], lens=[9000, 8193], Hq=4, G=1, k=33),
+    "k128": dict(counts=[2], lens=[128 * 140 + 5], Hq=2, G=1, k=128),
+    "many_rows": dict(counts=[40, 1, 30], lens=[2040, 1, 1037], Hq=8, G=2, k=4),
+}
+
+
+def _sparse(msa, b, k, **kw):
+    import torch
+
+    shape, cache, t = b.gpu(k)
+    ws = msa.alloc_paged_workspace(shape, msa.MSA_WS_PAGED_SPARSE)
+    ws.fill_(255)  # no result may depend on what a workspace held
+    bi = torch.full((b.N, b.G, k), -7, dtype=torch.int32, device="cuda")
+    O = torch.full((b.N, b.Hq, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    LSE = torch.full((b.N, b.Hq), 5.0, device="cuda")
+    msa.msa_paged_sparse_attn(shape, cache, t["Q"], t["q_idx"], bi, O, LSE, ws, **kw)
+    msa.msa_check_device_status(ws)
+    return O.cpu(), LSE.cpu(), bi.cpu().numpy()
+
+
+def _check_padding(b, O, LSE, bi=None):
+    assert bool((O[b.n:] == 5.0).all()) and bool((LSE[b.n:] == 5.0).all())
+    assert bi is None or (bi[b.n:] == -7).all()
+
+
+@pytest.mark.parametrize("stale", [NAN, INF, 3e38], ids=["nan", "inf", "huge"])
+@pytest.mark.parametrize("name", SPARSE)
+def test_sparse(msa, name, stale):
+    kw = dict(SPARSE[name])
+    k = kw.pop("k")
+    b = ref.Batch(stale=stale, seed=3, **kw)
+    O, LSE, bi = _sparse(msa, b, k)
+    for r in range(b.n):
+        np.testing.assert_array_equal(bi[r], ref.select(b, r, k), err_msg=f"row {r}")
+    rows = range(b.n) if b.n < 20 else range(0, b.n, 5)
+    ref.check_attention(b, rows, range(b.Hq), O, LSE, lambda r, g: bi[r, g].tolist())
+    _check_padding(b, O, LSE, bi)
+
+
+def test_sparse_long(msa):
+    """A quarter of a million tokens, two rows: more blocks than a pass of the selection's threads."""
+    b = ref.Batch(counts=[2], lens=[1 << 18], Hq=2, G=1, seed=8)
+    O, LSE, bi = _sparse(msa, b, 16)
+    for r in range(2):
+        np.testing.assert_array_equal(bi[r], ref.select(b, r, 16))
+    ref.check_attention(b, range(2), range(2), O, LSE, lambda r, g: bi[r, g].tolist())
+
+
+@pytest.mark.parametrize("k", [2, 4, 9])
+def test_selection_at_narrow_borders(msa, k):
+    """Blocks that fp32 sums cannot tell apart: exact ties (equal pages, equal rows in another order) go to the lower
+    id, and gaps of 2^-26 of the score are decided as they are."""
+    import torch
+
+    b = ref.Batch(counts=[1, 3], lens=[128 * 24 + 40, 128 * 24 + 3], Hq=2, G=2, seed=11)
+    gen = torch.Generator().manual_seed(2)
+    for s in range(2):
+        first = b.k_idx[b.table[s, 0].long()].clone()
+        for c in range(1, 24):
+            page = int(b.table[s, c])
+            if c % 3 == 0:
+                b.k_idx[page] = first                                   # the same page again
+            elif c % 3 == 1:
+                b.k_idx[page] = first[torch.randperm(128, generator=gen)]  # its keys in another order
+            else:
+                b.k_idx[page] = first
+                # every key's dim e moves by a value far below the score's fp32 step
+                e = int(torch.randint(0, 64, (1,), generator=gen))
+                b.k_idx[page, :, e] = first[:, e] * (1 + 2.0 ** -7 * int(torch.randint(-1, 2, (1,), generator=gen)))
+                b.q_idx[:, :, e] = (b.q_idx[:, :, e].float() * 2.0 ** -18).to(torch.bfloat16)
+    _, _, bi = _sparse(msa, b, k)
+    for r in range(b.n):
+        np.testing.assert_array_equal(bi[r], ref.select(b, r, k), err_msg=f"row {r}")
+
+
+def test_selection_with_nan_and_infinite_index_values(msa):
+    """A NaN score counts as -infinity; infinite scores order as they are; huge ones do not overflow."""
+    b = ref.Batch(counts=[1, 2, 1, 1], lens=[128 * 12 + 7] * 4, Hq=2, G=2, seed=12)
+    for s, v in ((0, NAN), (1, INF), (2, 2e38)):
+        b.k_idx[int(b.table[s, 3]), 5] = v
+        b.k_idx[int(b.table[s, 7]), :, 9] = v
+        b.k_idx[int(b.table[s, 8]), 100] = -v
+    b.q_idx[4, 0, 3] = NAN  # every score of this (row, group)
+    b.q_idx[4, 1] = 0.0     # every score zero: the lowest ids
+    _, _, bi = _sparse(msa, b, 4)
+    for r in range(b.n):
+        np.testing.assert_array_equal(bi[r], ref.select(b, r, 4), err_msg=f"row {r}")
+
+
+def test_sparse_with_a_given_selection(msa):
+    """IndexShare: block_idx is read; no index keys are needed; an empty list gives O = 0 and LSE = -infinity."""
+    import torch
+
+    b = ref.Batch(counts=[1, 3, 0, 2], lens=[1000, 2000, 9, 130], Hq=8, G=2, seed=4, index=False, pad=1)
+    k = 6
+    rng = np.random.default_rng(0)
+    bi = np.full((b.N, b.G, k), -1, np.int32)
+    for r in range(b.n):
+        for g in range(b.G):
+            last = b.row_pos[r] // 128
+            ids = sorted(rng.choice(last, min(last, k - 1), replace=False).tolist() + [last]) if last else [0]
+            bi[r, g, :len(ids)] = ids
+    bi[1, 0] = -1                     # nothing selected
+    bi[2, 1] = [0, 3, -1, -1, -1, -1]  # without the own block
+    shape, cache, t = b.gpu(k)
+    ws = msa.alloc_paged_workspace(shape, msa.MSA_WS_PAGED_SPARSE)
+    O, LSE, _ = msa.paged_sparse_attn(shape, cache, t["Q"], block_idx=torch.from_numpy(bi).cuda(), workspace=ws)
+    msa.msa_check_device_status(ws)
+    ref.check_attention(b, range(b.n), range(b.Hq), O.cpu(), LSE.cpu(), lambda r, g: bi[r, g].tolist())
+    assert float(LSE[1, 0]) == -INF and bool((O[1, :4] == 0).all())
+
+
+# ----------------------------------------------------------------- dense
+DENSE = {
+    "first_token": dict(counts=[1], lens=[1], Hq=8, G=2),
+    "page_ends": dict(counts=[1, 1, 1, 1, 1], lens=[127, 128, 129, 256, 257], Hq=8, G=2),
+    "rows_hg1": dict(counts=[20, 3, 17], lens=[20, 131, 400], Hq=3, G=3),
+    "rows_hg2_idle": dict(counts=[0, 7, 0, 1], lens=[0, 300, 77, 900], Hq=4, G=2, pad=2),
+    "rows_hg4": dict(counts=[9, 1, 5], lens=[1000, 2, 133], Hq=8, G=2),
+    "rows_hg8": dict(counts=[3, 4], lens=[1500, 260], Hq=16, G=2),
+    "g8_long": dict(counts=[1, 2], lens=[7000, 6001], Hq=32, G=8),
+    "prefix1": dict(counts=[1, 1], lens=[129, 200], Hq=8, G=2, prefix=1),
+    "prefix_hg1": dict(counts=[1, 3, 0, 2], lens=[128 * 5 + 1, 128 * 5 + 300, 9, 128 * 5 + 2], Hq=3, G=3, prefix=5, pad=1),
+    "prefix_hg2": dict(counts=[2, 1], lens=[128 * 9 + 2, 128 * 9 + 128], Hq=2, G=1, prefix=9),
+    "prefix_hg4_rows": dict(counts=[1] * 30 + [4] * 11, lens=[128 * 12 + 4 + i for i in range(41)], Hq=8, G=2, prefix=12),
+    "prefix_hg8": dict(counts=[1] * 21, lens=[128 * 40 + 1 + 9 * i for i in range(21)], Hq=16, G=2, prefix=40),
+    "prefix_two_pairs": dict(counts=[5] * 20, lens=[128 * 6 + 7 + 3 * i for i in range(20)], Hq=32, G=8, prefix=6),
+    "prefix_idle_first": dict(counts=[0, 1, 2], lens=[0, 128 * 3 + 5, 128 * 3 + 9], Hq=4, G=1, prefix=3),
+}
+
+
+def _dense(msa, b, **kw):
+    import torch
+
+    shape, cache, t = b.gpu()
+    ws = msa.alloc_paged_workspace(shape, msa.MSA_WS_PAGED_DENSE)
+    ws.fill_(255)
+    O = torch.full((b.N, b.Hq, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    LSE = torch.full((b.N, b.Hq), 5.0, device="cuda")
+    msa.msa_paged_dense_attn(shape, cache, t["Q"], O, LSE, ws, **kw)
+    msa.msa_check_device_status(ws)
+    return O.cpu(), LSE.cpu()
+
+
+def _all(b):
+    return lambda r, g: list(range(b.row_pos[r] // 128 + 1))
+
+
+@pytest.mark.parametrize("stale", [NAN, INF], ids=["nan", "inf"])
+@pytest.mark.parametrize("name", DENSE)
+def test_dense(msa, name, stale):
+    b = ref.Batch(stale=stale, seed=6, **DENSE[name])
+    O, LSE = _dense(msa, b)
+    rows = range(b.n) if b.n < 30 else range(0, b.n, 7)
+    heads = range(b.Hq) if b.Hq <= 8 else range(0, b.Hq, 5)
+    ref.check_attention(b, rows, heads, O, LSE, _all(b), bf16_p=b.prefix > 0)
+    _check_padding(b, O, LSE)
+
+
+def test_dense_large_scores(msa):
+    """Scores whose maximum moves by far more than exp2's range from page to page."""
+    b = ref.Batch(counts=[2, 1, 1], lens=[128 * 6 + 90, 128 * 7, 128 * 6 + 1], Hq=8, G=2, prefix=4, seed=9)
+    for s in range(3):
+        for c in range(6):
+            b.K[int(b.table[s, c])] *= 1.0 if s else float(1 + 3 * c)
+    b.Q *= 4
+    O, LSE = _dense(msa, b)
+    ref.check_attention(b, range(b.n), range(b.Hq), O, LSE, _all(b), bf16_p=True)
+
+
+def test_later_rows_do_not_reach_earlier_ones(msa):
+    """Infinite and NaN values of a sequence's later rows: the rows before them are as without them."""
+    b = ref.Batch(counts=[6, 5], lens=[262, 5], Hq=4, G=2, seed=10)
+    clean = _dense(msa, b)
+    for s in range(2):
+        for i, v in ((1, NAN), (3, INF)):  # the sequence's last but i row
+            t = b.lens[s] - 1 - i
+            b.V[int(b.table[s, t // 128]), :, t % 128] = v
+            b.K[int(b.table[s, t // 128]), :, t % 128] = v
+    O, LSE = _dense(msa, b)
+    for r in range(b.n):
+        if b.row_pos[r] < b.lens[b.row_seq[r]] - 4:
+            assert bool((O[r] == clean[0][r]).all()) and bool((LSE[r] == clean[1][r]).all()), r
+
+
+def test_pools_past_32_bit_offsets(msa):
+    """Pages whose values lie more than 2^31 elements (and 2^32 bytes) into the pools."""
+    import torch
+
+    G, pages = 8, 16500
+    K, V = (torch.zeros(pages, G, 128, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k_idx = torch.zeros(pages, 128, 64, dtype=torch.bfloat16, device="cuda")
+    b = ref.Batch(counts=[1], lens=[128 * 9 + 30], Hq=8, G=G, seed=13, spare=0)
+    far = torch.tensor([pages - 1 - 3 * i for i in range(b.num_pages)], device="cuda")
+    K[far], V[far], k_idx[far] = b.K.cuda(), b.V.cuda(), b.k_idx.cuda()
+    table = far.cpu()[b.table.long()].to(torch.int32).cuda()
+    one, ln = torch.tensor([0, 1], dtype=torch.int32, device="cuda"), torch.tensor(b.lens, dtype=torch.int32, device="cuda")
+    cache = msa.PagedCache(K, V, k_idx, table, one, ln)
+    shape = msa.PagedShape(S=1, N=1, Hq=8, G=G, num_pages=pages, max_blocks=b.max_blocks, k=5)
+    O, LSE, bi = msa.paged_sparse_attn(shape, cache, b.Q.cuda(), b.q_idx.cuda())
+    np.testing.assert_array_equal(bi[0].cpu().numpy(), ref.select(b, 0, 5))
+    ref.check_attention(b, [0], range(8), O.cpu(), LSE.cpu(), lambda r, g: bi[r, g].tolist())
+    shape4 = msa.PagedShape(S=1, N=1, Hq=8, G=G, num_pages=pages, max_blocks=b.max_blocks, prefix_blocks=4)
+    O, LSE = msa.paged_dense_attn(shape4, cache, b.Q.cuda())
+    ref.check_attention(b, [0], range(8), O.cpu(), LSE.cpu(), _all(b), bf16_p=True)
+    new = torch.randn(1, G, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    msa.paged_append(shape, cache, msa.Rope(), new, new)
+    assert torch.equal(K[int(far[b.table[0, 9].long()]), :, 29], new[0])
+    del K, V, k_idx
+
+
+# ----------------------------------------------------------------- the batch description's faults
+def test_bad_pages_and_positions_are_reported(msa):
+    import torch
+
+    def run(change, which="sparse", prefix=0, good=None):
+        b = ref.Batch(counts=[1, 2], lens=[128 * 5 + 3, 128 * 6 + 9], Hq=8, G=2, prefix=prefix, seed=1)
+        change(b)
+        shape, cache, t = b.gpu(4)
+        if which == "append":
+            ws = msa.alloc_paged_workspace(shape, msa.MSA_WS_PAGED_APPEND)
+            new = torch.ones(b.N, 2, 128, dtype=torch.bfloat16, device="cuda")
+            msa.paged_append(shape, cache, msa.Rope(), new, new, workspace=ws)
+        elif which == "sparse":
+            ws = msa.alloc_paged_workspace(shape, msa.MSA_WS_PAGED_SPARSE)
+            O, LSE, bi = msa.paged_sparse_attn(shape, cache, t["Q"], t["q_idx"], workspace=ws)
+        else:
+            ws = msa.alloc_paged_workspace(shape, msa.MSA_WS_PAGED_DENSE)
+            O, LSE = msa.paged_dense_attn(shape, cache, t["Q"], workspace=ws)
+        with pytest.raises(msa.MsaError) as e:
+            msa.msa_check_device_status(ws)
+        assert e.value.status == msa.MSA_ERR_DEVICE
+        msa.msa_check_device_status(ws)  # the word was cleared
+        if good is not None:  # the rows that were in order
+            blocks = (lambda r, g: bi[r, g].tolist()) if which == "sparse" else _all(b)
+            ref.check_attention(b, good, range(8), O.cpu(), LSE.cpu(), blocks, bf16_p=prefix > 0)
+
+    def page(s, c, v):
+        def change(b):
+            b.table[s, c] = v
+        return change
+
+    def length(s, v):
+        def change(b):
+            b.lens[s] = v
+        return change
+
+    for v in (-1, 1 << 20, 2 ** 31 - 1, -2 ** 31):
+        run(page(0, 2, v), "sparse", good=[1, 2])
+        run(page(1, 6, v), "sparse", good=[0])
+        run(page(0, 5, v), "dense", good=[1, 2])
+        run(page(0, 5, v), "append")
+        run(page(0, 1, v), "dense", prefix=3)
+    for v in (0, -5, 128 * 7 + 1, 2 ** 31 - 1, -2 ** 31):
+        run(length(0, v), "sparse", good=[1, 2])
+        run(length(0, v), "dense", good=[1, 2])
+        run(length(0, v), "append")
+    run(length(1, 128 * 3 + 1), "dense", prefix=3, good=[0])  # a row inside the prefix
+    run(page(1, 2, 0), "dense", prefix=3)                      # a prefix that is not shared
+
+
+def test_bad_selections_are_reported(msa):
+    import torch
+
+    for ids in ([0, 6, -1], [3, 1, 5], [2, 2, 5], [0, -1, 5], [-5, 1, 2], [2 ** 31 - 1, -1, -1]):
+        b = ref.Batch(counts=[1, 1], lens=[128 * 5 + 3, 128 * 5 + 3], Hq=8, G=2, seed=1)
+        bi = torch.tensor([[[0, 2, 5]] * 2] * 2, dtype=torch.int32)
+        bi[0, 1] = torch.tensor(ids, dtype=torch.int32)
+        shape, cache, t = b.gpu(3)
+        ws = msa.alloc_paged_workspace(shape, msa.MSA_WS_PAGED_SPARSE)
+        O, LSE, _ = msa.paged_sparse_attn(shape, cache, t["Q"], block_idx=bi.cuda(), workspace=ws)
+        with pytest.raises(msa.MsaError) as e:
+            msa.msa_check_device_status(ws)
+        assert e.value.status == msa.MSA_ERR_DEVICE, ids
+        ref.check_attention(b, [1], range(8), O.cpu(), LSE.cpu(), lambda r, g: [0, 2, 5])
+
+
+# ----------------------------------------------------------------- streams, graphs, reruns
+def test_same_bits_on_other_streams_and_at_once(msa):
+    import torch
+
+    b = ref.Batch(counts=[1, 4, 2], lens=[3000, 2500, 1200], Hq=16, G=4, seed=2)
+    p = ref.Batch(counts=[1] * 9, lens=[128 * 30 + 5 + i for i in range(9)], Hq=16, G=4, prefix=30, seed=2)
+    O, LSE, bi = _sparse(msa, b, 8)
+    Od, LSEd = _dense(msa, p)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    s1.wait_stream(torch.cuda.current_stream())
+    s2.wait_stream(torch.cuda.current_stream())
+    kept = []
+    for _ in range(3):
+        with torch.cuda.stream(s1):
+            shape, cache, t = b.gpu(8)
+            kept.append((cache, t) + msa.paged_sparse_attn(shape, cache, t["Q"], t["q_idx"]))
+        shape, cache, t = p.gpu()
+        s2.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s2):
+            ws = msa.alloc_paged_workspace(shape, msa.MSA_WS_PAGED_DENSE)
+        kept.append((cache, t, ws) + msa.paged_dense_attn(shape, cache, t["Q"], workspace=ws, stream=s2))
+    torch.cuda.synchronize()
+    for i in range(0, 6, 2):
+        assert torch.equal(kept[i][2].cpu(), O) and torch.equal(kept[i][3].cpu(), LSE)
+        np.testing.assert_array_equal(kept[i][4].cpu().numpy(), bi)
+        assert torch.equal(kept[i + 1][3].cpu(), Od) and torch.equal(kept[i + 1][4].cpu(), LSEd)
+
+
+def test_captured_step_replays_on_another_batch(msa):
+    """One decode step (append, selection and attention, full attention) captured once, replayed with other lengths,
+    pages and rows of the same shape; two graphs share nothing but the cache."""
+    import torch
+
+    b = ref.Batch(counts=[1, 2, 1], lens=[900, 700, 129], Hq=8, G=2, pad=2, seed=20, max_blocks=12, spare=8, stale=0.0)
+    shape, cache, t = b.gpu(4)
+    N = b.N
+    new = {n: torch.zeros(N, *s, dtype=torch.bfloat16, device="cuda")
+           for n, s in (("K", (2, 128)), ("V", (2, 128)), ("k_idx", (64,)), ("Q", (8, 128)), ("q_idx", (2, 64)))}
+    rope = msa.Rope(_freq(128).cuda(), _freq(64).cuda())
+    wsa, wss, wsd = (msa.alloc_paged_workspace(shape, w) for w in range(3))
+    Qr, qir = torch.zeros_like(new["Q"]), torch.zeros_like(new["q_idx"])
+    O, Od = torch.zeros_like(Qr), torch.zeros_like(Qr)
+    LSE, LSEd = (torch.zeros(N, 8, device="cuda") for _ in range(2))
+    bi = torch.zeros(N, 2, 4, dtype=torch.int32, device="cuda")
+
+    def step():
+        msa.msa_paged_append(shape, cache, rope, new["K"], new["V"], new["k_idx"], new["Q"], new["q_idx"], Qr, qir, wsa)
+        msa.msa_paged_sparse_attn(shape, cache, Qr, qir, bi, O, LSE, wss)
+        msa.msa_paged_dense_attn(shape, cache, Qr, Od, LSEd, wsd)
+
+    step()  # once before the capture
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for seed, counts, lens in ((1, [1, 2, 1], [900, 700, 129]), (2, [0, 1, 4], [0, 1300, 500]), (3, [6, 0, 0], [6, 0, 0])):
+        c = ref.Batch(counts=counts, lens=lens, Hq=8, G=2, pad=N - sum(counts), seed=seed, max_blocks=12, spare=0,
+                      stale=0.0)
+        gen = torch.Generator().manual_seed(seed)
+        t["table"].copy_(c.table)
+        t["row_start"].copy_(torch.tensor(c.starts, dtype=torch.int32))
+        t["seq_len"].copy_(torch.tensor(lens, dtype=torch.int32))
+        for n in ("K", "V", "k_idx"):
+            t[n].zero_()
+            t[n][:c.num_pages].copy_(getattr(c, n))
+        for v in new.values():
+            v.copy_(torch.randn(v.shape, generator=gen))
+        g.replay()
+        for ws in (wsa, wss, wsd):
+            msa.msa_check_device_status(ws)
+        c.K, c.V, c.k_idx = (t[n].cpu() for n in ("K", "V", "k_idx"))
+        c.Q, c.q_idx = Qr.cpu(), qir.cpu()
+        got = bi.cpu().numpy()
+        for r in range(c.n):
+            np.testing.assert_array_equal(got[r], ref.select(c, r, 4))
+        ref.check_attention(c, range(c.n), range(8), O.cpu(), LSE.cpu(), lambda r, g_: got[r, g_].tolist())
+        ref.check_attention(c, range(c.n), range(8), Od.cpu(), LSEd.cpu(), _all(c))
+
+
+# ----------------------------------------------------------------- together, as a model would use them
+def test_served_rows_are_those_of_the_training_calls(msa):
+    """A sequence written into the cache in pieces (a prompt, drafts, single tokens) and attended to from there gives
+    what msa_index_topk + msa_sparse_fwd and msa_dense_fwd give for the whole sequence at once."""
+    import torch
+
+    T, Hq, G, k = 1536, 8, 2, 5
+    gen = torch.Generator().manual_seed(30)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=gen).to(torch.bfloat16).cuda()
+
+    Q, K, V, qi, ki = normal(T, Hq, 128), normal(T, G, 128), normal(T, G, 128), normal(T, G, 64), normal(T, 64)
+    f, fi = _freq(128).cuda(), _freq(64).cuda()
+    pages = 20
+    order = torch.randperm(pages, generator=gen)[:12].to(torch.int32)
+    pk, pv = (torch.full((pages, G, 128, 128), NAN, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pi = torch.full((pages, 128, 64), NAN, dtype=torch.bfloat16, device="cuda")
+    table = order.view(1, 12).cuda()
+    got = {n: [] for n in ("Q", "qi", "O", "LSE", "bi", "Od", "LSEd")}
+    at = 0
+    for n in (700, 1, 1, 5, 128, 61, 512, 1, 127):
+        cache = msa.PagedCache(pk, pv, pi, table, torch.tensor([0, n], dtype=torch.int32, device="cuda"),
+                               torch.tensor([at + n], dtype=torch.int32, device="cuda"))
+        shape = msa.PagedShape(S=1, N=n, Hq=Hq, G=G, num_pages=pages, max_blocks=12, k=k, prefix_blocks=at // 128)
+        s = slice(at, at + n)
+        Qr, qir = msa.paged_append(shape, cache, msa.Rope(f, fi), K[s], V[s], ki[s], Q[s], qi[s])
+        O, LSE, bi = msa.paged_sparse_attn(shape, cache, Qr, qir)
+        Od, LSEd = msa.paged_dense_attn(shape, cache, Qr)  # the sequence's own full blocks as the shared prefix
+        for name, v in zip(got, (Qr, qir, O, LSE, bi, Od, LSEd)):
+            got[name].append(v)
+        at += n
+    assert at == T
+    got = {n: torch.cat(v) for n, v in got.items()}
+    # the rotated sequence, read back from the pages
+    Kr = pk[order.long().cuda()].transpose(1, 2).reshape(1, T, G, 128).contiguous()
+    Vr = pv[order.long().cuda()].transpose(1, 2).reshape(1, T, G, 128).contiguous()
+    kir = pi[order.long().cuda()].reshape(1, T, 64).contiguous()
+    assert torch.equal(Vr[0], V)
+    s = msa.Shape(B=1, T=T, Hq=Hq, G=G, k=k)
+    bi = msa.index_topk(s, got["qi"][None].contiguous(), kir)
+    same = (bi[0].transpose(0, 1) == got["bi"]).all(dim=2)
+    assert float(same.float().mean()) > 0.999  # the training call decides near-ties in fp32
+    O, LSE = msa.sparse_fwd(s, got["Q"][None].contiguous(), Kr, Vr, bi)
+    Od, LSEd = msa.dense_fwd(s, got["Q"][None].contiguous(), Kr, Vr)
+    same = same.repeat_interleave(Hq // G, dim=1)
+    # both round P to bf16 at most, O to bf16, from scores within 1e-4: 2^-8 of |O| twice and of sum p |v| (< 4.5) once
+    for a, c, m in ((got["O"], O[0], same), (got["Od"], Od[0], torch.ones_like(same))):
+        err = (a.float() - c.float()).abs()
+        assert float((err * m[..., None]).max()) <= 2.0 ** -8 * (4.5 + 2 * float(c.float().abs().max()))
+        assert float((err * m[..., None]).mean()) <= 2.0 ** -8
+    assert float(((got["LSE"] - LSE[0]).abs() * same).max()) <= 1e-3
+    assert float((got["LSEd"] - LSEd[0]).abs().max()) <= 1e-3
