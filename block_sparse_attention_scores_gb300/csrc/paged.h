@@ -18,7 +18,9 @@ struct PagedProb {
 
 // Workspace regions (byte offsets, 256-aligned) and how the work is cut.
 struct PagedWs {
-  size_t rows = 0;      // int4 [N]  per new row: sequence (-1: none), position, rows of its sequence before it, and from it on
+  size_t rows = 0;      // int4 [N]  per new row: sequence (-1: none, -2: refused), position, rows of its sequence before
+                        //           it, and from it on
+  size_t arrived = 0;   // int32 [N, G, 3] parts of a (row tile, group) that are done, as each joining warp counts them
   size_t pooled = 0;    // fp32 [N, G, max_blocks] block maxima of the index scores
   size_t amax = 0;      // fp32 [S, max_blocks]    largest |index key| value of a block
   size_t part_o = 0;    // fp32 [pslots + splits, N, Hq, d] partial outputs (normalised)
@@ -56,7 +58,8 @@ struct RopeRows {
 
 cudaError_t launch_paged_append(const PagedProb& p, const PagedCachePtrs& c, const RopeRows& r, uint8_t* ws,
                                 cudaStream_t st);
-// Sequence and position of every new row; checks of the batch description.
+// Clears the header and the counters, and finds the sequence and position of
+// every new row: the first launch of the attentions.
 cudaError_t launch_paged_rows(const PagedProb& p, const PagedCachePtrs& c, uint8_t* ws, const PagedWs& L,
                               cudaStream_t st);
 cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, const void* q_idx, int32_t* block_idx,
@@ -67,8 +70,9 @@ cudaError_t launch_paged_attn(const PagedProb& p, const PagedCachePtrs& c, const
                               void* O, float* LSE, uint8_t* ws, const PagedWs& L, cudaStream_t st);
 cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, const void* Q, uint8_t* ws,
                                 const PagedWs& L, cudaStream_t st);
-cudaError_t launch_paged_merge(const PagedProb& p, const int32_t* block_idx, void* O, float* LSE, uint8_t* ws,
-                               const PagedWs& L, cudaStream_t st);
+// Joins the parts of the shared prefix and of the own pages (without a prefix the attention does).
+cudaError_t launch_paged_merge(const PagedProb& p, void* O, float* LSE, uint8_t* ws, const PagedWs& L,
+                               cudaStream_t st);
 
 // Tensor map over a K or V pool as rows of 128 values: box of 64 columns x 128 rows (half a page of one group).
 bool encode_pool_map(CUtensorMap* m, const PagedProb& p, void* pool);

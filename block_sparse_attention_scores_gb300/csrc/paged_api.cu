@@ -8,14 +8,25 @@ namespace msa {
 
 static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Splits of `pages` pages into runs of equal length, so that `tiles` row
-// tiles give each SM about six items (their lengths differ: ragged batches,
-// page counts that do not divide).
+// Cuts `pages` pages of each of `tiles` row tiles into runs of equal length.
+// Every SM takes items in turn, so the time is the rounds of items times their
+// length, and an item costs about half a page more than its pages (its
+// queries, the warps' meeting, its part of O).
 static void cut_pages(long long tiles, int pages, PagedWs* L) {
-  const long long target = 6LL * kCutSms;
-  long long splits = std::min<long long>(std::max(1, pages), std::max(1LL, target / std::max(1LL, tiles)));
-  L->per_split = (int)((std::max(1, pages) + splits - 1) / splits);
-  L->splits = (std::max(1, pages) + L->per_split - 1) / L->per_split;
+  tiles = std::max(1LL, tiles);
+  pages = std::max(1, pages);
+  long long best = 0;
+  for (int rounds = 0; rounds <= 8; ++rounds) {
+    const long long want = rounds ? std::max(1LL, rounds * (long long)kCutSms / tiles) : 1;
+    const int per = (int)((pages + std::min<long long>(want, pages) - 1) / std::min<long long>(want, pages));
+    const int splits = (pages + per - 1) / per;
+    const long long cost = (tiles * splits + kCutSms - 1) / kCutSms * (2 * per + 1);
+    if (!best || cost < best) {
+      best = cost;
+      L->per_split = per;
+      L->splits = splits;
+    }
+  }
 }
 
 PagedWs paged_ws_layout(const PagedProb& p, int which) {
@@ -31,15 +42,16 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
     return L;
   }
   L.rows = take((size_t)p.N * 16);
+  L.arrived = take((size_t)p.N * p.G * 12);
   if (which == MSA_WS_PAGED_SPARSE) {
     L.pooled = take((size_t)p.N * p.G * p.max_blocks * 4);
     L.amax = take((size_t)p.S * p.max_blocks * 4);
     cut_pages((long long)p.N * p.G, std::min(p.k, p.max_blocks), &L);
   } else {
-    // several rows a sequence on average: two column tiles share each page
-    const int cols = p.N >= 2LL * p.S ? 16 : 8;
+    // more columns (rows x heads of a sequence) than eight on average: two column tiles share each page
+    const int cols = (long long)p.N * p.hg > 8LL * p.S ? 16 : 8;
     L.tile_rows = cols / p.hg;
-    cut_pages((long long)p.N * p.G / L.tile_rows, p.max_blocks - p.prefix, &L);
+    cut_pages((long long)std::max(p.N / L.tile_rows, std::min(p.S, p.N)) * p.G, p.max_blocks - p.prefix, &L);
     if (p.prefix > 0) {
       const int tiles = (int)(((long long)p.N * p.hg + 127) / 128);
       L.pairs = (tiles + 1) / 2;
@@ -228,13 +240,10 @@ msa_status msa_paged_sparse_attn(const msa_paged_shape* shape, const msa_paged_c
   if ((s = check_device()) != MSA_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  if ((s = clear_header(w, st)) != MSA_OK) return s;
   if ((s = cuda_status(launch_paged_rows(p, c, w, L, st), "paged rows launch")) != MSA_OK) return s;
   if (q_idx && (s = cuda_status(launch_paged_index(p, c, q_idx, block_idx, w, L, st), "paged index launch")) != MSA_OK)
     return s;
-  if ((s = cuda_status(launch_paged_attn(p, c, Q, block_idx, O, LSE, w, L, st), "paged attention launch")) != MSA_OK)
-    return s;
-  return cuda_status(launch_paged_merge(p, block_idx, O, LSE, w, L, st), "paged merge launch");
+  return cuda_status(launch_paged_attn(p, c, Q, block_idx, O, LSE, w, L, st), "paged attention launch");
 }
 
 msa_status msa_paged_dense_attn(const msa_paged_shape* shape, const msa_paged_cache* cache, const void* Q, void* O,
@@ -252,14 +261,13 @@ msa_status msa_paged_dense_attn(const msa_paged_shape* shape, const msa_paged_ca
   if ((s = check_device()) != MSA_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  if ((s = clear_header(w, st)) != MSA_OK) return s;
   if ((s = cuda_status(launch_paged_rows(p, c, w, L, st), "paged rows launch")) != MSA_OK) return s;
   if (p.prefix &&
       (s = cuda_status(launch_paged_prefix(p, c, Q, w, L, st), "paged prefix launch")) != MSA_OK)
     return s;
   if ((s = cuda_status(launch_paged_attn(p, c, Q, nullptr, O, LSE, w, L, st), "paged attention launch")) != MSA_OK)
     return s;
-  return cuda_status(launch_paged_merge(p, nullptr, O, LSE, w, L, st), "paged merge launch");
+  return p.prefix ? cuda_status(launch_paged_merge(p, O, LSE, w, L, st), "paged merge launch") : MSA_OK;
 }
 
 }  // extern "C"

@@ -191,15 +191,15 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Sequence and position of every new row (the attentions' first step), and
-// what the batch description must satisfy: positions inside the page table
-// and behind the shared prefix, and one shared prefix for every sequence that
-// has rows. A row that does not satisfy it is left out (sequence -1).
+// First launch of the attentions: clears the error word and the counters of
+// finished parts, and finds every new row's sequence and position. A row whose
+// position lies outside the page table (or, behind a shared prefix, inside the
+// prefix) is marked; the attention reports it and leaves it out.
 struct RowsArgs {
-  const int32_t *page_table, *row_start, *seq_len;
+  const int32_t *row_start, *seq_len;
   int4* rows;
-  int S, N, max_blocks, prefix, row_blocks;
-  int* err;
+  int *arrived, *err;
+  int S, N, G, max_blocks, prefix;
 };
 
 __device__ __forceinline__ int bisect_rows(const int32_t* row_start, int S, int r) {
@@ -213,33 +213,20 @@ __device__ __forceinline__ int bisect_rows(const int32_t* row_start, int S, int 
 }
 
 __global__ void __launch_bounds__(kThreads) paged_rows_kernel(RowsArgs a) {
-  if ((int)blockIdx.x < a.row_blocks) {
-    const int r = blockIdx.x * kThreads + threadIdx.x;
-    if (r >= a.N) return;
-    const int s = bisect_rows(a.row_start, a.S, r);
-    int4 out = make_int4(-1, 0, 0, 0);
-    if (s < a.S) {
-      const int len = __ldg(a.seq_len + s), begin = __ldg(a.row_start + s), end = __ldg(a.row_start + s + 1);
-      if (len < end - r + a.prefix * 128 || len > a.max_blocks * 128)
-        dev_fail(a.err, kDevBadIndex, 1211);
-      else
-        out = make_int4(s, len - (end - r), r - begin, (end < a.N ? end : a.N) - r);
-    }
-    a.rows[r] = out;
-    return;
+  if (blockIdx.x == 0 && threadIdx.x < 64) a.err[threadIdx.x] = 0;
+  const int r = blockIdx.x * kThreads + threadIdx.x;
+  if (r >= a.N) return;
+  for (int i = 0; i < 3 * a.G; ++i) a.arrived[(size_t)r * 3 * a.G + i] = 0;
+  const int s = bisect_rows(a.row_start, a.S, r);
+  int4 out = make_int4(-1, 0, 0, 0);
+  if (s < a.S) {
+    const int len = __ldg(a.seq_len + s), begin = __ldg(a.row_start + s), end = __ldg(a.row_start + s + 1);
+    if (len < end - r + a.prefix * 128 || len > a.max_blocks * 128)
+      out.x = -2;
+    else
+      out = make_int4(s, len - (end - r), r - begin, (end < a.N ? end : a.N) - r);
   }
-  // the prefix columns of the page table: the same pages for every sequence with rows
-  const int first = bisect_rows(a.row_start, a.S, 0);  // the first sequence with rows
-  if (first >= a.S) return;
-  const long long cells = (long long)a.S * a.prefix;
-  bool bad = false;
-  for (long long i = (long long)(blockIdx.x - a.row_blocks) * kThreads + threadIdx.x; i < cells;
-       i += (long long)(gridDim.x - a.row_blocks) * kThreads) {
-    const int s = (int)(i / a.prefix), c = (int)(i % a.prefix);
-    if (__ldg(a.row_start + s + 1) > __ldg(a.row_start + s))
-      bad |= __ldg(a.page_table + (size_t)s * a.max_blocks + c) != __ldg(a.page_table + (size_t)first * a.max_blocks + c);
-  }
-  if (bad) dev_fail(a.err, kDevBadIndex, 1212);
+  a.rows[r] = out;
 }
 
 }  // namespace
@@ -269,19 +256,17 @@ cudaError_t launch_paged_append(const PagedProb& p, const PagedCachePtrs& c, con
 cudaError_t launch_paged_rows(const PagedProb& p, const PagedCachePtrs& c, uint8_t* ws, const PagedWs& L,
                               cudaStream_t st) {
   RowsArgs a;
-  a.page_table = c.page_table;
   a.row_start = c.row_start;
   a.seq_len = c.seq_len;
   a.rows = reinterpret_cast<int4*>(ws + L.rows);
+  a.arrived = reinterpret_cast<int*>(ws + L.arrived);
+  a.err = reinterpret_cast<int*>(ws);
   a.S = p.S;
   a.N = p.N;
+  a.G = p.G;
   a.max_blocks = p.max_blocks;
   a.prefix = p.prefix;
-  a.row_blocks = (p.N + kThreads - 1) / kThreads;
-  a.err = reinterpret_cast<int*>(ws);
-  const long long cells = (long long)p.S * p.prefix;
-  const int check_blocks = (int)std::min<long long>((cells + 4 * kThreads - 1) / (4 * kThreads), 2 * kCutSms);
-  paged_rows_kernel<<<a.row_blocks + check_blocks, kThreads, 0, st>>>(a);
+  paged_rows_kernel<<<(p.N + kThreads - 1) / kThreads, kThreads, 0, st>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }

@@ -4,14 +4,17 @@
 // Few query columns against streamed keys: 64 KB of K and V per page and group
 // serve at most 8 (or 16) columns, so the time is the memory's. One persistent
 // CTA per SM: a producer warp keeps three whole pages in flight (192 KB, TMA
-// boxes of half a page each), four warps take 32 keys of every page each:
+// boxes of half a page each), eight warps take 16 keys of every page each:
 //   S^T = K q^T   (mma.sync, keys in rows, columns = rows of the sequence x heads of the group)
 //   P   = exp2(S scale log2 e - m), m the warp's own running maximum per column
 //   O^T += V^T P^T, P as a sum of two bf16 values (16 bits of it: the rounding
 //          of P would otherwise be as large as the output's own)
-// with the warp's own maximum, sum and O in registers; the four warps meet once
-// per item (a run of pages of one (row tile, group)), whose normalised O and
-// log-sum-exp leave in fp32 for the merge.
+// with the warp's own maximum, sum and O in registers; the warps meet once per
+// item (a run of pages of one (row tile, group)). The CTA whose item is done
+// last of its (row tile, group) joins the fp32 parts in their order, so the
+// result does not depend on which one it is; warps of their own do that, so
+// that the next pages are not kept waiting by its loads. Behind a shared prefix
+// the merge kernel below joins them with the prefix's.
 //
 // Masked places: a page is masked per column only where it crosses a row's end.
 // There, each row of the tile is accumulated on its own with the values behind
@@ -25,16 +28,19 @@ namespace msa {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kWarps = 4;                          // consumers; the producer is warp kWarps
-constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kWarps = 8;                          // consumers; then the producer and the joining warps
+constexpr int kJoinWarps = 3;
+constexpr int kThreads = (kWarps + 1 + kJoinWarps) * 32;
 constexpr int kHalf = 16384;                       // 128 rows x 64 bf16, 128-byte swizzle
 constexpr int kTile = 2 * kHalf;                   // K or V of a page and group
 constexpr int kStages = 3;
-constexpr int kOStride = 132;                      // floats between columns of the warps' O (no bank conflicts)
+constexpr int kSlots = 4;                          // shared-memory O buffers: two warps meet in each
+constexpr unsigned long long kIdleLimitNs = 20000000000ull;  // the joining warps may have nothing to do for a while
+constexpr int kOStride = 132;                      // floats between columns of an O buffer (no bank conflicts)
 
 template <int NT>
 constexpr int smem_bytes() {
-  return kStages * 2 * kTile + kWarps * 8 * kOStride * 4 + 2 * NT * 8 * 256 + 1024;
+  return kStages * 2 * kTile + kSlots * 8 * kOStride * 4 + 2 * NT * 8 * 256 + 1024;
 }
 
 struct AttnArgs {
@@ -42,20 +48,30 @@ struct AttnArgs {
   const __nv_bfloat16* Q;
   const int32_t *page_table, *block_idx;  // block_idx null: the sequence's own pages from block `prefix` on
   float *part_o, *part_lse;
-  int N, Hq, G, hg, k, num_pages, max_blocks, prefix, splits, per_split, tile_rows, items, slot0;
+  int* arrived;                           // [N, G, kJoinWarps] items of a (row tile, group) that are done
+  __nv_bfloat16* O;
+  float* LSE;
+  int N, Hq, G, hg, k, num_pages, max_blocks, prefix, splits, per_split, tile_rows, items, slot0, join;
   float scale_log2;
   int* err;
+};
+
+struct AttnItem {
+  int row, g, split, pages;  // pages -1: the end
+  int parts;                 // items of this (row tile, group)
+  int pos, rows;             // position of the first row; rows of the tile
 };
 
 struct AttnShared {
   uint64_t k_full[kStages], v_full[kStages], empty[kStages];
   uint64_t q_full[2], q_empty[2];
   uint64_t meet;              // the consumer warps' rendezvous
-  int4 item[2];               // row, group, split, pages (0: the end)
-  int4 info[2];               // the first row's entry of the row table
+  uint64_t s_free;            // the O buffers have been read
+  uint64_t j_full[2], j_empty[2];
+  AttnItem item[2];
+  AttnItem join[2];           // for the joining warps; parts 0: the end
   int token0[kStages];        // first token of the stage's page
-  float m[kWarps][16], l[kWarps][16];
-  int abort;
+  float m[2][kSlots][8], l[2][kSlots][8];  // [0]: of the warps that store first, [1]: of two warps together
 };
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -74,12 +90,125 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// What the producer knows about an item, fetched in steps while earlier items
+// are on their way: what a step loads is first looked at in the next one, so
+// that no load's latency (microseconds while the pages' traffic fills the
+// memory's queues) holds up the pages.
+struct Fetch {
+  int row, split, g;   // row -1: no item
+  int4 info;
+  int id, before;      // sparse: this lane's block id and the one in front of it
+  int ids[4];          // the row's ids lane, lane + 32, ...
+  int pages, parts;
+  int block, page;     // of this lane's page (the item's first 32)
+};
+
 // Items: (row, split, group), group fastest. A row that does not lead its tile has none.
-__device__ __forceinline__ void decode_item(int id, const AttnArgs& a, int& row, int& split, int& g) {
-  g = id % a.G;
-  const int t = id / a.G;
-  split = t % a.splits;
-  row = t / a.splits;
+__device__ __forceinline__ void fetch_row(const AttnArgs& a, int item, int lane, Fetch& f) {
+  f.row = -1;
+  if (item >= a.items) return;
+  f.g = item % a.G;
+  const int t = item / a.G;
+  f.split = t % a.splits;
+  f.row = t / a.splits;
+  f.info = __ldg(a.rows + f.row);
+  if (a.block_idx) {
+    const int32_t* ids = a.block_idx + ((size_t)f.row * a.G + f.g) * a.k;
+    const int at = f.split * a.per_split + lane;
+    f.id = at < a.k ? __ldg(ids + at) : -1;
+    f.before = at > 0 && at < a.k ? __ldg(ids + at - 1) : -1;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) f.ids[c] = c * 32 + lane < a.k ? __ldg(ids + c * 32 + lane) : -1;
+  }
+}
+
+__device__ __forceinline__ void fetch_pages(const AttnArgs& a, int lane, Fetch& f) {
+  f.page = -1;
+  if (f.row < 0) return;
+  if (f.info.x == -2 && f.split == 0 && f.g == 0 && lane == 0) dev_fail(a.err, kDevBadIndex, 1211);
+  if (f.info.x < 0 || f.info.z % a.tile_rows) {
+    f.row = -1;
+    return;
+  }
+  if (a.block_idx) {
+    int have = 0;  // ids stand at the front of the list
+#pragma unroll
+    for (int c = 0; c < 4; ++c) have += __popc(__ballot_sync(0xffffffffu, f.ids[c] >= 0));
+    f.parts = max(1, (have + a.per_split - 1) / a.per_split);
+    f.pages = min(a.per_split, have - f.split * a.per_split);
+    if (f.pages <= 0 && f.split) f.row = -1;  // a row without any block has one item, without pages
+    f.pages = max(f.pages, 0);
+    f.block = f.id;
+  } else {
+    const int rows = min(a.tile_rows, f.info.w);
+    const int own = (f.info.y + rows - 1) / 128 + 1 - a.prefix;  // pages up to the own one of the tile's last row
+    f.parts = (own + a.per_split - 1) / a.per_split;
+    f.pages = min(a.per_split, own - f.split * a.per_split);
+    if (f.pages <= 0) f.row = -1;
+    f.block = a.prefix + f.split * a.per_split + lane;
+  }
+  if (f.row < 0 || lane >= f.pages) f.block = -1;
+  else if (f.block >= 0 && f.block <= f.info.y / 128 + a.tile_rows)
+    f.page = __ldg(a.page_table + (size_t)f.info.x * a.max_blocks + min(f.block, a.max_blocks - 1));
+}
+
+// The page as it was read, or -1 (reported) where it may not be: ids ascend up to the row's own block, pages lie in
+// the pool. `before`: the list's id in front of this one, or -1.
+__device__ __forceinline__ int checked_page(const AttnArgs& a, const int4& info, int block, int before, int page) {
+  if (a.block_idx && (block < 0 || block > info.y / 128 || before >= block)) {
+    dev_fail(a.err, kDevBadIndex, 1411);
+    return -1;
+  }
+  if (page < 0 || page >= a.num_pages) {
+    dev_fail(a.err, kDevBadIndex, 1412);
+    return -1;
+  }
+  return page;
+}
+
+// Joins an item's (row tile, group), every kJoinWarps-th column from `first`
+// on: the parts in their order, two columns and eight parts in flight.
+__device__ __forceinline__ void join_parts(const AttnArgs& a, const AttnItem& item, int first, int lane) {
+  const size_t step = (size_t)a.N * a.Hq;
+  const int cols = item.rows * a.hg;
+  for (int c0 = first; c0 < cols; c0 += 2 * kJoinWarps) {
+    size_t at[2];
+    float mm[2], den[2] = {0.f, 0.f};
+    float4 acc[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int col = min(c0 + x * kJoinWarps, cols - 1);
+      at[x] = (size_t)(item.row + col / a.hg) * a.Hq + item.g * a.hg + col % a.hg;
+      mm[x] = -INFINITY;
+      acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = lane; i < item.parts; i += 32) mm[x] = fmaxf(mm[x], __ldcg(a.part_lse + i * step + at[x]));
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int o = 16; o; o >>= 1) mm[x] = fmaxf(mm[x], __shfl_xor_sync(0xffffffffu, mm[x], o));
+#pragma unroll 8
+    for (int i = 0; i < item.parts; ++i)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float lse = __ldcg(a.part_lse + i * step + at[x]);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (i * step + at[x]) * 128) + lane);
+        const float w = lse == -INFINITY ? 0.f : fast_exp2(lse - mm[x]);
+        den[x] += w;
+        acc[x].x = fmaf(w, v.x, acc[x].x);
+        acc[x].y = fmaf(w, v.y, acc[x].y);
+        acc[x].z = fmaf(w, v.z, acc[x].z);
+        acc[x].w = fmaf(w, v.w, acc[x].w);
+      }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      if (c0 + x * kJoinWarps >= cols) break;
+      const float inv = den[x] > 0.f ? 1.f / den[x] : 0.f;
+      reinterpret_cast<uint2*>(a.O + at[x] * 128)[lane] =
+          make_uint2(pack_bf16(acc[x].x * inv, acc[x].y * inv), pack_bf16(acc[x].z * inv, acc[x].w * inv));
+      if (lane == 0) a.LSE[at[x]] = mm[x] > -INFINITY ? (mm[x] + log2f(den[x])) * 0.6931471805599453f : -INFINITY;
+    }
+  }
 }
 
 template <int NT>
@@ -88,8 +217,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ AttnShared sh;
-  float* s_o = reinterpret_cast<float*>(smem + kStages * 2 * kTile);  // [warp][8 columns][kOStride]
-  uint8_t* s_q = smem + kStages * 2 * kTile + kWarps * 8 * kOStride * 4;  // [2][NT * 8][256 bytes]
+  float* s_o = reinterpret_cast<float*>(smem + kStages * 2 * kTile);  // [slot][8 columns][kOStride]
+  uint8_t* s_q = smem + kStages * 2 * kTile + kSlots * 8 * kOStride * 4;  // [2][NT * 8][256 bytes]
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -101,12 +230,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], kWarps);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.j_full[i], kWarps);
+      mbar_init(&sh.j_empty[i], kJoinWarps);
+    }
     mbar_init(&sh.meet, kWarps);
-    sh.abort = 0;
+    mbar_init(&sh.s_free, kWarps);
     fence_barrier_init();
   }
   __syncthreads();
-  volatile int* abort_flag = &sh.abort;
 
   if (warp == kWarps) {
     // ---------------------------------------------------------------- producer
@@ -117,105 +249,106 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t st = 0, st_ph = 0;  // stage and its parity
     int n_item = 0;              // items handed over
     bool ok = true;
-    for (int id = blockIdx.x; ok && id < a.items; id += gridDim.x) {
-      int row, split, g;
-      decode_item(id, a, row, split, g);
-      const int4 info = __ldg(a.rows + row);
-      if (info.x < 0 || info.z % a.tile_rows) continue;
-      const int rows = min(a.tile_rows, info.w);
-      // the item's pages
-      int first, count;
-      if (a.block_idx) {
-        // ids stand at the front of the list: as many as are >= 0
-        first = split * a.per_split;
-        const int32_t* ids = a.block_idx + ((size_t)row * a.G + g) * a.k;
-        int have = 0;
-        for (int j0 = 0; j0 < a.k; j0 += 32) {
-          const int b = j0 + lane < a.k ? __ldg(ids + j0 + lane) : -1;
-          have += __popc(__ballot_sync(0xffffffffu, b >= 0));
+    const int step = gridDim.x;
+    int id = blockIdx.x;
+    Fetch now, next, after;
+    fetch_row(a, id, lane, now);
+    fetch_row(a, id + step, lane, next);
+    fetch_pages(a, lane, now);
+    for (; ok && id < a.items; id += step) {
+      fetch_row(a, id + 2 * step, lane, after);
+      fetch_pages(a, lane, next);
+      if (now.row >= 0) {
+        const int rows = min(a.tile_rows, now.info.w), qs = n_item & 1;
+        if (!mbar_wait(&sh.q_empty[qs], ((n_item >> 1) & 1) ^ 1, a.err, 1401)) { ok = false; break; }
+        if (lane == 0) {
+          sh.item[qs] = {now.row, now.g, now.split, now.pages, now.parts, now.info.y, rows};
+          mbar_arrive_expect_tx(&sh.q_full[qs], rows * a.hg * 256);
+          for (int i = 0; i < rows; ++i)
+            bulk_load(s_q + (qs * NT * 8 + i * a.hg) * 256, a.Q + ((size_t)(now.row + i) * a.Hq + now.g * a.hg) * 128,
+                      a.hg * 256, &sh.q_full[qs]);
         }
-        count = min(a.per_split, have - first);
-      } else {
-        const int last = (info.y + rows - 1) / 128;  // own block of the tile's last row
-        first = a.prefix + split * a.per_split;
-        count = min(a.per_split, last + 1 - first);
-      }
-      if (count <= 0) continue;
-      const int qs = n_item & 1;
-      if (!mbar_wait(&sh.q_empty[qs], ((n_item >> 1) & 1) ^ 1, a.err, 1401)) { ok = false; break; }
-      if (lane == 0) {
-        sh.item[qs] = make_int4(row, g, split, count);
-        sh.info[qs] = info;
-        mbar_arrive_expect_tx(&sh.q_full[qs], rows * a.hg * 256);
-        for (int i = 0; i < rows; ++i)
-          bulk_load(s_q + (qs * NT * 8 + i * a.hg) * 256, a.Q + ((size_t)(row + i) * a.Hq + g * a.hg) * 128,
-                    a.hg * 256, &sh.q_full[qs]);
-      }
-      __syncwarp();
-      ++n_item;
-      for (int j0 = 0; j0 < count && ok; j0 += 32) {
-        const int j = j0 + lane;
-        int block = -1, page = -1;
-        if (j < count) {
-          block = a.block_idx ? __ldg(a.block_idx + ((size_t)row * a.G + g) * a.k + first + j) : first + j;
-          // ids ascend, each one once, up to the row's own block
-          if (a.block_idx &&
-              (block < 0 || block > info.y / 128 ||
-               (first + j > 0 && __ldg(a.block_idx + ((size_t)row * a.G + g) * a.k + first + j - 1) >= block))) {
-            dev_fail(a.err, kDevBadIndex, 1411);
-            block = -1;
+        __syncwarp();
+        ++n_item;
+        for (int j0 = 0; j0 < now.pages && ok; j0 += 32) {
+          int block = now.block, page = now.page, before = now.before;
+          const int j = j0 + lane;
+          if (j0 && j < now.pages) {  // past the fetched ones
+            const int at = now.split * a.per_split + j;
+            const int32_t* ids = a.block_idx ? a.block_idx + ((size_t)now.row * a.G + now.g) * a.k + at : nullptr;
+            block = ids ? __ldg(ids) : a.prefix + at;
+            before = ids ? __ldg(ids - 1) : -1;
+            page = block >= 0 && block < a.max_blocks
+                       ? __ldg(a.page_table + (size_t)now.info.x * a.max_blocks + block)
+                       : -1;
           }
-          if (block >= 0) page = __ldg(a.page_table + (size_t)info.x * a.max_blocks + block);
-          if (block >= 0 && (page < 0 || page >= a.num_pages)) {
-            dev_fail(a.err, kDevBadIndex, 1412);
-            page = -1;
-          }
-        }
-        const int here = min(32, count - j0);
-        for (int i = 0; i < here; ++i) {
-          const int pg = __shfl_sync(0xffffffffu, page, i), bl = __shfl_sync(0xffffffffu, block, i);
-          if (!mbar_wait(&sh.empty[st], st_ph ^ 1, a.err, 1402)) { ok = false; break; }
-          if (lane == 0) {
-            // a page that may not be read counts as one whose tokens all lie behind the row's end
-            sh.token0[st] = pg >= 0 ? bl * 128 : 0x3fffff00;
-            const int y = (max(pg, 0) * a.G + g) * 128;
-            uint8_t* d = smem + st * 2 * kTile;
-            mbar_arrive_expect_tx(&sh.k_full[st], kTile);
-            tma_load_2d(d, &map_k, &sh.k_full[st], 0, y);
-            tma_load_2d(d + kHalf, &map_k, &sh.k_full[st], 64, y);
-            mbar_arrive_expect_tx(&sh.v_full[st], kTile);
-            tma_load_2d(d + kTile, &map_v, &sh.v_full[st], 0, y);
-            tma_load_2d(d + kTile + kHalf, &map_v, &sh.v_full[st], 64, y);
-          }
-          __syncwarp();
-          if (++st == kStages) {
-            st = 0;
-            st_ph ^= 1;
+          if (j < now.pages) page = checked_page(a, now.info, block, before, page);
+          const int here = min(32, now.pages - j0);
+          for (int i = 0; i < here; ++i) {
+            const int pg = __shfl_sync(0xffffffffu, page, i), bl = __shfl_sync(0xffffffffu, block, i);
+            if (!mbar_wait(&sh.empty[st], st_ph ^ 1, a.err, 1402)) { ok = false; break; }
+            if (lane == 0) {
+              // a page that may not be read counts as one whose tokens all lie behind the row's end
+              sh.token0[st] = pg >= 0 ? bl * 128 : 0x3fffff00;
+              const int y = (max(pg, 0) * a.G + now.g) * 128;
+              uint8_t* d = smem + st * 2 * kTile;
+              mbar_arrive_expect_tx(&sh.k_full[st], kTile);
+              tma_load_2d(d, &map_k, &sh.k_full[st], 0, y);
+              tma_load_2d(d + kHalf, &map_k, &sh.k_full[st], 64, y);
+              mbar_arrive_expect_tx(&sh.v_full[st], kTile);
+              tma_load_2d(d + kTile, &map_v, &sh.v_full[st], 0, y);
+              tma_load_2d(d + kTile + kHalf, &map_v, &sh.v_full[st], 64, y);
+            }
+            __syncwarp();
+            if (++st == kStages) {
+              st = 0;
+              st_ph ^= 1;
+            }
           }
         }
       }
+      now = next;
+      next = after;
     }
-    if (!ok) *abort_flag = 1;
-    // the end: an item without pages
+    // the end
     const int qs = n_item & 1;
     if (ok && mbar_wait(&sh.q_empty[qs], ((n_item >> 1) & 1) ^ 1, a.err, 1403)) {
       if (lane == 0) {
-        sh.item[qs] = make_int4(0, 0, 0, 0);
+        sh.item[qs].pages = -1;
         mbar_arrive(&sh.q_full[qs]);
       }
+    }
+  } else if (warp > kWarps) {
+    // ---------------------------------------------------------------- joining warps
+    for (int n_join = 0;; ++n_join) {
+      const int js = n_join & 1;
+      if (!mbar_wait(&sh.j_full[js], (n_join >> 1) & 1, a.err, 1431, kIdleLimitNs)) break;
+      const AttnItem item = sh.join[js];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.j_empty[js]);
+      if (item.parts == 0) break;
+      // each warp counts for itself: the one that finds all parts done joins its columns
+      int done = 0;
+      if (lane == 0) {
+        __threadfence();
+        done = atomicAdd(a.arrived + ((size_t)item.row * a.G + item.g) * kJoinWarps + warp - kWarps - 1, 1);
+      }
+      if (__shfl_sync(0xffffffffu, done, 0) != item.parts - 1) continue;
+      __threadfence();
+      join_parts(a, item, warp - kWarps - 1, lane);
     }
   } else {
     // ---------------------------------------------------------------- consumers
     const int r = lane >> 2, q = lane & 3;
     uint32_t st = 0, st_ph = 0, meet_ph = 0;
+    int n_pass = 0, n_join = 0;  // uses of the O buffers; items handed to the joining warps
     bool ok = true;
     for (int n_item = 0; ok; ++n_item) {
       const int qs = n_item & 1;
       if (!mbar_wait(&sh.q_full[qs], (n_item >> 1) & 1, a.err, 1421)) { ok = false; break; }
-      const int4 item = sh.item[qs], info = sh.info[qs];
-      const int count = item.w;
-      if (count == 0) break;
-      const int rows = min(a.tile_rows, info.w), cols = rows * a.hg;
+      const AttnItem item = sh.item[qs];
+      if (item.pages < 0) break;
+      const int cols = item.rows * a.hg;
       // query fragments: column 8 nt + r, dims 16 ks + 2 q, + 1 and + 8, + 9
       uint32_t qb[NT][8][2];
 #pragma unroll
@@ -235,8 +368,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int z = 0; z < 2; ++z) lim[nt][z] = info.y + 1 + (8 * nt + 2 * q + z) / a.hg;
-      const int lim_lo = info.y + 1;
+        for (int z = 0; z < 2; ++z) lim[nt][z] = item.pos + 1 + (8 * nt + 2 * q + z) / a.hg;
+      const int lim_lo = item.pos + 1;
 
       float m_run[NT][2], l_run[NT][2], o[NT][8][4];
 #pragma unroll
@@ -252,41 +385,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int z = 0; z < 4; ++z) o[nt][mt][z] = 0.f;
       }
 
-      for (int j = 0; j < count; ++j) {
+      for (int j = 0; j < item.pages; ++j) {
         if (!mbar_wait(&sh.k_full[st], st_ph, a.err, 1422)) { ok = false; break; }
-        const int token0 = sh.token0[st];
+        const int token0 = sh.token0[st] + warp * 16;  // of this warp's keys
         const uint32_t kaddr = smem_u32(smem + st * 2 * kTile), vaddr = kaddr + kTile;
-        float sc[2][NT][4];
+        float sc[NT][4], sd[NT][4];  // even and odd steps of the sum over d
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int z = 0; z < 4; ++z) sc[kt][nt][z] = 0.f;
-          const int key = warp * 32 + kt * 16 + (lane & 15);
+          for (int z = 0; z < 4; ++z) sc[nt][z] = sd[nt][z] = 0.f;
+        {
+          const int key = warp * 16 + (lane & 15);
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks) {
             uint32_t f[4];
             ldmatrix_x4(f, kaddr + (ks >> 2) * kHalf + sw128_off(key, (ks & 3) * 2 + (lane >> 4)));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma_16816(sc[kt][nt], f[0], f[1], f[2], f[3], qb[nt][ks][0], qb[nt][ks][1]);
+              mma_16816(ks & 1 ? sd[nt] : sc[nt], f[0], f[1], f[2], f[3], qb[nt][ks][0], qb[nt][ks][1]);
           }
         }
-        const bool masked = token0 + 128 > lim_lo;
+        const bool masked = token0 + 16 > lim_lo;
         float mx[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           mx[nt][0] = mx[nt][1] = -INFINITY;
 #pragma unroll
-          for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              float v = sc[kt][nt][z] * a.scale_log2;
-              if (masked && token0 + warp * 32 + kt * 16 + r + (z >> 1) * 8 >= lim[nt][z & 1]) v = -INFINITY;
-              sc[kt][nt][z] = v;
-              mx[nt][z & 1] = fmaxf(mx[nt][z & 1], v);
-            }
+          for (int z = 0; z < 4; ++z) {
+            float v = (sc[nt][z] + sd[nt][z]) * a.scale_log2;
+            if (masked && token0 + r + (z >> 1) * 8 >= lim[nt][z & 1]) v = -INFINITY;
+            sc[nt][z] = v;
+            mx[nt][z & 1] = fmaxf(mx[nt][z & 1], v);
+          }
         }
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1)
@@ -318,64 +448,54 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // P as hi + lo, turned so that a lane holds two neighbouring keys of one column
-        uint32_t ph[2][NT][2], pl[2][NT][2];
+        uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const float p0 = fast_exp2(sc[kt][nt][2 * y] - base[nt][0]);
-              const float p1 = fast_exp2(sc[kt][nt][2 * y + 1] - base[nt][1]);
-              l_run[nt][0] += p0;
-              l_run[nt][1] += p1;
-              const uint32_t h = pack_bf16(p0, p1);
-              ph[kt][nt][y] = movmatrix_trans(h);
-              pl[kt][nt][y] = movmatrix_trans(pack_bf16(p0 - __uint_as_float(h << 16),
-                                                        p1 - __uint_as_float(h & 0xffff0000u)));
-            }
+          for (int y = 0; y < 2; ++y) {
+            const float p0 = fast_exp2(sc[nt][2 * y] - base[nt][0]);
+            const float p1 = fast_exp2(sc[nt][2 * y + 1] - base[nt][1]);
+            l_run[nt][0] += p0;
+            l_run[nt][1] += p1;
+            const uint32_t h = pack_bf16(p0, p1);
+            ph[nt][y] = movmatrix_trans(h);
+            pl[nt][y] = movmatrix_trans(pack_bf16(p0 - __uint_as_float(h << 16),
+                                                  p1 - __uint_as_float(h & 0xffff0000u)));
+          }
         if (!mbar_wait(&sh.v_full[st], st_ph, a.err, 1423)) { ok = false; break; }
+        const int key = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
         if (!masked) {
 #pragma unroll
-          for (int kt = 0; kt < 2; ++kt) {
-            const int key = warp * 32 + kt * 16 + (lane & 7) + ((lane >> 4) << 3);
+          for (int mt = 0; mt < 8; ++mt) {
+            uint32_t f[4];
+            ldmatrix_x4_trans(f, vaddr + (mt >> 2) * kHalf + sw128_off(key, (mt & 3) * 2 + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_16816(o[nt][mt], f[0], f[1], f[2], f[3], ph[nt][0], ph[nt][1]);
+              mma_16816(o[nt][mt], f[0], f[1], f[2], f[3], pl[nt][0], pl[nt][1]);
+            }
+          }
+        } else {
+          // each row on its own: values behind its end cleared, and only its own columns kept
+#pragma unroll 1
+          for (int i = 0; i < item.rows; ++i) {
+            const int end = lim_lo + i;
+            if (token0 >= end) continue;
+            const int t0 = token0 + 2 * q;  // this lane's keys: t0, t0 + 1 (f0, f1) and t0 + 8, t0 + 9 (f2, f3)
+            const uint32_t keep0 = (t0 < end ? 0xffffu : 0u) | (t0 + 1 < end ? 0xffff0000u : 0u);
+            const uint32_t keep1 = (t0 + 8 < end ? 0xffffu : 0u) | (t0 + 9 < end ? 0xffff0000u : 0u);
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
               uint32_t f[4];
               ldmatrix_x4_trans(f, vaddr + (mt >> 2) * kHalf + sw128_off(key, (mt & 3) * 2 + ((lane >> 3) & 1)));
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                mma_16816(o[nt][mt], f[0], f[1], f[2], f[3], ph[kt][nt][0], ph[kt][nt][1]);
-                mma_16816(o[nt][mt], f[0], f[1], f[2], f[3], pl[kt][nt][0], pl[kt][nt][1]);
-              }
-            }
-          }
-        } else {
-          // each row on its own: values behind its end cleared, and only its own columns kept
-#pragma unroll 1
-          for (int i = 0; i < rows; ++i) {
-            const int end = lim_lo + i;
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_16816(t, f[0] & keep0, f[1] & keep0, f[2] & keep1, f[3] & keep1, ph[nt][0], ph[nt][1]);
+                mma_16816(t, f[0] & keep0, f[1] & keep0, f[2] & keep1, f[3] & keep1, pl[nt][0], pl[nt][1]);
 #pragma unroll
-            for (int kt = 0; kt < 2; ++kt) {
-              const int kbase = token0 + warp * 32 + kt * 16;
-              if (kbase >= end) continue;
-              const int key = warp * 32 + kt * 16 + (lane & 7) + ((lane >> 4) << 3);
-              const int t0 = kbase + 2 * q;  // this lane's keys: t0, t0 + 1 (f0, f1) and t0 + 8, t0 + 9 (f2, f3)
-              const uint32_t keep0 = (t0 < end ? 0xffffu : 0u) | (t0 + 1 < end ? 0xffff0000u : 0u);
-              const uint32_t keep1 = (t0 + 8 < end ? 0xffffu : 0u) | (t0 + 9 < end ? 0xffff0000u : 0u);
-#pragma unroll
-              for (int mt = 0; mt < 8; ++mt) {
-                uint32_t f[4];
-                ldmatrix_x4_trans(f, vaddr + (mt >> 2) * kHalf + sw128_off(key, (mt & 3) * 2 + ((lane >> 3) & 1)));
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  float t[4] = {0.f, 0.f, 0.f, 0.f};
-                  mma_16816(t, f[0] & keep0, f[1] & keep0, f[2] & keep1, f[3] & keep1, ph[kt][nt][0], ph[kt][nt][1]);
-                  mma_16816(t, f[0] & keep0, f[1] & keep0, f[2] & keep1, f[3] & keep1, pl[kt][nt][0], pl[kt][nt][1]);
-#pragma unroll
-                  for (int z = 0; z < 4; ++z)
-                    if ((8 * nt + 2 * q + (z & 1)) / a.hg == i) o[nt][mt][z] += t[z];
-                }
+                for (int z = 0; z < 4; ++z)
+                  if (lim[nt][z & 1] == end) o[nt][mt][z] += t[z];
               }
             }
           }
@@ -389,95 +509,132 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
 
-      // ---- the four warps' results meet, eight columns at a time
+      // ---- the warps' results meet, eight columns at a time: the upper four warps store theirs, the lower four add
+      // them to their own, and all 256 threads add up the four sums
+      const bool joined = a.join && item.parts > 1;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt, ++n_pass) {
+        float l[2];
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-          float l = l_run[nt][z];
+          l[z] = l_run[nt][z];
 #pragma unroll
-          for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-          if (r == 0) {
-            sh.m[warp][8 * nt + 2 * q + z] = m_run[nt][z];
-            sh.l[warp][8 * nt + 2 * q + z] = l;
-          }
+          for (int x = 4; x < 32; x <<= 1) l[z] += __shfl_xor_sync(0xffffffffu, l[z], x);
         }
+        const int slot = warp & (kSlots - 1);
+        float* mine = s_o + slot * 8 * kOStride;
+        auto place = [&](int mt, int z) { return (2 * q + (z & 1)) * kOStride + mt * 16 + r + (z >> 1) * 8; };
+        if (!mbar_wait(&sh.s_free, (n_pass & 1) ^ 1, a.err, 1424)) { ok = false; break; }
+        if (warp >= kSlots) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float* mine = s_o + warp * 8 * kOStride;
+          for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
-        for (int mt = 0; mt < 8; ++mt)
+            for (int z = 0; z < 4; ++z) mine[place(mt, z)] = o[nt][mt][z];
+          if (r == 0) {
 #pragma unroll
-          for (int z = 0; z < 4; ++z) mine[(2 * q + (z & 1)) * kOStride + mt * 16 + r + (z >> 1) * 8] = o[nt][mt][z];
-        if (!warps_sync(&sh.meet, meet_ph, a.err, 1424)) { ok = false; break; }
-        const int d = threadIdx.x;  // 128 consumers: one dim each
-        for (int c = 0; c < 8; ++c) {
-          const int col = 8 * nt + c;
-          if (col >= cols) break;
-          float mm = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sh.m[w][col]);
-          float num = 0.f, den = 0.f;
-          if (mm > -INFINITY) {
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-              const float f = fast_exp2(sh.m[w][col] - mm);
-              num = fmaf(f, s_o[(w * 8 + c) * kOStride + d], num);
-              den = fmaf(f, sh.l[w][col], den);
+            for (int z = 0; z < 2; ++z) {
+              sh.m[0][slot][2 * q + z] = m_run[nt][z];
+              sh.l[0][slot][2 * q + z] = l[z];
             }
           }
-          const int row = item.x + col / a.hg, head = item.y * a.hg + col % a.hg;
-          const size_t at = ((size_t)(a.slot0 + item.z) * a.N + row) * a.Hq + head;
-          a.part_o[at * 128 + d] = mm > -INFINITY ? num / den : 0.f;
-          if (d == 0) a.part_lse[at] = mm > -INFINITY ? mm + log2f(den) : -INFINITY;
         }
         if (!warps_sync(&sh.meet, meet_ph, a.err, 1425)) { ok = false; break; }
+        if (warp < kSlots) {
+          float f[2], g[2];
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const float m2 = sh.m[0][slot][2 * q + z], mm = fmaxf(m_run[nt][z], m2);
+            f[z] = m_run[nt][z] == -INFINITY ? 0.f : fast_exp2(m_run[nt][z] - mm);
+            g[z] = m2 == -INFINITY ? 0.f : fast_exp2(m2 - mm);
+            if (r == 0) {
+              sh.m[1][slot][2 * q + z] = mm;
+              sh.l[1][slot][2 * q + z] = fmaf(l[z], f[z], sh.l[0][slot][2 * q + z] * g[z]);
+            }
+          }
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              float& at = mine[place(mt, z)];
+              at = fmaf(o[nt][mt][z], f[z & 1], at * g[z & 1]);
+            }
+        }
+        if (!warps_sync(&sh.meet, meet_ph, a.err, 1426)) { ok = false; break; }
+        const int d = threadIdx.x & 127;  // one dim, four columns
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int cc = (threadIdx.x >> 7) * 4 + c, col = 8 * nt + cc;
+          if (col >= cols) break;
+          float mm = sh.m[1][0][cc];
+#pragma unroll
+          for (int w = 1; w < kSlots; ++w) mm = fmaxf(mm, sh.m[1][w][cc]);
+          float num = 0.f, den = 0.f;
+#pragma unroll
+          for (int w = 0; w < kSlots; ++w) {
+            const float mw = sh.m[1][w][cc], f = mw == -INFINITY ? 0.f : fast_exp2(mw - mm);
+            den = fmaf(f, sh.l[1][w][cc], den);
+            num = fmaf(f, s_o[(w * 8 + cc) * kOStride + d], num);
+          }
+          const float val = mm > -INFINITY ? num / den : 0.f;
+          const float lse = mm > -INFINITY ? mm + log2f(den) : -INFINITY;
+          const size_t at = (size_t)(item.row + col / a.hg) * a.Hq + item.g * a.hg + col % a.hg;
+          if (a.join && !joined) {
+            a.O[at * 128 + d] = __float2bfloat16_rn(val);
+            if (d == 0) a.LSE[at] = lse * 0.6931471805599453f;
+          } else {
+            const size_t pt = (size_t)(a.slot0 + item.split) * a.N * a.Hq + at;
+            a.part_o[pt * 128 + d] = val;
+            if (d == 0) a.part_lse[pt] = lse;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.s_free);
+      }
+      if (!ok) break;
+      if (joined) {
+        const int js = n_join & 1;
+        if (!mbar_wait(&sh.j_empty[js], ((n_join >> 1) & 1) ^ 1, a.err, 1427)) { ok = false; break; }
+        if (threadIdx.x == 0) sh.join[js] = item;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.j_full[js]);
+        ++n_join;
       }
     }
-    if (!ok) *abort_flag = 1;
+    // the joining warps' end
+    const int js = n_join & 1;
+    if (mbar_wait(&sh.j_empty[js], ((n_join >> 1) & 1) ^ 1, a.err, 1428)) {
+      if (threadIdx.x == 0) sh.join[js].parts = 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.j_full[js]);
+    }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Joins a row's partials: the shared prefix's (one per run of pages that
-// reaches into the group's) and the own pages' splits, in that order.
+// Joins a row's parts behind a shared prefix: the prefix's (one per run of
+// pages that reaches into the group's) and the own pages' splits, in that order.
 struct MergeArgs {
   const int4* rows;
-  const int32_t* block_idx;
   const float *part_o, *part_lse;
   __nv_bfloat16* O;
   float* LSE;
-  int N, Hq, G, hg, k, prefix, per_split, tile_rows, teams, pslots;
+  int N, Hq, G, hg, prefix, per_split, tile_rows, teams, pslots;
 };
 
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 128;
 
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(MergeArgs a) {
+__global__ void __launch_bounds__(kMergeThreads, 8) paged_merge_kernel(MergeArgs a) {
   const int lane = threadIdx.x % 32;
   const long long item = (long long)blockIdx.x * (kMergeThreads / 32) + threadIdx.x / 32;
   if (item >= (long long)a.N * a.Hq) return;
   const int row = (int)(item / a.Hq), head = (int)(item % a.Hq), g = head / a.hg;
   const int4 info = __ldg(a.rows + row);
   if (info.x < 0) return;  // behind the last sequence, or left out
-  int own;                 // partials of the own pages
-  if (a.block_idx) {
-    int have = 0;
-    for (int j0 = 0; j0 < a.k; j0 += 32) {
-      const int b = j0 + lane < a.k ? __ldg(a.block_idx + ((size_t)row * a.G + g) * a.k + j0 + lane) : -1;
-      have += __popc(__ballot_sync(0xffffffffu, b >= 0));
-    }
-    own = (have + a.per_split - 1) / a.per_split;
-  } else {
-    // the tile's last row decides how far its items went
-    const int lead = info.z % a.tile_rows, rows = min(a.tile_rows, info.w + lead);
-    const int last = (info.y - lead + rows - 1) / 128;
-    own = (last - a.prefix) / a.per_split + 1;
-  }
-  int shared_parts = 0;
-  if (a.teams) {
-    const int units = a.G * a.prefix;
-    shared_parts = team_of((g + 1) * a.prefix - 1, units, a.teams) - team_of(g * a.prefix, units, a.teams) + 1;
-  }
+  // the tile's last row decides how far its items went
+  const int lead = info.z % a.tile_rows, rows = min(a.tile_rows, info.w + lead);
+  const int own = ((info.y - lead + rows - 1) / 128 - a.prefix) / a.per_split + 1;
+  const int units = a.G * a.prefix;
+  const int shared_parts = team_of((g + 1) * a.prefix - 1, units, a.teams) - team_of(g * a.prefix, units, a.teams) + 1;
   const int n = shared_parts + own;
   const size_t step = (size_t)a.N * a.Hq;
   auto slot = [&](int i) { return (size_t)(i < shared_parts ? i : a.pslots + i - shared_parts) * step + item; };
@@ -487,22 +644,21 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(MergeArgs a)
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float den = 0.f;
-  if (m > -INFINITY) {
-    for (int i = 0; i < n; ++i) {
-      const size_t at = slot(i);
-      const float w = fast_exp2(__ldg(a.part_lse + at) - m);
-      const float4 v = __ldg(reinterpret_cast<const float4*>(a.part_o + at * 128) + lane);
-      den += w;
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z);
-      acc.w = fmaf(w, v.w, acc.w);
-    }
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) {
+    const size_t at = slot(i);
+    const float w = fast_exp2(__ldg(a.part_lse + at) - m);
+    const float4 v = __ldg(reinterpret_cast<const float4*>(a.part_o + at * 128) + lane);
+    den += w;
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
   }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
-  uint2 out = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  const float inv = 1.f / den;
+  const uint2 out = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
   reinterpret_cast<uint2*>(a.O + (size_t)item * 128)[lane] = out;
-  if (lane == 0) a.LSE[item] = m > -INFINITY ? (m + log2f(den)) * 0.6931471805599453f : -INFINITY;
+  if (lane == 0) a.LSE[item] = (m + log2f(den)) * 0.6931471805599453f;
 }
 
 template <int NT>
@@ -553,16 +709,19 @@ cudaError_t launch_paged_attn(const PagedProb& p, const PagedCachePtrs& c, const
   a.tile_rows = L.tile_rows;
   a.items = p.N * L.splits * p.G;  // at most 2^28: more than one split only where N * G is small
   a.slot0 = L.pslots;
+  a.join = L.pslots == 0;
+  a.arrived = reinterpret_cast<int*>(ws + L.arrived);
+  a.O = static_cast<__nv_bfloat16*>(O);
+  a.LSE = LSE;
   a.scale_log2 = p.scale * kLog2e;
   a.err = reinterpret_cast<int*>(ws);
   return L.tile_rows * p.hg > 8 ? launch_attn<2>(a, mk, mv, st) : launch_attn<1>(a, mk, mv, st);
 }
 
-cudaError_t launch_paged_merge(const PagedProb& p, const int32_t* block_idx, void* O, float* LSE, uint8_t* ws,
-                               const PagedWs& L, cudaStream_t st) {
+cudaError_t launch_paged_merge(const PagedProb& p, void* O, float* LSE, uint8_t* ws, const PagedWs& L,
+                               cudaStream_t st) {
   MergeArgs a;
   a.rows = reinterpret_cast<const int4*>(ws + L.rows);
-  a.block_idx = block_idx;
   a.part_o = reinterpret_cast<const float*>(ws + L.part_o);
   a.part_lse = reinterpret_cast<const float*>(ws + L.part_lse);
   a.O = static_cast<__nv_bfloat16*>(O);
@@ -571,14 +730,13 @@ cudaError_t launch_paged_merge(const PagedProb& p, const int32_t* block_idx, voi
   a.Hq = p.Hq;
   a.G = p.G;
   a.hg = p.hg;
-  a.k = p.k;
   a.prefix = p.prefix;
   a.per_split = L.per_split;
   a.tile_rows = L.tile_rows;
   a.teams = L.teams;
   a.pslots = L.pslots;
   const long long items = (long long)p.N * p.Hq;
-  paged_merge_kernel<<<(unsigned)((items + 7) / 8), kMergeThreads, 0, st>>>(a);
+  paged_merge_kernel<<<(unsigned)((items + 3) / 4), kMergeThreads, 0, st>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }

@@ -14,6 +14,12 @@
 // row sum is taken before the rounding. The running maximum moves only when a
 // page raises it by more than 2^8 (an O_t rescale is a TMEM round trip).
 //
+// What bounds it is the chain S -> softmax -> PV -> next S of a tile: its two
+// products take 1,024 cycles, and the softmax has to fit into the other tile's
+// 1,024. So two warps share each row, 64 keys each: they compute P under the
+// maximum they have and only then look at each other's page maximum (by shared
+// memory); a page that raises it is computed again.
+//
 // Work: all (group, page) pairs in a line, cut into `teams` runs of equal
 // length; a run is walked by `pairs` CTAs at once, one per pair of tiles, so
 // that a page is read from HBM once and from L2 by the others. A run leaves
@@ -26,7 +32,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kHeadroom = 8.f;  // P = exp2(s - m) stays <= 2^kHeadroom
-constexpr int kThreads = 320;     // warp 0 TMA, warp 1 UMMA + TMEM, warps 2-5 and 6-9 softmax of tiles 0 and 1
+constexpr int kThreads = 640;     // warp 0 TMA, warp 1 UMMA + TMEM; warps 4-11 and 12-19 softmax of tiles 0 and 1
 constexpr int kTile = 32768;      // 128 rows x 128 bf16, two 64-column SW128 chunks
 constexpr int kChunk = 16384;
 constexpr int kStages = 2;        // K/V ring
@@ -35,9 +41,9 @@ constexpr int kSmem = oV + kStages * kTile + 1024;
 
 struct PrefixArgs {
   const int4* rows;
-  const int32_t* page_table;
+  const int32_t *page_table, *row_start;
   float *part_o, *part_lse;
-  int N, Hq, G, hg, prefix, pairs, teams, num_pages, max_blocks;
+  int S, N, Hq, G, hg, prefix, pairs, teams, num_pages, max_blocks;
   float scale_log2;
   int* err;
 };
@@ -46,8 +52,10 @@ struct PrefixShared {
   uint64_t q_full, q_empty;
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t pair[2][4];           // the two warps of a tile's 32 rows
+  float row_max[2][2][2][128];   // [page parity][tile][half][row]
+  int raised[2][2][2][4];        // [page parity][tile][half][quarter]: some row's maximum moves
   uint32_t tmem_base;
-  int abort;
 };
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -76,9 +84,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.p_full[i], 8);
       mbar_init(&sh.o_full[i], 1);
-      mbar_init(&sh.o_free[i], 4);
+      mbar_init(&sh.o_free[i], 8);
+      for (int j = 0; j < 4; ++j) mbar_init(&sh.pair[i][j], 2);
     }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sh.k_full[i], 1);
@@ -88,7 +97,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, 1);
-    sh.abort = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -158,30 +166,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       constexpr uint32_t id_s = make_idesc_bf16(128, 128, false, false);  // Q, K both K-major
       constexpr uint32_t id_o = make_idesc_bf16(128, 128, false, true);   // P from TMEM, V MN-major
-      const uint32_t q0 = smem_u32(smem + oQ);
+      // the operands' descriptors as 32-bit words: one add per instruction, so that the issuing thread keeps up
+      constexpr uint32_t hi = sdesc_hi_sw128_sbo1024();
+      const uint32_t q_lo = sdesc_lo(smem_u32(smem + oQ), 16), k_lo = sdesc_lo(smem_u32(smem + oK), 16);
+      const uint32_t v_lo = sdesc_lo(smem_u32(smem + oV), kChunk);
       uint32_t kc = 0;
       bool ok = true;
       auto issue_s = [&](int t, int st) {
-        const uint32_t qa = q0 + t * kTile, ka = smem_u32(smem + oK + st * kTile);
+        const uint32_t qa = q_lo + t * (kTile >> 4), ka = k_lo + st * (kTile >> 4), d = tmem + t * 128;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-          const uint32_t off = (ks >> 2) * kChunk + (ks & 3) * 32;
-          umma_bf16_ss(tmem + t * 128, make_sdesc(qa + off, 16, 1024, kSw128), make_sdesc(ka + off, 16, 1024, kSw128),
-                       id_s, ks > 0);
+          const uint32_t off = ((ks >> 2) * kChunk + (ks & 3) * 32) >> 4;
+          umma_bf16_ss_w(d, qa + off, ka + off, hi, id_s, ks > 0);
         }
         umma_commit(&sh.s_full[t]);
       };
       auto issue_o = [&](int t, int st, bool acc) {
-        const uint32_t va = smem_u32(smem + oV + st * kTile);
+        const uint32_t va = v_lo + st * (kTile >> 4), d = tmem + 256 + t * 128, p = tmem + t * 128;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          umma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + ks * 8, make_sdesc(va + ks * 2048, kChunk, 1024, kSw128),
-                       id_o, acc || ks > 0);
+          umma_bf16_ts_w(d, p + (ks >> 2) * 64 + (ks & 3) * 8, va + ks * (2048 >> 4), hi, id_o, ks > 0 ? 1u : (uint32_t)acc);
       };
       int seg = 0;
       for (int u = u_begin; u < u_end && ok; ++seg) {
         const int g = u / a.prefix, stop = min(u_end, (g + 1) * a.prefix), pages = stop - u;
-        if (!mbar_wait(&sh.q_full, seg & 1, a.err, 1512)) { ok = false; break; }
+        if (!mbar_wait(&sh.q_full, seg & 1, a.err, 1520)) { ok = false; break; }
         {
           const int st = kc % kStages;
           if (!mbar_wait(&sh.k_full[st], (kc / kStages) & 1, a.err, 1513)) { ok = false; break; }
@@ -195,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int st = kc % kStages, st1 = (kc + 1) % kStages;
           const uint32_t par = (kc / kStages) & 1, par1 = ((kc + 1) / kStages) & 1;
           const bool last = c == pages - 1;
-#pragma unroll 1
+#pragma unroll
           for (int t = 0; t < 2; ++t) {
             // P_t of this page written (and O_t rescaled if its row maximum moved)
             if (!mbar_wait(&sh.p_full[t], kc & 1, a.err, 1514 + t)) { ok = false; break; }
@@ -221,88 +230,126 @@ __global__ void __launch_bounds__(kThreads, 1)
         u = stop;
       }
     }
-  } else {
-    // ---------------------------------------------------------------- softmax (thread = one head of one new row)
-    const int t = (warp - 2) >> 2;
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- softmax (thread = one head of one new row, 64 keys)
+    const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;
     const int quarter = warp & 3;
     const int lrow = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t s_col = t * 128, o_col = 256 + t * 128;
+    const uint32_t s_at = tmem + lane_off + t * 128 + half * 64;        // this warp's scores, and P over their first half
+    const uint32_t o_at = tmem + lane_off + 256 + t * 128 + half * 64;  // the columns of O that it rescales and reads out
     const int row = (2 * pair + t) * tile_rows + lrow / a.hg;
-    uint32_t kc = 0;
+    {
+      // while the first pages are on their way: is the prefix the same one for every sequence with rows?
+      bool bad = false;
+      const long long cells = (long long)a.S * a.prefix;
+      for (long long i = (long long)blockIdx.x * 512 + threadIdx.x - 128; i < cells; i += (long long)gridDim.x * 512) {
+        const int s = (int)(i / a.prefix), c = (int)(i % a.prefix);
+        const int32_t* table = a.page_table + c;
+        if (__ldg(a.row_start + s + 1) > __ldg(a.row_start + s))
+          bad |= __ldg(table + (size_t)s * a.max_blocks) != __ldg(table + (size_t)ref * a.max_blocks);
+      }
+      if (bad) dev_fail(a.err, kDevBadIndex, 1512);
+    }
+    uint32_t kc = 0, pair_ph = 0;
     bool ok = true;
     int seg = 0;
     for (int u = u_begin; u < u_end && ok; ++seg) {
       const int g = u / a.prefix, stop = min(u_end, (g + 1) * a.prefix), pages = stop - u;
-      float m_run = -INFINITY, l_run = 0.f;
+      float m_run = -INFINITY, l_run = 0.f;  // the maximum is the row's, the sum that of this warp's keys
       for (int c = 0; c < pages; ++c, ++kc) {
         if (!mbar_wait(&sh.s_full[t], kc & 1, a.err, 1522 + t)) { ok = false; break; }
         tc_fence_after();
-        float sv[128], mq[4];
-#pragma unroll
-        for (int z = 0; z < 4; ++z)
-          tmem_ld32_max(tmem + lane_off + s_col + z * 32, *reinterpret_cast<float(*)[32]>(sv + 32 * z), mq[z]);
+        float sv[64], mq[2];
+        tmem_ld32_max(s_at, *reinterpret_cast<float(*)[32]>(sv), mq[0]);
+        tmem_ld32_max(s_at + 32, *reinterpret_cast<float(*)[32]>(sv + 32), mq[1]);
         tmem_wait_ld();
-        const float m_blk = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * a.scale_log2;
-        const bool need = m_blk > m_run + kHeadroom;
-        if (__any_sync(0xffffffffu, need)) {
-          const float alpha = need ? fast_exp2(m_run - m_blk) : 1.f;
-          if (need) m_run = m_blk;
+        const float m_blk = fmaxf(mq[0], mq[1]) * a.scale_log2;
+        const int b = kc & 1;
+        const bool raised = __any_sync(0xffffffffu, m_blk > m_run + kHeadroom);
+        sh.row_max[b][t][half][lrow] = m_blk;
+        if (lane == 0) sh.raised[b][t][half][quarter] = raised;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.pair[t][quarter]);
+        float l_add = 0.f;
+        auto write_p = [&]() {
+          float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t pk[8];
+#pragma unroll
+            for (int z = 0; z < 8; ++z) {
+              const float p0 = fast_exp2(fmaf(sv[16 * h + 2 * z], a.scale_log2, -m_run));
+              const float p1 = fast_exp2(fmaf(sv[16 * h + 2 * z + 1], a.scale_log2, -m_run));
+              l4[(2 * z) & 3] += p0;
+              l4[(2 * z + 1) & 3] += p1;
+              pk[z] = pack_bf16(p0, p1);
+            }
+            tmem_st8(s_at + 8 * h, pk);
+          }
+          l_add = (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        };
+        if (c > 0 && !raised) write_p();
+        if (!mbar_wait(&sh.pair[t][quarter], pair_ph, a.err, 1526 + t)) { ok = false; break; }
+        pair_ph ^= 1u;
+        if (raised || sh.raised[b][t][half ^ 1][quarter]) {
+          const float m_new = fmaxf(m_blk, sh.row_max[b][t][half ^ 1][lrow]);
+          const bool need = m_new > m_run + kHeadroom;
+          const float alpha = need ? fast_exp2(m_run - m_new) : 1.f;
+          if (need) m_run = m_new;
           l_run *= alpha;
           if (c > 0) {
+            // O_t to the new maximum: PV_t of the previous page is done (it was issued before this page's S_t)
 #pragma unroll 1
-            for (int z = 0; z < 4; ++z) {
-              float o[32];
-              tmem_ld32(tmem + lane_off + o_col + z * 32, o);
+            for (int z = 0; z < 8; ++z) {
+              float o[8];
+              tmem_ld8(o_at + z * 8, o);
               tmem_wait_ld();
-              uint32_t ob[32];
+              uint32_t ob[8];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) ob[i] = __float_as_uint(o[i] * alpha);
-              tmem_st32(tmem + lane_off + o_col + z * 32, ob);
+              for (int i = 0; i < 8; ++i) ob[i] = __float_as_uint(o[i] * alpha);
+              tmem_st8(o_at + z * 8, ob);
             }
-            tmem_wait_st();
           }
-        }
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int z = 0; z < 32; ++z) {
-            const float p0 = fast_exp2(fmaf(sv[64 * h + 2 * z], a.scale_log2, -m_run));
-            const float p1 = fast_exp2(fmaf(sv[64 * h + 2 * z + 1], a.scale_log2, -m_run));
-            l4[(2 * z) & 3] += p0;
-            l4[(2 * z + 1) & 3] += p1;
-            pk[z] = pack_bf16(p0, p1);
-          }
-          tmem_st32(tmem + lane_off + s_col + 32 * h, pk);
+          write_p();
         }
         tmem_wait_st();
-        l_run += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        l_run += l_add;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_full[t]);
       }
       if (!ok) break;
       // ---- the run's end in this group: the row's partial
+      sh.row_max[kc & 1][t][half][lrow] = l_run;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.pair[t][quarter]);
+      if (!mbar_wait(&sh.pair[t][quarter], pair_ph, a.err, 1528 + t)) { ok = false; break; }
+      pair_ph ^= 1u;
+      const float l = half ? sh.row_max[kc & 1][t][0][lrow] + l_run : l_run + sh.row_max[kc & 1][t][1][lrow];
+      // the next group's first page writes the buffer of this parity again
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.pair[t][quarter]);
+      if (!mbar_wait(&sh.pair[t][quarter], pair_ph, a.err, 1530 + t)) { ok = false; break; }
+      pair_ph ^= 1u;
       if (!mbar_wait(&sh.o_full[t], seg & 1, a.err, 1524 + t)) { ok = false; break; }
       tc_fence_after();
       const int slot = team - team_of(g * a.prefix, units, a.teams);
       const size_t at = ((size_t)slot * a.N + row) * a.Hq + g * a.hg + lrow % a.hg;
-      const float inv = 1.f / l_run;
-      float4* dst = reinterpret_cast<float4*>(a.part_o + at * 128);
+      const float inv = 1.f / l;
+      float4* dst = reinterpret_cast<float4*>(a.part_o + at * 128 + half * 64);
 #pragma unroll
       for (int z = 0; z < 4; ++z) {
-        float o[32];
-        tmem_ld32(tmem + lane_off + o_col + z * 32, o);
+        float o[16];
+        tmem_ld16(o_at + z * 16, o);
         tmem_wait_ld();
         if (row < a.N) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[8 * z + i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+          for (int i = 0; i < 4; ++i)
+            dst[4 * z + i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
         }
       }
-      if (row < a.N) a.part_lse[at] = m_run + log2f(l_run);
+      if (row < a.N && half == 0) a.part_lse[at] = m_run + log2f(l);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.o_free[t]);
@@ -332,6 +379,8 @@ cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, con
   PrefixArgs a;
   a.rows = reinterpret_cast<const int4*>(ws + L.rows);
   a.page_table = c.page_table;
+  a.row_start = c.row_start;
+  a.S = p.S;
   a.part_o = reinterpret_cast<float*>(ws + L.part_o);
   a.part_lse = reinterpret_cast<float*>(ws + L.part_lse);
   a.N = p.N;

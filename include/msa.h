@@ -318,7 +318,7 @@ MSA_API msa_status msa_dense_bwd(const msa_shape *shape, const void *Q, const vo
  * (or, with a shared prefix, inside the prefix), a page id outside
  * [0, num_pages), prefix pages that differ between sequences, or a block list
  * that is not ascending ids up to the row's own block sets the error word, and
- * the outputs of the rows concerned (of every row, for the prefix) are
+ * the outputs of the sequences concerned (of all, for the prefix) are
  * unspecified; nothing is read or written out of range.
  *
  * Supported: d = 128, d_idx = 64, Bk = 128, Hq / G in {1, 2, 4, 8},

@@ -205,6 +205,28 @@ def test_selection_at_narrow_borders(msa, k):
         np.testing.assert_array_equal(bi[r], ref.select(b, r, k), err_msg=f"row {r}")
 
 
+def test_selection_with_one_large_component(msa):
+    """One product of a score dwarfs the others, which a sum that starts with it cuts off: what decides between the
+    blocks lies below its fp32 step."""
+    import torch
+
+    b = ref.Batch(counts=[2, 1], lens=[128 * 60 + 9, 128 * 77], Hq=2, G=2, seed=14)
+    gen = torch.Generator().manual_seed(3)
+
+    def small(*shape):
+        return (2.0 ** -12 * (1 + torch.rand(*shape, generator=gen))).to(torch.bfloat16)
+
+    for s in range(2):
+        for c in range(60 + 17 * s):
+            b.k_idx[int(b.table[s, c])] = small(128, 64)
+            b.k_idx[int(b.table[s, c]), :, 0] = 1.0
+    b.q_idx[:b.n] = small(b.n, 2, 64)
+    b.q_idx[:b.n, :, 0] = 1.0
+    _, _, bi = _sparse(msa, b, 9)
+    for r in range(b.n):
+        np.testing.assert_array_equal(bi[r], ref.select(b, r, 9), err_msg=f"row {r}")
+
+
 def test_selection_with_nan_and_infinite_index_values(msa):
     """A NaN score counts as -infinity; infinite scores order as they are; huge ones do not overflow."""
     b = ref.Batch(counts=[1, 2, 1, 1], lens=[128 * 12 + 7] * 4, Hq=2, G=2, seed=12)
