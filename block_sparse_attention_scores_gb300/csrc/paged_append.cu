@@ -12,6 +12,7 @@
 // row: a row's K, V, Q and index vectors are cut into items of two 16-byte
 // pieces (the two halves of eight pairs, or two neighbours), one thread each.
 #include "paged.h"
+#include "pdl.cuh"
 #include "sm100.cuh"
 
 namespace msa {
@@ -206,13 +207,15 @@ __device__ __forceinline__ int bisect_rows(const int32_t* row_start, int S, int 
   int lo = 0, hi = S + 1;  // row_start[lo] <= r (row_start[0] counts as 0), row_start[hi] > r
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(row_start + mid) <= r) lo = mid;
+    if (ld_in(row_start + mid) <= r) lo = mid;
     else hi = mid;
   }
   return lo;
 }
 
 __global__ void __launch_bounds__(kThreads) paged_rows_kernel(RowsArgs a) {
+  pdl_release();
+  pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x < 64) a.err[threadIdx.x] = 0;
   const int r = blockIdx.x * kThreads + threadIdx.x;
   if (r >= a.N) return;
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(RowsArgs a) {
   const int s = bisect_rows(a.row_start, a.S, r);
   int4 out = make_int4(-1, 0, 0, 0);
   if (s < a.S) {
-    const int len = __ldg(a.seq_len + s), begin = __ldg(a.row_start + s), end = __ldg(a.row_start + s + 1);
+    const int len = ld_in(a.seq_len + s), begin = ld_in(a.row_start + s), end = ld_in(a.row_start + s + 1);
     if (len < end - r + a.prefix * 128 || len > a.max_blocks * 128)
       out.x = -2;
     else
@@ -266,9 +269,8 @@ cudaError_t launch_paged_rows(const PagedProb& p, const PagedCachePtrs& c, uint8
   a.G = p.G;
   a.max_blocks = p.max_blocks;
   a.prefix = p.prefix;
-  paged_rows_kernel<<<(p.N + kThreads - 1) / kThreads, kThreads, 0, st>>>(a);
   count_launches(1);
-  return cudaGetLastError();
+  return launch_dependent(paged_rows_kernel, (p.N + kThreads - 1) / kThreads, kThreads, 0, st, a);
 }
 
 }  // namespace msa

@@ -22,6 +22,7 @@
 // tokens, stale cache lines, NaN or infinities) reaches it through 0 * x.
 #include "mma_sync.cuh"
 #include "paged.h"
+#include "pdl.cuh"
 #include "sm100.cuh"
 
 namespace msa {
@@ -111,14 +112,14 @@ __device__ __forceinline__ void fetch_row(const AttnArgs& a, int item, int lane,
   const int t = item / a.G;
   f.split = t % a.splits;
   f.row = t / a.splits;
-  f.info = __ldg(a.rows + f.row);
+  f.info = ld_in(a.rows + f.row);
   if (a.block_idx) {
     const int32_t* ids = a.block_idx + ((size_t)f.row * a.G + f.g) * a.k;
     const int at = f.split * a.per_split + lane;
-    f.id = at < a.k ? __ldg(ids + at) : -1;
-    f.before = at > 0 && at < a.k ? __ldg(ids + at - 1) : -1;
+    f.id = at < a.k ? ld_in(ids + at) : -1;
+    f.before = at > 0 && at < a.k ? ld_in(ids + at - 1) : -1;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) f.ids[c] = c * 32 + lane < a.k ? __ldg(ids + c * 32 + lane) : -1;
+    for (int c = 0; c < 4; ++c) f.ids[c] = c * 32 + lane < a.k ? ld_in(ids + c * 32 + lane) : -1;
   }
 }
 
@@ -149,7 +150,7 @@ __device__ __forceinline__ void fetch_pages(const AttnArgs& a, int lane, Fetch& 
   }
   if (f.row < 0 || lane >= f.pages) f.block = -1;
   else if (f.block >= 0 && f.block <= f.info.y / 128 + a.tile_rows)
-    f.page = __ldg(a.page_table + (size_t)f.info.x * a.max_blocks + min(f.block, a.max_blocks - 1));
+    f.page = ld_in(a.page_table + (size_t)f.info.x * a.max_blocks + min(f.block, a.max_blocks - 1));
 }
 
 // The page as it was read, or -1 (reported) where it may not be: ids ascend up to the row's own block, pages lie in
@@ -237,15 +238,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.meet, kWarps);
     mbar_init(&sh.s_free, kWarps);
     fence_barrier_init();
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
   }
+  pdl_release();
   __syncthreads();
+  pdl_wait();
 
   if (warp == kWarps) {
     // ---------------------------------------------------------------- producer
-    if (lane == 0) {
-      tma_prefetch_desc(&map_k);
-      tma_prefetch_desc(&map_v);
-    }
     uint32_t st = 0, st_ph = 0;  // stage and its parity
     int n_item = 0;              // items handed over
     bool ok = true;
@@ -276,10 +277,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j0 && j < now.pages) {  // past the fetched ones
             const int at = now.split * a.per_split + j;
             const int32_t* ids = a.block_idx ? a.block_idx + ((size_t)now.row * a.G + now.g) * a.k + at : nullptr;
-            block = ids ? __ldg(ids) : a.prefix + at;
-            before = ids ? __ldg(ids - 1) : -1;
+            block = ids ? ld_in(ids) : a.prefix + at;
+            before = ids ? ld_in(ids - 1) : -1;
             page = block >= 0 && block < a.max_blocks
-                       ? __ldg(a.page_table + (size_t)now.info.x * a.max_blocks + block)
+                       ? ld_in(a.page_table + (size_t)now.info.x * a.max_blocks + block)
                        : -1;
           }
           if (j < now.pages) page = checked_page(a, now.info, block, before, page);
@@ -624,11 +625,13 @@ struct MergeArgs {
 constexpr int kMergeThreads = 128;
 
 __global__ void __launch_bounds__(kMergeThreads, 8) paged_merge_kernel(MergeArgs a) {
+  pdl_release();
+  pdl_wait();
   const int lane = threadIdx.x % 32;
   const long long item = (long long)blockIdx.x * (kMergeThreads / 32) + threadIdx.x / 32;
   if (item >= (long long)a.N * a.Hq) return;
   const int row = (int)(item / a.Hq), head = (int)(item % a.Hq), g = head / a.hg;
-  const int4 info = __ldg(a.rows + row);
+  const int4 info = ld_in(a.rows + row);
   if (info.x < 0) return;  // behind the last sequence, or left out
   // the tile's last row decides how far its items went
   const int lead = info.z % a.tile_rows, rows = min(a.tile_rows, info.w + lead);
@@ -639,7 +642,7 @@ __global__ void __launch_bounds__(kMergeThreads, 8) paged_merge_kernel(MergeArgs
   const size_t step = (size_t)a.N * a.Hq;
   auto slot = [&](int i) { return (size_t)(i < shared_parts ? i : a.pslots + i - shared_parts) * step + item; };
   float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, a.part_lse[slot(i)]);
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, ld_in(a.part_lse + slot(i)));
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -647,8 +650,8 @@ __global__ void __launch_bounds__(kMergeThreads, 8) paged_merge_kernel(MergeArgs
 #pragma unroll 8
   for (int i = 0; i < n; ++i) {
     const size_t at = slot(i);
-    const float w = fast_exp2(__ldg(a.part_lse + at) - m);
-    const float4 v = __ldg(reinterpret_cast<const float4*>(a.part_o + at * 128) + lane);
+    const float w = fast_exp2(ld_in(a.part_lse + at) - m);
+    const float4 v = ld_in(reinterpret_cast<const float4*>(a.part_o + at * 128) + lane);
     den += w;
     acc.x = fmaf(w, v.x, acc.x);
     acc.y = fmaf(w, v.y, acc.y);
@@ -671,9 +674,8 @@ cudaError_t launch_attn(const AttnArgs& a, const CUtensorMap& mk, const CUtensor
     if (e != cudaSuccess) return e;
     attr[dslot] = true;
   }
-  paged_attn_kernel<NT><<<std::min(a.items, num_sms()), kThreads, smem_bytes<NT>(), st>>>(a, mk, mv);
   count_launches(1);
-  return cudaGetLastError();
+  return launch_dependent(paged_attn_kernel<NT>, std::min(a.items, num_sms()), kThreads, smem_bytes<NT>(), st, a, mk, mv);
 }
 
 }  // namespace
@@ -736,9 +738,8 @@ cudaError_t launch_paged_merge(const PagedProb& p, void* O, float* LSE, uint8_t*
   a.teams = L.teams;
   a.pslots = L.pslots;
   const long long items = (long long)p.N * p.Hq;
-  paged_merge_kernel<<<(unsigned)((items + 3) / 4), kMergeThreads, 0, st>>>(a);
   count_launches(1);
-  return cudaGetLastError();
+  return launch_dependent(paged_merge_kernel, (unsigned)((items + 3) / 4), kMergeThreads, 0, st, a);
 }
 
 }  // namespace msa

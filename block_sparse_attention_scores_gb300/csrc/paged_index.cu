@@ -19,6 +19,7 @@
 // normally distributed values 2^-24.5).
 #include "mma_sync.cuh"
 #include "paged.h"
+#include "pdl.cuh"
 #include "sm100.cuh"
 
 namespace msa {
@@ -39,21 +40,23 @@ struct ScoreArgs {
 
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
 }
 
 __global__ void __launch_bounds__(kScoreThreads, 3) paged_scores_kernel(ScoreArgs a) {
+  pdl_release();
+  pdl_wait();
   const int s = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   int c = blockIdx.x * kScorePages * a.per_warp + warp;
   const int32_t* table = a.page_table + (size_t)s * a.max_blocks;
-  int page = c < a.max_blocks ? __ldg(table + c) : 0;
-  const int begin = __ldg(a.row_start + s);
-  int rows = __ldg(a.row_start + s + 1) - begin;
+  int page = c < a.max_blocks ? ld_in(table + c) : 0;
+  const int begin = ld_in(a.row_start + s);
+  int rows = ld_in(a.row_start + s + 1) - begin;
   // blocks before the last row's own one; all their tokens exist
-  const int len = min(__ldg(a.seq_len + s), a.max_blocks * 128);
+  const int len = min(ld_in(a.seq_len + s), a.max_blocks * 128);
   if (begin < 0 || rows <= 0 || begin >= a.N || len <= 0) return;
   rows = min(rows, a.N - begin);
   const int end = min((len - 1) / 128, c - warp + kScorePages * a.per_warp);
@@ -63,6 +66,13 @@ __global__ void __launch_bounds__(kScoreThreads, 3) paged_scores_kernel(ScoreArg
     const bool bad = page < 0 || page >= a.num_pages;
     if (bad && lane == 0) dev_fail(a.err, kDevBadIndex, 1301);
 
+    const int cols = rows * a.G;
+    const uint4* qp = reinterpret_cast<const uint4*>(a.q_idx + (size_t)begin * a.G * 64);
+    uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};  // the first eight columns' queries
+    if (r < cols) {
+      w[0] = ld_in(qp + (size_t)r * 8 + q);
+      w[1] = ld_in(qp + (size_t)r * 8 + 4 + q);
+    }
     // key 16 m + r (x) and 16 m + 8 + r (y): dims 8 q .. 8 q + 7 and 32 + 8 q .. (one piece per h)
     uint4 x[8][2], y[8][2];
     const uint4* kp = reinterpret_cast<const uint4*>(a.k_idx + (size_t)(bad ? 0 : page) * 128 * 64) + r * 8 + q;
@@ -73,7 +83,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) paged_scores_kernel(ScoreArg
         x[m][h] = ld_stream(kp + m * 128 + h * 4);
         y[m][h] = ld_stream(kp + m * 128 + 64 + h * 4);
       }
-    if (c + kScorePages < end) page = __ldg(table + c + kScorePages);
+    if (c + kScorePages < end) page = ld_in(table + c + kScorePages);
     uint32_t top = 0;  // largest magnitude, two bf16 at a time
 #pragma unroll
     for (int m = 0; m < 8; ++m)
@@ -88,13 +98,11 @@ __global__ void __launch_bounds__(kScoreThreads, 3) paged_scores_kernel(ScoreArg
     top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
     if (lane == 0) a.amax[(size_t)s * a.max_blocks + c] = __uint_as_float(top << 16);
 
-    const int cols = rows * a.G;
-    const uint4* qp = reinterpret_cast<const uint4*>(a.q_idx + (size_t)begin * a.G * 64);
     for (int n0 = 0; n0 < cols; n0 += 8) {
-      uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-      if (n0 + r < cols) {
-        w[0] = __ldg(qp + (size_t)(n0 + r) * 8 + q);
-        w[1] = __ldg(qp + (size_t)(n0 + r) * 8 + 4 + q);
+      if (n0) w[0] = w[1] = make_uint4(0, 0, 0, 0);
+      if (n0 && n0 + r < cols) {
+        w[0] = ld_in(qp + (size_t)(n0 + r) * 8 + q);
+        w[1] = ld_in(qp + (size_t)(n0 + r) * 8 + 4 + q);
       }
       float best0 = -INFINITY, best1 = -INFINITY;
 #pragma unroll
@@ -169,10 +177,10 @@ __device__ double exact_max(const __nv_bfloat16* page, const __nv_bfloat16* q, f
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        k[i][c] = __ldg(reinterpret_cast<const uint4*>(page + (lane + 32 * i) * 64 + 32 * h) + c);
+        k[i][c] = ld_in(reinterpret_cast<const uint4*>(page + (lane + 32 * i) * 64 + 32 * h) + c);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(q + 32 * h) + c);
+      const uint4 w = ld_in(reinterpret_cast<const uint4*>(q + 32 * h) + c);
       const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -185,14 +193,14 @@ __device__ double exact_max(const __nv_bfloat16* page, const __nv_bfloat16* q, f
   float best = fmaxf(fmaxf(s32[0], s32[1]), fmaxf(s32[2], s32[3]));
 #pragma unroll
   for (int o = 16; o; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-  const uint32_t qq = __ldg(reinterpret_cast<const uint32_t*>(q) + lane);
+  const uint32_t qq = ld_in(reinterpret_cast<const uint32_t*>(q) + lane);
   double top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     // the comparison is false for NaN: such a key is looked at in 64 bits
     for (unsigned m = __ballot_sync(0xffffffffu, !(s32[i] < best - margin)); m; m &= m - 1) {
       const int key = __ffs(m) - 1 + 32 * i;
-      const uint32_t kk = __ldg(reinterpret_cast<const uint32_t*>(page + key * 64) + lane);
+      const uint32_t kk = ld_in(reinterpret_cast<const uint32_t*>(page + key * 64) + lane);
       double t = fma((double)hi_f(qq), (double)hi_f(kk), (double)lo_f(qq) * (double)lo_f(kk));
 #pragma unroll
       for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
@@ -207,13 +215,15 @@ __device__ double exact_max(const __nv_bfloat16* page, const __nv_bfloat16* q, f
 // undecided blocks and their scores.
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
+  pdl_release();
+  pdl_wait();
   constexpr int kWarps = kThreads / 32;
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ SelectShared sh;
   const int rg = blockIdx.x, row = rg / a.G, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const __nv_bfloat16* q = a.q_idx + (size_t)rg * 64;
-  const uint32_t qq = __ldg(reinterpret_cast<const uint32_t*>(q) + lane);
-  const int4 info = a.rows[row];
+  const uint32_t qq = ld_in(reinterpret_cast<const uint32_t*>(q) + lane);
+  const int4 info = ld_in(a.rows + row);
   if (info.x < 0) return;
   const int n = info.y / 128;  // earlier blocks
   const int want = min(a.k - 1, n);
@@ -235,8 +245,8 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
 #pragma unroll
   for (int z = 0; z < kSelItems; ++z) {
     const int i = z * kThreads + tid;
-    x[z] = i < n ? v[i] : -INFINITY;
-    e[z] = i < n ? am[i] : 0.f;
+    x[z] = i < n ? ld_in(v + i) : -INFINITY;
+    e[z] = i < n ? ld_in(am + i) : 0.f;
   }
   if (tid == 0) sh.n_in = sh.n_open = 0;
   if (tid < 256) sh.chosen[tid] = 0;
@@ -353,8 +363,8 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
   } else {
     // the border runs through the open blocks: their exact maxima decide, equal ones by the lower id
     for (int i = warp; i < n_open; i += kWarps) {
-      const int c = open[i], page = a.page_table[(size_t)info.x * a.max_blocks + c];
-      const float t0 = fmaf(err_q, am[c], kTiny), margin = t0 < 1e30f ? t0 : INFINITY;
+      const int c = open[i], page = ld_in(a.page_table + (size_t)info.x * a.max_blocks + c);
+      const float t0 = fmaf(err_q, ld_in(am + c), kTiny), margin = t0 < 1e30f ? t0 : INFINITY;
       double t = -INFINITY;
       if (page >= 0 && page < a.num_pages) t = exact_max(a.k_idx + (size_t)page * 128 * 64, q, margin, lane);
       if (lane == 0) score[i] = t;
@@ -397,9 +407,8 @@ cudaError_t launch_select(const PagedProb& p, const SelectArgs& a, cudaStream_t 
     if (e != cudaSuccess) return e;
     attr[dslot] = true;
   }
-  paged_select_kernel<kThreads><<<p.N * p.G, kThreads, p.max_blocks * 12, st>>>(a);
   count_launches(1);
-  return cudaGetLastError();
+  return launch_dependent(paged_select_kernel<kThreads>, p.N * p.G, kThreads, p.max_blocks * 12, st, a);
 }
 
 }  // namespace
@@ -425,9 +434,10 @@ cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, cons
     const long long blocks = (long long)p.S * ((p.max_blocks - 1 + kScorePages - 1) / kScorePages);
     a.per_warp = (int)std::min<long long>(8, std::max<long long>(1, blocks / (3 * kCutSms)));
     const int per_block = kScorePages * a.per_warp;
+    // an ordinary launch: placed early, its blocks filled SMs unevenly (64 sequences at 32K tokens: 161 us against 135)
     paged_scores_kernel<<<dim3((p.max_blocks - 1 + per_block - 1) / per_block, p.S), kScoreThreads, 0, st>>>(a);
     count_launches(1);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   SelectArgs b;

@@ -15,16 +15,18 @@
 // page raises it by more than 2^8 (an O_t rescale is a TMEM round trip).
 //
 // What bounds it is the chain S -> softmax -> PV -> next S of a tile: its two
-// products take 1,024 cycles, and the softmax has to fit into the other tile's
-// 1,024. So two warps share each row, 64 keys each: they compute P under the
-// maximum they have and only then look at each other's page maximum (by shared
-// memory); a page that raises it is computed again.
+// products take 1,100 cycles, and the softmax should fit into the other tile's.
+// So two warps share each row, 64 keys each, and do not wait for each other:
+// both compute P under the row's common maximum, and only a warp that finds a
+// value 2^8 above it calls the other (which is then still waiting for the next
+// S), after which both raise the maximum, rescale O and compute P again.
 //
 // Work: all (group, page) pairs in a line, cut into `teams` runs of equal
 // length; a run is walked by `pairs` CTAs at once, one per pair of tiles, so
 // that a page is read from HBM once and from L2 by the others. A run leaves
 // one partial O (fp32, normalised) and log-sum-exp per row and group.
 #include "paged.h"
+#include "pdl.cuh"
 #include "sm100.cuh"
 
 namespace msa {
@@ -53,8 +55,8 @@ struct PrefixShared {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
   uint64_t pair[2][4];           // the two warps of a tile's 32 rows
-  float row_max[2][2][2][128];   // [page parity][tile][half][row]
-  int raised[2][2][2][4];        // [page parity][tile][half][quarter]: some row's maximum moves
+  float row_max[2][2][128];      // [tile][half][row] of the page's scores (at the end: the row's sums)
+  int raised[2][2][4];           // [tile][half][quarter] the page (counted from 1) at which this warp called the other
   uint32_t tmem_base;
 };
 
@@ -62,6 +64,26 @@ __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// (x0, x1) * a + b, two at a time.
+__device__ __forceinline__ void fma2(float& x0, float& x1, float a, float b) {
+  asm("{\n\t.reg .b64 x, m, n;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 m, {%2, %2};\n\tmov.b64 n, {%3, %3};\n\t"
+      "fma.rn.f32x2 x, x, m, n;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(a), "f"(b));
+}
+// (s0, s1) += (x0, x1)
+__device__ __forceinline__ void add2(float& s0, float& s1, float x0, float x1) {
+  asm("{\n\t.reg .b64 s, x;\n\tmov.b64 s, {%0, %1};\n\tmov.b64 x, {%2, %3};\n\tadd.rn.f32x2 s, s, x;\n\t"
+      "mov.b64 {%0, %1}, s;\n\t}"
+      : "+f"(s0), "+f"(s1)
+      : "f"(x0), "f"(x1));
+}
+// Eight floats to a 32-byte boundary in one store.
+__device__ __forceinline__ void st_global8(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+               "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -77,10 +99,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int team = blockIdx.x / a.pairs, pair = blockIdx.x % a.pairs;
   const int units = a.G * a.prefix;
-  const int u_begin = team_start(team, units, a.teams), u_end = team_start(team + 1, units, a.teams);
+  int u_begin = team_start(team, units, a.teams);
+  const int u_end = team_start(team + 1, units, a.teams);
   const int tile_rows = 128 / a.hg;
-  const int ref = __ldg(a.rows).x;  // the first sequence with rows; its table holds the shared pages
-  if (ref < 0) return;              // no rows at all, or the first one was refused
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
@@ -97,15 +118,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, 1);
+    for (int i = 0; i < 16; ++i) sh.raised[i >> 3][(i >> 2) & 1][i & 3] = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
     tmem_alloc(&sh.tmem_base, 512);
     tmem_relinquish();
   }
+  pdl_release();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait();
+  // the first sequence with rows: its table holds the shared pages (-1: no rows at all, -2: the first one was refused)
+  const int ref = ld_in(&a.rows[0].x);
+  if (ref < 0) u_begin = u_end;  // nothing to do
   const uint32_t tmem = sh.tmem_base;  // S_0 [0,128), S_1 [128,256), O_0 [256,384), O_1 [384,512)
 
   if (warp == 0) {
@@ -132,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u0 = u; u0 < stop && ok; u0 += 32) {
         int page = 0;
         if (u0 + lane < stop) {
-          page = __ldg(a.page_table + (size_t)ref * a.max_blocks + (u0 + lane - g * a.prefix));
+          page = ld_in(a.page_table + (size_t)ref * a.max_blocks + (u0 + lane - g * a.prefix));
           if (page < 0 || page >= a.num_pages) {
             dev_fail(a.err, kDevBadIndex, 1511);
             page = 0;
@@ -206,17 +233,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool last = c == pages - 1;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            // P_t of this page written (and O_t rescaled if its row maximum moved)
-            if (!mbar_wait(&sh.p_full[t], kc & 1, a.err, 1514 + t)) { ok = false; break; }
+            // the page's V and the next one's K first: nothing then stands between P_t and its products
             if (c == 0 && !mbar_wait(&sh.o_free[t], (seg & 1) ^ 1, a.err, 1516 + t)) { ok = false; break; }
             if (t == 0 && !mbar_wait(&sh.v_full[st], par, a.err, 1518)) { ok = false; break; }
+            if (t == 0 && !last && !mbar_wait(&sh.k_full[st1], par1, a.err, 1519)) { ok = false; break; }
+            // P_t of this page written (and O_t rescaled if its row maximum moved)
+            if (!mbar_wait(&sh.p_full[t], kc & 1, a.err, 1514 + t)) { ok = false; break; }
             tc_fence_after();
             issue_o(t, st, c > 0);
             if (t == 1) umma_commit(&sh.v_empty[st]);
             if (!last) {
               // the next page's S_t: after this PV_t in issue order, so it overwrites P_t only once read
-              if (t == 0 && !mbar_wait(&sh.k_full[st1], par1, a.err, 1519)) { ok = false; break; }
-              tc_fence_after();
               issue_s(t, st1);
               if (t == 1) {
                 umma_commit(&sh.k_empty[st1]);
@@ -243,11 +270,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // while the first pages are on their way: is the prefix the same one for every sequence with rows?
       bool bad = false;
       const long long cells = (long long)a.S * a.prefix;
-      for (long long i = (long long)blockIdx.x * 512 + threadIdx.x - 128; i < cells; i += (long long)gridDim.x * 512) {
+      for (long long i = (long long)blockIdx.x * 512 + threadIdx.x - 128; ref >= 0 && i < cells; i += (long long)gridDim.x * 512) {
         const int s = (int)(i / a.prefix), c = (int)(i % a.prefix);
         const int32_t* table = a.page_table + c;
-        if (__ldg(a.row_start + s + 1) > __ldg(a.row_start + s))
-          bad |= __ldg(table + (size_t)s * a.max_blocks) != __ldg(table + (size_t)ref * a.max_blocks);
+        if (ld_in(a.row_start + s + 1) > ld_in(a.row_start + s))
+          bad |= ld_in(table + (size_t)s * a.max_blocks) != ld_in(table + (size_t)ref * a.max_blocks);
       }
       if (bad) dev_fail(a.err, kDevBadIndex, 1512);
     }
@@ -257,43 +284,73 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = u_begin; u < u_end && ok; ++seg) {
       const int g = u / a.prefix, stop = min(u_end, (g + 1) * a.prefix), pages = stop - u;
       float m_run = -INFINITY, l_run = 0.f;  // the maximum is the row's, the sum that of this warp's keys
-      for (int c = 0; c < pages; ++c, ++kc) {
-        if (!mbar_wait(&sh.s_full[t], kc & 1, a.err, 1522 + t)) { ok = false; break; }
+      if (!mbar_wait(&sh.s_full[t], kc & 1, a.err, 1522 + t)) { ok = false; break; }
+      for (int c = 0; c < pages && ok; ++c, ++kc) {
         tc_fence_after();
         float sv[64], mq[2];
         tmem_ld32_max(s_at, *reinterpret_cast<float(*)[32]>(sv), mq[0]);
         tmem_ld32_max(s_at + 32, *reinterpret_cast<float(*)[32]>(sv + 32), mq[1]);
         tmem_wait_ld();
         const float m_blk = fmaxf(mq[0], mq[1]) * a.scale_log2;
-        const int b = kc & 1;
-        const bool raised = __any_sync(0xffffffffu, m_blk > m_run + kHeadroom);
-        sh.row_max[b][t][half][lrow] = m_blk;
-        if (lane == 0) sh.raised[b][t][half][quarter] = raised;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.pair[t][quarter]);
+        sh.row_max[t][half][lrow] = m_blk;
+        bool mine = c == 0 || __any_sync(0xffffffffu, m_blk > m_run + kHeadroom);  // this warp calls the other
         float l_add = 0.f;
         auto write_p = [&]() {
-          float l4[4] = {0.f, 0.f, 0.f, 0.f};
+          float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             uint32_t pk[8];
 #pragma unroll
             for (int z = 0; z < 8; ++z) {
-              const float p0 = fast_exp2(fmaf(sv[16 * h + 2 * z], a.scale_log2, -m_run));
-              const float p1 = fast_exp2(fmaf(sv[16 * h + 2 * z + 1], a.scale_log2, -m_run));
-              l4[(2 * z) & 3] += p0;
-              l4[(2 * z + 1) & 3] += p1;
+              float p0 = sv[16 * h + 2 * z], p1 = sv[16 * h + 2 * z + 1];
+              fma2(p0, p1, a.scale_log2, -m_run);
+              p0 = fast_exp2(p0);
+              p1 = fast_exp2(p1);
+              if (z & 1) add2(t0, t1, p0, p1);
+              else add2(s0, s1, p0, p1);
               pk[z] = pack_bf16(p0, p1);
             }
             tmem_st8(s_at + 8 * h, pk);
           }
-          l_add = (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          l_add = (s0 + s1) + (t0 + t1);
         };
-        if (c > 0 && !raised) write_p();
-        if (!mbar_wait(&sh.pair[t][quarter], pair_ph, a.err, 1526 + t)) { ok = false; break; }
-        pair_ph ^= 1u;
-        if (raised || sh.raised[b][t][half ^ 1][quarter]) {
-          const float m_new = fmaxf(m_blk, sh.row_max[b][t][half ^ 1][lrow]);
+        if (!mine) {
+          write_p();
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.p_full[t]);
+        } else if (c > 0) {
+          __syncwarp();
+          if (lane == 0) *static_cast<volatile int*>(&sh.raised[t][half][quarter]) = (int)kc + 1;
+        }
+        // what comes next: the other warp's call, or the next page's scores (after the last page, O)
+        uint64_t* next = c + 1 < pages ? &sh.s_full[t] : &sh.o_full[t];
+        const uint32_t next_ph = c + 1 < pages ? (kc + 1) & 1 : seg & 1;
+        bool redo = mine;
+        if (!mine) {
+          const uint32_t bar = smem_u32(next);
+          const volatile int* call = &sh.raised[t][half ^ 1][quarter];
+          unsigned long long since = 0;
+          for (uint32_t i = 1;; ++i) {
+            redo = __any_sync(0xffffffffu, *call == (int)kc + 1);
+            if (redo) break;
+            if (__all_sync(0xffffffffu, mbar_test(bar, next_ph))) break;
+            if ((i & 255u) == 0) {
+              const unsigned long long at = global_ns();
+              if (!since) since = at;
+              if (__any_sync(0xffffffffu, at - since > kWaitLimitNs)) {
+                dev_fail(a.err, kDevTimeout, 1524 + t);
+                ok = false;
+                break;
+              }
+            }
+          }
+          if (!ok) break;
+        }
+        if (redo) {
+          if (!warps_sync(&sh.pair[t][quarter], pair_ph, a.err, 1526 + t)) { ok = false; break; }
+          const float m_new = fmaxf(m_blk, sh.row_max[t][half ^ 1][lrow]);
           const bool need = m_new > m_run + kHeadroom;
           const float alpha = need ? fast_exp2(m_run - m_new) : 1.f;
           if (need) m_run = m_new;
@@ -312,41 +369,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           write_p();
+          tmem_wait_st();
+          tc_fence_before();
+          // both warps are through before the one that called (or both) hands P on
+          if (!warps_sync(&sh.pair[t][quarter], pair_ph, a.err, 1528 + t)) { ok = false; break; }
+          if (mine) {
+            tc_fence_after();
+            tc_fence_before();
+            if (lane == 0) mbar_arrive(&sh.p_full[t]);
+          }
+          if (!mbar_wait(next, next_ph, a.err, 1530 + t)) { ok = false; break; }
         }
-        tmem_wait_st();
         l_run += l_add;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full[t]);
       }
       if (!ok) break;
       // ---- the run's end in this group: the row's partial
-      sh.row_max[kc & 1][t][half][lrow] = l_run;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.pair[t][quarter]);
-      if (!mbar_wait(&sh.pair[t][quarter], pair_ph, a.err, 1528 + t)) { ok = false; break; }
-      pair_ph ^= 1u;
-      const float l = half ? sh.row_max[kc & 1][t][0][lrow] + l_run : l_run + sh.row_max[kc & 1][t][1][lrow];
-      // the next group's first page writes the buffer of this parity again
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.pair[t][quarter]);
-      if (!mbar_wait(&sh.pair[t][quarter], pair_ph, a.err, 1530 + t)) { ok = false; break; }
-      pair_ph ^= 1u;
-      if (!mbar_wait(&sh.o_full[t], seg & 1, a.err, 1524 + t)) { ok = false; break; }
+      sh.row_max[t][half][lrow] = l_run;
+      if (!warps_sync(&sh.pair[t][quarter], pair_ph, a.err, 1532 + t)) { ok = false; break; }
+      const float l = half ? sh.row_max[t][0][lrow] + l_run : l_run + sh.row_max[t][1][lrow];
+      if (!warps_sync(&sh.pair[t][quarter], pair_ph, a.err, 1534 + t)) { ok = false; break; }
       tc_fence_after();
       const int slot = team - team_of(g * a.prefix, units, a.teams);
       const size_t at = ((size_t)slot * a.N + row) * a.Hq + g * a.hg + lrow % a.hg;
       const float inv = 1.f / l;
-      float4* dst = reinterpret_cast<float4*>(a.part_o + at * 128 + half * 64);
+      float* dst = a.part_o + at * 128 + half * 64;
 #pragma unroll
       for (int z = 0; z < 4; ++z) {
         float o[16];
         tmem_ld16(o_at + z * 16, o);
         tmem_wait_ld();
-        if (row < a.N) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dst[4 * z + i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+        for (int i = 0; i < 16; ++i) o[i] *= inv;
+        if (row < a.N) {
+          st_global8(dst + 16 * z, o);
+          st_global8(dst + 16 * z + 8, o + 8);
         }
       }
       if (row < a.N && half == 0) a.part_lse[at] = m_run + log2f(l);
@@ -401,9 +457,8 @@ cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, con
     if (e != cudaSuccess) return e;
     attr[dslot] = true;
   }
-  paged_prefix_kernel<<<L.teams * L.pairs, kThreads, kSmem, st>>>(a, mq, mk, mv);
   count_launches(1);
-  return cudaGetLastError();
+  return launch_dependent(paged_prefix_kernel, L.teams * L.pairs, kThreads, kSmem, st, a, mq, mk, mv);
 }
 
 }  // namespace msa

@@ -15,7 +15,7 @@ stream unless ``stream`` is given.
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass, field
+from dataclasses import dataclass
 
 from . import (MSA_ERR_UNSUPPORTED, MSA_WS_PAGED_APPEND, MSA_WS_PAGED_DENSE, MSA_WS_PAGED_SPARSE, MsaError, _check,
                load_library)
@@ -54,28 +54,56 @@ class PagedShape:
     d_idx: int = 64
     Bk: int = 128
     scale: float = 0.0
-    _c: list = field(default_factory=list, init=False, repr=False, compare=False)
+
+    def __post_init__(self):
+        # what every call would work out again: the C struct and the shapes of the tensors
+        put = lambda n, v: object.__setattr__(self, n, v)  # noqa: E731
+        put("_c", MsaPagedShape(self.S, self.N, self.Hq, self.G, self.d, self.d_idx, self.Bk, self.k, self.num_pages,
+                                self.max_blocks, self.prefix_blocks, self.scale))
+        put("_addr", ctypes.addressof(self._c))
+        put("_sizes", (self.S, self.G, self.num_pages, self.max_blocks, self.d, self.Bk))
+        N, Hq, G = self.N, self.Hq, self.G
+        put("_q", (N, Hq, self.d))
+        put("_kv", (N, G, self.d))
+        put("_qi", (N, G, self.d_idx))
+        put("_ki", (N, self.d_idx))
+        put("_bi", (N, G, self.k))
+        put("_lse", (N, Hq))
 
     def c(self) -> MsaPagedShape:
-        if not self._c:
-            self._c.append(MsaPagedShape(self.S, self.N, self.Hq, self.G, self.d, self.d_idx, self.Bk, self.k,
-                                         self.num_pages, self.max_blocks, self.prefix_blocks, self.scale))
-        return self._c[0]
+        return self._c
 
 
-def _want(name, t, dtype, shape=None, device=None):
-    """A GPU tensor of this type and shape (None in the shape: any size), packed."""
-    if not t.is_cuda:
+_torch = None
+
+
+def _t():
+    """torch, imported at the first use."""
+    global _torch
+    if _torch is None:
+        import torch
+
+        _torch = torch
+    return _torch
+
+
+def _refuse(name, t, dtype, shape, device, packed=True):
+    if not t.is_cuda and device != -1:
         raise ValueError(f"{name} must live on the GPU")
     if t.dtype != dtype:
         raise ValueError(f"{name} is {t.dtype}, {dtype} is needed")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, {tuple(shape)} is needed")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} lives on {t.device}, the cache on {device}")
-    return t.data_ptr()
+    if t.get_device() != device:
+        raise ValueError(f"{name} lives on {t.device}, the cache on cuda:{device}")
+    raise ValueError(f"{name} must be contiguous" if packed else f"the rows of {name} must be packed")
+
+
+def _want(name, t, dtype, shape, device):
+    """Address of a packed tensor of this type and shape on GPU `device`."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(name, t, dtype, shape, device)
 
 
 class PagedCache:
@@ -84,30 +112,31 @@ class PagedCache:
     contents may change between calls."""
 
     def __init__(self, K, V, k_idx, page_table, row_start, seq_len):
-        import torch
-
+        torch = _t()
+        if not K.is_cuda:
+            raise ValueError("K must live on the GPU")
         pages, G, Bk, d = K.shape
-        dev = K.device
+        dev = K.get_device()
         S = seq_len.shape[0]
         bf, i32 = torch.bfloat16, torch.int32
         self._struct = MsaPagedCache(
-            _want("K", K, bf), _want("V", V, bf, (pages, G, Bk, d), dev),
+            _want("K", K, bf, (pages, G, Bk, d), dev), _want("V", V, bf, (pages, G, Bk, d), dev),
             None if k_idx is None else _want("k_idx", k_idx, bf, (pages, Bk, k_idx.shape[-1]), dev),
             _want("page_table", page_table, i32, (S, page_table.shape[-1]), dev),
             _want("row_start", row_start, i32, (S + 1,), dev), _want("seq_len", seq_len, i32, (S,), dev))
+        self._addr = ctypes.addressof(self._struct)
         self.K, self.V, self.k_idx = K, V, k_idx
         self.page_table, self.row_start, self.seq_len = page_table, row_start, seq_len
-        self.device = dev
-        self.sizes = (S, G, pages, page_table.shape[-1], d, Bk)
-        self.index_dim = None if k_idx is None else k_idx.shape[-1]
+        self.device, self._device = K.device, dev
+        self._sizes = (S, G, pages, page_table.shape[-1], d, Bk)
+        self._index_dim = None if k_idx is None else k_idx.shape[-1]
 
     def check(self, shape):
         """The cache is one of `shape`."""
-        if self.sizes != (shape.S, shape.G, shape.num_pages, shape.max_blocks, shape.d, shape.Bk):
-            raise ValueError(f"the cache has (S, G, num_pages, max_blocks, d, Bk) = {self.sizes}, the shape "
-                             f"{(shape.S, shape.G, shape.num_pages, shape.max_blocks, shape.d, shape.Bk)}")
-        if self.index_dim is not None and self.index_dim != shape.d_idx:
-            raise ValueError(f"the cache's index keys have {self.index_dim} dims, the shape {shape.d_idx}")
+        if self._sizes != shape._sizes:
+            raise ValueError(f"the cache has (S, G, num_pages, max_blocks, d, Bk) = {self._sizes}, the shape {shape._sizes}")
+        if self._index_dim is not None and self._index_dim != shape.d_idx:
+            raise ValueError(f"the cache's index keys have {self._index_dim} dims, the shape {shape.d_idx}")
 
 
 class Rope:
@@ -115,135 +144,119 @@ class Rope:
     [rot_dim_idx / 2] for the index branch; None rotates nothing."""
 
     def __init__(self, inv_freq=None, inv_freq_idx=None, interleaved=False):
-        import torch
+        torch = _t()
 
         def ptr(name, t):
             if t is None or t.numel() == 0:
                 return None, 0
-            return _want(name, t, torch.float32, (t.numel(),)), 2 * t.numel()
+            if not t.is_cuda:
+                raise ValueError(f"{name} must live on the GPU")
+            return _want(name, t, torch.float32, (t.numel(),), t.get_device()), 2 * t.numel()
 
         p, n = ptr("inv_freq", inv_freq)
         pi, ni = ptr("inv_freq_idx", inv_freq_idx)
         self.inv_freq, self.inv_freq_idx = inv_freq, inv_freq_idx
-        self.devices = [t.device for t in (inv_freq, inv_freq_idx) if t is not None]
+        self._devices = {t.get_device() for t, q in ((inv_freq, p), (inv_freq_idx, pi)) if q is not None}
         self._struct = MsaRope(p, pi, n, ni, 1 if interleaved else 0)
+        self._addr = ctypes.addressof(self._struct)
 
 
 def _rows(name, t, shape, device):
     """Address and row stride of a [N, ...] input whose rows are packed (the pieces of a fused projection are)."""
-    import torch
-
-    if t.dtype != torch.bfloat16 or t.device != device:
-        raise ValueError(f"{name} must be bfloat16 on {device}, it is {t.dtype} on {t.device}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, {shape} is needed")
-    packed = 1
-    for n, st in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
+    if t.dtype is not _t().bfloat16 or t.shape != shape or t.get_device() != device:
+        _refuse(name, t, _t().bfloat16, shape, device, packed=False)
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    strides, packed = t.stride(), 1
+    for n, st in zip(shape[:0:-1], strides[:0:-1]):
         if n != 1 and st != packed:
-            raise ValueError(f"the rows of {name} must be packed")
+            _refuse(name, t, t.dtype, shape, device, packed=False)
         packed *= n
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else packed
+    return t.data_ptr(), strides[0] if shape[0] > 1 else packed
 
 
-def _call(cache, stream, workspace, run):
-    """run(workspace, its bytes, stream) with the cache's GPU current."""
-    import torch
-
-    if workspace.device != cache.device or not workspace.is_contiguous():
+def _run(call, cache, stream, workspace, *args):
+    """call(*args, workspace, its bytes, stream) with the cache's GPU current."""
+    torch = _t()
+    dev = cache._device
+    if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"the workspace must be contiguous on {cache.device}")
-    dev = cache.device.index
-    here = torch.cuda.current_device()
-    if dev != here:
-        torch.cuda.set_device(dev)
-    try:
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        raw = stream if isinstance(stream, int) else stream.cuda_stream
-        _check(run(workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw))
-    finally:
-        if dev != here:
-            torch.cuda.set_device(here)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    ws, n = workspace.data_ptr(), workspace.nbytes
+    if torch._C._cuda_getDevice() == dev:
+        status = call(*args, ws, n, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = call(*args, ws, n, stream)
+    if status:
+        _check(status)
 
 
 def msa_paged_workspace_size(shape, which: int) -> int:
-    return int(load_library().msa_paged_workspace_size(ctypes.addressof(shape.c()), which))
+    return int(load_library().msa_paged_workspace_size(shape._addr, which))
 
 
 def alloc_paged_workspace(shape, which: int, device="cuda"):
-    import torch
-
     n = msa_paged_workspace_size(shape, which)
     if n == 0:
         raise MsaError(MSA_ERR_UNSUPPORTED, "shape not supported (see include/msa.h)")
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    return _t().empty(n, dtype=_t().uint8, device=device)
 
 
 def msa_paged_append(shape, cache, rope, K, V, k_idx, Q, q_idx, Q_out, q_idx_out, workspace, stream=None) -> None:
     """New tokens into their pages, K and k_idx rotated; Q and q_idx rotated into Q_out and q_idx_out. Inputs may be
     row-strided. k_idx, and Q or q_idx with its output, may be None."""
-    import torch
-
+    bf = _t().bfloat16
     cache.check(shape)
-    N, dev = shape.N, cache.device
+    dev = cache._device
     if k_idx is not None and cache.k_idx is None:
         raise ValueError("the cache has no index keys (k_idx)")
-    if any(d != dev for d in rope.devices):
-        raise ValueError(f"the rotation's frequencies must live on {dev}")
-    r = MsaNewRows()
-    r.K, r.ld_K = _rows("K", K, (N, shape.G, shape.d), dev)
-    r.V, r.ld_V = _rows("V", V, (N, shape.G, shape.d), dev)
-    out = qi_out = None
-    if Q is not None:
-        r.Q, r.ld_Q = _rows("Q", Q, (N, shape.Hq, shape.d), dev)
-    if q_idx is not None:
-        r.q_idx, r.ld_q_idx = _rows("q_idx", q_idx, (N, shape.G, shape.d_idx), dev)
-    if k_idx is not None:
-        r.k_idx, r.ld_k_idx = _rows("k_idx", k_idx, (N, shape.d_idx), dev)
-    if Q_out is not None:
-        out = _want("Q_out", Q_out, torch.bfloat16, (N, shape.Hq, shape.d), dev)
-    if q_idx_out is not None:
-        qi_out = _want("q_idx_out", q_idx_out, torch.bfloat16, (N, shape.G, shape.d_idx), dev)
-    lib = load_library()
-    _call(cache, stream, workspace, lambda ws, n, st: lib.msa_paged_append(
-        ctypes.addressof(shape.c()), ctypes.addressof(cache._struct), ctypes.addressof(rope._struct),
-        ctypes.addressof(r), out, qi_out, ws, n, st))
+    if rope._devices and rope._devices != {dev}:
+        raise ValueError(f"the rotation's frequencies must live on {cache.device}")
+    none = (None, 0)
+    kp, k_ld = _rows("K", K, shape._kv, dev)
+    vp, v_ld = _rows("V", V, shape._kv, dev)
+    qp, q_ld = none if Q is None else _rows("Q", Q, shape._q, dev)
+    ip, i_ld = none if q_idx is None else _rows("q_idx", q_idx, shape._qi, dev)
+    xp, x_ld = none if k_idx is None else _rows("k_idx", k_idx, shape._ki, dev)
+    rows = MsaNewRows(qp, kp, vp, ip, xp, q_ld, k_ld, v_ld, i_ld, x_ld)
+    _run(load_library().msa_paged_append, cache, stream, workspace, shape._addr, cache._addr, rope._addr,
+         ctypes.addressof(rows), None if Q_out is None else _want("Q_out", Q_out, bf, shape._q, dev),
+         None if q_idx_out is None else _want("q_idx_out", q_idx_out, bf, shape._qi, dev))
 
 
 def msa_paged_sparse_attn(shape, cache, Q, q_idx, block_idx, O, LSE, workspace, stream=None) -> None:
     """Selection (q_idx given: block_idx is written; None: block_idx is read) and attention over the selected pages."""
-    import torch
-
+    torch = _t()
+    bf = torch.bfloat16
     cache.check(shape)
-    N, dev, bf = shape.N, cache.device, torch.bfloat16
+    dev = cache._device
     if q_idx is not None and cache.k_idx is None:
         raise ValueError("the cache has no index keys (k_idx)")
-    args = (_want("Q", Q, bf, (N, shape.Hq, shape.d), dev),
-            None if q_idx is None else _want("q_idx", q_idx, bf, (N, shape.G, shape.d_idx), dev),
-            _want("block_idx", block_idx, torch.int32, (N, shape.G, shape.k), dev),
-            _want("O", O, bf, (N, shape.Hq, shape.d), dev), _want("LSE", LSE, torch.float32, (N, shape.Hq), dev))
-    lib = load_library()
-    _call(cache, stream, workspace, lambda ws, n, st: lib.msa_paged_sparse_attn(
-        ctypes.addressof(shape.c()), ctypes.addressof(cache._struct), *args, ws, n, st))
+    _run(load_library().msa_paged_sparse_attn, cache, stream, workspace, shape._addr, cache._addr,
+         _want("Q", Q, bf, shape._q, dev), None if q_idx is None else _want("q_idx", q_idx, bf, shape._qi, dev),
+         _want("block_idx", block_idx, torch.int32, shape._bi, dev), _want("O", O, bf, shape._q, dev),
+         _want("LSE", LSE, torch.float32, shape._lse, dev))
 
 
 def msa_paged_dense_attn(shape, cache, Q, O, LSE, workspace, stream=None) -> None:
     """Full attention for the new rows; the first shape.prefix_blocks pages are those of every sequence."""
-    import torch
-
+    torch = _t()
+    bf = torch.bfloat16
     cache.check(shape)
-    N, dev, bf = shape.N, cache.device, torch.bfloat16
-    args = (_want("Q", Q, bf, (N, shape.Hq, shape.d), dev), _want("O", O, bf, (N, shape.Hq, shape.d), dev),
-            _want("LSE", LSE, torch.float32, (N, shape.Hq), dev))
-    lib = load_library()
-    _call(cache, stream, workspace, lambda ws, n, st: lib.msa_paged_dense_attn(
-        ctypes.addressof(shape.c()), ctypes.addressof(cache._struct), *args, ws, n, st))
+    dev = cache._device
+    _run(load_library().msa_paged_dense_attn, cache, stream, workspace, shape._addr, cache._addr,
+         _want("Q", Q, bf, shape._q, dev), _want("O", O, bf, shape._q, dev),
+         _want("LSE", LSE, torch.float32, shape._lse, dev))
 
 
 # ----------------------------------------------------------------- allocation helpers
 def paged_append(shape, cache, rope, K, V, k_idx=None, Q=None, q_idx=None, workspace=None, stream=None):
     """Allocate the rotated queries, run msa_paged_append and return (Q_out, q_idx_out); None where none was given."""
-    import torch
-
+    torch = _t()
     dev = cache.device
     ws = workspace if workspace is not None else alloc_paged_workspace(shape, MSA_WS_PAGED_APPEND, dev)
     Q_out = None if Q is None else torch.empty((shape.N, shape.Hq, shape.d), dtype=torch.bfloat16, device=dev)
@@ -254,8 +267,7 @@ def paged_append(shape, cache, rope, K, V, k_idx=None, Q=None, q_idx=None, works
 
 def paged_sparse_attn(shape, cache, Q, q_idx=None, block_idx=None, workspace=None, stream=None):
     """Allocate O, LSE (and block_idx, when q_idx selects) and run msa_paged_sparse_attn; returns (O, LSE, block_idx)."""
-    import torch
-
+    torch = _t()
     dev = cache.device
     ws = workspace if workspace is not None else alloc_paged_workspace(shape, MSA_WS_PAGED_SPARSE, dev)
     if block_idx is None:
@@ -270,8 +282,7 @@ def paged_sparse_attn(shape, cache, Q, q_idx=None, block_idx=None, workspace=Non
 
 def paged_dense_attn(shape, cache, Q, workspace=None, stream=None):
     """Allocate O and LSE and run msa_paged_dense_attn."""
-    import torch
-
+    torch = _t()
     dev = cache.device
     ws = workspace if workspace is not None else alloc_paged_workspace(shape, MSA_WS_PAGED_DENSE, dev)
     O = torch.empty((shape.N, shape.Hq, shape.d), dtype=torch.bfloat16, device=dev)

@@ -181,15 +181,14 @@ def test_binding_refuses_tensors_of_another_kind(msa):
         msa.PagedCache(*[torch.zeros(2, 2, 128, 128, dtype=torch.bfloat16)] * 2, None,
                        torch.zeros(2, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32),
                        torch.zeros(2, dtype=torch.int32))
-    cpu = torch.device("cpu")
     x = torch.zeros(3, 2, 128, dtype=torch.bfloat16)
-    assert rows("K", x, (3, 2, 128), cpu)[1] == 256
+    assert rows("K", x, (3, 2, 128), -1)[1] == 0  # packed
     fused = torch.zeros(3, 640, dtype=torch.bfloat16)[:, 128:384].unflatten(1, (2, 128))
-    assert rows("K", fused, (3, 2, 128), cpu)[1] == 640
+    assert rows("K", fused, (3, 2, 128), -1)[1] == 640
     with pytest.raises(ValueError, match="packed"):
-        rows("K", torch.zeros(2, 3, 128, dtype=torch.bfloat16).transpose(0, 1), (3, 2, 128), cpu)[1] and rows(
-            "K", torch.zeros(3, 128, 2, dtype=torch.bfloat16).transpose(1, 2), (3, 2, 128), cpu)
+        rows("K", torch.zeros(2, 3, 128, dtype=torch.bfloat16).transpose(0, 1), (3, 2, 128), -1)[1] and rows(
+            "K", torch.zeros(3, 128, 2, dtype=torch.bfloat16).transpose(1, 2), (3, 2, 128), -1)
     with pytest.raises(ValueError, match="shape"):
-        rows("K", x, (3, 4, 128), cpu)
+        rows("K", x, (3, 4, 128), -1)
     with pytest.raises(ValueError, match="bfloat16"):
-        rows("K", x.float(), (3, 2, 128), cpu)
+        rows("K", x.float(), (3, 2, 128), -1)
