@@ -52,7 +52,8 @@ struct PrefixArgs {
 
 struct PrefixShared {
   uint64_t q_full, q_empty;
-  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t k0_full, kv_full[kStages];  // the first page's K; then a page's V with the next one's K
+  uint64_t k_empty[kStages], v_empty[kStages];
   uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
   uint64_t pair[2][4];           // the two warps of a tile's 32 rows
   float row_max[2][2][128];      // [tile][half][row] of the page's scores (at the end: the row's sums)
@@ -111,11 +112,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 4; ++j) mbar_init(&sh.pair[i][j], 2);
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.kv_full[i], 1);
       mbar_init(&sh.k_empty[i], 1);
-      mbar_init(&sh.v_full[i], 1);
       mbar_init(&sh.v_empty[i], 1);
     }
+    mbar_init(&sh.k0_full, 1);
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, 1);
     for (int i = 0; i < 16; ++i) sh.raised[i >> 3][(i >> 2) & 1][i & 3] = 0;
@@ -140,53 +141,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&map_q);
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
-    uint32_t kc = 0;
-    bool ok = true;
-    int seg = 0;
-    for (int u = u_begin; u < u_end && ok; ++seg) {
-      const int g = u / a.prefix, stop = min(u_end, (g + 1) * a.prefix);
-      if (!mbar_wait(&sh.q_empty, (seg & 1) ^ 1, a.err, 1502)) { ok = false; break; }
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&sh.q_full, 2 * kTile);
+    const int n = u_end - u_begin;
+    // row of the pool's tensor map of the CTA's page i + lane
+    auto rows_of = [&](int i) {
+      const int u = u_begin + i + lane;
+      if (u >= u_end) return 0;
+      const int g = u / a.prefix;
+      int page = ld_in(a.page_table + (size_t)ref * a.max_blocks + (u - g * a.prefix));
+      if (page < 0 || page >= a.num_pages) {
+        dev_fail(a.err, kDevBadIndex, 1511);
+        page = 0;
+      }
+      return (page * a.G + g) * 128;
+    };
+    auto load_q = [&](int g) {
+      mbar_arrive_expect_tx(&sh.q_full, 2 * kTile);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int row0 = (2 * pair + t) * tile_rows;  // rows past N arrive as zeros
-          tma_load_3d(smem + oQ + t * kTile, &map_q, &sh.q_full, 0, g * a.hg, row0);
-          tma_load_3d(smem + oQ + t * kTile + kChunk, &map_q, &sh.q_full, 64, g * a.hg, row0);
-        }
+      for (int t = 0; t < 2; ++t) {
+        const int row0 = (2 * pair + t) * tile_rows;  // rows past N arrive as zeros
+        tma_load_3d(smem + oQ + t * kTile, &map_q, &sh.q_full, 0, g * a.hg, row0);
+        tma_load_3d(smem + oQ + t * kTile + kChunk, &map_q, &sh.q_full, 64, g * a.hg, row0);
+      }
+    };
+    auto load_tile = [&](int at, const CUtensorMap* map, uint64_t* bar, int y) {
+      tma_load_2d(smem + at, map, bar, 0, y);
+      tma_load_2d(smem + at + kChunk, map, bar, 64, y);
+    };
+    int cur = rows_of(0), ahead = rows_of(32), seg = 0;
+    if (n > 0 && lane == 0) {
+      load_q(u_begin / a.prefix);
+      mbar_arrive_expect_tx(&sh.k0_full, kTile);
+      load_tile(oK, &map_k, &sh.k0_full, cur);
+    }
+    for (int i = 0; i < n; ++i) {
+      const int st = i % kStages, st1 = (i + 1) % kStages;
+      const int y = __shfl_sync(0xffffffffu, cur, i & 31);
+      const int y1 = (i & 31) == 31 ? __shfl_sync(0xffffffffu, ahead, 0) : __shfl_sync(0xffffffffu, cur, (i & 31) + 1);
+      const bool more = i + 1 < n;
+      if (!mbar_wait(&sh.v_empty[st], ((i / kStages) & 1) ^ 1, a.err, 1504)) break;
+      if (more && !mbar_wait(&sh.k_empty[st1], (((i + 1) / kStages) & 1) ^ 1, a.err, 1503)) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sh.kv_full[st], more ? 2 * kTile : kTile);
+        load_tile(oV + st * kTile, &map_v, &sh.kv_full[st], y);
+        if (more) load_tile(oK + st1 * kTile, &map_k, &sh.kv_full[st], y1);
       }
       __syncwarp();
-      for (int u0 = u; u0 < stop && ok; u0 += 32) {
-        int page = 0;
-        if (u0 + lane < stop) {
-          page = ld_in(a.page_table + (size_t)ref * a.max_blocks + (u0 + lane - g * a.prefix));
-          if (page < 0 || page >= a.num_pages) {
-            dev_fail(a.err, kDevBadIndex, 1511);
-            page = 0;
-          }
-        }
-        const int here = min(32, stop - u0);
-        for (int i = 0; i < here; ++i, ++kc) {
-          const int st = kc % kStages;
-          const uint32_t par = ((kc / kStages) & 1) ^ 1;
-          const int y = (__shfl_sync(0xffffffffu, page, i) * a.G + g) * 128;
-          if (!mbar_wait(&sh.k_empty[st], par, a.err, 1503)) { ok = false; break; }
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&sh.k_full[st], kTile);
-            tma_load_2d(smem + oK + st * kTile, &map_k, &sh.k_full[st], 0, y);
-            tma_load_2d(smem + oK + st * kTile + kChunk, &map_k, &sh.k_full[st], 64, y);
-          }
-          __syncwarp();
-          if (!mbar_wait(&sh.v_empty[st], par, a.err, 1504)) { ok = false; break; }
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&sh.v_full[st], kTile);
-            tma_load_2d(smem + oV + st * kTile, &map_v, &sh.v_full[st], 0, y);
-            tma_load_2d(smem + oV + st * kTile + kChunk, &map_v, &sh.v_full[st], 64, y);
-          }
-          __syncwarp();
-        }
+      const int g1 = (u_begin + i + 1) / a.prefix;
+      if (more && g1 != (u_begin + i) / a.prefix) {  // the next page is another group's: its queries
+        if (!mbar_wait(&sh.q_empty, seg & 1, a.err, 1502)) break;
+        ++seg;
+        if (lane == 0) load_q(g1);
+        __syncwarp();
       }
-      u = stop;
+      if ((i & 31) == 31) {
+        cur = ahead;
+        ahead = rows_of(i + 33);
+      }
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- UMMA issuer
@@ -220,7 +230,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait(&sh.q_full, seg & 1, a.err, 1520)) { ok = false; break; }
         {
           const int st = kc % kStages;
-          if (!mbar_wait(&sh.k_full[st], (kc / kStages) & 1, a.err, 1513)) { ok = false; break; }
+          // (a later run's first K came with the V of the page before it)
+          if (kc == 0 && !mbar_wait(&sh.k0_full, 0, a.err, 1513)) { ok = false; break; }
           tc_fence_after();
           issue_s(0, st);
           issue_s(1, st);
@@ -229,14 +240,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int c = 0; c < pages && ok; ++c, ++kc) {
           const int st = kc % kStages, st1 = (kc + 1) % kStages;
-          const uint32_t par = (kc / kStages) & 1, par1 = ((kc + 1) / kStages) & 1;
+          const uint32_t par = (kc / kStages) & 1;
           const bool last = c == pages - 1;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             // the page's V and the next one's K first: nothing then stands between P_t and its products
             if (c == 0 && !mbar_wait(&sh.o_free[t], (seg & 1) ^ 1, a.err, 1516 + t)) { ok = false; break; }
-            if (t == 0 && !mbar_wait(&sh.v_full[st], par, a.err, 1518)) { ok = false; break; }
-            if (t == 0 && !last && !mbar_wait(&sh.k_full[st1], par1, a.err, 1519)) { ok = false; break; }
+            if (t == 0 && !mbar_wait(&sh.kv_full[st], par, a.err, 1518)) { ok = false; break; }
             // P_t of this page written (and O_t rescaled if its row maximum moved)
             if (!mbar_wait(&sh.p_full[t], kc & 1, a.err, 1514 + t)) { ok = false; break; }
             tc_fence_after();
