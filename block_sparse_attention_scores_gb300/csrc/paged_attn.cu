@@ -39,9 +39,11 @@ constexpr int kSlots = 4;                          // shared-memory O buffers: t
 constexpr unsigned long long kIdleLimitNs = 20000000000ull;  // the joining warps may have nothing to do for a while
 constexpr int kOStride = 132;                      // floats between columns of an O buffer (no bank conflicts)
 
+constexpr int kQStride = 272;                      // bytes between the queries' rows in shared memory (no bank conflicts)
+
 template <int NT>
 constexpr int smem_bytes() {
-  return kStages * 2 * kTile + kSlots * 8 * kOStride * 4 + 2 * NT * 8 * 256 + 1024;
+  return kStages * 2 * kTile + kSlots * 8 * kOStride * 4 + 2 * NT * 8 * kQStride + 1024;
 }
 
 struct AttnArgs {
@@ -52,7 +54,7 @@ struct AttnArgs {
   int* arrived;                           // [N, G, kJoinWarps] items of a (row tile, group) that are done
   __nv_bfloat16* O;
   float* LSE;
-  int N, Hq, G, hg, k, num_pages, max_blocks, prefix, splits, per_split, tile_rows, items, slot0, join;
+  int N, Hq, G, hg, hg_log2, k, num_pages, max_blocks, prefix, splits, per_split, tile_rows, items, slot0, join;
   float scale_log2;
   int* err;
 };
@@ -72,7 +74,8 @@ struct AttnShared {
   AttnItem item[2];
   AttnItem join[2];           // for the joining warps; parts 0: the end
   int token0[kStages];        // first token of the stage's page
-  float m[2][kSlots][8], l[2][kSlots][8];  // [0]: of the warps that store first, [1]: of two warps together
+  float m[kWarps][8], l[kWarps][8];
+  float inv[8], lse[8];       // of all warps together: 1 / sum, and log2 of the sum
 };
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -179,7 +182,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const AttnItem& it
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int col = min(c0 + x * kJoinWarps, cols - 1);
-      at[x] = (size_t)(item.row + col / a.hg) * a.Hq + item.g * a.hg + col % a.hg;
+      at[x] = (size_t)(item.row + (col >> a.hg_log2)) * a.Hq + item.g * a.hg + (col & (a.hg - 1));
       mm[x] = -INFINITY;
       acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int i = lane; i < item.parts; i += 32) mm[x] = fmaxf(mm[x], __ldcg(a.part_lse + i * step + at[x]));
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ AttnShared sh;
   float* s_o = reinterpret_cast<float*>(smem + kStages * 2 * kTile);  // [slot][8 columns][kOStride]
-  uint8_t* s_q = smem + kStages * 2 * kTile + kSlots * 8 * kOStride * 4;  // [2][NT * 8][256 bytes]
+  uint8_t* s_q = smem + kStages * 2 * kTile + kSlots * 8 * kOStride * 4;  // [2][NT * 8][kQStride]
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -265,11 +268,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           sh.item[qs] = {now.row, now.g, now.split, now.pages, now.parts, now.info.y, rows};
           mbar_arrive_expect_tx(&sh.q_full[qs], rows * a.hg * 256);
-          for (int i = 0; i < rows; ++i)
-            bulk_load(s_q + (qs * NT * 8 + i * a.hg) * 256, a.Q + ((size_t)(now.row + i) * a.Hq + now.g * a.hg) * 128,
-                      a.hg * 256, &sh.q_full[qs]);
         }
         __syncwarp();
+        if (lane < rows * a.hg)  // one column each
+          bulk_load(s_q + (qs * NT * 8 + lane) * kQStride,
+                    a.Q + ((size_t)(now.row + (lane >> a.hg_log2)) * a.Hq + now.g * a.hg + (lane & (a.hg - 1))) * 128, 256,
+                    &sh.q_full[qs]);
         ++n_item;
         for (int j0 = 0; j0 < now.pages && ok; j0 += 32) {
           int block = now.block, page = now.page, before = now.before;
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int col = 8 * nt + r;
-        const uint8_t* src = s_q + (qs * NT * 8 + col) * 256;
+        const uint8_t* src = s_q + (qs * NT * 8 + col) * kQStride;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
           qb[nt][ks][0] = col < cols ? *reinterpret_cast<const uint32_t*>(src + ks * 32 + q * 4) : 0u;
@@ -369,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int z = 0; z < 2; ++z) lim[nt][z] = item.pos + 1 + (8 * nt + 2 * q + z) / a.hg;
+        for (int z = 0; z < 2; ++z) lim[nt][z] = item.pos + 1 + ((8 * nt + 2 * q + z) >> a.hg_log2);
       const int lim_lo = item.pos + 1;
 
       float m_run[NT][2], l_run[NT][2], o[NT][8][4];
@@ -510,8 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
 
-      // ---- the warps' results meet, eight columns at a time: the upper four warps store theirs, the lower four add
-      // them to their own, and all 256 threads add up the four sums
+      // ---- the warps' results meet, eight columns at a time: the upper four warps store theirs, the lower four scale
+      // them and their own to the maximum of all and add them, and all 256 threads add up the four sums
       const bool joined = a.join && item.parts > 1;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt, ++n_pass) {
@@ -522,34 +526,45 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) l[z] += __shfl_xor_sync(0xffffffffu, l[z], x);
         }
-        const int slot = warp & (kSlots - 1);
-        float* mine = s_o + slot * 8 * kOStride;
+        float* mine = s_o + (warp & (kSlots - 1)) * 8 * kOStride;
         auto place = [&](int mt, int z) { return (2 * q + (z & 1)) * kOStride + mt * 16 + r + (z >> 1) * 8; };
         if (!mbar_wait(&sh.s_free, (n_pass & 1) ^ 1, a.err, 1424)) { ok = false; break; }
+        if (r == 0) {
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            sh.m[warp][2 * q + z] = m_run[nt][z];
+            sh.l[warp][2 * q + z] = l[z];
+          }
+        }
         if (warp >= kSlots) {
 #pragma unroll
           for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
             for (int z = 0; z < 4; ++z) mine[place(mt, z)] = o[nt][mt][z];
-          if (r == 0) {
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              sh.m[0][slot][2 * q + z] = m_run[nt][z];
-              sh.l[0][slot][2 * q + z] = l[z];
-            }
-          }
         }
         if (!warps_sync(&sh.meet, meet_ph, a.err, 1425)) { ok = false; break; }
         if (warp < kSlots) {
           float f[2], g[2];
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            const float m2 = sh.m[0][slot][2 * q + z], mm = fmaxf(m_run[nt][z], m2);
-            f[z] = m_run[nt][z] == -INFINITY ? 0.f : fast_exp2(m_run[nt][z] - mm);
-            g[z] = m2 == -INFINITY ? 0.f : fast_exp2(m2 - mm);
-            if (r == 0) {
-              sh.m[1][slot][2 * q + z] = mm;
-              sh.l[1][slot][2 * q + z] = fmaf(l[z], f[z], sh.l[0][slot][2 * q + z] * g[z]);
+            const int c = 2 * q + z;
+            float mw[kWarps], mm = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+              mw[w] = sh.m[w][c];
+              mm = fmaxf(mm, mw[w]);
+            }
+            const float base = mm == -INFINITY ? 0.f : mm;  // no warp saw a key: every factor is 0
+            f[z] = fast_exp2(m_run[nt][z] - base);
+            g[z] = fast_exp2(sh.m[warp + kSlots][c] - base);
+            if (warp == 0) {
+              float den = 0.f;
+#pragma unroll
+              for (int w = 0; w < kWarps; ++w) den = fmaf(fast_exp2(mw[w] - base), sh.l[w][c], den);
+              if (r == 0) {
+                sh.inv[c] = mm > -INFINITY ? 1.f / den : 0.f;
+                sh.lse[c] = mm > -INFINITY ? mm + log2f(den) : -INFINITY;
+              }
             }
           }
 #pragma unroll
@@ -561,31 +576,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (!warps_sync(&sh.meet, meet_ph, a.err, 1426)) { ok = false; break; }
-        const int d = threadIdx.x & 127;  // one dim, four columns
+        const int d = threadIdx.x & 127;  // one dim of every other column
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int cc = (threadIdx.x >> 7) * 4 + c, col = 8 * nt + cc;
+        for (int c = 0; c < 8; c += 2) {
+          const int cc = c + (threadIdx.x >> 7), col = 8 * nt + cc;
           if (col >= cols) break;
-          float mm = sh.m[1][0][cc];
+          float val = 0.f;
 #pragma unroll
-          for (int w = 1; w < kSlots; ++w) mm = fmaxf(mm, sh.m[1][w][cc]);
-          float num = 0.f, den = 0.f;
-#pragma unroll
-          for (int w = 0; w < kSlots; ++w) {
-            const float mw = sh.m[1][w][cc], f = mw == -INFINITY ? 0.f : fast_exp2(mw - mm);
-            den = fmaf(f, sh.l[1][w][cc], den);
-            num = fmaf(f, s_o[(w * 8 + cc) * kOStride + d], num);
-          }
-          const float val = mm > -INFINITY ? num / den : 0.f;
-          const float lse = mm > -INFINITY ? mm + log2f(den) : -INFINITY;
-          const size_t at = (size_t)(item.row + col / a.hg) * a.Hq + item.g * a.hg + col % a.hg;
+          for (int w = 0; w < kSlots; ++w) val += s_o[(w * 8 + cc) * kOStride + d];
+          val *= sh.inv[cc];
+          const size_t at = (size_t)(item.row + (col >> a.hg_log2)) * a.Hq + item.g * a.hg + (col & (a.hg - 1));
           if (a.join && !joined) {
             a.O[at * 128 + d] = __float2bfloat16_rn(val);
-            if (d == 0) a.LSE[at] = lse * 0.6931471805599453f;
+            if (d == 0) a.LSE[at] = sh.lse[cc] * 0.6931471805599453f;
           } else {
             const size_t pt = (size_t)(a.slot0 + item.split) * a.N * a.Hq + at;
             a.part_o[pt * 128 + d] = val;
-            if (d == 0) a.part_lse[pt] = lse;
+            if (d == 0) a.part_lse[pt] = sh.lse[cc];
           }
         }
         __syncwarp();
@@ -702,6 +709,7 @@ cudaError_t launch_paged_attn(const PagedProb& p, const PagedCachePtrs& c, const
   a.Hq = p.Hq;
   a.G = p.G;
   a.hg = p.hg;
+  a.hg_log2 = p.hg == 8 ? 3 : p.hg == 4 ? 2 : p.hg - 1;
   a.k = p.k;
   a.num_pages = p.num_pages;
   a.max_blocks = p.max_blocks;
