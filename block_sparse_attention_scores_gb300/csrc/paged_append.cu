@@ -203,31 +203,37 @@ struct RowsArgs {
   int S, N, G, max_blocks, prefix;
 };
 
-__device__ __forceinline__ int bisect_rows(const int32_t* row_start, int S, int r) {
-  int lo = 0, hi = S + 1;  // row_start[lo] <= r (row_start[0] counts as 0), row_start[hi] > r
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (ld_in(row_start + mid) <= r) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
+constexpr int kStaged = 4096;  // sequence starts kept in shared memory
 
 __global__ void __launch_bounds__(kThreads) paged_rows_kernel(RowsArgs a) {
-  pdl_release();
+  __shared__ int staged[kStaged];
+  // released after the wait: the index scores, launched then, have only this kernel's own work to wait for (at their end)
   pdl_wait();
-  if (blockIdx.x == 0 && threadIdx.x < 64) a.err[threadIdx.x] = 0;
-  const int r = blockIdx.x * kThreads + threadIdx.x;
+  pdl_release();
+  const int tid = threadIdx.x;
+  if (blockIdx.x == 0 && tid < 64) a.err[tid] = 0;
+  const bool all = a.S + 1 <= kStaged;
+  if (all) {
+    for (int i = tid; i <= a.S; i += kThreads) staged[i] = ld_in(a.row_start + i);
+    __syncthreads();
+  }
+  auto start = [&](int i) { return all ? staged[i] : ld_in(a.row_start + i); };
+  const int r = blockIdx.x * kThreads + tid;
   if (r >= a.N) return;
   for (int i = 0; i < 3 * a.G; ++i) a.arrived[(size_t)r * 3 * a.G + i] = 0;
-  const int s = bisect_rows(a.row_start, a.S, r);
+  int lo = 0, hi = a.S + 1;  // start(lo) <= r (the first counts as 0), start(hi) > r
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start(mid) <= r) lo = mid;
+    else hi = mid;
+  }
   int4 out = make_int4(-1, 0, 0, 0);
-  if (s < a.S) {
-    const int len = ld_in(a.seq_len + s), begin = ld_in(a.row_start + s), end = ld_in(a.row_start + s + 1);
+  if (lo < a.S) {
+    const int len = ld_in(a.seq_len + lo), begin = start(lo), end = start(lo + 1);
     if (len < end - r + a.prefix * 128 || len > a.max_blocks * 128)
       out.x = -2;
     else
-      out = make_int4(s, len - (end - r), r - begin, (end < a.N ? end : a.N) - r);
+      out = make_int4(lo, len - (end - r), r - begin, (end < a.N ? end : a.N) - r);
   }
   a.rows[r] = out;
 }

@@ -1,12 +1,11 @@
 // Index branch for new tokens over the paged cache: block maxima of the index
 // scores, and each (row, group)'s own block plus its best k - 1 earlier ones.
 //
-// paged_scores_kernel reads every index key of a sequence once: a warp holds
-// one page (128 keys x 64) in registers, straight from 16-byte loads, and
-// multiplies it with the sequence's index queries (rows x groups, eight
-// columns at a time). The sum over the 64 dims may run in any order, so the
-// pieces that a thread loads serve as its matrix fragments as they are: no
-// shared memory, no shuffles before the maximum.
+// paged_scores_kernel reads every index key of a sequence once: a producer keeps
+// twelve pages (128 keys x 64, 16 KB by TMA) in flight per SM, and each of twelve
+// warps takes a whole page and multiplies it with the sequence's index queries
+// (rows x groups, eight columns at a time, mma.sync): the memory's time, at a
+// tenth of the tensor pipe's.
 //
 // The selection has to be exact, not exact up to the rounding of fp32: the
 // order of two blocks decides whole pages. An fp32 maximum v_c differs from
@@ -27,107 +26,177 @@ namespace {
 
 constexpr float kErr = 68.f / 8388608.f;
 constexpr float kTiny = 1e-35f;               // products below the normal range may count as zero
-constexpr int kScoreThreads = 128;
-constexpr int kScorePages = kScoreThreads / 32;
+constexpr int kScoreWarps = 12;
+constexpr int kScoreThreads = (kScoreWarps + 1) * 32;  // the last warp loads
+constexpr int kScoreStages = 12;
+// page n lies in stage n % stages and is warp n % warps's: a stage is always the same warp's, so that nobody waits for a
+// stage's next page before the one in it has been taken (a barrier's parity tells only two pages apart)
+static_assert(kScoreStages % kScoreWarps == 0, "a stage belongs to one warp");
+constexpr int kScorePage = 16384;
+constexpr int kScoreQ = 8 * 128;  // the first eight columns' queries, which come with each page
+constexpr int kScoreSmem = kScoreStages * (kScorePage + kScoreQ) + 1024;
+constexpr int kScoreRun = 6;    // pages of a work item
+constexpr int kScoreBatch = 5;  // items whose description is fetched at once (a lane per page)
 
 struct ScoreArgs {
-  const __nv_bfloat16 *q_idx, *k_idx;
+  const __nv_bfloat16* q_idx;
   const int32_t *page_table, *row_start, *seq_len;
   float *pooled, *amax;
-  int S, N, G, num_pages, max_blocks, per_warp;
+  int S, N, G, num_pages, max_blocks, runs, items;
   int* err;
 };
 
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
-__global__ void __launch_bounds__(kScoreThreads, 3) paged_scores_kernel(ScoreArgs a) {
-  pdl_release();
-  pdl_wait();
-  const int s = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  int c = blockIdx.x * kScorePages * a.per_warp + warp;
-  const int32_t* table = a.page_table + (size_t)s * a.max_blocks;
-  int page = c < a.max_blocks ? ld_in(table + c) : 0;
-  const int begin = ld_in(a.row_start + s);
-  int rows = ld_in(a.row_start + s + 1) - begin;
-  // blocks before the last row's own one; all their tokens exist
-  const int len = min(ld_in(a.seq_len + s), a.max_blocks * 128);
-  if (begin < 0 || rows <= 0 || begin >= a.N || len <= 0) return;
-  rows = min(rows, a.N - begin);
-  const int end = min((len - 1) / 128, c - warp + kScorePages * a.per_warp);
-  const int r = lane >> 2, q = lane & 3;
-#pragma unroll 1
-  for (; c < end; c += kScorePages) {
-    const bool bad = page < 0 || page >= a.num_pages;
-    if (bad && lane == 0) dev_fail(a.err, kDevBadIndex, 1301);
+struct ScoreShared {
+  uint64_t full[kScoreStages], empty[kScoreStages];
+  int4 info[kScoreStages];  // sequence (-1: the end), block (its complement where the page may not be read), first row, columns
+};
 
-    const int cols = rows * a.G;
-    const uint4* qp = reinterpret_cast<const uint4*>(a.q_idx + (size_t)begin * a.G * 64);
-    uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};  // the first eight columns' queries
-    if (r < cols) {
-      w[0] = ld_in(qp + (size_t)r * 8 + q);
-      w[1] = ld_in(qp + (size_t)r * 8 + 4 + q);
+// Starts when the kernel before it has passed its wait, so everything earlier is done; what it reads of that goes past
+// L1, and the end of that kernel (which clears the error word) is waited for at the end.
+__global__ void __launch_bounds__(kScoreThreads, 1)
+    paged_scores_kernel(ScoreArgs a, const __grid_constant__ CUtensorMap map_k) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ ScoreShared sh;
+  uint8_t* s_q = smem + kScoreStages * kScorePage;  // [stage][8][128]
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kScoreStages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
     }
-    // key 16 m + r (x) and 16 m + 8 + r (y): dims 8 q .. 8 q + 7 and 32 + 8 q .. (one piece per h)
-    uint4 x[8][2], y[8][2];
-    const uint4* kp = reinterpret_cast<const uint4*>(a.k_idx + (size_t)(bad ? 0 : page) * 128 * 64) + r * 8 + q;
-#pragma unroll
-    for (int m = 0; m < 8; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        x[m][h] = ld_stream(kp + m * 128 + h * 4);
-        y[m][h] = ld_stream(kp + m * 128 + 64 + h * 4);
-      }
-    if (c + kScorePages < end) page = ld_in(table + c + kScorePages);
-    uint32_t top = 0;  // largest magnitude, two bf16 at a time
-#pragma unroll
-    for (int m = 0; m < 8; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint4 u = x[m][h], v = y[m][h];
-        top = __vmaxu2(top, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
-                                     __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
-        top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                     __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-      }
-    top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-    if (lane == 0) a.amax[(size_t)s * a.max_blocks + c] = __uint_as_float(top << 16);
+    fence_barrier_init();
+    tma_prefetch_desc(&map_k);
+  }
+  pdl_release();
+  __syncthreads();
+  int failed = 0;
+  int* const err = &failed;  // (the error word itself may only be written at the end)
 
-    for (int n0 = 0; n0 < cols; n0 += 8) {
-      if (n0) w[0] = w[1] = make_uint4(0, 0, 0, 0);
-      if (n0 && n0 + r < cols) {
-        w[0] = ld_in(qp + (size_t)(n0 + r) * 8 + q);
-        w[1] = ld_in(qp + (size_t)(n0 + r) * 8 + 4 + q);
-      }
-      float best0 = -INFINITY, best1 = -INFINITY;
-#pragma unroll
-      for (int m = 0; m < 8; ++m) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          mma_16816(d, x[m][h].x, y[m][h].x, x[m][h].y, y[m][h].y, w[h].x, w[h].y);
-          mma_16816(d, x[m][h].z, y[m][h].z, x[m][h].w, y[m][h].w, w[h].z, w[h].w);
+  if (warp == kScoreWarps) {
+    // ---------------------------------------------------------------- producer
+    // An item is a run of pages of one sequence. Five of them are described by 30 lanes, one page each, and the next
+    // five are fetched meanwhile.
+    struct Batch {
+      int s, c, begin, end, len, page;
+    } now, next;
+    const int step = gridDim.x;
+    auto fetch = [&](int first, Batch& f) {
+      const int id = first + lane / kScoreRun * step;
+      f.s = -1;
+      f.c = f.begin = f.end = f.len = f.page = 0;
+      if (lane >= kScoreRun * kScoreBatch || id >= a.items) return;
+      f.s = id / a.runs;
+      f.c = id % a.runs * kScoreRun + lane % kScoreRun;
+      f.begin = __ldcg(a.row_start + f.s);
+      f.end = __ldcg(a.row_start + f.s + 1);
+      f.len = __ldcg(a.seq_len + f.s);
+      if (f.c < a.max_blocks) f.page = __ldcg(a.page_table + (size_t)f.s * a.max_blocks + f.c);
+    };
+    int n = 0;  // pages handed over
+    bool ok = true;
+    fetch(blockIdx.x, now);
+    for (int id = blockIdx.x; id < a.items && ok; id += kScoreBatch * step, now = next) {
+      fetch(id + kScoreBatch * step, next);
+      const int rows = min(now.end, a.N) - now.begin;
+      // blocks before the last row's own one
+      const bool want = now.s >= 0 && now.begin >= 0 && rows > 0 && now.len > 0 && now.len <= a.max_blocks * 128 &&
+                        now.c < (now.len - 1) / 128;
+      const bool bad = want && (now.page < 0 || now.page >= a.num_pages);
+      if (bad) failed = kDevBadIndex * 65536 + 1301;
+      const int page = bad ? 0 : now.page, cols = rows * a.G;
+      for (unsigned m = __ballot_sync(0xffffffffu, want); m; m &= m - 1, ++n) {
+        const int from = __ffs(m) - 1, st = n % kScoreStages;
+        if (!mbar_wait(&sh.empty[st], ((n / kScoreStages) & 1) ^ 1, nullptr, 0)) { ok = false; break; }
+        if (lane == from) {
+          sh.info[st] = make_int4(now.s, bad ? ~now.c : now.c, now.begin, cols);
+          const int first = min(cols, 8);
+          mbar_arrive_expect_tx(&sh.full[st], kScorePage + first * 128);
+          tma_load_2d(smem + st * kScorePage, &map_k, &sh.full[st], 0, page * 128);
+          // (one copy: eight of 128 bytes that avoid bank conflicts took longer to issue than the page to arrive)
+          bulk_load(s_q + st * kScoreQ, a.q_idx + (size_t)now.begin * a.G * 64, first * 128, &sh.full[st]);
         }
-        best0 = fmaxf(best0, fmaxf(d[0], d[2]));  // a NaN score counts as -infinity (fmaxf leaves it out)
-        best1 = fmaxf(best1, fmaxf(d[1], d[3]));
+        __syncwarp();
       }
+    }
+    for (int i = 0; i < kScoreWarps && ok; ++i, ++n) {  // the end, for every warp
+      const int st = n % kScoreStages;
+      ok = mbar_wait(&sh.empty[st], ((n / kScoreStages) & 1) ^ 1, nullptr, 0);
+      if (ok && lane == 0) {
+        sh.info[st].x = -1;
+        mbar_arrive(&sh.full[st]);
+      }
+    }
+    if (!ok) failed = kDevTimeout * 65536 + 1302;
+  } else {
+    // ---------------------------------------------------------------- one page per warp
+    const int r = lane >> 2, q = lane & 3;
+    for (int n = warp;; n += kScoreWarps) {
+      const int st = n % kScoreStages;
+      if (!mbar_wait(&sh.full[st], (n / kScoreStages) & 1, nullptr, 0)) {
+        failed = kDevTimeout * 65536 + 1303;
+        break;
+      }
+      const int4 info = sh.info[st];
+      if (info.x < 0) break;
+      const bool bad = info.y < 0;
+      const int c = bad ? ~info.y : info.y, cols = info.w;
+      const uint32_t base = smem_u32(smem + st * kScorePage);
+      const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q_idx + (size_t)info.z * a.G * 64);
+      uint32_t top = 0;  // largest magnitude, two bf16 at a time
+      for (int n0 = 0; n0 < cols; n0 += 8) {
+        uint32_t b[4][2];  // queries' column n0 + r, dims 16 ks + 2 q, + 1 and + 8, + 9
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        best0 = fmaxf(best0, __shfl_xor_sync(0xffffffffu, best0, o));
-        best1 = fmaxf(best1, __shfl_xor_sync(0xffffffffu, best1, o));
+        for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int at = ks * 8 + h * 4 + q;
+            b[ks][h] = n0 + r >= cols ? 0u
+                       : n0           ? __ldcg(qp + (size_t)(n0 + r) * 32 + at)
+                                      : *reinterpret_cast<const uint32_t*>(s_q + st * kScoreQ + r * 128 + at * 4);
+          }
+        float best0 = -INFINITY, best1 = -INFINITY;
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            uint32_t f[4];
+            ldmatrix_x4(f, base + sw128_off(m * 16 + (lane & 15), ks * 2 + (lane >> 4)));
+            mma_16816(d, f[0], f[1], f[2], f[3], b[ks][0], b[ks][1]);
+            if (n0 == 0)
+              top = __vmaxu2(top, __vmaxu2(__vmaxu2(f[0] & 0x7fff7fffu, f[1] & 0x7fff7fffu),
+                                           __vmaxu2(f[2] & 0x7fff7fffu, f[3] & 0x7fff7fffu)));
+          }
+          best0 = fmaxf(best0, fmaxf(d[0], d[2]));  // a NaN score counts as -infinity (fmaxf leaves it out)
+          best1 = fmaxf(best1, fmaxf(d[1], d[3]));
+        }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          best0 = fmaxf(best0, __shfl_xor_sync(0xffffffffu, best0, o));
+          best1 = fmaxf(best1, __shfl_xor_sync(0xffffffffu, best1, o));
+        }
+        if (r == 0) {
+          const size_t col = (size_t)info.z * a.G + n0 + 2 * q;
+          if (n0 + 2 * q < cols) a.pooled[col * a.max_blocks + c] = bad ? -INFINITY : best0;
+          if (n0 + 2 * q + 1 < cols) a.pooled[(col + 1) * a.max_blocks + c] = bad ? -INFINITY : best1;
+        }
       }
-      if (r == 0) {
-        const size_t col = (size_t)begin * a.G + n0 + 2 * q;
-        if (n0 + 2 * q < cols) a.pooled[col * a.max_blocks + c] = bad ? -INFINITY : best0;
-        if (n0 + 2 * q + 1 < cols) a.pooled[(col + 1) * a.max_blocks + c] = bad ? -INFINITY : best1;
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.empty[st]);
+      top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+      if (lane == 0) a.amax[(size_t)info.x * a.max_blocks + c] = __uint_as_float(top << 16);
     }
   }
+  pdl_wait();
+  if (*err) dev_fail(a.err, *err / 65536, *err % 65536);
 }
 
 // ---------------------------------------------------------------------------
@@ -417,7 +486,6 @@ cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, cons
                                uint8_t* ws, const PagedWs& L, cudaStream_t st) {
   ScoreArgs a;
   a.q_idx = static_cast<const __nv_bfloat16*>(q_idx);
-  a.k_idx = static_cast<const __nv_bfloat16*>(c.k_idx);
   a.page_table = c.page_table;
   a.row_start = c.row_start;
   a.seq_len = c.seq_len;
@@ -430,14 +498,23 @@ cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, cons
   a.max_blocks = p.max_blocks;
   a.err = reinterpret_cast<int*>(ws);
   if (p.max_blocks > 1 && p.k > 1) {
-    // one page a warp until every SM has its blocks, then up to eight
-    const long long blocks = (long long)p.S * ((p.max_blocks - 1 + kScorePages - 1) / kScorePages);
-    a.per_warp = (int)std::min<long long>(8, std::max<long long>(1, blocks / (3 * kCutSms)));
-    const int per_block = kScorePages * a.per_warp;
-    // an ordinary launch: placed early, its blocks filled SMs unevenly (64 sequences at 32K tokens: 161 us against 135)
-    paged_scores_kernel<<<dim3((p.max_blocks - 1 + per_block - 1) / per_block, p.S), kScoreThreads, 0, st>>>(a);
+    CUtensorMap mk;
+    const uint64_t dims[2] = {64, (uint64_t)p.num_pages * 128};
+    const uint64_t strides[1] = {128};
+    const uint32_t box[2] = {64, 128};
+    if (!encode_tmap(&mk, c.k_idx, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+    a.runs = (p.max_blocks - 1 + kScoreRun - 1) / kScoreRun;
+    a.items = p.S * a.runs;
+    static bool attr[kMaxDevices] = {};
+    const int dslot = device_slot();
+    cudaError_t e;
+    if (!attr[dslot]) {
+      e = cudaFuncSetAttribute(paged_scores_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
+      if (e != cudaSuccess) return e;
+      attr[dslot] = true;
+    }
     count_launches(1);
-    const cudaError_t e = cudaGetLastError();
+    e = launch_dependent(paged_scores_kernel, std::min(a.items, num_sms()), kScoreThreads, kScoreSmem, st, a, mk);
     if (e != cudaSuccess) return e;
   }
   SelectArgs b;
@@ -445,7 +522,7 @@ cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, cons
   b.pooled = a.pooled;
   b.amax = a.amax;
   b.q_idx = a.q_idx;
-  b.k_idx = a.k_idx;
+  b.k_idx = static_cast<const __nv_bfloat16*>(c.k_idx);
   b.page_table = c.page_table;
   b.block_idx = block_idx;
   b.G = p.G;
