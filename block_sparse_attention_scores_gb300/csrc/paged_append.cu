@@ -8,9 +8,12 @@
 // a million costs no accuracy (a product in 32 bits is off by 0.06 radians
 // there); the top 32 bits then give sin and cos in fp32.
 //
-// Every value is read and written once; nothing else moves. One block per new
-// row: a row's K, V, Q and index vectors are cut into items of two 16-byte
-// pieces (the two halves of eight pairs, or two neighbours), one thread each.
+// Every value is read and written once; nothing else moves. A block takes one
+// new row, or four where there are many (the frequencies are then turned into
+// fixed point once for four rows): a row's K, V, Q and index vectors are cut
+// into items of two 16-byte pieces (the two halves of eight pairs, or two
+// neighbours), one thread each, whose loads are on their way before the row's
+// place and angles are looked up.
 #include "paged.h"
 #include "pdl.cuh"
 #include "sm100.cuh"
@@ -19,13 +22,18 @@ namespace msa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kInFlight = 2;  // items a thread has loaded before it needs the angles
+constexpr int kInFlight = 2;  // items a thread loads at a time
+constexpr int kMaxRows = 4;   // rows of a block
+constexpr int kPairs = 64 + 32;
 
 struct AppendArgs {
   RopeRows r;
   __nv_bfloat16 *K, *V, *k_idx;
   const int32_t *page_table, *row_start, *seq_len;
   int S, N, Hq, G, num_pages, max_blocks;
+  int rows;                      // of a block
+  int n_q, n_k, n_qi, items;     // items of a row: queries, keys (values as many), index queries; all
+  float inv_items;
   int* err;
 };
 
@@ -87,106 +95,126 @@ __device__ __forceinline__ void rotate(uint4& x, uint4& y, const float2* cs, int
   }
 }
 
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
-  __shared__ float2 turn[64 + 32];  // cos, sin of the row's pairs: d, then d_idx
-  __shared__ int place[3];          // sequence found, page (-1: not to be written), slot
-  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+struct Piece {
+  uint4 x, y;
+  int row, kind, vec, a, b, pair;  // kind -1: none; 0 Q, 1 K, 2 V, 3 q_idx, 4 k_idx
+};
 
-  // the row's sequence and position; every warp looks them up, so that no warp waits for another's loads
-  const int s = find_sequence(a.row_start, a.S, r, lane);
-  if (s >= a.S) return;  // behind the last sequence
-  const int len = __ldg(a.seq_len + s), end = __ldg(a.row_start + s + 1);
-  if (len < end - r || len > a.max_blocks * 128) {
-    if (tid == 0) dev_fail(a.err, kDevBadIndex, 1201);
-    return;
+// Item `it` of the block's rows: which vector's pieces, and their loads.
+__device__ __forceinline__ void load_piece(const AppendArgs& a, int r0, int it, Piece& p) {
+  p.kind = -1;
+  const int row = (int)(((float)it + 0.5f) * a.inv_items);
+  it -= row * a.items;
+  if (row >= a.rows || r0 + row >= a.N) return;
+  p.row = row;
+  const __nv_bfloat16* src;
+  const size_t r = r0 + row;
+  if (it < a.n_q) {
+    p.kind = 0;
+    src = static_cast<const __nv_bfloat16*>(a.r.Q) + r * a.r.ld_Q;
+  } else if ((it -= a.n_q) < a.n_k) {
+    p.kind = 1;
+    src = static_cast<const __nv_bfloat16*>(a.r.K) + r * a.r.ld_K;
+  } else if ((it -= a.n_k) < a.n_k) {
+    p.kind = 2;
+    src = static_cast<const __nv_bfloat16*>(a.r.V) + r * a.r.ld_V;
+  } else if ((it -= a.n_k) < a.n_qi) {
+    p.kind = 3;
+    src = static_cast<const __nv_bfloat16*>(a.r.q_idx) + r * a.r.ld_q_idx;
+  } else {
+    it -= a.n_qi;
+    p.kind = 4;
+    src = static_cast<const __nv_bfloat16*>(a.r.k_idx) + r * a.r.ld_k_idx;
   }
-  const int pos = len - (end - r);
-  if (tid == 0) {
-    int page = __ldg(a.page_table + (size_t)s * a.max_blocks + (pos >> 7));
-    if (page < 0 || page >= a.num_pages) {
-      dev_fail(a.err, kDevBadIndex, 1202);
-      page = -1;
-    }
-    place[1] = page;
-    place[2] = pos & 127;
-  }
+  const bool idx = p.kind >= 3;
+  p.vec = idx ? it >> 2 : it >> 3;
+  item_pieces(idx ? it & 3 : it & 7, p.kind == 2 ? 0 : (idx ? a.r.rot_idx : a.r.rot), a.r.interleaved, p.a, p.b, p.pair);
+  const uint4* v = reinterpret_cast<const uint4*>(src + (size_t)p.vec * (idx ? 64 : 128));
+  p.x = v[p.a];
+  p.y = v[p.b];
+}
+
+__global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
+  __shared__ unsigned long long turns_of[kPairs];  // frequency as a fraction of a turn per position
+  __shared__ float2 turn[kMaxRows][kPairs];        // cos, sin of a row's pairs: d, then d_idx
+  __shared__ int pos_of[kMaxRows], page_of[kMaxRows];  // -1: no row, or not to be written
+  const int r0 = blockIdx.x * a.rows, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  Piece p[kInFlight];
+#pragma unroll
+  for (int z = 0; z < kInFlight; ++z) load_piece(a, r0, z * kThreads + tid, p[z]);
+
   const int half = a.r.rot / 2, half_idx = a.r.rot_idx / 2;
-  if (tid < 96) {
-    const bool idx = tid >= 64;
-    const int i = idx ? tid - 64 : tid;
+  if (tid >= kThreads - kPairs) {  // the last three warps
+    const int t = tid - (kThreads - kPairs);
+    const bool idx = t >= 64;
+    const int i = idx ? t - 64 : t;
     if (i < (idx ? half_idx : half)) {
       const double turns = (double)__ldg((idx ? a.r.inv_freq_idx : a.r.inv_freq) + i) * 0.15915494309189533577;
-      const unsigned long long f = (unsigned long long)((turns - floor(turns)) * 18446744073709551616.0);
-      const unsigned long long phase = f * (unsigned long long)pos;
-      float sn, cs;
-      sincospif((float)(int)(uint32_t)(phase >> 32) * 4.656612873077393e-10f, &sn, &cs);  // the top 32 bits, in half turns
-      turn[tid] = make_float2(cs, sn);
+      turns_of[t] = (unsigned long long)((turns - floor(turns)) * 18446744073709551616.0);
+    }
+  } else if (warp < a.rows) {  // the rows' sequences, positions and pages, a warp each
+    const int r = r0 + warp;
+    int pos = -1, page = -1;
+    const int s = r < a.N ? find_sequence(a.row_start, a.S, r, lane) : a.S;
+    if (s < a.S) {  // not behind the last sequence
+      const int len = __ldg(a.seq_len + s), end = __ldg(a.row_start + s + 1);
+      if (len < end - r || len > a.max_blocks * 128) {
+        if (lane == 0) dev_fail(a.err, kDevBadIndex, 1201);
+      } else {
+        pos = len - (end - r);
+        page = __ldg(a.page_table + (size_t)s * a.max_blocks + (pos >> 7));
+        if (page < 0 || page >= a.num_pages) {
+          if (lane == 0) dev_fail(a.err, kDevBadIndex, 1202);
+          page = -1;
+        }
+      }
+    }
+    if (lane == 0) {
+      pos_of[warp] = pos;
+      page_of[warp] = page;
     }
   }
+  __syncthreads();
+  for (int i = tid; i < a.rows * kPairs; i += kThreads) {
+    const int row = i / kPairs, t = i - row * kPairs, pos = pos_of[row];
+    if (pos >= 0 && (t < 64 ? t < half : t - 64 < half_idx)) {
+      const unsigned long long phase = turns_of[t] * (unsigned long long)pos;
+      float sn, cs;
+      sincospif((float)(int)(uint32_t)(phase >> 32) * 4.656612873077393e-10f, &sn, &cs);  // the top 32 bits, in half turns
+      turn[row][t] = make_float2(cs, sn);
+    }
+  }
+  __syncthreads();
 
-  // vectors: Hq queries, G keys, G values (8 items each), then G index queries and the index key (4 items each)
-  const int n_q = a.r.Q ? 8 * a.Hq : 0, n_k = 8 * a.G, n_v = 8 * a.G;
-  const int n_qi = a.r.q_idx ? 4 * a.G : 0, n_ki = a.r.k_idx ? 4 : 0;
-  const int n = n_q + n_k + n_v + n_qi + n_ki;
-  bool synced = false;
-  for (int base = 0; base < n; base += kThreads * kInFlight) {
-    uint4 x[kInFlight], y[kInFlight];
-    int pa[kInFlight], pb[kInFlight], pair[kInFlight], kind[kInFlight], vec[kInFlight];
+  for (int base = 0; base < a.rows * a.items; base += kThreads * kInFlight) {
+    if (base) {
+#pragma unroll
+      for (int z = 0; z < kInFlight; ++z) load_piece(a, r0, base + z * kThreads + tid, p[z]);
+    }
 #pragma unroll
     for (int z = 0; z < kInFlight; ++z) {
-      int it = base + z * kThreads + tid;
-      kind[z] = -1;
-      if (it >= n) continue;
-      const __nv_bfloat16* src;
-      if (it < n_q) {
-        kind[z] = 0;
-        src = static_cast<const __nv_bfloat16*>(a.r.Q) + (size_t)r * a.r.ld_Q;
-      } else if ((it -= n_q) < n_k) {
-        kind[z] = 1;
-        src = static_cast<const __nv_bfloat16*>(a.r.K) + (size_t)r * a.r.ld_K;
-      } else if ((it -= n_k) < n_v) {
-        kind[z] = 2;
-        src = static_cast<const __nv_bfloat16*>(a.r.V) + (size_t)r * a.r.ld_V;
-      } else if ((it -= n_v) < n_qi) {
-        kind[z] = 3;
-        src = static_cast<const __nv_bfloat16*>(a.r.q_idx) + (size_t)r * a.r.ld_q_idx;
-      } else {
-        it -= n_qi;
-        kind[z] = 4;
-        src = static_cast<const __nv_bfloat16*>(a.r.k_idx) + (size_t)r * a.r.ld_k_idx;
-      }
-      const bool idx = kind[z] >= 3;
-      vec[z] = idx ? it >> 2 : it >> 3;
-      item_pieces(idx ? it & 3 : it & 7, kind[z] == 2 ? 0 : (idx ? a.r.rot_idx : a.r.rot), a.r.interleaved, pa[z],
-                  pb[z], pair[z]);
-      const uint4* v = reinterpret_cast<const uint4*>(src + (size_t)vec[z] * (idx ? 64 : 128));
-      x[z] = v[pa[z]];
-      y[z] = v[pb[z]];
-    }
-    if (!synced) {
-      __syncthreads();
-      synced = true;
-    }
-    const int page = place[1], slot = place[2];
-#pragma unroll
-    for (int z = 0; z < kInFlight; ++z) {
-      if (kind[z] < 0) continue;
-      const bool idx = kind[z] >= 3;
-      if (pair[z] >= 0) rotate(x[z], y[z], turn + (idx ? 64 : 0) + pair[z], a.r.interleaved);
+      Piece& e = p[z];
+      if (e.kind < 0) continue;
+      const int pos = pos_of[e.row], page = page_of[e.row];
+      if (pos < 0) continue;
+      const bool idx = e.kind >= 3;
+      if (e.pair >= 0) rotate(e.x, e.y, turn[e.row] + (idx ? 64 : 0) + e.pair, a.r.interleaved);
+      const size_t r = r0 + e.row;
       __nv_bfloat16* dst;
-      if (kind[z] == 0) {
-        dst = static_cast<__nv_bfloat16*>(a.r.Q_out) + ((size_t)r * a.Hq + vec[z]) * 128;
-      } else if (kind[z] == 3) {
-        dst = static_cast<__nv_bfloat16*>(a.r.q_idx_out) + ((size_t)r * a.G + vec[z]) * 64;
+      if (e.kind == 0) {
+        dst = static_cast<__nv_bfloat16*>(a.r.Q_out) + (r * a.Hq + e.vec) * 128;
+      } else if (e.kind == 3) {
+        dst = static_cast<__nv_bfloat16*>(a.r.q_idx_out) + (r * a.G + e.vec) * 64;
       } else {
         if (page < 0) continue;
-        if (kind[z] == 4)
+        const int slot = pos & 127;
+        if (e.kind == 4)
           dst = a.k_idx + ((size_t)page * 128 + slot) * 64;
         else
-          dst = (kind[z] == 1 ? a.K : a.V) + (((size_t)page * a.G + vec[z]) * 128 + slot) * 128;
+          dst = (e.kind == 1 ? a.K : a.V) + (((size_t)page * a.G + e.vec) * 128 + slot) * 128;
       }
-      reinterpret_cast<uint4*>(dst)[pa[z]] = x[z];
-      reinterpret_cast<uint4*>(dst)[pb[z]] = y[z];
+      reinterpret_cast<uint4*>(dst)[e.a] = e.x;
+      reinterpret_cast<uint4*>(dst)[e.b] = e.y;
     }
   }
 }
@@ -257,7 +285,14 @@ cudaError_t launch_paged_append(const PagedProb& p, const PagedCachePtrs& c, con
   a.num_pages = p.num_pages;
   a.max_blocks = p.max_blocks;
   a.err = reinterpret_cast<int*>(ws);
-  paged_append_kernel<<<p.N, kThreads, 0, st>>>(a);
+  // four rows a block from where that still fills every SM a few times
+  a.rows = p.N >= 16 * kCutSms ? kMaxRows : 1;
+  a.n_q = r.Q ? 8 * p.Hq : 0;
+  a.n_k = 8 * p.G;
+  a.n_qi = r.q_idx ? 4 * p.G : 0;
+  a.items = a.n_q + 2 * a.n_k + a.n_qi + (r.k_idx ? 4 : 0);
+  a.inv_items = 1.f / (float)a.items;
+  paged_append_kernel<<<(p.N + a.rows - 1) / a.rows, kThreads, 0, st>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }

@@ -168,6 +168,8 @@ def _rows(name, t, shape, device):
     if t.is_contiguous():
         return t.data_ptr(), 0
     strides, packed = t.stride(), 1
+    if shape[0] > 1 and strides[-1] == 1 and (len(shape) == 2 or strides[1] == shape[2]):
+        return t.data_ptr(), strides[0]
     for n, st in zip(shape[:0:-1], strides[:0:-1]):
         if n != 1 and st != packed:
             _refuse(name, t, t.dtype, shape, device, packed=False)

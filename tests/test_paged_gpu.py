@@ -38,6 +38,8 @@ APPEND = {
     "no_rotation": dict(counts=[6], lens=[6], Hq=2, G=2, rot=0, rot_idx=0, fused=True),
     "no_index": dict(counts=[2, 2], lens=[140, 129], Hq=64, G=8, rot=128, rot_idx=0, index=False),
     "many_sequences": dict(counts=[1] * 70, lens=list(range(1, 141, 2)), Hq=2, G=1, rot=32, rot_idx=64),
+    "prefill": dict(counts=[2500, 0, 37], lens=[2600, 5, 37], pad=2, Hq=2, G=1, rot=128, rot_idx=64, fused=True),
+    "prefill_interleaved": dict(counts=[2433], lens=[4000], Hq=4, G=2, rot=64, rot_idx=16, interleaved=True),
     "in_place": dict(counts=[5], lens=[5], Hq=8, G=2, rot=128, rot_idx=64, in_place=True),
 }
 
