@@ -10,6 +10,10 @@ namespace msa {
 // depend on the machine that asks for it (any SM count runs the same cuts).
 constexpr int kCutSms = 152;
 
+// Words of a workspace's header behind the error word.
+constexpr int kLeadCount = 16;  // rows in PagedWs::lead
+constexpr int kWorkNext = 17;   // items that attention CTAs have taken beyond their first ones
+
 struct PagedProb {
   int S, N, Hq, G, hg, k;
   int num_pages, max_blocks, prefix;
@@ -20,6 +24,7 @@ struct PagedProb {
 struct PagedWs {
   size_t rows = 0;      // int4 [N]  per new row: sequence (-1: none, -2: refused), position, rows of its sequence before
                         //           it, and from it on
+  size_t lead = 0;      // int4 [N]  the rows that lead a tile: sequence, position, row, rows of the tile
   size_t arrived = 0;   // int32 [N, G, 3] parts of a (row tile, group) that are done, as each joining warp counts them
   size_t pooled = 0;    // fp32 [N, G, max_blocks] block maxima of the index scores
   size_t amax = 0;      // fp32 [S, max_blocks]    largest |index key| value of a block

@@ -9,19 +9,20 @@ namespace msa {
 static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Cuts `pages` pages of each of `tiles` row tiles into runs of equal length.
-// Every SM takes items in turn, so the time is the rounds of items times their
-// length, and an item costs about half a page more than its pages (its
-// queries, the warps' meeting, its part of O).
+// An item costs about a page more than its pages (its queries, the warps'
+// meeting, its part of O); SMs take items as they come, so the end is half an
+// item long.
 static void cut_pages(long long tiles, int pages, PagedWs* L) {
   tiles = std::max(1LL, tiles);
   pages = std::max(1, pages);
-  long long best = 0;
-  for (int rounds = 0; rounds <= 8; ++rounds) {
-    const long long want = rounds ? std::max(1LL, rounds * (long long)kCutSms / tiles) : 1;
+  double best = 0;
+  for (int i = -2; i <= 8; ++i) {
+    // two and three runs, and what gives every SM one, two, ... items
+    const long long want = i < 0 ? 1 - i : i == 0 ? 1 : std::max(1LL, i * (long long)kCutSms / tiles);
     const int per = (int)((pages + std::min<long long>(want, pages) - 1) / std::min<long long>(want, pages));
     const int splits = (pages + per - 1) / per;
-    const long long cost = (tiles * splits + kCutSms - 1) / kCutSms * (2 * per + 1);
-    if (!best || cost < best) {
+    const double cost = (std::max(1.0, (double)tiles * splits / kCutSms) + 0.5) * (per + 1);
+    if (best == 0 || cost < best) {
       best = cost;
       L->per_split = per;
       L->splits = splits;
@@ -42,6 +43,7 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
     return L;
   }
   L.rows = take((size_t)p.N * 16);
+  L.lead = take((size_t)p.N * 16);
   L.arrived = take((size_t)p.N * p.G * 12);
   if (which == MSA_WS_PAGED_SPARSE) {
     L.pooled = take((size_t)p.N * p.G * p.max_blocks * 4);

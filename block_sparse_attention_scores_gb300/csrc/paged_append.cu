@@ -220,50 +220,72 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// First launch of the attentions: clears the error word and the counters of
-// finished parts, and finds every new row's sequence and position. A row whose
+// First launch of the attentions: clears the header and the counters of
+// finished parts, finds every new row's sequence and position, and lists the
+// rows that lead a tile. One block: it moves a few bytes per row. A row whose
 // position lies outside the page table (or, behind a shared prefix, inside the
-// prefix) is marked; the attention reports it and leaves it out.
+// prefix) is reported and left out.
 struct RowsArgs {
   const int32_t *row_start, *seq_len;
-  int4* rows;
-  int *arrived, *err;
-  int S, N, G, max_blocks, prefix;
+  int4 *rows, *lead;
+  int *arrived, *header;
+  int S, N, n_arrived, max_blocks, prefix, tile_rows;
 };
 
+constexpr int kRowThreads = 1024;
 constexpr int kStaged = 4096;  // sequence starts kept in shared memory
 
-__global__ void __launch_bounds__(kThreads) paged_rows_kernel(RowsArgs a) {
+__global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(RowsArgs a) {
   __shared__ int staged[kStaged];
+  __shared__ int sums[32];
   // released after the wait: the index scores, launched then, have only this kernel's own work to wait for (at their end)
   pdl_wait();
   pdl_release();
-  const int tid = threadIdx.x;
-  if (blockIdx.x == 0 && tid < 64) a.err[tid] = 0;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool all = a.S + 1 <= kStaged;
-  if (all) {
-    for (int i = tid; i <= a.S; i += kThreads) staged[i] = ld_in(a.row_start + i);
+  if (tid < 64) a.header[tid] = 0;
+  if (all)
+    for (int i = tid; i <= a.S; i += kRowThreads) staged[i] = ld_in(a.row_start + i);
+  for (int i = tid; i < a.n_arrived; i += kRowThreads) a.arrived[i] = 0;
+  __syncthreads();
+  auto start = [&](int i) { return all ? staged[i] : ld_in(a.row_start + i); };
+  int leads = 0;
+  for (int r0 = 0; r0 < a.N; r0 += kRowThreads) {
+    const int r = r0 + tid;
+    int4 out = make_int4(-1, 0, 0, 0);
+    if (r < a.N) {
+      int lo = 0, hi = a.S + 1;  // start(lo) <= r (the first counts as 0), start(hi) > r
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start(mid) <= r) lo = mid;
+        else hi = mid;
+      }
+      if (lo < a.S) {
+        const int len = ld_in(a.seq_len + lo), begin = start(lo), end = start(lo + 1);
+        if (len < end - r + a.prefix * 128 || len > a.max_blocks * 128) {
+          out.x = -2;
+          dev_fail(a.header, kDevBadIndex, 1211);
+        } else {
+          out = make_int4(lo, len - (end - r), r - begin, (end < a.N ? end : a.N) - r);
+        }
+      }
+      a.rows[r] = out;
+    }
+    if (a.tile_rows == 1) continue;
+    // the rows that lead a tile, in order
+    const bool lead = out.x >= 0 && out.z % a.tile_rows == 0;
+    const unsigned m = __ballot_sync(0xffffffffu, lead);
+    if (lane == 0) sums[warp] = __popc(m);
+    __syncthreads();
+    int before = leads;
+    for (int w = 0; w < kRowThreads / 32; ++w) {
+      if (w < warp) before += sums[w];
+      leads += sums[w];
+    }
+    if (lead) a.lead[before + __popc(m & ((1u << lane) - 1))] = make_int4(out.x, out.y, r, min(a.tile_rows, out.w));
     __syncthreads();
   }
-  auto start = [&](int i) { return all ? staged[i] : ld_in(a.row_start + i); };
-  const int r = blockIdx.x * kThreads + tid;
-  if (r >= a.N) return;
-  for (int i = 0; i < 3 * a.G; ++i) a.arrived[(size_t)r * 3 * a.G + i] = 0;
-  int lo = 0, hi = a.S + 1;  // start(lo) <= r (the first counts as 0), start(hi) > r
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (start(mid) <= r) lo = mid;
-    else hi = mid;
-  }
-  int4 out = make_int4(-1, 0, 0, 0);
-  if (lo < a.S) {
-    const int len = ld_in(a.seq_len + lo), begin = start(lo), end = start(lo + 1);
-    if (len < end - r + a.prefix * 128 || len > a.max_blocks * 128)
-      out.x = -2;
-    else
-      out = make_int4(lo, len - (end - r), r - begin, (end < a.N ? end : a.N) - r);
-  }
-  a.rows[r] = out;
+  if (tid == 0) a.header[kLeadCount] = leads;
 }
 
 }  // namespace
@@ -303,15 +325,17 @@ cudaError_t launch_paged_rows(const PagedProb& p, const PagedCachePtrs& c, uint8
   a.row_start = c.row_start;
   a.seq_len = c.seq_len;
   a.rows = reinterpret_cast<int4*>(ws + L.rows);
+  a.lead = reinterpret_cast<int4*>(ws + L.lead);
   a.arrived = reinterpret_cast<int*>(ws + L.arrived);
-  a.err = reinterpret_cast<int*>(ws);
+  a.header = reinterpret_cast<int*>(ws);
   a.S = p.S;
   a.N = p.N;
-  a.G = p.G;
+  a.n_arrived = L.splits > 1 ? p.N * p.G * 3 : 0;  // (few rows: others are not cut)
   a.max_blocks = p.max_blocks;
   a.prefix = p.prefix;
+  a.tile_rows = L.tile_rows;
   count_launches(1);
-  return launch_dependent(paged_rows_kernel, (p.N + kThreads - 1) / kThreads, kThreads, 0, st, a);
+  return launch_dependent(paged_rows_kernel, 1, kRowThreads, 0, st, a);
 }
 
 }  // namespace msa

@@ -48,6 +48,8 @@ constexpr int smem_bytes() {
 
 struct AttnArgs {
   const int4* rows;
+  const int4* lead;                       // the rows that lead a tile (null: every row does)
+  int* header;                            // of the workspace: kLeadCount, kWorkNext
   const __nv_bfloat16* Q;
   const int32_t *page_table, *block_idx;  // block_idx null: the sequence's own pages from block `prefix` on
   float *part_o, *part_lse;
@@ -107,15 +109,15 @@ struct Fetch {
   int block, page;     // of this lane's page (the item's first 32)
 };
 
-// Items: (row, split, group), group fastest. A row that does not lead its tile has none.
-__device__ __forceinline__ void fetch_row(const AttnArgs& a, int item, int lane, Fetch& f) {
+// Items: (row tile, split, group), group fastest.
+__device__ __forceinline__ void fetch_row(const AttnArgs& a, int item, int items, int lane, Fetch& f) {
   f.row = -1;
-  if (item >= a.items) return;
+  if (item >= items) return;
   f.g = item % a.G;
   const int t = item / a.G;
   f.split = t % a.splits;
   f.row = t / a.splits;
-  f.info = ld_in(a.rows + f.row);
+  f.info = ld_in((a.lead ? a.lead : a.rows) + f.row);
   if (a.block_idx) {
     const int32_t* ids = a.block_idx + ((size_t)f.row * a.G + f.g) * a.k;
     const int at = f.split * a.per_split + lane;
@@ -129,11 +131,11 @@ __device__ __forceinline__ void fetch_row(const AttnArgs& a, int item, int lane,
 __device__ __forceinline__ void fetch_pages(const AttnArgs& a, int lane, Fetch& f) {
   f.page = -1;
   if (f.row < 0) return;
-  if (f.info.x == -2 && f.split == 0 && f.g == 0 && lane == 0) dev_fail(a.err, kDevBadIndex, 1211);
-  if (f.info.x < 0 || f.info.z % a.tile_rows) {
+  if (f.info.x < 0) {
     f.row = -1;
     return;
   }
+  if (a.lead) f.row = f.info.z;
   if (a.block_idx) {
     int have = 0;  // ids stand at the front of the list
 #pragma unroll
@@ -253,15 +255,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t st = 0, st_ph = 0;  // stage and its parity
     int n_item = 0;              // items handed over
     bool ok = true;
-    const int step = gridDim.x;
-    int id = blockIdx.x;
-    Fetch now, next, after;
-    fetch_row(a, id, lane, now);
-    fetch_row(a, id + step, lane, next);
+    // Items are taken as they come, the first one by the CTA's number: their lengths differ. The next one is looked for
+    // when the last four pages are being asked for, one step a page: its number, its row, its pages.
+    const int items = a.lead ? ld_in(a.header + kLeadCount) * a.splits * a.G : a.items;
+    int id = blockIdx.x, id_next = 0, taken = 0, step = 0;
+    Fetch now, next;
+    auto advance = [&]() {
+      if (step == 0) {
+        if (lane == 0) taken = atomicAdd(a.header + kWorkNext, 1);
+      } else if (step == 1) {
+        id_next = gridDim.x + __shfl_sync(0xffffffffu, taken, 0);
+        fetch_row(a, id_next, items, lane, next);
+      } else if (step == 2) {
+        fetch_pages(a, lane, next);
+      }
+      ++step;
+    };
+    fetch_row(a, id, items, lane, now);
     fetch_pages(a, lane, now);
-    for (; ok && id < a.items; id += step) {
-      fetch_row(a, id + 2 * step, lane, after);
-      fetch_pages(a, lane, next);
+    for (; ok && id < items; id = id_next, now = next) {
+      step = 0;
       if (now.row >= 0) {
         const int rows = min(a.tile_rows, now.info.w), qs = n_item & 1;
         if (!mbar_wait(&sh.q_empty[qs], ((n_item >> 1) & 1) ^ 1, a.err, 1401)) { ok = false; break; }
@@ -309,11 +322,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               st = 0;
               st_ph ^= 1;
             }
+            if (now.pages - (j0 + i) <= 4) advance();
           }
         }
       }
-      now = next;
-      next = after;
+      while (step < 3) advance();
     }
     // the end
     const int qs = n_item & 1;
@@ -700,6 +713,8 @@ cudaError_t launch_paged_attn(const PagedProb& p, const PagedCachePtrs& c, const
   if (!encode_pool_map(&mk, p, c.K) || !encode_pool_map(&mv, p, c.V)) return cudaErrorInvalidValue;
   AttnArgs a;
   a.rows = reinterpret_cast<const int4*>(ws + L.rows);
+  a.lead = L.tile_rows > 1 ? reinterpret_cast<const int4*>(ws + L.lead) : nullptr;
+  a.header = reinterpret_cast<int*>(ws);
   a.Q = static_cast<const __nv_bfloat16*>(Q);
   a.page_table = c.page_table;
   a.block_idx = block_idx;
