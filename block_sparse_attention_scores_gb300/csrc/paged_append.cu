@@ -232,7 +232,7 @@ struct RowsArgs {
   int S, N, n_arrived, max_blocks, prefix, tile_rows;
 };
 
-constexpr int kRowThreads = 1024;
+constexpr int kRowThreads = 1024;  // 256 for up to as many rows: a smaller block starts sooner
 constexpr int kStaged = 4096;  // sequence starts kept in shared memory
 
 __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(RowsArgs a) {
@@ -241,16 +241,16 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(RowsArgs a) {
   // released after the wait: the index scores, launched then, have only this kernel's own work to wait for (at their end)
   pdl_wait();
   pdl_release();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   const bool all = a.S + 1 <= kStaged;
   if (tid < 64) a.header[tid] = 0;
   if (all)
-    for (int i = tid; i <= a.S; i += kRowThreads) staged[i] = ld_in(a.row_start + i);
-  for (int i = tid; i < a.n_arrived; i += kRowThreads) a.arrived[i] = 0;
+    for (int i = tid; i <= a.S; i += threads) staged[i] = ld_in(a.row_start + i);
+  for (int i = tid; i < a.n_arrived; i += threads) a.arrived[i] = 0;
   __syncthreads();
   auto start = [&](int i) { return all ? staged[i] : ld_in(a.row_start + i); };
   int leads = 0;
-  for (int r0 = 0; r0 < a.N; r0 += kRowThreads) {
+  for (int r0 = 0; r0 < a.N; r0 += threads) {
     const int r = r0 + tid;
     int4 out = make_int4(-1, 0, 0, 0);
     if (r < a.N) {
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(RowsArgs a) {
     if (lane == 0) sums[warp] = __popc(m);
     __syncthreads();
     int before = leads;
-    for (int w = 0; w < kRowThreads / 32; ++w) {
+    for (int w = 0; w < threads / 32; ++w) {
       if (w < warp) before += sums[w];
       leads += sums[w];
     }
@@ -335,7 +335,7 @@ cudaError_t launch_paged_rows(const PagedProb& p, const PagedCachePtrs& c, uint8
   a.prefix = p.prefix;
   a.tile_rows = L.tile_rows;
   count_launches(1);
-  return launch_dependent(paged_rows_kernel, 1, kRowThreads, 0, st, a);
+  return launch_dependent(paged_rows_kernel, 1, p.N <= 256 ? 256 : kRowThreads, 0, st, a);
 }
 
 }  // namespace msa
