@@ -35,15 +35,13 @@ constexpr int kThreads = (kWarps + 1 + kJoinWarps) * 32;
 constexpr int kHalf = 16384;                       // 128 rows x 64 bf16, 128-byte swizzle
 constexpr int kTile = 2 * kHalf;                   // K or V of a page and group
 constexpr int kStages = 3;
-constexpr int kSlots = 4;                          // shared-memory O buffers: two warps meet in each
 constexpr unsigned long long kIdleLimitNs = 20000000000ull;  // the joining warps may have nothing to do for a while
-constexpr int kOStride = 132;                      // floats between columns of an O buffer (no bank conflicts)
 
 constexpr int kQStride = 272;                      // bytes between the queries' rows in shared memory (no bank conflicts)
 
 template <int NT>
 constexpr int smem_bytes() {
-  return kStages * 2 * kTile + kSlots * 8 * kOStride * 4 + 2 * NT * 8 * kQStride + 1024;
+  return kStages * 2 * kTile + 2 * NT * 8 * kQStride + 1024;
 }
 
 struct AttnArgs {
@@ -71,13 +69,12 @@ struct AttnShared {
   uint64_t k_full[kStages], v_full[kStages], empty[kStages];
   uint64_t q_full[2], q_empty[2];
   uint64_t meet;              // the consumer warps' rendezvous
-  uint64_t s_free;            // the O buffers have been read
   uint64_t j_full[2], j_empty[2];
   AttnItem item[2];
   AttnItem join[2];           // for the joining warps; parts 0: the end
   int token0[kStages];        // first token of the stage's page
-  float m[kWarps][8], l[kWarps][8];
-  float inv[8], lse[8];       // of all warps together: 1 / sum, and log2 of the sum
+  float m[kWarps][16], l[kWarps][16];  // maximum and sum of a warp's columns
+  float inv[16], lse[16];              // of all warps together: 1 / sum, and log2 of the sum
 };
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -223,8 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ AttnShared sh;
-  float* s_o = reinterpret_cast<float*>(smem + kStages * 2 * kTile);  // [slot][8 columns][kOStride]
-  uint8_t* s_q = smem + kStages * 2 * kTile + kSlots * 8 * kOStride * 4;  // [2][NT * 8][kQStride]
+  uint8_t* s_q = smem + kStages * 2 * kTile;  // [2][NT * 8][kQStride]
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -241,7 +237,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.j_empty[i], kJoinWarps);
     }
     mbar_init(&sh.meet, kWarps);
-    mbar_init(&sh.s_free, kWarps);
     fence_barrier_init();
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
@@ -359,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- consumers
     const int r = lane >> 2, q = lane & 3;
     uint32_t st = 0, st_ph = 0, meet_ph = 0;
-    int n_pass = 0, n_join = 0;  // uses of the O buffers; items handed to the joining warps
+    int n_join = 0;  // items handed to the joining warps
     bool ok = true;
     for (int n_item = 0; ok; ++n_item) {
       const int qs = n_item & 1;
@@ -518,6 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        if (j + 1 == item.pages) break;  // the last page's stage is kept: the warps' results meet in it
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[st]);
         if (++st == kStages) {
@@ -527,89 +523,87 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
 
-      // ---- the warps' results meet, eight columns at a time: the upper four warps store theirs, the lower four scale
-      // them and their own to the maximum of all and add them, and all 256 threads add up the four sums
+      // ---- the warps' results meet: each scales its O to the maximum of all and puts it into the last page's stage
+      // ([warp][column][d], d exchanged by column against bank conflicts), and all 256 threads add up the eight
       const bool joined = a.join && item.parts > 1;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt, ++n_pass) {
-        float l[2];
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          l[z] = l_run[nt][z];
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) l[z] += __shfl_xor_sync(0xffffffffu, l[z], x);
+      const int d = threadIdx.x & 127;  // one dim of every other column
+      auto put = [&](int col, float val, float lse) {
+        const size_t at = (size_t)(item.row + (col >> a.hg_log2)) * a.Hq + item.g * a.hg + (col & (a.hg - 1));
+        if (a.join && !joined) {
+          a.O[at * 128 + d] = __float2bfloat16_rn(val);
+          if (d == 0) a.LSE[at] = lse * 0.6931471805599453f;
+        } else {
+          const size_t pt = (size_t)(a.slot0 + item.split) * a.N * a.Hq + at;
+          a.part_o[pt * 128 + d] = val;
+          if (d == 0) a.part_lse[pt] = lse;
         }
-        float* mine = s_o + (warp & (kSlots - 1)) * 8 * kOStride;
-        auto place = [&](int mt, int z) { return (2 * q + (z & 1)) * kOStride + mt * 16 + r + (z >> 1) * 8; };
-        if (!mbar_wait(&sh.s_free, (n_pass & 1) ^ 1, a.err, 1424)) { ok = false; break; }
-        if (r == 0) {
+      };
+      if (item.pages == 0) {  // nothing selected
+        for (int col = threadIdx.x >> 7; col < cols; col += 2) put(col, 0.f, -INFINITY);
+      } else {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            sh.m[warp][2 * q + z] = m_run[nt][z];
-            sh.l[warp][2 * q + z] = l[z];
+            float l = l_run[nt][z];
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+            if (r == 0) {
+              sh.m[warp][8 * nt + 2 * q + z] = m_run[nt][z];
+              sh.l[warp][8 * nt + 2 * q + z] = l;
+            }
           }
-        }
-        if (warp >= kSlots) {
-#pragma unroll
-          for (int mt = 0; mt < 8; ++mt)
-#pragma unroll
-            for (int z = 0; z < 4; ++z) mine[place(mt, z)] = o[nt][mt][z];
-        }
         if (!warps_sync(&sh.meet, meet_ph, a.err, 1425)) { ok = false; break; }
-        if (warp < kSlots) {
-          float f[2], g[2];
+        float* s_o = reinterpret_cast<float*>(smem + st * 2 * kTile);
+        float* mine = s_o + warp * NT * 8 * 128;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float f[2];  // what this warp's O counts for (0 where no warp saw a key)
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            const int c = 2 * q + z;
-            float mw[kWarps], mm = -INFINITY;
+            float mm = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-              mw[w] = sh.m[w][c];
-              mm = fmaxf(mm, mw[w]);
-            }
-            const float base = mm == -INFINITY ? 0.f : mm;  // no warp saw a key: every factor is 0
-            f[z] = fast_exp2(m_run[nt][z] - base);
-            g[z] = fast_exp2(sh.m[warp + kSlots][c] - base);
-            if (warp == 0) {
-              float den = 0.f;
-#pragma unroll
-              for (int w = 0; w < kWarps; ++w) den = fmaf(fast_exp2(mw[w] - base), sh.l[w][c], den);
-              if (r == 0) {
-                sh.inv[c] = mm > -INFINITY ? 1.f / den : 0.f;
-                sh.lse[c] = mm > -INFINITY ? mm + log2f(den) : -INFINITY;
-              }
-            }
+            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sh.m[w][8 * nt + 2 * q + z]);
+            f[z] = fast_exp2(m_run[nt][z] - (mm == -INFINITY ? 0.f : mm));
           }
 #pragma unroll
           for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              float& at = mine[place(mt, z)];
-              at = fmaf(o[nt][mt][z], f[z & 1], at * g[z & 1]);
+            for (int z = 0; z < 4; ++z)
+              mine[(8 * nt + 2 * q + (z & 1)) * 128 + ((mt * 16 + r + (z >> 1) * 8) ^ (q << 3))] = o[nt][mt][z] * f[z & 1];
+          {
+            // column 8 nt + warp's sum: lane w % 8 has warp w's
+            const int c = 8 * nt + warp;
+            const float m = sh.m[lane & 7][c];
+            float mm = m;
+#pragma unroll
+            for (int x = 1; x < 8; x <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
+            float den = fast_exp2(m - (mm == -INFINITY ? 0.f : mm)) * sh.l[lane & 7][c];
+#pragma unroll
+            for (int x = 1; x < 8; x <<= 1) den += __shfl_xor_sync(0xffffffffu, den, x);
+            if (lane == 0) {
+              sh.inv[c] = mm > -INFINITY ? __frcp_rn(den) : 0.f;
+              sh.lse[c] = mm > -INFINITY ? mm + log2f(den) : -INFINITY;
             }
+          }
         }
         if (!warps_sync(&sh.meet, meet_ph, a.err, 1426)) { ok = false; break; }
-        const int d = threadIdx.x & 127;  // one dim of every other column
 #pragma unroll
-        for (int c = 0; c < 8; c += 2) {
-          const int cc = c + (threadIdx.x >> 7), col = 8 * nt + cc;
+        for (int c = 0; c < 8 * NT; c += 2) {
+          const int col = c + (threadIdx.x >> 7);
           if (col >= cols) break;
           float val = 0.f;
 #pragma unroll
-          for (int w = 0; w < kSlots; ++w) val += s_o[(w * 8 + cc) * kOStride + d];
-          val *= sh.inv[cc];
-          const size_t at = (size_t)(item.row + (col >> a.hg_log2)) * a.Hq + item.g * a.hg + (col & (a.hg - 1));
-          if (a.join && !joined) {
-            a.O[at * 128 + d] = __float2bfloat16_rn(val);
-            if (d == 0) a.LSE[at] = sh.lse[cc] * 0.6931471805599453f;
-          } else {
-            const size_t pt = (size_t)(a.slot0 + item.split) * a.N * a.Hq + at;
-            a.part_o[pt * 128 + d] = val;
-            if (d == 0) a.part_lse[pt] = sh.lse[cc];
-          }
+          for (int w = 0; w < kWarps; ++w) val += s_o[(w * NT * 8 + col) * 128 + (d ^ ((col & 6) << 2))];
+          put(col, val * sh.inv[col], sh.lse[col]);
         }
+        fence_proxy_async_smem();  // the stage goes back to TMA
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.s_free);
+        if (lane == 0) mbar_arrive(&sh.empty[st]);
+        if (++st == kStages) {
+          st = 0;
+          st_ph ^= 1;
+        }
       }
       if (!ok) break;
       if (joined) {
