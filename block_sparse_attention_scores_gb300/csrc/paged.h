@@ -25,6 +25,8 @@ struct PagedWs {
   size_t rows = 0;      // int4 [N]  per new row: sequence (-1: none, -2: refused), position, rows of its sequence before
                         //           it, and from it on
   size_t lead = 0;      // int4 [N]  the rows that lead a tile: sequence, position, row, rows of the tile
+  size_t flags = 0;     // int32 [n_flags] what the blocks of the index scores or of the shared prefix found wrong
+  int n_flags = 0;      // those blocks
   size_t arrived = 0;   // int32 [N, G, 3] parts of a (row tile, group) that are done, as each joining warp counts them
   size_t pooled = 0;    // fp32 [N, G, max_blocks] block maxima of the index scores
   size_t amax = 0;      // fp32 [S, max_blocks]    largest |index key| value of a block
@@ -63,8 +65,7 @@ struct RopeRows {
 
 cudaError_t launch_paged_append(const PagedProb& p, const PagedCachePtrs& c, const RopeRows& r, uint8_t* ws,
                                 cudaStream_t st);
-// Clears the header and the counters, and finds the sequence and position of
-// every new row: the first launch of the attentions.
+// The call's first work (paged_rows.cuh) as a kernel of its own; the index scores and the shared prefix do it themselves.
 cudaError_t launch_paged_rows(const PagedProb& p, const PagedCachePtrs& c, uint8_t* ws, const PagedWs& L,
                               cudaStream_t st);
 cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, const void* q_idx, int32_t* block_idx,

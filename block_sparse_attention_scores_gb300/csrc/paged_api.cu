@@ -48,6 +48,8 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
   if (which == MSA_WS_PAGED_SPARSE) {
     L.pooled = take((size_t)p.N * p.G * p.max_blocks * 4);
     L.amax = take((size_t)p.S * p.max_blocks * 4);
+    if (p.k > 1) L.n_flags = (int)std::min<long long>((long long)p.S * ((p.max_blocks + 4) / 6), kCutSms - 1);
+    L.flags = take(kCutSms * 4);
     cut_pages((long long)p.N * p.G, std::min(p.k, p.max_blocks), &L);
   } else {
     // more columns (rows x heads of a sequence) than eight on average: two column tiles share each page
@@ -59,6 +61,8 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
       L.pairs = (tiles + 1) / 2;
       const int units = p.G * p.prefix;
       L.teams = std::min(units, std::max(1, kCutSms / L.pairs));
+      L.n_flags = L.teams * L.pairs;
+      L.flags = take((size_t)L.n_flags * 4);
       for (int g = 0; g < p.G; ++g)
         L.pslots = std::max(L.pslots, team_of((g + 1) * p.prefix - 1, units, L.teams) -
                                           team_of(g * p.prefix, units, L.teams) + 1);
@@ -133,10 +137,6 @@ static msa_status check_paged_ws(const PagedProb& p, int which, void* ws, size_t
   return MSA_OK;
 }
 
-static msa_status clear_header(void* ws, cudaStream_t st) {
-  return cuda_status(cudaMemsetAsync(ws, 0, 256, st), "clearing workspace header");
-}
-
 // One new-row input: present with its output, 16-byte rows.
 static msa_status check_rows(const void* ptr, const char* name, int64_t* ld, int64_t packed) {
   msa_status s;
@@ -201,7 +201,6 @@ msa_status msa_paged_append(const msa_paged_shape* shape, const msa_paged_cache*
   if ((s = check_paged_ws(p, MSA_WS_PAGED_APPEND, workspace, workspace_bytes, &L)) != MSA_OK) return s;
   if ((s = check_device()) != MSA_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if ((s = clear_header(workspace, st)) != MSA_OK) return s;
   RopeRows r;
   r.Q = n.Q;
   r.K = n.K;
@@ -242,8 +241,9 @@ msa_status msa_paged_sparse_attn(const msa_paged_shape* shape, const msa_paged_c
   if ((s = check_device()) != MSA_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  if ((s = cuda_status(launch_paged_rows(p, c, w, L, st), "paged rows launch")) != MSA_OK) return s;
-  if (q_idx && (s = cuda_status(launch_paged_index(p, c, q_idx, block_idx, w, L, st), "paged index launch")) != MSA_OK)
+  if (!q_idx) L.n_flags = 0;
+  if ((s = cuda_status(q_idx ? launch_paged_index(p, c, q_idx, block_idx, w, L, st) : launch_paged_rows(p, c, w, L, st),
+                       "paged index launch")) != MSA_OK)
     return s;
   return cuda_status(launch_paged_attn(p, c, Q, block_idx, O, LSE, w, L, st), "paged attention launch");
 }
@@ -263,9 +263,8 @@ msa_status msa_paged_dense_attn(const msa_paged_shape* shape, const msa_paged_ca
   if ((s = check_device()) != MSA_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  if ((s = cuda_status(launch_paged_rows(p, c, w, L, st), "paged rows launch")) != MSA_OK) return s;
-  if (p.prefix &&
-      (s = cuda_status(launch_paged_prefix(p, c, Q, w, L, st), "paged prefix launch")) != MSA_OK)
+  if ((s = cuda_status(p.prefix ? launch_paged_prefix(p, c, Q, w, L, st) : launch_paged_rows(p, c, w, L, st),
+                       "paged prefix launch")) != MSA_OK)
     return s;
   if ((s = cuda_status(launch_paged_attn(p, c, Q, nullptr, O, LSE, w, L, st), "paged attention launch")) != MSA_OK)
     return s;

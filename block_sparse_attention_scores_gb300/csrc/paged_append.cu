@@ -14,9 +14,7 @@
 // into items of two 16-byte pieces (the two halves of eight pairs, or two
 // neighbours), one thread each, whose loads are on their way before the row's
 // place and angles are looked up.
-#include "paged.h"
-#include "pdl.cuh"
-#include "sm100.cuh"
+#include "paged_rows.cuh"
 
 namespace msa {
 namespace {
@@ -32,26 +30,11 @@ struct AppendArgs {
   const int32_t *page_table, *row_start, *seq_len;
   int S, N, Hq, G, num_pages, max_blocks;
   int rows;                      // of a block
+  int report;                    // the last block checks every row and writes the error word; the others write none
   int n_q, n_k, n_qi, items;     // items of a row: queries, keys (values as many), index queries; all
   float inv_items;
   int* err;
 };
-
-// Largest s with row_start[s] <= r, by the whole warp: 32 probes a step.
-__device__ __forceinline__ int find_sequence(const int32_t* row_start, int S, int r, int lane) {
-  int lo = 0, n = S + 1;  // the answer lies in [lo, lo + n); row_start[0] counts as 0
-  while (n > 1) {
-    const int step = (n + 31) / 32;
-    const int at = lo + lane * step;
-    const bool in = lane == 0 || (lane * step < n && __ldg(row_start + at) <= r);
-    const unsigned m = __ballot_sync(0xffffffffu, in);
-    const int last = 31 - __clz(m);
-    const int left = n - last * step;
-    lo += last * step;
-    n = left < step ? left : step;
-  }
-  return lo;
-}
 
 __device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
@@ -134,7 +117,30 @@ __device__ __forceinline__ void load_piece(const AppendArgs& a, int r0, int it, 
   p.y = v[p.b];
 }
 
+// Place of row r in a sequence of length len with `left` rows from r on, or a code for what is wrong with it.
+__device__ __forceinline__ int place_row(const AppendArgs& a, int s, int len, int left, int& pos, int& page) {
+  pos = page = -1;
+  if (len < left || len > a.max_blocks * 128) return 1201;
+  pos = len - left;
+  page = ld_in(a.page_table + (size_t)s * a.max_blocks + (pos >> 7));
+  if (page >= 0 && page < a.num_pages) return 0;
+  page = -1;
+  return 1202;
+}
+
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
+  if (a.report && blockIdx.x == gridDim.x - 1) {
+    int bad = 0;
+    const auto start = [&](int i) { return ld_in(a.row_start + i); };
+    for (int r = threadIdx.x; r < a.N; r += kThreads) {
+      const int s = bisect_rows(start, a.S, r);
+      int pos, page;
+      if (s < a.S) bad = max(bad, place_row(a, s, ld_in(a.seq_len + s), start(s + 1) - r, pos, page));
+    }
+    const int second = __syncthreads_or(bad == 1202), first = __syncthreads_or(bad == 1201);
+    if (threadIdx.x == 0) *a.err = first ? kDevBadIndex * 65536 + 1201 : second ? kDevBadIndex * 65536 + 1202 : kDevOk;
+    return;
+  }
   __shared__ unsigned long long turns_of[kPairs];  // frequency as a fraction of a turn per position
   __shared__ float2 turn[kMaxRows][kPairs];        // cos, sin of a row's pairs: d, then d_idx
   __shared__ int pos_of[kMaxRows], page_of[kMaxRows];  // -1: no row, or not to be written
@@ -157,17 +163,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
     int pos = -1, page = -1;
     const int s = r < a.N ? find_sequence(a.row_start, a.S, r, lane) : a.S;
     if (s < a.S) {  // not behind the last sequence
-      const int len = __ldg(a.seq_len + s), end = __ldg(a.row_start + s + 1);
-      if (len < end - r || len > a.max_blocks * 128) {
-        if (lane == 0) dev_fail(a.err, kDevBadIndex, 1201);
-      } else {
-        pos = len - (end - r);
-        page = __ldg(a.page_table + (size_t)s * a.max_blocks + (pos >> 7));
-        if (page < 0 || page >= a.num_pages) {
-          if (lane == 0) dev_fail(a.err, kDevBadIndex, 1202);
-          page = -1;
-        }
-      }
+      const int bad = place_row(a, s, ld_in(a.seq_len + s), ld_in(a.row_start + s + 1) - r, pos, page);
+      if (bad && !a.report && lane == 0) dev_fail(a.err, kDevBadIndex, bad);
     }
     if (lane == 0) {
       pos_of[warp] = pos;
@@ -219,75 +216,6 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
   }
 }
 
-// ---------------------------------------------------------------------------
-// First launch of the attentions: clears the header and the counters of
-// finished parts, finds every new row's sequence and position, and lists the
-// rows that lead a tile. One block: it moves a few bytes per row. A row whose
-// position lies outside the page table (or, behind a shared prefix, inside the
-// prefix) is reported and left out.
-struct RowsArgs {
-  const int32_t *row_start, *seq_len;
-  int4 *rows, *lead;
-  int *arrived, *header;
-  int S, N, n_arrived, max_blocks, prefix, tile_rows;
-};
-
-constexpr int kRowThreads = 1024;  // 256 for up to as many rows: a smaller block starts sooner
-constexpr int kStaged = 4096;  // sequence starts kept in shared memory
-
-__global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(RowsArgs a) {
-  __shared__ int staged[kStaged];
-  __shared__ int sums[32];
-  // released after the wait: the index scores, launched then, have only this kernel's own work to wait for (at their end)
-  pdl_wait();
-  pdl_release();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
-  const bool all = a.S + 1 <= kStaged;
-  if (tid < 64) a.header[tid] = 0;
-  if (all)
-    for (int i = tid; i <= a.S; i += threads) staged[i] = ld_in(a.row_start + i);
-  for (int i = tid; i < a.n_arrived; i += threads) a.arrived[i] = 0;
-  __syncthreads();
-  auto start = [&](int i) { return all ? staged[i] : ld_in(a.row_start + i); };
-  int leads = 0;
-  for (int r0 = 0; r0 < a.N; r0 += threads) {
-    const int r = r0 + tid;
-    int4 out = make_int4(-1, 0, 0, 0);
-    if (r < a.N) {
-      int lo = 0, hi = a.S + 1;  // start(lo) <= r (the first counts as 0), start(hi) > r
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (start(mid) <= r) lo = mid;
-        else hi = mid;
-      }
-      if (lo < a.S) {
-        const int len = ld_in(a.seq_len + lo), begin = start(lo), end = start(lo + 1);
-        if (len < end - r + a.prefix * 128 || len > a.max_blocks * 128) {
-          out.x = -2;
-          dev_fail(a.header, kDevBadIndex, 1211);
-        } else {
-          out = make_int4(lo, len - (end - r), r - begin, (end < a.N ? end : a.N) - r);
-        }
-      }
-      a.rows[r] = out;
-    }
-    if (a.tile_rows == 1) continue;
-    // the rows that lead a tile, in order
-    const bool lead = out.x >= 0 && out.z % a.tile_rows == 0;
-    const unsigned m = __ballot_sync(0xffffffffu, lead);
-    if (lane == 0) sums[warp] = __popc(m);
-    __syncthreads();
-    int before = leads;
-    for (int w = 0; w < threads / 32; ++w) {
-      if (w < warp) before += sums[w];
-      leads += sums[w];
-    }
-    if (lead) a.lead[before + __popc(m & ((1u << lane) - 1))] = make_int4(out.x, out.y, r, min(a.tile_rows, out.w));
-    __syncthreads();
-  }
-  if (tid == 0) a.header[kLeadCount] = leads;
-}
-
 }  // namespace
 
 cudaError_t launch_paged_append(const PagedProb& p, const PagedCachePtrs& c, const RopeRows& r, uint8_t* ws,
@@ -314,28 +242,16 @@ cudaError_t launch_paged_append(const PagedProb& p, const PagedCachePtrs& c, con
   a.n_qi = r.q_idx ? 4 * p.G : 0;
   a.items = a.n_q + 2 * a.n_k + a.n_qi + (r.k_idx ? 4 : 0);
   a.inv_items = 1.f / (float)a.items;
-  paged_append_kernel<<<(p.N + a.rows - 1) / a.rows, kThreads, 0, st>>>(a);
+  // Few rows: a block of its own checks them and writes the error word, so that nothing has to clear it first (a memset
+  // costs as much as the rest of a single row's launch); it would outlast the others from about this many rows on.
+  a.report = p.N <= 4096;
+  if (!a.report) {
+    const cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
+    if (e != cudaSuccess) return e;
+  }
+  paged_append_kernel<<<(p.N + a.rows - 1) / a.rows + a.report, kThreads, 0, st>>>(a);
   count_launches(1);
   return cudaGetLastError();
-}
-
-cudaError_t launch_paged_rows(const PagedProb& p, const PagedCachePtrs& c, uint8_t* ws, const PagedWs& L,
-                              cudaStream_t st) {
-  RowsArgs a;
-  a.row_start = c.row_start;
-  a.seq_len = c.seq_len;
-  a.rows = reinterpret_cast<int4*>(ws + L.rows);
-  a.lead = reinterpret_cast<int4*>(ws + L.lead);
-  a.arrived = reinterpret_cast<int*>(ws + L.arrived);
-  a.header = reinterpret_cast<int*>(ws);
-  a.S = p.S;
-  a.N = p.N;
-  a.n_arrived = L.splits > 1 ? p.N * p.G * 3 : 0;  // (few rows: others are not cut)
-  a.max_blocks = p.max_blocks;
-  a.prefix = p.prefix;
-  a.tile_rows = L.tile_rows;
-  count_launches(1);
-  return launch_dependent(paged_rows_kernel, 1, p.N <= 256 ? 256 : kRowThreads, 0, st, a);
 }
 
 }  // namespace msa

@@ -21,9 +21,7 @@
 // its end cleared, so that nothing stored behind a row's end (another row's
 // tokens, stale cache lines, NaN or infinities) reaches it through 0 * x.
 #include "mma_sync.cuh"
-#include "paged.h"
-#include "pdl.cuh"
-#include "sm100.cuh"
+#include "paged_rows.cuh"
 
 namespace msa {
 namespace {
@@ -56,6 +54,8 @@ struct AttnArgs {
   float* LSE;
   int N, Hq, G, hg, hg_log2, k, num_pages, max_blocks, prefix, splits, per_split, tile_rows, items, slot0, join;
   float scale_log2;
+  const int* flags;                       // [n_flags] of the first kernel's blocks
+  int n_flags;
   int* err;
 };
 
@@ -333,6 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp > kWarps) {
     // ---------------------------------------------------------------- joining warps
+    if (blockIdx.x == 0 && warp == kWarps + 1) report_flags(a.flags, a.n_flags, a.err, lane);
     for (int n_join = 0;; ++n_join) {
       const int js = n_join & 1;
       if (!mbar_wait(&sh.j_full[js], (n_join >> 1) & 1, a.err, 1431, kIdleLimitNs)) break;
@@ -750,6 +751,8 @@ cudaError_t launch_paged_attn(const PagedProb& p, const PagedCachePtrs& c, const
   a.O = static_cast<__nv_bfloat16*>(O);
   a.LSE = LSE;
   a.scale_log2 = p.scale * kLog2e;
+  a.flags = reinterpret_cast<const int*>(ws + L.flags);
+  a.n_flags = L.n_flags;
   a.err = reinterpret_cast<int*>(ws);
   return L.tile_rows * p.hg > 8 ? launch_attn<2>(a, mk, mv, st) : launch_attn<1>(a, mk, mv, st);
 }

@@ -17,9 +17,7 @@
 // bounds (measured: one large product among 63 small ones loses 2^-19.3 of it,
 // normally distributed values 2^-24.5).
 #include "mma_sync.cuh"
-#include "paged.h"
-#include "pdl.cuh"
-#include "sm100.cuh"
+#include "paged_rows.cuh"
 
 namespace msa {
 namespace {
@@ -43,7 +41,8 @@ struct ScoreArgs {
   const int32_t *page_table, *row_start, *seq_len;
   float *pooled, *amax;
   int S, N, G, num_pages, max_blocks, runs, items;
-  int* err;
+  int* flags;  // [blocks but the last] what a block found wrong
+  RowsArgs rows;
 };
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -56,29 +55,36 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 struct ScoreShared {
   uint64_t full[kScoreStages], empty[kScoreStages];
   int4 info[kScoreStages];  // sequence (-1: the end), block (its complement where the page may not be read), first row, columns
+  int flag;
 };
 
-// Starts when the kernel before it has passed its wait, so everything earlier is done; what it reads of that goes past
-// L1, and the end of that kernel (which clears the error word) is waited for at the end.
+// The last block lines up the rows for the kernels after this one.
 __global__ void __launch_bounds__(kScoreThreads, 1)
     paged_scores_kernel(ScoreArgs a, const __grid_constant__ CUtensorMap map_k) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  if (blockIdx.x == gridDim.x - 1) {
+    pdl_release();
+    pdl_wait();
+    line_up_rows(a.rows, *reinterpret_cast<RowsShared*>(smem), threadIdx.x, kScoreThreads, [] { __syncthreads(); });
+    return;
+  }
   __shared__ ScoreShared sh;
   uint8_t* s_q = smem + kScoreStages * kScorePage;  // [stage][8][128]
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int ctas = gridDim.x - 1;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kScoreStages; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
     }
+    sh.flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&map_k);
   }
   pdl_release();
   __syncthreads();
-  int failed = 0;
-  int* const err = &failed;  // (the error word itself may only be written at the end)
+  pdl_wait();
 
   if (warp == kScoreWarps) {
     // ---------------------------------------------------------------- producer
@@ -87,7 +93,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     struct Batch {
       int s, c, begin, end, len, page;
     } now, next;
-    const int step = gridDim.x;
+    const int step = ctas;
     auto fetch = [&](int first, Batch& f) {
       const int id = first + lane / kScoreRun * step;
       f.s = -1;
@@ -95,10 +101,10 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       if (lane >= kScoreRun * kScoreBatch || id >= a.items) return;
       f.s = id / a.runs;
       f.c = id % a.runs * kScoreRun + lane % kScoreRun;
-      f.begin = __ldcg(a.row_start + f.s);
-      f.end = __ldcg(a.row_start + f.s + 1);
-      f.len = __ldcg(a.seq_len + f.s);
-      if (f.c < a.max_blocks) f.page = __ldcg(a.page_table + (size_t)f.s * a.max_blocks + f.c);
+      f.begin = ld_in(a.row_start + f.s);
+      f.end = ld_in(a.row_start + f.s + 1);
+      f.len = ld_in(a.seq_len + f.s);
+      if (f.c < a.max_blocks) f.page = ld_in(a.page_table + (size_t)f.s * a.max_blocks + f.c);
     };
     int n = 0;  // pages handed over
     bool ok = true;
@@ -110,11 +116,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       const bool want = now.s >= 0 && now.begin >= 0 && rows > 0 && now.len > 0 && now.len <= a.max_blocks * 128 &&
                         now.c < (now.len - 1) / 128;
       const bool bad = want && (now.page < 0 || now.page >= a.num_pages);
-      if (bad) failed = kDevBadIndex * 65536 + 1301;
+      if (bad) dev_fail(&sh.flag, kDevBadIndex, 1301);
       const int page = bad ? 0 : now.page, cols = rows * a.G;
       for (unsigned m = __ballot_sync(0xffffffffu, want); m; m &= m - 1, ++n) {
         const int from = __ffs(m) - 1, st = n % kScoreStages;
-        if (!mbar_wait(&sh.empty[st], ((n / kScoreStages) & 1) ^ 1, nullptr, 0)) { ok = false; break; }
+        if (!mbar_wait(&sh.empty[st], ((n / kScoreStages) & 1) ^ 1, &sh.flag, 1302)) { ok = false; break; }
         if (lane == from) {
           sh.info[st] = make_int4(now.s, bad ? ~now.c : now.c, now.begin, cols);
           const int first = min(cols, 8);
@@ -128,22 +134,18 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     }
     for (int i = 0; i < kScoreWarps && ok; ++i, ++n) {  // the end, for every warp
       const int st = n % kScoreStages;
-      ok = mbar_wait(&sh.empty[st], ((n / kScoreStages) & 1) ^ 1, nullptr, 0);
+      ok = mbar_wait(&sh.empty[st], ((n / kScoreStages) & 1) ^ 1, &sh.flag, 1302);
       if (ok && lane == 0) {
         sh.info[st].x = -1;
         mbar_arrive(&sh.full[st]);
       }
     }
-    if (!ok) failed = kDevTimeout * 65536 + 1302;
   } else {
     // ---------------------------------------------------------------- one page per warp
     const int r = lane >> 2, q = lane & 3;
     for (int n = warp;; n += kScoreWarps) {
       const int st = n % kScoreStages;
-      if (!mbar_wait(&sh.full[st], (n / kScoreStages) & 1, nullptr, 0)) {
-        failed = kDevTimeout * 65536 + 1303;
-        break;
-      }
+      if (!mbar_wait(&sh.full[st], (n / kScoreStages) & 1, &sh.flag, 1303)) break;
       const int4 info = sh.info[st];
       if (info.x < 0) break;
       const bool bad = info.y < 0;
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
           for (int h = 0; h < 2; ++h) {
             const int at = ks * 8 + h * 4 + q;
             b[ks][h] = n0 + r >= cols ? 0u
-                       : n0           ? __ldcg(qp + (size_t)(n0 + r) * 32 + at)
+                       : n0           ? ld_in(qp + (size_t)(n0 + r) * 32 + at)
                                       : *reinterpret_cast<const uint32_t*>(s_q + st * kScoreQ + r * 128 + at * 4);
           }
         float best0 = -INFINITY, best1 = -INFINITY;
@@ -195,8 +197,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       if (lane == 0) a.amax[(size_t)info.x * a.max_blocks + c] = __uint_as_float(top << 16);
     }
   }
-  pdl_wait();
-  if (*err) dev_fail(a.err, *err / 65536, *err % 65536);
+  __syncthreads();
+  if (threadIdx.x == 0) a.flags[blockIdx.x] = sh.flag;
 }
 
 // ---------------------------------------------------------------------------
@@ -480,7 +482,23 @@ cudaError_t launch_select(const PagedProb& p, const SelectArgs& a, cudaStream_t 
   return launch_dependent(paged_select_kernel<kThreads>, p.N * p.G, kThreads, p.max_blocks * 12, st, a);
 }
 
+// The rows alone, where no index scores are wanted and no prefix is shared.
+constexpr int kRowThreads = 1024;  // 256 for up to as many rows: a smaller block starts sooner
+
+__global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(RowsArgs a) {
+  __shared__ RowsShared sh;
+  pdl_release();
+  pdl_wait();
+  line_up_rows(a, sh, threadIdx.x, blockDim.x, [] { __syncthreads(); });
+}
+
 }  // namespace
+
+cudaError_t launch_paged_rows(const PagedProb& p, const PagedCachePtrs& c, uint8_t* ws, const PagedWs& L,
+                              cudaStream_t st) {
+  count_launches(1);
+  return launch_dependent(paged_rows_kernel, 1, p.N <= 256 ? 256 : kRowThreads, 0, st, rows_args(p, c, ws, L));
+}
 
 cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, const void* q_idx, int32_t* block_idx,
                                uint8_t* ws, const PagedWs& L, cudaStream_t st) {
@@ -496,8 +514,9 @@ cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, cons
   a.G = p.G;
   a.num_pages = p.num_pages;
   a.max_blocks = p.max_blocks;
-  a.err = reinterpret_cast<int*>(ws);
-  if (p.max_blocks > 1 && p.k > 1) {
+  a.flags = reinterpret_cast<int*>(ws + L.flags);
+  a.rows = rows_args(p, c, ws, L);
+  if (L.n_flags > 0) {
     CUtensorMap mk;
     const uint64_t dims[2] = {64, (uint64_t)p.num_pages * 128};
     const uint64_t strides[1] = {128};
@@ -514,7 +533,10 @@ cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, cons
       attr[dslot] = true;
     }
     count_launches(1);
-    e = launch_dependent(paged_scores_kernel, std::min(a.items, num_sms()), kScoreThreads, kScoreSmem, st, a, mk);
+    e = launch_dependent(paged_scores_kernel, L.n_flags + 1, kScoreThreads, kScoreSmem, st, a, mk);
+    if (e != cudaSuccess) return e;
+  } else {
+    const cudaError_t e = launch_paged_rows(p, c, ws, L, st);
     if (e != cudaSuccess) return e;
   }
   SelectArgs b;

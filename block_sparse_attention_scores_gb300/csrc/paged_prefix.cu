@@ -25,16 +25,14 @@
 // length; a run is walked by `pairs` CTAs at once, one per pair of tiles, so
 // that a page is read from HBM once and from L2 by the others. A run leaves
 // one partial O (fp32, normalised) and log-sum-exp per row and group.
-#include "paged.h"
-#include "pdl.cuh"
-#include "sm100.cuh"
+#include "paged_rows.cuh"
 
 namespace msa {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kHeadroom = 8.f;  // P = exp2(s - m) stays <= 2^kHeadroom
-constexpr int kThreads = 640;     // warp 0 TMA, warp 1 UMMA + TMEM; warps 4-11 and 12-19 softmax of tiles 0 and 1
+constexpr int kThreads = 640;     // warp 0 TMA, warp 1 UMMA + TMEM; 2, 3 the rows; warps 4-11 and 12-19 softmax of tiles 0 and 1
 constexpr int kTile = 32768;      // 128 rows x 128 bf16, two 64-column SW128 chunks
 constexpr int kChunk = 16384;
 constexpr int kStages = 2;        // K/V ring
@@ -42,15 +40,16 @@ constexpr int oQ = 0, oK = 2 * kTile, oV = oK + kStages * kTile;
 constexpr int kSmem = oV + kStages * kTile + 1024;
 
 struct PrefixArgs {
-  const int4* rows;
+  RowsArgs lineup;
+  int* flags;  // [blocks] what a block found wrong (the error word is cleared meanwhile; the merge reports it)
   const int32_t *page_table, *row_start;
   float *part_o, *part_lse;
   int S, N, Hq, G, hg, prefix, pairs, teams, num_pages, max_blocks;
   float scale_log2;
-  int* err;
 };
 
 struct PrefixShared {
+  int flag;
   uint64_t q_full, q_empty;
   uint64_t k0_full, kv_full[kStages];  // the first page's K; then a page's V with the next one's K
   uint64_t k_empty[kStages], v_empty[kStages];
@@ -97,6 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ PrefixShared sh;
+  __shared__ RowsShared sh_rows;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int team = blockIdx.x / a.pairs, pair = blockIdx.x % a.pairs;
   const int units = a.G * a.prefix;
@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, 1);
     for (int i = 0; i < 16; ++i) sh.raised[i >> 3][(i >> 2) & 1][i & 3] = 0;
+    sh.flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -131,9 +132,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   pdl_wait();
-  // the first sequence with rows: its table holds the shared pages (-1: no rows at all, -2: the first one was refused)
-  const int ref = ld_in(&a.rows[0].x);
-  if (ref < 0) u_begin = u_end;  // nothing to do
+  // the first sequence with rows: its table holds the shared pages
+  const int ref = find_sequence(a.row_start, a.S, 0, lane);
+  int* const err = &sh.flag;
+  if (ref >= a.S) u_begin = u_end;  // no rows at all
   const uint32_t tmem = sh.tmem_base;  // S_0 [0,128), S_1 [128,256), O_0 [256,384), O_1 [384,512)
 
   if (warp == 0) {
@@ -149,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int g = u / a.prefix;
       int page = ld_in(a.page_table + (size_t)ref * a.max_blocks + (u - g * a.prefix));
       if (page < 0 || page >= a.num_pages) {
-        dev_fail(a.err, kDevBadIndex, 1511);
+        dev_fail(err, kDevBadIndex, 1511);
         page = 0;
       }
       return (page * a.G + g) * 128;
@@ -178,8 +180,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int y = __shfl_sync(0xffffffffu, cur, i & 31);
       const int y1 = (i & 31) == 31 ? __shfl_sync(0xffffffffu, ahead, 0) : __shfl_sync(0xffffffffu, cur, (i & 31) + 1);
       const bool more = i + 1 < n;
-      if (!mbar_wait(&sh.v_empty[st], ((i / kStages) & 1) ^ 1, a.err, 1504)) break;
-      if (more && !mbar_wait(&sh.k_empty[st1], (((i + 1) / kStages) & 1) ^ 1, a.err, 1503)) break;
+      if (!mbar_wait(&sh.v_empty[st], ((i / kStages) & 1) ^ 1, err, 1504)) break;
+      if (more && !mbar_wait(&sh.k_empty[st1], (((i + 1) / kStages) & 1) ^ 1, err, 1503)) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(&sh.kv_full[st], more ? 2 * kTile : kTile);
         load_tile(oV + st * kTile, &map_v, &sh.kv_full[st], y);
@@ -188,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       const int g1 = (u_begin + i + 1) / a.prefix;
       if (more && g1 != (u_begin + i) / a.prefix) {  // the next page is another group's: its queries
-        if (!mbar_wait(&sh.q_empty, seg & 1, a.err, 1502)) break;
+        if (!mbar_wait(&sh.q_empty, seg & 1, err, 1502)) break;
         ++seg;
         if (lane == 0) load_q(g1);
         __syncwarp();
@@ -227,11 +229,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int seg = 0;
       for (int u = u_begin; u < u_end && ok; ++seg) {
         const int g = u / a.prefix, stop = min(u_end, (g + 1) * a.prefix), pages = stop - u;
-        if (!mbar_wait(&sh.q_full, seg & 1, a.err, 1520)) { ok = false; break; }
+        if (!mbar_wait(&sh.q_full, seg & 1, err, 1520)) { ok = false; break; }
         {
           const int st = kc % kStages;
           // (a later run's first K came with the V of the page before it)
-          if (kc == 0 && !mbar_wait(&sh.k0_full, 0, a.err, 1513)) { ok = false; break; }
+          if (kc == 0 && !mbar_wait(&sh.k0_full, 0, err, 1513)) { ok = false; break; }
           tc_fence_after();
           issue_s(0, st);
           issue_s(1, st);
@@ -245,10 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             // the page's V and the next one's K first: nothing then stands between P_t and its products
-            if (c == 0 && !mbar_wait(&sh.o_free[t], (seg & 1) ^ 1, a.err, 1516 + t)) { ok = false; break; }
-            if (t == 0 && !mbar_wait(&sh.kv_full[st], par, a.err, 1518)) { ok = false; break; }
+            if (c == 0 && !mbar_wait(&sh.o_free[t], (seg & 1) ^ 1, err, 1516 + t)) { ok = false; break; }
+            if (t == 0 && !mbar_wait(&sh.kv_full[st], par, err, 1518)) { ok = false; break; }
             // P_t of this page written (and O_t rescaled if its row maximum moved)
-            if (!mbar_wait(&sh.p_full[t], kc & 1, a.err, 1514 + t)) { ok = false; break; }
+            if (!mbar_wait(&sh.p_full[t], kc & 1, err, 1514 + t)) { ok = false; break; }
             tc_fence_after();
             issue_o(t, st, c > 0);
             if (t == 1) umma_commit(&sh.v_empty[st]);
@@ -267,7 +269,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         u = stop;
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp < 4) {
+    // ---------------------------------------------------------------- rows, for the kernels after this one
+    if (blockIdx.x == 0)
+      line_up_rows(a.lineup, sh_rows, threadIdx.x - 64, 64, [] { asm volatile("bar.sync 1, 64;" ::: "memory"); });
+  } else {
     // ---------------------------------------------------------------- softmax (thread = one head of one new row, 64 keys)
     const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;
     const int quarter = warp & 3;
@@ -280,13 +286,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // while the first pages are on their way: is the prefix the same one for every sequence with rows?
       bool bad = false;
       const long long cells = (long long)a.S * a.prefix;
-      for (long long i = (long long)blockIdx.x * 512 + threadIdx.x - 128; ref >= 0 && i < cells; i += (long long)gridDim.x * 512) {
+      for (long long i = (long long)blockIdx.x * 512 + threadIdx.x - 128; ref < a.S && i < cells; i += (long long)gridDim.x * 512) {
         const int s = (int)(i / a.prefix), c = (int)(i % a.prefix);
         const int32_t* table = a.page_table + c;
         if (ld_in(a.row_start + s + 1) > ld_in(a.row_start + s))
           bad |= ld_in(table + (size_t)s * a.max_blocks) != ld_in(table + (size_t)ref * a.max_blocks);
       }
-      if (bad) dev_fail(a.err, kDevBadIndex, 1512);
+      if (bad) dev_fail(err, kDevBadIndex, 1512);
     }
     uint32_t kc = 0, pair_ph = 0;
     bool ok = true;
@@ -294,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = u_begin; u < u_end && ok; ++seg) {
       const int g = u / a.prefix, stop = min(u_end, (g + 1) * a.prefix), pages = stop - u;
       float m_run = -INFINITY, l_run = 0.f;  // the maximum is the row's, the sum that of this warp's keys
-      if (!mbar_wait(&sh.s_full[t], kc & 1, a.err, 1522 + t)) { ok = false; break; }
+      if (!mbar_wait(&sh.s_full[t], kc & 1, err, 1522 + t)) { ok = false; break; }
       for (int c = 0; c < pages && ok; ++c, ++kc) {
         tc_fence_after();
         float sv[64], mq[2];
@@ -350,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const unsigned long long at = global_ns();
               if (!since) since = at;
               if (__any_sync(0xffffffffu, at - since > kWaitLimitNs)) {
-                dev_fail(a.err, kDevTimeout, 1524 + t);
+                dev_fail(err, kDevTimeout, 1524 + t);
                 ok = false;
                 break;
               }
@@ -359,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
         }
         if (redo) {
-          if (!warps_sync(&sh.pair[t][quarter], pair_ph, a.err, 1526 + t)) { ok = false; break; }
+          if (!warps_sync(&sh.pair[t][quarter], pair_ph, err, 1526 + t)) { ok = false; break; }
           const float m_new = fmaxf(m_blk, sh.row_max[t][half ^ 1][lrow]);
           const bool need = m_new > m_run + kHeadroom;
           const float alpha = need ? fast_exp2(m_run - m_new) : 1.f;
@@ -382,22 +388,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_st();
           tc_fence_before();
           // both warps are through before the one that called (or both) hands P on
-          if (!warps_sync(&sh.pair[t][quarter], pair_ph, a.err, 1528 + t)) { ok = false; break; }
+          if (!warps_sync(&sh.pair[t][quarter], pair_ph, err, 1528 + t)) { ok = false; break; }
           if (mine) {
             tc_fence_after();
             tc_fence_before();
             if (lane == 0) mbar_arrive(&sh.p_full[t]);
           }
-          if (!mbar_wait(next, next_ph, a.err, 1530 + t)) { ok = false; break; }
+          if (!mbar_wait(next, next_ph, err, 1530 + t)) { ok = false; break; }
         }
         l_run += l_add;
       }
       if (!ok) break;
       // ---- the run's end in this group: the row's partial
       sh.row_max[t][half][lrow] = l_run;
-      if (!warps_sync(&sh.pair[t][quarter], pair_ph, a.err, 1532 + t)) { ok = false; break; }
+      if (!warps_sync(&sh.pair[t][quarter], pair_ph, err, 1532 + t)) { ok = false; break; }
       const float l = half ? sh.row_max[t][0][lrow] + l_run : l_run + sh.row_max[t][1][lrow];
-      if (!warps_sync(&sh.pair[t][quarter], pair_ph, a.err, 1534 + t)) { ok = false; break; }
+      if (!warps_sync(&sh.pair[t][quarter], pair_ph, err, 1534 + t)) { ok = false; break; }
       tc_fence_after();
       const int slot = team - team_of(g * a.prefix, units, a.teams);
       const size_t at = ((size_t)slot * a.N + row) * a.Hq + g * a.hg + lrow % a.hg;
@@ -425,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0) a.flags[blockIdx.x] = sh.flag;
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
@@ -443,7 +450,8 @@ cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, con
   }
   if (!encode_pool_map(&mk, p, c.K) || !encode_pool_map(&mv, p, c.V)) return cudaErrorInvalidValue;
   PrefixArgs a;
-  a.rows = reinterpret_cast<const int4*>(ws + L.rows);
+  a.lineup = rows_args(p, c, ws, L);
+  a.flags = reinterpret_cast<int*>(ws + L.flags);
   a.page_table = c.page_table;
   a.row_start = c.row_start;
   a.S = p.S;
@@ -459,7 +467,6 @@ cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, con
   a.num_pages = p.num_pages;
   a.max_blocks = p.max_blocks;
   a.scale_log2 = p.scale * kLog2e;
-  a.err = reinterpret_cast<int*>(ws);
   static bool attr[kMaxDevices] = {};
   const int dslot = device_slot();
   if (!attr[dslot]) {
