@@ -13,6 +13,8 @@ constexpr int kCutSms = 152;
 // Words of a workspace's header behind the error word.
 constexpr int kLeadCount = 16;  // rows in PagedWs::lead
 constexpr int kWorkNext = 17;   // items that attention CTAs have taken beyond their first ones
+constexpr int kRunCount = 18;   // entries of PagedWs::runs
+constexpr int kRunNext = 19;    // runs that have been taken beyond the CTAs' first ones
 
 struct PagedProb {
   int S, N, Hq, G, hg, k;
@@ -24,14 +26,15 @@ struct PagedProb {
 struct PagedWs {
   size_t rows = 0;      // int4 [N]  per new row: sequence (-1: none, -2: refused), position, rows of its sequence before
                         //           it, and from it on
-  size_t lead = 0;      // int4 [N]  the rows that lead a tile: sequence, position, row, rows of the tile
+  size_t lead = 0;      // int4 [N]  the rows that lead a tile of the mma.sync path: sequence, position, row, rows of the tile
+  size_t runs = 0;      // int4 [N]  the rows that lead a pair of 128-row tiles: sequence, position, row, rows of the pair
   size_t flags = 0;     // int32 [n_flags] what the blocks of the index scores or of the shared prefix found wrong
   int n_flags = 0;      // those blocks
   size_t arrived = 0;   // int32 [N, G, 3] parts of a (row tile, group) that are done, as each joining warp counts them
   size_t pooled = 0;    // fp32 [N, G, max_blocks] block maxima of the index scores
   size_t amax = 0;      // fp32 [S, max_blocks]    largest |index key| value of a block
-  size_t part_o = 0;    // fp32 [pslots + splits, N, Hq, d] partial outputs (normalised)
-  size_t part_lse = 0;  // fp32 [pslots + splits, N, Hq]    their log2-sum-exp2
+  size_t part_o = 0;    // fp32 [pslots + rslots or splits, N, Hq, d] partial outputs (normalised)
+  size_t part_lse = 0;  // fp32 [pslots + rslots or splits, N, Hq]    their log2-sum-exp2
   size_t total = 256;
   int splits = 1;       // partials a row's own pages are cut into ...
   int per_split = 1;    // ... of this many pages
@@ -39,6 +42,10 @@ struct PagedWs {
   int pairs = 0;        // shared prefix: pairs of 128-row query tiles
   int teams = 0;        // shared prefix: runs of pages, each walked by `pairs` CTAs
   int pslots = 0;       // shared prefix: partials per row
+  int run_rows = 0;     // new rows of one sequence in a pair of 128-row tiles of the tcgen05 path, which takes a sequence's
+                        // own pages where this is not 0
+  int per_run = 1;      // pages of such a pair's runs ...
+  int rslots = 0;       // ... and how many runs at most: partials per row
 };
 
 PagedWs paged_ws_layout(const PagedProb& p, int which);

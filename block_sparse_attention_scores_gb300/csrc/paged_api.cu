@@ -9,10 +9,11 @@ namespace msa {
 static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Cuts `pages` pages of each of `tiles` row tiles into runs of equal length.
-// An item costs about a page more than its pages (its queries, the warps'
-// meeting, its part of O); SMs take items as they come, so the end is half an
+// An item costs `extra` pages more than its pages (its queries, the warps'
+// meeting, its part of O: about one page's time in the mma.sync path, three in
+// the tcgen05 one); SMs take items as they come, so the end is half an
 // item long.
-static void cut_pages(long long tiles, int pages, PagedWs* L) {
+static void cut_pages(long long tiles, int pages, double extra, int* per_split, int* n_splits) {
   tiles = std::max(1LL, tiles);
   pages = std::max(1, pages);
   double best = 0;
@@ -21,11 +22,11 @@ static void cut_pages(long long tiles, int pages, PagedWs* L) {
     const long long want = i < 0 ? 1 - i : i == 0 ? 1 : std::max(1LL, i * (long long)kCutSms / tiles);
     const int per = (int)((pages + std::min<long long>(want, pages) - 1) / std::min<long long>(want, pages));
     const int splits = (pages + per - 1) / per;
-    const double cost = (std::max(1.0, (double)tiles * splits / kCutSms) + 0.5) * (per + 1);
+    const double cost = (std::max(1.0, (double)tiles * splits / kCutSms) + 0.5) * (per + extra);
     if (best == 0 || cost < best) {
       best = cost;
-      L->per_split = per;
-      L->splits = splits;
+      *per_split = per;
+      *n_splits = splits;
     }
   }
 }
@@ -50,25 +51,36 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
     L.amax = take((size_t)p.S * p.max_blocks * 4);
     if (p.k > 1) L.n_flags = (int)std::min<long long>((long long)p.S * ((p.max_blocks + 4) / 6), kCutSms - 1);
     L.flags = take(kCutSms * 4);
-    cut_pages((long long)p.N * p.G, std::min(p.k, p.max_blocks), &L);
+    cut_pages((long long)p.N * p.G, std::min(p.k, p.max_blocks), 1, &L.per_split, &L.splits);
   } else {
-    // more columns (rows x heads of a sequence) than eight on average: two column tiles share each page
-    const int cols = (long long)p.N * p.hg > 8LL * p.S ? 16 : 8;
-    L.tile_rows = cols / p.hg;
-    cut_pages((long long)std::max(p.N / L.tile_rows, std::min(p.S, p.N)) * p.G, p.max_blocks - p.prefix, &L);
+    L.tile_rows = 8 / p.hg;
+    // More columns (rows x heads of a sequence) than eight on average, and more than a page each: 128-row tiles, tcgen05.
+    // Against eight columns at a time: 32 sequences of 2 rows x 64 heads over 2000 tokens 63 -> 62 us, of 8 rows 135 -> 71,
+    // 300 rows x 32 heads over 8000 274 -> 64; the other way for one page (8 rows x 64 heads over 100 tokens 17 -> 10).
+    if ((long long)p.N * p.hg > 8LL * p.S && p.max_blocks - p.prefix > 1) {
+      L.run_rows = 256 / p.hg;
+      L.runs = take((size_t)p.N * 16);
+      cut_pages((long long)std::max(p.N / L.run_rows, std::min(p.S, p.N)) * p.G, p.max_blocks - p.prefix, 3, &L.per_run,
+                &L.rslots);
+      L.splits = 0;
+      L.n_flags = kCutSms;
+    } else {
+      cut_pages((long long)std::max(p.N / L.tile_rows, std::min(p.S, p.N)) * p.G, p.max_blocks - p.prefix, 1, &L.per_split,
+                &L.splits);
+    }
     if (p.prefix > 0) {
       const int tiles = (int)(((long long)p.N * p.hg + 127) / 128);
       L.pairs = (tiles + 1) / 2;
       const int units = p.G * p.prefix;
       L.teams = std::min(units, std::max(1, kCutSms / L.pairs));
-      L.n_flags = L.teams * L.pairs;
-      L.flags = take((size_t)L.n_flags * 4);
+      L.n_flags = std::max(L.n_flags, L.teams * L.pairs);
       for (int g = 0; g < p.G; ++g)
         L.pslots = std::max(L.pslots, team_of((g + 1) * p.prefix - 1, units, L.teams) -
                                           team_of(g * p.prefix, units, L.teams) + 1);
     }
+    L.flags = take((size_t)L.n_flags * 4);
   }
-  const size_t rows = (size_t)(L.pslots + L.splits) * p.N * p.Hq;
+  const size_t rows = (size_t)(L.pslots + L.rslots + L.splits) * p.N * p.Hq;
   L.part_o = take(rows * 128 * 4);
   L.part_lse = take(rows * 4);
   L.total = off;
@@ -263,12 +275,14 @@ msa_status msa_paged_dense_attn(const msa_paged_shape* shape, const msa_paged_ca
   if ((s = check_device()) != MSA_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  if ((s = cuda_status(p.prefix ? launch_paged_prefix(p, c, Q, w, L, st) : launch_paged_rows(p, c, w, L, st),
-                       "paged prefix launch")) != MSA_OK)
+  const bool parts = p.prefix || L.run_rows;
+  if ((!p.prefix || L.run_rows) && (s = cuda_status(launch_paged_rows(p, c, w, L, st), "paged rows launch")) != MSA_OK)
     return s;
-  if ((s = cuda_status(launch_paged_attn(p, c, Q, nullptr, O, LSE, w, L, st), "paged attention launch")) != MSA_OK)
+  if (parts && (s = cuda_status(launch_paged_prefix(p, c, Q, w, L, st), "paged prefix launch")) != MSA_OK) return s;
+  if (!L.run_rows &&
+      (s = cuda_status(launch_paged_attn(p, c, Q, nullptr, O, LSE, w, L, st), "paged attention launch")) != MSA_OK)
     return s;
-  return p.prefix ? cuda_status(launch_paged_merge(p, O, LSE, w, L, st), "paged merge launch") : MSA_OK;
+  return parts ? cuda_status(launch_paged_merge(p, O, LSE, w, L, st), "paged merge launch") : MSA_OK;
 }
 
 }  // extern "C"

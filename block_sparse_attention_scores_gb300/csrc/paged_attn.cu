@@ -2,7 +2,7 @@
 // (row, group), or a sequence's own pages behind a shared prefix.
 //
 // Few query columns against streamed keys: 64 KB of K and V per page and group
-// serve at most 8 (or 16) columns, so the time is the memory's. One persistent
+// serve at most 8 columns, so the time is the memory's. One persistent
 // CTA per SM: a producer warp keeps three whole pages in flight (192 KB, TMA
 // boxes of half a page each), eight warps take 16 keys of every page each:
 //   S^T = K q^T   (mma.sync, keys in rows, columns = rows of the sequence x heads of the group)
@@ -37,10 +37,8 @@ constexpr unsigned long long kIdleLimitNs = 20000000000ull;  // the joining warp
 
 constexpr int kQStride = 272;                      // bytes between the queries' rows in shared memory (no bank conflicts)
 
-template <int NT>
-constexpr int smem_bytes() {
-  return kStages * 2 * kTile + 2 * NT * 8 * kQStride + 1024;
-}
+constexpr int kCols = 8;                           // query columns of a tile
+constexpr int kSmem = kStages * 2 * kTile + 2 * kCols * kQStride + 1024;
 
 struct AttnArgs {
   const int4* rows;
@@ -73,14 +71,19 @@ struct AttnShared {
   AttnItem item[2];
   AttnItem join[2];           // for the joining warps; parts 0: the end
   int token0[kStages];        // first token of the stage's page
-  float m[kWarps][16], l[kWarps][16];  // maximum and sum of a warp's columns
-  float inv[16], lse[16];              // of all warps together: 1 / sum, and log2 of the sum
+  float m[kWarps][kCols], l[kWarps][kCols];  // maximum and sum of a warp's columns
+  float inv[kCols], lse[kCols];            // of all warps together: 1 / sum, and log2 of the sum
 };
 
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// The bf16 pairs of keys t, t + 1 (x) and t + 8, t + 9 (y) that lie before `end`.
+__device__ __forceinline__ uint2 keep_keys(int t, int end) {
+  return make_uint2((t < end ? 0xffffu : 0u) | (t + 1 < end ? 0xffff0000u : 0u),
+                    (t + 8 < end ? 0xffffu : 0u) | (t + 9 < end ? 0xffff0000u : 0u));
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -214,13 +217,12 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const AttnItem& it
   }
 }
 
-template <int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attn_kernel(AttnArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ AttnShared sh;
-  uint8_t* s_q = smem + kStages * 2 * kTile;  // [2][NT * 8][kQStride]
+  uint8_t* s_q = smem + kStages * 2 * kTile;  // [2][kCols][kQStride]
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane < rows * a.hg)  // one column each
-          bulk_load(s_q + (qs * NT * 8 + lane) * kQStride,
+          bulk_load(s_q + (qs * kCols + lane) * kQStride,
                     a.Q + ((size_t)(now.row + (lane >> a.hg_log2)) * a.Hq + now.g * a.hg + (lane & (a.hg - 1))) * 128, 256,
                     &sh.q_full[qs]);
         ++n_item;
@@ -363,154 +365,115 @@ __global__ void __launch_bounds__(kThreads, 1)
       const AttnItem item = sh.item[qs];
       if (item.pages < 0) break;
       const int cols = item.rows * a.hg;
-      // query fragments: column 8 nt + r, dims 16 ks + 2 q, + 1 and + 8, + 9
-      uint32_t qb[NT][8][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int col = 8 * nt + r;
-        const uint8_t* src = s_q + (qs * NT * 8 + col) * kQStride;
+      // query fragments: column r, dims 16 ks + 2 q, + 1 and + 8, + 9
+      uint32_t qb[8][2];
+      {
+        const uint8_t* src = s_q + (qs * kCols + r) * kQStride;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-          qb[nt][ks][0] = col < cols ? *reinterpret_cast<const uint32_t*>(src + ks * 32 + q * 4) : 0u;
-          qb[nt][ks][1] = col < cols ? *reinterpret_cast<const uint32_t*>(src + ks * 32 + 16 + q * 4) : 0u;
+          qb[ks][0] = r < cols ? *reinterpret_cast<const uint32_t*>(src + ks * 32 + q * 4) : 0u;
+          qb[ks][1] = r < cols ? *reinterpret_cast<const uint32_t*>(src + ks * 32 + 16 + q * 4) : 0u;
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_empty[qs]);
-      // first token that columns 8 nt + 2 q, + 1 do not see
-      int lim[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int z = 0; z < 2; ++z) lim[nt][z] = item.pos + 1 + ((8 * nt + 2 * q + z) >> a.hg_log2);
       const int lim_lo = item.pos + 1;
+      int lim[2];  // first token that columns 2 q, + 1 do not see
+#pragma unroll
+      for (int z = 0; z < 2; ++z) lim[z] = lim_lo + ((2 * q + z) >> a.hg_log2);
 
-      float m_run[NT][2], l_run[NT][2], o[NT][8][4];
+      float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f}, o[8][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          m_run[nt][z] = -INFINITY;
-          l_run[nt][z] = 0.f;
-        }
-#pragma unroll
-        for (int mt = 0; mt < 8; ++mt)
-#pragma unroll
-          for (int z = 0; z < 4; ++z) o[nt][mt][z] = 0.f;
-      }
+        for (int z = 0; z < 4; ++z) o[mt][z] = 0.f;
 
       for (int j = 0; j < item.pages; ++j) {
         if (!mbar_wait(&sh.k_full[st], st_ph, a.err, 1422)) { ok = false; break; }
         const int token0 = sh.token0[st] + warp * 16;  // of this warp's keys
         const uint32_t kaddr = smem_u32(smem + st * 2 * kTile), vaddr = kaddr + kTile;
-        float sc[NT][4], sd[NT][4];  // even and odd steps of the sum over d
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int z = 0; z < 4; ++z) sc[nt][z] = sd[nt][z] = 0.f;
+        float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};  // even and odd steps of the sum over d
         {
           const int key = warp * 16 + (lane & 15);
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks) {
             uint32_t f[4];
             ldmatrix_x4(f, kaddr + (ks >> 2) * kHalf + sw128_off(key, (ks & 3) * 2 + (lane >> 4)));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_16816(ks & 1 ? sd[nt] : sc[nt], f[0], f[1], f[2], f[3], qb[nt][ks][0], qb[nt][ks][1]);
+            mma_16816(ks & 1 ? sd : sc, f[0], f[1], f[2], f[3], qb[ks][0], qb[ks][1]);
           }
         }
         const bool masked = token0 + 16 > lim_lo;
-        float mx[NT][2];
+        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mx[nt][0] = mx[nt][1] = -INFINITY;
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            float v = (sc[nt][z] + sd[nt][z]) * a.scale_log2;
-            if (masked && token0 + r + (z >> 1) * 8 >= lim[nt][z & 1]) v = -INFINITY;
-            sc[nt][z] = v;
-            mx[nt][z & 1] = fmaxf(mx[nt][z & 1], v);
-          }
+        for (int z = 0; z < 4; ++z) {
+          float v = (sc[z] + sd[z]) * a.scale_log2;
+          if (masked && token0 + r + (z >> 1) * 8 >= lim[z & 1]) v = -INFINITY;
+          sc[z] = v;
+          mx[z & 1] = fmaxf(mx[z & 1], v);
         }
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int z = 0; z < 2; ++z) mx[nt][z] = fmaxf(mx[nt][z], __shfl_xor_sync(0xffffffffu, mx[nt][z], x));
+          for (int z = 0; z < 2; ++z) mx[z] = fmaxf(mx[z], __shfl_xor_sync(0xffffffffu, mx[z], x));
         bool moved = false;
-        float alpha[NT][2], base[NT][2];
+        float alpha[2], base[2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const float m_new = fmaxf(m_run[nt][z], mx[nt][z]);
-            moved |= m_new > m_run[nt][z];
-            base[nt][z] = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet: exp2(-inf - 0) = 0
-            alpha[nt][z] = fast_exp2(m_run[nt][z] - base[nt][z]);
-            m_run[nt][z] = m_new;
-          }
+        for (int z = 0; z < 2; ++z) {
+          const float m_new = fmaxf(m_run[z], mx[z]);
+          moved |= m_new > m_run[z];
+          base[z] = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet: exp2(-inf - 0) = 0
+          alpha[z] = fast_exp2(m_run[z] - base[z]);
+          m_run[z] = m_new;
+        }
         if (__any_sync(0xffffffffu, moved)) {
+          l_run[0] *= alpha[0];
+          l_run[1] *= alpha[1];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            l_run[nt][0] *= alpha[nt][0];
-            l_run[nt][1] *= alpha[nt][1];
+          for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
-            for (int mt = 0; mt < 8; ++mt)
-#pragma unroll
-              for (int z = 0; z < 4; ++z) o[nt][mt][z] *= alpha[nt][z & 1];
-          }
+            for (int z = 0; z < 4; ++z) o[mt][z] *= alpha[z & 1];
         }
         // P as hi + lo, turned so that a lane holds two neighbouring keys of one column
-        uint32_t ph[NT][2], pl[NT][2];
+        uint32_t ph[2], pl[2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const float p0 = fast_exp2(sc[nt][2 * y] - base[nt][0]);
-            const float p1 = fast_exp2(sc[nt][2 * y + 1] - base[nt][1]);
-            l_run[nt][0] += p0;
-            l_run[nt][1] += p1;
-            const uint32_t h = pack_bf16(p0, p1);
-            ph[nt][y] = movmatrix_trans(h);
-            pl[nt][y] = movmatrix_trans(pack_bf16(p0 - __uint_as_float(h << 16),
-                                                  p1 - __uint_as_float(h & 0xffff0000u)));
-          }
+        for (int y = 0; y < 2; ++y) {
+          const float p0 = fast_exp2(sc[2 * y] - base[0]);
+          const float p1 = fast_exp2(sc[2 * y + 1] - base[1]);
+          l_run[0] += p0;
+          l_run[1] += p1;
+          const uint32_t h = pack_bf16(p0, p1);
+          ph[y] = movmatrix_trans(h);
+          pl[y] = movmatrix_trans(pack_bf16(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u)));
+        }
         if (!mbar_wait(&sh.v_full[st], st_ph, a.err, 1423)) { ok = false; break; }
         const int key = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
-        if (!masked) {
+        if (!masked || item.rows == 1) {
+          const uint2 keep = keep_keys(token0 + 2 * q, masked ? lim_lo : 0x7fffffff);
 #pragma unroll
           for (int mt = 0; mt < 8; ++mt) {
             uint32_t f[4];
             ldmatrix_x4_trans(f, vaddr + (mt >> 2) * kHalf + sw128_off(key, (mt & 3) * 2 + ((lane >> 3) & 1)));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_16816(o[nt][mt], f[0], f[1], f[2], f[3], ph[nt][0], ph[nt][1]);
-              mma_16816(o[nt][mt], f[0], f[1], f[2], f[3], pl[nt][0], pl[nt][1]);
-            }
+            const uint32_t v[4] = {f[0] & keep.x, f[1] & keep.x, f[2] & keep.y, f[3] & keep.y};
+            mma_16816(o[mt], v[0], v[1], v[2], v[3], ph[0], ph[1]);
+            mma_16816(o[mt], v[0], v[1], v[2], v[3], pl[0], pl[1]);
           }
         } else {
-          // each row on its own: values behind its end cleared, and only its own columns kept
+          // each row of the tile on its own: values behind its end cleared, and only its own columns kept
 #pragma unroll 1
           for (int i = 0; i < item.rows; ++i) {
             const int end = lim_lo + i;
             if (token0 >= end) continue;
-            const int t0 = token0 + 2 * q;  // this lane's keys: t0, t0 + 1 (f0, f1) and t0 + 8, t0 + 9 (f2, f3)
-            const uint32_t keep0 = (t0 < end ? 0xffffu : 0u) | (t0 + 1 < end ? 0xffff0000u : 0u);
-            const uint32_t keep1 = (t0 + 8 < end ? 0xffffu : 0u) | (t0 + 9 < end ? 0xffff0000u : 0u);
+            const uint2 keep = keep_keys(token0 + 2 * q, end);
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
               uint32_t f[4];
               ldmatrix_x4_trans(f, vaddr + (mt >> 2) * kHalf + sw128_off(key, (mt & 3) * 2 + ((lane >> 3) & 1)));
+              float t[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_16816(t, f[0] & keep.x, f[1] & keep.x, f[2] & keep.y, f[3] & keep.y, ph[0], ph[1]);
+              mma_16816(t, f[0] & keep.x, f[1] & keep.x, f[2] & keep.y, f[3] & keep.y, pl[0], pl[1]);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                float t[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_16816(t, f[0] & keep0, f[1] & keep0, f[2] & keep1, f[3] & keep1, ph[nt][0], ph[nt][1]);
-                mma_16816(t, f[0] & keep0, f[1] & keep0, f[2] & keep1, f[3] & keep1, pl[nt][0], pl[nt][1]);
-#pragma unroll
-                for (int z = 0; z < 4; ++z)
-                  if (lim[nt][z & 1] == end) o[nt][mt][z] += t[z];
-              }
+              for (int z = 0; z < 4; ++z)
+                if (lim[z & 1] == end) o[mt][z] += t[z];
             }
           }
         }
@@ -543,59 +506,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int col = threadIdx.x >> 7; col < cols; col += 2) put(col, 0.f, -INFINITY);
       } else {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int z = 0; z < 2; ++z) {
+          float l = l_run[z];
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            float l = l_run[nt][z];
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-            if (r == 0) {
-              sh.m[warp][8 * nt + 2 * q + z] = m_run[nt][z];
-              sh.l[warp][8 * nt + 2 * q + z] = l;
-            }
+          for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+          if (r == 0) {
+            sh.m[warp][2 * q + z] = m_run[z];
+            sh.l[warp][2 * q + z] = l;
           }
+        }
         if (!warps_sync(&sh.meet, meet_ph, a.err, 1425)) { ok = false; break; }
         float* s_o = reinterpret_cast<float*>(smem + st * 2 * kTile);
-        float* mine = s_o + warp * NT * 8 * 128;
+        float* mine = s_o + warp * kCols * 128;
+        float f[2];  // what this warp's O counts for (0 where no warp saw a key)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float f[2];  // what this warp's O counts for (0 where no warp saw a key)
+        for (int z = 0; z < 2; ++z) {
+          float mm = -INFINITY;
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            float mm = -INFINITY;
+          for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sh.m[w][2 * q + z]);
+          f[z] = fast_exp2(m_run[z] - (mm == -INFINITY ? 0.f : mm));
+        }
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sh.m[w][8 * nt + 2 * q + z]);
-            f[z] = fast_exp2(m_run[nt][z] - (mm == -INFINITY ? 0.f : mm));
-          }
+        for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
-          for (int mt = 0; mt < 8; ++mt)
+          for (int z = 0; z < 4; ++z)
+            mine[(2 * q + (z & 1)) * 128 + ((mt * 16 + r + (z >> 1) * 8) ^ (q << 3))] = o[mt][z] * f[z & 1];
+        {
+          // this warp's column's sum: lane w % 8 has warp w's
+          const float m = sh.m[lane & 7][warp];
+          float mm = m;
 #pragma unroll
-            for (int z = 0; z < 4; ++z)
-              mine[(8 * nt + 2 * q + (z & 1)) * 128 + ((mt * 16 + r + (z >> 1) * 8) ^ (q << 3))] = o[nt][mt][z] * f[z & 1];
-          {
-            // column 8 nt + warp's sum: lane w % 8 has warp w's
-            const int c = 8 * nt + warp;
-            const float m = sh.m[lane & 7][c];
-            float mm = m;
+          for (int x = 1; x < 8; x <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
+          float den = fast_exp2(m - (mm == -INFINITY ? 0.f : mm)) * sh.l[lane & 7][warp];
 #pragma unroll
-            for (int x = 1; x < 8; x <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
-            float den = fast_exp2(m - (mm == -INFINITY ? 0.f : mm)) * sh.l[lane & 7][c];
-#pragma unroll
-            for (int x = 1; x < 8; x <<= 1) den += __shfl_xor_sync(0xffffffffu, den, x);
-            if (lane == 0) {
-              sh.inv[c] = mm > -INFINITY ? __frcp_rn(den) : 0.f;
-              sh.lse[c] = mm > -INFINITY ? mm + log2f(den) : -INFINITY;
-            }
+          for (int x = 1; x < 8; x <<= 1) den += __shfl_xor_sync(0xffffffffu, den, x);
+          if (lane == 0) {
+            sh.inv[warp] = mm > -INFINITY ? __fdividef(1.f, den) : 0.f;
+            sh.lse[warp] = mm > -INFINITY ? mm + __log2f(den) : -INFINITY;
           }
         }
         if (!warps_sync(&sh.meet, meet_ph, a.err, 1426)) { ok = false; break; }
 #pragma unroll
-        for (int c = 0; c < 8 * NT; c += 2) {
+        for (int c = 0; c < kCols; c += 2) {
           const int col = c + (threadIdx.x >> 7);
           if (col >= cols) break;
           float val = 0.f;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) val += s_o[(w * NT * 8 + col) * 128 + (d ^ ((col & 6) << 2))];
+          for (int w = 0; w < kWarps; ++w) val += s_o[(w * kCols + col) * 128 + (d ^ ((col & 6) << 2))];
           put(col, val * sh.inv[col], sh.lse[col]);
         }
         fence_proxy_async_smem();  // the stage goes back to TMA
@@ -627,8 +584,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// Joins a row's parts behind a shared prefix: the own pages' splits and the
-// prefix's (one per run of pages that reaches into the group's), in that order.
+// Joins a row's parts: those of its sequence's own pages (the attention's splits,
+// or the runs of the tcgen05 path) and the shared prefix's (one per run of pages
+// that reaches into the group's), in that order.
 // One warp per row and head. Nothing but latency costs anything here (29 MB from
 // L2 at most among the measured cases), so eight parts are asked for at a time,
 // their sums with them, and the maximum is kept as they come.
@@ -638,6 +596,9 @@ struct MergeArgs {
   __nv_bfloat16* O;
   float* LSE;
   int N, Hq, G, hg, prefix, per_split, tile_rows, teams, pslots;
+  const int* flags;  // [n_flags] of the prefix kernel's blocks, where no attention kernel comes between
+  int n_flags;
+  int* err;
 };
 
 constexpr int kMergeThreads = 128;
@@ -649,11 +610,12 @@ __global__ void __launch_bounds__(kMergeThreads, 6) paged_merge_kernel(MergeArgs
   if (item >= (long long)a.N * a.Hq) return;
   const int row = (int)(item / a.Hq), g = (int)(item % a.Hq) / a.hg;
   const int units = a.G * a.prefix;
-  const int pre = team_of((g + 1) * a.prefix - 1, units, a.teams) - team_of(g * a.prefix, units, a.teams) + 1;
+  const int pre = units ? team_of((g + 1) * a.prefix - 1, units, a.teams) - team_of(g * a.prefix, units, a.teams) + 1 : 0;
   pdl_wait();
+  if (item == 0) report_flags(a.flags, a.n_flags, a.err, lane);
   const int4 info = ld_in(a.rows + row);
   if (info.x < 0) return;  // behind the last sequence, or left out
-  // the tile's last row decides how far its items went
+  // the last row of its tile (or pair of tiles) decides how far the items went
   const int lead = info.z % a.tile_rows, rows = min(a.tile_rows, info.w + lead);
   const int own = ((info.y - lead + rows - 1) / 128 - a.prefix) / a.per_split + 1, n = own + pre;
   const size_t step = (size_t)a.N * a.Hq;
@@ -696,18 +658,17 @@ __global__ void __launch_bounds__(kMergeThreads, 6) paged_merge_kernel(MergeArgs
   if (lane == 0) a.LSE[item] = (m + log2f(den)) * 0.6931471805599453f;
 }
 
-template <int NT>
 cudaError_t launch_attn(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
   static bool attr[kMaxDevices] = {};
   const int dslot = device_slot();
   if (!attr[dslot]) {
-    cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         smem_bytes<NT>());
+    cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSmem);
     if (e != cudaSuccess) return e;
     attr[dslot] = true;
   }
   count_launches(1);
-  return launch_dependent(paged_attn_kernel<NT>, std::min(a.items, num_sms()), kThreads, smem_bytes<NT>(), st, a, mk, mv);
+  return launch_dependent(paged_attn_kernel, std::min(a.items, num_sms()), kThreads, kSmem, st, a, mk, mv);
 }
 
 }  // namespace
@@ -754,7 +715,7 @@ cudaError_t launch_paged_attn(const PagedProb& p, const PagedCachePtrs& c, const
   a.flags = reinterpret_cast<const int*>(ws + L.flags);
   a.n_flags = L.n_flags;
   a.err = reinterpret_cast<int*>(ws);
-  return L.tile_rows * p.hg > 8 ? launch_attn<2>(a, mk, mv, st) : launch_attn<1>(a, mk, mv, st);
+  return launch_attn(a, mk, mv, st);
 }
 
 cudaError_t launch_paged_merge(const PagedProb& p, void* O, float* LSE, uint8_t* ws, const PagedWs& L,
@@ -774,6 +735,13 @@ cudaError_t launch_paged_merge(const PagedProb& p, void* O, float* LSE, uint8_t*
   a.tile_rows = L.tile_rows;
   a.teams = L.teams;
   a.pslots = L.pslots;
+  if (L.run_rows) {
+    a.per_split = L.per_run;
+    a.tile_rows = L.run_rows;
+  }
+  a.flags = reinterpret_cast<const int*>(ws + L.flags);
+  a.n_flags = L.run_rows ? L.n_flags : 0;
+  a.err = reinterpret_cast<int*>(ws);
   const long long items = (long long)p.N * p.Hq;
   count_launches(1);
   return launch_dependent(paged_merge_kernel, (unsigned)((items + 3) / 4), kMergeThreads, 0, st, a);

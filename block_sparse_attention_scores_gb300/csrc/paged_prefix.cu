@@ -1,5 +1,6 @@
-// Full attention of a batch's new rows over the pages that all its sequences
-// share: one pass over those pages for the whole batch.
+// Full attention by 128-row tiles: of a batch's new rows over the pages that all
+// its sequences share, in one pass over those pages for the whole batch, and of
+// the several new rows of a sequence over its own pages.
 //
 // The rows of every sequence times the heads of a group fill 128-row tiles
 // (128 / h_g rows each), so the shared part is a matrix product with as many
@@ -21,10 +22,30 @@
 // value 2^8 above it calls the other (which is then still waiting for the next
 // S), after which both raise the maximum, rescale O and compute P again.
 //
-// Work: all (group, page) pairs in a line, cut into `teams` runs of equal
-// length; a run is walked by `pairs` CTAs at once, one per pair of tiles, so
-// that a page is read from HBM once and from L2 by the others. A run leaves
-// one partial O (fp32, normalised) and log-sum-exp per row and group.
+// Work of the shared part: all (group, page) pairs in a line, cut into `teams`
+// runs of equal length; a run is walked by `pairs` CTAs at once, one per pair of
+// tiles, so that a page is read from HBM once and from L2 by the others. A run
+// leaves one partial O (fp32, normalised) and log-sum-exp per row and group.
+//
+// A sequence's own pages (kRuns): a run is up to 256 / h_g of its rows, a group
+// and some pages, taken as they come. Where its rows fill one tile only, the
+// second tile is the same rows of the next group against that group's pages: a
+// tile alone would leave the tensor core idle during its softmax and the memory
+// during both (32 sequences of 4 rows, 64 heads over 8 groups, 2000 tokens: 109
+// us against 92). What differs from the shared part:
+//   - P as the sum of two bf16 values, side by side over S (the second product
+//     costs little where the memory bounds: with one row or two the same result
+//     comes from the mma.sync path, which does that too);
+//   - masks, on the pages that not every row sees all of, and V cleaned there by
+//     a warp of its own before the tensor core may read it: a zero of P does not
+//     keep an infinity or a NaN of a later row's V from an earlier row;
+//   - K and V have a producer and barriers each, and the runs' descriptions go
+//     round in shared memory.
+//
+// Measured: the shared part of 128 sequences x 2 rows x 32 heads over 128K tokens
+// 354 us, 1550 TFLOP/s (0.8 of what a library product reaches); own pages of 32 x
+// 4 rows x 64 heads over 2000 tokens 59 us, 4.6 TB/s; 300 rows x 32 heads over
+// 8000 tokens 52 us, 740 TFLOP/s (P's second product not counted).
 #include "paged_rows.cuh"
 
 namespace msa {
@@ -32,24 +53,44 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kHeadroom = 8.f;  // P = exp2(s - m) stays <= 2^kHeadroom
-constexpr int kThreads = 640;     // warp 0 TMA, warp 1 UMMA + TMEM; 2, 3 the rows; warps 4-11 and 12-19 softmax of tiles 0 and 1
+// warp 0 TMA, warp 1 UMMA + TMEM, 2 and 3 the rows (or V), 4-11 and 12-19 softmax of tiles 0 and 1
+constexpr int kThreads = 640;
 constexpr int kTile = 32768;      // 128 rows x 128 bf16, two 64-column SW128 chunks
 constexpr int kChunk = 16384;
 constexpr int kStages = 2;        // K/V ring
 constexpr int oQ = 0, oK = 2 * kTile, oV = oK + kStages * kTile;
 constexpr int kSmem = oV + kStages * kTile + 1024;
 
+// One run: pages of one group against up to two tiles of rows.
+struct Run {
+  int row0, rows;   // the tiles' first row, and how many rows there are for them
+  int g, pages;     // (pages 0: the end)
+  int slot;         // of the rows' partials
+  int own;          // a sequence's own pages: P as the sum of two bf16, masks
+  int twin;         // the second tile is the same rows of group g + 1, against that group's pages
+  int seq, first;   // whose pages, from which block
+  int pos;          // own: position of the first row
+  int masked;       // the first page that not every row sees all of
+};
+
 struct PrefixArgs {
   RowsArgs lineup;
   int* flags;  // [blocks] what a block found wrong (the error word is cleared meanwhile; the merge reports it)
   const int32_t *page_table, *row_start;
   float *part_o, *part_lse;
+  const int4* runs;
+  const __nv_bfloat16* V;
+  int* header;
   int S, N, Hq, G, hg, prefix, pairs, teams, num_pages, max_blocks;
+  int run_rows, per_run, rslots, pslots;
   float scale_log2;
 };
 
 struct PrefixShared {
   int flag;
+  Run run[2];
+  int odd[2];  // a run's V has infinities or NaN among the rows' own tokens
+  uint64_t run_full[2], run_empty[2], k_full[kStages], v_clean[kStages];  // (kRuns)
   uint64_t q_full, q_empty;
   uint64_t k0_full, kv_full[kStages];  // the first page's K; then a page's V with the next one's K
   uint64_t k_empty[kStages], v_empty[kStages];
@@ -90,6 +131,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+template <bool kRuns>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_prefix_kernel(PrefixArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v) {
@@ -98,10 +140,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ PrefixShared sh;
   __shared__ RowsShared sh_rows;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int team = blockIdx.x / a.pairs, pair = blockIdx.x % a.pairs;
+  const int team = a.pairs ? blockIdx.x / a.pairs : 0, pair = a.pairs ? blockIdx.x % a.pairs : 0;
   const int units = a.G * a.prefix;
-  int u_begin = team_start(team, units, a.teams);
-  const int u_end = team_start(team + 1, units, a.teams);
+  int u_begin = 0, u_end = 0;
+  if (!kRuns || team < a.teams) {  // (with runs there may be more CTAs than the prefix has work for)
+    u_begin = team_start(team, units, a.teams);
+    u_end = team_start(team + 1, units, a.teams);
+  }
   const int tile_rows = 128 / a.hg;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -115,6 +160,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.kv_full[i], 1);
       mbar_init(&sh.k_empty[i], 1);
       mbar_init(&sh.v_empty[i], 1);
+    }
+    if (kRuns) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sh.run_full[i], 1);
+        mbar_init(&sh.run_empty[i], 19);
+        mbar_init(&sh.k_full[i], 1);
+        mbar_init(&sh.v_clean[i], 1);
+      }
     }
     mbar_init(&sh.k0_full, 1);
     mbar_init(&sh.q_full, 1);
@@ -138,66 +191,202 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (ref >= a.S) u_begin = u_end;  // no rows at all
   const uint32_t tmem = sh.tmem_base;  // S_0 [0,128), S_1 [128,256), O_0 [256,384), O_1 [384,512)
 
+  // The next run (false: the end, or a wait that ran out). Without kRuns everybody counts for himself.
+  int n_run = 0, u = u_begin;
+  auto next_run = [&](Run& run) {
+    if constexpr (kRuns) {
+      if (!mbar_wait(&sh.run_full[n_run & 1], (n_run >> 1) & 1, err, 1505)) return false;
+      run = sh.run[n_run & 1];
+      ++n_run;
+      return run.pages > 0;
+    } else {
+      if (u >= u_end) return false;
+      const int g = u / a.prefix, stop = min(u_end, (g + 1) * a.prefix);
+      run = {2 * pair * tile_rows, a.N, g, stop - u, team - team_of(g * a.prefix, units, a.teams)};
+      u = stop;
+      return true;
+    }
+  };
+
+  auto run_done = [&](bool solo) {  // solo: said by one thread of the warp
+    if constexpr (kRuns) {
+      if (!solo) __syncwarp();
+      if (solo || lane == 0) mbar_arrive(&sh.run_empty[(n_run - 1) & 1]);
+    }
+  };
+
+  // Row of the pools' tensor maps of the run's page i.
+  auto table_row = [&](const Run& run, int i) {
+    if (i >= run.pages) return 0;
+    int page = ld_in(a.page_table + (size_t)run.seq * a.max_blocks + run.first + i);
+    if (page < 0 || page >= a.num_pages) {
+      dev_fail(err, kDevBadIndex, 1511);
+      page = 0;
+    }
+    return (page * a.G + run.g) * 128;
+  };
+
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
     tma_prefetch_desc(&map_q);
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
-    const int n = u_end - u_begin;
-    // row of the pool's tensor map of the CTA's page i + lane
-    auto rows_of = [&](int i) {
-      const int u = u_begin + i + lane;
-      if (u >= u_end) return 0;
-      const int g = u / a.prefix;
-      int page = ld_in(a.page_table + (size_t)ref * a.max_blocks + (u - g * a.prefix));
-      if (page < 0 || page >= a.num_pages) {
-        dev_fail(err, kDevBadIndex, 1511);
-        page = 0;
-      }
-      return (page * a.G + g) * 128;
-    };
-    auto load_q = [&](int g) {
-      mbar_arrive_expect_tx(&sh.q_full, 2 * kTile);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int row0 = (2 * pair + t) * tile_rows;  // rows past N arrive as zeros
-        tma_load_3d(smem + oQ + t * kTile, &map_q, &sh.q_full, 0, g * a.hg, row0);
-        tma_load_3d(smem + oQ + t * kTile + kChunk, &map_q, &sh.q_full, 64, g * a.hg, row0);
-      }
-    };
     auto load_tile = [&](int at, const CUtensorMap* map, uint64_t* bar, int y) {
       tma_load_2d(smem + at, map, bar, 0, y);
       tma_load_2d(smem + at + kChunk, map, bar, 64, y);
     };
-    int cur = rows_of(0), ahead = rows_of(32), seg = 0;
-    if (n > 0 && lane == 0) {
-      load_q(u_begin / a.prefix);
-      mbar_arrive_expect_tx(&sh.k0_full, kTile);
-      load_tile(oK, &map_k, &sh.k0_full, cur);
-    }
-    for (int i = 0; i < n; ++i) {
-      const int st = i % kStages, st1 = (i + 1) % kStages;
-      const int y = __shfl_sync(0xffffffffu, cur, i & 31);
-      const int y1 = (i & 31) == 31 ? __shfl_sync(0xffffffffu, ahead, 0) : __shfl_sync(0xffffffffu, cur, (i & 31) + 1);
-      const bool more = i + 1 < n;
-      if (!mbar_wait(&sh.v_empty[st], ((i / kStages) & 1) ^ 1, err, 1504)) break;
-      if (more && !mbar_wait(&sh.k_empty[st1], (((i + 1) / kStages) & 1) ^ 1, err, 1503)) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&sh.kv_full[st], more ? 2 * kTile : kTile);
-        load_tile(oV + st * kTile, &map_v, &sh.kv_full[st], y);
-        if (more) load_tile(oK + st1 * kTile, &map_k, &sh.kv_full[st], y1);
-      }
-      __syncwarp();
-      const int g1 = (u_begin + i + 1) / a.prefix;
-      if (more && g1 != (u_begin + i) / a.prefix) {  // the next page is another group's: its queries
-        if (!mbar_wait(&sh.q_empty, seg & 1, err, 1502)) break;
-        ++seg;
-        if (lane == 0) load_q(g1);
+    auto load_kv = [&](int at, const CUtensorMap* map, uint64_t* bar, int y) {
+      mbar_arrive_expect_tx(bar, kTile);
+      load_tile(at, map, bar, y);
+    };
+    if constexpr (kRuns) {
+      // The prefix's runs first, as below, then the sequences' own ones as they come. A run's first 32 pages are looked
+      // up ahead, one step a page: the number, the rows, the pages.
+      struct Ahead {
+        Run run;
+        int y;  // of this lane's page
+      };
+      int u = u_begin, id = 0, taken = 0, own = -1;  // own: runs of its own that this CTA has asked for
+      const int pair_g = a.G % 2 ? 1 : 2;  // groups of an item: both tiles' at once, or one after the other
+      const int items = a.run_rows ? ld_in(a.header + kRunCount) * a.rslots * (a.G / pair_g) : 0;
+      bool second = false;  // the item's second group is still to come
+      bool own_now = false;
+      int4 lead = make_int4(0, 0, 0, 0);
+      auto step1 = [&]() {
+        own_now = second || u >= u_end;
+        if (!own_now || second) return;
+        if (++own > 0 && lane == 0) taken = atomicAdd(a.header + kRunNext, 1);
+      };
+      auto step2 = [&]() {
+        if (!own_now || second) return;
+        id = own ? gridDim.x + __shfl_sync(0xffffffffu, taken, 0) : blockIdx.x;
+        if (id < items) lead = ld_in(a.runs + id / (a.rslots * (a.G / pair_g)));
+      };
+      auto step3 = [&](Ahead& h) {
+        h.run.pages = 0;
+        if (!own_now) {
+          const int g = u / a.prefix, stop = min(u_end, (g + 1) * a.prefix);
+          const int row0 = 2 * pair * tile_rows;
+          h.run = {row0, min(a.N - row0, 2 * tile_rows), g, stop - u, team - team_of(g * a.prefix, units, a.teams), 0, 0, ref,
+                   u - g * a.prefix, 0, 1 << 30};
+          u = stop;
+        } else if (id < items) {
+          const int pairs_g = a.G / pair_g, part = id % (a.rslots * pairs_g), split = part / pairs_g;
+          const int twin = pair_g == 2 && lead.w <= tile_rows;
+          const int first = a.prefix + split * a.per_run, own_pages = (lead.y + lead.w - 1) / 128 + 1 - first;
+          h.run = {lead.z, lead.w, part % pairs_g * pair_g + second, max(0, min(a.per_run, own_pages)), a.pslots + split, 1,
+                   twin, lead.x, first, lead.y, max(0, (lead.y + 1) / 128 - first)};
+          second = pair_g == 2 && !twin && !second && h.run.pages;
+        }
+        h.y = table_row(h.run, lane);
+      };
+      Ahead now, next;
+      now.run.pages = next.run.pages = 0;
+      auto find = [&](Ahead& h, int step) {  // the next run with pages (or the end), or one step on the way there
+        if (step == 0) step1();
+        else if (step == 1) step2();
+        else if (step == 2) step3(h);
+      };
+      auto more = [&] { return u < u_end || second || id < items; };  // what step 3 of the last one leaves to be asked for
+      for (int s = 0; s < 3; ++s) find(now, s);
+      int n_run = 0;
+      uint32_t kc = 0;
+      bool ok = true;
+      while (ok) {
+        const bool end = now.run.pages == 0;
+        if (end && more()) {  // a run without pages: on to the next one
+          for (int s = 0; s < 3; ++s) find(now, s);
+          continue;
+        }
+        const int slot = n_run & 1;
+        if (!mbar_wait(&sh.run_empty[slot], ((n_run >> 1) & 1) ^ 1, err, 1501)) break;
+        if (lane == 0) {
+          sh.run[slot] = now.run;
+          mbar_arrive(&sh.run_full[slot]);
+        }
         __syncwarp();
+        if (end) break;
+        int y = now.y, step = 0;
+        const int tiles = now.run.twin || now.run.rows > tile_rows ? 2 : 1;
+        const int streams = now.run.twin ? 2 : 1;  // of pages
+        for (int i = 0; i < now.run.pages * streams; ++i, ++kc) {
+          const int page = now.run.twin ? i >> 1 : i, other = now.run.twin ? (i & 1) * 128 : 0;
+          if (page && !other && (page & 31) == 0) y = table_row(now.run, page + lane);
+          const int st = kc % kStages, at = __shfl_sync(0xffffffffu, y, page & 31) + other;
+          const uint32_t par = ((kc / kStages) & 1) ^ 1;
+          if (!mbar_wait(&sh.k_empty[st], par, err, 1503)) { ok = false; break; }
+          if (lane == 0) load_kv(oK + st * kTile, &map_k, &sh.k_full[st], at);
+          __syncwarp();
+          if (i == 0 && !mbar_wait(&sh.q_empty, (n_run & 1) ^ 1, err, 1502)) { ok = false; break; }
+          if (i == 0 && lane == 0) {  // (the first K may come while the run before still needs its queries)
+            mbar_arrive_expect_tx(&sh.q_full, tiles * kTile);
+            for (int t = 0; t < tiles; ++t) {
+              const int row0 = now.run.row0 + (now.run.twin ? 0 : t * tile_rows);  // rows past N arrive as zeros
+              const int head = (now.run.g + (now.run.twin ? t : 0)) * a.hg;
+              tma_load_3d(smem + oQ + t * kTile, &map_q, &sh.q_full, 0, head, row0);
+              tma_load_3d(smem + oQ + t * kTile + kChunk, &map_q, &sh.q_full, 64, head, row0);
+            }
+          }
+          __syncwarp();
+          if (step < 3) find(next, step++);
+        }
+        ++n_run;
+        for (; step < 3; ++step) find(next, step);
+        now = next;
       }
-      if ((i & 31) == 31) {
-        cur = ahead;
-        ahead = rows_of(i + 33);
+    } else {
+      const int n = u_end - u_begin;
+      // row of the pool's tensor map of the CTA's page i + lane
+      auto rows_of = [&](int i) {
+        const int u = u_begin + i + lane;
+        if (u >= u_end) return 0;
+        const int g = u / a.prefix;
+        int page = ld_in(a.page_table + (size_t)ref * a.max_blocks + (u - g * a.prefix));
+        if (page < 0 || page >= a.num_pages) {
+          dev_fail(err, kDevBadIndex, 1511);
+          page = 0;
+        }
+        return (page * a.G + g) * 128;
+      };
+      auto load_q = [&](int g) {
+        mbar_arrive_expect_tx(&sh.q_full, 2 * kTile);
+  #pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int row0 = (2 * pair + t) * tile_rows;  // rows past N arrive as zeros
+          tma_load_3d(smem + oQ + t * kTile, &map_q, &sh.q_full, 0, g * a.hg, row0);
+          tma_load_3d(smem + oQ + t * kTile + kChunk, &map_q, &sh.q_full, 64, g * a.hg, row0);
+        }
+      };
+      int cur = rows_of(0), ahead = rows_of(32), seg = 0;
+      if (n > 0 && lane == 0) {
+        load_q(u_begin / a.prefix);
+        mbar_arrive_expect_tx(&sh.k0_full, kTile);
+        load_tile(oK, &map_k, &sh.k0_full, cur);
+      }
+      for (int i = 0; i < n; ++i) {
+        const int st = i % kStages, st1 = (i + 1) % kStages;
+        const int y = __shfl_sync(0xffffffffu, cur, i & 31);
+        const int y1 = (i & 31) == 31 ? __shfl_sync(0xffffffffu, ahead, 0) : __shfl_sync(0xffffffffu, cur, (i & 31) + 1);
+        const bool more = i + 1 < n;
+        if (!mbar_wait(&sh.v_empty[st], ((i / kStages) & 1) ^ 1, err, 1504)) break;
+        if (more && !mbar_wait(&sh.k_empty[st1], (((i + 1) / kStages) & 1) ^ 1, err, 1503)) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sh.kv_full[st], more ? 2 * kTile : kTile);
+          load_tile(oV + st * kTile, &map_v, &sh.kv_full[st], y);
+          if (more) load_tile(oK + st1 * kTile, &map_k, &sh.kv_full[st], y1);
+        }
+        __syncwarp();
+        const int g1 = (u_begin + i + 1) / a.prefix;
+        if (more && g1 != (u_begin + i) / a.prefix) {  // the next page is another group's: its queries
+          if (!mbar_wait(&sh.q_empty, seg & 1, err, 1502)) break;
+          ++seg;
+          if (lane == 0) load_q(g1);
+          __syncwarp();
+        }
+        if ((i & 31) == 31) {
+          cur = ahead;
+          ahead = rows_of(i + 33);
+        }
       }
     }
   } else if (warp == 1) {
@@ -220,59 +409,137 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         umma_commit(&sh.s_full[t]);
       };
-      auto issue_o = [&](int t, int st, bool acc) {
+      auto issue_o = [&](int t, int st, bool acc, bool own) {
         const uint32_t va = v_lo + st * (kTile >> 4), d = tmem + 256 + t * 128, p = tmem + t * 128;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
           umma_bf16_ts_w(d, p + (ks >> 2) * 64 + (ks & 3) * 8, va + ks * (2048 >> 4), hi, id_o, ks > 0 ? 1u : (uint32_t)acc);
+        if (kRuns && own)
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            umma_bf16_ts_w(d, p + (ks >> 2) * 64 + 32 + (ks & 3) * 8, va + ks * (2048 >> 4), hi, id_o, 1u);
       };
-      int seg = 0;
-      for (int u = u_begin; u < u_end && ok; ++seg) {
-        const int g = u / a.prefix, stop = min(u_end, (g + 1) * a.prefix), pages = stop - u;
+      // pages and runs of each tile (the second one has none in a run of few rows)
+      uint32_t pages_of[2] = {0, 0}, runs_of[2] = {0, 0};
+      Run run;
+      for (int seg = 0; ok && next_run(run); ++seg) {
+        run_done(true);
+        const bool twin = kRuns && run.twin;
+        const int pages = run.pages, last_t = !kRuns || twin || run.rows > tile_rows, streams = twin ? 2 : 1;
         if (!mbar_wait(&sh.q_full, seg & 1, err, 1520)) { ok = false; break; }
-        {
-          const int st = kc % kStages;
-          // (a later run's first K came with the V of the page before it)
-          if (kc == 0 && !mbar_wait(&sh.k0_full, 0, err, 1513)) { ok = false; break; }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t > last_t) break;
+          const uint32_t kk = kc + (twin ? t : 0), st = kk % kStages;
+          if (kRuns) {
+            if ((t == 0 || twin) && !mbar_wait(&sh.k_full[st], (kk / kStages) & 1, err, 1513)) { ok = false; break; }
+          } else {
+            // (a later run's first K came with the V of the page before it)
+            if (kc == 0 && t == 0 && !mbar_wait(&sh.k0_full, 0, err, 1513)) { ok = false; break; }
+          }
           tc_fence_after();
-          issue_s(0, st);
-          issue_s(1, st);
-          umma_commit(&sh.k_empty[st]);
-          if (pages == 1) umma_commit(&sh.q_empty);
+          issue_s(t, st);
+          if (twin || t == last_t) umma_commit(&sh.k_empty[st]);
         }
-        for (int c = 0; c < pages && ok; ++c, ++kc) {
-          const int st = kc % kStages, st1 = (kc + 1) % kStages;
-          const uint32_t par = (kc / kStages) & 1;
+        if (pages == 1) umma_commit(&sh.q_empty);
+        for (int c = 0; c < pages && ok; ++c, kc += streams) {
           const bool last = c == pages - 1;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
+            if (t > last_t) break;
+            const uint32_t kk = kc + (twin ? t : 0), st = kk % kStages, kk1 = kk + streams, st1 = kk1 % kStages;
             // the page's V and the next one's K first: nothing then stands between P_t and its products
-            if (c == 0 && !mbar_wait(&sh.o_free[t], (seg & 1) ^ 1, err, 1516 + t)) { ok = false; break; }
-            if (t == 0 && !mbar_wait(&sh.kv_full[st], par, err, 1518)) { ok = false; break; }
+            if (c == 0 && !mbar_wait(&sh.o_free[t], (runs_of[t] & 1) ^ 1, err, 1516 + t)) { ok = false; break; }
+            if ((t == 0 || twin) && !mbar_wait(&sh.kv_full[st], (kk / kStages) & 1, err, 1518)) { ok = false; break; }
+            if (kRuns && (t == 0 || twin) && !mbar_wait(&sh.v_clean[st], (kk / kStages) & 1, err, 1519)) { ok = false; break; }
             // P_t of this page written (and O_t rescaled if its row maximum moved)
-            if (!mbar_wait(&sh.p_full[t], kc & 1, err, 1514 + t)) { ok = false; break; }
+            if (!mbar_wait(&sh.p_full[t], pages_of[t] & 1, err, 1514 + t)) { ok = false; break; }
+            ++pages_of[t];
             tc_fence_after();
-            issue_o(t, st, c > 0);
-            if (t == 1) umma_commit(&sh.v_empty[st]);
+            issue_o(t, st, c > 0, run.own);
+            if (twin || t == last_t) umma_commit(&sh.v_empty[st]);
             if (!last) {
               // the next page's S_t: after this PV_t in issue order, so it overwrites P_t only once read
-              issue_s(t, st1);
-              if (t == 1) {
-                umma_commit(&sh.k_empty[st1]);
-                if (c + 1 == pages - 1) umma_commit(&sh.q_empty);
+              if (kRuns && (t == 0 || twin)) {
+                if (!mbar_wait(&sh.k_full[st1], (kk1 / kStages) & 1, err, 1513)) { ok = false; break; }
+                tc_fence_after();
               }
+              issue_s(t, st1);
+              if (twin || t == last_t) umma_commit(&sh.k_empty[st1]);
+              if (t == last_t && c + 1 == pages - 1) umma_commit(&sh.q_empty);
             } else {
               umma_commit(&sh.o_full[t]);
+              ++runs_of[t];
             }
           }
         }
-        u = stop;
       }
     }
   } else if (warp < 4) {
     // ---------------------------------------------------------------- rows, for the kernels after this one
-    if (blockIdx.x == 0)
-      line_up_rows(a.lineup, sh_rows, threadIdx.x - 64, 64, [] { asm volatile("bar.sync 1, 64;" ::: "memory"); });
+    if constexpr (!kRuns) {
+      if (blockIdx.x == 0)
+        line_up_rows(a.lineup, sh_rows, threadIdx.x - 64, 64, [] { asm volatile("bar.sync 1, 64;" ::: "memory"); });
+    } else {
+      // Two warps for V. The first loads it; K has a producer of its own (and arrives a softmax earlier), so that neither
+      // waits for the other's stages. The second looks at V of pages that not every row sees all of: what lies behind the
+      // last row's end is cleared, and infinities and NaN among the rows' own tokens, which would reach the rows before
+      // them as 0 * x; where there are any, each row's own ones are added at the end.
+      uint32_t kc = 0;
+      Run run;
+      bool ok = true;
+      while (ok && next_run(run)) {
+        const int streams = run.twin ? 2 : 1;
+        int y = 0;
+        if (warp == 2) y = table_row(run, lane);
+        else if (lane == 0) sh.odd[(n_run - 1) & 1] = 0;
+        __syncwarp();
+        for (int i = 0; i < run.pages * streams; ++i, ++kc) {
+          const int st = kc % kStages, page = run.twin ? i >> 1 : i, other = run.twin ? i & 1 : 0;
+          const uint32_t par = (kc / kStages) & 1;
+          if (warp == 2) {
+            if (page && !other && (page & 31) == 0) y = table_row(run, page + lane);
+            const int at = __shfl_sync(0xffffffffu, y, page & 31) + other * 128;
+            if (!mbar_wait(&sh.v_empty[st], par ^ 1, err, 1504)) { ok = false; break; }
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&sh.kv_full[st], kTile);
+              tma_load_2d(smem + oV + st * kTile, &map_v, &sh.kv_full[st], 0, at);
+              tma_load_2d(smem + oV + st * kTile + kChunk, &map_v, &sh.kv_full[st], 64, at);
+            }
+            __syncwarp();
+            continue;
+          }
+          if (!mbar_wait(&sh.kv_full[st], par, err, 1506)) { ok = false; break; }
+          if (page >= run.masked) {
+            const int token0 = (run.first + page) * 128;
+            bool odd = false;
+            // 16 lanes per key: 8 dims each
+            for (int key = max(0, run.pos + 1 - token0) + lane / 16; key < 128; key += 2) {
+              const int chunk = lane & 15;
+              uint4* at = reinterpret_cast<uint4*>(smem + oV + st * kTile + (chunk >> 3) * kChunk + sw128_off(key, chunk & 7));
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (token0 + key < run.pos + run.rows) {
+                v = *at;
+                bool bad = false;
+                auto check = [&](uint32_t& w) {
+                  if ((w & 0x7f80u) == 0x7f80u) { w &= 0xffff0000u; bad = true; }
+                  if ((w & 0x7f800000u) == 0x7f800000u) { w &= 0xffffu; bad = true; }
+                };
+                check(v.x); check(v.y); check(v.z); check(v.w);
+                if (!bad) continue;
+                odd = true;
+              }
+              *at = v;
+            }
+            if (odd) sh.odd[(n_run - 1) & 1] = 1;
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.v_clean[st]);
+        }
+        run_done(false);
+      }
+    }
   } else {
     // ---------------------------------------------------------------- softmax (thread = one head of one new row, 64 keys)
     const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;
@@ -281,7 +548,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_at = tmem + lane_off + t * 128 + half * 64;        // this warp's scores, and P over their first half
     const uint32_t o_at = tmem + lane_off + 256 + t * 128 + half * 64;  // the columns of O that it rescales and reads out
-    const int row = (2 * pair + t) * tile_rows + lrow / a.hg;
     {
       // while the first pages are on their way: is the prefix the same one for every sequence with rows?
       bool bad = false;
@@ -296,9 +562,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     uint32_t kc = 0, pair_ph = 0;
     bool ok = true;
-    int seg = 0;
-    for (int u = u_begin; u < u_end && ok; ++seg) {
-      const int g = u / a.prefix, stop = min(u_end, (g + 1) * a.prefix), pages = stop - u;
+    Run run;
+    for (int seg = 0; ok && next_run(run);) {
+      if (kRuns && t && !run.twin && run.rows <= tile_rows) {  // no second tile
+        run_done(false);
+        continue;
+      }
+      const bool twin = kRuns && run.twin;
+      const int in = (twin ? 0 : t * tile_rows) + lrow / a.hg, row = run.row0 + in;
+      const int pages = run.pages;
       float m_run = -INFINITY, l_run = 0.f;  // the maximum is the row's, the sum that of this warp's keys
       if (!mbar_wait(&sh.s_full[t], kc & 1, err, 1522 + t)) { ok = false; break; }
       for (int c = 0; c < pages && ok; ++c, ++kc) {
@@ -307,26 +579,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32_max(s_at, *reinterpret_cast<float(*)[32]>(sv), mq[0]);
         tmem_ld32_max(s_at + 32, *reinterpret_cast<float(*)[32]>(sv + 32), mq[1]);
         tmem_wait_ld();
+        if (kRuns && c >= run.masked) {
+          const int seen = run.pos + in + 1 - (run.first + c) * 128 - half * 64;  // keys of this warp's before the row's end
+          mq[0] = mq[1] = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 64; ++i) {
+            if (i >= seen) sv[i] = -INFINITY;
+            mq[i & 1] = fmaxf(mq[i & 1], sv[i]);
+          }
+        }
         const float m_blk = fmaxf(mq[0], mq[1]) * a.scale_log2;
         sh.row_max[t][half][lrow] = m_blk;
         bool mine = c == 0 || __any_sync(0xffffffffu, m_blk > m_run + kHeadroom);  // this warp calls the other
         float l_add = 0.f;
         auto write_p = [&]() {
           float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
+          const float base = kRuns && m_run == -INFINITY ? 0.f : m_run;  // (nothing seen: exp2(-inf - 0) = 0)
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            uint32_t pk[8];
+            uint32_t pk[8], rest[8];
 #pragma unroll
             for (int z = 0; z < 8; ++z) {
               float p0 = sv[16 * h + 2 * z], p1 = sv[16 * h + 2 * z + 1];
-              fma2(p0, p1, a.scale_log2, -m_run);
+              fma2(p0, p1, a.scale_log2, -base);
               p0 = fast_exp2(p0);
               p1 = fast_exp2(p1);
               if (z & 1) add2(t0, t1, p0, p1);
               else add2(s0, s1, p0, p1);
               pk[z] = pack_bf16(p0, p1);
+              if (kRuns) rest[z] = pack_bf16(p0 - __uint_as_float(pk[z] << 16), p1 - __uint_as_float(pk[z] & 0xffff0000u));
             }
             tmem_st8(s_at + 8 * h, pk);
+            if (kRuns && run.own) tmem_st8(s_at + 32 + 8 * h, rest);
           }
           l_add = (s0 + s1) + (t0 + t1);
         };
@@ -405,9 +689,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float l = half ? sh.row_max[t][0][lrow] + l_run : l_run + sh.row_max[t][1][lrow];
       if (!warps_sync(&sh.pair[t][quarter], pair_ph, err, 1534 + t)) { ok = false; break; }
       tc_fence_after();
-      const int slot = team - team_of(g * a.prefix, units, a.teams);
-      const size_t at = ((size_t)slot * a.N + row) * a.Hq + g * a.hg + lrow % a.hg;
-      const float inv = 1.f / l;
+      const bool valid = kRuns ? in < run.rows : row < a.N;
+      const int group = run.g + (twin ? t : 0);
+      const size_t at = ((size_t)run.slot * a.N + row) * a.Hq + group * a.hg + lrow % a.hg;
+      const bool odd = kRuns && run.own && sh.odd[(n_run - 1) & 1];
+      const float inv = kRuns && l == 0.f ? 0.f : 1.f / l;  // (a run behind the row's end)
       float* dst = a.part_o + at * 128 + half * 64;
 #pragma unroll
       for (int z = 0; z < 4; ++z) {
@@ -416,16 +702,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i] *= inv;
-        if (row < a.N) {
+        if (odd && valid) {  // infinities and NaN of the own tokens that this row sees, and of this run's
+          const int begin = max(run.pos + 1, run.first * 128), end = min(run.pos + in + 1, (run.first + run.pages) * 128);
+          for (int k = begin; k < end; ++k) {
+            const int page = ld_in(a.page_table + (size_t)run.seq * a.max_blocks + k / 128);
+            if (page < 0 || page >= a.num_pages) continue;
+            const __nv_bfloat16* v = a.V + (((size_t)page * a.G + group) * 128 + k % 128) * 128 + half * 64 + z * 16;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float x = __bfloat162float(v[i]);
+              if (!(fabsf(x) < INFINITY)) o[i] += x;
+            }
+          }
+        }
+        if (valid) {
           st_global8(dst + 16 * z, o);
           st_global8(dst + 16 * z + 8, o + 8);
         }
       }
-      if (row < a.N && half == 0) a.part_lse[at] = m_run + log2f(l);
+      if (valid && half == 0) a.part_lse[at] = m_run + log2f(l);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.o_free[t]);
-      u = stop;
+      ++seg;
+      run_done(false);
     }
   }
   __syncwarp();
@@ -433,6 +733,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (threadIdx.x == 0) a.flags[blockIdx.x] = sh.flag;
   if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <bool kRuns>
+cudaError_t launch_prefix(const PrefixArgs& a, int blocks, const CUtensorMap& mq, const CUtensorMap& mk,
+                          const CUtensorMap& mv, cudaStream_t st) {
+  static bool attr[kMaxDevices] = {};
+  const int dslot = device_slot();
+  if (!attr[dslot]) {
+    cudaError_t e = cudaFuncSetAttribute(paged_prefix_kernel<kRuns>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    attr[dslot] = true;
+  }
+  count_launches(1);
+  return launch_dependent(paged_prefix_kernel<kRuns>, blocks, kThreads, kSmem, st, a, mq, mk, mv);
 }
 
 }  // namespace
@@ -467,15 +781,14 @@ cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, con
   a.num_pages = p.num_pages;
   a.max_blocks = p.max_blocks;
   a.scale_log2 = p.scale * kLog2e;
-  static bool attr[kMaxDevices] = {};
-  const int dslot = device_slot();
-  if (!attr[dslot]) {
-    cudaError_t e = cudaFuncSetAttribute(paged_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    attr[dslot] = true;
-  }
-  count_launches(1);
-  return launch_dependent(paged_prefix_kernel, L.teams * L.pairs, kThreads, kSmem, st, a, mq, mk, mv);
+  a.runs = reinterpret_cast<const int4*>(ws + L.runs);
+  a.V = static_cast<const __nv_bfloat16*>(c.V);
+  a.header = reinterpret_cast<int*>(ws);
+  a.run_rows = L.run_rows;
+  a.per_run = L.per_run;
+  a.rslots = L.rslots;
+  a.pslots = L.pslots;
+  return L.run_rows ? launch_prefix<true>(a, L.n_flags, mq, mk, mv, st) : launch_prefix<false>(a, L.n_flags, mq, mk, mv, st);
 }
 
 }  // namespace msa

@@ -19,9 +19,9 @@ namespace msa {
 
 struct RowsArgs {
   const int32_t *row_start, *seq_len;
-  int4 *rows, *lead;
+  int4 *rows, *lead, *runs;
   int *arrived, *header;
-  int S, N, n_arrived, max_blocks, prefix, tile_rows;
+  int S, N, n_arrived, max_blocks, prefix, tile_rows, run_rows;
 };
 
 inline RowsArgs rows_args(const PagedProb& p, const PagedCachePtrs& c, uint8_t* ws, const PagedWs& L) {
@@ -30,6 +30,7 @@ inline RowsArgs rows_args(const PagedProb& p, const PagedCachePtrs& c, uint8_t* 
   a.seq_len = c.seq_len;
   a.rows = reinterpret_cast<int4*>(ws + L.rows);
   a.lead = reinterpret_cast<int4*>(ws + L.lead);
+  a.runs = reinterpret_cast<int4*>(ws + L.runs);
   a.arrived = reinterpret_cast<int*>(ws + L.arrived);
   a.header = reinterpret_cast<int*>(ws);
   a.S = p.S;
@@ -38,6 +39,7 @@ inline RowsArgs rows_args(const PagedProb& p, const PagedCachePtrs& c, uint8_t* 
   a.max_blocks = p.max_blocks;
   a.prefix = p.prefix;
   a.tile_rows = L.tile_rows;
+  a.run_rows = L.run_rows;
   return a;
 }
 
@@ -86,7 +88,7 @@ __device__ __forceinline__ void line_up_rows(const RowsArgs& a, RowsShared& sh, 
   for (int i = tid; i < a.n_arrived; i += threads) a.arrived[i] = 0;
   sync();
   auto start = [&](int i) { return all ? sh.staged[i] : ld_in(a.row_start + i); };
-  int leads = 0;
+  int leads = 0, runs = 0;
   for (int r0 = 0; r0 < a.N; r0 += threads) {
     const int r = r0 + tid;
     int4 out = make_int4(-1, 0, 0, 0);
@@ -103,21 +105,27 @@ __device__ __forceinline__ void line_up_rows(const RowsArgs& a, RowsShared& sh, 
       }
       a.rows[r] = out;
     }
-    if (a.tile_rows == 1) continue;
     // the rows that lead a tile, in order
-    const bool lead = out.x >= 0 && out.z % a.tile_rows == 0;
-    const unsigned m = __ballot_sync(0xffffffffu, lead);
-    if (lane == 0) sh.sums[warp] = __popc(m);
-    sync();
-    int before = leads;
-    for (int w = 0; w < threads / 32; ++w) {
-      if (w < warp) before += sh.sums[w];
-      leads += sh.sums[w];
-    }
-    if (lead) a.lead[before + __popc(m & ((1u << lane) - 1))] = make_int4(out.x, out.y, r, min(a.tile_rows, out.w));
-    sync();
+    auto list = [&](int rows, int4* to, int& count) {
+      const bool lead = out.x >= 0 && out.z % rows == 0;
+      const unsigned m = __ballot_sync(0xffffffffu, lead);
+      if (lane == 0) sh.sums[warp] = __popc(m);
+      sync();
+      int before = count;
+      for (int w = 0; w < threads / 32; ++w) {
+        if (w < warp) before += sh.sums[w];
+        count += sh.sums[w];
+      }
+      if (lead) to[before + __popc(m & ((1u << lane) - 1))] = make_int4(out.x, out.y, r, min(rows, out.w));
+      sync();
+    };
+    if (a.tile_rows > 1 && !a.run_rows) list(a.tile_rows, a.lead, leads);
+    if (a.run_rows) list(a.run_rows, a.runs, runs);
   }
-  if (tid == 0) a.header[kLeadCount] = leads;
+  if (tid == 0) {
+    a.header[kLeadCount] = leads;
+    a.header[kRunCount] = runs;
+  }
 }
 
 // What the blocks of the kernel before found wrong; by one warp.

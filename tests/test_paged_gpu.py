@@ -313,6 +313,140 @@ def test_dense(msa, name, stale):
     _check_padding(b, O, LSE)
 
 
+# Several rows per sequence: more than eight columns on average and more than a page take 128-row tiles (of 128 / h_g
+# rows, two at a time).
+RUNS = {
+    "hg8": dict(counts=[5, 3, 8], lens=[700, 130, 1000], Hq=16, G=2),
+    "one_group": dict(counts=[4, 9], lens=[513, 900], Hq=8, G=1),
+    "two_tiles": dict(counts=[20, 33, 1], lens=[600, 400, 300], Hq=16, G=2, pad=3),
+    "two_tiles_one_group": dict(counts=[17, 40], lens=[17, 390], Hq=8, G=1),
+    "hg1": dict(counts=[300, 10, 0, 129], lens=[1000, 300, 50, 129], Hq=2, G=2),
+    "hg2_three_groups": dict(counts=[6, 70], lens=[256, 500], Hq=6, G=3),
+    "hg4_ends": dict(counts=[4, 4, 4, 4, 4], lens=[127, 128, 130, 256, 259], Hq=8, G=2),
+    "long": dict(counts=[4], lens=[128 * 70 + 2], Hq=16, G=2),
+    "long_across_pages": dict(counts=[16], lens=[128 * 30 + 7], Hq=8, G=1),
+    "prefix": dict(counts=[3, 18, 0, 5], lens=[128 * 6 + 3, 128 * 6 + 400, 4, 128 * 7 + 5], Hq=16, G=2, prefix=6),
+    "prefix_three_pairs": dict(counts=[7] * 13, lens=[128 * 3 + 7 + 11 * i for i in range(13)], Hq=24, G=3, prefix=3),
+    "prefix_hg1_one_group": dict(counts=[12, 140], lens=[128 * 2 + 12, 128 * 2 + 300], Hq=1, G=1, prefix=2, pad=2),
+}
+
+
+@pytest.mark.parametrize("stale", [NAN, INF], ids=["nan", "inf"])
+@pytest.mark.parametrize("name", RUNS)
+def test_dense_rows(msa, name, stale):
+    b = ref.Batch(stale=stale, seed=16, **RUNS[name])
+    O, LSE = _dense(msa, b)
+    rows = range(b.n) if b.n < 60 else range(0, b.n, 7)
+    heads = range(b.Hq) if b.Hq <= 8 else range(0, b.Hq, 5)
+    ref.check_attention(b, rows, heads, O, LSE, _all(b), bf16_p=b.prefix > 0)
+    _check_padding(b, O, LSE)
+
+
+@pytest.mark.parametrize("shape", [dict(counts=[6, 5], lens=[262, 140], Hq=16, G=2),
+                                   dict(counts=[20, 9], lens=[400, 134], Hq=8, G=1),
+                                   dict(counts=[140, 9], lens=[400, 262], Hq=3, G=3),
+                                   dict(counts=[6, 5], lens=[520, 515], Hq=16, G=2, prefix=3)], ids=str)
+def test_later_rows_do_not_reach_earlier_ones_of_a_tile(msa, shape):
+    """As above for 128-row tiles; and the rows that see such values have them: those of V as they are added up."""
+    import torch
+
+    b = ref.Batch(seed=10, **shape)
+    clean = _dense(msa, b)
+    # the sequence's last but i row: NaN, infinities of one and of both signs in V alone; NaN in K and V
+    for s in range(2):
+        for i, d, v in ((0, 3, NAN), (1, 40, INF), (2, 70, -INF), (2, 90, INF), (3, 90, -INF)):
+            t = b.lens[s] - 1 - i
+            b.V[int(b.table[s, t // 128]), :, t % 128, d] = v
+    O, LSE = _dense(msa, b)
+    assert bool((LSE[:b.n] == clean[1][:b.n]).all())
+    for r in range(b.n):
+        want = clean[0][r].clone()
+        behind = b.lens[b.row_seq[r]] - 1 - b.row_pos[r]
+        if behind <= 3:
+            want[:, 90] = -INF
+        if behind <= 2:
+            want[:, 70], want[:, 90] = -INF, NAN
+        if behind <= 1:
+            want[:, 40] = INF
+        if behind <= 0:
+            want[:, 3] = NAN
+        same = (O[r] == want) | (O[r].isnan() & want.isnan())
+        assert bool(same.all()), (r, behind, torch.nonzero(~same)[:4].tolist())
+    for s in range(2):
+        t = b.lens[s] - 1 - 2
+        b.K[int(b.table[s, t // 128]), :, t % 128] = NAN
+    O, LSE = _dense(msa, b)
+    for r in range(b.n):
+        behind = b.lens[b.row_seq[r]] - 1 - b.row_pos[r]
+        if behind > 3:
+            assert bool((O[r] == clean[0][r]).all()) and bool((LSE[r] == clean[1][r]).all()), r
+        elif behind <= 2:
+            assert bool(O[r].isnan().all()) and bool(LSE[r].isnan().all()), r
+
+
+def test_dense_rows_large_scores(msa):
+    b = ref.Batch(counts=[3, 2, 20], lens=[128 * 6 + 90, 128 * 7, 128 * 6 + 1], Hq=16, G=2, seed=9)
+    for s in range(3):
+        for c in range(6):
+            b.K[int(b.table[s, c])] *= 1.0 if s else float(1 + 3 * c)
+    b.Q *= 4
+    O, LSE = _dense(msa, b)
+    ref.check_attention(b, range(b.n), range(0, b.Hq, 3), O, LSE, _all(b))
+
+
+def _shared_pages(S, rows, length, Hq, G, seed=21):
+    """A batch whose sequences all have the same pages (nothing is appended here, so they may)."""
+    one = ref.Batch(counts=[rows], lens=[length], Hq=Hq, G=G, seed=seed)
+    b = ref.Batch(counts=[rows] * S, lens=[0] * S, Hq=Hq, G=G, seed=seed + 1, spare=0, index=False)
+    b.K, b.V, b.k_idx, b.num_pages, b.max_blocks = one.K, one.V, one.k_idx, one.num_pages, one.max_blocks
+    b.table, b.lens = one.table.expand(S, -1).contiguous(), [length] * S
+    b.row_pos = [length - rows + j for _ in range(S) for j in range(rows)]
+    return b
+
+
+def test_dense_rows_many_long(msa):
+    """So many sequences that a run has all their pages: more than the 32 that are looked up at a time."""
+    b = _shared_pages(1530, 2, 128 * 69 + 5, 8, 1)
+    O, LSE = _dense(msa, b)
+    ref.check_attention(b, [0, 1, 700, 1531, 3059], range(0, 8, 3), O, LSE, _all(b))
+
+
+def test_dense_single_rows_many_long(msa):
+    b = _shared_pages(1600, 1, 128 * 69 + 5, 8, 1)
+    O, LSE = _dense(msa, b)
+    ref.check_attention(b, [0, 1, 700, 1599], range(0, 8, 3), O, LSE, _all(b))
+
+
+@pytest.mark.parametrize("S,rows,Hq,G", [(4500, 1, 2, 1), (2100, 3, 2, 1), (700, 3, 8, 1), (1, 1200, 2, 2)], ids=str)
+def test_many_sequences_and_rows(msa, S, rows, Hq, G):
+    """More sequences than are kept in shared memory, and more rows than a pass over them takes."""
+    b = _shared_pages(S, rows, max(rows, 200), Hq, G)
+    O, LSE = _dense(msa, b)
+    some = sorted({0, 1, 300, 1023, 1024, 1025, 1100, b.n - 2, b.n - 1})
+    ref.check_attention(b, some, range(Hq), O, LSE, _all(b))
+    O, LSE, bi = _sparse(msa, b, 2)
+    for r in some:
+        np.testing.assert_array_equal(bi[r], ref.select(b, r, 2))
+    ref.check_attention(b, some, range(Hq), O, LSE, lambda r, g: bi[r, g].tolist())
+
+
+def test_sparse_whole_rows_many(msa):
+    """More selected blocks in a row's run than the 32 that are looked up at a time."""
+    b = _shared_pages(1600, 1, 128 * 69 + 5, 2, 1)
+    O, LSE, bi = _sparse(msa, b, 100)
+    for r in (0, 5, 1599):
+        np.testing.assert_array_equal(bi[r], ref.select(b, r, 100))
+    ref.check_attention(b, [0, 5, 1599], range(2), O, LSE, lambda r, g: bi[r, g].tolist())
+
+
+def test_sparse_half_a_million(msa):
+    """More blocks than the selection's smaller block of threads holds."""
+    b = ref.Batch(counts=[1], lens=[(1 << 19) - 3], Hq=2, G=1, seed=18)
+    O, LSE, bi = _sparse(msa, b, 16)
+    np.testing.assert_array_equal(bi[0], ref.select(b, 0, 16))
+    ref.check_attention(b, [0], range(2), O, LSE, lambda r, g: bi[r, g].tolist())
+
+
 def test_dense_large_scores(msa):
     """Scores whose maximum moves by far more than exp2's range from page to page."""
     b = ref.Batch(counts=[2, 1, 1], lens=[128 * 6 + 90, 128 * 7, 128 * 6 + 1], Hq=8, G=2, prefix=4, seed=9)
