@@ -72,7 +72,7 @@ struct RopeRows {
 
 cudaError_t launch_paged_append(const PagedProb& p, const PagedCachePtrs& c, const RopeRows& r, uint8_t* ws,
                                 cudaStream_t st);
-// The call's first work (paged_rows.cuh) as a kernel of its own; the index scores and the shared prefix do it themselves.
+// The call's first work (paged_rows.cuh) as a kernel of its own (the index scores' kernel does it itself).
 cudaError_t launch_paged_rows(const PagedProb& p, const PagedCachePtrs& c, uint8_t* ws, const PagedWs& L,
                               cudaStream_t st);
 cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, const void* q_idx, int32_t* block_idx,
@@ -81,6 +81,7 @@ cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, cons
 // block_idx null, over its sequence's pages behind the shared prefix.
 cudaError_t launch_paged_attn(const PagedProb& p, const PagedCachePtrs& c, const void* Q, const int32_t* block_idx,
                               void* O, float* LSE, uint8_t* ws, const PagedWs& L, cudaStream_t st);
+// Shared prefix, and runs of the sequences' own pages. The attention kernel may start while it still runs.
 cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, const void* Q, uint8_t* ws,
                                 const PagedWs& L, cudaStream_t st);
 // Joins the parts of the shared prefix and of the own pages (without a prefix the attention does).

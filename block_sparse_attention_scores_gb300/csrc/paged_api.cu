@@ -72,7 +72,15 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
       const int tiles = (int)(((long long)p.N * p.hg + 127) / 128);
       L.pairs = (tiles + 1) / 2;
       const int units = p.G * p.prefix;
-      L.teams = std::min(units, std::max(1, kCutSms / L.pairs));
+      // The own pages' kernel runs beside: its CTAs start on the SMs left over, the others as the prefix's end, so that the
+      // memory is busy while the tensor core is. Both are estimated (a page takes a pair of tiles 2,750 cycles, a row tile
+      // 2,000; own pages: half of what the table holds), and the prefix has half of the SMs at least, lest a poor estimate
+      // make it the longer one. 64 sequences behind 32K tokens with up to 2K of their own: 112 us one after the other,
+      // 100 with two thirds, 94 with half, 102 with 0.35 of the SMs; 100 sequences with 2000 each: 67, 49, 48, 48.
+      const double own = (double)std::max(p.N / L.tile_rows, std::min(p.S, p.N)) * p.G * (p.max_blocks - p.prefix + 1) / 2 * 2000;
+      const double shared = (double)units * L.pairs * 2750;
+      const int sms = L.run_rows ? kCutSms : (int)(kCutSms * std::max(0.5, shared / (shared + own)));
+      L.teams = std::min(units, std::max(1, sms / L.pairs));
       L.n_flags = std::max(L.n_flags, L.teams * L.pairs);
       for (int g = 0; g < p.G; ++g)
         L.pslots = std::max(L.pslots, team_of((g + 1) * p.prefix - 1, units, L.teams) -
@@ -276,8 +284,7 @@ msa_status msa_paged_dense_attn(const msa_paged_shape* shape, const msa_paged_ca
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(workspace);
   const bool parts = p.prefix || L.run_rows;
-  if ((!p.prefix || L.run_rows) && (s = cuda_status(launch_paged_rows(p, c, w, L, st), "paged rows launch")) != MSA_OK)
-    return s;
+  if ((s = cuda_status(launch_paged_rows(p, c, w, L, st), "paged rows launch")) != MSA_OK) return s;
   if (parts && (s = cuda_status(launch_paged_prefix(p, c, Q, w, L, st), "paged prefix launch")) != MSA_OK) return s;
   if (!L.run_rows &&
       (s = cuda_status(launch_paged_attn(p, c, Q, nullptr, O, LSE, w, L, st), "paged attention launch")) != MSA_OK)

@@ -51,6 +51,7 @@ struct AttnArgs {
   __nv_bfloat16* O;
   float* LSE;
   int N, Hq, G, hg, hg_log2, k, num_pages, max_blocks, prefix, splits, per_split, tile_rows, items, slot0, join;
+  int beside;                             // the prefix kernel may still be running (what it writes is not read here)
   float scale_log2;
   const int* flags;                       // [n_flags] of the first kernel's blocks
   int n_flags;
@@ -117,14 +118,14 @@ __device__ __forceinline__ void fetch_row(const AttnArgs& a, int item, int items
   const int t = item / a.G;
   f.split = t % a.splits;
   f.row = t / a.splits;
-  f.info = ld_in((a.lead ? a.lead : a.rows) + f.row);
+  f.info = __ldcg((a.lead ? a.lead : a.rows) + f.row);
   if (a.block_idx) {
     const int32_t* ids = a.block_idx + ((size_t)f.row * a.G + f.g) * a.k;
     const int at = f.split * a.per_split + lane;
-    f.id = at < a.k ? ld_in(ids + at) : -1;
-    f.before = at > 0 && at < a.k ? ld_in(ids + at - 1) : -1;
+    f.id = at < a.k ? __ldcg(ids + at) : -1;
+    f.before = at > 0 && at < a.k ? __ldcg(ids + at - 1) : -1;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) f.ids[c] = c * 32 + lane < a.k ? ld_in(ids + c * 32 + lane) : -1;
+    for (int c = 0; c < 4; ++c) f.ids[c] = c * 32 + lane < a.k ? __ldcg(ids + c * 32 + lane) : -1;
   }
 }
 
@@ -155,7 +156,7 @@ __device__ __forceinline__ void fetch_pages(const AttnArgs& a, int lane, Fetch& 
   }
   if (f.row < 0 || lane >= f.pages) f.block = -1;
   else if (f.block >= 0 && f.block <= f.info.y / 128 + a.tile_rows)
-    f.page = ld_in(a.page_table + (size_t)f.info.x * a.max_blocks + min(f.block, a.max_blocks - 1));
+    f.page = __ldcg(a.page_table + (size_t)f.info.x * a.max_blocks + min(f.block, a.max_blocks - 1));
 }
 
 // The page as it was read, or -1 (reported) where it may not be: ids ascend up to the row's own block, pages lie in
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_release();
   __syncthreads();
-  pdl_wait();
+  if (!a.beside) pdl_wait();
 
   if (warp == kWarps) {
     // ---------------------------------------------------------------- producer
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     // Items are taken as they come, the first one by the CTA's number: their lengths differ. The next one is looked for
     // when the last four pages are being asked for, one step a page: its number, its row, its pages.
-    const int items = a.lead ? ld_in(a.header + kLeadCount) * a.splits * a.G : a.items;
+    const int items = a.lead ? __ldcg(a.header + kLeadCount) * a.splits * a.G : a.items;
     int id = blockIdx.x, id_next = 0, taken = 0, step = 0;
     Fetch now, next;
     auto advance = [&]() {
@@ -353,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __threadfence();
       join_parts(a, item, warp - kWarps - 1, lane);
     }
+    if (a.beside) pdl_wait();  // the kernel after this one takes both to be done
   } else {
     // ---------------------------------------------------------------- consumers
     const int r = lane >> 2, q = lane & 3;
@@ -596,7 +598,7 @@ struct MergeArgs {
   __nv_bfloat16* O;
   float* LSE;
   int N, Hq, G, hg, prefix, per_split, tile_rows, teams, pslots;
-  const int* flags;  // [n_flags] of the prefix kernel's blocks, where no attention kernel comes between
+  const int* flags;  // [n_flags] of the prefix kernel's blocks
   int n_flags;
   int* err;
 };
@@ -713,7 +715,8 @@ cudaError_t launch_paged_attn(const PagedProb& p, const PagedCachePtrs& c, const
   a.LSE = LSE;
   a.scale_log2 = p.scale * kLog2e;
   a.flags = reinterpret_cast<const int*>(ws + L.flags);
-  a.n_flags = L.n_flags;
+  a.beside = L.pslots > 0;
+  a.n_flags = a.beside ? 0 : L.n_flags;
   a.err = reinterpret_cast<int*>(ws);
   return launch_attn(a, mk, mv, st);
 }
@@ -740,7 +743,7 @@ cudaError_t launch_paged_merge(const PagedProb& p, void* O, float* LSE, uint8_t*
     a.tile_rows = L.run_rows;
   }
   a.flags = reinterpret_cast<const int*>(ws + L.flags);
-  a.n_flags = L.run_rows ? L.n_flags : 0;
+  a.n_flags = L.n_flags;
   a.err = reinterpret_cast<int*>(ws);
   const long long items = (long long)p.N * p.Hq;
   count_launches(1);

@@ -53,7 +53,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kHeadroom = 8.f;  // P = exp2(s - m) stays <= 2^kHeadroom
-// warp 0 TMA, warp 1 UMMA + TMEM, 2 and 3 the rows (or V), 4-11 and 12-19 softmax of tiles 0 and 1
+// warp 0 TMA, warp 1 UMMA + TMEM, 2 and 3 V of own pages, 4-11 and 12-19 softmax of tiles 0 and 1
 constexpr int kThreads = 640;
 constexpr int kTile = 32768;      // 128 rows x 128 bf16, two 64-column SW128 chunks
 constexpr int kChunk = 16384;
@@ -74,7 +74,6 @@ struct Run {
 };
 
 struct PrefixArgs {
-  RowsArgs lineup;
   int* flags;  // [blocks] what a block found wrong (the error word is cleared meanwhile; the merge reports it)
   const int32_t *page_table, *row_start;
   float *part_o, *part_lse;
@@ -138,7 +137,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ PrefixShared sh;
-  __shared__ RowsShared sh_rows;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int team = a.pairs ? blockIdx.x / a.pairs : 0, pair = a.pairs ? blockIdx.x % a.pairs : 0;
   const int units = a.G * a.prefix;
@@ -180,11 +178,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&sh.tmem_base, 512);
     tmem_relinquish();
   }
-  pdl_release();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   pdl_wait();
+  pdl_release();  // (not before: the kernel that starts on the SMs left over reads what the one before this wrote)
   // the first sequence with rows: its table holds the shared pages
   const int ref = find_sequence(a.row_start, a.S, 0, lane);
   int* const err = &sh.flag;
@@ -476,11 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp < 4) {
-    // ---------------------------------------------------------------- rows, for the kernels after this one
-    if constexpr (!kRuns) {
-      if (blockIdx.x == 0)
-        line_up_rows(a.lineup, sh_rows, threadIdx.x - 64, 64, [] { asm volatile("bar.sync 1, 64;" ::: "memory"); });
-    } else {
+    // ---------------------------------------------------------------- V of the sequences' own pages
+    if constexpr (kRuns) {
       // Two warps for V. The first loads it; K has a producer of its own (and arrives a softmax earlier), so that neither
       // waits for the other's stages. The second looks at V of pages that not every row sees all of: what lies behind the
       // last row's end is cleared, and infinities and NaN among the rows' own tokens, which would reach the rows before
@@ -764,7 +759,6 @@ cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, con
   }
   if (!encode_pool_map(&mk, p, c.K) || !encode_pool_map(&mv, p, c.V)) return cudaErrorInvalidValue;
   PrefixArgs a;
-  a.lineup = rows_args(p, c, ws, L);
   a.flags = reinterpret_cast<int*>(ws + L.flags);
   a.page_table = c.page_table;
   a.row_start = c.row_start;

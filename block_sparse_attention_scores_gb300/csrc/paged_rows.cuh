@@ -4,11 +4,11 @@
 // outside the page table (or, behind a shared prefix, inside the prefix) is
 // reported and left out.
 //
-// A few warps of the call's first kernel do this (the index scores', the shared
-// prefix's); nobody else in that kernel needs it, and a kernel of its own costs
-// two to four microseconds of every call. The others there must not write the
-// error word, which this clears: they leave what they find in `flags`, a word
-// per block, and the next kernel reports it.
+// In front of the index scores a block of their kernel does this: nobody else in
+// it needs the rows, and a kernel of its own costs two to four microseconds. The
+// blocks there must not write the error word, which this clears: they leave what
+// they find in `flags`, a word per block, and a later kernel reports it (so do
+// the shared prefix's blocks).
 #pragma once
 
 #include "paged.h"

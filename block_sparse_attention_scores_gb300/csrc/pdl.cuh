@@ -1,8 +1,8 @@
 // Programmatic dependent launch: a kernel of a call is launched while the one
 // before it still runs, sets itself up (barriers, TMEM, descriptors), and waits
 // for that one's end and its writes before it touches global memory. What an
-// earlier kernel may have written is read through L2 (ld_l2), not through the
-// read-only path.
+// earlier kernel may have written is read with ordinary loads (ld_in), not through
+// the read-only path.
 #pragma once
 
 #include <cuda_runtime.h>
