@@ -202,8 +202,6 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-constexpr int kSelItems = 8;  // blocks a thread holds: 256 threads up to 2048 blocks, 1024 up to 8192
-
 struct SelectArgs {
   const int4* rows;
   const float *pooled, *amax;
@@ -234,12 +232,40 @@ __device__ __forceinline__ float from_key(uint32_t k) {
 __device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// The block's exact maximum for a query (64 bf16 at q), by one warp: a lane
-// scores four keys in fp32, and the keys within `margin` of the best one are
-// summed again in 64 bits, two dims per lane. 64 fused steps are off by
-// 64 * 2^-24 of the products' magnitudes at worst, so a difference of two
-// scores by less than kErr of them.
-__device__ double exact_max(const __nv_bfloat16* page, const __nv_bfloat16* q, float margin, int lane) {
+// The largest of a block's scores for a query (64 bf16 at q), by one warp, in 64-bit integers: the products (exact in fp32)
+// in units of 2^-57 of `most`, the largest that q and the block's keys could have, 64 of which stay below 2^63.
+__device__ __noinline__ double integer_max(const __nv_bfloat16* page, const __nv_bfloat16* q, float most, int lane) {
+  const int up = 56 - ((int)(__float_as_uint(most) >> 23) - 127);
+  const float scale = __uint_as_float((uint32_t)(up + 127) << 23);
+  long long top = -0x7fffffffffffffffll;
+#pragma unroll 1
+  for (int key = lane; key < 128; key += 32) {
+    long long sum = 0;
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+      const uint4 w = ld_in(reinterpret_cast<const uint4*>(q) + c), k = ld_in(reinterpret_cast<const uint4*>(page + key * 64) + c);
+      const uint32_t wv[4] = {w.x, w.y, w.z, w.w}, kv[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+        sum += __float2ll_rz(lo_f(wv[z]) * scale * lo_f(kv[z])) + __float2ll_rz(hi_f(wv[z]) * scale * hi_f(kv[z]));
+    }
+    top = max(top, sum);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  return (double)top * __longlong_as_double((long long)(1023 - up) << 52);
+}
+
+// The block's exact maximum for a query, by one warp: a lane scores four keys in
+// fp32, and the keys within `margin` of the best one are summed again in 64 bits.
+// 64 fused steps are off by 64 * 2^-24 of the products' magnitudes at worst, so a
+// difference of two scores by less than kErr of them.
+//
+// Few such keys (as a rule one): doubles, two dims per lane. Many, as where all
+// keys of a block are the same (one token over and over: then every block is
+// undecided, too): integers, a key per lane, since a row of 128K such tokens
+// takes doubles 24 ms and integers 0.2.
+__device__ __noinline__ double exact_max(const __nv_bfloat16* page, const __nv_bfloat16* q, float margin, float qmax, float kmax, int lane) {
   float s32[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -264,6 +290,13 @@ __device__ double exact_max(const __nv_bfloat16* page, const __nv_bfloat16* q, f
   float best = fmaxf(fmaxf(s32[0], s32[1]), fmaxf(s32[2], s32[3]));
 #pragma unroll
   for (int o = 16; o; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+  const float most = qmax * kmax;
+  if (most >= 0x1p-60f && most <= 0x1p90f && kmax >= 0x1p-60f) {
+    int many = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) many += __popc(__ballot_sync(0xffffffffu, !(s32[i] < best - margin)));
+    if (many > 8) return integer_max(page, q, most, lane);
+  }
   const uint32_t qq = ld_in(reinterpret_cast<const uint32_t*>(q) + lane);
   double top = -INFINITY;
 #pragma unroll
@@ -284,7 +317,7 @@ __device__ double exact_max(const __nv_bfloat16* page, const __nv_bfloat16* q, f
 // One block per (row, group). A thread keeps its blocks' lower bounds (as
 // ordered keys) and errors in registers; shared memory has room for the list of
 // undecided blocks and their scores.
-template <int kThreads>
+template <int kThreads, int kSelItems>
 __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
   pdl_release();
   pdl_wait();
@@ -320,7 +353,7 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
     e[z] = i < n ? ld_in(am + i) : 0.f;
   }
   if (tid == 0) sh.n_in = sh.n_open = 0;
-  if (tid < 256) sh.chosen[tid] = 0;
+  for (int i = tid; i < kThreads * kSelItems / 32; i += kThreads) sh.chosen[i] = 0;
   float l1 = fabsf(lo_f(qq)) + fabsf(hi_f(qq));  // |q|_1
 #pragma unroll
   for (int o = 16; o; o >>= 1) l1 += __shfl_xor_sync(0xffffffffu, l1, o);
@@ -433,11 +466,18 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
     for (int i = tid; i < n_open; i += kThreads) atomicOr(&sh.chosen[open[i] / 32], 1u << (open[i] % 32));
   } else {
     // the border runs through the open blocks: their exact maxima decide, equal ones by the lower id
+    float qmax = fmaxf(fabsf(lo_f(qq)), fabsf(hi_f(qq)));
+    if (!(l1 < INFINITY)) qmax = INFINITY;  // (a NaN as well)
+#pragma unroll
+    for (int o = 16; o; o >>= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, o));
     for (int i = warp; i < n_open; i += kWarps) {
       const int c = open[i], page = ld_in(a.page_table + (size_t)info.x * a.max_blocks + c);
       const float t0 = fmaf(err_q, ld_in(am + c), kTiny), margin = t0 < 1e30f ? t0 : INFINITY;
       double t = -INFINITY;
-      if (page >= 0 && page < a.num_pages) t = exact_max(a.k_idx + (size_t)page * 128 * 64, q, margin, lane);
+      const float kmax = ld_in(am + c);
+      if (page < 0 || page >= a.num_pages) t = -INFINITY;  // (reported)
+      else if ((qmax == 0.f || kmax == 0.f) && qmax < INFINITY && kmax < INFINITY) t = 0.;  // nothing but zeros
+      else t = exact_max(a.k_idx + (size_t)page * 128 * 64, q, margin, qmax, kmax, lane);
       if (lane == 0) score[i] = t;
     }
     __syncthreads();
@@ -445,13 +485,14 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
       const double t = score[i];
       const int c = open[i];
       int before = 0;
-      for (int j = 0; j < n_open; ++j) before += score[j] > t || (score[j] == t && open[j] < c);
+      for (int j = 0; j < n_open && before < need; ++j) before += score[j] > t || (score[j] == t && open[j] < c);
       if (before < need) atomicOr(&sh.chosen[c / 32], 1u << (c % 32));
     }
   }
   __syncthreads();
   // ascending ids, the own block after them, then -1
-  uint32_t w = tid < 256 ? sh.chosen[tid] : 0;
+  static_assert(kSelItems <= 32, "a thread has a word of the chosen ones");
+  uint32_t w = tid < kThreads * kSelItems / 32 ? sh.chosen[tid] : 0;
   int before = __popc(w);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -467,19 +508,21 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
   for (int i = want + tid; i < a.k; i += kThreads) out[i] = i == want ? n : -1;
 }
 
-// 256 threads where they hold every block (2048): fewer warps to wait for.
-template <int kThreads>
+// As few threads as hold every block with eight each, fewer warps to wait for: 1,200 rows and groups of 40 blocks take
+// 199 us in all with 128 threads, 211 with 256. (One warp, or half the threads with twice the blocks, is slower: a row
+// over 8,192 blocks 72 us with 1,024 threads, 83 with 512, 89 with 256.)
+template <int kThreads, int kSelItems>
 cudaError_t launch_select(const PagedProb& p, const SelectArgs& a, cudaStream_t st) {
   static bool attr[kMaxDevices] = {};
   const int dslot = device_slot();
   if (!attr[dslot]) {
-    cudaError_t e = cudaFuncSetAttribute(paged_select_kernel<kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(paged_select_kernel<kThreads, kSelItems>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kThreads * kSelItems * 12);
     if (e != cudaSuccess) return e;
     attr[dslot] = true;
   }
   count_launches(1);
-  return launch_dependent(paged_select_kernel<kThreads>, p.N * p.G, kThreads, p.max_blocks * 12, st, a);
+  return launch_dependent(paged_select_kernel<kThreads, kSelItems>, p.N * p.G, kThreads, p.max_blocks * 12, st, a);
 }
 
 // The rows alone, where no index scores are wanted and no prefix is shared.
@@ -551,7 +594,9 @@ cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, cons
   b.k = p.k;
   b.num_pages = p.num_pages;
   b.max_blocks = p.max_blocks;
-  return p.max_blocks - 1 > kSelItems * 256 ? launch_select<1024>(p, b, st) : launch_select<256>(p, b, st);
+  const int n = p.max_blocks - 1;
+  if (n <= 256) return launch_select<128, 2>(p, b, st);
+  return n <= 2048 ? launch_select<256, 8>(p, b, st) : launch_select<1024, 8>(p, b, st);
 }
 
 }  // namespace msa

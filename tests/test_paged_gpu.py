@@ -447,6 +447,34 @@ def test_sparse_half_a_million(msa):
     ref.check_attention(b, [0], range(2), O, LSE, lambda r, g: bi[r, g].tolist())
 
 
+@pytest.mark.parametrize("what", ["zero queries", "zero keys", "equal keys", "equal rows, huge", "tiny", "one infinity"])
+def test_selection_of_ties_everywhere(msa, what):
+    """Every block undecided by fp32 (a dummy batch, one token over and over): the lower ids, and what differs by a bit."""
+    import torch
+
+    b = ref.Batch(counts=[1, 2], lens=[128 * 300 + 5, 128 * 41], Hq=2, G=2, seed=31)
+    if what == "zero queries":
+        b.q_idx[:] = 0
+    elif what == "zero keys":
+        b.k_idx[:] = 0
+    elif what == "equal keys":
+        b.k_idx[:] = torch.randn(64, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    elif what == "equal rows, huge":
+        b.k_idx[:] = (torch.randn(64, generator=torch.Generator().manual_seed(3)) * 2.0 ** 70).to(torch.bfloat16)
+        b.q_idx *= 2.0 ** 30
+    elif what == "tiny":
+        b.k_idx[:] = (torch.randn(64, generator=torch.Generator().manual_seed(3)) * 2.0 ** -70).to(torch.bfloat16)
+    else:
+        b.k_idx[:] = 1.0
+        b.k_idx[int(b.table[0, 250]), 3, 7] = INF
+        b.q_idx[:, :, 7] = b.q_idx[:, :, 7].abs() + 1
+    if what != "zero keys":
+        b.k_idx[int(b.table[1, 33]), 9] *= 1.5  # one key of one block
+    O, LSE, bi = _sparse(msa, b, 16)
+    for r in range(b.n):
+        np.testing.assert_array_equal(bi[r], ref.select(b, r, 16))
+
+
 def test_dense_large_scores(msa):
     """Scores whose maximum moves by far more than exp2's range from page to page."""
     b = ref.Batch(counts=[2, 1, 1], lens=[128 * 6 + 90, 128 * 7, 128 * 6 + 1], Hq=8, G=2, prefix=4, seed=9)
