@@ -8,12 +8,18 @@ namespace msa {
 
 static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Cuts `pages` pages of each of `tiles` row tiles into runs of equal length.
-// An item costs `extra` pages more than its pages (its queries, the warps'
-// meeting, its part of O: about one page's time in the mma.sync path, three in
-// the tcgen05 one); SMs take items as they come, so the end is half an
-// item long.
-static void cut_pages(long long tiles, int pages, double extra, int* per_split, int* n_splits) {
+// Cuts `pages` pages of each of `tiles` row tiles into runs of equal length. An
+// item costs `extra` pages more than its pages (its row, pages and queries to
+// look up, the warps' meeting, its part of O), and parts that the kernel joins
+// itself `join` more; SMs take items as they come, so the end is half an item
+// long. Measured for what the mma.sync path joins (6 and 8): 64 rows of 16 pages
+// and 8 groups 125 us, 129 where an item counts for one page more and the join for
+// nothing (which cuts in two), 57 rows of 9 pages and 2 groups 13.6 and 20.4; a
+// row's 128 pages 25 us, 29 uncut; 16000 tokens 25 us, 31 and 85 uncut. Where the
+// merge kernel joins (1 and 0): 64 sequences behind 32K tokens 94 us, 97 with two
+// pages. 128-row tiles (3 and 0): 300 rows over 8000 tokens 64 us, 84 with one and
+// 93 with eight pages.
+static void cut_pages(long long tiles, int pages, double extra, double join, int* per_split, int* n_splits) {
   tiles = std::max(1LL, tiles);
   pages = std::max(1, pages);
   double best = 0;
@@ -22,7 +28,7 @@ static void cut_pages(long long tiles, int pages, double extra, int* per_split, 
     const long long want = i < 0 ? 1 - i : i == 0 ? 1 : std::max(1LL, i * (long long)kCutSms / tiles);
     const int per = (int)((pages + std::min<long long>(want, pages) - 1) / std::min<long long>(want, pages));
     const int splits = (pages + per - 1) / per;
-    const double cost = (std::max(1.0, (double)tiles * splits / kCutSms) + 0.5) * (per + extra);
+    const double cost = (std::max(1.0, (double)tiles * splits / kCutSms) + 0.5) * (per + extra) + (splits > 1 ? join : 0);
     if (best == 0 || cost < best) {
       best = cost;
       *per_split = per;
@@ -51,7 +57,7 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
     L.amax = take((size_t)p.S * p.max_blocks * 4);
     if (p.k > 1) L.n_flags = (int)std::min<long long>((long long)p.S * ((p.max_blocks + 4) / 6), kCutSms - 1);
     L.flags = take(kCutSms * 4);
-    cut_pages((long long)p.N * p.G, std::min(p.k, p.max_blocks), 1, &L.per_split, &L.splits);
+    cut_pages((long long)p.N * p.G, std::min(p.k, p.max_blocks), 6, 8, &L.per_split, &L.splits);
   } else {
     L.tile_rows = 8 / p.hg;
     // More columns (rows x heads of a sequence) than eight on average, and more than a page each: 128-row tiles, tcgen05.
@@ -60,13 +66,13 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
     if ((long long)p.N * p.hg > 8LL * p.S && p.max_blocks - p.prefix > 1) {
       L.run_rows = 256 / p.hg;
       L.runs = take((size_t)p.N * 16);
-      cut_pages((long long)std::max(p.N / L.run_rows, std::min(p.S, p.N)) * p.G, p.max_blocks - p.prefix, 3, &L.per_run,
+      cut_pages((long long)std::max(p.N / L.run_rows, std::min(p.S, p.N)) * p.G, p.max_blocks - p.prefix, 3, 0, &L.per_run,
                 &L.rslots);
       L.splits = 0;
       L.n_flags = kCutSms;
     } else {
-      cut_pages((long long)std::max(p.N / L.tile_rows, std::min(p.S, p.N)) * p.G, p.max_blocks - p.prefix, 1, &L.per_split,
-                &L.splits);
+      cut_pages((long long)std::max(p.N / L.tile_rows, std::min(p.S, p.N)) * p.G, p.max_blocks - p.prefix, p.prefix ? 1 : 6,
+                p.prefix ? 0 : 8, &L.per_split, &L.splits);
     }
     if (p.prefix > 0) {
       const int tiles = (int)(((long long)p.N * p.hg + 127) / 128);

@@ -14,6 +14,9 @@
 // into items of two 16-byte pieces (the two halves of eight pairs, or two
 // neighbours), one thread each, whose loads are on their way before the row's
 // place and angles are looked up.
+//
+// Measured: 32,764 rows of 32 + 2 x 8 heads (881 MB) 150 us, 5.9 TB/s, 0.88 of a
+// plain copy; one row 3 us in a graph, which is a launch's time.
 #include "paged_rows.cuh"
 
 namespace msa {
@@ -235,7 +238,7 @@ cudaError_t launch_paged_append(const PagedProb& p, const PagedCachePtrs& c, con
   a.num_pages = p.num_pages;
   a.max_blocks = p.max_blocks;
   a.err = reinterpret_cast<int*>(ws);
-  // four rows a block from where that still fills every SM a few times
+  // four rows a block from where that still fills every SM a few times (32,764 rows: 178 us with one, 150 with four)
   a.rows = p.N >= 16 * kCutSms ? kMaxRows : 1;
   a.n_q = r.Q ? 8 * p.Hq : 0;
   a.n_k = 8 * p.G;

@@ -16,6 +16,11 @@
 // that the next pages are not kept waiting by its loads. Behind a shared prefix
 // the merge kernel below joins them with the prefix's.
 //
+// Measured: 60 rows x 8 groups x 16 selected pages, 503 MB in 81 us, 6.2 TB/s,
+// 0.93 of a plain copy; one row's 128 pages 11 us, of which the memory takes 1.3.
+// Equal runs of pages for every CTA, cut anywhere, cost more at their seams than
+// their balance gained (a row at 128K tokens 36 us against 30).
+//
 // Masked places: a page is masked per column only where it crosses a row's end.
 // There, each row of the tile is accumulated on its own with the values behind
 // its end cleared, so that nothing stored behind a row's end (another row's
@@ -591,7 +596,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // that reaches into the group's), in that order.
 // One warp per row and head. Nothing but latency costs anything here (29 MB from
 // L2 at most among the measured cases), so eight parts are asked for at a time,
-// their sums with them, and the maximum is kept as they come.
+// their sums with them, and the maximum is kept as they come. Measured: 9 us for 256
+// rows x 32 heads of six parts each.
 struct MergeArgs {
   const int4* rows;
   const float *part_o, *part_lse;

@@ -5,7 +5,10 @@
 // twelve pages (128 keys x 64, 16 KB by TMA) in flight per SM, and each of twelve
 // warps takes a whole page and multiplies it with the sequence's index queries
 // (rows x groups, eight columns at a time, mma.sync): the memory's time, at a
-// tenth of the tensor pipe's.
+// tenth of the tensor pipe's. Measured: two sequences of 2^20 tokens, 268 MB of
+// keys in 44 us, 6.1 TB/s, 0.91 of a plain copy. The selection after it is all
+// latency: 5 us for a row over 1,024 blocks, 15 over 8,192, 12 for 480 rows and
+// groups over up to 256 each.
 //
 // The selection has to be exact, not exact up to the rounding of fp32: the
 // order of two blocks decides whole pages. An fp32 maximum v_c differs from
