@@ -520,7 +520,7 @@ cudaError_t launch_select(const PagedProb& p, const SelectArgs& a, cudaStream_t 
   const int dslot = device_slot();
   if (!attr[dslot]) {
     cudaError_t e = cudaFuncSetAttribute(paged_select_kernel<kThreads, kSelItems>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kThreads * kSelItems * 12);
+                                         (kThreads * kSelItems + 1) * 12);
     if (e != cudaSuccess) return e;
     attr[dslot] = true;
   }

@@ -439,6 +439,121 @@ def test_sparse_whole_rows_many(msa):
     ref.check_attention(b, [0, 5, 1599], range(2), O, LSE, lambda r, g: bi[r, g].tolist())
 
 
+@pytest.mark.parametrize("blocks", [256, 257, 258, 2049, 2050])
+def test_selection_threads_change(msa, blocks):
+    """Page tables of the widths around which the selection's block of threads grows."""
+    b = ref.Batch(counts=[1, 1], lens=[128 * blocks, 128 * (blocks - 1) + 1], Hq=1, G=1, seed=19)
+    assert b.max_blocks == blocks
+    O, LSE, bi = _sparse(msa, b, 7)
+    for r in range(2):
+        np.testing.assert_array_equal(bi[r], ref.select(b, r, 7))
+    ref.check_attention(b, range(2), range(1), O, LSE, lambda r, g: bi[r, g].tolist())
+
+
+@pytest.mark.parametrize("Hq,pad,prefix", [(16, 4, 0), (16, 4, 2), (2, 1, 2), (2, 1, 0)], ids=str)
+def test_batch_without_rows(msa, Hq, pad, prefix):
+    """Idle slots and padded rows only: outputs and pools as they were."""
+    import torch
+
+    b = ref.Batch(counts=[0, 0, 0], lens=[0, 300, 128 * 5], Hq=Hq, G=2, pad=pad, prefix=prefix, seed=3)
+    O, LSE = _dense(msa, b)
+    assert bool((O == 5).all()) and bool((LSE == 5).all())
+    O, LSE, bi = _sparse(msa, b, 3)
+    assert bool((O == 5).all()) and bool((LSE == 5).all()) and bool((bi == -7).all())
+    shape, cache, t = b.gpu()
+    before = t["K"].clone().view(torch.int16)
+    ws = msa.alloc_paged_workspace(shape, msa.MSA_WS_PAGED_APPEND)
+    new = torch.ones(b.N, 2, 128, dtype=torch.bfloat16, device="cuda")
+    msa.paged_append(shape, cache, msa.Rope(), new, new, workspace=ws)
+    msa.msa_check_device_status(ws)
+    assert torch.equal(t["K"].view(torch.int16), before)
+
+
+@pytest.mark.parametrize("S,rows", [(5000, 1), (2500, 2)], ids=str)
+def test_prefix_of_more_rows_than_a_wave(msa, S, rows):
+    """More pairs of row tiles than SMs."""
+    b = _shared_pages(S, rows, 128 * 4 + 9, 8, 1)
+    b.prefix = 2
+    O, LSE = _dense(msa, b)
+    some = [0, 1, 31, 32, 2047, 4865, b.n - 1]
+    ref.check_attention(b, some, range(0, 8, 3), O, LSE, _all(b), bf16_p=True)
+
+
+def test_dense_rows_bad_batches(msa):
+    """Several rows per sequence: faults of one sequence are reported and leave the others alone."""
+    import torch
+
+    def run(change, good, prefix=0):
+        b = ref.Batch(counts=[3, 4, 20], lens=[128 * 5 + 2, 128 * 6 + 9, 128 * 4 + 60], Hq=16, G=2, prefix=prefix, seed=1)
+        change(b)
+        shape, cache, t = b.gpu()
+        ws = msa.alloc_paged_workspace(shape, msa.MSA_WS_PAGED_DENSE)
+        ws.fill_(255)
+        O, LSE = msa.paged_dense_attn(shape, cache, t["Q"], workspace=ws)
+        with pytest.raises(msa.MsaError) as e:
+            msa.msa_check_device_status(ws)
+        assert e.value.status == msa.MSA_ERR_DEVICE
+        ref.check_attention(b, good, range(0, 16, 5), O.cpu(), LSE.cpu(), _all(b), bf16_p=prefix > 0)
+
+    def page(s, c, v):
+        return lambda b: b.table.__setitem__((s, c), v)
+
+    def length(s, v):
+        return lambda b: b.lens.__setitem__(s, v)
+
+    for v in (-1, 1 << 20, 2 ** 31 - 1, -2 ** 31):
+        run(page(0, 5, v), [3, 6, 7, 26])
+        run(page(0, 2, v), [3, 6, 7, 26])
+        run(page(2, 4, v), [0, 2, 3, 6], prefix=2)
+    for v in (0, -5, 2, 128 * 7 + 1, 2 ** 31 - 1, -2 ** 31):
+        run(length(1, v), [0, 2, 7, 26])
+        run(length(1, v), [0, 2, 7, 26], prefix=2)
+    run(lambda b: b.table.__setitem__((1, 1), b.table[1, 3]), [], prefix=2)  # a prefix that is not shared
+
+
+def test_dense_rows_same_bits(msa):
+    """Again, on another stream beside another call, and from a graph that is replayed on another batch."""
+    import torch
+
+    args = dict(counts=[5, 0, 33, 2, 9], Hq=16, G=2, prefix=2, pad=2)
+    b = ref.Batch(lens=[128 * 5 + 9, 0, 128 * 3 + 40, 128 * 9, 128 * 12 + 77], seed=4, **args)
+    want = _dense(msa, b)
+    shape, cache, t = b.gpu()
+    ws = [msa.alloc_paged_workspace(shape, msa.MSA_WS_PAGED_DENSE) for _ in range(2)]
+    out = [(torch.full_like(t["Q"], 5.0), torch.full((b.N, b.Hq), 5.0, device="cuda")) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for w, (O, LSE), s in zip(ws, out, streams):
+            msa.msa_paged_dense_attn(shape, cache, t["Q"], O, LSE, w, s)
+    torch.cuda.synchronize()
+    for w, (O, LSE) in zip(ws, out):
+        msa.msa_check_device_status(w)
+        assert torch.equal(O[:b.n].cpu(), want[0][:b.n]) and torch.equal(LSE[:b.n].cpu(), want[1][:b.n])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        msa.msa_paged_dense_attn(shape, cache, t["Q"], *out[0], ws[0])
+        msa.msa_paged_dense_attn(shape, cache, t["Q"], *out[1], ws[0])
+    # other rows of the same shape: fewer, elsewhere
+    counts, lens = [1, 20, 0, 18, 10], [128 * 4, 128 * 3 + 20, 7, 128 * 8 + 99, 128 * 12 + 1]
+    starts = np.cumsum([0] + counts)
+    cache.row_start.copy_(torch.tensor(starts, dtype=torch.int32))
+    cache.seq_len.copy_(torch.tensor(lens, dtype=torch.int32))
+    table = b.table.clone()
+    table[1, :4] = torch.tensor([int(table[0, 0]), int(table[0, 1]), int(table[4, 5]), int(table[4, 6])])
+    cache.page_table.copy_(table)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    msa.msa_check_device_status(ws[0])
+    b.table, b.lens, b.counts, b.n = table, lens, counts, int(starts[-1])
+    b.row_seq = [i for i, c in enumerate(counts) for _ in range(c)]
+    b.row_pos = [x - c + j for c, x in zip(counts, lens) for j in range(c)]
+    for O, LSE in out:
+        ref.check_attention(b, range(0, b.n, 2), range(0, 16, 5), O.cpu(), LSE.cpu(), _all(b), bf16_p=True)
+    assert torch.equal(out[0][0][:b.n], out[1][0][:b.n])
+
+
 def test_sparse_half_a_million(msa):
     """More blocks than the selection's smaller block of threads holds."""
     b = ref.Batch(counts=[1], lens=[(1 << 19) - 3], Hq=2, G=1, seed=18)
