@@ -62,6 +62,11 @@ struct PagedCachePtrs {
   const int32_t *page_table, *row_start, *seq_len;
 };
 
+// Tensor maps over the K and V pools as rows of 128 values: boxes of 64 columns x 128 rows (half a page of one group).
+struct PoolMaps {
+  CUtensorMap k, v;
+};
+
 struct RopeRows {
   const void *Q, *K, *V, *q_idx, *k_idx;
   long long ld_Q, ld_K, ld_V, ld_q_idx, ld_k_idx;  // elements between consecutive rows
@@ -79,16 +84,14 @@ cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, cons
                                uint8_t* ws, const PagedWs& L, cudaStream_t st);
 // Attention of every new row over its selected pages (block_idx) or, with
 // block_idx null, over its sequence's pages behind the shared prefix.
-cudaError_t launch_paged_attn(const PagedProb& p, const PagedCachePtrs& c, const void* Q, const int32_t* block_idx,
-                              void* O, float* LSE, uint8_t* ws, const PagedWs& L, cudaStream_t st);
+cudaError_t launch_paged_attn(const PagedProb& p, const PagedCachePtrs& c, const PoolMaps& maps, const void* Q,
+                              const int32_t* block_idx, void* O, float* LSE, uint8_t* ws, const PagedWs& L, cudaStream_t st);
 // Shared prefix, and runs of the sequences' own pages. The attention kernel may start while it still runs.
-cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, const void* Q, uint8_t* ws,
-                                const PagedWs& L, cudaStream_t st);
+cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, const PoolMaps& maps, const void* Q,
+                                uint8_t* ws, const PagedWs& L, cudaStream_t st);
 // Joins the parts of the shared prefix and of the own pages (without a prefix the attention does).
 cudaError_t launch_paged_merge(const PagedProb& p, void* O, float* LSE, uint8_t* ws, const PagedWs& L,
                                cudaStream_t st);
 
-// Tensor map over a K or V pool as rows of 128 values: box of 64 columns x 128 rows (half a page of one group).
-bool encode_pool_map(CUtensorMap* m, const PagedProb& p, void* pool);
 
 }  // namespace msa

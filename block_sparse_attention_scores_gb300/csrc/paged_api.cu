@@ -155,6 +155,16 @@ static msa_status check_cache(const msa_paged_cache* c, bool index, PagedCachePt
   return MSA_OK;
 }
 
+static msa_status encode_pools(const PagedProb& p, const PagedCachePtrs& c, PoolMaps* m) {
+  const uint64_t dims[2] = {128, (uint64_t)p.num_pages * p.G * 128};
+  const uint64_t strides[1] = {256};
+  const uint32_t box[2] = {64, 128};
+  if (encode_tmap(&m->k, c.K, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
+      encode_tmap(&m->v, c.V, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+    return MSA_OK;
+  return fail(MSA_ERR_CUDA, "tensor maps of the pools could not be encoded");
+}
+
 static msa_status check_paged_ws(const PagedProb& p, int which, void* ws, size_t bytes, PagedWs* L) {
   *L = paged_ws_layout(p, which);
   if (!ws) return fail(MSA_ERR_WORKSPACE, "workspace is NULL");
@@ -267,11 +277,13 @@ msa_status msa_paged_sparse_attn(const msa_paged_shape* shape, const msa_paged_c
   if ((s = check_device()) != MSA_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(workspace);
+  PoolMaps maps;
+  if ((s = encode_pools(p, c, &maps)) != MSA_OK) return s;
   if (!q_idx) L.n_flags = 0;
   if ((s = cuda_status(q_idx ? launch_paged_index(p, c, q_idx, block_idx, w, L, st) : launch_paged_rows(p, c, w, L, st),
                        "paged index launch")) != MSA_OK)
     return s;
-  return cuda_status(launch_paged_attn(p, c, Q, block_idx, O, LSE, w, L, st), "paged attention launch");
+  return cuda_status(launch_paged_attn(p, c, maps, Q, block_idx, O, LSE, w, L, st), "paged attention launch");
 }
 
 msa_status msa_paged_dense_attn(const msa_paged_shape* shape, const msa_paged_cache* cache, const void* Q, void* O,
@@ -289,11 +301,13 @@ msa_status msa_paged_dense_attn(const msa_paged_shape* shape, const msa_paged_ca
   if ((s = check_device()) != MSA_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(workspace);
+  PoolMaps maps;
+  if ((s = encode_pools(p, c, &maps)) != MSA_OK) return s;
   const bool parts = p.prefix || L.run_rows;
   if ((s = cuda_status(launch_paged_rows(p, c, w, L, st), "paged rows launch")) != MSA_OK) return s;
-  if (parts && (s = cuda_status(launch_paged_prefix(p, c, Q, w, L, st), "paged prefix launch")) != MSA_OK) return s;
+  if (parts && (s = cuda_status(launch_paged_prefix(p, c, maps, Q, w, L, st), "paged prefix launch")) != MSA_OK) return s;
   if (!L.run_rows &&
-      (s = cuda_status(launch_paged_attn(p, c, Q, nullptr, O, LSE, w, L, st), "paged attention launch")) != MSA_OK)
+      (s = cuda_status(launch_paged_attn(p, c, maps, Q, nullptr, O, LSE, w, L, st), "paged attention launch")) != MSA_OK)
     return s;
   return parts ? cuda_status(launch_paged_merge(p, O, LSE, w, L, st), "paged merge launch") : MSA_OK;
 }

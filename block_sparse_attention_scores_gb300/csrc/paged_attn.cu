@@ -681,17 +681,9 @@ cudaError_t launch_attn(const AttnArgs& a, const CUtensorMap& mk, const CUtensor
 
 }  // namespace
 
-bool encode_pool_map(CUtensorMap* m, const PagedProb& p, void* pool) {
-  const uint64_t dims[2] = {128, (uint64_t)p.num_pages * p.G * 128};
-  const uint64_t strides[1] = {256};
-  const uint32_t box[2] = {64, 128};
-  return encode_tmap(m, pool, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-cudaError_t launch_paged_attn(const PagedProb& p, const PagedCachePtrs& c, const void* Q, const int32_t* block_idx,
-                              void* O, float* LSE, uint8_t* ws, const PagedWs& L, cudaStream_t st) {
-  CUtensorMap mk, mv;
-  if (!encode_pool_map(&mk, p, c.K) || !encode_pool_map(&mv, p, c.V)) return cudaErrorInvalidValue;
+cudaError_t launch_paged_attn(const PagedProb& p, const PagedCachePtrs& c, const PoolMaps& maps, const void* Q,
+                              const int32_t* block_idx, void* O, float* LSE, uint8_t* ws, const PagedWs& L,
+                              cudaStream_t st) {
   AttnArgs a;
   a.rows = reinterpret_cast<const int4*>(ws + L.rows);
   a.lead = L.tile_rows > 1 ? reinterpret_cast<const int4*>(ws + L.lead) : nullptr;
@@ -724,7 +716,7 @@ cudaError_t launch_paged_attn(const PagedProb& p, const PagedCachePtrs& c, const
   a.beside = L.pslots > 0;
   a.n_flags = a.beside ? 0 : L.n_flags;
   a.err = reinterpret_cast<int*>(ws);
-  return launch_attn(a, mk, mv, st);
+  return launch_attn(a, maps.k, maps.v, st);
 }
 
 cudaError_t launch_paged_merge(const PagedProb& p, void* O, float* LSE, uint8_t* ws, const PagedWs& L,

@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_release();  // (not before: the kernel that starts on the SMs left over reads what the one before this wrote)
   // the first sequence with rows: its table holds the shared pages
-  const int ref = find_sequence(a.row_start, a.S, 0, lane);
+  const int ref = a.prefix ? find_sequence(a.row_start, a.S, 0, lane) : a.S;
   int* const err = &sh.flag;
   if (ref >= a.S) u_begin = u_end;  // no rows at all
   const uint32_t tmem = sh.tmem_base;  // S_0 [0,128), S_1 [128,256), O_0 [256,384), O_1 [384,512)
@@ -731,8 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool kRuns>
-cudaError_t launch_prefix(const PrefixArgs& a, int blocks, const CUtensorMap& mq, const CUtensorMap& mk,
-                          const CUtensorMap& mv, cudaStream_t st) {
+cudaError_t launch_prefix(const PrefixArgs& a, int blocks, const CUtensorMap& mq, const PoolMaps& maps, cudaStream_t st) {
   static bool attr[kMaxDevices] = {};
   const int dslot = device_slot();
   if (!attr[dslot]) {
@@ -741,14 +740,14 @@ cudaError_t launch_prefix(const PrefixArgs& a, int blocks, const CUtensorMap& mq
     attr[dslot] = true;
   }
   count_launches(1);
-  return launch_dependent(paged_prefix_kernel<kRuns>, blocks, kThreads, kSmem, st, a, mq, mk, mv);
+  return launch_dependent(paged_prefix_kernel<kRuns>, blocks, kThreads, kSmem, st, a, mq, maps.k, maps.v);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, const void* Q, uint8_t* ws,
-                                const PagedWs& L, cudaStream_t st) {
-  CUtensorMap mq, mk, mv;
+cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, const PoolMaps& maps, const void* Q,
+                                uint8_t* ws, const PagedWs& L, cudaStream_t st) {
+  CUtensorMap mq;
   {
     // a tile's rows times the heads of one group: box {64 d, h_g heads, 128 / h_g rows}
     const uint64_t dims[3] = {128, (uint64_t)p.Hq, (uint64_t)p.N};
@@ -757,7 +756,6 @@ cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, con
     if (!encode_tmap(&mq, const_cast<void*>(Q), 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
-  if (!encode_pool_map(&mk, p, c.K) || !encode_pool_map(&mv, p, c.V)) return cudaErrorInvalidValue;
   PrefixArgs a;
   a.flags = reinterpret_cast<int*>(ws + L.flags);
   a.page_table = c.page_table;
@@ -782,7 +780,7 @@ cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, con
   a.per_run = L.per_run;
   a.rslots = L.rslots;
   a.pslots = L.pslots;
-  return L.run_rows ? launch_prefix<true>(a, L.n_flags, mq, mk, mv, st) : launch_prefix<false>(a, L.n_flags, mq, mk, mv, st);
+  return L.run_rows ? launch_prefix<true>(a, L.n_flags, mq, maps, st) : launch_prefix<false>(a, L.n_flags, mq, maps, st);
 }
 
 }  // namespace msa
