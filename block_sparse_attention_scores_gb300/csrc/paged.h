@@ -31,8 +31,7 @@ struct PagedWs {
   size_t flags = 0;     // int32 [n_flags] what the blocks of the index scores or of the shared prefix found wrong
   int n_flags = 0;      // those blocks
   size_t arrived = 0;   // int32 [N, G, 3] parts of a (row tile, group) that are done, as each joining warp counts them
-  size_t pooled = 0;    // fp32 [N, G, max_blocks] block maxima of the index scores
-  size_t amax = 0;      // fp32 [S, max_blocks]    largest |index key| value of a block
+  size_t pooled = 0;    // fp32 [N, G, max_blocks, 2] block maxima of the index scores, and the block's largest |key| value
   size_t part_o = 0;    // fp32 [pslots + rslots or splits, N, Hq, d] partial outputs (normalised)
   size_t part_lse = 0;  // fp32 [pslots + rslots or splits, N, Hq]    their log2-sum-exp2
   size_t total = 256;

@@ -53,8 +53,7 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
   L.lead = take((size_t)p.N * 16);
   L.arrived = take((size_t)p.N * p.G * 12);
   if (which == MSA_WS_PAGED_SPARSE) {
-    L.pooled = take((size_t)p.N * p.G * p.max_blocks * 4);
-    L.amax = take((size_t)p.S * p.max_blocks * 4);
+    L.pooled = take((size_t)p.N * p.G * p.max_blocks * 8);
     if (p.k > 1) L.n_flags = (int)std::min<long long>((long long)p.S * ((p.max_blocks + 4) / 6), kCutSms - 1);
     L.flags = take(kCutSms * 4);
     cut_pages((long long)p.N * p.G, std::min(p.k, p.max_blocks), 6, 8, &L.per_split, &L.splits);

@@ -42,7 +42,7 @@ constexpr int kScoreBatch = 5;  // items whose description is fetched at once (a
 struct ScoreArgs {
   const __nv_bfloat16* q_idx;
   const int32_t *page_table, *row_start, *seq_len;
-  float *pooled, *amax;
+  float2* pooled;
   int S, N, G, num_pages, max_blocks, runs, items;
   int* flags;  // [blocks but the last] what a block found wrong
   RowsArgs rows;
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       const int c = bad ? ~info.y : info.y, cols = info.w;
       const uint32_t base = smem_u32(smem + st * kScorePage);
       const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q_idx + (size_t)info.z * a.G * 64);
-      uint32_t top = 0;  // largest magnitude, two bf16 at a time
+      uint32_t top = 0;  // largest magnitude, two bf16 at a time (after the first columns: of all)
       for (int n0 = 0; n0 < cols; n0 += 8) {
         uint32_t b[4][2];  // queries' column n0 + r, dims 16 ks + 2 q, + 1 and + 8, + 9
 #pragma unroll
@@ -188,16 +188,16 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
           best0 = fmaxf(best0, __shfl_xor_sync(0xffffffffu, best0, o));
           best1 = fmaxf(best1, __shfl_xor_sync(0xffffffffu, best1, o));
         }
+        if (n0 == 0) top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16)) << 16;
         if (r == 0) {
           const size_t col = (size_t)info.z * a.G + n0 + 2 * q;
-          if (n0 + 2 * q < cols) a.pooled[col * a.max_blocks + c] = bad ? -INFINITY : best0;
-          if (n0 + 2 * q + 1 < cols) a.pooled[(col + 1) * a.max_blocks + c] = bad ? -INFINITY : best1;
+          if (n0 + 2 * q < cols) a.pooled[col * a.max_blocks + c] = make_float2(bad ? -INFINITY : best0, __uint_as_float(top));
+          if (n0 + 2 * q + 1 < cols) 
+            a.pooled[(col + 1) * a.max_blocks + c] = make_float2(bad ? -INFINITY : best1, __uint_as_float(top));
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.empty[st]);
-      top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-      if (lane == 0) a.amax[(size_t)info.x * a.max_blocks + c] = __uint_as_float(top << 16);
     }
   }
   __syncthreads();
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
 // ---------------------------------------------------------------------------
 struct SelectArgs {
   const int4* rows;
-  const float *pooled, *amax;
+  const float2* pooled;
   const __nv_bfloat16 *q_idx, *k_idx;
   const int32_t* page_table;
   int32_t* block_idx;
@@ -330,6 +330,15 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
   const int rg = blockIdx.x, row = rg / a.G, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const __nv_bfloat16* q = a.q_idx + (size_t)rg * 64;
   const uint32_t qq = ld_in(reinterpret_cast<const uint32_t*>(q) + lane);
+  const float2* v = a.pooled + (size_t)rg * a.max_blocks;
+  float x[kSelItems], e[kSelItems];
+#pragma unroll
+  for (int z = 0; z < kSelItems; ++z) {  // (before it is known how many of them there are)
+    const int i = z * kThreads + tid;
+    const float2 f = i < a.max_blocks ? ld_in(v + i) : make_float2(-INFINITY, 0.f);
+    x[z] = f.x;
+    e[z] = f.y;
+  }
   const int4 info = ld_in(a.rows + row);
   if (info.x < 0) return;
   const int n = info.y / 128;  // earlier blocks
@@ -345,16 +354,7 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
   }
   double* score = reinterpret_cast<double*>(dyn);               // [n] of the open blocks
   int* open = reinterpret_cast<int*>(score + a.max_blocks);     // [n]
-  const float* v = a.pooled + (size_t)rg * a.max_blocks;
-  const float* am = a.amax + (size_t)info.x * a.max_blocks;
 
-  float x[kSelItems], e[kSelItems];
-#pragma unroll
-  for (int z = 0; z < kSelItems; ++z) {
-    const int i = z * kThreads + tid;
-    x[z] = i < n ? ld_in(v + i) : -INFINITY;
-    e[z] = i < n ? ld_in(am + i) : 0.f;
-  }
   if (tid == 0) sh.n_in = sh.n_open = 0;
   for (int i = tid; i < kThreads * kSelItems / 32; i += kThreads) sh.chosen[i] = 0;
   float l1 = fabsf(lo_f(qq)) + fabsf(hi_f(qq));  // |q|_1
@@ -366,6 +366,8 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
   float emax = 0.f;
 #pragma unroll
   for (int z = 0; z < kSelItems; ++z) {
+    key[z] = 0u;
+    if (z * kThreads >= n) continue;
     const bool in = z * kThreads + tid < n;
     const float t = fmaf(err_q, e[z], kTiny);
     e[z] = t < 1e30f ? t : INFINITY;  // not finite, or so large that fp32 may have overflowed: undecided
@@ -378,20 +380,16 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
   }
   kmax = __reduce_max_sync(0xffffffffu, kmax);
   kmin = __reduce_min_sync(0xffffffffu, kmin);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) emax = fmaxf(emax, __shfl_xor_sync(0xffffffffu, emax, o));
+  emax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(emax)));  // (not negative)
   if (lane == 0) {
     sh.kmax[warp] = kmax;
     sh.kmin[warp] = kmin;
     sh.emax[warp] = emax;
   }
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    kmax = max(kmax, sh.kmax[i]);
-    kmin = min(kmin, sh.kmin[i]);
-    emax = fmaxf(emax, sh.emax[i]);
-  }
+  kmax = __reduce_max_sync(0xffffffffu, lane < kWarps ? sh.kmax[lane] : 0u);
+  kmin = __reduce_min_sync(0xffffffffu, lane < kWarps ? sh.kmin[lane] : 0xffffffffu);
+  emax = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < kWarps ? __float_as_uint(sh.emax[lane]) : 0u));
 
   // A threshold that `want` keys reach: lo is reached by enough, hi + 1 by too few; three probes a step.
   uint32_t lo = kmin, hi = kmax;
@@ -400,6 +398,7 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
     uint32_t c12 = 0, c3 = 0;  // counts of t1 (low half), t2 (high half), t3
 #pragma unroll
     for (int z = 0; z < kSelItems; ++z) {
+      if (z * kThreads >= n) break;
       c12 += (key[z] >= t1 ? 1u : 0u) + (key[z] >= t2 ? 0x10000u : 0u);
       c3 += key[z] >= t3 ? 1u : 0u;
     }
@@ -475,12 +474,11 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
     for (int o = 16; o; o >>= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, o));
     for (int i = warp; i < n_open; i += kWarps) {
       const int c = open[i], page = ld_in(a.page_table + (size_t)info.x * a.max_blocks + c);
-      const float t0 = fmaf(err_q, ld_in(am + c), kTiny), margin = t0 < 1e30f ? t0 : INFINITY;
+      const float top = ld_in(v + c).y, t0 = fmaf(err_q, top, kTiny), margin = t0 < 1e30f ? t0 : INFINITY;
       double t = -INFINITY;
-      const float kmax = ld_in(am + c);
       if (page < 0 || page >= a.num_pages) t = -INFINITY;  // (reported)
-      else if ((qmax == 0.f || kmax == 0.f) && qmax < INFINITY && kmax < INFINITY) t = 0.;  // nothing but zeros
-      else t = exact_max(a.k_idx + (size_t)page * 128 * 64, q, margin, qmax, kmax, lane);
+      else if ((qmax == 0.f || top == 0.f) && qmax < INFINITY && top < INFINITY) t = 0.;  // nothing but zeros
+      else t = exact_max(a.k_idx + (size_t)page * 128 * 64, q, margin, qmax, top, lane);
       if (lane == 0) score[i] = t;
     }
     __syncthreads();
@@ -504,8 +502,7 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
   }
   if (lane == 31) sh.scan[warp] = before;
   __syncthreads();
-  before -= __popc(w);
-  for (int i = 0; i < warp; ++i) before += sh.scan[i];
+  before += (int)__reduce_add_sync(0xffffffffu, lane < warp ? (uint32_t)sh.scan[lane] : 0u) - __popc(w);
   for (; w; w &= w - 1, ++before)
     if (before < want) out[before] = tid * 32 + __ffs(w) - 1;
   for (int i = want + tid; i < a.k; i += kThreads) out[i] = i == want ? n : -1;
@@ -553,8 +550,7 @@ cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, cons
   a.page_table = c.page_table;
   a.row_start = c.row_start;
   a.seq_len = c.seq_len;
-  a.pooled = reinterpret_cast<float*>(ws + L.pooled);
-  a.amax = reinterpret_cast<float*>(ws + L.amax);
+  a.pooled = reinterpret_cast<float2*>(ws + L.pooled);
   a.S = p.S;
   a.N = p.N;
   a.G = p.G;
@@ -588,7 +584,6 @@ cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, cons
   SelectArgs b;
   b.rows = reinterpret_cast<const int4*>(ws + L.rows);
   b.pooled = a.pooled;
-  b.amax = a.amax;
   b.q_idx = a.q_idx;
   b.k_idx = static_cast<const __nv_bfloat16*>(c.k_idx);
   b.page_table = c.page_table;

@@ -26,6 +26,11 @@ __device__ __forceinline__ uint32_t ld_in(const uint32_t* p) { return (uint32_t)
 __device__ __forceinline__ float ld_in(const float* p) {
   return __int_as_float(ld_in(reinterpret_cast<const int*>(p)));
 }
+__device__ __forceinline__ float2 ld_in(const float2* p) {
+  float2 v;
+  asm volatile("ld.global.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p));
+  return v;
+}
 __device__ __forceinline__ uint4 ld_in(const uint4* p) {
   uint4 v;
   asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
