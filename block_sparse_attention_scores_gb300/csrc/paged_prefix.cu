@@ -506,26 +506,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!mbar_wait(&sh.kv_full[st], par, err, 1506)) { ok = false; break; }
           if (page >= run.masked) {
-            const int token0 = (run.first + page) * 128;
+            // 16 lanes per key, 8 dims each: first the rows' own tokens, then what is behind them
+            const int token0 = (run.first + page) * 128, chunk = lane & 15;
+            const int own = max(0, run.pos + 1 - token0), behind = min(128, max(0, run.pos + run.rows - token0));
+            uint8_t* tile = smem + oV + st * kTile + (chunk >> 3) * kChunk;
             bool odd = false;
-            // 16 lanes per key: 8 dims each
-            for (int key = max(0, run.pos + 1 - token0) + lane / 16; key < 128; key += 2) {
-              const int chunk = lane & 15;
-              uint4* at = reinterpret_cast<uint4*>(smem + oV + st * kTile + (chunk >> 3) * kChunk + sw128_off(key, chunk & 7));
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (token0 + key < run.pos + run.rows) {
-                v = *at;
-                bool bad = false;
-                auto check = [&](uint32_t& w) {
-                  if ((w & 0x7f80u) == 0x7f80u) { w &= 0xffff0000u; bad = true; }
-                  if ((w & 0x7f800000u) == 0x7f800000u) { w &= 0xffffu; bad = true; }
-                };
-                check(v.x); check(v.y); check(v.z); check(v.w);
-                if (!bad) continue;
-                odd = true;
-              }
-              *at = v;
+            for (int key = own + lane / 16; key < behind; key += 2) {
+              uint4* at = reinterpret_cast<uint4*>(tile + sw128_off(key, chunk & 7));
+              uint4 v = *at;
+              bool bad = false;
+              auto check = [&](uint32_t& w) {
+                if ((w & 0x7f80u) == 0x7f80u) { w &= 0xffff0000u; bad = true; }
+                if ((w & 0x7f800000u) == 0x7f800000u) { w &= 0xffffu; bad = true; }
+              };
+              check(v.x); check(v.y); check(v.z); check(v.w);
+              if (bad) *at = v;
+              odd |= bad;
             }
+#pragma unroll 8
+            for (int key = behind + lane / 16; key < 128; key += 2)
+              *reinterpret_cast<uint4*>(tile + sw128_off(key, chunk & 7)) = make_uint4(0, 0, 0, 0);
             if (odd) sh.odd[(n_run - 1) & 1] = 1;
             fence_proxy_async_smem();
           }
