@@ -9,8 +9,8 @@
 // there); the top 32 bits then give sin and cos in fp32.
 //
 // Every value is read and written once; nothing else moves. A block takes one
-// new row, or four where there are many (the frequencies are then turned into
-// fixed point once for four rows): a row's K, V, Q and index vectors are cut
+// new row, or up to four where there are many short ones (the frequencies are then
+// turned into fixed point once for all of them): a row's K, V, Q and index vectors are cut
 // into items of two 16-byte pieces (the two halves of eight pairs, or two
 // neighbours), one thread each, whose loads are on their way before the row's
 // place and angles are looked up.
@@ -238,13 +238,16 @@ cudaError_t launch_paged_append(const PagedProb& p, const PagedCachePtrs& c, con
   a.num_pages = p.num_pages;
   a.max_blocks = p.max_blocks;
   a.err = reinterpret_cast<int*>(ws);
-  // four rows a block from where that still fills every SM a few times (32,764 rows: 178 us with one, 150 with four)
-  a.rows = p.N >= 16 * kCutSms ? kMaxRows : 1;
   a.n_q = r.Q ? 8 * p.Hq : 0;
   a.n_k = 8 * p.G;
   a.n_qi = r.q_idx ? 4 * p.G : 0;
   a.items = a.n_q + 2 * a.n_k + a.n_qi + (r.k_idx ? 4 : 0);
   a.inv_items = 1.f / (float)a.items;
+  // Rows for two rounds of a block's loads, so that its look-ups are shared, as long as every SM gets three blocks. 38,610
+  // rows of 4 + 2 x 4 heads take 97 us with one row a block and 57 with four; 6,710 rows of 64 + 2 x 8, whose blocks are long
+  // enough with one, 64 and 68; 2,400 rows of 8 + 2 x 2 heads 12 and 8.
+  a.rows = std::min(kMaxRows, std::max(1, 2 * kInFlight * kThreads / a.items));
+  while (a.rows > 1 && p.N < 3 * kCutSms * a.rows) --a.rows;
   // Few rows: a block of its own checks them and writes the error word, so that nothing has to clear it first (256 rows in
   // a graph: 3.0 us against 6.2 with a memset). For many rows it would be the last to end: 1024 sequences' rows 9.1 us
   // against 9.7, 2000 sequences' 16.8 against 12.3.
