@@ -38,6 +38,7 @@ struct PagedWs {
   int splits = 1;       // partials a row's own pages are cut into ...
   int per_split = 1;    // ... of this many pages
   int tile_rows = 1;    // new rows of one sequence that share the key tiles (mma.sync path)
+  int prefix = 0;       // pages that are read once for the batch (0 where a small shared prefix is read as own pages)
   int pairs = 0;        // shared prefix: pairs of 128-row query tiles
   int teams = 0;        // shared prefix: runs of pages, each walked by `pairs` CTAs
   int pslots = 0;       // shared prefix: partials per row

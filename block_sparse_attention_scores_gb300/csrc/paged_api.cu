@@ -59,10 +59,17 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
     cut_pages((long long)p.N * p.G, std::min(p.k, p.max_blocks), 6, 8, &L.per_split, &L.splits);
   } else {
     L.tile_rows = 8 / p.hg;
-    // More columns (rows x heads of a sequence) than eight on average, and more than a page each: 128-row tiles, tcgen05.
+    // More columns (rows x heads of a sequence) than eight on average, padded rows aside, and more than a page each: 128-row
+    // tiles, tcgen05.
     // Against eight columns at a time: 32 sequences of 2 rows x 64 heads over 2000 tokens 63 -> 62 us, of 8 rows 135 -> 71,
     // 300 rows x 32 heads over 8000 274 -> 64; the other way for one page (8 rows x 64 heads over 100 tokens 17 -> 10).
-    if ((long long)p.N * p.hg > 8LL * p.S && p.max_blocks - p.prefix > 1) {
+    const bool runs = (long long)p.N * p.hg > 9LL * p.S && p.max_blocks - p.prefix > 1;
+    // A shared prefix of ten pages an SM, counted for every sequence, is read as own pages: it stays in L2, and two kernels
+    // do with it what four do. 4 sequences of 32 heads over 8 groups behind 16 pages 15 us against 20, 16 behind 8 pages 16
+    // and 22, 8 of 16 heads over 2 groups behind 64 pages 19 and 23; beyond: 8 of 32 heads over 4 groups behind 100 33 and 28.
+    const bool fold = !runs && (long long)p.S * p.prefix * p.G <= 1500;
+    L.prefix = fold ? 0 : p.prefix;
+    if (runs) {
       L.run_rows = 256 / p.hg;
       L.runs = take((size_t)p.N * 16);
       cut_pages((long long)std::max(p.N / L.run_rows, std::min(p.S, p.N)) * p.G, p.max_blocks - p.prefix, 3, 0, &L.per_run,
@@ -70,10 +77,10 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
       L.splits = 0;
       L.n_flags = kCutSms;
     } else {
-      cut_pages((long long)std::max(p.N / L.tile_rows, std::min(p.S, p.N)) * p.G, p.max_blocks - p.prefix, p.prefix ? 1 : 6,
-                p.prefix ? 0 : 8, &L.per_split, &L.splits);
+      cut_pages((long long)std::max(p.N / L.tile_rows, std::min(p.S, p.N)) * p.G, p.max_blocks - L.prefix, L.prefix ? 1 : 6,
+                L.prefix ? 0 : 8, &L.per_split, &L.splits);
     }
-    if (p.prefix > 0) {
+    if (L.prefix > 0) {
       const int tiles = (int)(((long long)p.N * p.hg + 127) / 128);
       L.pairs = (tiles + 1) / 2;
       const int units = p.G * p.prefix;
@@ -302,7 +309,7 @@ msa_status msa_paged_dense_attn(const msa_paged_shape* shape, const msa_paged_ca
   uint8_t* w = static_cast<uint8_t*>(workspace);
   PoolMaps maps;
   if ((s = encode_pools(p, c, &maps)) != MSA_OK) return s;
-  const bool parts = p.prefix || L.run_rows;
+  const bool parts = L.prefix || L.run_rows;
   if ((s = cuda_status(launch_paged_rows(p, c, w, L, st), "paged rows launch")) != MSA_OK) return s;
   if (parts && (s = cuda_status(launch_paged_prefix(p, c, maps, Q, w, L, st), "paged prefix launch")) != MSA_OK) return s;
   if (!L.run_rows &&

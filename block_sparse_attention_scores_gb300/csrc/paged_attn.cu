@@ -701,7 +701,7 @@ cudaError_t launch_paged_attn(const PagedProb& p, const PagedCachePtrs& c, const
   a.k = p.k;
   a.num_pages = p.num_pages;
   a.max_blocks = p.max_blocks;
-  a.prefix = p.prefix;
+  a.prefix = L.prefix;
   a.splits = L.splits;
   a.per_split = L.per_split;
   a.tile_rows = L.tile_rows;
@@ -731,7 +731,7 @@ cudaError_t launch_paged_merge(const PagedProb& p, void* O, float* LSE, uint8_t*
   a.Hq = p.Hq;
   a.G = p.G;
   a.hg = p.hg;
-  a.prefix = p.prefix;
+  a.prefix = L.prefix;
   a.per_split = L.per_split;
   a.tile_rows = L.tile_rows;
   a.teams = L.teams;

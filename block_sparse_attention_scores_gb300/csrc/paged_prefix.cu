@@ -767,7 +767,7 @@ cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, con
   a.Hq = p.Hq;
   a.G = p.G;
   a.hg = p.hg;
-  a.prefix = p.prefix;
+  a.prefix = L.prefix;
   a.pairs = L.pairs;
   a.teams = L.teams;
   a.num_pages = p.num_pages;

@@ -18,16 +18,18 @@
 namespace msa {
 
 struct RowsArgs {
-  const int32_t *row_start, *seq_len;
+  const int32_t *row_start, *seq_len, *page_table;
   int4 *rows, *lead, *runs;
   int *arrived, *header;
   int S, N, n_arrived, max_blocks, prefix, tile_rows, run_rows;
+  int check;  // pages of a shared prefix that are compared here, as no kernel of their own does
 };
 
 inline RowsArgs rows_args(const PagedProb& p, const PagedCachePtrs& c, uint8_t* ws, const PagedWs& L) {
   RowsArgs a;
   a.row_start = c.row_start;
   a.seq_len = c.seq_len;
+  a.page_table = c.page_table;
   a.rows = reinterpret_cast<int4*>(ws + L.rows);
   a.lead = reinterpret_cast<int4*>(ws + L.lead);
   a.runs = reinterpret_cast<int4*>(ws + L.runs);
@@ -40,6 +42,7 @@ inline RowsArgs rows_args(const PagedProb& p, const PagedCachePtrs& c, uint8_t* 
   a.prefix = p.prefix;
   a.tile_rows = L.tile_rows;
   a.run_rows = L.run_rows;
+  a.check = p.prefix - L.prefix;
   return a;
 }
 
@@ -88,6 +91,16 @@ __device__ __forceinline__ void line_up_rows(const RowsArgs& a, RowsShared& sh, 
   for (int i = tid; i < a.n_arrived; i += threads) a.arrived[i] = 0;
   sync();
   auto start = [&](int i) { return all ? sh.staged[i] : ld_in(a.row_start + i); };
+  if (a.check) {
+    const int ref = bisect_rows(start, a.S, 0);  // the first sequence with rows
+    bool bad = false;
+    for (int i = tid; ref < a.S && i < a.S * a.check; i += threads) {
+      const int s = i / a.check, c = i % a.check;
+      if (start(s + 1) > start(s))
+        bad |= ld_in(a.page_table + (size_t)s * a.max_blocks + c) != ld_in(a.page_table + (size_t)ref * a.max_blocks + c);
+    }
+    if (bad) dev_fail(a.header, kDevBadIndex, 1512);
+  }
   int leads = 0, runs = 0;
   for (int r0 = 0; r0 < a.N; r0 += threads) {
     const int r = r0 + tid;

@@ -313,6 +313,88 @@ def test_dense(msa, name, stale):
     _check_padding(b, O, LSE)
 
 
+# Shared prefixes of enough pages (counted for every sequence and group) to be read once for the batch.
+PREFIX = {
+    "hg1": dict(counts=[1, 3, 0, 2] * 5, lens=[128 * 40 + 3 + 9 * i for i in range(20)], Hq=2, G=2, prefix=40, pad=1),
+    "hg2": dict(counts=[2, 1, 1] * 10, lens=[128 * 26 + 2 + 41 * i for i in range(30)], Hq=4, G=2, prefix=26),
+    "hg4": dict(counts=[0] + [1, 2] * 12 + [1], lens=[7] + [128 * 60 + 2 + 17 * i for i in range(25)], Hq=4, G=1, prefix=60),
+    "hg8": dict(counts=[1] * 16, lens=[128 * 100 + 1 + 64 * i for i in range(16)], Hq=8, G=1, prefix=100, pad=2),
+    "three_pairs": dict(counts=[1] * 70, lens=[128 * 12 + 1 + i for i in range(70)], Hq=16, G=2, prefix=12),
+}
+
+
+@pytest.mark.parametrize("stale", [NAN, INF], ids=["nan", "inf"])
+@pytest.mark.parametrize("name", PREFIX)
+def test_dense_prefix(msa, name, stale):
+    b = ref.Batch(stale=stale, seed=26, **PREFIX[name])
+    assert b.S * b.prefix * b.G > 1500 and b.N * b.hg <= 9 * b.S
+    O, LSE = _dense(msa, b)
+    rows = range(0, b.n, 1 if b.n < 30 else 7)
+    ref.check_attention(b, rows, range(b.Hq) if b.Hq <= 8 else range(0, b.Hq, 5), O, LSE, _all(b), bf16_p=True)
+    _check_padding(b, O, LSE)
+
+
+def test_dense_prefix_large_scores(msa):
+    b = ref.Batch(counts=[2, 1] * 20, lens=[128 * 20 + 90 + 3 * i for i in range(40)], Hq=8, G=2, prefix=20, seed=9)
+    for c in range(20):
+        b.K[int(b.table[0, c])] *= float(1 + 3 * (c % 7))
+    b.Q *= 4
+    O, LSE = _dense(msa, b)
+    ref.check_attention(b, range(0, b.n, 5), range(b.Hq), O, LSE, _all(b), bf16_p=True)
+
+
+def test_dense_prefix_bad_batches(msa):
+    def run(change, good):
+        b = ref.Batch(counts=[1] * 20, lens=[128 * 40 + 3 + 9 * i for i in range(20)], Hq=8, G=2, prefix=40, seed=1)
+        change(b)
+        shape, cache, t = b.gpu()
+        ws = msa.alloc_paged_workspace(shape, msa.MSA_WS_PAGED_DENSE)
+        ws.fill_(255)
+        O, LSE = msa.paged_dense_attn(shape, cache, t["Q"], workspace=ws)
+        with pytest.raises(msa.MsaError) as e:
+            msa.msa_check_device_status(ws)
+        assert e.value.status == msa.MSA_ERR_DEVICE
+        ref.check_attention(b, good, range(0, 8, 3), O.cpu(), LSE.cpu(), _all(b), bf16_p=True)
+
+    def everywhere(c, v):
+        return lambda b: b.table.__setitem__((slice(None), c), v)
+
+    for v in (-1, 1 << 20, 2 ** 31 - 1, -2 ** 31):
+        run(everywhere(17, v), [])                                         # a bad page of the prefix
+        run(lambda b: b.table.__setitem__((3, 40), v), [0, 2, 4, 19])      # of a sequence's own
+        run(lambda b: b.lens.__setitem__(5, v if v < 0 else 128 * 40), [0, 4, 6, 19])  # no row, or one inside the prefix
+    run(lambda b: b.table.__setitem__((7, 11), b.table[7, 12]), [])       # a prefix that is not shared
+
+
+def test_dense_prefix_same_bits(msa):
+    """Again, beside itself on another stream, and from a graph."""
+    import torch
+
+    b = ref.Batch(counts=[1] * 14, lens=[128 * 30 + 5 + 37 * i for i in range(14)], Hq=16, G=4, prefix=30, seed=2)
+    want = _dense(msa, b)
+    shape, cache, t = b.gpu()
+    ws = [msa.alloc_paged_workspace(shape, msa.MSA_WS_PAGED_DENSE) for _ in range(2)]
+    out = [(torch.zeros_like(t["Q"]), torch.zeros(b.N, b.Hq, device="cuda")) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for w, (O, LSE), s in zip(ws, out, streams):
+            msa.msa_paged_dense_attn(shape, cache, t["Q"], O, LSE, w, s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for i in (0, 1, 0):
+            msa.msa_paged_dense_attn(shape, cache, t["Q"], *out[i], ws[0])
+    for again in range(3):
+        for w, (O, LSE) in zip(ws, out):
+            msa.msa_check_device_status(w)
+            assert torch.equal(O.cpu(), want[0]) and torch.equal(LSE.cpu(), want[1]), again
+            O.zero_()
+            LSE.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+
+
 # Several rows per sequence: more than eight columns on average and more than a page take 128-row tiles (of 128 / h_g
 # rows, two at a time).
 RUNS = {
