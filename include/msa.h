@@ -422,8 +422,9 @@ MSA_API msa_status msa_paged_sparse_attn(const msa_paged_shape *shape, const msa
  * Full attention for new tokens (msa_dense_fwd's result for each row, over all
  * tokens j <= t): the layers and training stages without a selection. The
  * first shape->prefix_blocks pages of every sequence must be the same (a
- * prompt that the batch shares); they are read once for the whole batch, and
- * every row's position must lie behind them. prefix_blocks = 0 shares nothing.
+ * prompt that the batch shares); they are read once for the whole batch (a few
+ * pages once a sequence, from L2, where that is quicker), and every row's
+ * position must lie behind them. prefix_blocks = 0 shares nothing.
  */
 MSA_API msa_status msa_paged_dense_attn(const msa_paged_shape *shape, const msa_paged_cache *cache, const void *Q,
                                         void *O, float *LSE, void *workspace, size_t workspace_bytes,
