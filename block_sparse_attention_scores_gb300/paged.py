@@ -171,12 +171,16 @@ def _rows(name, t, shape, device):
         return t.data_ptr(), 0
     strides, packed = t.stride(), 1
     if shape[0] > 1 and strides[-1] == 1 and (len(shape) == 2 or strides[1] == shape[2]):
-        return t.data_ptr(), strides[0]
-    for n, st in zip(shape[:0:-1], strides[:0:-1]):
-        if n != 1 and st != packed:
-            _refuse(name, t, t.dtype, shape, device, packed=False)
-        packed *= n
-    return t.data_ptr(), strides[0] if shape[0] > 1 else packed
+        ld, packed = strides[0], shape[-1] if len(shape) == 2 else shape[1] * shape[2]
+    else:
+        for n, st in zip(shape[:0:-1], strides[:0:-1]):
+            if n != 1 and st != packed:
+                _refuse(name, t, t.dtype, shape, device, packed=False)
+            packed *= n
+        ld = strides[0] if shape[0] > 1 else packed
+    if ld < packed:  # rows that lie on one another; expanded ones have stride 0, which the C call takes for packed rows
+        raise ValueError(f"the rows of {name} must not overlap (their stride is {ld}): an expanded tensor is to be made contiguous")
+    return t.data_ptr(), ld
 
 
 def _run(call, cache, stream, workspace, *args):

@@ -192,3 +192,38 @@ def test_binding_refuses_tensors_of_another_kind(msa):
         rows("K", x, (3, 4, 128), -1)
     with pytest.raises(ValueError, match="bfloat16"):
         rows("K", x.float(), (3, 2, 128), -1)
+
+
+@pytest.mark.parametrize("x,shape", [
+    ((1, 2, 128), (64, 2, 128)), ((1, 1, 128), (64, 1, 128)), ((1, 64), (64, 64)), ((1, 1, 64), (9, 2, 64)),
+    ((3, 1, 128), (3, 2, 128)), ((1, 1, 1), (3, 2, 128)),
+], ids=str)
+def test_binding_refuses_expanded_rows(msa, x, shape):
+    """A row stride of 0 means packed rows to the C call, which would read past the end of an expanded tensor."""
+    import torch
+
+    from block_sparse_attention_scores_gb300.paged import _rows as rows
+
+    t = torch.zeros(x, dtype=torch.bfloat16).expand(shape)
+    with pytest.raises(ValueError, match="overlap|packed"):
+        rows("K", t, shape, -1)
+    assert rows("K", t.contiguous(), shape, -1)[1] == 0
+
+
+def test_binding_refuses_overlapping_rows(msa):
+    import torch
+
+    from block_sparse_attention_scores_gb300.paged import _rows as rows
+
+    for ld in (0, 8, 128, 248):
+        t = torch.zeros(1024, dtype=torch.bfloat16).as_strided((3, 2, 128), (ld, 128, 1))
+        with pytest.raises(ValueError, match="overlap"):
+            rows("K", t, (3, 2, 128), -1)
+    # one group: the stride between groups says nothing
+    t = torch.zeros(1024, dtype=torch.bfloat16).as_strided((3, 1, 128), (0, 640, 1))
+    with pytest.raises(ValueError, match="overlap"):
+        rows("K", t, (3, 1, 128), -1)
+    # a single row may have any stride
+    t = torch.zeros(1024, dtype=torch.bfloat16).as_strided((1, 2, 128), (0, 128, 1))
+    assert rows("K", t, (1, 2, 128), -1)[1] in (0, 256)
+    assert rows("k_idx", torch.zeros(1, 64, dtype=torch.bfloat16).expand(1, 64), (1, 64), -1)[1] in (0, 64)
