@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import struct
+from ctypes import addressof
 from dataclasses import dataclass
 
 from . import (MSA_ERR_UNSUPPORTED, MSA_WS_PAGED_APPEND, MSA_WS_PAGED_DENSE, MSA_WS_PAGED_SPARSE, MsaError, _check,
@@ -57,11 +58,11 @@ class PagedShape:
     scale: float = 0.0
 
     def __post_init__(self):
-        # what every call would work out again: the C struct and the shapes of the tensors
+        # what every call would work out again: the C struct (not its address, which a copy does not share) and the
+        # shapes of the tensors
         put = lambda n, v: object.__setattr__(self, n, v)  # noqa: E731
         put("_c", MsaPagedShape(self.S, self.N, self.Hq, self.G, self.d, self.d_idx, self.Bk, self.k, self.num_pages,
                                 self.max_blocks, self.prefix_blocks, self.scale))
-        put("_addr", ctypes.addressof(self._c))
         put("_sizes", (self.S, self.G, self.num_pages, self.max_blocks, self.d, self.Bk))
         N, Hq, G = self.N, self.Hq, self.G
         put("_q", (N, Hq, self.d))
@@ -203,7 +204,7 @@ def _run(call, cache, stream, workspace, *args):
 
 
 def msa_paged_workspace_size(shape, which: int) -> int:
-    return int(load_library().msa_paged_workspace_size(shape._addr, which))
+    return int(load_library().msa_paged_workspace_size(addressof(shape._c), which))
 
 
 def alloc_paged_workspace(shape, which: int, device="cuda"):
@@ -228,7 +229,7 @@ def msa_paged_append(shape, cache, rope, K, V, k_idx, Q, q_idx, Q_out, q_idx_out
     qp, q_ld = none if Q is None else _rows("Q", Q, shape._q, dev)
     ip, i_ld = none if q_idx is None else _rows("q_idx", q_idx, shape._qi, dev)
     xp, x_ld = none if k_idx is None else _rows("k_idx", k_idx, shape._ki, dev)
-    _run(load_library().msa_paged_append, cache, stream, workspace, shape._addr, cache._addr, rope._addr,
+    _run(load_library().msa_paged_append, cache, stream, workspace, addressof(shape._c), cache._addr, rope._addr,
          _new_rows(qp, kp, vp, ip, xp, q_ld, k_ld, v_ld, i_ld, x_ld),
          None if Q_out is None else _want("Q_out", Q_out, _bf16, shape._q, dev),
          None if q_idx_out is None else _want("q_idx_out", q_idx_out, _bf16, shape._qi, dev))
@@ -241,7 +242,7 @@ def msa_paged_sparse_attn(shape, cache, Q, q_idx, block_idx, O, LSE, workspace, 
     dev = cache._device
     if q_idx is not None and cache.k_idx is None:
         raise ValueError("the cache has no index keys (k_idx)")
-    _run(load_library().msa_paged_sparse_attn, cache, stream, workspace, shape._addr, cache._addr,
+    _run(load_library().msa_paged_sparse_attn, cache, stream, workspace, addressof(shape._c), cache._addr,
          _want("Q", Q, bf, shape._q, dev), None if q_idx is None else _want("q_idx", q_idx, bf, shape._qi, dev),
          _want("block_idx", block_idx, torch.int32, shape._bi, dev), _want("O", O, bf, shape._q, dev),
          _want("LSE", LSE, torch.float32, shape._lse, dev))
@@ -252,7 +253,7 @@ def msa_paged_dense_attn(shape, cache, Q, O, LSE, workspace, stream=None) -> Non
     torch, bf = _torch, _bf16
     cache.check(shape)
     dev = cache._device
-    _run(load_library().msa_paged_dense_attn, cache, stream, workspace, shape._addr, cache._addr,
+    _run(load_library().msa_paged_dense_attn, cache, stream, workspace, addressof(shape._c), cache._addr,
          _want("Q", Q, bf, shape._q, dev), _want("O", O, bf, shape._q, dev),
          _want("LSE", LSE, torch.float32, shape._lse, dev))
 

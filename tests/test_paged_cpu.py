@@ -227,3 +227,42 @@ def test_binding_refuses_overlapping_rows(msa):
     t = torch.zeros(1024, dtype=torch.bfloat16).as_strided((1, 2, 128), (0, 128, 1))
     assert rows("K", t, (1, 2, 128), -1)[1] in (0, 256)
     assert rows("k_idx", torch.zeros(1, 64, dtype=torch.bfloat16).expand(1, 64), (1, 64), -1)[1] in (0, 64)
+
+
+@pytest.mark.parametrize("how", ["copy", "deepcopy", "pickle", "replace"])
+def test_copied_shapes_stand_on_their_own(msa, how):
+    """A copy works after its original is gone, and in another process: it holds no address of the original's struct."""
+    import copy
+    import dataclasses
+    import gc
+    import pickle
+
+    kw = dict(N=7, max_blocks=40, num_pages=100)
+    want = [msa.msa_paged_workspace_size(_shape(msa, **kw), w) for w in range(3)]
+    s = _shape(msa, **kw)
+    assert not [n for n, v in vars(s).items() if isinstance(v, int) and n.startswith("_")]
+    c = {"copy": copy.copy, "deepcopy": copy.deepcopy, "pickle": lambda x: pickle.loads(pickle.dumps(x)),
+         "replace": dataclasses.replace}[how](s)
+    del s
+    gc.collect()
+    others = [_shape(msa, N=1 + i) for i in range(50)]  # what takes its memory
+    assert len(others) == 50
+    assert [msa.msa_paged_workspace_size(c, w) for w in range(3)] == want
+    assert c == _shape(msa, **kw)
+
+
+def test_pickled_shape_in_another_process(msa):
+    import pathlib
+    import pickle
+    import subprocess
+    import sys
+
+    s = _shape(msa, N=7, max_blocks=40, num_pages=100)
+    code = ("import pickle, sys\n"
+            "import block_sparse_attention_scores_gb300 as msa\n"
+            "s = pickle.loads(bytes.fromhex(sys.argv[1]))\n"
+            "print(msa.msa_paged_workspace_size(s, msa.MSA_WS_PAGED_DENSE))\n")
+    out = subprocess.run([sys.executable, "-c", code, pickle.dumps(s).hex()], capture_output=True, text=True, timeout=600,
+                         cwd=pathlib.Path(__file__).resolve().parent.parent)
+    assert out.returncode == 0, out.stderr[-2000:]
+    assert int(out.stdout) == msa.msa_paged_workspace_size(s, msa.MSA_WS_PAGED_DENSE)
