@@ -109,10 +109,34 @@ def _want(name, t, dtype, shape, device):
     _refuse(name, t, dtype, shape, device)
 
 
-class PagedCache:
+class _Fixed:
+    """Has a C struct with its tensors' addresses: no tensor is replaced afterwards, and a copy has a struct of its own."""
+
+    _held = ()  # the attributes in question
+
+    def __setattr__(self, name, value):
+        self._keep(name)
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        self._keep(name)
+        object.__delattr__(self, name)
+
+    def _keep(self, name):
+        if name in self._held:
+            raise AttributeError(f"{name} of a {type(self).__name__} cannot be replaced (the calls use the tensor's "
+                                 f"address): write into the tensor, or make another {type(self).__name__}")
+
+    def __reduce__(self):
+        return type(self), self._args
+
+
+class PagedCache(_Fixed):
     """Pools K, V [num_pages, G, 128, 128] and k_idx [num_pages, 128, 64] (or None) in bf16, and the batch description
-    page_table [S, max_blocks], row_start [S + 1], seq_len [S] in int32. The tensors are kept as they are; their
-    contents may change between calls."""
+    page_table [S, max_blocks], row_start [S + 1], seq_len [S] in int32. The tensors are kept as they are: their
+    contents may change between calls, neither they nor their storage may be replaced."""
+
+    _held = ("K", "V", "k_idx", "page_table", "row_start", "seq_len", "device")
 
     def __init__(self, K, V, k_idx, page_table, row_start, seq_len):
         torch = _t()
@@ -122,17 +146,15 @@ class PagedCache:
         dev = K.get_device()
         S = seq_len.shape[0]
         bf, i32 = torch.bfloat16, torch.int32
-        self._struct = MsaPagedCache(
+        struct = MsaPagedCache(
             _want("K", K, bf, (pages, G, Bk, d), dev), _want("V", V, bf, (pages, G, Bk, d), dev),
             None if k_idx is None else _want("k_idx", k_idx, bf, (pages, Bk, k_idx.shape[-1]), dev),
             _want("page_table", page_table, i32, (S, page_table.shape[-1]), dev),
             _want("row_start", row_start, i32, (S + 1,), dev), _want("seq_len", seq_len, i32, (S,), dev))
-        self._addr = ctypes.addressof(self._struct)
-        self.K, self.V, self.k_idx = K, V, k_idx
-        self.page_table, self.row_start, self.seq_len = page_table, row_start, seq_len
-        self.device, self._device = K.device, dev
-        self._sizes = (S, G, pages, page_table.shape[-1], d, Bk)
-        self._index_dim = None if k_idx is None else k_idx.shape[-1]
+        self.__dict__.update(
+            K=K, V=V, k_idx=k_idx, page_table=page_table, row_start=row_start, seq_len=seq_len, device=K.device,
+            _args=(K, V, k_idx, page_table, row_start, seq_len), _struct=struct, _addr=addressof(struct), _device=dev,
+            _sizes=(S, G, pages, page_table.shape[-1], d, Bk), _index_dim=None if k_idx is None else k_idx.shape[-1])
 
     def check(self, shape):
         """The cache is one of `shape`."""
@@ -142,9 +164,11 @@ class PagedCache:
             raise ValueError(f"the cache's index keys have {self._index_dim} dims, the shape {shape.d_idx}")
 
 
-class Rope:
+class Rope(_Fixed):
     """Rotation frequencies (radians per position, fp32): inv_freq [rot_dim / 2] for Q and K, inv_freq_idx
     [rot_dim_idx / 2] for the index branch; None rotates nothing."""
+
+    _held = ("inv_freq", "inv_freq_idx")
 
     def __init__(self, inv_freq=None, inv_freq_idx=None, interleaved=False):
         torch = _t()
@@ -158,10 +182,11 @@ class Rope:
 
         p, n = ptr("inv_freq", inv_freq)
         pi, ni = ptr("inv_freq_idx", inv_freq_idx)
-        self.inv_freq, self.inv_freq_idx = inv_freq, inv_freq_idx
-        self._devices = {t.get_device() for t, q in ((inv_freq, p), (inv_freq_idx, pi)) if q is not None}
-        self._struct = MsaRope(p, pi, n, ni, 1 if interleaved else 0)
-        self._addr = ctypes.addressof(self._struct)
+        struct = MsaRope(p, pi, n, ni, 1 if interleaved else 0)
+        self.__dict__.update(
+            inv_freq=inv_freq, inv_freq_idx=inv_freq_idx, _args=(inv_freq, inv_freq_idx, interleaved), _struct=struct,
+            _addr=addressof(struct),
+            _devices={t.get_device() for t, q in ((inv_freq, p), (inv_freq_idx, pi)) if q is not None})
 
 
 def _rows(name, t, shape, device):

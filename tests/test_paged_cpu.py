@@ -266,3 +266,23 @@ def test_pickled_shape_in_another_process(msa):
                          cwd=pathlib.Path(__file__).resolve().parent.parent)
     assert out.returncode == 0, out.stderr[-2000:]
     assert int(out.stdout) == msa.msa_paged_workspace_size(s, msa.MSA_WS_PAGED_DENSE)
+
+
+@pytest.mark.parametrize("kind,names", [("PagedCache", ("K", "V", "k_idx", "page_table", "row_start", "seq_len")),
+                                        ("Rope", ("inv_freq", "inv_freq_idx"))])
+def test_tensors_of_a_cache_are_not_replaced(msa, kind, names):
+    """The calls go by the addresses taken when the object was made: a replaced tensor would be a freed one to them."""
+    import copy
+    import pickle
+
+    rope = msa.Rope(interleaved=True)
+    thing = rope if kind == "Rope" else msa.PagedCache.__new__(msa.PagedCache)
+    for n in names:
+        with pytest.raises(AttributeError, match=f"{n} of a {kind}"):
+            setattr(thing, n, None)
+        with pytest.raises(AttributeError, match=f"{n} of a {kind}"):
+            delattr(thing, n)
+    thing.layer = 3  # a user's own
+    for c in (copy.copy(rope), copy.deepcopy(rope), pickle.loads(pickle.dumps(rope))):
+        assert c._addr == ctypes.addressof(c._struct) != rope._addr
+        assert (c._struct.rot_dim, c._struct.rot_dim_idx, c._struct.interleaved) == (0, 0, 1)

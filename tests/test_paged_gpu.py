@@ -791,6 +791,25 @@ def test_bad_selections_are_reported(msa):
 
 
 # ----------------------------------------------------------------- streams, graphs, reruns
+def test_copied_cache_has_its_own_tensors(msa):
+    """A deep copy is another cache: appending to it leaves the first one alone, and works after that one is gone."""
+    import copy
+
+    import torch
+
+    b = ref.Batch(counts=[1, 3], lens=[130, 259], Hq=8, G=2, seed=7, stale=0.0)
+    shape, cache, t = b.gpu()
+    same, other = copy.copy(cache), copy.deepcopy(cache)
+    assert same.K.data_ptr() == cache.K.data_ptr() and other.K.data_ptr() != cache.K.data_ptr()
+    assert other._struct.K == other.K.data_ptr() and other._struct.seq_len == other.seq_len.data_ptr()
+    before = t["K"].clone()
+    new = torch.ones(b.N, 2, 128, dtype=torch.bfloat16, device="cuda")
+    msa.paged_append(shape, other, msa.Rope(), new, new)
+    assert torch.equal(cache.K, before) and not torch.equal(other.K, before)
+    msa.paged_append(shape, same, msa.Rope(), new, new)
+    assert torch.equal(cache.K, other.K)
+
+
 def test_same_bits_on_other_streams_and_at_once(msa):
     import torch
 
