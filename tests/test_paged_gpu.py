@@ -837,6 +837,44 @@ def test_same_bits_on_other_streams_and_at_once(msa):
         assert torch.equal(kept[i + 1][3].cpu(), Od) and torch.equal(kept[i + 1][4].cpu(), LSEd)
 
 
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_helpers_allocate_on_the_stream_they_run_on(msa, raw):
+    """A helper on a side stream without a workspace: what it allocates is neither handed out to the current stream while
+    the side stream still has the call to do, nor taken from what the current stream still writes to."""
+    import torch
+
+    b = ref.Batch(counts=[1, 2], lens=[128 * 30 + 4, 128 * 25], Hq=8, G=2, seed=17, stale=0.0)
+    shape, cache, t = b.gpu(6)
+    want_s = [x.clone() for x in msa.paged_sparse_attn(shape, cache, t["Q"], t["q_idx"])]
+    want_d = [x.clone() for x in msa.paged_dense_attn(shape, cache, t["Q"])]
+    new = torch.zeros(b.N, 2, 128, dtype=torch.bfloat16, device="cuda")
+    scratch = ref.Batch(counts=[1, 2], lens=[128 * 30 + 4, 128 * 25], Hq=8, G=2, seed=18, stale=0.0).gpu(6)[1]
+    want_q, _ = msa.paged_append(shape, scratch, msa.Rope(_freq(128).cuda()), new, new, Q=t["Q"])
+    want_q = want_q.clone()
+    rope = msa.Rope(_freq(128).cuda())
+    sizes = [msa.msa_paged_workspace_size(shape, w) for w in range(3)]
+    sizes += [x.nbytes for x in want_s + want_d + [want_q]]
+    side, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    stream = side.cuda_stream if raw else side
+    torch.cuda.synchronize()
+    for _ in range(10):
+        # the current stream is busy with memory that it has given back
+        torch.cuda._sleep(3_000_000)
+        for n in sizes:
+            torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(1_000_000)
+        s = msa.paged_sparse_attn(shape, cache, t["Q"], t["q_idx"], stream=stream)
+        d = msa.paged_dense_attn(shape, cache, t["Q"], stream=stream)
+        q, _ = msa.paged_append(shape, scratch, rope, new, new, Q=t["Q"], stream=stream)
+        # and takes memory while the side stream has not come to the calls
+        held = [torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255) for n in sizes * 2]
+        here.wait_stream(side)
+        for got, want in list(zip(s, want_s)) + list(zip(d, want_d)) + [(q, want_q)]:
+            assert torch.equal(got, want)
+        del s, d, q, got, held
+
+
 def test_captured_step_replays_on_another_batch(msa):
     """One decode step (append, selection and attention, full attention) captured once, replayed with other lengths,
     pages and rows of the same shape; two graphs share nothing but the cache."""
