@@ -269,6 +269,26 @@ def msa_check_device_status(workspace, stream=None) -> None:
 
 
 # ----------------------------------------------------------------- allocation helpers (torch plumbing)
+def _on_stream(stream, device, call, *args):
+    """call(*args) with `stream` current. What it allocates then belongs to the stream that its kernels run on: memory of
+    the caller's stream could be handed out again while the kernels still use it, or still be in use when they start.
+    The outputs are recorded on the caller's stream, too, which may be the one that reads them."""
+    import torch
+
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device)
+    elif stream.device != device:
+        raise ValueError(f"the stream is one of {stream.device}, the tensors live on {device}")
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        out = call(*args)
+    if here.cuda_stream != stream.cuda_stream:
+        for t in (out,) if isinstance(out, torch.Tensor) else out.values() if isinstance(out, dict) else out:
+            if t is not None:
+                t.record_stream(here)
+    return out
+
+
 def alloc_workspace(shape, which: int = MSA_WS_BWD, device="cuda"):
     import torch
 
@@ -282,9 +302,11 @@ def index_topk(shape: Shape, q_idx, k_idx, workspace=None, stream=None):
     """Allocate block_idx [B,G,T,k] int32 and run msa_index_topk."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, q_idx.device, index_topk, shape, q_idx, k_idx, workspace)
     ws = workspace if workspace is not None else alloc_workspace(shape, MSA_WS_TOPK, q_idx.device)
     bi = torch.empty((shape.B, shape.G, shape.T, shape.k), dtype=torch.int32, device=q_idx.device)
-    msa_index_topk(shape, q_idx, k_idx, bi, ws, stream)
+    msa_index_topk(shape, q_idx, k_idx, bi, ws)
     return bi
 
 
@@ -292,8 +314,10 @@ def warmup_block_idx(shape: Shape, device="cuda", stream=None):
     """Allocate block_idx [B,G,T,k] int32 and fill it with msa_warmup_block_idx."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, torch.empty(0, device=device).device, warmup_block_idx, shape, device)
     bi = torch.empty((shape.B, shape.G, shape.T, shape.k), dtype=torch.int32, device=device)
-    msa_warmup_block_idx(shape, bi, stream)
+    msa_warmup_block_idx(shape, bi)
     return bi
 
 
@@ -301,10 +325,12 @@ def sparse_fwd(shape: Shape, Q, K, V, block_idx, workspace=None, stream=None):
     """Allocate O [B,T,Hq,d] bf16 and LSE [B,T,Hq] fp32 and run msa_sparse_fwd."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, Q.device, sparse_fwd, shape, Q, K, V, block_idx, workspace)
     ws = workspace if workspace is not None else alloc_workspace(shape, MSA_WS_FWD, Q.device)
     O = torch.empty_like(Q)
     LSE = torch.empty((shape.B, shape.T, shape.Hq), dtype=torch.float32, device=Q.device)
-    msa_sparse_fwd(shape, Q, K, V, block_idx, O, LSE, ws, stream)
+    msa_sparse_fwd(shape, Q, K, V, block_idx, O, LSE, ws)
     return O, LSE
 
 
@@ -312,13 +338,15 @@ def bwd(shape: Shape, Q, K, V, O, dO, LSE, q_idx, k_idx, block_idx, kl_weight=1.
     """Allocate the fp32 gradients and KL and run msa_bwd. Returns a dict."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, Q.device, bwd, shape, Q, K, V, O, dO, LSE, q_idx, k_idx, block_idx, kl_weight, workspace)
     ws = workspace if workspace is not None else alloc_workspace(shape, MSA_WS_BWD, Q.device)
     f32 = dict(dtype=torch.float32, device=Q.device)
     out = dict(dQ=torch.empty(Q.shape, **f32), dK=torch.empty(K.shape, **f32), dV=torch.empty(V.shape, **f32),
                dq_idx=torch.empty(q_idx.shape, **f32), dk_idx=torch.empty(k_idx.shape, **f32),
                KL=torch.empty((shape.B, shape.G, shape.T), **f32))
     msa_bwd(shape, Q, K, V, O, dO, LSE, q_idx, k_idx, block_idx, kl_weight, out["dQ"], out["dK"], out["dV"],
-            out["dq_idx"], out["dk_idx"], out["KL"], ws, stream)
+            out["dq_idx"], out["dk_idx"], out["KL"], ws)
     return out
 
 
@@ -326,10 +354,12 @@ def dense_fwd(shape: Shape, Q, K, V, workspace=None, stream=None):
     """Allocate O and LSE and run msa_dense_fwd (full causal attention)."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, Q.device, dense_fwd, shape, Q, K, V, workspace)
     ws = workspace if workspace is not None else alloc_workspace(shape, MSA_WS_DENSE, Q.device)
     O = torch.empty_like(Q)
     LSE = torch.empty((shape.B, shape.T, shape.Hq), dtype=torch.float32, device=Q.device)
-    msa_dense_fwd(shape, Q, K, V, O, LSE, ws, stream)
+    msa_dense_fwd(shape, Q, K, V, O, LSE, ws)
     return O, LSE
 
 
@@ -337,13 +367,15 @@ def dense_bwd(shape: Shape, Q, K, V, O, dO, LSE, q_idx, k_idx, kl_weight=1.0, wo
     """Allocate the fp32 gradients and KL and run msa_dense_bwd. Returns a dict."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, Q.device, dense_bwd, shape, Q, K, V, O, dO, LSE, q_idx, k_idx, kl_weight, workspace)
     ws = workspace if workspace is not None else alloc_workspace(shape, MSA_WS_DENSE, Q.device)
     f32 = dict(dtype=torch.float32, device=Q.device)
     out = dict(dQ=torch.empty(Q.shape, **f32), dK=torch.empty(K.shape, **f32), dV=torch.empty(V.shape, **f32),
                dq_idx=torch.empty(q_idx.shape, **f32), dk_idx=torch.empty(k_idx.shape, **f32),
                KL=torch.empty((shape.B, shape.G, shape.T), **f32))
     msa_dense_bwd(shape, Q, K, V, O, dO, LSE, q_idx, k_idx, kl_weight, out["dQ"], out["dK"], out["dV"],
-                  out["dq_idx"], out["dk_idx"], out["KL"], ws, stream)
+                  out["dq_idx"], out["dk_idx"], out["KL"], ws)
     return out
 
 

@@ -19,7 +19,7 @@ import struct
 from ctypes import addressof
 from dataclasses import dataclass
 
-from . import (MSA_ERR_UNSUPPORTED, MSA_WS_PAGED_APPEND, MSA_WS_PAGED_DENSE, MSA_WS_PAGED_SPARSE, MsaError, _check,
+from . import (MSA_ERR_UNSUPPORTED, MSA_WS_PAGED_APPEND, MSA_WS_PAGED_DENSE, MSA_WS_PAGED_SPARSE, MsaError, _check, _on_stream,
                load_library)
 
 
@@ -284,30 +284,11 @@ def msa_paged_dense_attn(shape, cache, Q, O, LSE, workspace, stream=None) -> Non
 
 
 # ----------------------------------------------------------------- allocation helpers
-def _on(stream, device, call, *args):
-    """call(*args) with `stream` current. What it allocates then belongs to the stream that its kernels run on: memory of
-    the caller's stream could be handed out again while the kernels still use it, or still be in use when they start.
-    The outputs are recorded on the caller's stream, too, which may be the one that reads them."""
-    torch = _t()
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device)
-    elif stream.device != device:
-        raise ValueError(f"the stream is one of {stream.device}, the cache lives on {device}")
-    here = torch.cuda.current_stream(device)
-    with torch.cuda.stream(stream):
-        out = call(*args)
-    if here.cuda_stream != stream.cuda_stream:
-        for t in out:
-            if t is not None:
-                t.record_stream(here)
-    return out
-
-
 def paged_append(shape, cache, rope, K, V, k_idx=None, Q=None, q_idx=None, workspace=None, stream=None):
     """Allocate the rotated queries, run msa_paged_append and return (Q_out, q_idx_out); None where none was given."""
     dev = cache.device
     if stream is not None:
-        return _on(stream, dev, paged_append, shape, cache, rope, K, V, k_idx, Q, q_idx, workspace)
+        return _on_stream(stream, dev, paged_append, shape, cache, rope, K, V, k_idx, Q, q_idx, workspace)
     ws = workspace if workspace is not None else alloc_paged_workspace(shape, MSA_WS_PAGED_APPEND, dev)
     Q_out = None if Q is None else _torch.empty(shape._q, dtype=_bf16, device=dev)
     qi_out = None if q_idx is None else _torch.empty(shape._qi, dtype=_bf16, device=dev)
@@ -319,7 +300,7 @@ def paged_sparse_attn(shape, cache, Q, q_idx=None, block_idx=None, workspace=Non
     """Allocate O, LSE (and block_idx, when q_idx selects) and run msa_paged_sparse_attn; returns (O, LSE, block_idx)."""
     dev = cache.device
     if stream is not None:
-        return _on(stream, dev, paged_sparse_attn, shape, cache, Q, q_idx, block_idx, workspace)
+        return _on_stream(stream, dev, paged_sparse_attn, shape, cache, Q, q_idx, block_idx, workspace)
     if block_idx is None:
         if q_idx is None:
             raise ValueError("give q_idx to select blocks, or the block_idx to attend to")
@@ -335,7 +316,7 @@ def paged_dense_attn(shape, cache, Q, workspace=None, stream=None):
     """Allocate O and LSE and run msa_paged_dense_attn."""
     dev = cache.device
     if stream is not None:
-        return _on(stream, dev, paged_dense_attn, shape, cache, Q, workspace)
+        return _on_stream(stream, dev, paged_dense_attn, shape, cache, Q, workspace)
     ws = workspace if workspace is not None else alloc_paged_workspace(shape, MSA_WS_PAGED_DENSE, dev)
     O = _torch.empty(shape._q, dtype=_bf16, device=dev)
     LSE = _torch.empty(shape._lse, dtype=_torch.float32, device=dev)
