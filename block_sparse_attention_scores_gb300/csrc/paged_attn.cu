@@ -146,6 +146,10 @@ __device__ __forceinline__ void fetch_pages(const AttnArgs& a, int lane, Fetch& 
     int have = 0;  // ids stand at the front of the list
 #pragma unroll
     for (int c = 0; c < 4; ++c) have += __popc(__ballot_sync(0xffffffffu, f.ids[c] >= 0));
+    if (have > a.splits * a.per_split) {  // more ids than the table has columns: the parts are counted for no more
+      if (lane == 0) dev_fail(a.err, kDevBadIndex, 1411);
+      have = a.splits * a.per_split;
+    }
     f.parts = max(1, (have + a.per_split - 1) / a.per_split);
     f.pages = min(a.per_split, have - f.split * a.per_split);
     if (f.pages <= 0 && f.split) f.row = -1;  // a row without any block has one item, without pages

@@ -790,6 +790,37 @@ def test_bad_selections_are_reported(msa):
         ref.check_attention(b, [1], range(8), O.cpu(), LSE.cpu(), lambda r, g: [0, 2, 5])
 
 
+@pytest.mark.parametrize("S,G", [(2, 2), (40, 8)], ids=str)  # a row's list cut into several parts, and not cut
+@pytest.mark.parametrize("k,ids", [(8, [0] * 8), (8, [0, 1, 2, 3, 3, 3, 3, 3]), (6, [0, 1, 2, 3, 4, 5]), (128, [3] * 128),
+                                   (128, list(range(128))), (9, [0, 1, 2, 3] + [2 ** 31 - 1] * 5)],
+                         ids=["zeros", "one_again", "past_the_table", "equal_128", "all_128", "huge"])
+def test_selections_longer_than_the_page_table_are_reported(msa, S, G, k, ids):
+    """More ids than the table has columns (k may be larger): no part of a row is counted that has no place in the
+    workspace, and the other rows are as they should be."""
+    import torch
+
+    b = ref.Batch(counts=[1] * S, lens=[128 * 3 + 5 + i for i in range(S)], Hq=G, G=G, seed=1)
+    assert b.max_blocks == 4
+    bi = torch.full((S, G, k), -1, dtype=torch.int32)
+    bi[:, :, :3] = torch.tensor([0, 2, 3])
+    good = bi.clone()
+    bi[0, 1] = torch.tensor(ids, dtype=torch.int32)
+    if S > 2:
+        bi[S // 2, 0] = torch.tensor(ids, dtype=torch.int32)
+    shape, cache, t = b.gpu(k)
+    ws = msa.alloc_paged_workspace(shape, msa.MSA_WS_PAGED_SPARSE)
+    for fill in (0, 255, 1):  # (what a count of parts might be taken for)
+        ws.fill_(fill)
+        O, LSE, _ = msa.paged_sparse_attn(shape, cache, t["Q"], block_idx=bi.cuda(), workspace=ws)
+        with pytest.raises(msa.MsaError) as e:
+            msa.msa_check_device_status(ws)
+        assert e.value.status == msa.MSA_ERR_DEVICE
+        ref.check_attention(b, [1, S - 1], range(G), O.cpu(), LSE.cpu(), lambda r, g: [0, 2, 3])
+        O, LSE, _ = msa.paged_sparse_attn(shape, cache, t["Q"], block_idx=good.cuda(), workspace=ws)
+        msa.msa_check_device_status(ws)
+        ref.check_attention(b, [0, S - 1], range(G), O.cpu(), LSE.cpu(), lambda r, g: [0, 2, 3])
+
+
 # ----------------------------------------------------------------- streams, graphs, reruns
 def test_copied_cache_has_its_own_tensors(msa):
     """A deep copy is another cache: appending to it leaves the first one alone, and works after that one is gone."""
