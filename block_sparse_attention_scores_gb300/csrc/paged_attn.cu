@@ -219,10 +219,11 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const AttnItem& it
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       if (c0 + x * kJoinWarps >= cols) break;
-      const float inv = den[x] > 0.f ? 1.f / den[x] : 0.f;
+      const bool none = den[x] == 0.f;  // (NaN scores: a maximum of -infinity, too, but a sum of NaN)
+      const float inv = none ? 0.f : 1.f / den[x];
       reinterpret_cast<uint2*>(a.O + at[x] * 128)[lane] =
           make_uint2(pack_bf16(acc[x].x * inv, acc[x].y * inv), pack_bf16(acc[x].z * inv, acc[x].w * inv));
-      if (lane == 0) a.LSE[at[x]] = mm[x] > -INFINITY ? (mm[x] + log2f(den[x])) * 0.6931471805599453f : -INFINITY;
+      if (lane == 0) a.LSE[at[x]] = none ? -INFINITY : (mm[x] + log2f(den[x])) * 0.6931471805599453f;
     }
   }
 }
@@ -551,9 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           float den = fast_exp2(m - (mm == -INFINITY ? 0.f : mm)) * sh.l[lane & 7][warp];
 #pragma unroll
           for (int x = 1; x < 8; x <<= 1) den += __shfl_xor_sync(0xffffffffu, den, x);
-          if (lane == 0) {
-            sh.inv[warp] = mm > -INFINITY ? __fdividef(1.f, den) : 0.f;
-            sh.lse[warp] = mm > -INFINITY ? mm + __log2f(den) : -INFINITY;
+          if (lane == 0) {  // nothing but NaN scores: a maximum of -infinity and a sum of NaN, which stays
+            sh.inv[warp] = den == 0.f ? 0.f : __fdividef(1.f, den);
+            sh.lse[warp] = den == 0.f ? -INFINITY : mm + __log2f(den);
           }
         }
         if (!warps_sync(&sh.meet, meet_ph, a.err, 1426)) { ok = false; break; }

@@ -698,6 +698,52 @@ def test_later_rows_do_not_reach_earlier_ones(msa):
             assert bool((O[r] == clean[0][r]).all()) and bool((LSE[r] == clean[1][r]).all()), r
 
 
+# Batches of every path: single rows, rows that share a tile of eight columns, 128-row tiles (two of them, two groups),
+# behind a prefix that is read as own pages, once for the batch, or in front of 128-row tiles.
+PATHS = {
+    "single": dict(counts=[1, 1], lens=[128 * 20 + 9, 300], Hq=16, G=2),
+    "single_whole": dict(counts=[1] * 90, lens=[128 * 4 + 9 + i for i in range(90)], Hq=16, G=2),
+    "columns": dict(counts=[3, 1, 4], lens=[128 * 6 + 9, 300, 128 * 2], Hq=2, G=1),
+    "tiles": dict(counts=[20, 33], lens=[600, 128 * 9 + 40], Hq=16, G=2),
+    "tiles_two_groups": dict(counts=[5, 9], lens=[600, 128 * 9 + 40], Hq=16, G=2),
+    "folded": dict(counts=[1, 1, 1], lens=[128 * 6 + 9, 128 * 5 + 3, 128 * 7], Hq=8, G=2, prefix=5),
+    "prefix": dict(counts=[1] * 20, lens=[128 * 40 + 3 + 9 * i for i in range(20)], Hq=8, G=2, prefix=40),
+    "prefix_and_tiles": dict(counts=[3, 18], lens=[128 * 6 + 3, 128 * 6 + 400], Hq=16, G=2, prefix=6),
+}
+
+
+@pytest.mark.parametrize("name", PATHS)
+def test_nan_scores_are_reported_as_such(msa, name):
+    """A row whose visible scores are all NaN has LSE NaN (and not -infinity, which says that there was nothing to see),
+    one that sees a single NaN as well; the other rows are as without them."""
+    import torch
+
+    b = ref.Batch(seed=22, **PATHS[name])
+    clean = _dense(msa, b)
+    rows, head = [0, b.n // 2], b.hg // 2  # a head of the first group
+    for r in rows:
+        b.Q[r, head] = NAN
+    O, LSE = _dense(msa, b)
+    bad = torch.zeros(b.n, b.Hq, dtype=torch.bool)
+    bad[rows, head] = True
+    assert bool(LSE[:b.n][bad].isnan().all()) and bool(O[:b.n][bad].isnan().all())
+    assert torch.equal(LSE[:b.n][~bad], clean[1][:b.n][~bad]) and torch.equal(O[:b.n][~bad], clean[0][:b.n][~bad])
+    # a block of NaN keys, of which a row has selected nothing but, or others too
+    if not b.prefix:
+        b = ref.Batch(seed=22, **PATHS[name])
+        b.K[int(b.table[0, 1])] = NAN
+        shape, cache, t = b.gpu(16)
+        for ids in ([1], [0, 1], [1, 2], [0, 1, 2, 3]):
+            bi = torch.full((b.N, b.G, 16), -1, dtype=torch.int32)
+            bi[:, :, 0] = 0
+            bi[0, 0, :len(ids)] = torch.tensor(ids)
+            ws = msa.alloc_paged_workspace(shape, msa.MSA_WS_PAGED_SPARSE)
+            O, LSE, _ = msa.paged_sparse_attn(shape, cache, t["Q"], block_idx=bi.cuda(), workspace=ws)
+            msa.msa_check_device_status(ws)
+            assert bool(LSE[0, :b.hg].isnan().all()) and bool(O[0, :b.hg].isnan().all()), ids
+            assert not bool(LSE[0, b.hg:].isnan().any()) and not bool(LSE[1:b.n].isnan().any())
+
+
 def test_pools_past_32_bit_offsets(msa):
     """Pages whose values lie more than 2^31 elements (and 2^32 bytes) into the pools."""
     import torch
