@@ -8,7 +8,8 @@
 //   S^T = K q^T   (mma.sync, keys in rows, columns = rows of the sequence x heads of the group)
 //   P   = exp2(S scale log2 e - m), m the warp's own running maximum per column
 //   O^T += V^T P^T, P as a sum of two bf16 values (16 bits of it: the rounding
-//          of P would otherwise be as large as the output's own)
+//          of P would otherwise be as large as the output's own), both positive,
+//          so that an infinity of V comes out as such
 // with the warp's own maximum, sum and O in registers; the warps meet once per
 // item (a run of pages of one (row tile, group)). The CTA whose item is done
 // last of its (row tile, group) joins the fp32 parts in their order, so the
@@ -453,9 +454,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float p1 = fast_exp2(sc[2 * y + 1] - base[1]);
           l_run[0] += p0;
           l_run[1] += p1;
-          const uint32_t h = pack_bf16(p0, p1);
+          const uint32_t h = bf16_cut(p0, p1);
           ph[y] = movmatrix_trans(h);
-          pl[y] = movmatrix_trans(pack_bf16(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u)));
+          pl[y] = movmatrix_trans(bf16_rest(p0, p1, h));
         }
         if (!mbar_wait(&sh.v_full[st], st_ph, a.err, 1423)) { ok = false; break; }
         const int key = warp * 16 + (lane & 7) + ((lane >> 4) << 3);

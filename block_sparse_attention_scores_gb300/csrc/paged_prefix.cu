@@ -33,7 +33,7 @@
 // tile alone would leave the tensor core idle during its softmax and the memory
 // during both (32 sequences of 4 rows, 64 heads over 8 groups, 2000 tokens: 109
 // us against 92). What differs from the shared part:
-//   - P as the sum of two bf16 values, side by side over S (the second product
+//   - P as the sum of two positive bf16 values, side by side over S (the second product
 //     costs little where the memory bounds: with one row or two the same result
 //     comes from the mma.sync path, which does that too);
 //   - masks, on the pages that not every row sees all of, and V cleaned there by
@@ -130,7 +130,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-template <bool kRuns>
+// kShared: the call has a shared prefix. Without one every page is a sequence's own, and its P has both parts: told at run
+// time, as where there are both kinds, it costs 2 % (32 x 4 rows x 64 heads over 2000 tokens 63.3 -> 64.9 us).
+template <bool kRuns, bool kShared>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_prefix_kernel(PrefixArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v) {
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto load_q = [&](int g) {
         mbar_arrive_expect_tx(&sh.q_full, 2 * kTile);
-  #pragma unroll
+#pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int row0 = (2 * pair + t) * tile_rows;  // rows past N arrive as zeros
           tma_load_3d(smem + oQ + t * kTile, &map_q, &sh.q_full, 0, g * a.hg, row0);
@@ -590,22 +592,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto write_p = [&]() {
           float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
           const float base = kRuns && m_run == -INFINITY ? 0.f : m_run;  // (nothing seen: exp2(-inf - 0) = 0)
+          if (kRuns && (!kShared || run.own)) {
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint32_t pk[8], rest[8];
+            for (int h = 0; h < 4; ++h) {
+              uint32_t pk[8], rest[8];
 #pragma unroll
-            for (int z = 0; z < 8; ++z) {
-              float p0 = sv[16 * h + 2 * z], p1 = sv[16 * h + 2 * z + 1];
-              fma2(p0, p1, a.scale_log2, -base);
-              p0 = fast_exp2(p0);
-              p1 = fast_exp2(p1);
-              if (z & 1) add2(t0, t1, p0, p1);
-              else add2(s0, s1, p0, p1);
-              pk[z] = pack_bf16(p0, p1);
-              if (kRuns) rest[z] = pack_bf16(p0 - __uint_as_float(pk[z] << 16), p1 - __uint_as_float(pk[z] & 0xffff0000u));
+              for (int z = 0; z < 8; ++z) {
+                float p0 = sv[16 * h + 2 * z], p1 = sv[16 * h + 2 * z + 1];
+                fma2(p0, p1, a.scale_log2, -base);
+                p0 = fast_exp2(p0);
+                p1 = fast_exp2(p1);
+                if (z & 1) add2(t0, t1, p0, p1);
+                else add2(s0, s1, p0, p1);
+                pk[z] = bf16_cut(p0, p1);
+                rest[z] = bf16_rest(p0, p1, pk[z]);
+              }
+              tmem_st8(s_at + 8 * h, pk);
+              tmem_st8(s_at + 32 + 8 * h, rest);
             }
-            tmem_st8(s_at + 8 * h, pk);
-            if (kRuns && run.own) tmem_st8(s_at + 32 + 8 * h, rest);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              uint32_t pk[8];
+#pragma unroll
+              for (int z = 0; z < 8; ++z) {
+                float p0 = sv[16 * h + 2 * z], p1 = sv[16 * h + 2 * z + 1];
+                fma2(p0, p1, a.scale_log2, -base);
+                p0 = fast_exp2(p0);
+                p1 = fast_exp2(p1);
+                if (z & 1) add2(t0, t1, p0, p1);
+                else add2(s0, s1, p0, p1);
+                pk[z] = pack_bf16(p0, p1);
+              }
+              tmem_st8(s_at + 8 * h, pk);
+            }
           }
           l_add = (s0 + s1) + (t0 + t1);
         };
@@ -730,17 +750,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <bool kRuns>
+template <bool kRuns, bool kShared>
 cudaError_t launch_prefix(const PrefixArgs& a, int blocks, const CUtensorMap& mq, const PoolMaps& maps, cudaStream_t st) {
   static bool attr[kMaxDevices] = {};
   const int dslot = device_slot();
   if (!attr[dslot]) {
-    cudaError_t e = cudaFuncSetAttribute(paged_prefix_kernel<kRuns>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    cudaError_t e = cudaFuncSetAttribute(paged_prefix_kernel<kRuns, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     attr[dslot] = true;
   }
   count_launches(1);
-  return launch_dependent(paged_prefix_kernel<kRuns>, blocks, kThreads, kSmem, st, a, mq, maps.k, maps.v);
+  return launch_dependent(paged_prefix_kernel<kRuns, kShared>, blocks, kThreads, kSmem, st, a, mq, maps.k, maps.v);
 }
 
 }  // namespace
@@ -780,7 +800,8 @@ cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, con
   a.per_run = L.per_run;
   a.rslots = L.rslots;
   a.pslots = L.pslots;
-  return L.run_rows ? launch_prefix<true>(a, L.n_flags, mq, maps, st) : launch_prefix<false>(a, L.n_flags, mq, maps, st);
+  if (!L.run_rows) return launch_prefix<false, true>(a, L.n_flags, mq, maps, st);
+  return L.prefix ? launch_prefix<true, true>(a, L.n_flags, mq, maps, st) : launch_prefix<true, false>(a, L.n_flags, mq, maps, st);
 }
 
 }  // namespace msa

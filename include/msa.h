@@ -326,6 +326,11 @@ MSA_API msa_status msa_dense_bwd(const msa_shape *shape, const void *Q, const vo
  * (2^20 tokens), num_pages * G < 2^24. Two calls may run at the same time if
  * they have workspaces of their own. All results are the same bits in every
  * run on the same inputs.
+ *
+ * Values that are not finite, where a row sees them: an infinity in V gives
+ * that infinity in O (both signs, or NaN, give NaN), in the dims that have it
+ * alone, unless the token's probability is below 2^-126; a NaN score gives NaN
+ * in the row's O and LSE.
  */
 typedef struct msa_paged_shape {
   int32_t S;             /* sequences                                            */

@@ -744,6 +744,66 @@ def test_nan_scores_are_reported_as_such(msa, name):
             assert not bool(LSE[0, b.hg:].isnan().any()) and not bool(LSE[1:b.n].isnan().any())
 
 
+def _with_infinities(b, clean, blocks_of):
+    """What rows are to have whose V holds infinities or NaN in some places: those (every visible token counts for more
+    than 0), and `clean`, the result without them, elsewhere."""
+    import torch
+
+    want = clean.clone()
+    for r in range(b.n):
+        for g in range(b.G):
+            blocks = [c for c in blocks_of(r, g) if c >= 0]
+            v = b.V[b.table[b.row_seq[r], blocks].long(), g].reshape(-1, 128).float()
+            token = (torch.tensor(blocks)[:, None] * 128 + torch.arange(128)).reshape(-1)
+            odd = torch.where(v.isfinite(), 0.0, v)[token <= b.row_pos[r]].sum(0).to(torch.bfloat16)
+            heads = slice(g * b.hg, (g + 1) * b.hg)
+            want[r, heads] = torch.where(odd == 0, want[r, heads], odd)
+    return want
+
+
+@pytest.mark.parametrize("name", PATHS)
+def test_infinite_values(msa, name):
+    """An infinity in V, in the cache or among the new rows, gives that infinity wherever it is seen (both signs, or NaN:
+    NaN), and changes nothing else. Some tokens have the row's largest score, whose probability is 1 before the sum."""
+    import torch
+
+    b = ref.Batch(seed=23, **PATHS[name])
+    clean = _dense(msa, b)
+    shape, cache, t = b.gpu(3)
+    last = torch.tensor([p // 128 for p in b.row_pos])
+    bi = torch.full((b.N, b.G, 3), -1, dtype=torch.int32)
+    bi[:b.n, :, 0], bi[:b.n, :, 1] = 0, last[:, None]
+    bi[:b.n][last == 0, :, 1] = -1
+    sparse = (lambda r, g: bi[r, g].tolist())
+    clean_s = msa.paged_sparse_attn(shape, cache, t["Q"], block_idx=bi.cuda())
+    clean_s = [x[:b.n].cpu() for x in clean_s[:2]]
+    rng = np.random.default_rng(1)
+    for s in range(b.S):
+        pages = b.table[s, :-(-b.lens[s] // 128)].tolist()
+        for c, page in enumerate(pages):
+            end = min(128, b.lens[s] - 128 * c)
+            b.V[page, :, :end, 3] = INF             # every token, the one with the largest score among them
+            b.V[page, :, rng.integers(end), 17] = -INF
+            if c == len(pages) - 1:                 # among the new rows
+                b.V[page, :, end - 1, 40] = INF
+            if c == 0:
+                b.V[page, :, 5, 64] = INF           # both signs
+                b.V[page, :, 9, 64] = -INF
+                b.V[page, :, 11, 90] = NAN
+                b.V[page, 0, 127, 127] = INF
+    O, LSE = _dense(msa, b)
+    assert torch.equal(LSE[:b.n], clean[1][:b.n])
+    want = _with_infinities(b, clean[0][:b.n], _all(b))
+    assert torch.equal(O[:b.n].nan_to_num(nan=1e30, posinf=2e30, neginf=-2e30), want.nan_to_num(nan=1e30, posinf=2e30, neginf=-2e30))
+    assert int(want.isnan().sum()) and int((want == INF).sum()) and int((want == -INF).sum())
+    t["V"].copy_(b.V)
+    O, LSE, _ = msa.paged_sparse_attn(shape, cache, t["Q"], block_idx=bi.cuda())
+    assert torch.equal(LSE[:b.n].cpu(), clean_s[1])
+    want = _with_infinities(b, clean_s[0], sparse)
+    assert torch.equal(O[:b.n].cpu().nan_to_num(nan=1e30, posinf=2e30, neginf=-2e30),
+                       want.nan_to_num(nan=1e30, posinf=2e30, neginf=-2e30))
+
+
 def test_pools_past_32_bit_offsets(msa):
     """Pages whose values lie more than 2^31 elements (and 2^32 bytes) into the pools."""
     import torch
