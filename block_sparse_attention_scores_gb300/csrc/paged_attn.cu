@@ -652,13 +652,14 @@ __global__ void __launch_bounds__(kMergeThreads, 6) paged_merge_kernel(MergeArgs
     float top = m;
 #pragma unroll
     for (int j = 0; j < 8; ++j) top = fmaxf(top, lse[j]);
-    const float old = fast_exp2(m - top);  // (the first own part sees the row's own token: top is finite)
+    const float base = top == -INFINITY ? 0.f : top;  // (parts whose scores are all -infinity)
+    const float old = fast_exp2(m - base);
     m = top;
     den *= old;
     acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float w = fast_exp2(lse[j] - m);
+      const float w = fast_exp2(lse[j] - base);
       den += w;
       acc.x = fmaf(w, v[j].x, acc.x);
       acc.y = fmaf(w, v[j].y, acc.y);

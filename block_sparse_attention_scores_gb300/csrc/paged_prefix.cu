@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float l_add = 0.f;
         auto write_p = [&]() {
           float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
-          const float base = kRuns && m_run == -INFINITY ? 0.f : m_run;  // (nothing seen: exp2(-inf - 0) = 0)
+          const float base = m_run == -INFINITY ? 0.f : m_run;  // (nothing but -infinity so far: exp2(-inf - 0) = 0)
           if (kRuns && (!kShared || run.own)) {
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int group = run.g + (twin ? t : 0);
       const size_t at = ((size_t)run.slot * a.N + row) * a.Hq + group * a.hg + lrow % a.hg;
       const bool odd = kRuns && run.own && sh.odd[(n_run - 1) & 1];
-      const float inv = kRuns && l == 0.f ? 0.f : 1.f / l;  // (a run behind the row's end)
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // (a run behind the row's end, or scores of -infinity)
       float* dst = a.part_o + at * 128 + half * 64;
 #pragma unroll
       for (int z = 0; z < 4; ++z) {

@@ -804,6 +804,27 @@ def test_infinite_values(msa, name):
                        want.nan_to_num(nan=1e30, posinf=2e30, neginf=-2e30))
 
 
+@pytest.mark.parametrize("name", [*PATHS, "one_long"])
+def test_keys_that_nobody_attends_to(msa, name):
+    """Scores of -infinity (an infinite key value) count for nothing: in the first page, on whole runs of pages, on the
+    whole shared prefix, on every page but the row's own."""
+    kw = PATHS.get(name) or dict(counts=[1], lens=[128 * 240 + 9], Hq=8, G=8, prefix=200)
+    for which in ("first", "prefix", "all but the own"):
+        b = ref.Batch(seed=24, **kw)
+        assert min(b.row_pos) >= 128
+        b.Q[:, :, 0] = 1.0
+        own = [min(p for p, s in zip(b.row_pos, b.row_seq) if s == i) // 128 for i in range(b.S)]  # of the first row
+        n = {"first": [1] * b.S, "prefix": [max(1, b.prefix)] * b.S, "all but the own": own}[which]
+        for s in range(b.S):
+            for c in range(n[s]):
+                b.K[int(b.table[s, c]), :, :, 0] = -INF
+        # (in a page that is shared, all the tokens)
+        O, LSE = _dense(msa, b)
+        rows = range(b.n) if b.n < 30 else range(0, b.n, 7)
+        ref.check_attention(b, rows, range(0, b.Hq, 3), O, LSE,
+                            lambda r, g: list(range(n[b.row_seq[r]], b.row_pos[r] // 128 + 1)), bf16_p=b.prefix > 5)
+
+
 def test_pools_past_32_bit_offsets(msa):
     """Pages whose values lie more than 2^31 elements (and 2^32 bytes) into the pools."""
     import torch
