@@ -64,10 +64,14 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
     // Against eight columns at a time: 32 sequences of 2 rows x 64 heads over 2000 tokens 63 -> 62 us, of 8 rows 135 -> 71,
     // 300 rows x 32 heads over 8000 274 -> 64; the other way for one page (8 rows x 64 heads over 100 tokens 17 -> 10).
     const bool runs = (long long)p.N * p.hg > 9LL * p.S && p.max_blocks - p.prefix > 1;
-    // A shared prefix of ten pages an SM, counted for every sequence, is read as own pages: it stays in L2, and two kernels
-    // do with it what four do. 4 sequences of 32 heads over 8 groups behind 16 pages 15 us against 20, 16 behind 8 pages 16
-    // and 22, 8 of 16 heads over 2 groups behind 64 pages 19 and 23; beyond: 8 of 32 heads over 4 groups behind 100 33 and 28.
-    const bool fold = !runs && (long long)p.S * p.prefix * p.G <= 1500;
+    // A shared prefix of ten pages an SM (13 where a sequence has several tiles of eight columns), counted for every such
+    // tile, is read as own pages: it stays in L2, and two kernels do with it what four do. 4 sequences of 32 heads over 8
+    // groups behind 16 pages 15 us against 19, 16 behind 8 pages 14 and 19, 8 of 4 rows behind 12 pages (1536) 17 and 21,
+    // one of 16 rows x 64 heads over 8 groups behind 10 pages (1280) 15 and 21, of 64 x 32 heads behind 6 (1536) 19 and
+    // 23; beyond: 16 rows x 64 heads behind 50 pages (6400) 50 and 29, 64 behind 6 (3072) 30 and 25, 128 behind 10 (10240) 66 and 41, behind 180
+    // (1,440 pages, read 128 times) 797 and 99.
+    const long long tiles = std::max(p.N / L.tile_rows, std::min(p.S, p.N));
+    const bool fold = !runs && tiles * p.prefix * p.G <= (tiles > p.S ? 2000 : 1500);
     L.prefix = fold ? 0 : p.prefix;
     if (runs) {
       L.run_rows = 256 / p.hg;
@@ -77,8 +81,7 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
       L.splits = 0;
       L.n_flags = kCutSms;
     } else {
-      cut_pages((long long)std::max(p.N / L.tile_rows, std::min(p.S, p.N)) * p.G, p.max_blocks - L.prefix, L.prefix ? 1 : 6,
-                L.prefix ? 0 : 8, &L.per_split, &L.splits);
+      cut_pages(tiles * p.G, p.max_blocks - L.prefix, L.prefix ? 1 : 6, L.prefix ? 0 : 8, &L.per_split, &L.splits);
     }
     if (L.prefix > 0) {
       const int tiles = (int)(((long long)p.N * p.hg + 127) / 128);
@@ -89,7 +92,7 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
       // 2,000; own pages: half of what the table holds), and the prefix has half of the SMs at least, lest a poor estimate
       // make it the longer one. 64 sequences behind 32K tokens with up to 2K of their own: 112 us one after the other,
       // 100 with two thirds, 94 with half, 102 with 0.35 of the SMs; 100 sequences with 2000 each: 67, 49, 48, 48.
-      const double own = (double)std::max(p.N / L.tile_rows, std::min(p.S, p.N)) * p.G * (p.max_blocks - p.prefix + 1) / 2 * 2000;
+      const double own = (double)tiles * p.G * (p.max_blocks - p.prefix + 1) / 2 * 2000;
       const double shared = (double)units * L.pairs * 2750;
       const int sms = L.run_rows ? kCutSms : (int)(kCutSms * std::max(0.5, shared / (shared + own)));
       L.teams = std::min(units, std::max(1, sms / L.pairs));

@@ -286,3 +286,19 @@ def test_tensors_of_a_cache_are_not_replaced(msa, kind, names):
     for c in (copy.copy(rope), copy.deepcopy(rope), pickle.loads(pickle.dumps(rope))):
         assert c._addr == ctypes.addressof(c._struct) != rope._addr
         assert (c._struct.rot_dim, c._struct.rot_dim_idx, c._struct.interleaved) == (0, 0, 1)
+
+
+def _slots(msa, shape):
+    """Parts of a row's output that the full call's workspace has room for."""
+    return msa.msa_paged_workspace_size(shape, msa.MSA_WS_PAGED_DENSE) // (shape.N * shape.Hq * 516)
+
+
+@pytest.mark.parametrize("kw", [dict(S=1, N=128, Hq=64, G=8, prefix_blocks=187), dict(S=2, N=64, Hq=64, G=8, prefix_blocks=60),
+                                dict(S=1, N=127, Hq=32, G=8, prefix_blocks=50), dict(S=4, N=128, Hq=64, G=8, prefix_blocks=40)],
+                         ids=str)
+def test_a_prefix_that_many_rows_read_is_shared(msa, kw):
+    """A prefix is read as own pages where that is little work: its pages count once for every tile of eight columns, not
+    once for every sequence (one sequence's 128 rows would read theirs 128 times)."""
+    shape = msa.PagedShape(**kw, num_pages=1000, max_blocks=kw["prefix_blocks"] + 1)
+    # (one part of the own page, and the prefix cut into more than one; read as own pages it is not cut at all)
+    assert _slots(msa, shape) >= 3

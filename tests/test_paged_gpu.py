@@ -395,6 +395,19 @@ def test_dense_prefix_same_bits(msa):
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("stale", [NAN, INF], ids=["nan", "inf"])
+@pytest.mark.parametrize("counts,lens,Hq,G,prefix", [([127], [128 * 60 + 127], 16, 2, 60), ([16], [128 * 200 + 50], 8, 1, 200),
+                                                     ([40, 0, 9], [128 * 30 + 128, 4, 128 * 30 + 77], 24, 3, 30)], ids=str)
+def test_dense_chunk_of_a_page_behind_a_prefix(msa, counts, lens, Hq, G, prefix, stale):
+    """Many rows of a sequence whose own part is one page: the pages before it are read once for all of them."""
+    b = ref.Batch(counts=counts, lens=lens, Hq=Hq, G=G, prefix=prefix, seed=27, stale=stale, pad=1)
+    before = msa.msa_kernel_launches()
+    O, LSE = _dense(msa, b)
+    assert msa.msa_kernel_launches() - before == 4  # rows, prefix, own pages, merge
+    ref.check_attention(b, range(0, b.n, 5), range(0, b.Hq, 3), O, LSE, _all(b), bf16_p=True)
+    _check_padding(b, O, LSE)
+
+
 # Several rows per sequence: more than eight columns on average and more than a page take 128-row tiles (of 128 / h_g
 # rows, two at a time).
 RUNS = {
