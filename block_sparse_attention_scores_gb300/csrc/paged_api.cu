@@ -132,6 +132,8 @@ static msa_status validate_paged(const msa_paged_shape* s, PagedProb* p) {
   if (s->S > 65535) return fail(MSA_ERR_UNSUPPORTED, "S=%d exceeds 65535 sequences", s->S);
   if (s->max_blocks > 8192) return fail(MSA_ERR_UNSUPPORTED, "max_blocks=%d exceeds 8192 (2^20 tokens)", s->max_blocks);
   if (s->N > (1 << 20)) return fail(MSA_ERR_UNSUPPORTED, "N=%d exceeds 2^20 rows", s->N);
+  // (items of a row's vectors are counted in fp32 and 32 bits, pages times groups in 32)
+  if (s->Hq > 65536) return fail(MSA_ERR_UNSUPPORTED, "Hq=%d exceeds 65536 heads", s->Hq);
   if ((long long)s->N * s->Hq > (1LL << 28)) return fail(MSA_ERR_UNSUPPORTED, "N*Hq too large");
   if ((long long)s->num_pages * s->G > (1LL << 24) - 1)
     return fail(MSA_ERR_UNSUPPORTED, "num_pages*G=%lld: at most 2^24 - 1 page tiles are addressed",

@@ -322,8 +322,8 @@ MSA_API msa_status msa_dense_bwd(const msa_shape *shape, const void *Q, const vo
  * unspecified; nothing is read or written out of range.
  *
  * Supported: d = 128, d_idx = 64, Bk = 128, Hq / G in {1, 2, 4, 8},
- * 1 <= k <= 128, S <= 65535, N <= 2^20 (N * Hq <= 2^28), max_blocks <= 8192
- * (2^20 tokens), num_pages * G < 2^24. Two calls may run at the same time if
+ * 1 <= k <= 128, S <= 65535, N <= 2^20, Hq <= 65536 (N * Hq <= 2^28),
+ * max_blocks <= 8192 (2^20 tokens), num_pages * G < 2^24. Two calls may run at the same time if
  * they have workspaces of their own. All results are the same bits in every
  * run on the same inputs.
  *

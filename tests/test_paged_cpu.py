@@ -302,3 +302,16 @@ def test_a_prefix_that_many_rows_read_is_shared(msa, kw):
     shape = msa.PagedShape(**kw, num_pages=1000, max_blocks=kw["prefix_blocks"] + 1)
     # (one part of the own page, and the prefix cut into more than one; read as own pages it is not cut at all)
     assert _slots(msa, shape) >= 3
+
+
+@pytest.mark.parametrize("Hq,G", [(65544, 65544), (1 << 17, 1 << 17), (1 << 23, 1 << 20), (1 << 27, 1 << 24)], ids=str)
+def test_more_heads_than_are_counted(msa, Hq, G):
+    """A row of more than 2^22 16-byte pieces would lose its last ones, and pages times groups leave 32 bits."""
+    s = _shape(msa, N=1, S=1, Hq=Hq, G=G, num_pages=1, max_blocks=8192)
+    for which in range(3):
+        assert msa.msa_paged_workspace_size(s, which) == 0
+    for call in (_append, _sparse, _dense):
+        st, msg = call(msa, shape=s.c())
+        assert st == msa.MSA_ERR_UNSUPPORTED and ("Hq" in msg or "G" in msg)
+    s = _shape(msa, N=1, S=1, Hq=65536, G=65536, num_pages=1, max_blocks=8)
+    assert msa.msa_paged_workspace_size(s, msa.MSA_WS_PAGED_DENSE) > 0
