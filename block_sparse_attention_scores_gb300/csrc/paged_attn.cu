@@ -39,7 +39,9 @@ constexpr int kThreads = (kWarps + 1 + kJoinWarps) * 32;
 constexpr int kHalf = 16384;                       // 128 rows x 64 bf16, 128-byte swizzle
 constexpr int kTile = 2 * kHalf;                   // K or V of a page and group
 constexpr int kStages = 3;
-constexpr unsigned long long kIdleLimitNs = 20000000000ull;  // the joining warps may have nothing to do for a while
+// The joining warps may have nothing to do until the kernel's end: 20 s, and 20 us for every page that a CTA takes if it
+// takes them all in turn (it takes 1.5).
+constexpr unsigned long long kIdleNs = 20000000000ull, kIdlePageNs = 20000ull;
 
 constexpr int kQStride = 272;                      // bytes between the queries' rows in shared memory (no bank conflicts)
 
@@ -62,6 +64,7 @@ struct AttnArgs {
   const int* flags;                       // [n_flags] of the first kernel's blocks
   int n_flags;
   int* err;
+  unsigned long long idle_ns;
 };
 
 struct AttnItem {
@@ -350,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (blockIdx.x == 0 && warp == kWarps + 1) report_flags(a.flags, a.n_flags, a.err, lane);
     for (int n_join = 0;; ++n_join) {
       const int js = n_join & 1;
-      if (!mbar_wait(&sh.j_full[js], (n_join >> 1) & 1, a.err, 1431, kIdleLimitNs)) break;
+      if (!mbar_wait(&sh.j_full[js], (n_join >> 1) & 1, a.err, 1431, a.idle_ns)) break;
       const AttnItem item = sh.join[js];
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.j_empty[js]);
@@ -723,6 +726,7 @@ cudaError_t launch_paged_attn(const PagedProb& p, const PagedCachePtrs& c, const
   a.beside = L.pslots > 0;
   a.n_flags = a.beside ? 0 : L.n_flags;
   a.err = reinterpret_cast<int*>(ws);
+  a.idle_ns = kIdleNs + kIdlePageNs * L.per_split * (a.items / std::min(a.items, num_sms()) + 1);
   return launch_attn(a, maps.k, maps.v, st);
 }
 

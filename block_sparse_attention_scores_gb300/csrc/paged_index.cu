@@ -46,6 +46,7 @@ struct ScoreArgs {
   int S, N, G, num_pages, max_blocks, runs, items;
   int* flags;  // [blocks but the last] what a block found wrong
   RowsArgs rows;
+  unsigned long long wait_ns;  // a stage may be held for as long as a page takes a warp: the longer, the more columns
 };
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       const int page = bad ? 0 : now.page, cols = rows * a.G;
       for (unsigned m = __ballot_sync(0xffffffffu, want); m; m &= m - 1, ++n) {
         const int from = __ffs(m) - 1, st = n % kScoreStages;
-        if (!mbar_wait(&sh.empty[st], ((n / kScoreStages) & 1) ^ 1, &sh.flag, 1302)) { ok = false; break; }
+        if (!mbar_wait(&sh.empty[st], ((n / kScoreStages) & 1) ^ 1, &sh.flag, 1302, a.wait_ns)) { ok = false; break; }
         if (lane == from) {
           sh.info[st] = make_int4(now.s, bad ? ~now.c : now.c, now.begin, cols);
           const int first = min(cols, 8);
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     }
     for (int i = 0; i < kScoreWarps && ok; ++i, ++n) {  // the end, for every warp
       const int st = n % kScoreStages;
-      ok = mbar_wait(&sh.empty[st], ((n / kScoreStages) & 1) ^ 1, &sh.flag, 1302);
+      ok = mbar_wait(&sh.empty[st], ((n / kScoreStages) & 1) ^ 1, &sh.flag, 1302, a.wait_ns);
       if (ok && lane == 0) {
         sh.info[st].x = -1;
         mbar_arrive(&sh.full[st]);
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     const int r = lane >> 2, q = lane & 3;
     for (int n = warp;; n += kScoreWarps) {
       const int st = n % kScoreStages;
-      if (!mbar_wait(&sh.full[st], (n / kScoreStages) & 1, &sh.flag, 1303)) break;
+      if (!mbar_wait(&sh.full[st], (n / kScoreStages) & 1, &sh.flag, 1303, a.wait_ns)) break;
       const int4 info = sh.info[st];
       if (info.x < 0) break;
       const bool bad = info.y < 0;
@@ -558,6 +559,7 @@ cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, cons
   a.max_blocks = p.max_blocks;
   a.flags = reinterpret_cast<int*>(ws + L.flags);
   a.rows = rows_args(p, c, ws, L);
+  a.wait_ns = kWaitLimitNs + 1000ull * p.N * p.G;  // eight columns take under a microsecond
   if (L.n_flags > 0) {
     CUtensorMap mk;
     const uint64_t dims[2] = {64, (uint64_t)p.num_pages * 128};

@@ -534,6 +534,17 @@ def test_sparse_whole_rows_many(msa):
     ref.check_attention(b, [0, 5, 1599], range(2), O, LSE, lambda r, g: bi[r, g].tolist())
 
 
+def test_sparse_prompt(msa):
+    """A prompt's thousands of rows (and a single one beside it): a page's scores take as many columns as rows and groups."""
+    b = ref.Batch(counts=[4000, 1], lens=[128 * 40 + 3, 128 * 33], Hq=8, G=4, seed=35, pad=2)
+    O, LSE, bi = _sparse(msa, b, 4)
+    some = [0, 1, 127, 128, 1999, 3990, 3999, 4000]
+    for r in some:
+        np.testing.assert_array_equal(bi[r], ref.select(b, r, 4), err_msg=f"row {r}")
+    ref.check_attention(b, some, range(8), O, LSE, lambda r, g: bi[r, g].tolist())
+    _check_padding(b, O, LSE, bi)
+
+
 @pytest.mark.parametrize("blocks", [256, 257, 258, 2049, 2050])
 def test_selection_threads_change(msa, blocks):
     """Page tables of the widths around which the selection's block of threads grows."""
