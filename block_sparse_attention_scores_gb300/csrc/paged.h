@@ -32,7 +32,8 @@ struct PagedWs {
   int n_flags = 0;      // those blocks
   size_t arrived = 0;   // int32 [N, G, 3] parts of a (row tile, group) that are done, as each joining warp counts them
   size_t pooled = 0;    // fp32 [N, G, max_blocks, 2] block maxima of the index scores, and the block's largest |key| value
-  size_t part_o = 0;    // fp32 [pslots + rslots or splits, N, Hq, d] partial outputs (normalised)
+                        //      (none where nothing is chosen: one block kept, or one column)
+  size_t part_o = 0;    // fp32 [pslots + rslots or splits, N, Hq, d] partial outputs (normalised; none for a single split)
   size_t part_lse = 0;  // fp32 [pslots + rslots or splits, N, Hq]    their log2-sum-exp2
   size_t total = 256;
   int splits = 1;       // partials a row's own pages are cut into ...

@@ -53,7 +53,7 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
   L.lead = take((size_t)p.N * 16);
   L.arrived = take((size_t)p.N * p.G * 12);
   if (which == MSA_WS_PAGED_SPARSE) {
-    L.pooled = take((size_t)p.N * p.G * p.max_blocks * 8);
+    if (p.k > 1 && p.max_blocks > 1) L.pooled = take((size_t)p.N * p.G * p.max_blocks * 8);
     if (p.k > 1) L.n_flags = (int)std::min<long long>((long long)p.S * ((p.max_blocks + 4) / 6), kCutSms - 1);
     L.flags = take(kCutSms * 4);
     cut_pages((long long)p.N * p.G, std::min(p.k, p.max_blocks), 6, 8, &L.per_split, &L.splits);
@@ -103,7 +103,9 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
     }
     L.flags = take((size_t)L.n_flags * 4);
   }
-  const size_t rows = (size_t)(L.pslots + L.rslots + L.splits) * p.N * p.Hq;
+  // (a row's only part, which no other joins, is its result)
+  const int slots = L.pslots + L.rslots + (L.pslots || L.splits > 1 ? L.splits : 0);
+  const size_t rows = (size_t)slots * p.N * p.Hq;
   L.part_o = take(rows * 128 * 4);
   L.part_lse = take(rows * 4);
   L.total = off;

@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
 #pragma unroll
   for (int z = 0; z < kSelItems; ++z) {  // (before it is known how many of them there are)
     const int i = z * kThreads + tid;
-    const float2 f = i < a.max_blocks ? ld_in(v + i) : make_float2(-INFINITY, 0.f);
+    const float2 f = a.k > 1 && i < a.max_blocks - 1 ? ld_in(v + i) : make_float2(-INFINITY, 0.f);
     x[z] = f.x;
     e[z] = f.y;
   }

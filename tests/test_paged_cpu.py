@@ -315,3 +315,23 @@ def test_more_heads_than_are_counted(msa, Hq, G):
         assert st == msa.MSA_ERR_UNSUPPORTED and ("Hq" in msg or "G" in msg)
     s = _shape(msa, N=1, S=1, Hq=65536, G=65536, num_pages=1, max_blocks=8)
     assert msa.msa_paged_workspace_size(s, msa.MSA_WS_PAGED_DENSE) > 0
+
+
+def test_workspaces_hold_what_is_written(msa):
+    """No parts of outputs where rows are not cut, no block maxima where nothing is chosen between blocks."""
+    def sparse(**kw):
+        return msa.msa_paged_workspace_size(
+            msa.PagedShape(**{**dict(S=1, N=32768, Hq=64, G=8, num_pages=1000, max_blocks=256, k=16), **kw}), msa.MSA_WS_PAGED_SPARSE)
+
+    rows = 32768 * (32 + 8 * 12)          # their places, and counters
+    pooled = 32768 * 8 * 256 * 8          # a block's maximum and its keys' largest value
+    assert rows + pooled <= sparse() < rows + pooled + 4096
+    assert rows <= sparse(k=1) < rows + 4096
+    assert sparse(max_blocks=1) < rows + 4096
+    dense = msa.msa_paged_workspace_size(msa.PagedShape(S=32768, N=32768, Hq=64, G=8, num_pages=1000, max_blocks=2),
+                                         msa.MSA_WS_PAGED_DENSE)
+    assert rows <= dense < rows + 4096
+    # few rows are cut: as many parts as before
+    one = msa.msa_paged_workspace_size(msa.PagedShape(S=1, N=1, Hq=32, G=8, num_pages=1000, max_blocks=100),
+                                       msa.MSA_WS_PAGED_DENSE)
+    assert one > 2 * 32 * 516

@@ -534,6 +534,29 @@ def test_sparse_whole_rows_many(msa):
     ref.check_attention(b, [0, 5, 1599], range(2), O, LSE, lambda r, g: bi[r, g].tolist())
 
 
+@pytest.mark.parametrize("k,lens", [(1, [700] * 90), (3, [128] * 200), (4, [128 * 9 + 3] * 90), (1, [5])], ids=str)
+def test_workspaces_of_the_least_size(msa, k, lens):
+    """Calls that need no block maxima, or no parts, leave what lies behind their workspace alone."""
+    import torch
+
+    b = ref.Batch(counts=[1] * len(lens), lens=lens, Hq=8, G=2, seed=36)
+    shape, cache, t = b.gpu(k)
+    for which in (msa.MSA_WS_PAGED_SPARSE, msa.MSA_WS_PAGED_DENSE):
+        n = msa.msa_paged_workspace_size(shape, which)
+        buf = torch.full((n + (1 << 20),), 255, dtype=torch.uint8, device="cuda")
+        if which == msa.MSA_WS_PAGED_SPARSE:
+            O, LSE, bi = msa.paged_sparse_attn(shape, cache, t["Q"], t["q_idx"], workspace=buf[:n])
+            for r in (0, b.n - 1):
+                np.testing.assert_array_equal(bi[r].cpu().numpy(), ref.select(b, r, k))
+            blocks = (lambda r, g: bi[r, g].tolist())
+        else:
+            O, LSE = msa.paged_dense_attn(shape, cache, t["Q"], workspace=buf[:n])
+            blocks = _all(b)
+        msa.msa_check_device_status(buf)
+        ref.check_attention(b, sorted({0, b.n // 2, b.n - 1}), range(8), O.cpu(), LSE.cpu(), blocks)
+        assert bool((buf[n:] == 255).all())
+
+
 def test_sparse_prompt(msa):
     """A prompt's thousands of rows (and a single one beside it): a page's scores take as many columns as rows and groups."""
     b = ref.Batch(counts=[4000, 1], lens=[128 * 40 + 3, 128 * 33], Hq=8, G=4, seed=35, pad=2)
