@@ -872,6 +872,104 @@ def test_keys_that_nobody_attends_to(msa, name):
                             lambda r, g: list(range(n[b.row_seq[r]], b.row_pos[r] // 128 + 1)), bf16_p=b.prefix > 5)
 
 
+def _slots(msa, shape):
+    """Parts of a row's output that the full call's workspace has room for."""
+    return msa.msa_paged_workspace_size(shape, msa.MSA_WS_PAGED_DENSE) // (shape.N * shape.Hq * 516)
+
+
+def _rising(b, pages, step=0.8, again=40):
+    """Scores that grow from page to page, by turns those of a page's first half, of its second one, and of all its keys."""
+    for i, page in enumerate(pages):
+        f = 1 + step * (i % again)
+        b.K[page, :, :64] *= f if i % 3 != 1 else 0.25
+        b.K[page, :, 64:] *= f if i % 3 != 0 else 0.25
+
+
+# Prefixes whose runs of pages are long: over more pages than are looked up at a time, and from one group to the next.
+LONG = {
+    "g3_hg8": dict(S=340, rows=1, blocks=203, Hq=24, G=3, prefix=201),
+    "g7_hg4": dict(S=300, rows=2, blocks=101, Hq=28, G=7, prefix=100),
+    "g2_hg1": dict(S=1500, rows=1, blocks=402, Hq=2, G=2, prefix=401),
+    "tiles_g8_hg2": dict(S=200, rows=5, blocks=106, Hq=16, G=8, prefix=100),
+    "tiles_g5_hg8": dict(S=30, rows=19, blocks=153, Hq=40, G=5, prefix=150),
+}
+
+
+@pytest.mark.parametrize("rising", [False, True], ids=["even", "rising"])
+@pytest.mark.parametrize("name", LONG)
+def test_dense_prefix_long_runs(msa, name, rising):
+    kw = dict(LONG[name])
+    prefix, blocks = kw.pop("prefix"), kw.pop("blocks")
+    b = _shared_pages(length=128 * blocks - 70, seed=41, **kw)
+    b.prefix = prefix
+    if rising:
+        _rising(b, b.table[0, :prefix].tolist())
+    shape, _, _ = b.gpu()
+    before = msa.msa_kernel_launches()
+    O, LSE = _dense(msa, b)
+    assert msa.msa_kernel_launches() - before == (3 if name.startswith("tiles") else 4)
+    # parts of a row: the prefix's and at least one of its own pages
+    assert prefix / (_slots(msa, shape) - 1) > 20
+    rows = sorted({0, 1, 15, 16, 17, b.n // 2, b.n - 1})
+    ref.check_attention(b, rows, range(0, b.Hq, 5 if b.Hq > 8 else 1), O, LSE, _all(b), bf16_p=True)
+
+
+@pytest.mark.parametrize("S,rows,blocks,Hq,G", [(90, 5, 12, 16, 8), (60, 70, 11, 16, 8), (160, 9, 10, 24, 3), (170, 3, 40, 8, 1)],
+                         ids=["twin", "two_tiles", "one_tile", "one_group"])
+def test_dense_rows_rising_scores(msa, S, rows, blocks, Hq, G):
+    """Runs of several own pages whose maxima rise, in both halves of a page and in either."""
+    b = _shared_pages(S, rows, 128 * blocks - 70, Hq, G, seed=43)
+    _rising(b, b.table[0, :blocks].tolist(), again=blocks)
+    shape, _, _ = b.gpu()
+    before = msa.msa_kernel_launches()
+    O, LSE = _dense(msa, b)
+    assert msa.msa_kernel_launches() - before == 3
+    assert blocks / _slots(msa, shape) >= 4
+    some = sorted({0, 1, rows - 1, rows, b.n // 2, b.n - 1})
+    ref.check_attention(b, some, range(0, Hq, 3), O, LSE, _all(b))
+
+
+@pytest.mark.parametrize("name", ["prefix1", "prefix_hg1", "prefix_hg2", "prefix_hg4_rows", "prefix_idle_first",
+                                  "large scores"])
+def test_dense_prefix_read_as_own_pages(msa, name):
+    """Behind a small shared prefix the probabilities have 16 bits, as without one."""
+    if name == "large scores":
+        b = ref.Batch(counts=[2, 1, 1], lens=[128 * 6 + 90, 128 * 7, 128 * 6 + 1], Hq=8, G=2, prefix=4, seed=9)
+        for s in range(3):
+            for c in range(6):
+                b.K[int(b.table[s, c])] *= 1.0 if s else float(1 + 3 * c)
+        b.Q *= 4
+    else:
+        b = ref.Batch(seed=6, **DENSE[name])
+    before = msa.msa_kernel_launches()
+    O, LSE = _dense(msa, b)
+    assert msa.msa_kernel_launches() - before == 2  # rows and attention
+    heads = range(b.Hq) if b.Hq <= 8 else range(0, b.Hq, 5)
+    ref.check_attention(b, range(0, b.n, 1 if b.n < 30 else 7), heads, O, LSE, _all(b))
+
+
+@pytest.mark.parametrize("rows,Hq,launches", [(1, 8, 4), (20, 64, 3)], ids=["shared", "tiles"])
+def test_prefix_in_pools_past_32_bit_offsets(msa, rows, Hq, launches):
+    """A shared prefix (and own pages of 128-row tiles) more than 2^31 elements into the pools."""
+    import torch
+
+    G, pages = 8, 17000
+    K, V = (torch.zeros(pages, G, 128, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    b = ref.Batch(counts=[rows], lens=[128 * 192 + 30], Hq=Hq, G=G, prefix=190, seed=13, spare=0, index=False)
+    far = torch.tensor([pages - 1 - 2 * i for i in range(b.num_pages)], device="cuda")
+    assert int(far.min()) * G * 128 * 128 > 2 ** 31
+    K[far], V[far] = b.K.cuda(), b.V.cuda()
+    table = far.cpu()[b.table.long()].to(torch.int32).cuda()
+    cache = msa.PagedCache(K, V, None, table, torch.tensor([0, rows], dtype=torch.int32, device="cuda"),
+                           torch.tensor(b.lens, dtype=torch.int32, device="cuda"))
+    shape = msa.PagedShape(S=1, N=rows, Hq=Hq, G=G, num_pages=pages, max_blocks=b.max_blocks, prefix_blocks=190)
+    before = msa.msa_kernel_launches()
+    O, LSE = msa.paged_dense_attn(shape, cache, b.Q.cuda())
+    assert msa.msa_kernel_launches() - before == launches
+    ref.check_attention(b, range(0, rows, 6), range(0, Hq, 5), O.cpu(), LSE.cpu(), _all(b), bf16_p=True)
+    del K, V
+
+
 def test_pools_past_32_bit_offsets(msa):
     """Pages whose values lie more than 2^31 elements (and 2^32 bytes) into the pools."""
     import torch
