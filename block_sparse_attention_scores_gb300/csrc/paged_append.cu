@@ -39,12 +39,6 @@ struct AppendArgs {
   int* err;
 };
 
-__device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
-__device__ __forceinline__ uint32_t pack(float a, float b) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
 
 // Item j of a vector: which two 16-byte pieces, and whether (and from which pair on) they are rotated.
 __device__ __forceinline__ void item_pieces(int j, int rot, int interleaved, int& a, int& b, int& pair) {
@@ -67,16 +61,16 @@ __device__ __forceinline__ void rotate(uint4& x, uint4& y, const float2* cs, int
     for (int i = 0; i < 4; ++i) {
       const float2 c = cs[i], d = cs[4 + i];
       const float a0 = lo_f(u[i]), b0 = hi_f(u[i]), a1 = lo_f(v[i]), b1 = hi_f(v[i]);
-      u[i] = pack(a0 * c.x - b0 * c.y, b0 * c.x + a0 * c.y);
-      v[i] = pack(a1 * d.x - b1 * d.y, b1 * d.x + a1 * d.y);
+      u[i] = pack_bf16(a0 * c.x - b0 * c.y, b0 * c.x + a0 * c.y);
+      v[i] = pack_bf16(a1 * d.x - b1 * d.y, b1 * d.x + a1 * d.y);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 c = cs[2 * i], d = cs[2 * i + 1];
       const float a0 = lo_f(u[i]), a1 = hi_f(u[i]), b0 = lo_f(v[i]), b1 = hi_f(v[i]);
-      u[i] = pack(a0 * c.x - b0 * c.y, a1 * d.x - b1 * d.y);
-      v[i] = pack(b0 * c.x + a0 * c.y, b1 * d.x + a1 * d.y);
+      u[i] = pack_bf16(a0 * c.x - b0 * c.y, a1 * d.x - b1 * d.y);
+      v[i] = pack_bf16(b0 * c.x + a0 * c.y, b1 * d.x + a1 * d.y);
     }
   }
 }

@@ -32,7 +32,6 @@
 namespace msa {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWarps = 8;                          // consumers; then the producer and the joining warps
 constexpr int kJoinWarps = 3;
 constexpr int kThreads = (kWarps + 1 + kJoinWarps) * 32;
@@ -85,25 +84,10 @@ struct AttnShared {
   float inv[kCols], lse[kCols];            // of all warps together: 1 / sum, and log2 of the sum
 };
 
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // The bf16 pairs of keys t, t + 1 (x) and t + 8, t + 9 (y) that lie before `end`.
 __device__ __forceinline__ uint2 keep_keys(int t, int end) {
   return make_uint2((t < end ? 0xffffu : 0u) | (t + 1 < end ? 0xffff0000u : 0u),
                     (t + 8 < end ? 0xffffu : 0u) | (t + 9 < end ? 0xffff0000u : 0u));
-}
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
 }
 
 // What the producer knows about an item, fetched in steps while earlier items

@@ -49,12 +49,6 @@ struct ScoreArgs {
   unsigned long long wait_ns;  // a stage may be held for as long as a page takes a warp: the longer, the more columns
 };
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 
 struct ScoreShared {
   uint64_t full[kScoreStages], empty[kScoreStages];
@@ -232,9 +226,6 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 __device__ __forceinline__ float from_key(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
-
-__device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
 // The largest of a block's scores for a query (64 bf16 at q), by one warp, in 64-bit integers: the products (exact in fp32)
 // in units of 2^-57 of `most`, the largest that q and the block's keys could have, 64 of which stay below 2^63.

@@ -51,7 +51,6 @@
 namespace msa {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kHeadroom = 8.f;  // P = exp2(s - m) stays <= 2^kHeadroom
 // warp 0 TMA, warp 1 UMMA + TMEM, 2 and 3 V of own pages, 4-11 and 12-19 softmax of tiles 0 and 1
 constexpr int kThreads = 640;
@@ -100,11 +99,6 @@ struct PrefixShared {
   uint32_t tmem_base;
 };
 
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // (x0, x1) * a + b, two at a time.
 __device__ __forceinline__ void fma2(float& x0, float& x1, float a, float b) {
   asm("{\n\t.reg .b64 x, m, n;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 m, {%2, %2};\n\tmov.b64 n, {%3, %3};\n\t"
@@ -124,10 +118,6 @@ __device__ __forceinline__ void st_global8(float* p, const float* v) {
   asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
                "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                : "memory");
-}
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&v);
 }
 
 // kShared: the call has a shared prefix. Without one every page is a sequence's own, and its P has both parts: told at run

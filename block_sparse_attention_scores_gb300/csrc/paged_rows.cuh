@@ -12,6 +12,7 @@
 #pragma once
 
 #include "paged.h"
+#include "paged_math.cuh"
 #include "pdl.cuh"
 #include "sm100.cuh"
 

@@ -39,19 +39,6 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-// P = (p0, p1), not negative, as the sum of two bf16 pairs that are both above 0 where P is: P cut off, and the rest. Both
-// times an infinity are then that infinity (a part of 0, or below, would make it NaN). The rest is exact but for 2^-23 P,
-// which keeps it above 0, and at most a bf16 step (2^-7 P), so it rounds to bf16 with 2^-16 P at most.
-__device__ __forceinline__ uint32_t bf16_cut(float p0, float p1) {
-  return __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
-}
-__device__ __forceinline__ uint32_t bf16_rest(float p0, float p1, uint32_t cut) {
-  constexpr float above = 1.f + 0x1p-23f;
-  __nv_bfloat162 v = __floats2bfloat162_rn(fmaf(p0, above, -__uint_as_float(cut << 16)),
-                                           fmaf(p1, above, -__uint_as_float(cut & 0xffff0000u)));
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
 // ------------------------------------------------------------------ mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
@@ -134,6 +121,14 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, uint64_t
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
       "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+// Untiled copy to shared memory: 16-byte boundaries on both sides, a multiple of 16 bytes.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
 // TMA tensor store from shared memory (bulk-group completion).
