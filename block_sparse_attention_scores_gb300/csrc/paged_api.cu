@@ -84,8 +84,7 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
       cut_pages(tiles * p.G, p.max_blocks - L.prefix, L.prefix ? 1 : 6, L.prefix ? 0 : 8, &L.per_split, &L.splits);
     }
     if (L.prefix > 0) {
-      const int tiles = (int)(((long long)p.N * p.hg + 127) / 128);
-      L.pairs = (tiles + 1) / 2;
+      L.pairs = (int)(((long long)p.N * p.hg + 255) / 256);
       const int units = p.G * p.prefix;
       // The own pages' kernel runs beside: its CTAs start on the SMs left over, the others as the prefix's end, so that the
       // memory is busy while the tensor core is. Both are estimated (a page takes a pair of tiles 2,750 cycles, a row tile

@@ -335,3 +335,11 @@ def test_workspaces_hold_what_is_written(msa):
     one = msa.msa_paged_workspace_size(msa.PagedShape(S=1, N=1, Hq=32, G=8, num_pages=1000, max_blocks=100),
                                        msa.MSA_WS_PAGED_DENSE)
     assert one > 2 * 32 * 516
+
+
+def test_a_shared_prefix_leaves_sms_to_the_own_pages(msa):
+    """64 sequences behind 256 pages with 16 pages of their own: the prefix's runs take half of the SMs (93 us; 108 with
+    nearly all of them), so a row has few parts of it."""
+    kw = dict(N=64, Hq=32, G=8, num_pages=5000, max_blocks=272, prefix_blocks=256)
+    few, all_of = _slots(msa, msa.PagedShape(S=64, **kw)), 152 * 256 / (8 * 256)
+    assert few - 1 <= 0.6 * all_of
