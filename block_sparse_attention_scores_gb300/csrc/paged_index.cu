@@ -14,7 +14,7 @@
 // order of two blocks decides whole pages. An fp32 maximum v_c differs from
 // the exact one by at most e_c = kErr * |q|_1 * max|k_c|, so the blocks whose
 // interval [v_c - e_c, v_c + e_c] lies clear of the border are decided, and
-// only the others (usually none) are scored again in 64 bits. kErr is
+// only the others (usually none) are scored again, exactly. kErr is
 // 68 * 2^-23: each of the 64 products and four partial sums of a score may be
 // cut off at fp32's step at the size of the largest of them, which |q|_1 max|k|
 // bounds (measured: one large product among 63 small ones loses 2^-19.3 of it,
@@ -227,12 +227,28 @@ __device__ __forceinline__ float from_key(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-// The largest of a block's scores for a query (64 bf16 at q), by one warp, in 64-bit integers: the products (exact in fp32)
-// in units of 2^-57 of `most`, the largest that q and the block's keys could have, 64 of which stay below 2^63.
+// Products of a query and a block's keys (exact in fp32) as integers, in units of 2^-57 of `most`, the largest that they
+// could have, so that 64 of them stay below 2^63. `cut` says that one is not a whole number of units.
+struct Units {
+  float scale;
+  double unit;
+  __device__ __forceinline__ explicit Units(float most) {
+    const int up = 56 - ((int)(__float_as_uint(most) >> 23) - 127);
+    scale = __uint_as_float((uint32_t)(up + 127) << 23);
+    unit = __longlong_as_double((long long)(1023 - up) << 52);
+  }
+  __device__ __forceinline__ long long of(float q, float k, bool& cut) const {
+    const float x = q * k * scale;
+    cut |= x != truncf(x);
+    return __float2ll_rz(x);
+  }
+};
+
+// The largest of a block's scores for a query (64 bf16 at q), by one warp, a key per lane. NaN where a product is cut.
 __device__ __noinline__ double integer_max(const __nv_bfloat16* page, const __nv_bfloat16* q, float most, int lane) {
-  const int up = 56 - ((int)(__float_as_uint(most) >> 23) - 127);
-  const float scale = __uint_as_float((uint32_t)(up + 127) << 23);
+  const Units units(most);
   long long top = -0x7fffffffffffffffll;
+  bool cut = false;
 #pragma unroll 1
   for (int key = lane; key < 128; key += 32) {
     long long sum = 0;
@@ -241,25 +257,33 @@ __device__ __noinline__ double integer_max(const __nv_bfloat16* page, const __nv
       const uint4 w = ld_in(reinterpret_cast<const uint4*>(q) + c), k = ld_in(reinterpret_cast<const uint4*>(page + key * 64) + c);
       const uint32_t wv[4] = {w.x, w.y, w.z, w.w}, kv[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-      for (int z = 0; z < 4; ++z)
-        sum += __float2ll_rz(lo_f(wv[z]) * scale * lo_f(kv[z])) + __float2ll_rz(hi_f(wv[z]) * scale * hi_f(kv[z]));
+      for (int z = 0; z < 4; ++z) sum += units.of(lo_f(wv[z]), lo_f(kv[z]), cut) + units.of(hi_f(wv[z]), hi_f(kv[z]), cut);
     }
     top = max(top, sum);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  return (double)top * __longlong_as_double((long long)(1023 - up) << 52);
+  return __any_sync(0xffffffffu, cut) ? (double)NAN : (double)top * units.unit;
 }
 
-// The block's exact maximum for a query, by one warp: a lane scores four keys in
-// fp32, and the keys within `margin` of the best one are summed again in 64 bits.
+// s + e += t + f, with s the rounded sum and e what it lacks.
+__device__ __forceinline__ void add_exactly(double& s, double& e, double t, double f) {
+  const double sum = s + t, z = sum - s;
+  e += f + ((s - (sum - z)) + (t - z));
+  s = sum;
+}
+
+// The block's exact maximum for a query, rounded once, by one warp: a lane scores
+// four keys in fp32, and the keys within `margin` of the best one are summed again.
 // 64 fused steps are off by 64 * 2^-24 of the products' magnitudes at worst, so a
 // difference of two scores by less than kErr of them.
 //
-// Few such keys (as a rule one): doubles, two dims per lane. Many, as where all
-// keys of a block are the same (one token over and over: then every block is
-// undecided, too): integers, a key per lane, since a row of 128K such tokens
-// takes doubles 24 ms and integers 0.2.
+// Those sums are of 64-bit integers: of few keys (as a rule one) with two dims per
+// lane, of many, as where all keys of a block are the same (one token over and
+// over: then every block is undecided, too), with a key per lane. Where products
+// lie too far apart for that, or are not finite, of doubles with what their
+// additions lose. A score is the same number in whichever way: one that was
+// rounded in between could part equal keys.
 __device__ __noinline__ double exact_max(const __nv_bfloat16* page, const __nv_bfloat16* q, float margin, float qmax, float kmax, int lane) {
   float s32[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -285,27 +309,49 @@ __device__ __noinline__ double exact_max(const __nv_bfloat16* page, const __nv_b
   float best = fmaxf(fmaxf(s32[0], s32[1]), fmaxf(s32[2], s32[3]));
 #pragma unroll
   for (int o = 16; o; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-  const float most = qmax * kmax;
-  if (most >= 0x1p-60f && most <= 0x1p90f && kmax >= 0x1p-60f) {
-    int many = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) many += __popc(__ballot_sync(0xffffffffu, !(s32[i] < best - margin)));
-    if (many > 8) return integer_max(page, q, most, lane);
-  }
-  const uint32_t qq = ld_in(reinterpret_cast<const uint32_t*>(q) + lane);
-  double top = -INFINITY;
+  unsigned near[4];  // (the comparison is false for NaN: such a key is looked at again)
+  int many = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    // the comparison is false for NaN: such a key is looked at in 64 bits
-    for (unsigned m = __ballot_sync(0xffffffffu, !(s32[i] < best - margin)); m; m &= m - 1) {
-      const int key = __ffs(m) - 1 + 32 * i;
-      const uint32_t kk = ld_in(reinterpret_cast<const uint32_t*>(page + key * 64) + lane);
-      double t = fma((double)hi_f(qq), (double)hi_f(kk), (double)lo_f(qq) * (double)lo_f(kk));
-#pragma unroll
-      for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      top = fmax(top, t);
-    }
+    near[i] = __ballot_sync(0xffffffffu, !(s32[i] < best - margin));
+    many += __popc(near[i]);
   }
+  const uint32_t qq = ld_in(reinterpret_cast<const uint32_t*>(q) + lane);
+  auto pair_of = [&](int key) { return ld_in(reinterpret_cast<const uint32_t*>(page + key * 64) + lane); };
+  const float most = qmax * kmax;
+  if (most >= 0x1p-60f && most <= 0x1p90f) {
+    double t;
+    if (many > 8) {
+      t = integer_max(page, q, most, lane);
+    } else {
+      const Units units(most);
+      long long top = -0x7fffffffffffffffll;
+      bool cut = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        for (unsigned m = near[i]; m; m &= m - 1) {
+          const uint32_t kk = pair_of(__ffs(m) - 1 + 32 * i);
+          long long sum = units.of(lo_f(qq), lo_f(kk), cut) + units.of(hi_f(qq), hi_f(kk), cut);
+#pragma unroll
+          for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          top = max(top, sum);
+        }
+      t = __any_sync(0xffffffffu, cut) ? (double)NAN : (double)top * units.unit;
+    }
+    if (t == t) return t;
+  }
+  double top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    for (unsigned m = near[i]; m; m &= m - 1) {
+      const uint32_t kk = pair_of(__ffs(m) - 1 + 32 * i);
+      double t = (double)lo_f(qq) * (double)lo_f(kk), e = 0.;
+      add_exactly(t, e, (double)hi_f(qq) * (double)hi_f(kk), 0.);
+#pragma unroll
+      for (int o = 16; o; o >>= 1)
+        add_exactly(t, e, __shfl_xor_sync(0xffffffffu, t, o), __shfl_xor_sync(0xffffffffu, e, o));
+      top = fmax(top, e == e ? t + e : t);  // (e is NaN where t is not finite)
+    }
   return top;
 }
 

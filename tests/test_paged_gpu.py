@@ -719,6 +719,37 @@ def test_selection_of_ties_everywhere(msa, what):
         np.testing.assert_array_equal(bi[r], ref.select(b, r, 16))
 
 
+@pytest.mark.parametrize("what", ["past 53 bits", "past 57 bits", "past 70 bits"])
+def test_selection_of_one_key_in_many_places(msa, what):
+    """A key that fills some blocks and stands once in others, with products too far apart for a sum in doubles to be
+    exact: however a block's score is computed, it is the same everywhere, and the lower ids are taken."""
+    import torch
+
+    b = ref.Batch(counts=[1, 2], lens=[128 * 90 + 5, 128 * 41 + 77], Hq=2, G=2, seed=33)
+    gen = torch.Generator().manual_seed(4)
+    e = {"past 53 bits": 27, "past 57 bits": 28, "past 70 bits": 30}[what]
+    for g in range(2):
+        b.q_idx[:b.n, g] = 2.0 ** -e
+        if e > 27:  # all of their bits
+            b.q_idx[:b.n, g] = (2.0 ** -e * (1 + torch.rand(64, generator=gen))).to(torch.bfloat16)
+    b.q_idx[:b.n, :, 0] = 1.0
+    for s in range(2):
+        key = (2.0 ** -e * (1 + (torch.rand(64, generator=gen) if e > 27 else torch.zeros(64)))).to(torch.bfloat16)
+        key[0] = 1.0
+        for c in range((b.lens[s] - 1) // 128):
+            page = int(b.table[s, c])
+            b.k_idx[page] = (torch.randn(128, 64, generator=gen) * 2.0 ** -e).to(torch.bfloat16)
+            b.k_idx[page, :, 0] = 0.5
+            b.k_idx[page, 77 if c % 3 == 0 else slice(None)] = key
+    for k in (4, 9, 30):
+        _, _, bi = _sparse(msa, b, k)
+        for r in range(b.n):
+            last = b.row_pos[r] // 128
+            want = [*range(min(k - 1, last)), last]
+            for g in range(2):
+                assert bi[r, g].tolist()[:len(want)] == want, (r, g, k)
+
+
 def test_dense_large_scores(msa):
     """Scores whose maximum moves by far more than exp2's range from page to page."""
     b = ref.Batch(counts=[2, 1, 1], lens=[128 * 6 + 90, 128 * 7, 128 * 6 + 1], Hq=8, G=2, prefix=4, seed=9)
