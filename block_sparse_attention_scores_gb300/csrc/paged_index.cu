@@ -273,6 +273,24 @@ __device__ __forceinline__ void add_exactly(double& s, double& e, double t, doub
   s = sum;
 }
 
+// The largest score among the keys of `near` (of lane i: the keys 32 i + bit), by one warp, two dims per lane.
+__device__ __noinline__ double double_max(const __nv_bfloat16* page, uint32_t qq, unsigned near, int lane) {
+  double top = -INFINITY;
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i)
+#pragma unroll 1
+    for (unsigned m = __shfl_sync(0xffffffffu, near, i); m; m &= m - 1) {
+      const uint32_t kk = ld_in(reinterpret_cast<const uint32_t*>(page + (__ffs(m) - 1 + 32 * i) * 64) + lane);
+      double t = (double)lo_f(qq) * (double)lo_f(kk), e = 0.;
+      add_exactly(t, e, (double)hi_f(qq) * (double)hi_f(kk), 0.);
+#pragma unroll
+      for (int o = 16; o; o >>= 1)
+        add_exactly(t, e, __shfl_xor_sync(0xffffffffu, t, o), __shfl_xor_sync(0xffffffffu, e, o));
+      top = fmax(top, e == e ? t + e : t);  // (e is NaN where t is not finite)
+    }
+  return top;
+}
+
 // The block's exact maximum for a query, rounded once, by one warp: a lane scores
 // four keys in fp32, and the keys within `margin` of the best one are summed again.
 // 64 fused steps are off by 64 * 2^-24 of the products' magnitudes at worst, so a
@@ -309,50 +327,38 @@ __device__ __noinline__ double exact_max(const __nv_bfloat16* page, const __nv_b
   float best = fmaxf(fmaxf(s32[0], s32[1]), fmaxf(s32[2], s32[3]));
 #pragma unroll
   for (int o = 16; o; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-  unsigned near[4];  // (the comparison is false for NaN: such a key is looked at again)
+  unsigned near = 0;  // lane i: which keys 32 i + bit (the comparison is false for NaN: such a key is looked at again)
   int many = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    near[i] = __ballot_sync(0xffffffffu, !(s32[i] < best - margin));
-    many += __popc(near[i]);
+    const unsigned m = __ballot_sync(0xffffffffu, !(s32[i] < best - margin));
+    if (lane == i) near = m;
+    many += __popc(m);
   }
   const uint32_t qq = ld_in(reinterpret_cast<const uint32_t*>(q) + lane);
-  auto pair_of = [&](int key) { return ld_in(reinterpret_cast<const uint32_t*>(page + key * 64) + lane); };
   const float most = qmax * kmax;
+  double t = NAN;
   if (most >= 0x1p-60f && most <= 0x1p90f) {
-    double t;
     if (many > 8) {
       t = integer_max(page, q, most, lane);
     } else {
       const Units units(most);
       long long top = -0x7fffffffffffffffll;
       bool cut = false;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < 4; ++i)
-        for (unsigned m = near[i]; m; m &= m - 1) {
-          const uint32_t kk = pair_of(__ffs(m) - 1 + 32 * i);
+#pragma unroll 1
+        for (unsigned m = __shfl_sync(0xffffffffu, near, i); m; m &= m - 1) {
+          const uint32_t kk = ld_in(reinterpret_cast<const uint32_t*>(page + (__ffs(m) - 1 + 32 * i) * 64) + lane);
           long long sum = units.of(lo_f(qq), lo_f(kk), cut) + units.of(hi_f(qq), hi_f(kk), cut);
 #pragma unroll
           for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
           top = max(top, sum);
         }
-      t = __any_sync(0xffffffffu, cut) ? (double)NAN : (double)top * units.unit;
+      if (!__any_sync(0xffffffffu, cut)) t = (double)top * units.unit;
     }
-    if (t == t) return t;
   }
-  double top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    for (unsigned m = near[i]; m; m &= m - 1) {
-      const uint32_t kk = pair_of(__ffs(m) - 1 + 32 * i);
-      double t = (double)lo_f(qq) * (double)lo_f(kk), e = 0.;
-      add_exactly(t, e, (double)hi_f(qq) * (double)hi_f(kk), 0.);
-#pragma unroll
-      for (int o = 16; o; o >>= 1)
-        add_exactly(t, e, __shfl_xor_sync(0xffffffffu, t, o), __shfl_xor_sync(0xffffffffu, e, o));
-      top = fmax(top, e == e ? t + e : t);  // (e is NaN where t is not finite)
-    }
-  return top;
+  return t == t ? t : double_max(page, qq, near, lane);
 }
 
 // One block per (row, group). A thread keeps its blocks' lower bounds (as
