@@ -13,12 +13,12 @@ static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // look up, the warps' meeting, its part of O), and parts that the kernel joins
 // itself `join` more; SMs take items as they come, so the end is half an item
 // long. Measured for what the mma.sync path joins (6 and 8): 64 rows of 16 pages
-// and 8 groups 125 us, 129 where an item counts for one page more and the join for
-// nothing (which cuts in two), 57 rows of 9 pages and 2 groups 13.6 and 20.4; a
-// row's 128 pages 25 us, 29 uncut; 16000 tokens 25 us, 31 and 85 uncut. Where the
-// merge kernel joins (1 and 0): 64 sequences behind 32K tokens 94 us, 97 with two
-// pages. 128-row tiles (3 and 0): 300 rows over 8000 tokens 64 us, 84 with one and
-// 93 with eight pages.
+// and 8 groups 125 us, 127 where an item counts for one page more and the join for
+// nothing (which cuts in two), 57 rows of 9 pages and 2 groups 15.3 and 22.9; a
+// row's 128 pages 23.7 us, 28.6 uncut; 16000 tokens of 8 groups 22.7 us, 84.7 uncut.
+// Where the merge kernel joins (1 and 0): 64 sequences behind 32K tokens 94 us, 97
+// with two pages. 128-row tiles (3 and 0): 300 rows x 32 heads over 4 groups and
+// 8000 tokens 64 us, 84 with one and 93 with eight pages.
 static void cut_pages(long long tiles, int pages, double extra, double join, int* per_split, int* n_splits) {
   tiles = std::max(1LL, tiles);
   pages = std::max(1, pages);
@@ -59,10 +59,10 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
     cut_pages((long long)p.N * p.G, std::min(p.k, p.max_blocks), 6, 8, &L.per_split, &L.splits);
   } else {
     L.tile_rows = 8 / p.hg;
-    // More columns (rows x heads of a sequence) than eight on average, padded rows aside, and more than a page each: 128-row
-    // tiles, tcgen05.
-    // Against eight columns at a time: 32 sequences of 2 rows x 64 heads over 2000 tokens 63 -> 62 us, of 8 rows 135 -> 71,
-    // 300 rows x 32 heads over 8000 274 -> 64; the other way for one page (8 rows x 64 heads over 100 tokens 17 -> 10).
+    // More than nine columns (rows x heads) a sequence on average and more than a page each: 128-row tiles, tcgen05. Padded
+    // rows count, as nothing here tells them from others: the ninth column is for a pad of up to an eighth. Against eight
+    // columns at a time: 32 sequences of 2 rows x 64 heads over 2000 tokens 63 -> 60 us, of 8 rows 135 -> 69, 300 rows x 32
+    // heads over 4 groups and 8000 tokens 274 -> 64; the other way for one page (8 rows x 64 heads over 100 tokens 17 -> 10).
     const bool runs = (long long)p.N * p.hg > 9LL * p.S && p.max_blocks - p.prefix > 1;
     // A shared prefix of ten pages an SM (13 where a sequence has several tiles of eight columns), counted for every such
     // tile, is read as own pages: it stays in L2, and two kernels do with it what four do. 4 sequences of 32 heads over 8

@@ -18,7 +18,7 @@
 // the merge kernel below joins them with the prefix's.
 //
 // Measured: 60 rows x 8 groups x 16 selected pages, 503 MB in 81 us, 6.2 TB/s,
-// 0.93 of a plain copy; one row's 128 pages 11 us, of which the memory takes 1.3.
+// 0.93 of a plain copy; one row's 128 pages 10.7 us, of which the memory takes 1.3.
 // Equal runs of pages for every CTA, cut anywhere, cost more at their seams than
 // their balance gained (a row at 128K tokens 36 us against 30).
 //

@@ -7,8 +7,13 @@
 // (rows x groups, eight columns at a time, mma.sync): the memory's time, at a
 // tenth of the tensor pipe's. Measured: two sequences of 2^20 tokens, 268 MB of
 // keys in 44 us, 6.1 TB/s, 0.91 of a plain copy. The selection after it is all
-// latency: 5 us for a row over 1,024 blocks, 15 over 8,192, 12 for 480 rows and
+// latency: 5 us for a row over 1,024 blocks, 15 over 8,192, 10.5 for 480 rows and
 // groups over up to 256 each.
+//
+// All columns (rows x groups) of a sequence go through one warp a page: made for
+// tokens and drafts. 16 rows x 8 groups over 8K tokens take the whole call 45 us, 256
+// rows 437, and a prompt of 8,192 rows 13 ms (each row reads its own pages, too),
+// where the training calls need 0.64 for the whole sequence.
 //
 // The selection has to be exact, not exact up to the rounding of fp32: the
 // order of two blocks decides whole pages. An fp32 maximum v_c differs from

@@ -33,9 +33,9 @@
 // tile alone would leave the tensor core idle during its softmax and the memory
 // during both (32 sequences of 4 rows, 64 heads over 8 groups, 2000 tokens: 109
 // us against 92). What differs from the shared part:
-//   - P as the sum of two positive bf16 values, side by side over S (the second product
-//     costs little where the memory bounds: with one row or two the same result
-//     comes from the mma.sync path, which does that too);
+//   - P as the sum of two positive bf16 values, side by side over S (the second
+//     product costs little where the memory bounds: with one row or two the same
+//     result comes from the mma.sync path, which does that too);
 //   - masks, on the pages that not every row sees all of, and V cleaned there by
 //     a warp of its own before the tensor core may read it: a zero of P does not
 //     keep an infinity or a NaN of a later row's V from an earlier row;
@@ -43,9 +43,10 @@
 //     round in shared memory.
 //
 // Measured: the shared part of 128 sequences x 2 rows x 32 heads over 128K tokens
-// 354 us, 1550 TFLOP/s (0.8 of what a library product reaches); own pages of 32 x
-// 4 rows x 64 heads over 2000 tokens 59 us, 4.6 TB/s; 300 rows x 32 heads over
-// 8000 tokens 52 us, 740 TFLOP/s (P's second product not counted).
+// 385 us on 136 SMs, 1430 TFLOP/s (0.74 of what a library product reaches on all);
+// own pages of 16 x 4 rows x 64 heads over 3000 tokens 50 us, 4.1 TB/s; the whole
+// call for 32 x 4 rows x 64 heads over 2000 tokens 63 us, for 300 rows x 32 heads
+// over 4 groups and 8000 tokens 64 us (610 TFLOP/s, P's second product not counted).
 #include "paged_rows.cuh"
 
 namespace msa {

@@ -411,8 +411,11 @@ MSA_API msa_status msa_paged_append(const msa_paged_shape *shape, const msa_page
  *   s_j = scale <Q[r,h,:], K[j,g,:]> over the tokens j <= t of those blocks,
  *   LSE = ln sum_j exp(s_j),  O[r,h,:] = sum_j exp(s_j - LSE) V[j,g,:].
  * The selection is that of the exact scores (blocks that fp32 sums cannot tell
- * apart are compared in 64 bits); a NaN score counts as -infinity. What lies in
- * the pages behind a row's position reaches no result.
+ * apart are summed again without rounding); a NaN score counts as -infinity. What
+ * lies in the pages behind a row's position reaches no result. Made for few rows
+ * a sequence (a token, a draft): each row reads its own pages, and the scores of
+ * a page are one warp's work for all rows of its sequence, so a prompt's rows
+ * are right but take a multiple of the training calls' time.
  *
  * Q [N, Hq, d], q_idx [N, G, d_idx] bf16 -> block_idx [N, G, k] int32, O
  * [N, Hq, d] bf16, LSE [N, Hq] fp32. With q_idx NULL the layer reuses a
@@ -430,6 +433,11 @@ MSA_API msa_status msa_paged_sparse_attn(const msa_paged_shape *shape, const msa
  * prompt that the batch shares); they are read once for the whole batch (a few
  * pages once a sequence, from L2, where that is quicker), and every row's
  * position must lie behind them. prefix_blocks = 0 shares nothing.
+ *
+ * Probabilities are multiplied with V in 16 bits. Where pages are shared, they
+ * may be rounded to bf16 against those (O then differs by up to 2^-8 of
+ * sum p |v|, as msa_dense_fwd's does), which depends on the shape alone; a
+ * caller who wants 16 bits throughout gives prefix_blocks = 0.
  */
 MSA_API msa_status msa_paged_dense_attn(const msa_paged_shape *shape, const msa_paged_cache *cache, const void *Q,
                                         void *O, float *LSE, void *workspace, size_t workspace_bytes,
