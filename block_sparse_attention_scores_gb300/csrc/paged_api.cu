@@ -71,7 +71,9 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
     // 23; beyond: 16 rows x 64 heads behind 50 pages (6400) 50 and 29, 64 behind 6 (3072) 30 and 25, 128 behind 10 (10240)
     // 66 and 41, behind 180 (1,440 pages, read 128 times) 797 and 99.
     const long long tiles = std::max(p.N / L.tile_rows, std::min(p.S, p.N));
-    const bool fold = !runs && tiles * p.prefix * p.G <= (tiles > p.S ? 2000 : 1500);
+    // (Idle sequences count too: their tables are looked at by the one block that lines up the rows.)
+    const long long readers = std::max<long long>(tiles, p.S);
+    const bool fold = !runs && readers * p.prefix * p.G <= (readers > p.S ? 2000 : 1500);
     L.prefix = fold ? 0 : p.prefix;
     if (runs) {
       L.run_rows = 256 / p.hg;

@@ -329,7 +329,7 @@ MSA_API msa_status msa_dense_bwd(const msa_shape *shape, const void *Q, const vo
  *
  * Values that are not finite, where a row sees them: an infinity in V gives
  * that infinity in O (both signs, or NaN, give NaN), in the dims that have it
- * alone, unless the token's probability is below 2^-126; a NaN score gives NaN
+ * alone, unless the token's probability is below 2^-100; a NaN score gives NaN
  * in the row's O and LSE.
  */
 typedef struct msa_paged_shape {

@@ -294,7 +294,8 @@ def _slots(msa, shape):
 
 
 @pytest.mark.parametrize("kw", [dict(S=1, N=128, Hq=64, G=8, prefix_blocks=187), dict(S=2, N=64, Hq=64, G=8, prefix_blocks=60),
-                                dict(S=1, N=127, Hq=32, G=8, prefix_blocks=50), dict(S=4, N=128, Hq=64, G=8, prefix_blocks=40)],
+                                dict(S=1, N=127, Hq=32, G=8, prefix_blocks=50), dict(S=4, N=128, Hq=64, G=8, prefix_blocks=40),
+                                dict(S=60000, N=160, Hq=8, G=1, prefix_blocks=9)],  # nearly all of them idle
                          ids=str)
 def test_a_prefix_that_many_rows_read_is_shared(msa, kw):
     """A prefix is read as own pages where that is little work: its pages count once for every tile of eight columns, not
