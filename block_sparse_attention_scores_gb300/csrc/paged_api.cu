@@ -68,8 +68,8 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
     // tile, is read as own pages: it stays in L2, and two kernels do with it what four do. 4 sequences of 32 heads over 8
     // groups behind 16 pages 15 us against 19, 16 behind 8 pages 14 and 19, 8 of 4 rows behind 12 pages (1536) 17 and 21,
     // one of 16 rows x 64 heads over 8 groups behind 10 pages (1280) 15 and 21, of 64 x 32 heads behind 6 (1536) 19 and
-    // 23; beyond: 16 rows x 64 heads behind 50 pages (6400) 50 and 29, 64 behind 6 (3072) 30 and 25, 128 behind 10 (10240)
-    // 66 and 41, behind 180 (1,440 pages, read 128 times) 797 and 99.
+    // 23; beyond: 16 rows x 64 heads behind 50 pages (6400) 50 and 29, 64 behind 10 (5120) 40 and 30, 128 behind 10
+    // (10240) 66 and 41, behind 180 (1,440 pages, read 128 times) 797 and 99.
     const long long tiles = std::max(p.N / L.tile_rows, std::min(p.S, p.N));
     // (Idle sequences count too: their tables are looked at by the one block that lines up the rows.)
     const long long readers = std::max<long long>(tiles, p.S);

@@ -259,7 +259,8 @@ __device__ __noinline__ double integer_max(const __nv_bfloat16* page, const __nv
     long long sum = 0;
 #pragma unroll 1
     for (int c = 0; c < 8; ++c) {
-      const uint4 w = ld_in(reinterpret_cast<const uint4*>(q) + c), k = ld_in(reinterpret_cast<const uint4*>(page + key * 64) + c);
+      const uint4 w = ld_in(reinterpret_cast<const uint4*>(q) + c);
+      const uint4 k = ld_in(reinterpret_cast<const uint4*>(page + key * 64) + c);
       const uint32_t wv[4] = {w.x, w.y, w.z, w.w}, kv[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
       for (int z = 0; z < 4; ++z) sum += units.of(lo_f(wv[z]), lo_f(kv[z]), cut) + units.of(hi_f(wv[z]), hi_f(kv[z]), cut);
@@ -307,7 +308,8 @@ __device__ __noinline__ double double_max(const __nv_bfloat16* page, uint32_t qq
 // lie too far apart for that, or are not finite, of doubles with what their
 // additions lose. A score is the same number in whichever way: one that was
 // rounded in between could part equal keys.
-__device__ __noinline__ double exact_max(const __nv_bfloat16* page, const __nv_bfloat16* q, float margin, float qmax, float kmax, int lane) {
+__device__ __noinline__ double exact_max(const __nv_bfloat16* page, const __nv_bfloat16* q, float margin, float qmax,
+                                         float kmax, int lane) {
   float s32[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {

@@ -746,7 +746,8 @@ cudaError_t launch_prefix(const PrefixArgs& a, int blocks, const CUtensorMap& mq
   static bool attr[kMaxDevices] = {};
   const int dslot = device_slot();
   if (!attr[dslot]) {
-    cudaError_t e = cudaFuncSetAttribute(paged_prefix_kernel<kRuns, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    cudaError_t e =
+        cudaFuncSetAttribute(paged_prefix_kernel<kRuns, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     attr[dslot] = true;
   }
@@ -792,7 +793,8 @@ cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, con
   a.rslots = L.rslots;
   a.pslots = L.pslots;
   if (!L.run_rows) return launch_prefix<false, true>(a, L.n_flags, mq, maps, st);
-  return L.prefix ? launch_prefix<true, true>(a, L.n_flags, mq, maps, st) : launch_prefix<true, false>(a, L.n_flags, mq, maps, st);
+  if (L.prefix) return launch_prefix<true, true>(a, L.n_flags, mq, maps, st);
+  return launch_prefix<true, false>(a, L.n_flags, mq, maps, st);
 }
 
 }  // namespace msa

@@ -205,7 +205,7 @@ def _rows(name, t, shape, device):
             packed *= n
         ld = strides[0] if shape[0] > 1 else packed
     if ld < packed:  # rows that lie on one another; expanded ones have stride 0, which the C call takes for packed rows
-        raise ValueError(f"the rows of {name} must not overlap (their stride is {ld}): an expanded tensor is to be made contiguous")
+        raise ValueError(f"the rows of {name} must not overlap (their stride is {ld}): make an expanded tensor contiguous")
     return t.data_ptr(), ld
 
 

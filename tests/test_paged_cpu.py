@@ -321,8 +321,8 @@ def test_more_heads_than_are_counted(msa, Hq, G):
 def test_workspaces_hold_what_is_written(msa):
     """No parts of outputs where rows are not cut, no block maxima where nothing is chosen between blocks."""
     def sparse(**kw):
-        return msa.msa_paged_workspace_size(
-            msa.PagedShape(**{**dict(S=1, N=32768, Hq=64, G=8, num_pages=1000, max_blocks=256, k=16), **kw}), msa.MSA_WS_PAGED_SPARSE)
+        base = dict(S=1, N=32768, Hq=64, G=8, num_pages=1000, max_blocks=256, k=16)
+        return msa.msa_paged_workspace_size(msa.PagedShape(**{**base, **kw}), msa.MSA_WS_PAGED_SPARSE)
 
     rows = 32768 * (32 + 8 * 12)          # their places, and counters
     pooled = 32768 * 8 * 256 * 8          # a block's maximum and its keys' largest value

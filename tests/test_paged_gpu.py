@@ -872,7 +872,8 @@ def test_infinite_values(msa, name):
     O, LSE = _dense(msa, b)
     assert torch.equal(LSE[:b.n], clean[1][:b.n])
     want = _with_infinities(b, clean[0][:b.n], _all(b))
-    assert torch.equal(O[:b.n].nan_to_num(nan=1e30, posinf=2e30, neginf=-2e30), want.nan_to_num(nan=1e30, posinf=2e30, neginf=-2e30))
+    assert torch.equal(O[:b.n].nan_to_num(nan=1e30, posinf=2e30, neginf=-2e30),
+                       want.nan_to_num(nan=1e30, posinf=2e30, neginf=-2e30))
     assert int(want.isnan().sum()) and int((want == INF).sum()) and int((want == -INF).sum())
     t["V"].copy_(b.V)
     O, LSE, _ = msa.paged_sparse_attn(shape, cache, t["Q"], block_idx=bi.cuda())
