@@ -13,7 +13,8 @@ Entry points (same names as the C ABI):
   dQ, dK, dV, dq_idx, dk_idx, KL, workspace, stream=None)``
 * ``msa_workspace_size(shape, which)``, ``msa_check_device_status(workspace, stream)``
 * serving, over a ``PagedCache``: ``msa_paged_append``, ``msa_paged_sparse_attn``,
-  ``msa_paged_dense_attn`` (see ``paged.py``)
+  ``msa_paged_dense_attn``; over a ``PagedCacheFp8`` (8 bits): the same with ``_fp8``,
+  and ``msa_paged_read_fp8`` (see ``paged.py``)
 
 Tensors are torch CUDA tensors (bf16 / int32 / fp32, contiguous, layouts as
 in the header) or raw device addresses (int). ``stream`` is a
@@ -32,13 +33,16 @@ LIB_PATH = os.path.join(_HERE, "libmsa_gb300.so")
 MSA_OK, MSA_ERR_INVALID_ARG, MSA_ERR_UNSUPPORTED, MSA_ERR_WORKSPACE, MSA_ERR_CUDA, MSA_ERR_DEVICE = range(6)
 MSA_WS_TOPK, MSA_WS_FWD, MSA_WS_BWD, MSA_WS_TOPK_FP8, MSA_WS_DENSE = 0, 1, 2, 3, 4
 MSA_WS_PAGED_APPEND, MSA_WS_PAGED_SPARSE, MSA_WS_PAGED_DENSE = 0, 1, 2
+MSA_WS_PAGED_SPARSE_FP8, MSA_WS_PAGED_DENSE_FP8 = 4, 5
 MSA_TIME_INDEX_TOPK, MSA_TIME_SPARSE_FWD, MSA_TIME_BWD, MSA_TIME_DENSE_FWD, MSA_TIME_DENSE_BWD = 0, 1, 2, 3, 4
 
 EXPORTED = ("msa_workspace_size", "msa_index_topk", "msa_sparse_fwd", "msa_bwd", "msa_last_error",
             "msa_check_device_status", "msa_selftest_wait_timeout", "msa_kernel_launches", "msa_version",
             "msa_index_topk_noalloc", "msa_index_topk_fp8", "msa_block_map", "msa_sparse_fwd_mapped", "msa_bwd_mapped",
             "msa_warmup_block_idx", "msa_set_timing_events", "msa_dense_fwd", "msa_dense_bwd",
-            "msa_paged_workspace_size", "msa_paged_append", "msa_paged_sparse_attn", "msa_paged_dense_attn")
+            "msa_paged_workspace_size", "msa_paged_append", "msa_paged_sparse_attn", "msa_paged_dense_attn",
+            "msa_paged_append_axes", "msa_paged_append_fp8", "msa_paged_read_fp8", "msa_paged_sparse_attn_fp8",
+            "msa_paged_dense_attn_fp8")
 
 
 class MsaError(RuntimeError):
@@ -116,7 +120,12 @@ def load_library():
     lib.msa_paged_append.argtypes = [R, R, R, R, P, P, P, ctypes.c_size_t, P]
     lib.msa_paged_sparse_attn.argtypes = [R, R, P, P, P, P, P, P, ctypes.c_size_t, P]
     lib.msa_paged_dense_attn.argtypes = [R, R, P, P, P, P, ctypes.c_size_t, P]
-    for f in (lib.msa_paged_append, lib.msa_paged_sparse_attn, lib.msa_paged_dense_attn):
+    lib.msa_paged_append_axes.argtypes = lib.msa_paged_append_fp8.argtypes = [R, R, R, R, R, P, P, P, ctypes.c_size_t, P]
+    lib.msa_paged_read_fp8.argtypes = [R, R, P, P, ctypes.c_int32, P, P, P, P, ctypes.c_size_t, P]
+    lib.msa_paged_sparse_attn_fp8.argtypes = lib.msa_paged_sparse_attn.argtypes
+    lib.msa_paged_dense_attn_fp8.argtypes = lib.msa_paged_dense_attn.argtypes
+    for f in (lib.msa_paged_append, lib.msa_paged_sparse_attn, lib.msa_paged_dense_attn, lib.msa_paged_append_axes,
+              lib.msa_paged_append_fp8, lib.msa_paged_read_fp8, lib.msa_paged_sparse_attn_fp8, lib.msa_paged_dense_attn_fp8):
         f.restype = ctypes.c_int
     lib.msa_selftest_wait_timeout.argtypes = [P, ctypes.c_int32, P]
     lib.msa_selftest_wait_timeout.restype = ctypes.c_int
@@ -379,5 +388,8 @@ def dense_bwd(shape: Shape, Q, K, V, O, dO, LSE, q_idx, k_idx, kl_weight=1.0, wo
     return out
 
 
-from .paged import (PagedCache, PagedShape, Rope, alloc_paged_workspace, msa_paged_append, msa_paged_dense_attn,  # noqa: E402,F401
-                    msa_paged_sparse_attn, msa_paged_workspace_size, paged_append, paged_dense_attn, paged_sparse_attn)
+from .paged import (PagedCache, PagedCacheFp8, PagedShape, Rope, alloc_paged_workspace, msa_paged_append,  # noqa: E402,F401
+                    msa_paged_append_fp8, msa_paged_dense_attn, msa_paged_dense_attn_fp8, msa_paged_read_fp8,
+                    msa_paged_sparse_attn, msa_paged_sparse_attn_fp8, msa_paged_workspace_size, paged_append,
+                    paged_append_fp8, paged_dense_attn, paged_dense_attn_fp8, paged_read_fp8, paged_sparse_attn,
+                    paged_sparse_attn_fp8)

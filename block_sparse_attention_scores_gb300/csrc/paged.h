@@ -61,9 +61,12 @@ __host__ __device__ inline int team_of(int u, int units, int teams) {
 struct PagedCachePtrs {
   void *K, *V, *k_idx;
   const int32_t *page_table, *row_start, *seq_len;
+  uint8_t *K_exp = nullptr, *V_exp = nullptr, *k_idx_exp = nullptr;  // a cache in 8 bits: the codes' powers of two
+  bool bytes() const { return K_exp != nullptr; }
 };
 
-// Tensor maps over the K and V pools as rows of 128 values: boxes of 64 columns x 128 rows (half a page of one group).
+// Tensor maps over the K and V pools as rows of 128 values: boxes of 64 columns x 128 rows (half a page of one group), or,
+// in 8 bits, of 128 x 128 codes (a page of one group).
 struct PoolMaps {
   CUtensorMap k, v;
 };
@@ -74,10 +77,20 @@ struct RopeRows {
   void *Q_out, *q_idx_out;
   const float *inv_freq, *inv_freq_idx;
   int rot, rot_idx, interleaved;
+  const int32_t *positions, *axis, *axis_idx;  // [N, axes] positions, and the pairs' axes (null: all on axis 0)
+  int axes;                                    // 0: the rows' positions in their sequences
+};
+
+// Rows out_start[s] .. out_start[s+1] - 1 of M are the tokens first[s], ... of sequence s.
+struct ReadRows {
+  const int32_t *first, *out_start;
+  void *K, *V, *k_idx;
+  int M;
 };
 
 cudaError_t launch_paged_append(const PagedProb& p, const PagedCachePtrs& c, const RopeRows& r, uint8_t* ws,
                                 cudaStream_t st);
+cudaError_t launch_paged_read(const PagedProb& p, const PagedCachePtrs& c, const ReadRows& r, uint8_t* ws, cudaStream_t st);
 // The call's first work (paged_rows.cuh) as a kernel of its own (the index scores' kernel does it itself).
 cudaError_t launch_paged_rows(const PagedProb& p, const PagedCachePtrs& c, uint8_t* ws, const PagedWs& L,
                               cudaStream_t st);
@@ -93,6 +106,5 @@ cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, con
 // Joins the parts of the shared prefix and of the own pages (without a prefix the attention does).
 cudaError_t launch_paged_merge(const PagedProb& p, void* O, float* LSE, uint8_t* ws, const PagedWs& L,
                                cudaStream_t st);
-
 
 }  // namespace msa

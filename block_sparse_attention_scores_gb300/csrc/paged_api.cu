@@ -38,6 +38,7 @@ static void cut_pages(long long tiles, int pages, double extra, double join, int
 }
 
 PagedWs paged_ws_layout(const PagedProb& p, int which) {
+  const bool bytes = which == MSA_WS_PAGED_SPARSE_FP8 || which == MSA_WS_PAGED_DENSE_FP8;
   PagedWs L;
   size_t off = 256;  // header: error word
   auto take = [&](size_t bytes) {
@@ -52,7 +53,7 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
   L.rows = take((size_t)p.N * 16);
   L.lead = take((size_t)p.N * 16);
   L.arrived = take((size_t)p.N * p.G * 12);
-  if (which == MSA_WS_PAGED_SPARSE) {
+  if (which == MSA_WS_PAGED_SPARSE || which == MSA_WS_PAGED_SPARSE_FP8) {
     if (p.k > 1 && p.max_blocks > 1) L.pooled = take((size_t)p.N * p.G * p.max_blocks * 8);
     if (p.k > 1) L.n_flags = (int)std::min<long long>((long long)p.S * ((p.max_blocks + 4) / 6), kCutSms - 1);
     L.flags = take(kCutSms * 4);
@@ -63,7 +64,7 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
     // rows count, as nothing here tells them from others: the ninth column is for a pad of up to an eighth. Against eight
     // columns at a time: 32 sequences of 2 rows x 64 heads over 2000 tokens 63 -> 60 us, of 8 rows 135 -> 69, 300 rows x 32
     // heads over 4 groups and 8000 tokens 274 -> 64; the other way for one page (8 rows x 64 heads over 100 tokens 17 -> 10).
-    const bool runs = (long long)p.N * p.hg > 9LL * p.S && p.max_blocks - p.prefix > 1;
+    const bool runs = !bytes && (long long)p.N * p.hg > 9LL * p.S && p.max_blocks - p.prefix > 1;
     // A shared prefix of ten pages an SM (13 where a sequence has several tiles of eight columns), counted for every such
     // tile, is read as own pages: it stays in L2, and two kernels do with it what four do. 4 sequences of 32 heads over 8
     // groups behind 16 pages 15 us against 19, 16 behind 8 pages 14 and 19, 8 of 4 rows behind 12 pages (1536) 17 and 21,
@@ -73,7 +74,7 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
     const long long tiles = std::max(p.N / L.tile_rows, std::min(p.S, p.N));
     // (Idle sequences count too: their tables are looked at by the one block that lines up the rows.)
     const long long readers = std::max<long long>(tiles, p.S);
-    const bool fold = !runs && readers * p.prefix * p.G <= (readers > p.S ? 2000 : 1500);
+    const bool fold = bytes || !runs && readers * p.prefix * p.G <= (readers > p.S ? 2000 : 1500);
     L.prefix = fold ? 0 : p.prefix;
     if (runs) {
       L.run_rows = 256 / p.hg;
@@ -169,12 +170,31 @@ static msa_status check_cache(const msa_paged_cache* c, bool index, PagedCachePt
   return MSA_OK;
 }
 
+static msa_status check_cache(const msa_paged_cache_fp8* c, bool index, PagedCachePtrs* out, bool rows = true) {
+  msa_status s;
+  if (!c) return fail(MSA_ERR_INVALID_ARG, "cache is NULL");
+  if ((s = check_ptr(c->K, "cache.K", 16)) != MSA_OK) return s;
+  if ((s = check_ptr(c->V, "cache.V", 16)) != MSA_OK) return s;
+  if ((s = check_ptr(c->K_exp, "cache.K_exp", 16)) != MSA_OK) return s;
+  if ((s = check_ptr(c->V_exp, "cache.V_exp", 16)) != MSA_OK) return s;
+  if (index && (s = check_ptr(c->k_idx, "cache.k_idx", 16)) != MSA_OK) return s;
+  if (index && (s = check_ptr(c->k_idx_exp, "cache.k_idx_exp", 16)) != MSA_OK) return s;
+  if ((s = check_ptr(c->page_table, "cache.page_table", 4)) != MSA_OK) return s;
+  if (rows && (s = check_ptr(c->row_start, "cache.row_start", 4)) != MSA_OK) return s;
+  if ((s = check_ptr(c->seq_len, "cache.seq_len", 4)) != MSA_OK) return s;
+  *out = {c->K,      c->V,     c->k_idx, c->page_table, c->row_start, c->seq_len, static_cast<uint8_t*>(c->K_exp),
+          static_cast<uint8_t*>(c->V_exp), static_cast<uint8_t*>(c->k_idx_exp)};
+  return MSA_OK;
+}
+
 static msa_status encode_pools(const PagedProb& p, const PagedCachePtrs& c, PoolMaps* m) {
+  const bool bytes = c.bytes();
   const uint64_t dims[2] = {128, (uint64_t)p.num_pages * p.G * 128};
-  const uint64_t strides[1] = {256};
-  const uint32_t box[2] = {64, 128};
-  if (encode_tmap(&m->k, c.K, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
-      encode_tmap(&m->v, c.V, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+  const uint64_t strides[1] = {bytes ? 128u : 256u};
+  const uint32_t box[2] = {bytes ? 128u : 64u, 128};
+  const CUtensorMapDataType type = bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if (encode_tmap(&m->k, c.K, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, type) &&
+      encode_tmap(&m->v, c.V, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, type))
     return MSA_OK;
   return fail(MSA_ERR_CUDA, "tensor maps of the pools could not be encoded");
 }
@@ -205,23 +225,11 @@ static msa_status check_rot(int rot, int dim, const float* freq, const char* nam
   return MSA_OK;
 }
 
-}  // namespace msa
-
-using namespace msa;
-
-extern "C" {
-
-size_t msa_paged_workspace_size(const msa_paged_shape* shape, int which) {
-  PagedProb p{};
-  if (which < MSA_WS_PAGED_APPEND || which > MSA_WS_PAGED_DENSE) return 0;
-  if (validate_paged(shape, &p) != MSA_OK) return 0;
-  if (which != MSA_WS_PAGED_DENSE) p.prefix = 0;
-  return paged_ws_layout(p, which).total;
-}
-
-msa_status msa_paged_append(const msa_paged_shape* shape, const msa_paged_cache* cache, const msa_rope* rope,
-                            const msa_new_rows* rows, void* Q_out, void* q_idx_out, void* workspace,
-                            size_t workspace_bytes, msa_stream_t stream) {
+// The appends into a cache of either type, with or without positions of several axes.
+template <class Cache>
+static msa_status append(const msa_paged_shape* shape, const Cache* cache, const msa_rope* rope, const msa_axes* axes,
+                         const msa_new_rows* rows, void* Q_out, void* q_idx_out, void* workspace, size_t workspace_bytes,
+                         msa_stream_t stream) {
   PagedProb p{};
   PagedCachePtrs c;
   PagedWs L;
@@ -248,6 +256,12 @@ msa_status msa_paged_append(const msa_paged_shape* shape, const msa_paged_cache*
   if ((s = check_rot(rope->rot_dim, 128, rope->inv_freq, "rot_dim")) != MSA_OK) return s;
   const bool index = n.q_idx || n.k_idx;
   if (index && (s = check_rot(rope->rot_dim_idx, 64, rope->inv_freq_idx, "rot_dim_idx")) != MSA_OK) return s;
+  if (axes) {
+    if (axes->axes < 1 || axes->axes > 8) return fail(MSA_ERR_INVALID_ARG, "axes=%d: 1 to 8 are needed", axes->axes);
+    if ((s = check_ptr(axes->positions, "axes.positions", 4)) != MSA_OK) return s;
+    if (axes->axis && (s = check_ptr(axes->axis, "axes.axis", 4)) != MSA_OK) return s;
+    if (axes->axis_idx && (s = check_ptr(axes->axis_idx, "axes.axis_idx", 4)) != MSA_OK) return s;
+  }
   if ((s = check_paged_ws(p, MSA_WS_PAGED_APPEND, workspace, workspace_bytes, &L)) != MSA_OK) return s;
   if ((s = check_device()) != MSA_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -269,12 +283,17 @@ msa_status msa_paged_append(const msa_paged_shape* shape, const msa_paged_cache*
   r.rot = rope->rot_dim;
   r.rot_idx = index ? rope->rot_dim_idx : 0;
   r.interleaved = rope->interleaved != 0;
+  r.axes = axes ? axes->axes : 0;
+  r.positions = axes ? axes->positions : nullptr;
+  r.axis = axes ? axes->axis : nullptr;
+  r.axis_idx = axes ? axes->axis_idx : nullptr;
   return cuda_status(launch_paged_append(p, c, r, static_cast<uint8_t*>(workspace), st), "paged append launch");
 }
 
-msa_status msa_paged_sparse_attn(const msa_paged_shape* shape, const msa_paged_cache* cache, const void* Q,
-                                 const void* q_idx, int32_t* block_idx, void* O, float* LSE, void* workspace,
-                                 size_t workspace_bytes, msa_stream_t stream) {
+template <class Cache>
+static msa_status sparse_attn(const msa_paged_shape* shape, const Cache* cache, int which, const void* Q, const void* q_idx,
+                              int32_t* block_idx, void* O, float* LSE, void* workspace, size_t workspace_bytes,
+                              msa_stream_t stream) {
   PagedProb p{};
   PagedCachePtrs c;
   PagedWs L;
@@ -287,7 +306,7 @@ msa_status msa_paged_sparse_attn(const msa_paged_shape* shape, const msa_paged_c
   if ((s = check_ptr(block_idx, "block_idx", 4)) != MSA_OK) return s;
   if ((s = check_ptr(O, "O", 16)) != MSA_OK) return s;
   if ((s = check_ptr(LSE, "LSE", 4)) != MSA_OK) return s;
-  if ((s = check_paged_ws(p, MSA_WS_PAGED_SPARSE, workspace, workspace_bytes, &L)) != MSA_OK) return s;
+  if ((s = check_paged_ws(p, which, workspace, workspace_bytes, &L)) != MSA_OK) return s;
   if ((s = check_device()) != MSA_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(workspace);
@@ -300,8 +319,9 @@ msa_status msa_paged_sparse_attn(const msa_paged_shape* shape, const msa_paged_c
   return cuda_status(launch_paged_attn(p, c, maps, Q, block_idx, O, LSE, w, L, st), "paged attention launch");
 }
 
-msa_status msa_paged_dense_attn(const msa_paged_shape* shape, const msa_paged_cache* cache, const void* Q, void* O,
-                                float* LSE, void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+template <class Cache>
+static msa_status dense_attn(const msa_paged_shape* shape, const Cache* cache, int which, const void* Q, void* O, float* LSE,
+                             void* workspace, size_t workspace_bytes, msa_stream_t stream) {
   PagedProb p{};
   PagedCachePtrs c;
   PagedWs L;
@@ -311,7 +331,7 @@ msa_status msa_paged_dense_attn(const msa_paged_shape* shape, const msa_paged_ca
   if ((s = check_ptr(Q, "Q", 16)) != MSA_OK) return s;
   if ((s = check_ptr(O, "O", 16)) != MSA_OK) return s;
   if ((s = check_ptr(LSE, "LSE", 4)) != MSA_OK) return s;
-  if ((s = check_paged_ws(p, MSA_WS_PAGED_DENSE, workspace, workspace_bytes, &L)) != MSA_OK) return s;
+  if ((s = check_paged_ws(p, which, workspace, workspace_bytes, &L)) != MSA_OK) return s;
   if ((s = check_device()) != MSA_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(workspace);
@@ -324,6 +344,85 @@ msa_status msa_paged_dense_attn(const msa_paged_shape* shape, const msa_paged_ca
       (s = cuda_status(launch_paged_attn(p, c, maps, Q, nullptr, O, LSE, w, L, st), "paged attention launch")) != MSA_OK)
     return s;
   return parts ? cuda_status(launch_paged_merge(p, O, LSE, w, L, st), "paged merge launch") : MSA_OK;
+}
+
+}  // namespace msa
+
+using namespace msa;
+
+extern "C" {
+
+size_t msa_paged_workspace_size(const msa_paged_shape* shape, int which) {
+  PagedProb p{};
+  const bool dense = which == MSA_WS_PAGED_DENSE || which == MSA_WS_PAGED_DENSE_FP8;
+  if (!dense && which != MSA_WS_PAGED_APPEND && which != MSA_WS_PAGED_SPARSE && which != MSA_WS_PAGED_SPARSE_FP8) return 0;
+  if (validate_paged(shape, &p) != MSA_OK) return 0;
+  if (!dense) p.prefix = 0;
+  return paged_ws_layout(p, which).total;
+}
+
+msa_status msa_paged_append(const msa_paged_shape* shape, const msa_paged_cache* cache, const msa_rope* rope,
+                            const msa_new_rows* rows, void* Q_out, void* q_idx_out, void* workspace,
+                            size_t workspace_bytes, msa_stream_t stream) {
+  return append(shape, cache, rope, nullptr, rows, Q_out, q_idx_out, workspace, workspace_bytes, stream);
+}
+
+msa_status msa_paged_append_axes(const msa_paged_shape* shape, const msa_paged_cache* cache, const msa_rope* rope,
+                                 const msa_axes* axes, const msa_new_rows* rows, void* Q_out, void* q_idx_out,
+                                 void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  return append(shape, cache, rope, axes, rows, Q_out, q_idx_out, workspace, workspace_bytes, stream);
+}
+
+msa_status msa_paged_append_fp8(const msa_paged_shape* shape, const msa_paged_cache_fp8* cache, const msa_rope* rope,
+                                const msa_axes* axes, const msa_new_rows* rows, void* Q_out, void* q_idx_out,
+                                void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  return append(shape, cache, rope, axes, rows, Q_out, q_idx_out, workspace, workspace_bytes, stream);
+}
+
+msa_status msa_paged_read_fp8(const msa_paged_shape* shape, const msa_paged_cache_fp8* cache, const int32_t* first,
+                              const int32_t* out_start, int32_t M, void* K_out, void* V_out, void* k_idx_out,
+                              void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  PagedProb p{};
+  PagedCachePtrs c;
+  PagedWs L;
+  msa_status s;
+  if ((s = validate_paged(shape, &p)) != MSA_OK) return s;
+  p.prefix = 0;
+  if (M < 1) return fail(MSA_ERR_INVALID_ARG, "M=%d: at least one row is needed", M);
+  if (M > (1 << 28)) return fail(MSA_ERR_UNSUPPORTED, "M=%d exceeds 2^28 rows", M);
+  if ((s = check_cache(cache, k_idx_out != nullptr, &c, false)) != MSA_OK) return s;
+  if (first && (s = check_ptr(first, "first", 4)) != MSA_OK) return s;
+  if ((s = check_ptr(out_start, "out_start", 4)) != MSA_OK) return s;
+  if ((s = check_ptr(K_out, "K_out", 32)) != MSA_OK) return s;
+  if ((s = check_ptr(V_out, "V_out", 32)) != MSA_OK) return s;
+  if (k_idx_out && (s = check_ptr(k_idx_out, "k_idx_out", 32)) != MSA_OK) return s;
+  if ((s = check_paged_ws(p, MSA_WS_PAGED_APPEND, workspace, workspace_bytes, &L)) != MSA_OK) return s;
+  if ((s = check_device()) != MSA_OK) return s;
+  const ReadRows r{first, out_start, K_out, V_out, k_idx_out, M};
+  return cuda_status(launch_paged_read(p, c, r, static_cast<uint8_t*>(workspace), reinterpret_cast<cudaStream_t>(stream)),
+                     "paged read launch");
+}
+
+msa_status msa_paged_sparse_attn(const msa_paged_shape* shape, const msa_paged_cache* cache, const void* Q,
+                                 const void* q_idx, int32_t* block_idx, void* O, float* LSE, void* workspace,
+                                 size_t workspace_bytes, msa_stream_t stream) {
+  return sparse_attn(shape, cache, MSA_WS_PAGED_SPARSE, Q, q_idx, block_idx, O, LSE, workspace, workspace_bytes, stream);
+}
+
+msa_status msa_paged_sparse_attn_fp8(const msa_paged_shape* shape, const msa_paged_cache_fp8* cache, const void* Q,
+                                     const void* q_idx, int32_t* block_idx, void* O, float* LSE, void* workspace,
+                                     size_t workspace_bytes, msa_stream_t stream) {
+  return sparse_attn(shape, cache, MSA_WS_PAGED_SPARSE_FP8, Q, q_idx, block_idx, O, LSE, workspace, workspace_bytes, stream);
+}
+
+msa_status msa_paged_dense_attn(const msa_paged_shape* shape, const msa_paged_cache* cache, const void* Q, void* O,
+                                float* LSE, void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  return dense_attn(shape, cache, MSA_WS_PAGED_DENSE, Q, O, LSE, workspace, workspace_bytes, stream);
+}
+
+msa_status msa_paged_dense_attn_fp8(const msa_paged_shape* shape, const msa_paged_cache_fp8* cache, const void* Q, void* O,
+                                    float* LSE, void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  return dense_attn(shape, cache, MSA_WS_PAGED_DENSE_FP8, Q, O, LSE, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

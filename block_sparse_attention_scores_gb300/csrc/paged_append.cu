@@ -17,6 +17,17 @@
 //
 // Measured: 32,764 rows of 32 + 2 x 8 heads (881 MB) 150 us, 5.9 TB/s, 0.88 of a
 // plain copy; one row 3 us in a graph, which is a launch's time.
+//
+// Positions with several axes (kind of token: time, height, width): a pair turns
+// with the position on its own axis, position[r][axis[i]] * f, while the row's
+// place in the cache stays its number in the sequence. Nothing else changes: the
+// positions come with the row's place, one look-up for all axes.
+//
+// A cache in 8 bits (kBytes): K, V and k_idx become codes and a power of two
+// (paged_fp8.cuh). Eight neighbouring threads hold a vector (four an index key),
+// so its largest magnitude takes three shuffles, and the values are quantised in
+// the registers in which they were rotated, from fp32, rounded once.
+#include "paged_fp8.cuh"
 #include "paged_rows.cuh"
 
 namespace msa {
@@ -26,15 +37,18 @@ constexpr int kThreads = 256;
 constexpr int kInFlight = 2;  // items a thread loads at a time
 constexpr int kMaxRows = 4;   // rows of a block
 constexpr int kPairs = 64 + 32;
+constexpr int kMaxAxes = 8;
 
 struct AppendArgs {
   RopeRows r;
-  __nv_bfloat16 *K, *V, *k_idx;
+  void *K, *V, *k_idx;
+  uint8_t *K_exp, *V_exp, *k_idx_exp;  // (kBytes)
   const int32_t *page_table, *row_start, *seq_len;
   int S, N, Hq, G, num_pages, max_blocks;
   int rows;                      // of a block
   int report;                    // the last block checks every row and writes the error word; the others write none
-  int n_q, n_k, n_qi, items;     // items of a row: queries, keys (values as many), index queries; all
+  int n_q, n_k, n_qi, n_ki;      // items of a row: queries, keys (values as many), index queries, its index key
+  int items;                     // all (kBytes: made a multiple of eight, so that no vector's threads are in two warps)
   float inv_items;
   int* err;
 };
@@ -75,6 +89,26 @@ __device__ __forceinline__ void rotate(uint4& x, uint4& y, const float2* cs, int
   }
 }
 
+// The rotated values of both pieces (pair < 0: as they are), not rounded: the first one's eight, then the second one's.
+__device__ __forceinline__ void rotated_values(const uint4& x, const uint4& y, int pair, const float2* cs, int interleaved,
+                                               float (&v)[16]) {
+  const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = lo_f(u[i]);
+    v[2 * i + 1] = hi_f(u[i]);
+  }
+  if (pair < 0) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int p = interleaved ? 2 * i : i, q = interleaved ? 2 * i + 1 : 8 + i;
+    const float2 c = cs[i];
+    const float a = v[p], b = v[q];
+    v[p] = a * c.x - b * c.y;
+    v[q] = b * c.x + a * c.y;
+  }
+}
+
 struct Piece {
   uint4 x, y;
   int row, kind, vec, a, b, pair;  // kind -1: none; 0 Q, 1 K, 2 V, 3 q_idx, 4 k_idx
@@ -83,6 +117,7 @@ struct Piece {
 // Item `it` of the block's rows: which vector's pieces, and their loads.
 __device__ __forceinline__ void load_piece(const AppendArgs& a, int r0, int it, Piece& p) {
   p.kind = -1;
+  p.row = 0;
   const int row = (int)(((float)it + 0.5f) * a.inv_items);
   it -= row * a.items;
   if (row >= a.rows || r0 + row >= a.N) return;
@@ -103,6 +138,7 @@ __device__ __forceinline__ void load_piece(const AppendArgs& a, int r0, int it, 
     src = static_cast<const __nv_bfloat16*>(a.r.q_idx) + r * a.r.ld_q_idx;
   } else {
     it -= a.n_qi;
+    if (it >= a.n_ki) return;  // (past the row's own items)
     p.kind = 4;
     src = static_cast<const __nv_bfloat16*>(a.r.k_idx) + r * a.r.ld_k_idx;
   }
@@ -125,7 +161,46 @@ __device__ __forceinline__ int place_row(const AppendArgs& a, int s, int len, in
   return 1202;
 }
 
+// What the axes of pair t (index pairs from 64 on) are: its own one, 0 (and `bad`) where there is none of that number.
+__device__ __forceinline__ int pair_axis(const AppendArgs& a, int t, bool& bad) {
+  const int32_t* axis = t < 64 ? a.r.axis : a.r.axis_idx;
+  const int x = axis ? __ldg(axis + (t & 63)) : 0;
+  if (x >= 0 && x < a.r.axes) return x;
+  bad = true;
+  return 0;
+}
+
+// A vector's codes and its power of two into the cache, by whole warps. `code`: this thread has a piece of such a vector,
+// of which eight neighbouring threads (four: an index key) have one each. cs: the row's turns.
+__device__ __forceinline__ void quantise_piece(const AppendArgs& a, const Piece& e, bool code, int pos, int page,
+                                               const float2* cs) {
+  const bool idx = e.kind == 4;
+  float v[16], most = 0.f;
+  if (code && pos >= 0) {
+    rotated_values(e.x, e.y, e.pair, cs + (idx ? 64 : 0) + e.pair, a.r.interleaved, v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) most = finite_max(most, v[i]);
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    const float other = __shfl_xor_sync(0xffffffffu, most, o);
+    if (o < 4 || !idx) most = fmaxf(most, other);
+  }
+  if (!code || pos < 0 || page < 0) return;
+  const int byte = exp_byte(most), slot = pos & 127;
+  const float scale = exp_inverse(byte);
+  const size_t at = idx ? (size_t)page * 128 + slot : ((size_t)page * a.G + e.vec) * 128 + slot;
+  uint8_t* dst = static_cast<uint8_t*>(idx ? a.k_idx : e.kind == 1 ? a.K : a.V) + at * (idx ? 64 : 128);
+  const uint2 lo = make_uint2(four_codes(v[0], v[1], v[2], v[3], scale), four_codes(v[4], v[5], v[6], v[7], scale));
+  const uint2 hi = make_uint2(four_codes(v[8], v[9], v[10], v[11], scale), four_codes(v[12], v[13], v[14], v[15], scale));
+  reinterpret_cast<uint2*>(dst)[e.a] = lo;
+  reinterpret_cast<uint2*>(dst)[e.b] = hi;
+  if (e.a == 0) (idx ? a.k_idx_exp : e.kind == 1 ? a.K_exp : a.V_exp)[at] = (uint8_t)byte;
+}
+
+template <bool kBytes>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
+  const int half = a.r.rot / 2, half_idx = a.r.rot_idx / 2;
   if (a.report && blockIdx.x == gridDim.x - 1) {
     int bad = 0;
     const auto start = [&](int i) { return ld_in(a.row_start + i); };
@@ -134,19 +209,25 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
       int pos, page;
       if (s < a.S) bad = max(bad, place_row(a, s, ld_in(a.seq_len + s), start(s + 1) - r, pos, page));
     }
-    const int second = __syncthreads_or(bad == 1202), first = __syncthreads_or(bad == 1201);
-    if (threadIdx.x == 0) *a.err = first ? kDevBadIndex * 65536 + 1201 : second ? kDevBadIndex * 65536 + 1202 : kDevOk;
+    bool axis = false;
+    if (a.r.axes && threadIdx.x < kPairs) {
+      const int t = threadIdx.x;
+      if (t < 64 ? t < half : t - 64 < half_idx) pair_axis(a, t, axis);
+    }
+    const int second = __syncthreads_or(bad == 1202), first = __syncthreads_or(bad == 1201), third = __syncthreads_or(axis);
+    const int where = first ? 1201 : second ? 1202 : third ? 1203 : 0;
+    if (threadIdx.x == 0) *a.err = where ? kDevBadIndex * 65536 + where : kDevOk;
     return;
   }
   __shared__ unsigned long long turns_of[kPairs];  // frequency as a fraction of a turn per position
   __shared__ float2 turn[kMaxRows][kPairs];        // cos, sin of a row's pairs: d, then d_idx
   __shared__ int pos_of[kMaxRows], page_of[kMaxRows];  // -1: no row, or not to be written
+  __shared__ int axis_of[kPairs], at_axis[kMaxRows][kMaxAxes];  // a pair's axis, and a row's positions on each
   const int r0 = blockIdx.x * a.rows, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   Piece p[kInFlight];
 #pragma unroll
   for (int z = 0; z < kInFlight; ++z) load_piece(a, r0, z * kThreads + tid, p[z]);
 
-  const int half = a.r.rot / 2, half_idx = a.r.rot_idx / 2;
   if (tid >= kThreads - kPairs) {  // the last three warps
     const int t = tid - (kThreads - kPairs);
     const bool idx = t >= 64;
@@ -154,10 +235,16 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
     if (i < (idx ? half_idx : half)) {
       const double turns = (double)__ldg((idx ? a.r.inv_freq_idx : a.r.inv_freq) + i) * 0.15915494309189533577;
       turns_of[t] = (unsigned long long)((turns - floor(turns)) * 18446744073709551616.0);
+      if (a.r.axes) {
+        bool bad = false;
+        axis_of[t] = pair_axis(a, t, bad);
+        if (bad && !a.report) dev_fail(a.err, kDevBadIndex, 1203);
+      }
     }
   } else if (warp < a.rows) {  // the rows' sequences, positions and pages, a warp each
     const int r = r0 + warp;
     int pos = -1, page = -1;
+    if (r < a.N && lane < a.r.axes) at_axis[warp][lane] = __ldg(a.r.positions + (size_t)r * a.r.axes + lane);
     const int s = r < a.N ? find_sequence(a.row_start, a.S, r, lane) : a.S;
     if (s < a.S) {  // not behind the last sequence
       const int bad = place_row(a, s, ld_in(a.seq_len + s), ld_in(a.row_start + s + 1) - r, pos, page);
@@ -172,7 +259,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
   for (int i = tid; i < a.rows * kPairs; i += kThreads) {
     const int row = i / kPairs, t = i - row * kPairs, pos = pos_of[row];
     if (pos >= 0 && (t < 64 ? t < half : t - 64 < half_idx)) {
-      const unsigned long long phase = turns_of[t] * (unsigned long long)pos;
+      const long long at = a.r.axes ? at_axis[row][axis_of[t]] : pos;  // (modulo 2^64 a negative one turns backward)
+      const unsigned long long phase = turns_of[t] * (unsigned long long)at;
       float sn, cs;
       sincospif((float)(int)(uint32_t)(phase >> 32) * 4.656612873077393e-10f, &sn, &cs);  // the top 32 bits, in half turns
       turn[row][t] = make_float2(cs, sn);
@@ -188,6 +276,11 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
 #pragma unroll
     for (int z = 0; z < kInFlight; ++z) {
       Piece& e = p[z];
+      if constexpr (kBytes) {
+        const bool code = e.kind == 1 || e.kind == 2 || e.kind == 4;
+        if (__any_sync(0xffffffffu, code)) quantise_piece(a, e, code, pos_of[e.row], page_of[e.row], turn[e.row]);
+        if (code) continue;
+      }
       if (e.kind < 0) continue;
       const int pos = pos_of[e.row], page = page_of[e.row];
       if (pos < 0) continue;
@@ -203,9 +296,9 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
         if (page < 0) continue;
         const int slot = pos & 127;
         if (e.kind == 4)
-          dst = a.k_idx + ((size_t)page * 128 + slot) * 64;
+          dst = static_cast<__nv_bfloat16*>(a.k_idx) + ((size_t)page * 128 + slot) * 64;
         else
-          dst = (e.kind == 1 ? a.K : a.V) + (((size_t)page * a.G + e.vec) * 128 + slot) * 128;
+          dst = static_cast<__nv_bfloat16*>(e.kind == 1 ? a.K : a.V) + (((size_t)page * a.G + e.vec) * 128 + slot) * 128;
       }
       reinterpret_cast<uint4*>(dst)[e.a] = e.x;
       reinterpret_cast<uint4*>(dst)[e.b] = e.y;
@@ -219,9 +312,12 @@ cudaError_t launch_paged_append(const PagedProb& p, const PagedCachePtrs& c, con
                                 cudaStream_t st) {
   AppendArgs a;
   a.r = r;
-  a.K = static_cast<__nv_bfloat16*>(c.K);
-  a.V = static_cast<__nv_bfloat16*>(c.V);
-  a.k_idx = static_cast<__nv_bfloat16*>(c.k_idx);
+  a.K = c.K;
+  a.V = c.V;
+  a.k_idx = c.k_idx;
+  a.K_exp = c.K_exp;
+  a.V_exp = c.V_exp;
+  a.k_idx_exp = c.k_idx_exp;
   a.page_table = c.page_table;
   a.row_start = c.row_start;
   a.seq_len = c.seq_len;
@@ -235,7 +331,9 @@ cudaError_t launch_paged_append(const PagedProb& p, const PagedCachePtrs& c, con
   a.n_q = r.Q ? 8 * p.Hq : 0;
   a.n_k = 8 * p.G;
   a.n_qi = r.q_idx ? 4 * p.G : 0;
-  a.items = a.n_q + 2 * a.n_k + a.n_qi + (r.k_idx ? 4 : 0);
+  a.n_ki = r.k_idx ? 4 : 0;
+  a.items = a.n_q + 2 * a.n_k + a.n_qi + a.n_ki;
+  if (c.bytes()) a.items = (a.items + 7) / 8 * 8;
   a.inv_items = 1.f / (float)a.items;
   // Rows for two rounds of a block's loads, so that its look-ups are shared, as long as every SM gets three blocks. 38,610
   // rows of 4 + 2 x 4 heads take 97 us with one row a block and 57 with four; 6,710 rows of 64 + 2 x 8, whose blocks are long
@@ -250,7 +348,8 @@ cudaError_t launch_paged_append(const PagedProb& p, const PagedCachePtrs& c, con
     const cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
     if (e != cudaSuccess) return e;
   }
-  paged_append_kernel<<<(p.N + a.rows - 1) / a.rows + a.report, kThreads, 0, st>>>(a);
+  (c.bytes() ? paged_append_kernel<true> : paged_append_kernel<false>)<<<(p.N + a.rows - 1) / a.rows + a.report, kThreads, 0,
+                                                                        st>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }

@@ -26,7 +26,24 @@
 // There, each row of the tile is accumulated on its own with the values behind
 // its end cleared, so that nothing stored behind a row's end (another row's
 // tokens, stale cache lines, NaN or infinities) reaches it through 0 * x.
+//
+// A cache in 8 bits (kBytes, paged_fp8.cuh): the same scheme over pages of half the
+// length, six in flight. Codes become fp16 pairs in one conversion each, which is
+// what the matrix instructions then take; the powers of two stay outside of them:
+//   s_j = (K_j' q') 2^(e_j + e_q) scale log2 e,   q = q' 2^e_q in fp16
+//   l   = sum_j exp2(s_j - m),                    m = max_j s_j
+//   O'  = sum_j fp16(2^15 exp2(s_j + f_j - w)) V_j',  w = max_j (s_j + f_j)
+//   O   = O' 2^(w - m - 15) / l
+// with e_j, f_j the exponents of token j's K and V. What is summed in O' is thus the
+// part that a token really has in it, at most 1 before the factor 2^15, which lets
+// fp16 hold it down to 2^-39 of the largest: all 2^20 tokens' roundings then stay
+// below 2^-19 of O. P needs no second part (fp16 has eleven bits), and V' no infinities.
+// A page's codes are read as they lie: K by ldmatrix (a lane gets four neighbouring
+// codes of a key, the sum's order over d follows), V by 16-byte loads of four keys'
+// 16 neighbouring dims, paired by key with byte permutes, so that the fragments of
+// the transposed V come without a transposing load, which there is none of for bytes.
 #include "mma_sync.cuh"
+#include "paged_fp8.cuh"
 #include "paged_rows.cuh"
 
 namespace msa {
@@ -36,8 +53,14 @@ constexpr int kWarps = 8;                          // consumers; then the produc
 constexpr int kJoinWarps = 3;
 constexpr int kThreads = (kWarps + 1 + kJoinWarps) * 32;
 constexpr int kHalf = 16384;                       // 128 rows x 64 bf16, 128-byte swizzle
-constexpr int kTile = 2 * kHalf;                   // K or V of a page and group
-constexpr int kStages = 3;
+template <bool kBytes>
+struct Pages {                                     // K or V of a page and group; pages in flight; a stage's powers of two
+  static constexpr int kTile = 2 * kHalf, kStages = 3, kExps = 0;
+};
+template <>
+struct Pages<true> {                               // 128 rows x 128 codes, 128-byte swizzle
+  static constexpr int kTile = kHalf, kStages = 6, kExps = 256;
+};
 // The joining warps may have nothing to do until the kernel's end: 20 s, and 20 us for every page that a CTA takes if it
 // takes them all in turn (it takes 1.5).
 constexpr unsigned long long kIdleNs = 20000000000ull, kIdlePageNs = 20000ull;
@@ -45,13 +68,15 @@ constexpr unsigned long long kIdleNs = 20000000000ull, kIdlePageNs = 20000ull;
 constexpr int kQStride = 272;                      // bytes between the queries' rows in shared memory (no bank conflicts)
 
 constexpr int kCols = 8;                           // query columns of a tile
-constexpr int kSmem = kStages * 2 * kTile + 2 * kCols * kQStride + 1024;
+template <bool kBytes>
+constexpr int kSmem = Pages<kBytes>::kStages * (2 * Pages<kBytes>::kTile + Pages<kBytes>::kExps) + 2 * kCols * kQStride + 1024;
 
 struct AttnArgs {
   const int4* rows;
   const int4* lead;                       // the rows that lead a tile (null: every row does)
   int* header;                            // of the workspace: kLeadCount, kWorkNext
   const __nv_bfloat16* Q;
+  const uint8_t *K_exp, *V_exp;           // (kBytes)
   const int32_t *page_table, *block_idx;  // block_idx null: the sequence's own pages from block `prefix` on
   float *part_o, *part_lse;
   int* arrived;                           // [N, G, kJoinWarps] items of a (row tile, group) that are done
@@ -72,6 +97,7 @@ struct AttnItem {
   int pos, rows;             // position of the first row; rows of the tile
 };
 
+template <int kStages>
 struct AttnShared {
   uint64_t k_full[kStages], v_full[kStages], empty[kStages];
   uint64_t q_full[2], q_empty[2];
@@ -81,6 +107,7 @@ struct AttnShared {
   AttnItem join[2];           // for the joining warps; parts 0: the end
   int token0[kStages];        // first token of the stage's page
   float m[kWarps][kCols], l[kWarps][kCols];  // maximum and sum of a warp's columns
+  float w[kWarps][kCols];                    // (kBytes) what its O is relative to
   float inv[kCols], lse[kCols];            // of all warps together: 1 / sum, and log2 of the sum
 };
 
@@ -216,12 +243,15 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const AttnItem& it
   }
 }
 
+template <bool kBytes>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attn_kernel(AttnArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ AttnShared sh;
-  uint8_t* s_q = smem + kStages * 2 * kTile;  // [2][kCols][kQStride]
+  constexpr int kTile = Pages<kBytes>::kTile, kStages = Pages<kBytes>::kStages;
+  __shared__ AttnShared<kStages> sh;
+  uint8_t* s_q = smem + kStages * 2 * kTile;    // [2][kCols][kQStride]
+  uint8_t* s_exp = s_q + 2 * kCols * kQStride;  // [kStages][K, V][128] (kBytes)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -306,12 +336,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               sh.token0[st] = pg >= 0 ? bl * 128 : 0x3fffff00;
               const int y = (max(pg, 0) * a.G + now.g) * 128;
               uint8_t* d = smem + st * 2 * kTile;
-              mbar_arrive_expect_tx(&sh.k_full[st], kTile);
+              mbar_arrive_expect_tx(&sh.k_full[st], kTile + Pages<kBytes>::kExps / 2);
               tma_load_2d(d, &map_k, &sh.k_full[st], 0, y);
-              tma_load_2d(d + kHalf, &map_k, &sh.k_full[st], 64, y);
-              mbar_arrive_expect_tx(&sh.v_full[st], kTile);
+              if (kBytes) bulk_load(s_exp + st * 256, a.K_exp + y, 128, &sh.k_full[st]);
+              else tma_load_2d(d + kHalf, &map_k, &sh.k_full[st], 64, y);
+              mbar_arrive_expect_tx(&sh.v_full[st], kTile + Pages<kBytes>::kExps / 2);
               tma_load_2d(d + kTile, &map_v, &sh.v_full[st], 0, y);
-              tma_load_2d(d + kTile + kHalf, &map_v, &sh.v_full[st], 64, y);
+              if (kBytes) bulk_load(s_exp + st * 256 + 128, a.V_exp + y, 128, &sh.v_full[st]);
+              else tma_load_2d(d + kTile + kHalf, &map_v, &sh.v_full[st], 64, y);
             }
             __syncwarp();
             if (++st == kStages) {
@@ -365,15 +397,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       const AttnItem item = sh.item[qs];
       if (item.pages < 0) break;
       const int cols = item.rows * a.hg;
-      // query fragments: column r, dims 16 ks + 2 q, + 1 and + 8, + 9
+      // query fragments: column r, dims 16 ks + 2 q, + 1 and + 8, + 9 (kBytes: + 4 q, + 1 and + 2, + 3, as the codes lie)
       uint32_t qb[8][2];
       {
         const uint8_t* src = s_q + (qs * kCols + r) * kQStride;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-          qb[ks][0] = r < cols ? *reinterpret_cast<const uint32_t*>(src + ks * 32 + q * 4) : 0u;
-          qb[ks][1] = r < cols ? *reinterpret_cast<const uint32_t*>(src + ks * 32 + 16 + q * 4) : 0u;
+          qb[ks][0] = r < cols ? *reinterpret_cast<const uint32_t*>(src + ks * 32 + q * (kBytes ? 8 : 4)) : 0u;
+          qb[ks][1] = r < cols ? *reinterpret_cast<const uint32_t*>(src + ks * 32 + (kBytes ? q * 8 + 4 : 16 + q * 4)) : 0u;
         }
+      }
+      float qscale[2] = {a.scale_log2, a.scale_log2};  // (kBytes) of columns 2 q, + 1: times what their fp16 values lack
+      if constexpr (kBytes) {
+        float most = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) most = finite_max2(finite_max2(most, qb[ks][0]), qb[ks][1]);
+#pragma unroll
+        for (int x = 1; x < 4; x <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
+        const uint32_t byte = query_scale_byte(most);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+          for (int z = 0; z < 2; ++z) qb[ks][z] = f16_of_bf16(qb[ks][z], exp_value(byte));
+#pragma unroll
+        for (int z = 0; z < 2; ++z) qscale[z] *= exp_value(254 - __shfl_sync(0xffffffffu, byte, (2 * q + z) * 4));
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_empty[qs]);
@@ -383,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int z = 0; z < 2; ++z) lim[z] = lim_lo + ((2 * q + z) >> a.hg_log2);
 
       float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f}, o[8][4];
+      float w_run[2] = {-INFINITY, -INFINITY};  // (kBytes)
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
@@ -392,88 +440,187 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait(&sh.k_full[st], st_ph, a.err, 1422)) { ok = false; break; }
         const int token0 = sh.token0[st] + warp * 16;  // of this warp's keys
         const uint32_t kaddr = smem_u32(smem + st * 2 * kTile), vaddr = kaddr + kTile;
-        float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};  // even and odd steps of the sum over d
-        {
-          const int key = warp * 16 + (lane & 15);
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            uint32_t f[4];
-            ldmatrix_x4(f, kaddr + (ks >> 2) * kHalf + sw128_off(key, (ks & 3) * 2 + (lane >> 4)));
-            mma_16816(ks & 1 ? sd : sc, f[0], f[1], f[2], f[3], qb[ks][0], qb[ks][1]);
-          }
-        }
         const bool masked = token0 + 16 > lim_lo;
-        float mx[2] = {-INFINITY, -INFINITY};
+        if constexpr (kBytes) {
+          float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};  // even and odd steps of the sum over d
+          {
+            const int key = warp * 16 + (lane & 15);
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          float v = (sc[z] + sd[z]) * a.scale_log2;
-          if (masked && token0 + r + (z >> 1) * 8 >= lim[z & 1]) v = -INFINITY;
-          sc[z] = v;
-          mx[z & 1] = fmaxf(mx[z & 1], v);
-        }
+            for (int c = 0; c < 8; c += 2) {  // keys r, r + 8, pieces c and c + 1 of 16 codes: four each
+              uint32_t f[4];
+              ldmatrix_x4(f, kaddr + sw128_off(key, c + (lane >> 4)));
+              mma_16816_f16(sc, f16_lo(f[0]), f16_lo(f[1]), f16_hi(f[0]), f16_hi(f[1]), qb[c][0], qb[c][1]);
+              mma_16816_f16(sd, f16_lo(f[2]), f16_lo(f[3]), f16_hi(f[2]), f16_hi(f[3]), qb[c + 1][0], qb[c + 1][1]);
+            }
+          }
+          const uint8_t* ke = s_exp + st * 256 + warp * 16 + r;
+          float k2[2], x[4], top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // maxima of s, then of s + f
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1)
+          for (int y = 0; y < 2; ++y) k2[y] = exp_value(ke[8 * y]);
 #pragma unroll
-          for (int z = 0; z < 2; ++z) mx[z] = fmaxf(mx[z], __shfl_xor_sync(0xffffffffu, mx[z], x));
-        bool moved = false;
-        float alpha[2], base[2];
+          for (int z = 0; z < 4; ++z) {
+            float v = (sc[z] + sd[z]) * k2[z >> 1] * qscale[z & 1];
+            if (masked && token0 + r + (z >> 1) * 8 >= lim[z & 1]) v = -INFINITY;
+            sc[z] = v;
+            top[z & 1] = fmaxf(top[z & 1], v);
+          }
+          if (!mbar_wait(&sh.v_full[st], st_ph, a.err, 1423)) { ok = false; break; }
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          const float m_new = fmaxf(m_run[z], mx[z]);
-          moved |= m_new > m_run[z];
-          base[z] = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet: exp2(-inf - 0) = 0
-          alpha[z] = fast_exp2(m_run[z] - base[z]);
-          m_run[z] = m_new;
-        }
-        if (__any_sync(0xffffffffu, moved)) {
-          l_run[0] *= alpha[0];
-          l_run[1] *= alpha[1];
+          for (int z = 0; z < 4; ++z) {
+            x[z] = sc[z] + (float)((int)ke[128 + 8 * (z >> 1)] - 127);
+            top[2 + (z & 1)] = fmaxf(top[2 + (z & 1)], x[z]);
+          }
 #pragma unroll
-          for (int mt = 0; mt < 8; ++mt)
+          for (int d = 4; d < 32; d <<= 1)
 #pragma unroll
-            for (int z = 0; z < 4; ++z) o[mt][z] *= alpha[z & 1];
-        }
-        // P as hi + lo, turned so that a lane holds two neighbouring keys of one column
-        uint32_t ph[2], pl[2];
+            for (int z = 0; z < 4; ++z) top[z] = fmaxf(top[z], __shfl_xor_sync(0xffffffffu, top[z], d));
+          bool moved = false;
+          float alpha[2], base[2], wbase[2];
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const float p0 = fast_exp2(sc[2 * y] - base[0]);
-          const float p1 = fast_exp2(sc[2 * y + 1] - base[1]);
-          l_run[0] += p0;
-          l_run[1] += p1;
-          const uint32_t h = bf16_cut(p0, p1);
-          ph[y] = movmatrix_trans(h);
-          pl[y] = movmatrix_trans(bf16_rest(p0, p1, h));
-        }
-        if (!mbar_wait(&sh.v_full[st], st_ph, a.err, 1423)) { ok = false; break; }
-        const int key = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
-        if (!masked || item.rows == 1) {
-          const uint2 keep = keep_keys(token0 + 2 * q, masked ? lim_lo : 0x7fffffff);
+          for (int z = 0; z < 2; ++z) {
+            const float m_new = fmaxf(m_run[z], top[z]), w_new = fmaxf(w_run[z], top[2 + z]);
+            moved |= w_new > w_run[z];
+            base[z] = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet: exp2(-inf - 0) = 0
+            wbase[z] = w_new == -INFINITY ? 0.f : w_new;
+            l_run[z] *= fast_exp2(m_run[z] - base[z]);
+            alpha[z] = fast_exp2(w_run[z] - wbase[z]);
+            wbase[z] -= 15.f;
+            m_run[z] = m_new;
+            w_run[z] = w_new;
+          }
+          if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-          for (int mt = 0; mt < 8; ++mt) {
-            uint32_t f[4];
-            ldmatrix_x4_trans(f, vaddr + (mt >> 2) * kHalf + sw128_off(key, (mt & 3) * 2 + ((lane >> 3) & 1)));
-            const uint32_t v[4] = {f[0] & keep.x, f[1] & keep.x, f[2] & keep.y, f[3] & keep.y};
-            mma_16816(o[mt], v[0], v[1], v[2], v[3], ph[0], ph[1]);
-            mma_16816(o[mt], v[0], v[1], v[2], v[3], pl[0], pl[1]);
+            for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+              for (int z = 0; z < 4; ++z) o[mt][z] *= alpha[z & 1];
+          }
+          uint32_t ph[2];  // turned so that a lane holds two neighbouring keys of one column
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            l_run[0] += fast_exp2(sc[2 * y] - base[0]);
+            l_run[1] += fast_exp2(sc[2 * y + 1] - base[1]);
+            ph[y] = movmatrix_trans(pack_f16(fast_exp2(x[2 * y] - wbase[0]), fast_exp2(x[2 * y + 1] - wbase[1])));
+          }
+          // dims 16 r .. + 15 of keys 2 q, + 1 and + 8, + 9: tile mt's row r is dim 16 r + 2 mt, its row r + 8 the next one
+          uint4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = warp * 16 + 2 * q + (i & 1) + (i >> 1) * 8;
+            v[i] = *reinterpret_cast<const uint4*>(smem + st * 2 * kTile + kTile + sw128_off(key, r));
+          }
+          auto add_values = [&](float (&to)[4], int mt, int end) {  // of the keys before token `end`
+            uint32_t c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t word[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+              c[i] = token0 + 2 * q + (i & 1) + (i >> 1) * 8 < end ? word[mt >> 1] : 0u;
+            }
+            const uint32_t by = mt & 1 ? 0x7362 : 0x5140;  // two dims' pairs of keys
+            const uint32_t lo = __byte_perm(c[0], c[1], by), hi = __byte_perm(c[2], c[3], by);
+            mma_16816_f16(to, f16_lo(lo), f16_hi(lo), f16_lo(hi), f16_hi(hi), ph[0], ph[1]);
+          };
+          if (!masked) {
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt) add_values(o[mt], mt, 0x7fffffff);
+          } else {
+            // each row of the tile on its own: values behind its end cleared, and only its own columns kept
+#pragma unroll 1
+            for (int i = 0; i < item.rows; ++i) {
+              const int end = lim_lo + i;
+              if (token0 >= end) continue;
+#pragma unroll
+              for (int mt = 0; mt < 8; ++mt) {
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                add_values(t, mt, end);
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                  if (lim[z & 1] == end) o[mt][z] += t[z];
+              }
+            }
           }
         } else {
-          // each row of the tile on its own: values behind its end cleared, and only its own columns kept
-#pragma unroll 1
-          for (int i = 0; i < item.rows; ++i) {
-            const int end = lim_lo + i;
-            if (token0 >= end) continue;
-            const uint2 keep = keep_keys(token0 + 2 * q, end);
+          float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};  // even and odd steps of the sum over d
+          {
+            const int key = warp * 16 + (lane & 15);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+              uint32_t f[4];
+              ldmatrix_x4(f, kaddr + (ks >> 2) * kHalf + sw128_off(key, (ks & 3) * 2 + (lane >> 4)));
+              mma_16816(ks & 1 ? sd : sc, f[0], f[1], f[2], f[3], qb[ks][0], qb[ks][1]);
+            }
+          }
+          float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            float v = (sc[z] + sd[z]) * a.scale_log2;
+            if (masked && token0 + r + (z >> 1) * 8 >= lim[z & 1]) v = -INFINITY;
+            sc[z] = v;
+            mx[z & 1] = fmaxf(mx[z & 1], v);
+          }
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) mx[z] = fmaxf(mx[z], __shfl_xor_sync(0xffffffffu, mx[z], x));
+          bool moved = false;
+          float alpha[2], base[2];
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const float m_new = fmaxf(m_run[z], mx[z]);
+            moved |= m_new > m_run[z];
+            base[z] = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet: exp2(-inf - 0) = 0
+            alpha[z] = fast_exp2(m_run[z] - base[z]);
+            m_run[z] = m_new;
+          }
+          if (__any_sync(0xffffffffu, moved)) {
+            l_run[0] *= alpha[0];
+            l_run[1] *= alpha[1];
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+              for (int z = 0; z < 4; ++z) o[mt][z] *= alpha[z & 1];
+          }
+          // P as hi + lo, turned so that a lane holds two neighbouring keys of one column
+          uint32_t ph[2], pl[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float p0 = fast_exp2(sc[2 * y] - base[0]);
+            const float p1 = fast_exp2(sc[2 * y + 1] - base[1]);
+            l_run[0] += p0;
+            l_run[1] += p1;
+            const uint32_t h = bf16_cut(p0, p1);
+            ph[y] = movmatrix_trans(h);
+            pl[y] = movmatrix_trans(bf16_rest(p0, p1, h));
+          }
+          if (!mbar_wait(&sh.v_full[st], st_ph, a.err, 1423)) { ok = false; break; }
+          const int key = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+          if (!masked || item.rows == 1) {
+            const uint2 keep = keep_keys(token0 + 2 * q, masked ? lim_lo : 0x7fffffff);
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
               uint32_t f[4];
               ldmatrix_x4_trans(f, vaddr + (mt >> 2) * kHalf + sw128_off(key, (mt & 3) * 2 + ((lane >> 3) & 1)));
-              float t[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_16816(t, f[0] & keep.x, f[1] & keep.x, f[2] & keep.y, f[3] & keep.y, ph[0], ph[1]);
-              mma_16816(t, f[0] & keep.x, f[1] & keep.x, f[2] & keep.y, f[3] & keep.y, pl[0], pl[1]);
+              const uint32_t v[4] = {f[0] & keep.x, f[1] & keep.x, f[2] & keep.y, f[3] & keep.y};
+              mma_16816(o[mt], v[0], v[1], v[2], v[3], ph[0], ph[1]);
+              mma_16816(o[mt], v[0], v[1], v[2], v[3], pl[0], pl[1]);
+            }
+          } else {
+            // each row of the tile on its own: values behind its end cleared, and only its own columns kept
+#pragma unroll 1
+            for (int i = 0; i < item.rows; ++i) {
+              const int end = lim_lo + i;
+              if (token0 >= end) continue;
+              const uint2 keep = keep_keys(token0 + 2 * q, end);
 #pragma unroll
-              for (int z = 0; z < 4; ++z)
-                if (lim[z & 1] == end) o[mt][z] += t[z];
+              for (int mt = 0; mt < 8; ++mt) {
+                uint32_t f[4];
+                ldmatrix_x4_trans(f, vaddr + (mt >> 2) * kHalf + sw128_off(key, (mt & 3) * 2 + ((lane >> 3) & 1)));
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_16816(t, f[0] & keep.x, f[1] & keep.x, f[2] & keep.y, f[3] & keep.y, ph[0], ph[1]);
+                mma_16816(t, f[0] & keep.x, f[1] & keep.x, f[2] & keep.y, f[3] & keep.y, pl[0], pl[1]);
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                  if (lim[z & 1] == end) o[mt][z] += t[z];
+              }
             }
           }
         }
@@ -490,7 +637,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the warps' results meet: each scales its O to the maximum of all and puts it into the last page's stage
       // ([warp][column][d], d exchanged by column against bank conflicts), and all 256 threads add up the eight
       const bool joined = a.join && item.parts > 1;
-      const int d = threadIdx.x & 127;  // one dim of every other column
+      // one dim of every other column (kBytes: the one whose sums lie at this thread's place, see below)
+      const int place = threadIdx.x & 127;
+      const int d = kBytes ? (place >> 1 & 7) * 16 + (place >> 4) * 2 + (place & 1) : place;
       auto put = [&](int col, float val, float lse) {
         const size_t at = (size_t)(item.row + (col >> a.hg_log2)) * a.Hq + item.g * a.hg + (col & (a.hg - 1));
         if (a.join && !joined) {
@@ -513,6 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (r == 0) {
             sh.m[warp][2 * q + z] = m_run[z];
             sh.l[warp][2 * q + z] = l;
+            if (kBytes) sh.w[warp][2 * q + z] = w_run[z];
           }
         }
         if (!warps_sync(&sh.meet, meet_ph, a.err, 1425)) { ok = false; break; }
@@ -523,14 +673,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int z = 0; z < 2; ++z) {
           float mm = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sh.m[w][2 * q + z]);
-          f[z] = fast_exp2(m_run[z] - (mm == -INFINITY ? 0.f : mm));
+          for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, (kBytes ? sh.w : sh.m)[w][2 * q + z]);
+          f[z] = kBytes ? fast_exp2(w_run[z] - (mm == -INFINITY ? 0.f : mm) - 15.f)
+                        : fast_exp2(m_run[z] - (mm == -INFINITY ? 0.f : mm));
         }
 #pragma unroll
-        for (int mt = 0; mt < 8; ++mt)
+        for (int mt = 0; mt < 8; ++mt) {
+          if constexpr (kBytes) {  // dims 16 r + 2 mt, + 1 at 16 mt + 2 r, + 1
 #pragma unroll
-          for (int z = 0; z < 4; ++z)
-            mine[(2 * q + (z & 1)) * 128 + ((mt * 16 + r + (z >> 1) * 8) ^ (q << 3))] = o[mt][z] * f[z & 1];
+            for (int z = 0; z < 2; ++z)
+              *reinterpret_cast<float2*>(mine + (2 * q + z) * 128 + ((mt * 16 + r * 2) ^ ((q & 1) << 4) ^ ((q >> 1) << 3))) =
+                  make_float2(o[mt][z] * f[z], o[mt][2 + z] * f[z]);
+          } else {
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              mine[(2 * q + (z & 1)) * 128 + ((mt * 16 + r + (z >> 1) * 8) ^ (q << 3))] = o[mt][z] * f[z & 1];
+          }
+        }
         {
           // this warp's column's sum: lane w % 8 has warp w's
           const float m = sh.m[lane & 7][warp];
@@ -540,8 +699,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           float den = fast_exp2(m - (mm == -INFINITY ? 0.f : mm)) * sh.l[lane & 7][warp];
 #pragma unroll
           for (int x = 1; x < 8; x <<= 1) den += __shfl_xor_sync(0xffffffffu, den, x);
+          float pow2 = 1.f;  // (kBytes) what the columns' O is relative to, over their maximum
+          if constexpr (kBytes) {
+            float w = sh.w[lane & 7][warp];
+#pragma unroll
+            for (int x = 1; x < 8; x <<= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, x));
+            pow2 = w == -INFINITY ? 1.f : fast_exp2(w - mm);
+          }
           if (lane == 0) {  // nothing but NaN scores: a maximum of -infinity and a sum of NaN, which stays
-            sh.inv[warp] = den == 0.f ? 0.f : __fdividef(1.f, den);
+            sh.inv[warp] = den == 0.f ? 0.f : __fdividef(pow2, den);
             sh.lse[warp] = den == 0.f ? -INFINITY : mm + __log2f(den);
           }
         }
@@ -552,7 +718,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (col >= cols) break;
           float val = 0.f;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) val += s_o[(w * kCols + col) * 128 + (d ^ ((col & 6) << 2))];
+          for (int w = 0; w < kWarps; ++w)
+            val += s_o[(w * kCols + col) * 128 + (place ^ (kBytes ? (col & 2) << 3 | (col & 4) << 1 : (col & 6) << 2))];
           put(col, val * sh.inv[col], sh.lse[col]);
         }
         fence_proxy_async_smem();  // the stage goes back to TMA
@@ -660,17 +827,18 @@ __global__ void __launch_bounds__(kMergeThreads, 6) paged_merge_kernel(MergeArgs
   if (lane == 0) a.LSE[item] = (m + log2f(den)) * 0.6931471805599453f;
 }
 
+template <bool kBytes>
 cudaError_t launch_attn(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
   static bool attr[kMaxDevices] = {};
   const int dslot = device_slot();
   if (!attr[dslot]) {
-    cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSmem);
+    cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<kBytes>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSmem<kBytes>);
     if (e != cudaSuccess) return e;
     attr[dslot] = true;
   }
   count_launches(1);
-  return launch_dependent(paged_attn_kernel, std::min(a.items, num_sms()), kThreads, kSmem, st, a, mk, mv);
+  return launch_dependent(paged_attn_kernel<kBytes>, std::min(a.items, num_sms()), kThreads, kSmem<kBytes>, st, a, mk, mv);
 }
 
 }  // namespace
@@ -683,6 +851,8 @@ cudaError_t launch_paged_attn(const PagedProb& p, const PagedCachePtrs& c, const
   a.lead = L.tile_rows > 1 ? reinterpret_cast<const int4*>(ws + L.lead) : nullptr;
   a.header = reinterpret_cast<int*>(ws);
   a.Q = static_cast<const __nv_bfloat16*>(Q);
+  a.K_exp = c.K_exp;
+  a.V_exp = c.V_exp;
   a.page_table = c.page_table;
   a.block_idx = block_idx;
   a.part_o = reinterpret_cast<float*>(ws + L.part_o);
@@ -711,7 +881,7 @@ cudaError_t launch_paged_attn(const PagedProb& p, const PagedCachePtrs& c, const
   a.n_flags = a.beside ? 0 : L.n_flags;
   a.err = reinterpret_cast<int*>(ws);
   a.idle_ns = kIdleNs + kIdlePageNs * L.per_split * (a.items / std::min(a.items, num_sms()) + 1);
-  return launch_attn(a, maps.k, maps.v, st);
+  return c.bytes() ? launch_attn<true>(a, maps.k, maps.v, st) : launch_attn<false>(a, maps.k, maps.v, st);
 }
 
 cudaError_t launch_paged_merge(const PagedProb& p, void* O, float* LSE, uint8_t* ws, const PagedWs& L,

@@ -24,28 +24,44 @@
 // cut off at fp32's step at the size of the largest of them, which |q|_1 max|k|
 // bounds (measured: one large product among 63 small ones loses 2^-19.3 of it,
 // normally distributed values 2^-24.5).
+//
+// A cache in 8 bits (kBytes, paged_fp8.cuh): the same selection over the values
+// that the codes stand for. A page is half as long, so twice as many are in
+// flight; codes become fp16 pairs in one conversion each, the queries fp16 with a
+// power of two for each (off by 2^-39 of their largest magnitude, 2^-33 of |q|_1
+// in a score), and a key's power of two multiplies its fp32 sum, exactly. max|k_c|
+// is taken from the powers of two (at most twice the true one). Scores that are
+// looked at again use the codes' values as bf16, which they are exactly.
 #include "mma_sync.cuh"
+#include "paged_fp8.cuh"
 #include "paged_rows.cuh"
 
 namespace msa {
 namespace {
 
-constexpr float kErr = 68.f / 8388608.f;
+template <bool kBytes>
+constexpr float kErr = (kBytes ? 69.f : 68.f) / 8388608.f;
 constexpr float kTiny = 1e-35f;               // products below the normal range may count as zero
 constexpr int kScoreWarps = 12;
 constexpr int kScoreThreads = (kScoreWarps + 1) * 32;  // the last warp loads
-constexpr int kScoreStages = 12;
+template <bool kBytes>
+constexpr int kScoreStages = kBytes ? 24 : 12;
 // page n lies in stage n % stages and is warp n % warps's: a stage is always the same warp's, so that nobody waits for a
 // stage's next page before the one in it has been taken (a barrier's parity tells only two pages apart)
-static_assert(kScoreStages % kScoreWarps == 0, "a stage belongs to one warp");
-constexpr int kScorePage = 16384;
+static_assert(kScoreStages<false> % kScoreWarps == 0 && kScoreStages<true> % kScoreWarps == 0, "a stage belongs to one warp");
+template <bool kBytes>
+constexpr int kScorePage = kBytes ? 8192 : 16384;
 constexpr int kScoreQ = 8 * 128;  // the first eight columns' queries, which come with each page
-constexpr int kScoreSmem = kScoreStages * (kScorePage + kScoreQ) + 1024;
+template <bool kBytes>
+constexpr int kScoreExp = kBytes ? 128 : 0;  // and the keys' powers of two
+template <bool kBytes>
+constexpr int kScoreSmem = kScoreStages<kBytes> * (kScorePage<kBytes> + kScoreQ + kScoreExp<kBytes>) + 1024;
 constexpr int kScoreRun = 6;    // pages of a work item
 constexpr int kScoreBatch = 5;  // items whose description is fetched at once (a lane per page)
 
 struct ScoreArgs {
   const __nv_bfloat16* q_idx;
+  const uint8_t* k_exp;  // (kBytes)
   const int32_t *page_table, *row_start, *seq_len;
   float2* pooled;
   int S, N, G, num_pages, max_blocks, runs, items;
@@ -55,13 +71,15 @@ struct ScoreArgs {
 };
 
 
+template <int kStages>
 struct ScoreShared {
-  uint64_t full[kScoreStages], empty[kScoreStages];
-  int4 info[kScoreStages];  // sequence (-1: the end), block (its complement where the page may not be read), first row, columns
+  uint64_t full[kStages], empty[kStages];
+  int4 info[kStages];  // sequence (-1: the end), block (its complement where the page may not be read), first row, columns
   int flag;
 };
 
 // The last block lines up the rows for the kernels after this one.
+template <bool kBytes>
 __global__ void __launch_bounds__(kScoreThreads, 1)
     paged_scores_kernel(ScoreArgs a, const __grid_constant__ CUtensorMap map_k) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -72,12 +90,14 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     line_up_rows(a.rows, *reinterpret_cast<RowsShared*>(smem), threadIdx.x, kScoreThreads, [] { __syncthreads(); });
     return;
   }
-  __shared__ ScoreShared sh;
-  uint8_t* s_q = smem + kScoreStages * kScorePage;  // [stage][8][128]
+  constexpr int kStages = kScoreStages<kBytes>, kPage = kScorePage<kBytes>;
+  __shared__ ScoreShared<kStages> sh;
+  uint8_t* s_q = smem + kStages * kPage;      // [stage][8][128]
+  uint8_t* s_exp = s_q + kStages * kScoreQ;   // [stage][128] (kBytes)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int ctas = gridDim.x - 1;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kScoreStages; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
     }
@@ -122,22 +142,23 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       if (bad) dev_fail(&sh.flag, kDevBadIndex, 1301);
       const int page = bad ? 0 : now.page, cols = rows * a.G;
       for (unsigned m = __ballot_sync(0xffffffffu, want); m; m &= m - 1, ++n) {
-        const int from = __ffs(m) - 1, st = n % kScoreStages;
-        if (!mbar_wait(&sh.empty[st], ((n / kScoreStages) & 1) ^ 1, &sh.flag, 1302, a.wait_ns)) { ok = false; break; }
+        const int from = __ffs(m) - 1, st = n % kStages;
+        if (!mbar_wait(&sh.empty[st], ((n / kStages) & 1) ^ 1, &sh.flag, 1302, a.wait_ns)) { ok = false; break; }
         if (lane == from) {
           sh.info[st] = make_int4(now.s, bad ? ~now.c : now.c, now.begin, cols);
           const int first = min(cols, 8);
-          mbar_arrive_expect_tx(&sh.full[st], kScorePage + first * 128);
-          tma_load_2d(smem + st * kScorePage, &map_k, &sh.full[st], 0, page * 128);
+          mbar_arrive_expect_tx(&sh.full[st], kPage + kScoreExp<kBytes> + first * 128);
+          tma_load_2d(smem + st * kPage, &map_k, &sh.full[st], 0, page * 128);
           // (one copy: eight of 128 bytes that avoid bank conflicts took longer to issue than the page to arrive)
           bulk_load(s_q + st * kScoreQ, a.q_idx + (size_t)now.begin * a.G * 64, first * 128, &sh.full[st]);
+          if (kBytes) bulk_load(s_exp + st * 128, a.k_exp + (size_t)page * 128, 128, &sh.full[st]);
         }
         __syncwarp();
       }
     }
     for (int i = 0; i < kScoreWarps && ok; ++i, ++n) {  // the end, for every warp
-      const int st = n % kScoreStages;
-      ok = mbar_wait(&sh.empty[st], ((n / kScoreStages) & 1) ^ 1, &sh.flag, 1302, a.wait_ns);
+      const int st = n % kStages;
+      ok = mbar_wait(&sh.empty[st], ((n / kStages) & 1) ^ 1, &sh.flag, 1302, a.wait_ns);
       if (ok && lane == 0) {
         sh.info[st].x = -1;
         mbar_arrive(&sh.full[st]);
@@ -147,48 +168,100 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     // ---------------------------------------------------------------- one page per warp
     const int r = lane >> 2, q = lane & 3;
     for (int n = warp;; n += kScoreWarps) {
-      const int st = n % kScoreStages;
-      if (!mbar_wait(&sh.full[st], (n / kScoreStages) & 1, &sh.flag, 1303, a.wait_ns)) break;
+      const int st = n % kStages;
+      if (!mbar_wait(&sh.full[st], (n / kStages) & 1, &sh.flag, 1303, a.wait_ns)) break;
       const int4 info = sh.info[st];
       if (info.x < 0) break;
       const bool bad = info.y < 0;
       const int c = bad ? ~info.y : info.y, cols = info.w;
-      const uint32_t base = smem_u32(smem + st * kScorePage);
+      const uint32_t base = smem_u32(smem + st * kPage);
       const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q_idx + (size_t)info.z * a.G * 64);
       uint32_t top = 0;  // largest magnitude, two bf16 at a time (after the first columns: of all)
+      float pow2[16];    // (kBytes) of the keys 8 i + r
+      if constexpr (kBytes) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t byte = s_exp[st * 128 + i * 8 + r];
+          most = max(most, byte);
+          pow2[i] = exp_value(byte);
+        }
+        // a bound on the magnitudes (0 below where all codes are 0); where products may not fit fp32 in between, infinity:
+        // such a block is undecided
+        most = __reduce_max_sync(0xffffffffu, most);
+        top = most > 207 ? 0x7f800000u : __float_as_uint(448.f * exp_value(most));
+      }
       for (int n0 = 0; n0 < cols; n0 += 8) {
-        uint32_t b[4][2];  // queries' column n0 + r, dims 16 ks + 2 q, + 1 and + 8, + 9
+        // queries' column n0 + r, dims 16 ks + 2 q, + 1 and + 8, + 9 (kBytes: + 4 q, + 1 and + 2, + 3, as the codes lie)
+        uint32_t b[4][2];
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int at = ks * 8 + h * 4 + q;
+            const int at = kBytes ? ks * 8 + q * 2 + h : ks * 8 + h * 4 + q;
             b[ks][h] = n0 + r >= cols ? 0u
                        : n0           ? ld_in(qp + (size_t)(n0 + r) * 32 + at)
                                       : *reinterpret_cast<const uint32_t*>(s_q + st * kScoreQ + r * 128 + at * 4);
           }
         float best0 = -INFINITY, best1 = -INFINITY;
+        if constexpr (kBytes) {
+          float most = 0.f;
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int ks = 0; ks < 4; ++ks) most = finite_max2(finite_max2(most, b[ks][0]), b[ks][1]);
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            uint32_t f[4];
-            ldmatrix_x4(f, base + sw128_off(m * 16 + (lane & 15), ks * 2 + (lane >> 4)));
-            mma_16816(d, f[0], f[1], f[2], f[3], b[ks][0], b[ks][1]);
-            if (n0 == 0)
-              top = __vmaxu2(top, __vmaxu2(__vmaxu2(f[0] & 0x7fff7fffu, f[1] & 0x7fff7fffu),
-                                           __vmaxu2(f[2] & 0x7fff7fffu, f[3] & 0x7fff7fffu)));
+          for (int o = 1; o < 4; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+          const uint32_t scale = query_scale_byte(most);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) b[ks][h] = f16_of_bf16(b[ks][h], exp_value(scale));
+          uint32_t any = 0;
+          bool nan = false;
+#pragma unroll
+          for (int m = 0; m < 8; ++m) {
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 4; c += 2) {
+              uint32_t f[4];  // keys r, r + 8 of piece c, then of c + 1: codes 4 q .. 4 q + 3
+              const int key = m * 16 + (lane & 15);
+              ldmatrix_x4(f, base + key * 64 + (((c + (lane >> 4)) ^ ((key >> 1) & 3)) << 4));
+              mma_16816_f16(d, f16_lo(f[0]), f16_lo(f[1]), f16_hi(f[0]), f16_hi(f[1]), b[c][0], b[c][1]);
+              mma_16816_f16(d, f16_lo(f[2]), f16_lo(f[3]), f16_hi(f[2]), f16_hi(f[3]), b[c + 1][0], b[c + 1][1]);
+              if (n0 == 0) any |= f[0] | f[1] | f[2] | f[3];
+            }
+            nan |= d[0] != d[0] || d[1] != d[1] || d[2] != d[2] || d[3] != d[3];
+            best0 = fmaxf(best0, fmaxf(d[0] * pow2[2 * m], d[2] * pow2[2 * m + 1]));
+            best1 = fmaxf(best1, fmaxf(d[1] * pow2[2 * m], d[3] * pow2[2 * m + 1]));
           }
-          best0 = fmaxf(best0, fmaxf(d[0], d[2]));  // a NaN score counts as -infinity (fmaxf leaves it out)
-          best1 = fmaxf(best1, fmaxf(d[1], d[3]));
+          if (n0 == 0 && !__any_sync(0xffffffffu, any & 0x7f7f7f7fu)) top = 0;
+          if (n0 == 0 && __any_sync(0xffffffffu, nan)) top = 0x7f800000u;  // (a NaN score is looked at again)
+          // the columns' scales back out (column c's is with the lanes of r = c)
+          const uint32_t back = 254 - scale;
+          best0 *= exp_value(__shfl_sync(0xffffffffu, back, q * 8));
+          best1 *= exp_value(__shfl_sync(0xffffffffu, back, q * 8 + 4));
+        } else {
+#pragma unroll
+          for (int m = 0; m < 8; ++m) {
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+              uint32_t f[4];
+              ldmatrix_x4(f, base + sw128_off(m * 16 + (lane & 15), ks * 2 + (lane >> 4)));
+              mma_16816(d, f[0], f[1], f[2], f[3], b[ks][0], b[ks][1]);
+              if (n0 == 0)
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(f[0] & 0x7fff7fffu, f[1] & 0x7fff7fffu),
+                                             __vmaxu2(f[2] & 0x7fff7fffu, f[3] & 0x7fff7fffu)));
+            }
+            best0 = fmaxf(best0, fmaxf(d[0], d[2]));  // a NaN score counts as -infinity (fmaxf leaves it out)
+            best1 = fmaxf(best1, fmaxf(d[1], d[3]));
+          }
         }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
           best0 = fmaxf(best0, __shfl_xor_sync(0xffffffffu, best0, o));
           best1 = fmaxf(best1, __shfl_xor_sync(0xffffffffu, best1, o));
         }
-        if (n0 == 0) top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16)) << 16;
+        if (!kBytes && n0 == 0) top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16)) << 16;
         if (r == 0) {
           const size_t col = (size_t)info.z * a.G + n0 + 2 * q;
           if (n0 + 2 * q < cols) a.pooled[col * a.max_blocks + c] = make_float2(bad ? -INFINITY : best0, __uint_as_float(top));
@@ -208,7 +281,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
 struct SelectArgs {
   const int4* rows;
   const float2* pooled;
-  const __nv_bfloat16 *q_idx, *k_idx;
+  const __nv_bfloat16* q_idx;
+  const void* k_idx;
+  const uint8_t* k_exp;  // (kBytes)
   const int32_t* page_table;
   int32_t* block_idx;
   int G, k, num_pages, max_blocks;
@@ -232,6 +307,31 @@ __device__ __forceinline__ float from_key(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
+// The index keys of a page: eight values, or two, of a key as bf16 (the codes' values are exact in it).
+template <bool kBytes>
+struct PageKeys;
+template <>
+struct PageKeys<false> {
+  const __nv_bfloat16* page;
+  __device__ __forceinline__ PageKeys(const SelectArgs& a, int at) : page(static_cast<const __nv_bfloat16*>(a.k_idx) + (size_t)at * 128 * 64) {}
+  __device__ __forceinline__ uint4 eight(int key, int c) const { return ld_in(reinterpret_cast<const uint4*>(page + key * 64) + c); }
+  __device__ __forceinline__ uint32_t two(int key, int i) const {
+    return ld_in(reinterpret_cast<const uint32_t*>(page + key * 64) + i);
+  }
+};
+template <>
+struct PageKeys<true> {
+  const uint8_t *page, *exps;
+  __device__ __forceinline__ PageKeys(const SelectArgs& a, int at)
+      : page(static_cast<const uint8_t*>(a.k_idx) + (size_t)at * 128 * 64), exps(a.k_exp + (size_t)at * 128) {}
+  __device__ __forceinline__ uint4 eight(int key, int c) const {
+    return eight_bf16(__ldcg(reinterpret_cast<const uint2*>(page + key * 64) + c), exp_value(__ldcg(exps + key)));
+  }
+  __device__ __forceinline__ uint32_t two(int key, int i) const {
+    return scaled_bf16(f16_lo(__ldcg(reinterpret_cast<const unsigned short*>(page + key * 64) + i)), exp_value(__ldcg(exps + key)));
+  }
+};
+
 // Products of a query and a block's keys (exact in fp32) as integers, in units of 2^-57 of `most`, the largest that they
 // could have, so that 64 of them stay below 2^63. `cut` says that one is not a whole number of units.
 struct Units {
@@ -250,7 +350,8 @@ struct Units {
 };
 
 // The largest of a block's scores for a query (64 bf16 at q), by one warp, a key per lane. NaN where a product is cut.
-__device__ __noinline__ double integer_max(const __nv_bfloat16* page, const __nv_bfloat16* q, float most, int lane) {
+template <class Keys>
+__device__ __noinline__ double integer_max(Keys keys, const __nv_bfloat16* q, float most, int lane) {
   const Units units(most);
   long long top = -0x7fffffffffffffffll;
   bool cut = false;
@@ -260,7 +361,7 @@ __device__ __noinline__ double integer_max(const __nv_bfloat16* page, const __nv
 #pragma unroll 1
     for (int c = 0; c < 8; ++c) {
       const uint4 w = ld_in(reinterpret_cast<const uint4*>(q) + c);
-      const uint4 k = ld_in(reinterpret_cast<const uint4*>(page + key * 64) + c);
+      const uint4 k = keys.eight(key, c);
       const uint32_t wv[4] = {w.x, w.y, w.z, w.w}, kv[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
       for (int z = 0; z < 4; ++z) sum += units.of(lo_f(wv[z]), lo_f(kv[z]), cut) + units.of(hi_f(wv[z]), hi_f(kv[z]), cut);
@@ -280,13 +381,14 @@ __device__ __forceinline__ void add_exactly(double& s, double& e, double t, doub
 }
 
 // The largest score among the keys of `near` (of lane i: the keys 32 i + bit), by one warp, two dims per lane.
-__device__ __noinline__ double double_max(const __nv_bfloat16* page, uint32_t qq, unsigned near, int lane) {
+template <class Keys>
+__device__ __noinline__ double double_max(Keys keys, uint32_t qq, unsigned near, int lane) {
   double top = -INFINITY;
 #pragma unroll 1
   for (int i = 0; i < 4; ++i)
 #pragma unroll 1
     for (unsigned m = __shfl_sync(0xffffffffu, near, i); m; m &= m - 1) {
-      const uint32_t kk = ld_in(reinterpret_cast<const uint32_t*>(page + (__ffs(m) - 1 + 32 * i) * 64) + lane);
+      const uint32_t kk = keys.two(__ffs(m) - 1 + 32 * i, lane);
       double t = (double)lo_f(qq) * (double)lo_f(kk), e = 0.;
       add_exactly(t, e, (double)hi_f(qq) * (double)hi_f(kk), 0.);
 #pragma unroll
@@ -308,8 +410,8 @@ __device__ __noinline__ double double_max(const __nv_bfloat16* page, uint32_t qq
 // lie too far apart for that, or are not finite, of doubles with what their
 // additions lose. A score is the same number in whichever way: one that was
 // rounded in between could part equal keys.
-__device__ __noinline__ double exact_max(const __nv_bfloat16* page, const __nv_bfloat16* q, float margin, float qmax,
-                                         float kmax, int lane) {
+template <class Keys>
+__device__ __noinline__ double exact_max(Keys keys, const __nv_bfloat16* q, float margin, float qmax, float kmax, int lane) {
   float s32[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -317,8 +419,7 @@ __device__ __noinline__ double exact_max(const __nv_bfloat16* page, const __nv_b
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        k[i][c] = ld_in(reinterpret_cast<const uint4*>(page + (lane + 32 * i) * 64 + 32 * h) + c);
+      for (int c = 0; c < 4; ++c) k[i][c] = keys.eight(lane + 32 * i, 4 * h + c);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const uint4 w = ld_in(reinterpret_cast<const uint4*>(q + 32 * h) + c);
@@ -347,7 +448,7 @@ __device__ __noinline__ double exact_max(const __nv_bfloat16* page, const __nv_b
   double t = NAN;
   if (most >= 0x1p-60f && most <= 0x1p90f) {
     if (many > 8) {
-      t = integer_max(page, q, most, lane);
+      t = integer_max(keys, q, most, lane);
     } else {
       const Units units(most);
       long long top = -0x7fffffffffffffffll;
@@ -356,7 +457,7 @@ __device__ __noinline__ double exact_max(const __nv_bfloat16* page, const __nv_b
       for (int i = 0; i < 4; ++i)
 #pragma unroll 1
         for (unsigned m = __shfl_sync(0xffffffffu, near, i); m; m &= m - 1) {
-          const uint32_t kk = ld_in(reinterpret_cast<const uint32_t*>(page + (__ffs(m) - 1 + 32 * i) * 64) + lane);
+          const uint32_t kk = keys.two(__ffs(m) - 1 + 32 * i, lane);
           long long sum = units.of(lo_f(qq), lo_f(kk), cut) + units.of(hi_f(qq), hi_f(kk), cut);
 #pragma unroll
           for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -365,13 +466,13 @@ __device__ __noinline__ double exact_max(const __nv_bfloat16* page, const __nv_b
       if (!__any_sync(0xffffffffu, cut)) t = (double)top * units.unit;
     }
   }
-  return t == t ? t : double_max(page, qq, near, lane);
+  return t == t ? t : double_max(keys, qq, near, lane);
 }
 
 // One block per (row, group). A thread keeps its blocks' lower bounds (as
 // ordered keys) and errors in registers; shared memory has room for the list of
 // undecided blocks and their scores.
-template <int kThreads, int kSelItems>
+template <int kThreads, int kSelItems, bool kBytes>
 __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
   pdl_release();
   pdl_wait();
@@ -411,7 +512,7 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
   float l1 = fabsf(lo_f(qq)) + fabsf(hi_f(qq));  // |q|_1
 #pragma unroll
   for (int o = 16; o; o >>= 1) l1 += __shfl_xor_sync(0xffffffffu, l1, o);
-  const float err_q = l1 * kErr;
+  const float err_q = l1 * kErr<kBytes>;
 
   uint32_t key[kSelItems], kmax = 0, kmin = 0xffffffffu;
   float emax = 0.f;
@@ -529,7 +630,7 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
       double t = -INFINITY;
       if (page < 0 || page >= a.num_pages) t = -INFINITY;  // (reported)
       else if ((qmax == 0.f || top == 0.f) && qmax < INFINITY && top < INFINITY) t = 0.;  // nothing but zeros
-      else t = exact_max(a.k_idx + (size_t)page * 128 * 64, q, margin, qmax, top, lane);
+      else t = exact_max(PageKeys<kBytes>(a, page), q, margin, qmax, top, lane);
       if (lane == 0) score[i] = t;
     }
     __syncthreads();
@@ -562,18 +663,18 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
 // As few threads as hold every block with eight each, fewer warps to wait for: 1,200 rows and groups of 40 blocks take
 // 199 us in all with 128 threads, 211 with 256. (One warp, or half the threads with twice the blocks, is slower: a row
 // over 8,192 blocks 72 us with 1,024 threads, 83 with 512, 89 with 256.)
-template <int kThreads, int kSelItems>
+template <int kThreads, int kSelItems, bool kBytes>
 cudaError_t launch_select(const PagedProb& p, const SelectArgs& a, cudaStream_t st) {
   static bool attr[kMaxDevices] = {};
   const int dslot = device_slot();
   if (!attr[dslot]) {
-    cudaError_t e = cudaFuncSetAttribute(paged_select_kernel<kThreads, kSelItems>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(paged_select_kernel<kThreads, kSelItems, kBytes>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (kThreads * kSelItems + 1) * 12);
     if (e != cudaSuccess) return e;
     attr[dslot] = true;
   }
   count_launches(1);
-  return launch_dependent(paged_select_kernel<kThreads, kSelItems>, p.N * p.G, kThreads, p.max_blocks * 12, st, a);
+  return launch_dependent(paged_select_kernel<kThreads, kSelItems, kBytes>, p.N * p.G, kThreads, p.max_blocks * 12, st, a);
 }
 
 // The rows alone, where no index scores are wanted and no prefix is shared.
@@ -594,10 +695,12 @@ cudaError_t launch_paged_rows(const PagedProb& p, const PagedCachePtrs& c, uint8
   return launch_dependent(paged_rows_kernel, 1, p.N <= 256 ? 256 : kRowThreads, 0, st, rows_args(p, c, ws, L));
 }
 
-cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, const void* q_idx, int32_t* block_idx,
-                               uint8_t* ws, const PagedWs& L, cudaStream_t st) {
+template <bool kBytes>
+static cudaError_t launch_index(const PagedProb& p, const PagedCachePtrs& c, const void* q_idx, int32_t* block_idx,
+                                uint8_t* ws, const PagedWs& L, cudaStream_t st) {
   ScoreArgs a;
   a.q_idx = static_cast<const __nv_bfloat16*>(q_idx);
+  a.k_exp = c.k_idx_exp;
   a.page_table = c.page_table;
   a.row_start = c.row_start;
   a.seq_len = c.seq_len;
@@ -613,21 +716,23 @@ cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, cons
   if (L.n_flags > 0) {
     CUtensorMap mk;
     const uint64_t dims[2] = {64, (uint64_t)p.num_pages * 128};
-    const uint64_t strides[1] = {128};
+    const uint64_t strides[1] = {kBytes ? 64 : 128};
     const uint32_t box[2] = {64, 128};
-    if (!encode_tmap(&mk, c.k_idx, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+    if (!encode_tmap(&mk, c.k_idx, 2, dims, strides, box, kBytes ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                     kBytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16))
+      return cudaErrorInvalidValue;
     a.runs = (p.max_blocks - 1 + kScoreRun - 1) / kScoreRun;
     a.items = p.S * a.runs;
     static bool attr[kMaxDevices] = {};
     const int dslot = device_slot();
     cudaError_t e;
     if (!attr[dslot]) {
-      e = cudaFuncSetAttribute(paged_scores_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
+      e = cudaFuncSetAttribute(paged_scores_kernel<kBytes>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem<kBytes>);
       if (e != cudaSuccess) return e;
       attr[dslot] = true;
     }
     count_launches(1);
-    e = launch_dependent(paged_scores_kernel, L.n_flags + 1, kScoreThreads, kScoreSmem, st, a, mk);
+    e = launch_dependent(paged_scores_kernel<kBytes>, L.n_flags + 1, kScoreThreads, kScoreSmem<kBytes>, st, a, mk);
     if (e != cudaSuccess) return e;
   } else {
     const cudaError_t e = launch_paged_rows(p, c, ws, L, st);
@@ -637,7 +742,8 @@ cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, cons
   b.rows = reinterpret_cast<const int4*>(ws + L.rows);
   b.pooled = a.pooled;
   b.q_idx = a.q_idx;
-  b.k_idx = static_cast<const __nv_bfloat16*>(c.k_idx);
+  b.k_idx = c.k_idx;
+  b.k_exp = c.k_idx_exp;
   b.page_table = c.page_table;
   b.block_idx = block_idx;
   b.G = p.G;
@@ -645,8 +751,13 @@ cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, cons
   b.num_pages = p.num_pages;
   b.max_blocks = p.max_blocks;
   const int n = p.max_blocks - 1;
-  if (n <= 256) return launch_select<128, 2>(p, b, st);
-  return n <= 2048 ? launch_select<256, 8>(p, b, st) : launch_select<1024, 8>(p, b, st);
+  if (n <= 256) return launch_select<128, 2, kBytes>(p, b, st);
+  return n <= 2048 ? launch_select<256, 8, kBytes>(p, b, st) : launch_select<1024, 8, kBytes>(p, b, st);
+}
+
+cudaError_t launch_paged_index(const PagedProb& p, const PagedCachePtrs& c, const void* q_idx, int32_t* block_idx,
+                               uint8_t* ws, const PagedWs& L, cudaStream_t st) {
+  return c.bytes() ? launch_index<true>(p, c, q_idx, block_idx, ws, L, st) : launch_index<false>(p, c, q_idx, block_idx, ws, L, st);
 }
 
 }  // namespace msa

@@ -4,12 +4,14 @@ A ``PagedShape`` names the sizes, a ``PagedCache`` holds the pools and the
 batch description, a ``Rope`` the rotation; each keeps its C struct, so that a
 decode step marshals only what changes. The calls are those of ``include/msa.h``:
 
-* ``msa_paged_append(shape, cache, rope, K, V, k_idx, Q, q_idx, Q_out, q_idx_out, workspace, stream=None)``
+* ``msa_paged_append(shape, cache, rope, K, V, k_idx, Q, q_idx, Q_out, q_idx_out, workspace, stream=None, positions=None)``
 * ``msa_paged_sparse_attn(shape, cache, Q, q_idx, block_idx, O, LSE, workspace, stream=None)``
 * ``msa_paged_dense_attn(shape, cache, Q, O, LSE, workspace, stream=None)``
 
 and ``paged_append``, ``paged_sparse_attn``, ``paged_dense_attn`` allocate the
-outputs. Tensors live on one GPU; a call runs on that GPU, on its current
+outputs. The same calls with ``_fp8`` at their end take a ``PagedCacheFp8``, which
+holds E4M3 codes and powers of two, and ``msa_paged_read_fp8`` (``paged_read_fp8``)
+gives its tokens back as bf16. Tensors live on one GPU; a call runs on that GPU, on its current
 stream unless ``stream`` is given.
 """
 from __future__ import annotations
@@ -19,8 +21,8 @@ import struct
 from ctypes import addressof
 from dataclasses import dataclass
 
-from . import (MSA_ERR_UNSUPPORTED, MSA_WS_PAGED_APPEND, MSA_WS_PAGED_DENSE, MSA_WS_PAGED_SPARSE, MsaError, _check, _on_stream,
-               load_library)
+from . import (MSA_ERR_UNSUPPORTED, MSA_WS_PAGED_APPEND, MSA_WS_PAGED_DENSE, MSA_WS_PAGED_DENSE_FP8, MSA_WS_PAGED_SPARSE,
+               MSA_WS_PAGED_SPARSE_FP8, MsaError, _check, _on_stream, load_library)
 
 
 class MsaPagedShape(ctypes.Structure):
@@ -30,6 +32,16 @@ class MsaPagedShape(ctypes.Structure):
 
 class MsaPagedCache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("K", "V", "k_idx", "page_table", "row_start", "seq_len")]
+
+
+class MsaPagedCacheFp8(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("K", "V", "K_exp", "V_exp", "k_idx", "k_idx_exp", "page_table", "row_start",
+                                               "seq_len")]
+
+
+class MsaAxes(ctypes.Structure):
+    _fields_ = [("positions", ctypes.c_void_p), ("axis", ctypes.c_void_p), ("axis_idx", ctypes.c_void_p),
+                ("axes", ctypes.c_int32)]
 
 
 class MsaRope(ctypes.Structure):
@@ -78,6 +90,7 @@ class PagedShape:
 
 _torch = _bf16 = None
 _new_rows = struct.Struct("5P5q").pack  # the bytes of a MsaNewRows (in a sixth of the time)
+_axes = struct.Struct("3Pi4x").pack     # and of a MsaAxes
 
 
 def _t():
@@ -131,7 +144,25 @@ class _Fixed:
         return type(self), self._args
 
 
-class PagedCache(_Fixed):
+class _Cache(_Fixed):
+    def check(self, shape):
+        """The cache is one of `shape`."""
+        if self._sizes != shape._sizes:
+            raise ValueError(f"the cache has (S, G, num_pages, max_blocks, d, Bk) = {self._sizes}, the shape {shape._sizes}")
+        if self._index_dim is not None and self._index_dim != shape.d_idx:
+            raise ValueError(f"the cache's index keys have {self._index_dim} dims, the shape {shape.d_idx}")
+
+    def _hold(self, args, struct, **tensors):
+        K, table = tensors["K"], tensors["page_table"]
+        pages, G, Bk, d = K.shape
+        k_idx = tensors["k_idx"]
+        self.__dict__.update(
+            tensors, device=K.device, _args=args, _struct=struct, _addr=addressof(struct), _device=K.get_device(),
+            _sizes=(tensors["seq_len"].shape[0], G, pages, table.shape[-1], d, Bk),
+            _index_dim=None if k_idx is None else k_idx.shape[-1])
+
+
+class PagedCache(_Cache):
     """Pools K, V [num_pages, G, 128, 128] and k_idx [num_pages, 128, 64] (or None) in bf16, and the batch description
     page_table [S, max_blocks], row_start [S + 1], seq_len [S] in int32. The tensors are kept as they are: their
     contents may change between calls, neither they nor their storage may be replaced."""
@@ -151,42 +182,66 @@ class PagedCache(_Fixed):
             None if k_idx is None else _want("k_idx", k_idx, bf, (pages, Bk, k_idx.shape[-1]), dev),
             _want("page_table", page_table, i32, (S, page_table.shape[-1]), dev),
             _want("row_start", row_start, i32, (S + 1,), dev), _want("seq_len", seq_len, i32, (S,), dev))
-        self.__dict__.update(
-            K=K, V=V, k_idx=k_idx, page_table=page_table, row_start=row_start, seq_len=seq_len, device=K.device,
-            _args=(K, V, k_idx, page_table, row_start, seq_len), _struct=struct, _addr=addressof(struct), _device=dev,
-            _sizes=(S, G, pages, page_table.shape[-1], d, Bk), _index_dim=None if k_idx is None else k_idx.shape[-1])
+        self._hold((K, V, k_idx, page_table, row_start, seq_len), struct, K=K, V=V, k_idx=k_idx, page_table=page_table,
+                   row_start=row_start, seq_len=seq_len)
 
-    def check(self, shape):
-        """The cache is one of `shape`."""
-        if self._sizes != shape._sizes:
-            raise ValueError(f"the cache has (S, G, num_pages, max_blocks, d, Bk) = {self._sizes}, the shape {shape._sizes}")
-        if self._index_dim is not None and self._index_dim != shape.d_idx:
-            raise ValueError(f"the cache's index keys have {self._index_dim} dims, the shape {shape.d_idx}")
+
+class PagedCacheFp8(_Cache):
+    """A cache in 8 bits: pools K, V [num_pages, G, 128, 128] and k_idx [num_pages, 128, 64] (or None) in
+    torch.float8_e4m3fn, and the exponents + 127 of their vectors' powers of two, K_exp, V_exp [num_pages, G, 128] and
+    k_idx_exp [num_pages, 128] in uint8; the batch description as a PagedCache's. The tensors are kept as they are."""
+
+    _held = ("K", "V", "K_exp", "V_exp", "k_idx", "k_idx_exp", "page_table", "row_start", "seq_len", "device")
+
+    def __init__(self, K, V, K_exp, V_exp, k_idx, k_idx_exp, page_table, row_start, seq_len):
+        torch = _t()
+        if not K.is_cuda:
+            raise ValueError("K must live on the GPU")
+        if (k_idx is None) != (k_idx_exp is None):
+            raise ValueError("give k_idx with k_idx_exp, or neither")
+        pages, G, Bk, d = K.shape
+        dev = K.get_device()
+        S = seq_len.shape[0]
+        f8, u8, i32 = torch.float8_e4m3fn, torch.uint8, torch.int32
+        struct = MsaPagedCacheFp8(
+            _want("K", K, f8, (pages, G, Bk, d), dev), _want("V", V, f8, (pages, G, Bk, d), dev),
+            _want("K_exp", K_exp, u8, (pages, G, Bk), dev), _want("V_exp", V_exp, u8, (pages, G, Bk), dev),
+            None if k_idx is None else _want("k_idx", k_idx, f8, (pages, Bk, k_idx.shape[-1]), dev),
+            None if k_idx is None else _want("k_idx_exp", k_idx_exp, u8, (pages, Bk), dev),
+            _want("page_table", page_table, i32, (S, page_table.shape[-1]), dev),
+            _want("row_start", row_start, i32, (S + 1,), dev), _want("seq_len", seq_len, i32, (S,), dev))
+        self._hold((K, V, K_exp, V_exp, k_idx, k_idx_exp, page_table, row_start, seq_len), struct, K=K, V=V, K_exp=K_exp,
+                   V_exp=V_exp, k_idx=k_idx, k_idx_exp=k_idx_exp, page_table=page_table, row_start=row_start,
+                   seq_len=seq_len)
 
 
 class Rope(_Fixed):
     """Rotation frequencies (radians per position, fp32): inv_freq [rot_dim / 2] for Q and K, inv_freq_idx
-    [rot_dim_idx / 2] for the index branch; None rotates nothing."""
+    [rot_dim_idx / 2] for the index branch; None rotates nothing. For positions with several axes, axis and axis_idx
+    (int32, as long) name each pair's axis; None: all on axis 0."""
 
-    _held = ("inv_freq", "inv_freq_idx")
+    _held = ("inv_freq", "inv_freq_idx", "axis", "axis_idx")
 
-    def __init__(self, inv_freq=None, inv_freq_idx=None, interleaved=False):
+    def __init__(self, inv_freq=None, inv_freq_idx=None, interleaved=False, axis=None, axis_idx=None):
         torch = _t()
 
-        def ptr(name, t):
+        def ptr(name, t, kind, length=None):
             if t is None or t.numel() == 0:
                 return None, 0
             if not t.is_cuda:
                 raise ValueError(f"{name} must live on the GPU")
-            return _want(name, t, torch.float32, (t.numel(),), t.get_device()), 2 * t.numel()
+            return _want(name, t, kind, (t.numel() if length is None else length,), t.get_device()), 2 * t.numel()
 
-        p, n = ptr("inv_freq", inv_freq)
-        pi, ni = ptr("inv_freq_idx", inv_freq_idx)
+        p, n = ptr("inv_freq", inv_freq, torch.float32)
+        pi, ni = ptr("inv_freq_idx", inv_freq_idx, torch.float32)
+        ax, _ = ptr("axis", axis, torch.int32, n // 2)
+        axi, _ = ptr("axis_idx", axis_idx, torch.int32, ni // 2)
         struct = MsaRope(p, pi, n, ni, 1 if interleaved else 0)
+        given = ((inv_freq, p), (inv_freq_idx, pi), (axis, ax), (axis_idx, axi))
         self.__dict__.update(
-            inv_freq=inv_freq, inv_freq_idx=inv_freq_idx, _args=(inv_freq, inv_freq_idx, interleaved), _struct=struct,
-            _addr=addressof(struct),
-            _devices={t.get_device() for t, q in ((inv_freq, p), (inv_freq_idx, pi)) if q is not None})
+            inv_freq=inv_freq, inv_freq_idx=inv_freq_idx, axis=axis, axis_idx=axis_idx,
+            _args=(inv_freq, inv_freq_idx, interleaved, axis, axis_idx), _struct=struct, _addr=addressof(struct),
+            _axis=ax, _axis_idx=axi, _devices={t.get_device() for t, q in given if q is not None})
 
 
 def _rows(name, t, shape, device):
@@ -239,9 +294,14 @@ def alloc_paged_workspace(shape, which: int, device="cuda"):
     return _t().empty(n, dtype=_t().uint8, device=device)
 
 
-def msa_paged_append(shape, cache, rope, K, V, k_idx, Q, q_idx, Q_out, q_idx_out, workspace, stream=None) -> None:
-    """New tokens into their pages, K and k_idx rotated; Q and q_idx rotated into Q_out and q_idx_out. Inputs may be
-    row-strided. k_idx, and Q or q_idx with its output, may be None."""
+def _is(kind, cache):
+    """The cache is of the type that the call takes."""
+    if type(cache) is not kind and not isinstance(cache, kind):
+        raise TypeError(f"a {kind.__name__} is needed, not a {type(cache).__name__}")
+
+
+def _append(kind, shape, cache, rope, K, V, k_idx, Q, q_idx, Q_out, q_idx_out, workspace, stream, positions):
+    _is(kind, cache)
     cache.check(shape)
     dev = cache._device
     if k_idx is not None and cache.k_idx is None:
@@ -254,71 +314,175 @@ def msa_paged_append(shape, cache, rope, K, V, k_idx, Q, q_idx, Q_out, q_idx_out
     qp, q_ld = none if Q is None else _rows("Q", Q, shape._q, dev)
     ip, i_ld = none if q_idx is None else _rows("q_idx", q_idx, shape._qi, dev)
     xp, x_ld = none if k_idx is None else _rows("k_idx", k_idx, shape._ki, dev)
-    _run(load_library().msa_paged_append, cache, stream, workspace, addressof(shape._c), cache._addr, rope._addr,
-         _new_rows(qp, kp, vp, ip, xp, q_ld, k_ld, v_ld, i_ld, x_ld),
-         None if Q_out is None else _want("Q_out", Q_out, _bf16, shape._q, dev),
-         None if q_idx_out is None else _want("q_idx_out", q_idx_out, _bf16, shape._qi, dev))
+    lib, axes = load_library(), None
+    if positions is not None:
+        n = positions.shape[-1] if positions.dim() == 2 else 0
+        axes = _axes(_want("positions", positions, _torch.int32, (shape.N, n), dev), rope._axis or 0, rope._axis_idx or 0, n)
+    elif rope._axis or rope._axis_idx:
+        raise ValueError("the rotation has axes: give the rows' positions on them")
+    rows = _new_rows(qp, kp, vp, ip, xp, q_ld, k_ld, v_ld, i_ld, x_ld)
+    out = (None if Q_out is None else _want("Q_out", Q_out, _bf16, shape._q, dev),
+           None if q_idx_out is None else _want("q_idx_out", q_idx_out, _bf16, shape._qi, dev))
+    if kind is PagedCacheFp8:
+        _run(lib.msa_paged_append_fp8, cache, stream, workspace, addressof(shape._c), cache._addr, rope._addr, axes, rows, *out)
+    elif axes is None:
+        _run(lib.msa_paged_append, cache, stream, workspace, addressof(shape._c), cache._addr, rope._addr, rows, *out)
+    else:
+        _run(lib.msa_paged_append_axes, cache, stream, workspace, addressof(shape._c), cache._addr, rope._addr, axes, rows, *out)
 
 
-def msa_paged_sparse_attn(shape, cache, Q, q_idx, block_idx, O, LSE, workspace, stream=None) -> None:
-    """Selection (q_idx given: block_idx is written; None: block_idx is read) and attention over the selected pages."""
+def _sparse(kind, call, shape, cache, Q, q_idx, block_idx, O, LSE, workspace, stream):
+    _is(kind, cache)
     torch, bf = _torch, _bf16
     cache.check(shape)
     dev = cache._device
     if q_idx is not None and cache.k_idx is None:
         raise ValueError("the cache has no index keys (k_idx)")
-    _run(load_library().msa_paged_sparse_attn, cache, stream, workspace, addressof(shape._c), cache._addr,
+    _run(call, cache, stream, workspace, addressof(shape._c), cache._addr,
          _want("Q", Q, bf, shape._q, dev), None if q_idx is None else _want("q_idx", q_idx, bf, shape._qi, dev),
          _want("block_idx", block_idx, torch.int32, shape._bi, dev), _want("O", O, bf, shape._q, dev),
          _want("LSE", LSE, torch.float32, shape._lse, dev))
 
 
-def msa_paged_dense_attn(shape, cache, Q, O, LSE, workspace, stream=None) -> None:
-    """Full attention for the new rows; the first shape.prefix_blocks pages are those of every sequence."""
+def _dense(kind, call, shape, cache, Q, O, LSE, workspace, stream):
+    _is(kind, cache)
     torch, bf = _torch, _bf16
     cache.check(shape)
     dev = cache._device
-    _run(load_library().msa_paged_dense_attn, cache, stream, workspace, addressof(shape._c), cache._addr,
+    _run(call, cache, stream, workspace, addressof(shape._c), cache._addr,
          _want("Q", Q, bf, shape._q, dev), _want("O", O, bf, shape._q, dev),
          _want("LSE", LSE, torch.float32, shape._lse, dev))
 
 
+def msa_paged_append(shape, cache, rope, K, V, k_idx, Q, q_idx, Q_out, q_idx_out, workspace, stream=None,
+                     positions=None) -> None:
+    """New tokens into their pages, K and k_idx rotated; Q and q_idx rotated into Q_out and q_idx_out. Inputs may be
+    row-strided. k_idx, and Q or q_idx with its output, may be None. positions [N, axes] (int32): the rows' positions on
+    the axes that the rotation's pairs turn on; None: in their sequences."""
+    _append(PagedCache, shape, cache, rope, K, V, k_idx, Q, q_idx, Q_out, q_idx_out, workspace, stream, positions)
+
+
+def msa_paged_append_fp8(shape, cache, rope, K, V, k_idx, Q, q_idx, Q_out, q_idx_out, workspace, stream=None,
+                         positions=None) -> None:
+    """msa_paged_append into a PagedCacheFp8: K, V and k_idx are quantised as they are written."""
+    _append(PagedCacheFp8, shape, cache, rope, K, V, k_idx, Q, q_idx, Q_out, q_idx_out, workspace, stream, positions)
+
+
+def msa_paged_sparse_attn(shape, cache, Q, q_idx, block_idx, O, LSE, workspace, stream=None) -> None:
+    """Selection (q_idx given: block_idx is written; None: block_idx is read) and attention over the selected pages."""
+    _sparse(PagedCache, load_library().msa_paged_sparse_attn, shape, cache, Q, q_idx, block_idx, O, LSE, workspace, stream)
+
+
+def msa_paged_sparse_attn_fp8(shape, cache, Q, q_idx, block_idx, O, LSE, workspace, stream=None) -> None:
+    """msa_paged_sparse_attn over a PagedCacheFp8."""
+    _sparse(PagedCacheFp8, load_library().msa_paged_sparse_attn_fp8, shape, cache, Q, q_idx, block_idx, O, LSE, workspace,
+            stream)
+
+
+def msa_paged_dense_attn(shape, cache, Q, O, LSE, workspace, stream=None) -> None:
+    """Full attention for the new rows; the first shape.prefix_blocks pages are those of every sequence."""
+    _dense(PagedCache, load_library().msa_paged_dense_attn, shape, cache, Q, O, LSE, workspace, stream)
+
+
+def msa_paged_dense_attn_fp8(shape, cache, Q, O, LSE, workspace, stream=None) -> None:
+    """msa_paged_dense_attn over a PagedCacheFp8."""
+    _dense(PagedCacheFp8, load_library().msa_paged_dense_attn_fp8, shape, cache, Q, O, LSE, workspace, stream)
+
+
+def msa_paged_read_fp8(shape, cache, first, out_start, K_out, V_out, k_idx_out, workspace, stream=None) -> None:
+    """Tokens of a PagedCacheFp8 as bf16: rows out_start[s] .. out_start[s + 1] - 1 of K_out, V_out [M, G, 128] and
+    k_idx_out [M, 64] (or None) are the tokens from first[s] on of sequence s (first None: from its beginning).
+    first [S] and out_start [S + 1] are int32."""
+    _is(PagedCacheFp8, cache)
+    cache.check(shape)
+    dev, i32, M = cache._device, _torch.int32, K_out.shape[0]
+    if k_idx_out is not None and cache.k_idx is None:
+        raise ValueError("the cache has no index keys (k_idx)")
+    _run(load_library().msa_paged_read_fp8, cache, stream, workspace, addressof(shape._c), cache._addr,
+         None if first is None else _want("first", first, i32, (shape.S,), dev),
+         _want("out_start", out_start, i32, (shape.S + 1,), dev), M,
+         _want("K_out", K_out, _bf16, (M, shape.G, shape.d), dev), _want("V_out", V_out, _bf16, (M, shape.G, shape.d), dev),
+         None if k_idx_out is None else _want("k_idx_out", k_idx_out, _bf16, (M, shape.d_idx), dev))
+
+
 # ----------------------------------------------------------------- allocation helpers
-def paged_append(shape, cache, rope, K, V, k_idx=None, Q=None, q_idx=None, workspace=None, stream=None):
-    """Allocate the rotated queries, run msa_paged_append and return (Q_out, q_idx_out); None where none was given."""
+def _new_append(call, shape, cache, rope, K, V, k_idx, Q, q_idx, workspace, positions):
     dev = cache.device
-    if stream is not None:
-        return _on_stream(stream, dev, paged_append, shape, cache, rope, K, V, k_idx, Q, q_idx, workspace)
     ws = workspace if workspace is not None else alloc_paged_workspace(shape, MSA_WS_PAGED_APPEND, dev)
     Q_out = None if Q is None else _torch.empty(shape._q, dtype=_bf16, device=dev)
     qi_out = None if q_idx is None else _torch.empty(shape._qi, dtype=_bf16, device=dev)
-    msa_paged_append(shape, cache, rope, K, V, k_idx, Q, q_idx, Q_out, qi_out, ws)
+    call(shape, cache, rope, K, V, k_idx, Q, q_idx, Q_out, qi_out, ws, positions=positions)
     return Q_out, qi_out
 
 
-def paged_sparse_attn(shape, cache, Q, q_idx=None, block_idx=None, workspace=None, stream=None):
-    """Allocate O, LSE (and block_idx, when q_idx selects) and run msa_paged_sparse_attn; returns (O, LSE, block_idx)."""
+def _new_sparse(call, which, shape, cache, Q, q_idx, block_idx, workspace):
     dev = cache.device
-    if stream is not None:
-        return _on_stream(stream, dev, paged_sparse_attn, shape, cache, Q, q_idx, block_idx, workspace)
     if block_idx is None:
         if q_idx is None:
             raise ValueError("give q_idx to select blocks, or the block_idx to attend to")
         block_idx = _torch.empty(shape._bi, dtype=_torch.int32, device=dev)
-    ws = workspace if workspace is not None else alloc_paged_workspace(shape, MSA_WS_PAGED_SPARSE, dev)
+    ws = workspace if workspace is not None else alloc_paged_workspace(shape, which, dev)
     O = _torch.empty(shape._q, dtype=_bf16, device=dev)
     LSE = _torch.empty(shape._lse, dtype=_torch.float32, device=dev)
-    msa_paged_sparse_attn(shape, cache, Q, q_idx, block_idx, O, LSE, ws)
+    call(shape, cache, Q, q_idx, block_idx, O, LSE, ws)
     return O, LSE, block_idx
+
+
+def _new_dense(call, which, shape, cache, Q, workspace):
+    dev = cache.device
+    ws = workspace if workspace is not None else alloc_paged_workspace(shape, which, dev)
+    O = _torch.empty(shape._q, dtype=_bf16, device=dev)
+    LSE = _torch.empty(shape._lse, dtype=_torch.float32, device=dev)
+    call(shape, cache, Q, O, LSE, ws)
+    return O, LSE
+
+
+def paged_append(shape, cache, rope, K, V, k_idx=None, Q=None, q_idx=None, workspace=None, stream=None, positions=None):
+    """Allocate the rotated queries, run msa_paged_append and return (Q_out, q_idx_out); None where none was given."""
+    args = msa_paged_append, shape, cache, rope, K, V, k_idx, Q, q_idx, workspace, positions
+    return _new_append(*args) if stream is None else _on_stream(stream, cache.device, _new_append, *args)
+
+
+def paged_append_fp8(shape, cache, rope, K, V, k_idx=None, Q=None, q_idx=None, workspace=None, stream=None, positions=None):
+    """paged_append for a PagedCacheFp8."""
+    args = msa_paged_append_fp8, shape, cache, rope, K, V, k_idx, Q, q_idx, workspace, positions
+    return _new_append(*args) if stream is None else _on_stream(stream, cache.device, _new_append, *args)
+
+
+def paged_sparse_attn(shape, cache, Q, q_idx=None, block_idx=None, workspace=None, stream=None):
+    """Allocate O, LSE (and block_idx, when q_idx selects) and run msa_paged_sparse_attn; returns (O, LSE, block_idx)."""
+    args = msa_paged_sparse_attn, MSA_WS_PAGED_SPARSE, shape, cache, Q, q_idx, block_idx, workspace
+    return _new_sparse(*args) if stream is None else _on_stream(stream, cache.device, _new_sparse, *args)
+
+
+def paged_sparse_attn_fp8(shape, cache, Q, q_idx=None, block_idx=None, workspace=None, stream=None):
+    """paged_sparse_attn over a PagedCacheFp8."""
+    args = msa_paged_sparse_attn_fp8, MSA_WS_PAGED_SPARSE_FP8, shape, cache, Q, q_idx, block_idx, workspace
+    return _new_sparse(*args) if stream is None else _on_stream(stream, cache.device, _new_sparse, *args)
 
 
 def paged_dense_attn(shape, cache, Q, workspace=None, stream=None):
     """Allocate O and LSE and run msa_paged_dense_attn."""
+    args = msa_paged_dense_attn, MSA_WS_PAGED_DENSE, shape, cache, Q, workspace
+    return _new_dense(*args) if stream is None else _on_stream(stream, cache.device, _new_dense, *args)
+
+
+def paged_dense_attn_fp8(shape, cache, Q, workspace=None, stream=None):
+    """paged_dense_attn over a PagedCacheFp8."""
+    args = msa_paged_dense_attn_fp8, MSA_WS_PAGED_DENSE_FP8, shape, cache, Q, workspace
+    return _new_dense(*args) if stream is None else _on_stream(stream, cache.device, _new_dense, *args)
+
+
+def _new_read(shape, cache, out_start, M, first, workspace):
     dev = cache.device
-    if stream is not None:
-        return _on_stream(stream, dev, paged_dense_attn, shape, cache, Q, workspace)
-    ws = workspace if workspace is not None else alloc_paged_workspace(shape, MSA_WS_PAGED_DENSE, dev)
-    O = _torch.empty(shape._q, dtype=_bf16, device=dev)
-    LSE = _torch.empty(shape._lse, dtype=_torch.float32, device=dev)
-    msa_paged_dense_attn(shape, cache, Q, O, LSE, ws)
-    return O, LSE
+    ws = workspace if workspace is not None else alloc_paged_workspace(shape, MSA_WS_PAGED_APPEND, dev)
+    K, V = (_torch.empty((M, shape.G, shape.d), dtype=_bf16, device=dev) for _ in range(2))
+    k_idx = None if cache.k_idx is None else _torch.empty((M, shape.d_idx), dtype=_bf16, device=dev)
+    msa_paged_read_fp8(shape, cache, first, out_start, K, V, k_idx, ws)
+    return K, V, k_idx
+
+
+def paged_read_fp8(shape, cache, out_start, M, first=None, workspace=None, stream=None):
+    """Allocate K, V [M, G, 128] and k_idx [M, 64] (None without index keys), run msa_paged_read_fp8 and return them."""
+    args = shape, cache, out_start, M, first, workspace
+    return _new_read(*args) if stream is None else _on_stream(stream, cache.device, _new_read, *args)

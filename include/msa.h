@@ -360,7 +360,13 @@ typedef struct msa_paged_cache {
 } msa_paged_cache;
 
 /* Which entry point a workspace is sized for. */
-enum { MSA_WS_PAGED_APPEND = 0, MSA_WS_PAGED_SPARSE = 1, MSA_WS_PAGED_DENSE = 2 };
+enum {
+  MSA_WS_PAGED_APPEND = 0, /* the appends and msa_paged_read_fp8 */
+  MSA_WS_PAGED_SPARSE = 1,
+  MSA_WS_PAGED_DENSE = 2,
+  MSA_WS_PAGED_SPARSE_FP8 = 4,
+  MSA_WS_PAGED_DENSE_FP8 = 5
+};
 
 /* Bytes of device workspace the entry point `which` needs for `shape` (0 if
  * the shape is invalid or unsupported). */
@@ -442,6 +448,88 @@ MSA_API msa_status msa_paged_sparse_attn(const msa_paged_shape *shape, const msa
 MSA_API msa_status msa_paged_dense_attn(const msa_paged_shape *shape, const msa_paged_cache *cache, const void *Q,
                                         void *O, float *LSE, void *workspace, size_t workspace_bytes,
                                         msa_stream_t stream);
+
+/*
+ * Positions with several axes (itself not part of the method): tokens of images
+ * and videos turn by their time, line and column, each pair of a vector on one of
+ * them: pair i of row r by the angle positions[r][axis[i]] * inv_freq[i]. A row's
+ * place in the cache, and what it sees, still go by its position in its sequence.
+ */
+typedef struct msa_axes {
+  const int32_t *positions; /* [N, axes] (device), any sign                         */
+  const int32_t *axis;      /* [rot_dim / 2] each pair's axis; NULL: all on axis 0  */
+  const int32_t *axis_idx;  /* [rot_dim_idx / 2] the same for q_idx and k_idx       */
+  int32_t axes;             /* 1 .. 8                                               */
+} msa_axes;
+
+/* msa_paged_append with positions of several axes (axes NULL: msa_paged_append).
+ * An axis outside [0, axes) is reported in the error word, and its pairs turn in
+ * no specified way. */
+MSA_API msa_status msa_paged_append_axes(const msa_paged_shape *shape, const msa_paged_cache *cache, const msa_rope *rope,
+                                         const msa_axes *axes, const msa_new_rows *rows, void *Q_out, void *q_idx_out,
+                                         void *workspace, size_t workspace_bytes, msa_stream_t stream);
+
+/*
+ * Serving from a cache in 8 bits: half the bytes of msa_paged_cache, so twice the
+ * tokens, and half the time where the memory's speed is what counts.
+ *
+ * Each vector of the cache (a token's K or V of one group, a token's index key) is
+ * held as E4M3 codes and one power of two, its exponent + 127 in a byte (E8M0); it
+ * stands for the values code * 2^e. Written is, for a vector x in fp32 (after its
+ * rotation),
+ *   e = the smallest with max |x_i| <= 448 * 2^e, in [-117, 120],
+ *   code_i = x_i * 2^-e rounded to nearest, ties to even,
+ * so a value is off by 2^-4 of itself at most (2^-10 * 2^e where that is more).
+ * Values that are not finite become NaN (E4M3 has no infinity) and count for
+ * nothing in e. The values are exact in bf16. Bytes other than 10 .. 247 (those e)
+ * are not supported.
+ *
+ * The calls below are the ones above over such a cache, their results those of the
+ * values it stands for: same batches, limits, errors, infinities of queries and
+ * NaN; workspaces are sized with the _FP8 values (the append: MSA_WS_PAGED_APPEND).
+ * Powers of two of a query and a key (a value) whose product leaves fp32's range
+ * may give infinities or zeros where the exact score would not.
+ */
+typedef struct msa_paged_cache_fp8 {
+  void *K, *V;               /* pools [num_pages, G, Bk, d] E4M3                    */
+  void *K_exp, *V_exp;       /* pools [num_pages, G, Bk] E8M0, 16-byte aligned      */
+  void *k_idx, *k_idx_exp;   /* pools [num_pages, Bk, d_idx] E4M3, [num_pages, Bk]
+                                E8M0; NULL as in msa_paged_cache                    */
+  const int32_t *page_table; /* as in msa_paged_cache                               */
+  const int32_t *row_start;
+  const int32_t *seq_len;
+} msa_paged_cache_fp8;
+
+/* msa_paged_append: K, V and k_idx quantised as they are written, from the fp32
+ * values of the rotation; Q and q_idx stay bf16. axes may be NULL. */
+MSA_API msa_status msa_paged_append_fp8(const msa_paged_shape *shape, const msa_paged_cache_fp8 *cache,
+                                        const msa_rope *rope, const msa_axes *axes, const msa_new_rows *rows, void *Q_out,
+                                        void *q_idx_out, void *workspace, size_t workspace_bytes, msa_stream_t stream);
+
+/*
+ * Tokens back as bf16, exactly the values that the cache stands for: row r of the
+ * M rows, out_start[s] <= r < out_start[s+1], is token first[s] + r - out_start[s]
+ * of sequence s (first NULL: from the first token on), K_out and V_out [M, G, d],
+ * k_idx_out [M, d_idx] (NULL: not wanted), all bf16 and 32-byte aligned. Rows from
+ * out_start[S] on are left alone. A token past seq_len[s] or a page outside the
+ * pools is reported in the error word and its row left alone. cache->row_start and
+ * shape->N, Hq, k are not used. M <= 2^28. first and out_start [S], [S + 1] are
+ * device memory.
+ */
+MSA_API msa_status msa_paged_read_fp8(const msa_paged_shape *shape, const msa_paged_cache_fp8 *cache, const int32_t *first,
+                                      const int32_t *out_start, int32_t M, void *K_out, void *V_out, void *k_idx_out,
+                                      void *workspace, size_t workspace_bytes, msa_stream_t stream);
+
+/* msa_paged_sparse_attn: the selection is that of the exact scores of the index
+ * keys that the cache stands for. */
+MSA_API msa_status msa_paged_sparse_attn_fp8(const msa_paged_shape *shape, const msa_paged_cache_fp8 *cache, const void *Q,
+                                             const void *q_idx, int32_t *block_idx, void *O, float *LSE, void *workspace,
+                                             size_t workspace_bytes, msa_stream_t stream);
+
+/* msa_paged_dense_attn. */
+MSA_API msa_status msa_paged_dense_attn_fp8(const msa_paged_shape *shape, const msa_paged_cache_fp8 *cache, const void *Q,
+                                            void *O, float *LSE, void *workspace, size_t workspace_bytes,
+                                            msa_stream_t stream);
 
 /* Message describing the last non-OK status returned on this thread. */
 MSA_API const char *msa_last_error(void);
