@@ -18,7 +18,10 @@ static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // row's 128 pages 23.7 us, 28.6 uncut; 16000 tokens of 8 groups 22.7 us, 84.7 uncut.
 // Where the merge kernel joins (1 and 0): 64 sequences behind 32K tokens 94 us, 97
 // with two pages. 128-row tiles (3 and 0): 300 rows x 32 heads over 4 groups and
-// 8000 tokens 64 us, 84 with one and 93 with eight pages.
+// 8000 tokens 64 us, 84 with one and 93 with eight pages. In 8 bits, where the
+// mma.sync path joins (8 and 8: a page takes half as long, and the items cost less,
+// too): 16 sequences of up to 4099 tokens and 8 groups 26.4 us, 31.4 with six, 29.5
+// with two.
 static void cut_pages(long long tiles, int pages, double extra, double join, int* per_split, int* n_splits) {
   tiles = std::max(1LL, tiles);
   pages = std::max(1, pages);
@@ -57,7 +60,7 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
     if (p.k > 1 && p.max_blocks > 1) L.pooled = take((size_t)p.N * p.G * p.max_blocks * 8);
     if (p.k > 1) L.n_flags = (int)std::min<long long>((long long)p.S * ((p.max_blocks + 4) / 6), kCutSms - 1);
     L.flags = take(kCutSms * 4);
-    cut_pages((long long)p.N * p.G, std::min(p.k, p.max_blocks), 6, 8, &L.per_split, &L.splits);
+    cut_pages((long long)p.N * p.G, std::min(p.k, p.max_blocks), bytes ? 8 : 6, 8, &L.per_split, &L.splits);
   } else {
     L.tile_rows = 8 / p.hg;
     // More than nine columns (rows x heads) a sequence on average and more than a page each: 128-row tiles, tcgen05. Padded
@@ -84,7 +87,7 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
       L.splits = 0;
       L.n_flags = kCutSms;
     } else {
-      cut_pages(tiles * p.G, p.max_blocks - L.prefix, L.prefix ? 1 : 6, L.prefix ? 0 : 8, &L.per_split, &L.splits);
+      cut_pages(tiles * p.G, p.max_blocks - L.prefix, L.prefix ? 1 : bytes ? 8 : 6, L.prefix ? 0 : 8, &L.per_split, &L.splits);
     }
     if (L.prefix > 0) {
       L.pairs = (int)(((long long)p.N * p.hg + 255) / 256);

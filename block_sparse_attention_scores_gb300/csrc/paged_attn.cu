@@ -53,13 +53,18 @@ constexpr int kWarps = 8;                          // consumers; then the produc
 constexpr int kJoinWarps = 3;
 constexpr int kThreads = (kWarps + 1 + kJoinWarps) * 32;
 constexpr int kHalf = 16384;                       // 128 rows x 64 bf16, 128-byte swizzle
+constexpr int kCols = 8;                           // query columns of a tile
+// K or V of a page and group; pages in flight; a stage's powers of two; warps that share a page; where the warps' results
+// meet, if not in a stage
 template <bool kBytes>
-struct Pages {                                     // K or V of a page and group; pages in flight; a stage's powers of two
-  static constexpr int kTile = 2 * kHalf, kStages = 3, kExps = 0;
+struct Pages {
+  static constexpr int kTile = 2 * kHalf, kStages = 3, kExps = 0, kTeam = kWarps, kMeet = 0;
 };
 template <>
 struct Pages<true> {                               // 128 rows x 128 codes, 128-byte swizzle
-  static constexpr int kTile = kHalf, kStages = 6, kExps = 256;
+  static constexpr int kTile = kHalf, kStages = 6, kExps = 256, kTeam = kWarps / 2, kMeet = kTeam * kCols * 512;
+  // a stage is always the same team's (a barrier's parity tells only two pages apart, and a team does not wait for the other)
+  static_assert(kStages % 2 == 0, "pages alternate between two teams");
 };
 // The joining warps may have nothing to do until the kernel's end: 20 s, and 20 us for every page that a CTA takes if it
 // takes them all in turn (it takes 1.5).
@@ -67,9 +72,9 @@ constexpr unsigned long long kIdleNs = 20000000000ull, kIdlePageNs = 20000ull;
 
 constexpr int kQStride = 272;                      // bytes between the queries' rows in shared memory (no bank conflicts)
 
-constexpr int kCols = 8;                           // query columns of a tile
 template <bool kBytes>
-constexpr int kSmem = Pages<kBytes>::kStages * (2 * Pages<kBytes>::kTile + Pages<kBytes>::kExps) + 2 * kCols * kQStride + 1024;
+constexpr int kSmem = Pages<kBytes>::kStages * (2 * Pages<kBytes>::kTile + Pages<kBytes>::kExps) + Pages<kBytes>::kMeet +
+                      2 * kCols * kQStride + 1024;
 
 struct AttnArgs {
   const int4* rows;
@@ -252,12 +257,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ AttnShared<kStages> sh;
   uint8_t* s_q = smem + kStages * 2 * kTile;    // [2][kCols][kQStride]
   uint8_t* s_exp = s_q + 2 * kCols * kQStride;  // [kStages][K, V][128] (kBytes)
+  uint8_t* s_meet = s_exp + kStages * Pages<kBytes>::kExps;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sh.k_full[i], 1);
       mbar_init(&sh.v_full[i], 1);
-      mbar_init(&sh.empty[i], kWarps);
+      mbar_init(&sh.empty[i], Pages<kBytes>::kTeam);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 1);
@@ -389,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- consumers
     const int r = lane >> 2, q = lane & 3;
     uint32_t st = 0, st_ph = 0, meet_ph = 0;
+    uint32_t n_page = 0;  // (kBytes) pages before this item's
     int n_join = 0;  // items handed to the joining warps
     bool ok = true;
     for (int n_item = 0; ok; ++n_item) {
@@ -436,39 +443,48 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int z = 0; z < 4; ++z) o[mt][z] = 0.f;
 
-      for (int j = 0; j < item.pages; ++j) {
-        if (!mbar_wait(&sh.k_full[st], st_ph, a.err, 1422)) { ok = false; break; }
-        const int token0 = sh.token0[st] + warp * 16;  // of this warp's keys
-        const uint32_t kaddr = smem_u32(smem + st * 2 * kTile), vaddr = kaddr + kTile;
-        const bool masked = token0 + 16 > lim_lo;
-        if constexpr (kBytes) {
-          float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};  // even and odd steps of the sum over d
+      if constexpr (kBytes) {
+        // two teams of four warps, which take a page each in turn, 32 keys a warp: two row tiles in flight in each warp, and
+        // what a page costs beside its products is paid once for 32 keys (387 instructions for 16 keys, 430 for 32)
+        const int key0 = (warp & 3) * 32;
+        for (int j = (n_page ^ warp >> 2) & 1; j < item.pages; j += 2) {
+          const uint32_t st = (n_page + j) % kStages, ph = (n_page + j) / kStages & 1;
+          if (!mbar_wait(&sh.k_full[st], ph, a.err, 1422)) { ok = false; break; }
+          const int token0 = sh.token0[st] + key0;  // of this warp's keys
+          const uint8_t* tile = smem + st * 2 * kTile;
+          const bool masked = token0 + 32 > lim_lo;
+          float sc[8];  // [row tile][key r, r + 8][column]
           {
-            const int key = warp * 16 + (lane & 15);
+            float acc[2][2][4];  // [row tile][even and odd steps of the sum over d]
 #pragma unroll
-            for (int c = 0; c < 8; c += 2) {  // keys r, r + 8, pieces c and c + 1 of 16 codes: four each
-              uint32_t f[4];
-              ldmatrix_x4(f, kaddr + sw128_off(key, c + (lane >> 4)));
-              mma_16816_f16(sc, f16_lo(f[0]), f16_lo(f[1]), f16_hi(f[0]), f16_hi(f[1]), qb[c][0], qb[c][1]);
-              mma_16816_f16(sd, f16_lo(f[2]), f16_lo(f[3]), f16_hi(f[2]), f16_hi(f[3]), qb[c + 1][0], qb[c + 1][1]);
-            }
+            for (int i = 0; i < 16; ++i) acc[i >> 3][i >> 2 & 1][i & 3] = 0.f;
+            const uint32_t kaddr = smem_u32(tile);
+#pragma unroll
+            for (int c = 0; c < 8; c += 2)
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {  // keys r, r + 8 of the tile, pieces c and c + 1 of 16 codes: four each
+                uint32_t f[4];
+                ldmatrix_x4(f, kaddr + sw128_off(key0 + t * 16 + (lane & 15), c + (lane >> 4)));
+                mma_16816_f16(acc[t][0], f16_lo(f[0]), f16_lo(f[1]), f16_hi(f[0]), f16_hi(f[1]), qb[c][0], qb[c][1]);
+                mma_16816_f16(acc[t][1], f16_lo(f[2]), f16_lo(f[3]), f16_hi(f[2]), f16_hi(f[3]), qb[c + 1][0], qb[c + 1][1]);
+              }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sc[i] = acc[i >> 2][0][i & 3] + acc[i >> 2][1][i & 3];
           }
-          const uint8_t* ke = s_exp + st * 256 + warp * 16 + r;
-          float k2[2], x[4], top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // maxima of s, then of s + f
+          const uint8_t* exps = s_exp + st * 256 + key0 + r;
+          float x[8], top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // s + f; the maxima of s, then of s + f
 #pragma unroll
-          for (int y = 0; y < 2; ++y) k2[y] = exp_value(ke[8 * y]);
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            float v = (sc[z] + sd[z]) * k2[z >> 1] * qscale[z & 1];
-            if (masked && token0 + r + (z >> 1) * 8 >= lim[z & 1]) v = -INFINITY;
-            sc[z] = v;
-            top[z & 1] = fmaxf(top[z & 1], v);
+          for (int i = 0; i < 8; ++i) {
+            float v = sc[i] * exp_value(exps[8 * (i >> 1)]) * qscale[i & 1];
+            if (masked && token0 + r + (i >> 1) * 8 >= lim[i & 1]) v = -INFINITY;
+            sc[i] = v;
+            top[i & 1] = fmaxf(top[i & 1], v);
           }
-          if (!mbar_wait(&sh.v_full[st], st_ph, a.err, 1423)) { ok = false; break; }
+          if (!mbar_wait(&sh.v_full[st], ph, a.err, 1423)) { ok = false; break; }
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            x[z] = sc[z] + (float)((int)ke[128 + 8 * (z >> 1)] - 127);
-            top[2 + (z & 1)] = fmaxf(top[2 + (z & 1)], x[z]);
+          for (int i = 0; i < 8; ++i) {
+            x[i] = sc[i] + (float)((int)exps[128 + 8 * (i >> 1)] - 127);
+            top[2 + (i & 1)] = fmaxf(top[2 + (i & 1)], x[i]);
           }
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1)
@@ -494,51 +510,67 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int z = 0; z < 4; ++z) o[mt][z] *= alpha[z & 1];
           }
-          uint32_t ph[2];  // turned so that a lane holds two neighbouring keys of one column
+          uint32_t p[4];  // turned so that a lane holds two neighbouring keys of one column
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
+          for (int y = 0; y < 4; ++y) {
             l_run[0] += fast_exp2(sc[2 * y] - base[0]);
             l_run[1] += fast_exp2(sc[2 * y + 1] - base[1]);
-            ph[y] = movmatrix_trans(pack_f16(fast_exp2(x[2 * y] - wbase[0]), fast_exp2(x[2 * y + 1] - wbase[1])));
+            p[y] = movmatrix_trans(pack_f16(fast_exp2(x[2 * y] - wbase[0]), fast_exp2(x[2 * y + 1] - wbase[1])));
           }
-          // dims 16 r .. + 15 of keys 2 q, + 1 and + 8, + 9: tile mt's row r is dim 16 r + 2 mt, its row r + 8 the next one
-          uint4 v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = warp * 16 + 2 * q + (i & 1) + (i >> 1) * 8;
-            v[i] = *reinterpret_cast<const uint4*>(smem + st * 2 * kTile + kTile + sw128_off(key, r));
-          }
-          auto add_values = [&](float (&to)[4], int mt, int end) {  // of the keys before token `end`
-            uint32_t c[4];
+          // dims 16 r .. + 15 of a row tile's keys 2 q, + 1 and + 8, + 9: tile mt's row r is dim 16 r + 2 mt, its row r + 8
+          // the next one. `end`: values of tokens from there on are cleared.
+          auto load_values = [&](uint4 (&v)[4], int t, int end) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint32_t word[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-              c[i] = token0 + 2 * q + (i & 1) + (i >> 1) * 8 < end ? word[mt >> 1] : 0u;
+              const int key = t * 16 + 2 * q + (i & 1) + (i >> 1) * 8;
+              v[i] = *reinterpret_cast<const uint4*>(tile + kTile + sw128_off(key0 + key, r));
+              if (token0 + key >= end) v[i] = make_uint4(0, 0, 0, 0);
             }
+          };
+          auto add_values = [&](float (&to)[4], const uint4 (&v)[4], int mt, int t) {
+            const uint32_t word[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w}, {v[1].x, v[1].y, v[1].z, v[1].w},
+                                         {v[2].x, v[2].y, v[2].z, v[2].w}, {v[3].x, v[3].y, v[3].z, v[3].w}};
             const uint32_t by = mt & 1 ? 0x7362 : 0x5140;  // two dims' pairs of keys
-            const uint32_t lo = __byte_perm(c[0], c[1], by), hi = __byte_perm(c[2], c[3], by);
-            mma_16816_f16(to, f16_lo(lo), f16_hi(lo), f16_lo(hi), f16_hi(hi), ph[0], ph[1]);
+            const uint32_t lo = __byte_perm(word[0][mt >> 1], word[1][mt >> 1], by);
+            const uint32_t hi = __byte_perm(word[2][mt >> 1], word[3][mt >> 1], by);
+            mma_16816_f16(to, f16_lo(lo), f16_hi(lo), f16_lo(hi), f16_hi(hi), p[2 * t], p[2 * t + 1]);
           };
           if (!masked) {
 #pragma unroll
-            for (int mt = 0; mt < 8; ++mt) add_values(o[mt], mt, 0x7fffffff);
+            for (int t = 0; t < 2; ++t) {
+              uint4 v[4];
+              load_values(v, t, 0x7fffffff);
+#pragma unroll
+              for (int mt = 0; mt < 8; ++mt) add_values(o[mt], v, mt, t);
+            }
           } else {
             // each row of the tile on its own: values behind its end cleared, and only its own columns kept
 #pragma unroll 1
-            for (int i = 0; i < item.rows; ++i) {
-              const int end = lim_lo + i;
-              if (token0 >= end) continue;
+            for (int i = 0; i < 2 * item.rows; ++i) {
+              const int end = lim_lo + (i >> 1), t = i & 1;
+              if (token0 + t * 16 >= end) continue;
+              uint4 v[4];
+              load_values(v, t, end);
 #pragma unroll
               for (int mt = 0; mt < 8; ++mt) {
-                float t[4] = {0.f, 0.f, 0.f, 0.f};
-                add_values(t, mt, end);
+                float add[4] = {0.f, 0.f, 0.f, 0.f};
+                if (t) add_values(add, v, mt, 1);
+                else add_values(add, v, mt, 0);
 #pragma unroll
                 for (int z = 0; z < 4; ++z)
-                  if (lim[z & 1] == end) o[mt][z] += t[z];
+                  if (lim[z & 1] == end) o[mt][z] += add[z];
               }
             }
           }
-        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.empty[st]);
+        }
+        n_page += item.pages;
+      } else {
+        for (int j = 0; j < item.pages; ++j) {
+          if (!mbar_wait(&sh.k_full[st], st_ph, a.err, 1422)) { ok = false; break; }
+          const int token0 = sh.token0[st] + warp * 16;  // of this warp's keys
+          const uint32_t kaddr = smem_u32(smem + st * 2 * kTile), vaddr = kaddr + kTile;
           float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};  // even and odd steps of the sum over d
           {
             const int key = warp * 16 + (lane & 15);
@@ -549,6 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_16816(ks & 1 ? sd : sc, f[0], f[1], f[2], f[3], qb[ks][0], qb[ks][1]);
             }
           }
+          const bool masked = token0 + 16 > lim_lo;
           float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
@@ -623,19 +656,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-        }
-        if (j + 1 == item.pages) break;  // the last page's stage is kept: the warps' results meet in it
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.empty[st]);
-        if (++st == kStages) {
-          st = 0;
-          st_ph ^= 1;
+          if (j + 1 == item.pages) break;  // the last page's stage is kept: the warps' results meet in it
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.empty[st]);
+          if (++st == kStages) {
+            st = 0;
+            st_ph ^= 1;
+          }
         }
       }
       if (!ok) break;
 
       // ---- the warps' results meet: each scales its O to the maximum of all and puts it into the last page's stage
-      // ([warp][column][d], d exchanged by column against bank conflicts), and all 256 threads add up the eight
+      // ([warp][column][d], d exchanged by column against bank conflicts), and all 256 threads add up the eight. (kBytes: a
+      // place of its own, so that the stages stay the teams' own; nobody writes to it before all have met again.)
       const bool joined = a.join && item.parts > 1;
       // one dim of every other column (kBytes: the one whose sums lie at this thread's place, see below)
       const int place = threadIdx.x & 127;
@@ -666,8 +700,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!warps_sync(&sh.meet, meet_ph, a.err, 1425)) { ok = false; break; }
-        float* s_o = reinterpret_cast<float*>(smem + st * 2 * kTile);
-        float* mine = s_o + warp * kCols * 128;
+        float* s_o = reinterpret_cast<float*>(kBytes ? s_meet : smem + st * 2 * kTile);
+        float* mine = s_o + warp % Pages<kBytes>::kTeam * kCols * 128;
         float f[2];  // what this warp's O counts for (0 where no warp saw a key)
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
@@ -679,16 +713,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
-          if constexpr (kBytes) {  // dims 16 r + 2 mt, + 1 at 16 mt + 2 r, + 1
+          if constexpr (kBytes) {
 #pragma unroll
-            for (int z = 0; z < 2; ++z)
-              *reinterpret_cast<float2*>(mine + (2 * q + z) * 128 + ((mt * 16 + r * 2) ^ ((q & 1) << 4) ^ ((q >> 1) << 3))) =
-                  make_float2(o[mt][z] * f[z], o[mt][2 + z] * f[z]);
+            for (int z = 0; z < 4; ++z) o[mt][z] *= f[z & 1];
           } else {
 #pragma unroll
             for (int z = 0; z < 4; ++z)
               mine[(2 * q + (z & 1)) * 128 + ((mt * 16 + r + (z >> 1) * 8) ^ (q << 3))] = o[mt][z] * f[z & 1];
           }
+        }
+        if constexpr (kBytes) {
+          // one team's, then the other's on top: a lane adds to what the same lane of the other team put there. Dims
+          // 16 r + 2 mt, + 1 lie at 16 mt + 2 r, + 1.
+          auto at = [&](int mt, int z) {
+            return reinterpret_cast<float2*>(mine + (2 * q + z) * 128 + ((mt * 16 + r * 2) ^ ((q & 1) << 4) ^ ((q >> 1) << 3)));
+          };
+          const bool second = warp >= Pages<kBytes>::kTeam;
+          if (second)
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+              for (int z = 0; z < 2; ++z) *at(mt, z) = make_float2(o[mt][z], o[mt][2 + z]);
+          if (!warps_sync(&sh.meet, meet_ph, a.err, 1424)) { ok = false; break; }
+          if (!second)
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const float2 other = *at(mt, z);
+                *at(mt, z) = make_float2(o[mt][z] + other.x, o[mt][2 + z] + other.y);
+              }
         }
         {
           // this warp's column's sum: lane w % 8 has warp w's
@@ -718,16 +772,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (col >= cols) break;
           float val = 0.f;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w)
+          for (int w = 0; w < Pages<kBytes>::kTeam; ++w)
             val += s_o[(w * kCols + col) * 128 + (place ^ (kBytes ? (col & 2) << 3 | (col & 4) << 1 : (col & 6) << 2))];
           put(col, val * sh.inv[col], sh.lse[col]);
         }
-        fence_proxy_async_smem();  // the stage goes back to TMA
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.empty[st]);
-        if (++st == kStages) {
-          st = 0;
-          st_ph ^= 1;
+        if constexpr (!kBytes) {
+          fence_proxy_async_smem();  // the stage goes back to TMA
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.empty[st]);
+          if (++st == kStages) {
+            st = 0;
+            st_ph ^= 1;
+          }
         }
       }
       if (!ok) break;

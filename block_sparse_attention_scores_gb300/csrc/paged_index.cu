@@ -141,19 +141,24 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       const bool bad = want && (now.page < 0 || now.page >= a.num_pages);
       if (bad) dev_fail(&sh.flag, kDevBadIndex, 1301);
       const int page = bad ? 0 : now.page, cols = rows * a.G;
-      for (unsigned m = __ballot_sync(0xffffffffu, want); m; m &= m - 1, ++n) {
-        const int from = __ffs(m) - 1, st = n % kStages;
-        if (!mbar_wait(&sh.empty[st], ((n / kStages) & 1) ^ 1, &sh.flag, 1302, a.wait_ns)) { ok = false; break; }
-        if (lane == from) {
-          sh.info[st] = make_int4(now.s, bad ? ~now.c : now.c, now.begin, cols);
-          const int first = min(cols, 8);
-          mbar_arrive_expect_tx(&sh.full[st], kPage + kScoreExp<kBytes> + first * 128);
-          tma_load_2d(smem + st * kPage, &map_k, &sh.full[st], 0, page * 128);
-          // (one copy: eight of 128 bytes that avoid bank conflicts took longer to issue than the page to arrive)
-          bulk_load(s_q + st * kScoreQ, a.q_idx + (size_t)now.begin * a.G * 64, first * 128, &sh.full[st]);
-          if (kBytes) bulk_load(s_exp + st * 128, a.k_exp + (size_t)page * 128, 128, &sh.full[st]);
+      const unsigned all = __ballot_sync(0xffffffffu, want);
+      for (int i = 0; i < kScoreBatch && ok; ++i) {  // an item's pages at once, a lane each: one after the other they took
+        const unsigned m = all & ((1u << kScoreRun) - 1) << i * kScoreRun;  // longer to be asked for than to arrive
+        if (m >> lane & 1) {
+          const int at = n + __popc(m & ((1u << lane) - 1)), st = at % kStages;
+          ok = mbar_wait(&sh.empty[st], ((at / kStages) & 1) ^ 1, &sh.flag, 1302, a.wait_ns);
+          if (ok) {
+            sh.info[st] = make_int4(now.s, bad ? ~now.c : now.c, now.begin, cols);
+            const int first = min(cols, 8);
+            mbar_arrive_expect_tx(&sh.full[st], kPage + kScoreExp<kBytes> + first * 128);
+            tma_load_2d(smem + st * kPage, &map_k, &sh.full[st], 0, page * 128);
+            // (one copy: eight of 128 bytes that avoid bank conflicts took longer to issue than the page to arrive)
+            bulk_load(s_q + st * kScoreQ, a.q_idx + (size_t)now.begin * a.G * 64, first * 128, &sh.full[st]);
+            if (kBytes) bulk_load(s_exp + st * 128, a.k_exp + (size_t)page * 128, 128, &sh.full[st]);
+          }
         }
-        __syncwarp();
+        ok = __all_sync(0xffffffffu, ok);
+        n += __popc(m);
       }
     }
     for (int i = 0; i < kScoreWarps && ok; ++i, ++n) {  // the end, for every warp
@@ -218,20 +223,26 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
           uint32_t any = 0;
           bool nan = false;
 #pragma unroll
-          for (int m = 0; m < 8; ++m) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int m0 = 0; m0 < 8; m0 += 2) {  // two tiles of 16 keys at a time: their sums are chains of four
+            float d[2][4] = {};
 #pragma unroll
-            for (int c = 0; c < 4; c += 2) {
-              uint32_t f[4];  // keys r, r + 8 of piece c, then of c + 1: codes 4 q .. 4 q + 3
-              const int key = m * 16 + (lane & 15);
-              ldmatrix_x4(f, base + key * 64 + (((c + (lane >> 4)) ^ ((key >> 1) & 3)) << 4));
-              mma_16816_f16(d, f16_lo(f[0]), f16_lo(f[1]), f16_hi(f[0]), f16_hi(f[1]), b[c][0], b[c][1]);
-              mma_16816_f16(d, f16_lo(f[2]), f16_lo(f[3]), f16_hi(f[2]), f16_hi(f[3]), b[c + 1][0], b[c + 1][1]);
-              if (n0 == 0) any |= f[0] | f[1] | f[2] | f[3];
+            for (int c = 0; c < 4; c += 2)
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                uint32_t f[4];  // keys r, r + 8 of piece c, then of c + 1: codes 4 q .. 4 q + 3
+                const int key = (m0 + t) * 16 + (lane & 15);
+                ldmatrix_x4(f, base + key * 64 + (((c + (lane >> 4)) ^ ((key >> 1) & 3)) << 4));
+                mma_16816_f16(d[t], f16_lo(f[0]), f16_lo(f[1]), f16_hi(f[0]), f16_hi(f[1]), b[c][0], b[c][1]);
+                mma_16816_f16(d[t], f16_lo(f[2]), f16_lo(f[3]), f16_hi(f[2]), f16_hi(f[3]), b[c + 1][0], b[c + 1][1]);
+                if (n0 == 0) any |= f[0] | f[1] | f[2] | f[3];
+              }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const float lo = pow2[2 * (m0 + t)], hi = pow2[2 * (m0 + t) + 1];
+              nan |= d[t][0] != d[t][0] || d[t][1] != d[t][1] || d[t][2] != d[t][2] || d[t][3] != d[t][3];
+              best0 = fmaxf(best0, fmaxf(d[t][0] * lo, d[t][2] * hi));
+              best1 = fmaxf(best1, fmaxf(d[t][1] * lo, d[t][3] * hi));
             }
-            nan |= d[0] != d[0] || d[1] != d[1] || d[2] != d[2] || d[3] != d[3];
-            best0 = fmaxf(best0, fmaxf(d[0] * pow2[2 * m], d[2] * pow2[2 * m + 1]));
-            best1 = fmaxf(best1, fmaxf(d[1] * pow2[2 * m], d[3] * pow2[2 * m + 1]));
           }
           if (n0 == 0 && !__any_sync(0xffffffffu, any & 0x7f7f7f7fu)) top = 0;
           if (n0 == 0 && __any_sync(0xffffffffu, nan)) top = 0x7f800000u;  // (a NaN score is looked at again)
