@@ -67,7 +67,7 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
     // rows count, as nothing here tells them from others: the ninth column is for a pad of up to an eighth. Against eight
     // columns at a time: 32 sequences of 2 rows x 64 heads over 2000 tokens 63 -> 60 us, of 8 rows 135 -> 69, 300 rows x 32
     // heads over 4 groups and 8000 tokens 274 -> 64; the other way for one page (8 rows x 64 heads over 100 tokens 17 -> 10).
-    const bool runs = !bytes && (long long)p.N * p.hg > 9LL * p.S && p.max_blocks - p.prefix > 1;
+    const bool runs = (long long)p.N * p.hg > 9LL * p.S && p.max_blocks - p.prefix > 1;
     // A shared prefix of ten pages an SM (13 where a sequence has several tiles of eight columns), counted for every such
     // tile, is read as own pages: it stays in L2, and two kernels do with it what four do. 4 sequences of 32 heads over 8
     // groups behind 16 pages 15 us against 19, 16 behind 8 pages 14 and 19, 8 of 4 rows behind 12 pages (1536) 17 and 21,
@@ -77,7 +77,7 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
     const long long tiles = std::max(p.N / L.tile_rows, std::min(p.S, p.N));
     // (Idle sequences count too: their tables are looked at by the one block that lines up the rows.)
     const long long readers = std::max<long long>(tiles, p.S);
-    const bool fold = bytes || !runs && readers * p.prefix * p.G <= (readers > p.S ? 2000 : 1500);
+    const bool fold = !runs && readers * p.prefix * p.G <= (readers > p.S ? 2000 : 1500);
     L.prefix = fold ? 0 : p.prefix;
     if (runs) {
       L.run_rows = 256 / p.hg;

@@ -47,6 +47,14 @@
 // own pages of 16 x 4 rows x 64 heads over 3000 tokens 50 us, 4.1 TB/s; the whole
 // call for 32 x 4 rows x 64 heads over 2000 tokens 63 us, for 300 rows x 32 heads
 // over 4 groups and 8000 tokens 64 us (610 TFLOP/s, P's second product not counted).
+//
+// A cache in 8 bits (kBytes, paged_fp8.cuh): the same products of the values that
+// the codes stand for, which bf16 holds exactly. Codes arrive by plain bulk copies,
+// half a tile at a time (a page's codes of a group lie in a row), and four warps
+// turn them into the bf16 tiles that the tensor core reads: 30 operations a pair of
+// softmax values stand against 4 a pair of codes, for as many codes as the two
+// tiles have scores, so the chain above stays what bounds. V is cleaned on the way.
+#include "paged_fp8.cuh"
 #include "paged_rows.cuh"
 
 namespace msa {
@@ -54,12 +62,19 @@ namespace {
 
 constexpr float kHeadroom = 8.f;  // P = exp2(s - m) stays <= 2^kHeadroom
 // warp 0 TMA, warp 1 UMMA + TMEM, 2 and 3 V of own pages, 4-11 and 12-19 softmax of tiles 0 and 1
-constexpr int kThreads = 640;
+// (kBytes: 20-23 make bf16 tiles of codes; 2 and 3 have nothing to do)
+template <bool kBytes>
+constexpr int kThreads = kBytes ? 768 : 640;
 constexpr int kTile = 32768;      // 128 rows x 128 bf16, two 64-column SW128 chunks
 constexpr int kChunk = 16384;
 constexpr int kStages = 2;        // K/V ring
 constexpr int oQ = 0, oK = 2 * kTile, oV = oK + kStages * kTile;
-constexpr int kSmem = oV + kStages * kTile + 1024;
+constexpr int oRaw = oV + kStages * kTile;  // (kBytes) codes on their way, and their powers of two
+constexpr int kRawStages = 4;
+constexpr int kRaw = 8192, kRawRows = 64;   // half a tile
+constexpr int oExp = oRaw + kRawStages * kRaw;
+constexpr int oShared = oExp + kRawStages * kRawRows;  // (kBytes) PrefixShared
+constexpr int kConverters = 4;
 
 // One run: pages of one group against up to two tiles of rows.
 struct Run {
@@ -78,7 +93,8 @@ struct PrefixArgs {
   const int32_t *page_table, *row_start;
   float *part_o, *part_lse;
   const int4* runs;
-  const __nv_bfloat16* V;
+  const void* V;
+  const uint8_t *K, *K_exp, *V_exp;  // (kBytes)
   int* header;
   int S, N, Hq, G, hg, prefix, pairs, teams, num_pages, max_blocks;
   int run_rows, per_run, rslots, pslots;
@@ -88,7 +104,7 @@ struct PrefixArgs {
 struct PrefixShared {
   int flag;
   Run run[2];
-  int odd[2];  // a run's V has infinities or NaN among the rows' own tokens
+  int odd[2][kConverters];  // a run's V has infinities or NaN among the rows' own tokens (as each warp that looks finds it)
   uint64_t run_full[2], run_empty[2], k_full[kStages], v_clean[kStages];  // (kRuns)
   uint64_t q_full, q_empty;
   uint64_t k0_full, kv_full[kStages];  // the first page's K; then a page's V with the next one's K
@@ -97,8 +113,33 @@ struct PrefixShared {
   uint64_t pair[2][4];           // the two warps of a tile's 32 rows
   float row_max[2][2][128];      // [tile][half][row] of the page's scores (at the end: the row's sums)
   int raised[2][2][4];           // [tile][half][quarter] the page (counted from 1) at which this warp called the other
+  uint64_t raw_full[kRawStages], raw_empty[kRawStages];  // (kBytes)
   uint32_t tmem_base;
 };
+// 8 bits: everything in the dynamic part, whose beginning is then a multiple of 1024 bytes from the SM's (there is no room
+// left to align it)
+template <bool kBytes>
+constexpr int kSmem = kBytes ? oShared + (int)sizeof(PrefixShared) : oRaw + 1024;
+static_assert(kSmem<true> <= 232448, "shared memory of a block");
+
+template <bool kBytes>
+struct PrefixSharedOf {
+  static __device__ __forceinline__ PrefixShared& at(uint8_t*) {
+    __shared__ PrefixShared sh;
+    return sh;
+  }
+};
+template <>
+struct PrefixSharedOf<true> {
+  static __device__ __forceinline__ PrefixShared& at(uint8_t* smem) { return *reinterpret_cast<PrefixShared*>(smem + oShared); }
+};
+
+// Registers of a thread, by whole warpgroups: more (of what others have given back) or fewer than before.
+template <int kCount, bool kMore>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (kMore) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kCount) : "memory");
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCount) : "memory");
+}
 
 // (x0, x1) * a + b, two at a time.
 __device__ __forceinline__ void fma2(float& x0, float& x1, float a, float b) {
@@ -123,13 +164,19 @@ __device__ __forceinline__ void st_global8(float* p, const float* v) {
 
 // kShared: the call has a shared prefix. Without one every page is a sequence's own, and its P has both parts: told at run
 // time, as where there are both kinds, it costs 2 % (32 x 4 rows x 64 heads over 2000 tokens 63.3 -> 64.9 us).
-template <bool kRuns, bool kShared>
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool kRuns, bool kShared, bool kBytes>
+__global__ void __launch_bounds__(kThreads<kBytes>, 1)
     paged_prefix_kernel(PrefixArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v) {
+  static_assert(kRuns || !kBytes, "8 bits: one instance for shared and own pages");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ PrefixShared sh;
+  uint8_t* smem = kBytes ? smem_raw
+                         : reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  PrefixShared& sh = PrefixSharedOf<kBytes>::at(smem);
+  if (kBytes && (smem_u32(smem) & 1023)) {  // (the tiles' swizzle goes by the address)
+    if (threadIdx.x == 0) a.flags[blockIdx.x] = kDevBadIndex * 65536 + 1500;
+    return;
+  }
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int team = a.pairs ? blockIdx.x / a.pairs : 0, pair = a.pairs ? blockIdx.x % a.pairs : 0;
   const int units = a.G * a.prefix;
@@ -148,16 +195,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 4; ++j) mbar_init(&sh.pair[i][j], 2);
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sh.kv_full[i], 1);
+      mbar_init(&sh.kv_full[i], kBytes ? kConverters : 1);
       mbar_init(&sh.k_empty[i], 1);
       mbar_init(&sh.v_empty[i], 1);
     }
     if (kRuns) {
       for (int i = 0; i < 2; ++i) {
         mbar_init(&sh.run_full[i], 1);
-        mbar_init(&sh.run_empty[i], 19);
-        mbar_init(&sh.k_full[i], 1);
+        mbar_init(&sh.run_empty[i], kBytes ? 17 + kConverters : 19);
+        mbar_init(&sh.k_full[i], kBytes ? kConverters : 1);
         mbar_init(&sh.v_clean[i], 1);
+      }
+    }
+    if (kBytes) {
+      for (int i = 0; i < kRawStages; ++i) {
+        mbar_init(&sh.raw_full[i], 1);
+        mbar_init(&sh.raw_empty[i], kConverters);
       }
     }
     mbar_init(&sh.k0_full, 1);
@@ -217,6 +270,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     return (page * a.G + run.g) * 128;
   };
 
+  // (kBytes) Of the 61,440 registers that the block starts with, the softmax gets 96 a thread.
+  static_assert(!kBytes || 512 * 96 + 128 * (56 + 40) <= 768 * 80, "registers of a block");
+  if (warp < 4) {
+    if constexpr (kBytes) set_registers<56, false>();
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
     tma_prefetch_desc(&map_q);
@@ -281,8 +338,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto more = [&] { return u < u_end || second || id < items; };  // what step 3 of the last one leaves to be asked for
       for (int s = 0; s < 3; ++s) find(now, s);
       int n_run = 0;
-      uint32_t kc = 0;
+      uint32_t kc = 0, rc = 0;  // pages; half tiles of codes
       bool ok = true;
+      // a tile of codes, whose first vector is `at`, and their powers of two
+      auto load_codes = [&](const uint8_t* codes, const uint8_t* exps, int at) {
+        for (int h = 0; h < 2 && ok; ++h, ++rc) {
+          const int rs = rc % kRawStages;
+          ok = mbar_wait(&sh.raw_empty[rs], ((rc / kRawStages) & 1) ^ 1, err, 1507);
+          if (ok && lane == 0) {
+            mbar_arrive_expect_tx(&sh.raw_full[rs], kRaw + kRawRows);
+            bulk_load(smem + oRaw + rs * kRaw, codes + ((size_t)at + h * kRawRows) * 128, kRaw, &sh.raw_full[rs]);
+            bulk_load(smem + oExp + rs * kRawRows, exps + at + h * kRawRows, kRawRows, &sh.raw_full[rs]);
+          }
+          __syncwarp();
+        }
+      };
       while (ok) {
         const bool end = now.run.pages == 0;
         if (end && more()) {  // a run without pages: on to the next one
@@ -305,8 +375,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (page && !other && (page & 31) == 0) y = table_row(now.run, page + lane);
           const int st = kc % kStages, at = __shfl_sync(0xffffffffu, y, page & 31) + other;
           const uint32_t par = ((kc / kStages) & 1) ^ 1;
-          if (!mbar_wait(&sh.k_empty[st], par, err, 1503)) { ok = false; break; }
-          if (lane == 0) load_kv(oK + st * kTile, &map_k, &sh.k_full[st], at);
+          if constexpr (kBytes) {
+            load_codes(a.K, a.K_exp, at);
+            if (!ok) break;
+          } else {
+            if (!mbar_wait(&sh.k_empty[st], par, err, 1503)) { ok = false; break; }
+            if (lane == 0) load_kv(oK + st * kTile, &map_k, &sh.k_full[st], at);
+          }
           __syncwarp();
           if (i == 0 && !mbar_wait(&sh.q_empty, (n_run & 1) ^ 1, err, 1502)) { ok = false; break; }
           if (i == 0 && lane == 0) {  // (the first K may come while the run before still needs its queries)
@@ -319,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           __syncwarp();
+          if constexpr (kBytes) load_codes(static_cast<const uint8_t*>(a.V), a.V_exp, at);
           if (step < 3) find(next, step++);
         }
         ++n_run;
@@ -442,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the page's V and the next one's K first: nothing then stands between P_t and its products
             if (c == 0 && !mbar_wait(&sh.o_free[t], (runs_of[t] & 1) ^ 1, err, 1516 + t)) { ok = false; break; }
             if ((t == 0 || twin) && !mbar_wait(&sh.kv_full[st], (kk / kStages) & 1, err, 1518)) { ok = false; break; }
-            if (kRuns && (t == 0 || twin) && !mbar_wait(&sh.v_clean[st], (kk / kStages) & 1, err, 1519)) { ok = false; break; }
+            if (kRuns && !kBytes && (t == 0 || twin) && !mbar_wait(&sh.v_clean[st], (kk / kStages) & 1, err, 1519)) { ok = false; break; }
             // P_t of this page written (and O_t rescaled if its row maximum moved)
             if (!mbar_wait(&sh.p_full[t], pages_of[t] & 1, err, 1514 + t)) { ok = false; break; }
             ++pages_of[t];
@@ -466,9 +542,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp < 4) {
+  } else {
     // ---------------------------------------------------------------- V of the sequences' own pages
-    if constexpr (kRuns) {
+    if constexpr (kRuns && !kBytes) {
       // Two warps for V. The first loads it; K has a producer of its own (and arrives a softmax earlier), so that neither
       // waits for the other's stages. The second looks at V of pages that not every row sees all of: what lies behind the
       // last row's end is cleared, and infinities and NaN among the rows' own tokens, which would reach the rows before
@@ -480,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int streams = run.twin ? 2 : 1;
         int y = 0;
         if (warp == 2) y = table_row(run, lane);
-        else if (lane == 0) sh.odd[(n_run - 1) & 1] = 0;
+        else if (lane < kConverters) sh.odd[(n_run - 1) & 1][lane] = 0;
         __syncwarp();
         for (int i = 0; i < run.pages * streams; ++i, ++kc) {
           const int st = kc % kStages, page = run.twin ? i >> 1 : i, other = run.twin ? i & 1 : 0;
@@ -519,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 8
             for (int key = behind + lane / 16; key < 128; key += 2)
               *reinterpret_cast<uint4*>(tile + sw128_off(key, chunk & 7)) = make_uint4(0, 0, 0, 0);
-            if (odd) sh.odd[(n_run - 1) & 1] = 1;
+            if (odd) sh.odd[(n_run - 1) & 1][0] = 1;
             fence_proxy_async_smem();
           }
           __syncwarp();
@@ -528,8 +604,82 @@ __global__ void __launch_bounds__(kThreads, 1)
         run_done(false);
       }
     }
+  }
+  } else if (kBytes && warp >= 20) {
+    // ---------------------------------------------------------------- codes to bf16 tiles
+    if constexpr (kBytes) {
+      set_registers<40, false>();
+      // Eight threads a key, 16 codes each: a warp takes four keys at a time. A thread's two 16-byte pieces go into one of
+      // the tile's 64-column chunks; the upper half's threads write theirs the other way round, so that the eight threads
+      // of a key meet in no bank.
+      const int piece = lane & 7, key_lane = (warp - 20) * 4 + (lane >> 3);
+      const uint32_t chunk = (piece >> 2) * kChunk;
+      const int c0 = (piece & 3) * 2 + (piece >> 2), c1 = c0 ^ 1;
+      uint32_t kc = 0, rc = 0;
+      Run run;
+      bool ok = true;
+      // behind, own: keys from `behind` on become zeros, NaN among those from `own` on too; returns whether there were any
+      auto convert = [&](uint8_t* tile, int own, int behind) {
+        bool odd = false;
+        for (int h = 0; h < 2 && ok; ++h, ++rc) {
+          const int rs = rc % kRawStages;
+          ok = mbar_wait(&sh.raw_full[rs], (rc / kRawStages) & 1, err, 1508);
+          if (!ok) break;
+          const uint8_t* raw = smem + oRaw + rs * kRaw + piece * 16;
+          const uint8_t* exps = smem + oExp + rs * kRawRows;
+#pragma unroll
+          for (int i = 0; i < kRawRows / 16; ++i) {
+            const int row = i * 16 + key_lane, key = h * kRawRows + row;
+            uint4 v = *reinterpret_cast<const uint4*>(raw + row * 128);
+            const float pow2 = key < behind ? exp_value(exps[row]) : 0.f;
+            if (key >= own) {
+              // (0x7f, the only code that is not finite, plus 1 has the top bit)
+              auto clean = [&](uint32_t& w) {
+                const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                odd |= nan != 0 && key < behind;
+                w = key < behind ? w & ~((nan >> 7) * 0xffu) : 0u;
+              };
+              clean(v.x); clean(v.y); clean(v.z); clean(v.w);
+            }
+            const uint4 lo = eight_bf16(make_uint2(v.x, v.y), pow2), hi = eight_bf16(make_uint2(v.z, v.w), pow2);
+            const bool up = piece >> 2;
+            *reinterpret_cast<uint4*>(tile + chunk + sw128_off(key, c0)) = up ? hi : lo;
+            *reinterpret_cast<uint4*>(tile + chunk + sw128_off(key, c1)) = up ? lo : hi;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.raw_empty[rs]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        return odd;
+      };
+      while (ok && next_run(run)) {
+        const int streams = run.twin ? 2 : 1, slot = (n_run - 1) & 1;
+        if (lane == 0) sh.odd[slot][warp - 20] = 0;
+        __syncwarp();
+        for (int i = 0; i < run.pages * streams; ++i, ++kc) {
+          const int st = kc % kStages, page = run.twin ? i >> 1 : i;
+          const uint32_t par = ((kc / kStages) & 1) ^ 1;
+          if (!mbar_wait(&sh.k_empty[st], par, err, 1503)) { ok = false; break; }
+          convert(smem + oK + st * kTile, 128, 128);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive(&sh.k_full[st]);
+          if (!mbar_wait(&sh.v_empty[st], par, err, 1504)) { ok = false; break; }
+          const int token0 = (run.first + page) * 128;
+          const bool masked = page >= run.masked;
+          const int own = masked ? max(0, run.pos + 1 - token0) : 128;
+          const int behind = masked ? min(128, max(0, run.pos + run.rows - token0)) : 128;
+          if (convert(smem + oV + st * kTile, min(own, behind), behind)) sh.odd[slot][warp - 20] = 1;
+          if (!ok) break;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.kv_full[st]);
+        }
+        run_done(false);
+      }
+    }
   } else {
     // ---------------------------------------------------------------- softmax (thread = one head of one new row, 64 keys)
+    if constexpr (kBytes) set_registers<96, true>();
     const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;
     const int quarter = warp & 3;
     const int lrow = quarter * 32 + lane;
@@ -698,7 +848,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = kRuns ? in < run.rows : row < a.N;
       const int group = run.g + (twin ? t : 0);
       const size_t at = ((size_t)run.slot * a.N + row) * a.Hq + group * a.hg + lrow % a.hg;
-      const bool odd = kRuns && run.own && sh.odd[(n_run - 1) & 1];
+      bool odd = false;
+      if (kRuns && run.own) {
+        const int* found = sh.odd[(n_run - 1) & 1];
+        odd = found[0] | found[1] | found[2] | found[3];
+      }
       const float inv = l == 0.f ? 0.f : 1.f / l;  // (a run behind the row's end, or scores of -infinity)
       float* dst = a.part_o + at * 128 + half * 64;
 #pragma unroll
@@ -713,11 +867,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = begin; k < end; ++k) {
             const int page = ld_in(a.page_table + (size_t)run.seq * a.max_blocks + k / 128);
             if (page < 0 || page >= a.num_pages) continue;
-            const __nv_bfloat16* v = a.V + (((size_t)page * a.G + group) * 128 + k % 128) * 128 + half * 64 + z * 16;
+            const size_t at = (((size_t)page * a.G + group) * 128 + k % 128) * 128 + half * 64 + z * 16;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float x = __bfloat162float(v[i]);
-              if (!(fabsf(x) < INFINITY)) o[i] += x;
+              if constexpr (kBytes) {
+                if ((static_cast<const uint8_t*>(a.V)[at + i] & 0x7f) == 0x7f) o[i] = NAN;
+              } else {
+                const float x = __bfloat162float(static_cast<const __nv_bfloat16*>(a.V)[at + i]);
+                if (!(fabsf(x) < INFINITY)) o[i] += x;
+              }
             }
           }
         }
@@ -741,18 +899,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <bool kRuns, bool kShared>
+template <bool kRuns, bool kShared, bool kBytes>
 cudaError_t launch_prefix(const PrefixArgs& a, int blocks, const CUtensorMap& mq, const PoolMaps& maps, cudaStream_t st) {
   static bool attr[kMaxDevices] = {};
   const int dslot = device_slot();
   if (!attr[dslot]) {
     cudaError_t e =
-        cudaFuncSetAttribute(paged_prefix_kernel<kRuns, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        cudaFuncSetAttribute(paged_prefix_kernel<kRuns, kShared, kBytes>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<kBytes>);
     if (e != cudaSuccess) return e;
     attr[dslot] = true;
   }
   count_launches(1);
-  return launch_dependent(paged_prefix_kernel<kRuns, kShared>, blocks, kThreads, kSmem, st, a, mq, maps.k, maps.v);
+  return launch_dependent(paged_prefix_kernel<kRuns, kShared, kBytes>, blocks, kThreads<kBytes>, kSmem<kBytes>, st, a, mq, maps.k, maps.v);
 }
 
 }  // namespace
@@ -786,15 +944,21 @@ cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, con
   a.max_blocks = p.max_blocks;
   a.scale_log2 = p.scale * kLog2e;
   a.runs = reinterpret_cast<const int4*>(ws + L.runs);
-  a.V = static_cast<const __nv_bfloat16*>(c.V);
+  a.V = c.V;
+  a.K = static_cast<const uint8_t*>(c.K);
+  a.K_exp = c.K_exp;
+  a.V_exp = c.V_exp;
   a.header = reinterpret_cast<int*>(ws);
   a.run_rows = L.run_rows;
   a.per_run = L.per_run;
   a.rslots = L.rslots;
   a.pslots = L.pslots;
-  if (!L.run_rows) return launch_prefix<false, true>(a, L.n_flags, mq, maps, st);
-  if (L.prefix) return launch_prefix<true, true>(a, L.n_flags, mq, maps, st);
-  return launch_prefix<true, false>(a, L.n_flags, mq, maps, st);
+  if (c.bytes())
+    return L.prefix ? launch_prefix<true, true, true>(a, L.n_flags, mq, maps, st)
+                    : launch_prefix<true, false, true>(a, L.n_flags, mq, maps, st);
+  if (!L.run_rows) return launch_prefix<false, true, false>(a, L.n_flags, mq, maps, st);
+  if (L.prefix) return launch_prefix<true, true, false>(a, L.n_flags, mq, maps, st);
+  return launch_prefix<true, false, false>(a, L.n_flags, mq, maps, st);
 }
 
 }  // namespace msa
