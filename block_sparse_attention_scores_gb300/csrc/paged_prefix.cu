@@ -50,7 +50,7 @@
 //
 // A cache in 8 bits (kBytes, paged_fp8.cuh): the same products of the values that
 // the codes stand for, which bf16 holds exactly. Codes arrive by plain bulk copies,
-// half a tile at a time (a page's codes of a group lie in a row), and four warps
+// half a tile at a time (a page's codes of a group lie in a row), and eight warps
 // turn them into the bf16 tiles that the tensor core reads: 30 operations a pair of
 // softmax values stand against 4 a pair of codes, for as many codes as the two
 // tiles have scores, so the chain above stays what bounds. V is cleaned on the way.
@@ -62,19 +62,19 @@ namespace {
 
 constexpr float kHeadroom = 8.f;  // P = exp2(s - m) stays <= 2^kHeadroom
 // warp 0 TMA, warp 1 UMMA + TMEM, 2 and 3 V of own pages, 4-11 and 12-19 softmax of tiles 0 and 1
-// (kBytes: 20-23 make bf16 tiles of codes; 2 and 3 have nothing to do)
+// (kBytes: 20-23 and 24-27 make bf16 tiles of K's and V's codes; 2 and 3 have nothing to do)
 template <bool kBytes>
-constexpr int kThreads = kBytes ? 768 : 640;
+constexpr int kThreads = kBytes ? 896 : 640;
 constexpr int kTile = 32768;      // 128 rows x 128 bf16, two 64-column SW128 chunks
 constexpr int kChunk = 16384;
 constexpr int kStages = 2;        // K/V ring
 constexpr int oQ = 0, oK = 2 * kTile, oV = oK + kStages * kTile;
-constexpr int oRaw = oV + kStages * kTile;  // (kBytes) codes on their way, and their powers of two
-constexpr int kRawStages = 4;
-constexpr int kRaw = 8192, kRawRows = 64;   // half a tile
-constexpr int oExp = oRaw + kRawStages * kRaw;
-constexpr int oShared = oExp + kRawStages * kRawRows;  // (kBytes) PrefixShared
-constexpr int kConverters = 4;
+// (kBytes) Codes on their way, by halves of a tile, and their powers of two
+constexpr int kConverters = 4;                                    // warps for each half
+constexpr int kHalfKeys = 64, kHalf = kHalfKeys * 128, kRaw = 2;  // halves in flight, of K and of V
+constexpr int oRawK = oV + kStages * kTile, oRawV = oRawK + kRaw * kHalf;
+constexpr int oExpK = oRawV + kRaw * kHalf, oExpV = oExpK + kRaw * kHalfKeys;
+constexpr int oShared = oExpV + kRaw * kHalfKeys;                 // PrefixShared
 
 // One run: pages of one group against up to two tiles of rows.
 struct Run {
@@ -104,7 +104,7 @@ struct PrefixArgs {
 struct PrefixShared {
   int flag;
   Run run[2];
-  int odd[2][kConverters];  // a run's V has infinities or NaN among the rows' own tokens (as each warp that looks finds it)
+  int odd[2][2 * kConverters];  // a run's V has infinities or NaN among the rows' own tokens (as each warp that looks finds it)
   uint64_t run_full[2], run_empty[2], k_full[kStages], v_clean[kStages];  // (kRuns)
   uint64_t q_full, q_empty;
   uint64_t k0_full, kv_full[kStages];  // the first page's K; then a page's V with the next one's K
@@ -113,13 +113,13 @@ struct PrefixShared {
   uint64_t pair[2][4];           // the two warps of a tile's 32 rows
   float row_max[2][2][128];      // [tile][half][row] of the page's scores (at the end: the row's sums)
   int raised[2][2][4];           // [tile][half][quarter] the page (counted from 1) at which this warp called the other
-  uint64_t raw_full[kRawStages], raw_empty[kRawStages];  // (kBytes)
+  uint64_t raw_full[2 * kRaw], raw_empty[2 * kRaw];  // (kBytes)
   uint32_t tmem_base;
 };
 // 8 bits: everything in the dynamic part, whose beginning is then a multiple of 1024 bytes from the SM's (there is no room
 // left to align it)
 template <bool kBytes>
-constexpr int kSmem = kBytes ? oShared + (int)sizeof(PrefixShared) : oRaw + 1024;
+constexpr int kSmem = kBytes ? oShared + (int)sizeof(PrefixShared) : oV + kStages * kTile + 1024;
 static_assert(kSmem<true> <= 232448, "shared memory of a block");
 
 template <bool kBytes>
@@ -139,6 +139,20 @@ template <int kCount, bool kMore>
 __device__ __forceinline__ void set_registers() {
   if constexpr (kMore) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kCount) : "memory");
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCount) : "memory");
+}
+
+__device__ __forceinline__ uint32_t ld_shared1(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 ld_shared2(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared(uint32_t at, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 // (x0, x1) * a + b, two at a time.
@@ -163,12 +177,15 @@ __device__ __forceinline__ void st_global8(float* p, const float* v) {
 }
 
 // kShared: the call has a shared prefix. Without one every page is a sequence's own, and its P has both parts: told at run
-// time, as where there are both kinds, it costs 2 % (32 x 4 rows x 64 heads over 2000 tokens 63.3 -> 64.9 us).
+// time, as where there are both kinds, it costs 2 % (32 x 4 rows x 64 heads over 2000 tokens 63.3 -> 64.9 us). kBytes: the
+// call has nothing but a shared prefix, and no masks (what they and P's second part take of the registers costs 128 x 2 rows
+// behind 256 pages 287 -> 245 us, without being run).
 template <bool kRuns, bool kShared, bool kBytes>
 __global__ void __launch_bounds__(kThreads<kBytes>, 1)
     paged_prefix_kernel(PrefixArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v) {
-  static_assert(kRuns || !kBytes, "8 bits: one instance for shared and own pages");
+  static_assert(kRuns || !kBytes, "8 bits: runs' descriptions always go round");
+  constexpr bool kOwn = kRuns && !(kBytes && kShared);  // there are sequences' own pages
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = kBytes ? smem_raw
                          : reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -195,20 +212,20 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
       for (int j = 0; j < 4; ++j) mbar_init(&sh.pair[i][j], 2);
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sh.kv_full[i], kBytes ? kConverters : 1);
+      mbar_init(&sh.kv_full[i], kBytes ? 2 * kConverters : 1);
       mbar_init(&sh.k_empty[i], 1);
       mbar_init(&sh.v_empty[i], 1);
     }
     if (kRuns) {
       for (int i = 0; i < 2; ++i) {
         mbar_init(&sh.run_full[i], 1);
-        mbar_init(&sh.run_empty[i], kBytes ? 17 + kConverters : 19);
-        mbar_init(&sh.k_full[i], kBytes ? kConverters : 1);
+        mbar_init(&sh.run_empty[i], kBytes ? 17 + 2 * kConverters : 19);
+        mbar_init(&sh.k_full[i], kBytes ? 2 * kConverters : 1);
         mbar_init(&sh.v_clean[i], 1);
       }
     }
     if (kBytes) {
-      for (int i = 0; i < kRawStages; ++i) {
+      for (int i = 0; i < 2 * kRaw; ++i) {
         mbar_init(&sh.raw_full[i], 1);
         mbar_init(&sh.raw_empty[i], kConverters);
       }
@@ -240,9 +257,10 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
   auto next_run = [&](Run& run) {
     if constexpr (kRuns) {
       if (!mbar_wait(&sh.run_full[n_run & 1], (n_run >> 1) & 1, err, 1505)) return false;
-      run = sh.run[n_run & 1];
+      const Run& next = sh.run[n_run & 1];
       ++n_run;
-      return run.pages > 0;
+      if (!kBytes) run = next;  // (kBytes: used where it lies, as registers are short; run_done gives it back)
+      return next.pages > 0;
     } else {
       if (u >= u_end) return false;
       const int g = u / a.prefix, stop = min(u_end, (g + 1) * a.prefix);
@@ -270,8 +288,8 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
     return (page * a.G + run.g) * 128;
   };
 
-  // (kBytes) Of the 61,440 registers that the block starts with, the softmax gets 96 a thread.
-  static_assert(!kBytes || 512 * 96 + 128 * (56 + 40) <= 768 * 80, "registers of a block");
+  // (kBytes) Of the 64,512 registers that the block starts with, the softmax gets 88 a thread.
+  static_assert(!kBytes || 512 * 88 + 128 * (56 + 2 * 48) <= 896 * 72, "registers of a block");
   if (warp < 4) {
     if constexpr (kBytes) set_registers<56, false>();
   if (warp == 0) {
@@ -338,17 +356,19 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
       auto more = [&] { return u < u_end || second || id < items; };  // what step 3 of the last one leaves to be asked for
       for (int s = 0; s < 3; ++s) find(now, s);
       int n_run = 0;
-      uint32_t kc = 0, rc = 0;  // pages; half tiles of codes
+      uint32_t kc = 0;
       bool ok = true;
-      // a tile of codes, whose first vector is `at`, and their powers of two
-      auto load_codes = [&](const uint8_t* codes, const uint8_t* exps, int at) {
-        for (int h = 0; h < 2 && ok; ++h, ++rc) {
-          const int rs = rc % kRawStages;
-          ok = mbar_wait(&sh.raw_empty[rs], ((rc / kRawStages) & 1) ^ 1, err, 1507);
+      // the page's codes of K or V whose first vector is `at`, in halves, and their powers of two
+      auto load_codes = [&](bool values, int at) {
+        const uint8_t* codes = (values ? static_cast<const uint8_t*>(a.V) : a.K) + (size_t)at * 128;
+        const uint8_t* exps = (values ? a.V_exp : a.K_exp) + at;
+        for (int h = 0; h < 2 && ok; ++h) {
+          const int bar = values ? kRaw + h : h;
+          ok = mbar_wait(&sh.raw_empty[bar], (kc & 1) ^ 1, err, 1507);
           if (ok && lane == 0) {
-            mbar_arrive_expect_tx(&sh.raw_full[rs], kRaw + kRawRows);
-            bulk_load(smem + oRaw + rs * kRaw, codes + ((size_t)at + h * kRawRows) * 128, kRaw, &sh.raw_full[rs]);
-            bulk_load(smem + oExp + rs * kRawRows, exps + at + h * kRawRows, kRawRows, &sh.raw_full[rs]);
+            mbar_arrive_expect_tx(&sh.raw_full[bar], kHalf + kHalfKeys);
+            bulk_load(smem + (values ? oRawV : oRawK) + h * kHalf, codes + h * kHalf, kHalf, &sh.raw_full[bar]);
+            bulk_load(smem + (values ? oExpV : oExpK) + h * kHalfKeys, exps + h * kHalfKeys, kHalfKeys, &sh.raw_full[bar]);
           }
           __syncwarp();
         }
@@ -376,7 +396,7 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
           const int st = kc % kStages, at = __shfl_sync(0xffffffffu, y, page & 31) + other;
           const uint32_t par = ((kc / kStages) & 1) ^ 1;
           if constexpr (kBytes) {
-            load_codes(a.K, a.K_exp, at);
+            load_codes(false, at);
             if (!ok) break;
           } else {
             if (!mbar_wait(&sh.k_empty[st], par, err, 1503)) { ok = false; break; }
@@ -394,7 +414,7 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
             }
           }
           __syncwarp();
-          if constexpr (kBytes) load_codes(static_cast<const uint8_t*>(a.V), a.V_exp, at);
+          if constexpr (kBytes) load_codes(true, at);
           if (step < 3) find(next, step++);
         }
         ++n_run;
@@ -481,15 +501,17 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
           umma_bf16_ts_w(d, p + (ks >> 2) * 64 + (ks & 3) * 8, va + ks * (2048 >> 4), hi, id_o, ks > 0 ? 1u : (uint32_t)acc);
-        if (kRuns && own)
+        if (kRuns && !kBytes && own)
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
             umma_bf16_ts_w(d, p + (ks >> 2) * 64 + 32 + (ks & 3) * 8, va + ks * (2048 >> 4), hi, id_o, 1u);
       };
       // pages and runs of each tile (the second one has none in a run of few rows)
       uint32_t pages_of[2] = {0, 0}, runs_of[2] = {0, 0};
-      Run run;
-      for (int seg = 0; ok && next_run(run); ++seg) {
+      Run copy;
+      for (int seg = 0; ok && next_run(copy); ++seg) {
+        if (kBytes) copy = sh.run[(n_run - 1) & 1];
+        const Run& run = copy;
         run_done(true);
         const bool twin = kRuns && run.twin;
         const int pages = run.pages, last_t = !kRuns || twin || run.rows > tile_rows, streams = twin ? 2 : 1;
@@ -556,7 +578,7 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
         const int streams = run.twin ? 2 : 1;
         int y = 0;
         if (warp == 2) y = table_row(run, lane);
-        else if (lane < kConverters) sh.odd[(n_run - 1) & 1][lane] = 0;
+        else if (lane < 2 * kConverters) sh.odd[(n_run - 1) & 1][lane] = 0;
         __syncwarp();
         for (int i = 0; i < run.pages * streams; ++i, ++kc) {
           const int st = kc % kStages, page = run.twin ? i >> 1 : i, other = run.twin ? i & 1 : 0;
@@ -608,31 +630,34 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
   } else if (kBytes && warp >= 20) {
     // ---------------------------------------------------------------- codes to bf16 tiles
     if constexpr (kBytes) {
-      set_registers<40, false>();
-      // Eight threads a key, 16 codes each: a warp takes four keys at a time. A thread's two 16-byte pieces go into one of
-      // the tile's 64-column chunks; the upper half's threads write theirs the other way round, so that the eight threads
-      // of a key meet in no bank.
-      const int piece = lane & 7, key_lane = (warp - 20) * 4 + (lane >> 3);
-      const uint32_t chunk = (piece >> 2) * kChunk;
-      const int c0 = (piece & 3) * 2 + (piece >> 2), c1 = c0 ^ 1;
-      uint32_t kc = 0, rc = 0;
-      Run run;
+      set_registers<48, false>();
+      // Eight threads a key, 16 codes each: a warp takes four keys at a time. A thread's two halves go into one of the
+      // tile's 64-column chunks; the upper chunk's threads take theirs the other way round, so that the eight threads of a
+      // key meet in no bank. (Addresses in shared memory, 32 bits, with what does not change added up before.)
+      const int half = (warp - 20) / kConverters, key0 = half * kHalfKeys + (warp & (kConverters - 1)) * 4 + (lane >> 3);
+      const int piece = lane & 7, up = piece >> 2, c0 = (((piece & 3) * 2 + up) ^ (key0 & 7)) << 4;
+      uint32_t kc = 0;
+      Run none;
       bool ok = true;
-      // behind, own: keys from `behind` on become zeros, NaN among those from `own` on too; returns whether there were any
-      auto convert = [&](uint8_t* tile, int own, int behind) {
+      while (ok && next_run(none)) {
+        const Run& run = sh.run[(n_run - 1) & 1];
+        const int tiles = run.twin ? run.pages * 2 : run.pages;
         bool odd = false;
-        for (int h = 0; h < 2 && ok; ++h, ++rc) {
-          const int rs = rc % kRawStages;
-          ok = mbar_wait(&sh.raw_full[rs], (rc / kRawStages) & 1, err, 1508);
-          if (!ok) break;
-          const uint8_t* raw = smem + oRaw + rs * kRaw + piece * 16;
-          const uint8_t* exps = smem + oExp + rs * kRawRows;
+        // this half of the CTA's tile kc of K or V; keys from `behind` on become zeros, NaN among those from `own` on too
+        auto make_half = [&](auto of_values, int own, int behind) {
+          constexpr bool values = decltype(of_values)::value;
+          const int st = kc % kStages, bar = (values ? kRaw : 0) + half;
+          if (!mbar_wait(values ? &sh.v_empty[st] : &sh.k_empty[st], ((kc / kStages) & 1) ^ 1, err, values ? 1504 : 1503)) return false;
+          if (!mbar_wait(&sh.raw_full[bar], kc & 1, err, values ? 1509 : 1508)) return false;
+          const uint8_t* const raw = smem + (values ? oRawV : oRawK) + key0 * 128 + piece * 16;
+          const uint8_t* const exps = smem + (values ? oExpV : oExpK) + key0;
+          uint8_t* const tile = smem + (values ? oV : oK) + st * kTile + up * kChunk + key0 * 128;
 #pragma unroll
-          for (int i = 0; i < kRawRows / 16; ++i) {
-            const int row = i * 16 + key_lane, key = h * kRawRows + row;
-            uint4 v = *reinterpret_cast<const uint4*>(raw + row * 128);
-            const float pow2 = key < behind ? exp_value(exps[row]) : 0.f;
-            if (key >= own) {
+          for (int j = 0; j < kHalfKeys; j += 4 * kConverters) {
+            uint4 v = *reinterpret_cast<const uint4*>(raw + j * 128);
+            uint32_t byte = exps[j];
+            const int key = key0 + j;
+            if (kOwn && values && key >= own) {
               // (0x7f, the only code that is not finite, plus 1 has the top bit)
               auto clean = [&](uint32_t& w) {
                 const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
@@ -640,46 +665,41 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
                 w = key < behind ? w & ~((nan >> 7) * 0xffu) : 0u;
               };
               clean(v.x); clean(v.y); clean(v.z); clean(v.w);
+              if (key >= behind) byte = 0;
             }
+            const float pow2 = exp_value(byte);
             const uint4 lo = eight_bf16(make_uint2(v.x, v.y), pow2), hi = eight_bf16(make_uint2(v.z, v.w), pow2);
-            const bool up = piece >> 2;
-            *reinterpret_cast<uint4*>(tile + chunk + sw128_off(key, c0)) = up ? hi : lo;
-            *reinterpret_cast<uint4*>(tile + chunk + sw128_off(key, c1)) = up ? lo : hi;
+            *reinterpret_cast<uint4*>(tile + j * 128 + c0) = up ? hi : lo;
+            *reinterpret_cast<uint4*>(tile + j * 128 + (c0 ^ 16)) = up ? lo : hi;
           }
+          if (kOwn && values) {
+            odd = __any_sync(0xffffffffu, odd);
+            if (lane == 0) sh.odd[(n_run - 1) & 1][warp - 20] = odd;
+          }
+          fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.raw_empty[rs]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        return odd;
-      };
-      while (ok && next_run(run)) {
-        const int streams = run.twin ? 2 : 1, slot = (n_run - 1) & 1;
-        if (lane == 0) sh.odd[slot][warp - 20] = 0;
-        __syncwarp();
-        for (int i = 0; i < run.pages * streams; ++i, ++kc) {
-          const int st = kc % kStages, page = run.twin ? i >> 1 : i;
-          const uint32_t par = ((kc / kStages) & 1) ^ 1;
-          if (!mbar_wait(&sh.k_empty[st], par, err, 1503)) { ok = false; break; }
-          convert(smem + oK + st * kTile, 128, 128);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive(&sh.k_full[st]);
-          if (!mbar_wait(&sh.v_empty[st], par, err, 1504)) { ok = false; break; }
-          const int token0 = (run.first + page) * 128;
-          const bool masked = page >= run.masked;
-          const int own = masked ? max(0, run.pos + 1 - token0) : 128;
-          const int behind = masked ? min(128, max(0, run.pos + run.rows - token0)) : 128;
-          if (convert(smem + oV + st * kTile, min(own, behind), behind)) sh.odd[slot][warp - 20] = 1;
-          if (!ok) break;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.kv_full[st]);
+          if (lane == 0) {
+            mbar_arrive(&sh.raw_empty[bar]);
+            mbar_arrive(values ? &sh.kv_full[st] : &sh.k_full[st]);
+          }
+          return true;
+        };
+        for (int i = 0; i < tiles && ok; ++i, ++kc) {
+          const int page = run.twin ? i >> 1 : i;
+          int own = 128, behind = 128;
+          if (kOwn && page >= run.masked) {
+            const int token0 = (run.first + page) * 128;
+            behind = min(128, max(0, run.pos + run.rows - token0));
+            own = min(behind, max(0, run.pos + 1 - token0));
+          }
+          ok = make_half(std::false_type(), 128, 128) && make_half(std::true_type(), own, behind);
         }
         run_done(false);
       }
     }
   } else {
     // ---------------------------------------------------------------- softmax (thread = one head of one new row, 64 keys)
-    if constexpr (kBytes) set_registers<96, true>();
+    if constexpr (kBytes) set_registers<88, true>();
     const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;
     const int quarter = warp & 3;
     const int lrow = quarter * 32 + lane;
@@ -700,8 +720,9 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
     }
     uint32_t kc = 0, pair_ph = 0;
     bool ok = true;
-    Run run;
-    for (int seg = 0; ok && next_run(run);) {
+    Run copy;
+    for (int seg = 0; ok && next_run(copy);) {
+      const Run& run = kBytes ? sh.run[(n_run - 1) & 1] : copy;
       if (kRuns && t && !run.twin && run.rows <= tile_rows) {  // no second tile
         run_done(false);
         continue;
@@ -717,7 +738,7 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
         tmem_ld32_max(s_at, *reinterpret_cast<float(*)[32]>(sv), mq[0]);
         tmem_ld32_max(s_at + 32, *reinterpret_cast<float(*)[32]>(sv + 32), mq[1]);
         tmem_wait_ld();
-        if (kRuns && c >= run.masked) {
+        if (kOwn && c >= run.masked) {
           const int seen = run.pos + in + 1 - (run.first + c) * 128 - half * 64;  // keys of this warp's before the row's end
           mq[0] = mq[1] = -INFINITY;
 #pragma unroll
@@ -733,7 +754,7 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
         auto write_p = [&]() {
           float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
           const float base = m_run == -INFINITY ? 0.f : m_run;  // (nothing but -infinity so far: exp2(-inf - 0) = 0)
-          if (kRuns && (!kShared || run.own)) {
+          if (kRuns && !kBytes && (!kShared || run.own)) {
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
               uint32_t pk[8], rest[8];
@@ -849,9 +870,10 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
       const int group = run.g + (twin ? t : 0);
       const size_t at = ((size_t)run.slot * a.N + row) * a.Hq + group * a.hg + lrow % a.hg;
       bool odd = false;
-      if (kRuns && run.own) {
+      if (kOwn && run.own) {
         const int* found = sh.odd[(n_run - 1) & 1];
-        odd = found[0] | found[1] | found[2] | found[3];
+#pragma unroll
+        for (int i = 0; i < 2 * kConverters; ++i) odd |= found[i] != 0;
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;  // (a run behind the row's end, or scores of -infinity)
       float* dst = a.part_o + at * 128 + half * 64;
@@ -954,8 +976,8 @@ cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, con
   a.rslots = L.rslots;
   a.pslots = L.pslots;
   if (c.bytes())
-    return L.prefix ? launch_prefix<true, true, true>(a, L.n_flags, mq, maps, st)
-                    : launch_prefix<true, false, true>(a, L.n_flags, mq, maps, st);
+    return L.run_rows ? launch_prefix<true, false, true>(a, L.n_flags, mq, maps, st)
+                      : launch_prefix<true, true, true>(a, L.n_flags, mq, maps, st);
   if (!L.run_rows) return launch_prefix<false, true, false>(a, L.n_flags, mq, maps, st);
   if (L.prefix) return launch_prefix<true, true, false>(a, L.n_flags, mq, maps, st);
   return launch_prefix<true, false, false>(a, L.n_flags, mq, maps, st);

@@ -104,10 +104,16 @@ class Batch(ref.Batch):
         return shape, cache, t
 
 
+def tiles(b):
+    """Whether the full attention may take 128-row tiles, where P is one bf16 (half a step of it: 2^-8): a shared prefix, or
+    more than nine columns (rows x heads) a sequence."""
+    return b.prefix > 0 or b.N * b.hg > 9 * b.S
+
+
 def check_attention(b, rows, heads, O, LSE, blocks_of, bf16_p=False):
     """paged_ref.check_attention with the bounds of the calls over 8 bits: a score's and the sums' as there; P is held in
     fp16 as 2^15 p 2^f / max(p 2^f), f its token's exponent of V, that is with 2^-11 of itself, and 2^-25 (half of fp16's
-    last step) at least: 2^-40 of max(p 2^f) times a code (448 at most) for each token. Where the shared-prefix path may run
+    last step) at least: 2^-40 of max(p 2^f) times a code (448 at most) for each token. Where 128-row tiles may be taken
     (`bf16_p`), P is one bf16: 2^-8."""
     import torch
 

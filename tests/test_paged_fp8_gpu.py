@@ -537,7 +537,7 @@ def _all(b):
 def _check_dense(b, O, LSE):
     rows = range(b.n) if b.n < 30 else range(0, b.n, 7)
     heads = range(b.Hq) if b.Hq <= 8 else range(0, b.Hq, 5)
-    ref8.check_attention(b, rows, heads, O, LSE, _all(b), bf16_p=b.prefix > 0)
+    ref8.check_attention(b, rows, heads, O, LSE, _all(b), bf16_p=ref8.tiles(b))
     _check_padding(b, O, LSE)
 
 
