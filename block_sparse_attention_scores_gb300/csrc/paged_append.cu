@@ -37,6 +37,21 @@ constexpr int kThreads = 256;
 constexpr int kInFlight = 2;  // items a thread loads at a time
 constexpr int kMaxRows = 4;   // rows of a block
 constexpr int kPairs = 64 + 32;
+// Eight pairs' turns lie together, 80 bytes from the next eight's: the eight threads that rotate a vector meet in no bank
+// (64 bytes apart they met four at a time).
+constexpr int kTurns = kPairs / 8 * 10;
+__device__ __forceinline__ int turn_at(int pair) { return pair + pair / 8 * 2; }
+struct Turns {
+  float2 c[8];
+  __device__ __forceinline__ explicit Turns(const float2* at) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = reinterpret_cast<const float4*>(at)[i];
+      c[2 * i] = make_float2(v.x, v.y);
+      c[2 * i + 1] = make_float2(v.z, v.w);
+    }
+  }
+};
 constexpr int kMaxAxes = 8;
 
 struct AppendArgs {
@@ -67,7 +82,9 @@ __device__ __forceinline__ void item_pieces(int j, int rot, int interleaved, int
   pair = turned ? 8 * j : -1;
 }
 
-__device__ __forceinline__ void rotate(uint4& x, uint4& y, const float2* cs, int interleaved) {
+__device__ __forceinline__ void rotate(uint4& x, uint4& y, const float2* at, int interleaved) {
+  const Turns turns(at);
+  const float2* cs = turns.c;
   uint32_t* u = reinterpret_cast<uint32_t*>(&x);
   uint32_t* v = reinterpret_cast<uint32_t*>(&y);
   if (interleaved) {
@@ -90,7 +107,7 @@ __device__ __forceinline__ void rotate(uint4& x, uint4& y, const float2* cs, int
 }
 
 // The rotated values of both pieces (pair < 0: as they are), not rounded: the first one's eight, then the second one's.
-__device__ __forceinline__ void rotated_values(const uint4& x, const uint4& y, int pair, const float2* cs, int interleaved,
+__device__ __forceinline__ void rotated_values(const uint4& x, const uint4& y, int pair, const float2* at, int interleaved,
                                                float (&v)[16]) {
   const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
@@ -99,55 +116,77 @@ __device__ __forceinline__ void rotated_values(const uint4& x, const uint4& y, i
     v[2 * i + 1] = hi_f(u[i]);
   }
   if (pair < 0) return;
+  const Turns turns(at);
+  const float2* cs = turns.c;
+  if (interleaved) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int p = interleaved ? 2 * i : i, q = interleaved ? 2 * i + 1 : 8 + i;
-    const float2 c = cs[i];
-    const float a = v[p], b = v[q];
-    v[p] = a * c.x - b * c.y;
-    v[q] = b * c.x + a * c.y;
+    for (int i = 0; i < 8; ++i) {
+      const float2 c = cs[i];
+      const float a = v[2 * i], b = v[2 * i + 1];
+      v[2 * i] = a * c.x - b * c.y;
+      v[2 * i + 1] = b * c.x + a * c.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 c = cs[i];
+      const float a = v[i], b = v[8 + i];
+      v[i] = a * c.x - b * c.y;
+      v[8 + i] = b * c.x + a * c.y;
+    }
   }
 }
 
+// What an item is: kind 0 Q, 1 K, 2 V, 3 q_idx, 4 k_idx, 7 none; its vector, and pieces a and b of it, rotated from `pair` on.
+struct What {
+  int kind, row, vec, a, b, pair;
+};
 struct Piece {
   uint4 x, y;
-  int row, kind, vec, a, b, pair;  // kind -1: none; 0 Q, 1 K, 2 V, 3 q_idx, 4 k_idx
+  uint32_t what;  // packed (kind 3 bits, row 2, item of the vector 3, vector 24), so that the values have the registers
 };
+__device__ __forceinline__ What what_of(const AppendArgs& a, uint32_t what) {
+  What w;
+  w.kind = what >> 29;
+  w.row = what >> 27 & 3;
+  w.vec = what & 0xffffff;
+  item_pieces(what >> 24 & 7, w.kind == 2 ? 0 : w.kind >= 3 ? a.r.rot_idx : a.r.rot, a.r.interleaved, w.a, w.b, w.pair);
+  return w;
+}
 
 // Item `it` of the block's rows: which vector's pieces, and their loads.
 __device__ __forceinline__ void load_piece(const AppendArgs& a, int r0, int it, Piece& p) {
-  p.kind = -1;
-  p.row = 0;
+  p.what = 7u << 29;
   const int row = (int)(((float)it + 0.5f) * a.inv_items);
   it -= row * a.items;
   if (row >= a.rows || r0 + row >= a.N) return;
-  p.row = row;
+  int kind;
   const __nv_bfloat16* src;
   const size_t r = r0 + row;
   if (it < a.n_q) {
-    p.kind = 0;
+    kind = 0;
     src = static_cast<const __nv_bfloat16*>(a.r.Q) + r * a.r.ld_Q;
   } else if ((it -= a.n_q) < a.n_k) {
-    p.kind = 1;
+    kind = 1;
     src = static_cast<const __nv_bfloat16*>(a.r.K) + r * a.r.ld_K;
   } else if ((it -= a.n_k) < a.n_k) {
-    p.kind = 2;
+    kind = 2;
     src = static_cast<const __nv_bfloat16*>(a.r.V) + r * a.r.ld_V;
   } else if ((it -= a.n_k) < a.n_qi) {
-    p.kind = 3;
+    kind = 3;
     src = static_cast<const __nv_bfloat16*>(a.r.q_idx) + r * a.r.ld_q_idx;
   } else {
     it -= a.n_qi;
     if (it >= a.n_ki) return;  // (past the row's own items)
-    p.kind = 4;
+    kind = 4;
     src = static_cast<const __nv_bfloat16*>(a.r.k_idx) + r * a.r.ld_k_idx;
   }
-  const bool idx = p.kind >= 3;
-  p.vec = idx ? it >> 2 : it >> 3;
-  item_pieces(idx ? it & 3 : it & 7, p.kind == 2 ? 0 : (idx ? a.r.rot_idx : a.r.rot), a.r.interleaved, p.a, p.b, p.pair);
-  const uint4* v = reinterpret_cast<const uint4*>(src + (size_t)p.vec * (idx ? 64 : 128));
-  p.x = v[p.a];
-  p.y = v[p.b];
+  const bool idx = kind >= 3;
+  p.what = (uint32_t)kind << 29 | row << 27 | (idx ? it & 3 : it & 7) << 24 | (idx ? it >> 2 : it >> 3);
+  const What w = what_of(a, p.what);
+  const uint4* v = reinterpret_cast<const uint4*>(src + (size_t)w.vec * (idx ? 64 : 128));
+  p.x = v[w.a];
+  p.y = v[w.b];
 }
 
 // Place of row r in a sequence of length len with `left` rows from r on, or a code for what is wrong with it.
@@ -172,19 +211,33 @@ __device__ __forceinline__ int pair_axis(const AppendArgs& a, int t, bool& bad) 
 
 // A vector's codes and its power of two into the cache, by whole warps. `code`: this thread has a piece of such a vector,
 // of which eight neighbouring threads (four: an index key) have one each. cs: the row's turns.
-__device__ __forceinline__ void quantise_piece(const AppendArgs& a, const Piece& e, bool code, int pos, int page,
+__device__ __forceinline__ void quantise_piece(const AppendArgs& a, const Piece& p, const What& e, bool code, int pos, int page,
                                                const float2* cs) {
   const bool idx = e.kind == 4;
   float v[16], most = 0.f;
   if (code && pos >= 0) {
-    rotated_values(e.x, e.y, e.pair, cs + (idx ? 64 : 0) + e.pair, a.r.interleaved, v);
+    rotated_values(p.x, p.y, e.pair, cs + turn_at((idx ? 64 : 0) + max(e.pair, 0)), a.r.interleaved, v);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) most = finite_max(most, v[i]);
+    for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(v[i]));  // (leaves NaN out)
   }
+  const auto over_vector = [&] {
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-    const float other = __shfl_xor_sync(0xffffffffu, most, o);
-    if (o < 4 || !idx) most = fmaxf(most, other);
+    for (int o = 1; o < 8; o <<= 1) {
+      const float other = __shfl_xor_sync(0xffffffffu, most, o);
+      if (o < 4 || !idx) most = fmaxf(most, other);
+    }
+  };
+  over_vector();
+  if (__any_sync(0xffffffffu, most == INFINITY)) {  // they become NaN and count for nothing in the scale
+    most = 0.f;
+    if (code && pos >= 0) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (!(fabsf(v[i]) < INFINITY)) v[i] = NAN;
+        most = fmaxf(most, fabsf(v[i]));
+      }
+    }
+    over_vector();
   }
   if (!code || pos < 0 || page < 0) return;
   const int byte = exp_byte(most), slot = pos & 127;
@@ -199,7 +252,7 @@ __device__ __forceinline__ void quantise_piece(const AppendArgs& a, const Piece&
 }
 
 template <bool kBytes>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, kBytes ? 4 : 5) paged_append_kernel(AppendArgs a) {
   const int half = a.r.rot / 2, half_idx = a.r.rot_idx / 2;
   if (a.report && blockIdx.x == gridDim.x - 1) {
     int bad = 0;
@@ -220,7 +273,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
     return;
   }
   __shared__ unsigned long long turns_of[kPairs];  // frequency as a fraction of a turn per position
-  __shared__ float2 turn[kMaxRows][kPairs];        // cos, sin of a row's pairs: d, then d_idx
+  __shared__ __align__(16) float2 turn[kMaxRows][kTurns];  // cos, sin of a row's pairs: d, then d_idx
   __shared__ int pos_of[kMaxRows], page_of[kMaxRows];  // -1: no row, or not to be written
   __shared__ int axis_of[kPairs], at_axis[kMaxRows][kMaxAxes];  // a pair's axis, and a row's positions on each
   const int r0 = blockIdx.x * a.rows, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -263,7 +316,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
       const unsigned long long phase = turns_of[t] * (unsigned long long)at;
       float sn, cs;
       sincospif((float)(int)(uint32_t)(phase >> 32) * 4.656612873077393e-10f, &sn, &cs);  // the top 32 bits, in half turns
-      turn[row][t] = make_float2(cs, sn);
+      turn[row][turn_at(t)] = make_float2(cs, sn);
     }
   }
   __syncthreads();
@@ -275,17 +328,17 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
     }
 #pragma unroll
     for (int z = 0; z < kInFlight; ++z) {
-      Piece& e = p[z];
+      const What e = what_of(a, p[z].what);
       if constexpr (kBytes) {
         const bool code = e.kind == 1 || e.kind == 2 || e.kind == 4;
-        if (__any_sync(0xffffffffu, code)) quantise_piece(a, e, code, pos_of[e.row], page_of[e.row], turn[e.row]);
+        if (__any_sync(0xffffffffu, code)) quantise_piece(a, p[z], e, code, pos_of[e.row], page_of[e.row], turn[e.row]);
         if (code) continue;
       }
-      if (e.kind < 0) continue;
+      if (e.kind == 7) continue;
       const int pos = pos_of[e.row], page = page_of[e.row];
       if (pos < 0) continue;
       const bool idx = e.kind >= 3;
-      if (e.pair >= 0) rotate(e.x, e.y, turn[e.row] + (idx ? 64 : 0) + e.pair, a.r.interleaved);
+      if (e.pair >= 0) rotate(p[z].x, p[z].y, turn[e.row] + turn_at((idx ? 64 : 0) + e.pair), a.r.interleaved);
       const size_t r = r0 + e.row;
       __nv_bfloat16* dst;
       if (e.kind == 0) {
@@ -300,8 +353,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
         else
           dst = static_cast<__nv_bfloat16*>(e.kind == 1 ? a.K : a.V) + (((size_t)page * a.G + e.vec) * 128 + slot) * 128;
       }
-      reinterpret_cast<uint4*>(dst)[e.a] = e.x;
-      reinterpret_cast<uint4*>(dst)[e.b] = e.y;
+      reinterpret_cast<uint4*>(dst)[e.a] = p[z].x;
+      reinterpret_cast<uint4*>(dst)[e.b] = p[z].y;
     }
   }
 }

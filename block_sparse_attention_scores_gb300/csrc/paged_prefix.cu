@@ -288,10 +288,9 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
     return (page * a.G + run.g) * 128;
   };
 
-  // (kBytes) Of the 64,512 registers that the block starts with, the softmax gets 88 a thread.
-  static_assert(!kBytes || 512 * 88 + 128 * (56 + 2 * 48) <= 896 * 72, "registers of a block");
+  // (kBytes) The block starts with 72 registers a thread; the warps that make tiles give some of theirs to the softmax.
+  static_assert(!kBytes || 512 * 88 + 128 * (72 + 2 * 40) <= 896 * 72, "registers of a block");
   if (warp < 4) {
-    if constexpr (kBytes) set_registers<56, false>();
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
     tma_prefetch_desc(&map_q);
@@ -630,7 +629,7 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
   } else if (kBytes && warp >= 20) {
     // ---------------------------------------------------------------- codes to bf16 tiles
     if constexpr (kBytes) {
-      set_registers<48, false>();
+      set_registers<40, false>();
       // Eight threads a key, 16 codes each: a warp takes four keys at a time. A thread's two halves go into one of the
       // tile's 64-column chunks; the upper chunk's threads take theirs the other way round, so that the eight threads of a
       // key meet in no bank. (Addresses in shared memory, 32 bits, with what does not change added up before.)
