@@ -96,9 +96,10 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
       // memory is busy while the tensor core is. Both are estimated (a page takes a pair of tiles 2,750 cycles, a row tile
       // 2,000; own pages: half of what the table holds), and the prefix has half of the SMs at least, lest a poor estimate
       // make it the longer one. 64 sequences behind 32K tokens with up to 2K of their own: 112 us one after the other,
-      // 100 with two thirds, 94 with half, 102 with 0.35 of the SMs; 100 sequences with 2000 each: 67, 49, 48, 48.
-      const double own = (double)tiles * p.G * (p.max_blocks - p.prefix + 1) / 2 * 2000;
-      const double shared = (double)units * L.pairs * 2750;
+      // 100 with two thirds, 94 with half, 102 with 0.35 of the SMs; 100 sequences with 2000 each: 67, 49, 48, 48. (In 8 bits
+      // 3,500 and 1,200 cycles: the first of these 95 -> 91 us.)
+      const double own = (double)tiles * p.G * (p.max_blocks - p.prefix + 1) / 2 * (bytes ? 1200 : 2000);
+      const double shared = (double)units * L.pairs * (bytes ? 3500 : 2750);
       const int sms = L.run_rows ? kCutSms : (int)(kCutSms * std::max(0.5, shared / (shared + own)));
       L.teams = std::min(units, std::max(1, sms / L.pairs));
       L.n_flags = std::max(L.n_flags, L.teams * L.pairs);

@@ -15,8 +15,10 @@
 // neighbours), one thread each, whose loads are on their way before the row's
 // place and angles are looked up.
 //
-// Measured: 32,764 rows of 32 + 2 x 8 heads (881 MB) 150 us, 5.9 TB/s, 0.88 of a
-// plain copy; one row 3 us in a graph, which is a launch's time.
+// Measured: 32,764 rows of 32 + 2 x 8 heads (881 MB) 139 us, 6.3 TB/s, 0.93 of a
+// plain copy; one row 3 us in a graph, which is a launch's time. Into 8 bits 812 MB
+// in 164 us (0.73): twice the instructions for K and V, and what bounds is issuing
+// them.
 //
 // Positions with several axes (kind of token: time, height, width): a pair turns
 // with the position on its own axis, position[r][axis[i]] * f, while the row's
@@ -33,7 +35,6 @@
 namespace msa {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kInFlight = 2;  // items a thread loads at a time
 constexpr int kMaxRows = 4;   // rows of a block
 constexpr int kPairs = 64 + 32;
@@ -155,36 +156,35 @@ __device__ __forceinline__ What what_of(const AppendArgs& a, uint32_t what) {
 }
 
 // Item `it` of the block's rows: which vector's pieces, and their loads.
-__device__ __forceinline__ void load_piece(const AppendArgs& a, int r0, int it, Piece& p) {
+__device__ __forceinline__ void load_piece(const AppendArgs& a, long long r0, int it, Piece& p) {
   p.what = 7u << 29;
   const int row = (int)(((float)it + 0.5f) * a.inv_items);
   it -= row * a.items;
   if (row >= a.rows || r0 + row >= a.N) return;
   int kind;
   const __nv_bfloat16* src;
-  const size_t r = r0 + row;
   if (it < a.n_q) {
     kind = 0;
-    src = static_cast<const __nv_bfloat16*>(a.r.Q) + r * a.r.ld_Q;
+    src = static_cast<const __nv_bfloat16*>(a.r.Q) + r0 * a.r.ld_Q + row * a.r.ld_Q;
   } else if ((it -= a.n_q) < a.n_k) {
     kind = 1;
-    src = static_cast<const __nv_bfloat16*>(a.r.K) + r * a.r.ld_K;
+    src = static_cast<const __nv_bfloat16*>(a.r.K) + r0 * a.r.ld_K + row * a.r.ld_K;
   } else if ((it -= a.n_k) < a.n_k) {
     kind = 2;
-    src = static_cast<const __nv_bfloat16*>(a.r.V) + r * a.r.ld_V;
+    src = static_cast<const __nv_bfloat16*>(a.r.V) + r0 * a.r.ld_V + row * a.r.ld_V;
   } else if ((it -= a.n_k) < a.n_qi) {
     kind = 3;
-    src = static_cast<const __nv_bfloat16*>(a.r.q_idx) + r * a.r.ld_q_idx;
+    src = static_cast<const __nv_bfloat16*>(a.r.q_idx) + r0 * a.r.ld_q_idx + row * a.r.ld_q_idx;
   } else {
     it -= a.n_qi;
     if (it >= a.n_ki) return;  // (past the row's own items)
     kind = 4;
-    src = static_cast<const __nv_bfloat16*>(a.r.k_idx) + r * a.r.ld_k_idx;
+    src = static_cast<const __nv_bfloat16*>(a.r.k_idx) + r0 * a.r.ld_k_idx + row * a.r.ld_k_idx;
   }
   const bool idx = kind >= 3;
   p.what = (uint32_t)kind << 29 | row << 27 | (idx ? it & 3 : it & 7) << 24 | (idx ? it >> 2 : it >> 3);
   const What w = what_of(a, p.what);
-  const uint4* v = reinterpret_cast<const uint4*>(src + (size_t)w.vec * (idx ? 64 : 128));
+  const uint4* v = reinterpret_cast<const uint4*>(src) + w.vec * (idx ? 8 : 16);
   p.x = v[w.a];
   p.y = v[w.b];
 }
@@ -242,8 +242,8 @@ __device__ __forceinline__ void quantise_piece(const AppendArgs& a, const Piece&
   if (!code || pos < 0 || page < 0) return;
   const int byte = exp_byte(most), slot = pos & 127;
   const float scale = exp_inverse(byte);
-  const size_t at = idx ? (size_t)page * 128 + slot : ((size_t)page * a.G + e.vec) * 128 + slot;
-  uint8_t* dst = static_cast<uint8_t*>(idx ? a.k_idx : e.kind == 1 ? a.K : a.V) + at * (idx ? 64 : 128);
+  const uint32_t at = (idx ? page : page * a.G + e.vec) * 128 + slot;  // (pages times groups are below 2^24)
+  uint8_t* dst = static_cast<uint8_t*>(idx ? a.k_idx : e.kind == 1 ? a.K : a.V) + (size_t)at * (idx ? 64 : 128);
   const uint2 lo = make_uint2(four_codes(v[0], v[1], v[2], v[3], scale), four_codes(v[4], v[5], v[6], v[7], scale));
   const uint2 hi = make_uint2(four_codes(v[8], v[9], v[10], v[11], scale), four_codes(v[12], v[13], v[14], v[15], scale));
   reinterpret_cast<uint2*>(dst)[e.a] = lo;
@@ -251,8 +251,8 @@ __device__ __forceinline__ void quantise_piece(const AppendArgs& a, const Piece&
   if (e.a == 0) (idx ? a.k_idx_exp : e.kind == 1 ? a.K_exp : a.V_exp)[at] = (uint8_t)byte;
 }
 
-template <bool kBytes>
-__global__ void __launch_bounds__(kThreads, kBytes ? 4 : 5) paged_append_kernel(AppendArgs a) {
+template <bool kBytes, int kThreads>
+__global__ void __launch_bounds__(kThreads, (kBytes ? 1024 : 1280) / kThreads) paged_append_kernel(AppendArgs a) {
   const int half = a.r.rot / 2, half_idx = a.r.rot_idx / 2;
   if (a.report && blockIdx.x == gridDim.x - 1) {
     int bad = 0;
@@ -294,7 +294,8 @@ __global__ void __launch_bounds__(kThreads, kBytes ? 4 : 5) paged_append_kernel(
         if (bad && !a.report) dev_fail(a.err, kDevBadIndex, 1203);
       }
     }
-  } else if (warp < a.rows) {  // the rows' sequences, positions and pages, a warp each
+  }
+  if (warp < a.rows) {  // the rows' sequences, positions and pages, a warp each
     const int r = r0 + warp;
     int pos = -1, page = -1;
     if (r < a.N && lane < a.r.axes) at_axis[warp][lane] = __ldg(a.r.positions + (size_t)r * a.r.axes + lane);
@@ -339,19 +340,19 @@ __global__ void __launch_bounds__(kThreads, kBytes ? 4 : 5) paged_append_kernel(
       if (pos < 0) continue;
       const bool idx = e.kind >= 3;
       if (e.pair >= 0) rotate(p[z].x, p[z].y, turn[e.row] + turn_at((idx ? 64 : 0) + e.pair), a.r.interleaved);
-      const size_t r = r0 + e.row;
+      const uint32_t r = r0 + e.row;  // (rows times heads are at most 2^28, pages times groups below 2^24)
       __nv_bfloat16* dst;
       if (e.kind == 0) {
-        dst = static_cast<__nv_bfloat16*>(a.r.Q_out) + (r * a.Hq + e.vec) * 128;
+        dst = static_cast<__nv_bfloat16*>(a.r.Q_out) + (size_t)(r * a.Hq + e.vec) * 128;
       } else if (e.kind == 3) {
-        dst = static_cast<__nv_bfloat16*>(a.r.q_idx_out) + (r * a.G + e.vec) * 64;
+        dst = static_cast<__nv_bfloat16*>(a.r.q_idx_out) + (size_t)(r * a.G + e.vec) * 64;
       } else {
         if (page < 0) continue;
         const int slot = pos & 127;
         if (e.kind == 4)
-          dst = static_cast<__nv_bfloat16*>(a.k_idx) + ((size_t)page * 128 + slot) * 64;
+          dst = static_cast<__nv_bfloat16*>(a.k_idx) + (size_t)(page * 128u + slot) * 64;
         else
-          dst = static_cast<__nv_bfloat16*>(e.kind == 1 ? a.K : a.V) + (((size_t)page * a.G + e.vec) * 128 + slot) * 128;
+          dst = static_cast<__nv_bfloat16*>(e.kind == 1 ? a.K : a.V) + (size_t)((uint32_t)(page * a.G + e.vec) * 128 + slot) * 128;
       }
       reinterpret_cast<uint4*>(dst)[e.a] = p[z].x;
       reinterpret_cast<uint4*>(dst)[e.b] = p[z].y;
@@ -360,6 +361,18 @@ __global__ void __launch_bounds__(kThreads, kBytes ? 4 : 5) paged_append_kernel(
 }
 
 }  // namespace
+
+template <bool kBytes, int kThreads>
+static cudaError_t launch_append(const PagedProb& p, AppendArgs& a, cudaStream_t st) {
+  // Rows for two rounds of a block's loads, so that its look-ups are shared, as long as every SM gets three blocks. 38,610
+  // rows of 4 + 2 x 4 heads take 97 us with one row a block and 57 with four; 6,710 rows of 64 + 2 x 8, whose blocks are long
+  // enough with one, 64 and 68; 2,400 rows of 8 + 2 x 2 heads 12 and 8.
+  a.rows = std::min(kMaxRows, std::max(1, 2 * kInFlight * kThreads / a.items));
+  while (a.rows > 1 && p.N < 3 * kCutSms * a.rows) --a.rows;
+  paged_append_kernel<kBytes, kThreads><<<(p.N + a.rows - 1) / a.rows + a.report, kThreads, 0, st>>>(a);
+  count_launches(1);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_paged_append(const PagedProb& p, const PagedCachePtrs& c, const RopeRows& r, uint8_t* ws,
                                 cudaStream_t st) {
@@ -388,11 +401,6 @@ cudaError_t launch_paged_append(const PagedProb& p, const PagedCachePtrs& c, con
   a.items = a.n_q + 2 * a.n_k + a.n_qi + a.n_ki;
   if (c.bytes()) a.items = (a.items + 7) / 8 * 8;
   a.inv_items = 1.f / (float)a.items;
-  // Rows for two rounds of a block's loads, so that its look-ups are shared, as long as every SM gets three blocks. 38,610
-  // rows of 4 + 2 x 4 heads take 97 us with one row a block and 57 with four; 6,710 rows of 64 + 2 x 8, whose blocks are long
-  // enough with one, 64 and 68; 2,400 rows of 8 + 2 x 2 heads 12 and 8.
-  a.rows = std::min(kMaxRows, std::max(1, 2 * kInFlight * kThreads / a.items));
-  while (a.rows > 1 && p.N < 3 * kCutSms * a.rows) --a.rows;
   // Few rows: a block of its own checks them and writes the error word, so that nothing has to clear it first (256 rows in
   // a graph: 3.0 us against 6.2 with a memset). For many rows it would be the last to end: 1024 sequences' rows 9.1 us
   // against 9.7, 2000 sequences' 16.8 against 12.3.
@@ -401,10 +409,12 @@ cudaError_t launch_paged_append(const PagedProb& p, const PagedCachePtrs& c, con
     const cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
     if (e != cudaSuccess) return e;
   }
-  (c.bytes() ? paged_append_kernel<true> : paged_append_kernel<false>)<<<(p.N + a.rows - 1) / a.rows + a.report, kThreads, 0,
-                                                                        st>>>(a);
-  count_launches(1);
-  return cudaGetLastError();
+  // Blocks of 128 threads for many long rows, whose waits for one another are shorter then: 32,764 rows of 32 + 2 x 8 heads
+  // take 146 us with 256 threads and 139 with 128 in bf16, 176 and 164 in 8 bits; but 64 of them 4.0 and 5.0 us in a graph, and
+  // 2,400 of 8 + 2 x 2 heads, of which a block has four, 8.4 and 10.4.
+  const bool small = !a.report && a.items >= 256;
+  if (c.bytes()) return small ? launch_append<true, 128>(p, a, st) : launch_append<true, 256>(p, a, st);
+  return small ? launch_append<false, 128>(p, a, st) : launch_append<false, 256>(p, a, st);
 }
 
 }  // namespace msa
