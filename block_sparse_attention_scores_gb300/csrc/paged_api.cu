@@ -67,17 +67,25 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
     // rows count, as nothing here tells them from others: the ninth column is for a pad of up to an eighth. Against eight
     // columns at a time: 32 sequences of 2 rows x 64 heads over 2000 tokens 63 -> 60 us, of 8 rows 135 -> 69, 300 rows x 32
     // heads over 4 groups and 8000 tokens 274 -> 64; the other way for one page (8 rows x 64 heads over 100 tokens 17 -> 10).
-    const bool runs = (long long)p.N * p.hg > 9LL * p.S && p.max_blocks - p.prefix > 1;
+    // In 8 bits a page of eight columns takes half the time, and one of the tiles' about as long: more than 20 columns a
+    // sequence (32 sequences over 2000 tokens, 64 heads over 8 groups, of 2 rows 70 us by tiles and 50, of 3 rows 69 and 71;
+    // 32 x 8 rows x 32 heads 70 and 84), unless all pages that are read, once for every eight columns, are 18 an SM at most
+    // (100 rows x 16 heads over 2 groups and 300 tokens, 600 of them, 24 and 13; 200 x 64 heads over 8 groups and 250, 3200,
+    // 28 and 40).
+    const long long tiles = std::max(p.N / L.tile_rows, std::min(p.S, p.N));
+    const bool runs = (long long)p.N * p.hg > (bytes ? 20LL : 9LL) * p.S && p.max_blocks - p.prefix > 1 &&
+                      !(bytes && tiles * p.G * (p.max_blocks - p.prefix) <= 2800);
     // A shared prefix of ten pages an SM (13 where a sequence has several tiles of eight columns), counted for every such
     // tile, is read as own pages: it stays in L2, and two kernels do with it what four do. 4 sequences of 32 heads over 8
     // groups behind 16 pages 15 us against 19, 16 behind 8 pages 14 and 19, 8 of 4 rows behind 12 pages (1536) 17 and 21,
     // one of 16 rows x 64 heads over 8 groups behind 10 pages (1280) 15 and 21, of 64 x 32 heads behind 6 (1536) 19 and
     // 23; beyond: 16 rows x 64 heads behind 50 pages (6400) 50 and 29, 64 behind 10 (5120) 40 and 30, 128 behind 10
     // (10240) 66 and 41, behind 180 (1,440 pages, read 128 times) 797 and 99.
-    const long long tiles = std::max(p.N / L.tile_rows, std::min(p.S, p.N));
+    // In 8 bits 18 pages an SM: 16 sequences of 32 heads over 8 groups behind 16 pages (2048) 18 us and 22, 32 behind 16 (4096)
+    // 31 and 25, 128 of 8 heads over 2 groups behind 16 (4096) 33 and 26.
     // (Idle sequences count too: their tables are looked at by the one block that lines up the rows.)
     const long long readers = std::max<long long>(tiles, p.S);
-    const bool fold = !runs && readers * p.prefix * p.G <= (readers > p.S ? 2000 : 1500);
+    const bool fold = !runs && readers * p.prefix * p.G <= (bytes ? 2800 : readers > p.S ? 2000 : 1500);
     L.prefix = fold ? 0 : p.prefix;
     if (runs) {
       L.run_rows = 256 / p.hg;

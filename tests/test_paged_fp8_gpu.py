@@ -495,7 +495,7 @@ DENSE = {
     "prefix_hg1": dict(counts=[1, 3, 0, 2], lens=[128 * 5 + 1, 128 * 5 + 300, 9, 128 * 5 + 2], Hq=3, G=3, prefix=5, pad=1),
     "prefix_hg2": dict(counts=[2, 1], lens=[128 * 9 + 2, 128 * 9 + 128], Hq=2, G=1, prefix=9),
     "prefix_idle_first": dict(counts=[0, 1, 2], lens=[0, 128 * 3 + 5, 128 * 3 + 9], Hq=4, G=1, prefix=3),
-    # shared prefixes of enough pages to be read once for the batch
+    # longer shared prefixes
     "shared_hg1": dict(counts=[1, 3, 0, 2] * 5, lens=[128 * 40 + 3 + 9 * i for i in range(20)], Hq=2, G=2, prefix=40, pad=1),
     "shared_hg2": dict(counts=[2, 1, 1] * 10, lens=[128 * 26 + 2 + 41 * i for i in range(30)], Hq=4, G=2, prefix=26),
     "shared_hg4": dict(counts=[0] + [1, 2] * 12 + [1], lens=[7] + [128 * 60 + 2 + 17 * i for i in range(25)], Hq=4, G=1, prefix=60),
@@ -514,6 +514,28 @@ DENSE = {
     "runs_prefix": dict(counts=[3, 18, 0, 5], lens=[128 * 6 + 3, 128 * 6 + 400, 4, 128 * 7 + 5], Hq=16, G=2, prefix=6),
     "runs_prefix_three_pairs": dict(counts=[7] * 13, lens=[128 * 3 + 7 + 11 * i for i in range(13)], Hq=24, G=3, prefix=3),
     "runs_prefix_hg1": dict(counts=[12, 140], lens=[128 * 2 + 12, 128 * 2 + 300], Hq=1, G=1, prefix=2, pad=2),
+}
+# shared prefixes of so many pages, counted for every eight columns that read them, that they are read once for the batch
+SHARED = {
+    "hg1": dict(counts=[1, 3, 0, 2] * 10, lens=[128 * 40 + 3 + 9 * i for i in range(40)], Hq=2, G=2, prefix=40, pad=1),
+    "hg2": dict(counts=[2, 1, 1] * 10, lens=[128 * 50 + 2 + 41 * i for i in range(30)], Hq=4, G=2, prefix=50),
+    "hg4": dict(counts=[0] + [1, 2] * 12 + [1], lens=[7] + [128 * 120 + 2 + 17 * i for i in range(25)], Hq=4, G=1, prefix=120),
+    "hg8": dict(counts=[1] * 16, lens=[128 * 180 + 1 + 64 * i for i in range(16)], Hq=8, G=1, prefix=180, pad=2),
+    "three_pairs": dict(counts=[1] * 70, lens=[128 * 21 + 1 + i for i in range(70)], Hq=16, G=2, prefix=21),
+    "page_of_rows": dict(counts=[127], lens=[128 * 60 + 127], Hq=16, G=2, prefix=60),
+}
+# several rows a sequence, and enough pages to read for them that 128-row tiles do it
+TILES = {
+    "hg8": dict(counts=[70, 33, 40], lens=[128 * 12 - 5, 900, 1400], Hq=16, G=2, pad=3),
+    "hg8_one_tile": dict(counts=[12, 16, 3, 0, 9] * 4, lens=[900 + 17 * i for i in range(20)], Hq=16, G=2),
+    "hg8_one_tile_three_groups": dict(counts=[12, 16, 3, 0, 9] * 3, lens=[900 + 17 * i for i in range(15)], Hq=24, G=3),
+    "hg8_one_group": dict(counts=[300, 290, 17], lens=[700, 650, 17], Hq=8, G=1),
+    "hg4_page_ends": dict(counts=[128, 129, 127, 64, 65], lens=[1024, 1025, 1023, 900, 128 * 7 + 1], Hq=8, G=2),
+    "hg2_three_groups": dict(counts=[250, 300], lens=[1100, 999], Hq=6, G=3, pad=1),
+    "hg1": dict(counts=[500, 400, 0, 300], lens=[1000, 470, 50, 300], Hq=3, G=3),
+    "long": dict(counts=[17], lens=[128 * 90 + 2], Hq=16, G=2),
+    "prefix": dict(counts=[12] * 16, lens=[128 * 14 - 90 + 5 * i for i in range(16)], Hq=16, G=2, prefix=6),
+    "prefix_two_tiles": dict(counts=[40, 3, 25, 61], lens=[128 * 20 + 3, 128 * 9 + 4, 128 * 19 + 60, 2500], Hq=16, G=2, prefix=9, pad=2),
 }
 
 
@@ -548,9 +570,40 @@ def test_dense(msa, name, stale):
     _check_dense(b, *_dense(msa, b))
 
 
+@pytest.mark.parametrize("stale", ["nan", "huge"])
+@pytest.mark.parametrize("name", TILES)
+def test_dense_tiles(msa, name, stale):
+    b = ref8.Batch(stale=stale, seed=6, **TILES[name])
+    before = msa.msa_kernel_launches()
+    O, LSE = _dense(msa, b)
+    assert msa.msa_kernel_launches() - before == 3  # rows, tiles, merge
+    _check_dense(b, O, LSE)
+
+
+@pytest.mark.parametrize("stale", ["nan", "huge"])
+@pytest.mark.parametrize("name", SHARED)
+def test_dense_shared(msa, name, stale):
+    b = ref8.Batch(stale=stale, seed=6, **SHARED[name])
+    before = msa.msa_kernel_launches()
+    O, LSE = _dense(msa, b)
+    assert msa.msa_kernel_launches() - before == 4  # rows, the prefix by tiles, own pages beside it, merge
+    _check_dense(b, O, LSE)
+
+
+@pytest.mark.parametrize("name", ["rows_hg4", "g8_long", "prefix1", "runs_hg1", "shared_hg1"])
+def test_dense_few_pages(msa, name):
+    """Eight columns at a time, a small shared prefix as own pages: two launches."""
+    b = ref8.Batch(seed=6, **DENSE[name])
+    before = msa.msa_kernel_launches()
+    _dense(msa, b)
+    assert msa.msa_kernel_launches() - before == 2
+
+
 SCALES = {"tokens": dict(counts=[1, 2], lens=[1000, 700], Hq=8, G=2),
           "shared": dict(counts=[1, 2] * 10, lens=[128 * 60 + 2 + 17 * i for i in range(20)], Hq=8, G=2, prefix=60),
-          "runs": dict(counts=[20, 9], lens=[600, 390], Hq=16, G=2)}
+          "prefix": dict(counts=[1, 2] * 13, lens=[128 * 60 + 2 + 17 * i for i in range(26)], Hq=8, G=2, prefix=60),
+          "runs": dict(counts=[20, 9], lens=[600, 390], Hq=16, G=2),
+          "tiles": dict(counts=[20] * 8 + [9, 31], lens=[1100 - 30 * i for i in range(8)] + [390, 1024], Hq=16, G=2)}
 
 
 @pytest.mark.parametrize("what", ["v outlier", "v tiny", "v huge", "v spread", "v zero", "k spread", "k huge, q tiny",
@@ -641,6 +694,43 @@ def test_values_that_are_not_finite(msa, name):
             assert bool((O[r] == clean[0][r]).all()) and bool((LSE[r] == clean[1][r]).all()), r
 
 
+@pytest.mark.parametrize("name", ["hg8", "hg8_one_tile", "hg4_page_ends", "hg1", "prefix"])
+def test_later_rows_do_not_reach_earlier_ones_of_a_tile(msa, name):
+    """NaN codes of V in the last tokens of every sequence: the rows that see them have NaN in their dims, and nothing else
+    of any row changes; of K: the rows before have the same bits."""
+    import torch
+
+    b = ref8.Batch(seed=10, **TILES[name])
+    clean = _dense(msa, b)
+
+    def put(pool, back, d):
+        for s in range(b.S):
+            t = b.lens[s] - 1 - back
+            if b.counts[s] > back:
+                pool.view(torch.uint8)[int(b.table[s, t // 128]), :, t % 128, d] = 0x7f if d % 2 else 0xff
+
+    for back, d in ((0, 3), (1, 40), (2, 77)):
+        put(b.V8, back, d)
+    O, LSE = _dense(msa, b)
+    assert bool((LSE[:b.n] == clean[1][:b.n]).all())
+    for r in range(b.n):
+        want = clean[0][r].clone()
+        behind = b.lens[b.row_seq[r]] - 1 - b.row_pos[r]
+        for back, d in ((0, 3), (1, 40), (2, 77)):
+            if behind <= back < b.counts[b.row_seq[r]]:
+                want[:, d] = NAN
+        same = (O[r] == want) | (O[r].isnan() & want.isnan())
+        assert bool(same.all()), (r, behind, torch.nonzero(~same)[:4].tolist())
+    put(b.K8, 1, 5)
+    O, LSE = _dense(msa, b)
+    for r in range(b.n):
+        behind = b.lens[b.row_seq[r]] - 1 - b.row_pos[r]
+        if behind > 2:
+            assert bool((O[r] == clean[0][r]).all()) and bool((LSE[r] == clean[1][r]).all()), r
+        elif behind <= 1 < b.counts[b.row_seq[r]]:
+            assert bool(O[r].isnan().all()) and bool(LSE[r].isnan().all()), r
+
+
 def test_pools_past_32_bit_offsets(msa):
     """Pages whose codes lie more than 2^32 bytes into the pools (and whose bytes past 2^25 vectors)."""
     import torch
@@ -729,7 +819,10 @@ def test_bad_pages_and_positions_are_reported(msa):
 BITS = {"sparse": (dict(counts=[1, 2, 0, 1], lens=[40000, 700, 3, 129], Hq=16, G=2), "sparse"),
         "tokens": (dict(counts=[1] * 6, lens=[30000 + 999 * i for i in range(6)], Hq=8, G=2), "dense"),
         "shared": (SCALES["shared"], "dense"),
-        "runs": (dict(counts=[5, 33, 9], lens=[3000, 700, 1290], Hq=16, G=2), "dense")}
+        "prefix": (SCALES["prefix"], "dense"),
+        "runs": (dict(counts=[5, 33, 9], lens=[3000, 700, 1290], Hq=16, G=2), "dense"),
+        "tiles": (dict(counts=[40, 33, 19], lens=[3000, 700, 1290], Hq=16, G=2), "dense"),
+        "many_pages": (dict(counts=[1] * 8, lens=[30000 + 999 * i for i in range(8)], Hq=32, G=8, index=False), "dense")}
 
 
 @pytest.mark.parametrize("name", BITS)
