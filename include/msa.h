@@ -485,8 +485,7 @@ MSA_API msa_status msa_paged_append_axes(const msa_paged_shape *shape, const msa
  * are not supported.
  *
  * The calls below are the ones above over such a cache, their results those of the
- * values it stands for: same batches, limits, errors, infinities of queries and
- * NaN; workspaces are sized with the _FP8 values (the append: MSA_WS_PAGED_APPEND).
+ * values it stands for: same batches, limits, errors and NaN; workspaces are sized with the _FP8 values (the append: MSA_WS_PAGED_APPEND).
  * Powers of two of a query and a key (a value) whose product leaves fp32's range
  * may give infinities or zeros where the exact score would not.
  */
@@ -526,7 +525,9 @@ MSA_API msa_status msa_paged_sparse_attn_fp8(const msa_paged_shape *shape, const
                                              const void *q_idx, int32_t *block_idx, void *O, float *LSE, void *workspace,
                                              size_t workspace_bytes, msa_stream_t stream);
 
-/* msa_paged_dense_attn. */
+/* msa_paged_dense_attn. Made for tokens and few rows a sequence; where there are
+ * more, or the prefix is shared by many, probabilities may be rounded to bf16 (O then
+ * differs by up to 2^-8 of sum p |v|), which depends on the shape alone. */
 MSA_API msa_status msa_paged_dense_attn_fp8(const msa_paged_shape *shape, const msa_paged_cache_fp8 *cache, const void *Q,
                                             void *O, float *LSE, void *workspace, size_t workspace_bytes,
                                             msa_stream_t stream);
