@@ -257,7 +257,7 @@ using namespace msa;
 
 extern "C" {
 
-int32_t msa_version(void) { return (1 << 16) | 5; }
+int32_t msa_version(void) { return (1 << 16) | 6; }
 
 int64_t msa_kernel_launches(void) { return g_launches.load(std::memory_order_relaxed); }
 

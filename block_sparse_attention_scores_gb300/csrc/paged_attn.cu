@@ -41,7 +41,10 @@
 // A page's codes are read as they lie: K by ldmatrix (a lane gets four neighbouring
 // codes of a key, the sum's order over d follows), V by 16-byte loads of four keys'
 // 16 neighbouring dims, paired by key with byte permutes, so that the fragments of
-// the transposed V come without a transposing load, which there is none of for bytes.
+// the transposed V come without another pass.
+// Measured: 64 rows over 8000 tokens of 8 groups, 729 MB in 120 us, 6.1 TB/s, 0.89
+// of a plain copy; 57 rows x 8 groups x 16 selected pages 46 us with the rows' kernel,
+// of which the memory takes 35 (k = 64: 149 and 142).
 #include "mma_sync.cuh"
 #include "paged_fp8.cuh"
 #include "paged_rows.cuh"

@@ -51,9 +51,13 @@
 // A cache in 8 bits (kBytes, paged_fp8.cuh): the same products of the values that
 // the codes stand for, which bf16 holds exactly. Codes arrive by plain bulk copies,
 // half a tile at a time (a page's codes of a group lie in a row), and eight warps
-// turn them into the bf16 tiles that the tensor core reads: 30 operations a pair of
-// softmax values stand against 4 a pair of codes, for as many codes as the two
-// tiles have scores, so the chain above stays what bounds. V is cleaned on the way.
+// turn them into the bf16 tiles that the tensor core reads, four a half, K's and then
+// V's of a page: a tile then takes them half of what four warps take, which V's way
+// (copied, converted, multiplied, and its place free again) needs. P is one bf16 for
+// own pages, too: that is below the codes' own rounding by far. What bounds is still
+// the chain above, beside which the conversion takes issue slots and shared memory:
+// the call of 128 x 2 rows x 32 heads behind 256 pages 160 us (155 without copies and
+// conversion, 132 in bf16), of 32 x 4 rows x 64 heads over 2000 tokens 72 us (64).
 #include "paged_fp8.cuh"
 #include "paged_rows.cuh"
 
@@ -116,8 +120,8 @@ struct PrefixShared {
   uint64_t raw_full[2 * kRaw], raw_empty[2 * kRaw];  // (kBytes)
   uint32_t tmem_base;
 };
-// 8 bits: everything in the dynamic part, whose beginning is then a multiple of 1024 bytes from the SM's (there is no room
-// left to align it)
+// 8 bits: everything in the dynamic part, which then begins at a multiple of 1024 bytes (there is no room left to align it;
+// the kernel looks)
 template <bool kBytes>
 constexpr int kSmem = kBytes ? oShared + (int)sizeof(PrefixShared) : oV + kStages * kTile + 1024;
 static_assert(kSmem<true> <= 232448, "shared memory of a block");

@@ -815,6 +815,67 @@ def test_bad_pages_and_positions_are_reported(msa):
     run(page(1, 2, 0), "dense", prefix=3)                      # a prefix that is not shared
 
 
+def test_binding_refuses_what_does_not_fit(msa):
+    import torch
+
+    b = ref8.Batch(counts=[1, 2], lens=[300, 200], Hq=4, G=2, seed=1)
+    shape, cache, t = b.gpu(4)
+    x = _new_rows(b)
+    f, fi = _freq(128).cuda(), _freq(64).cuda()
+    axis = torch.zeros(64, dtype=torch.int32, device="cuda")
+    at = torch.zeros(3, 2, dtype=torch.int32, device="cuda")
+
+    def append(rope, positions):
+        msa.paged_append_fp8(shape, cache, rope, x["K"], x["V"], x["k_idx"], x["Q"], x["q_idx"], positions=positions)
+
+    for rope, positions, what in ((msa.Rope(f, fi, axis=axis), None, "positions"), (msa.Rope(f, fi), at.long(), "int32"),
+                                  (msa.Rope(f, fi), at[:2], "shape"), (msa.Rope(f, fi), at[0], "shape"),
+                                  (msa.Rope(f, fi), at.cpu(), "GPU"), (msa.Rope(f, fi), at.t().contiguous().t(), "contiguous")):
+        with pytest.raises(ValueError, match=what):
+            append(rope, positions)
+    with pytest.raises(msa.MsaError, match="axes"):
+        append(msa.Rope(f, fi), torch.zeros(3, 9, dtype=torch.int32, device="cuda"))
+    for bad in (axis[:32], axis.long()):
+        with pytest.raises(ValueError, match="axis"):
+            msa.Rope(f, fi, axis=bad)
+    pools = [cache.K, cache.V, cache.K_exp, cache.V_exp, cache.k_idx, cache.k_idx_exp]
+    rest = [cache.page_table, cache.row_start, cache.seq_len]
+    for i, bad in ((0, cache.K.view(torch.uint8)), (1, cache.V[:, :1].contiguous()), (2, cache.K_exp.float()), (3, cache.V_exp[:-1]),
+                   (4, cache.k_idx[:, ::2]), (5, cache.k_idx_exp.cpu()), (5, None)):
+        with pytest.raises(ValueError):
+            msa.PagedCacheFp8(*[bad if j == i else p for j, p in enumerate(pools)], *rest)
+    with pytest.raises(TypeError, match="PagedCacheFp8"):
+        msa.paged_dense_attn_fp8(shape, msa.PagedCache(*[p.float().to(torch.bfloat16) for p in (cache.K, cache.V)], None, *rest), t["Q"])
+    start = torch.tensor([0, 10, 20], dtype=torch.int32, device="cuda")
+    for args, what in (((start.long(), 20), "int32"), ((start[:2], 20), "shape"), ((start, 20, start[:1]), "shape")):
+        with pytest.raises(ValueError, match=what):
+            msa.paged_read_fp8(shape, cache, *args)
+    none = msa.PagedCacheFp8(*pools[:4], None, None, *rest)
+    with pytest.raises(ValueError, match="k_idx"):
+        msa.paged_sparse_attn_fp8(shape, none, t["Q"], t["q_idx"])
+    with pytest.raises(ValueError, match="k_idx"):
+        msa.paged_append_fp8(shape, none, msa.Rope(f, fi), x["K"], x["V"], x["k_idx"])
+
+
+def test_copied_cache_has_its_own_tensors(msa):
+    """A deep copy is another cache: appending to it leaves the first one alone."""
+    import copy
+
+    import torch
+
+    b = ref8.Batch(counts=[2], lens=[130], Hq=2, G=1, seed=1)
+    shape, cache, t = b.gpu(4)
+    x = _new_rows(b)
+    same, other = copy.copy(cache), copy.deepcopy(cache)
+    was = [p.clone() for p in (cache.K.view(torch.uint8), cache.V_exp)]
+    msa.paged_append_fp8(shape, other, msa.Rope(), x["K"], x["V"], x["k_idx"])
+    assert torch.equal(cache.K.view(torch.uint8), was[0]) and torch.equal(cache.V_exp, was[1])
+    msa.paged_append_fp8(shape, same, msa.Rope(), x["K"], x["V"], x["k_idx"])
+    for n in ("K", "V", "k_idx"):
+        assert torch.equal(getattr(cache, n).view(torch.uint8), getattr(other, n).view(torch.uint8)), n
+        assert torch.equal(getattr(cache, n + "_exp"), getattr(other, n + "_exp")), n
+
+
 # ----------------------------------------------------------------- streams, graphs, together
 BITS = {"sparse": (dict(counts=[1, 2, 0, 1], lens=[40000, 700, 3, 129], Hq=16, G=2), "sparse"),
         "tokens": (dict(counts=[1] * 6, lens=[30000 + 999 * i for i in range(6)], Hq=8, G=2), "dense"),
