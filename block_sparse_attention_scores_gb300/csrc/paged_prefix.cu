@@ -56,8 +56,8 @@
 // (copied, converted, multiplied, and its place free again) needs. P is one bf16 for
 // own pages, too: that is below the codes' own rounding by far. What bounds is still
 // the chain above, beside which the conversion takes issue slots and shared memory:
-// the call of 128 x 2 rows x 32 heads behind 256 pages 160 us (155 without copies and
-// conversion, 132 in bf16), of 32 x 4 rows x 64 heads over 2000 tokens 72 us (64).
+// the call of 128 x 2 rows x 32 heads behind 256 pages 156 us (155 without copies and
+// conversion, 132 in bf16), of 32 x 4 rows x 64 heads over 2000 tokens 69 us (64).
 #include "paged_fp8.cuh"
 #include "paged_rows.cuh"
 
@@ -671,9 +671,9 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
               if (key >= behind) byte = 0;
             }
             const float pow2 = exp_value(byte);
-            const uint4 lo = eight_bf16(make_uint2(v.x, v.y), pow2), hi = eight_bf16(make_uint2(v.z, v.w), pow2);
-            *reinterpret_cast<uint4*>(tile + j * 128 + c0) = up ? hi : lo;
-            *reinterpret_cast<uint4*>(tile + j * 128 + (c0 ^ 16)) = up ? lo : hi;
+            const uint2 first = up ? make_uint2(v.z, v.w) : make_uint2(v.x, v.y), second = up ? make_uint2(v.x, v.y) : make_uint2(v.z, v.w);
+            *reinterpret_cast<uint4*>(tile + j * 128 + c0) = eight_bf16(first, pow2);
+            *reinterpret_cast<uint4*>(tile + j * 128 + (c0 ^ 16)) = eight_bf16(second, pow2);
           }
           if (kOwn && values) {
             odd = __any_sync(0xffffffffu, odd);
