@@ -14,7 +14,7 @@ constexpr int kCutSms = 152;
 constexpr int kLeadCount = 16;  // rows in PagedWs::lead
 constexpr int kWorkNext = 17;   // items that attention CTAs have taken beyond their first ones
 constexpr int kRunCount = 18;   // entries of PagedWs::runs
-constexpr int kRunNext = 19;    // runs that have been taken beyond the CTAs' first ones
+constexpr int kRunNext = 19;    // runs that have been taken (without a prefix: beyond the CTAs' first ones)
 
 struct PagedProb {
   int S, N, Hq, G, hg, k;

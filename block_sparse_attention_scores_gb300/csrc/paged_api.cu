@@ -40,6 +40,34 @@ static void cut_pages(long long tiles, int pages, double extra, double join, int
   }
 }
 
+// (8 bits) Into how many runs to cut a shared prefix that sequences' own pages follow in the same kernel: `units` pages of a
+// group, each read by `pairs` CTAs, and `items` of `pages` pages with `streams` tiles of codes a page. What has no part of
+// the prefix starts with the items, the others go on with them, and an item is not cut, so that the last ones decide. Times
+// in us, as measured: a page of the prefix 2.1, of an item 1.4 a stream, a run's start and end 5 and 4; a run that passes
+// from a group to the next has two of these. 23 sequences of 5 rows x 64 heads behind 64 pages, 700 tokens of their own:
+// 71 us with all CTAs in the prefix (38 runs), 65 with the 24 that this finds; 4 of 60 x 32 heads behind 12 pages 41 and 31.
+static int prefix_teams(int most, int units, int pairs, int G, long long items, double item) {
+  if (items > 8 * kCutSms) return most;
+  double best = 0;
+  int teams = most;
+  for (int n = most; n >= 1 && n * pairs * 2 >= kCutSms; --n) {
+    const int busy = n * pairs, idle = kCutSms - busy;
+    const double T = (units + n - 1) / n * 2.1 + (n % G == 0 ? 5 : n > G ? 10 : 5 * (1 + (G + n - 1) / n));
+    const long long before = (long long)(T / item);  // items of a CTA without prefix until then
+    double t = T;
+    if (idle * before < items) {
+      const long long left = items - idle * before - 1, rounds = left / kCutSms;
+      t = rounds * item + (left % kCutSms < idle ? (before + 1) * item : T + item);
+      t = std::max(t, T);
+    }
+    if (best == 0 || t < 0.97 * best) {
+      best = t;
+      teams = n;
+    }
+  }
+  return teams;
+}
+
 PagedWs paged_ws_layout(const PagedProb& p, int which) {
   const bool bytes = which == MSA_WS_PAGED_SPARSE_FP8 || which == MSA_WS_PAGED_DENSE_FP8;
   PagedWs L;
@@ -71,10 +99,19 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
     // sequence (32 sequences over 2000 tokens, 64 heads over 8 groups, of 2 rows 70 us by tiles and 50, of 3 rows 69 and 71;
     // 32 x 8 rows x 32 heads 70 and 84), unless all pages that are read, once for every eight columns, are 18 an SM at most
     // (100 rows x 16 heads over 2 groups and 300 tokens, 600 of them, 24 and 13; 200 x 64 heads over 8 groups and 250, 3200,
-    // 28 and 40).
+    // 28 and 40). Behind a prefix that is not read as own pages (below) the tiles' kernel runs anyway: then the tiles have
+    // the own pages above 20 columns whatever their number (23 sequences of 5 rows x 64 heads behind 64 pages with one of
+    // their own 58 us, 83 by eight columns; 4 of 60 x 32 heads behind 12 29 and 54), and above 12 where they are 40 an SM at
+    // most (64 of 2 rows x 64 heads behind 128: with 250 tokens, 2048 pages, 97 and 105, with 500 108 and 113, with 1000,
+    // 8192 pages, 134 and 129; of 5 x 32 with 500, 5120 pages, 129 and 144).
     const long long tiles = std::max(p.N / L.tile_rows, std::min(p.S, p.N));
-    const bool runs = (long long)p.N * p.hg > (bytes ? 20LL : 9LL) * p.S && p.max_blocks - p.prefix > 1 &&
-                      !(bytes && tiles * p.G * (p.max_blocks - p.prefix) <= 2800);
+    const long long readers = std::max<long long>(tiles, p.S);
+    const bool folds = readers * p.prefix * p.G <= (bytes ? 2800 : readers > p.S ? 2000 : 1500);
+    const int own_pages = p.max_blocks - p.prefix;
+    const long long reads = tiles * p.G * own_pages;
+    const bool runs = bytes ? (long long)p.N * p.hg > (!folds && reads <= 6000 ? 12LL : 20LL) * p.S &&
+                                  (!folds || (own_pages > 1 && reads > 2800))
+                            : (long long)p.N * p.hg > 9LL * p.S && own_pages > 1;
     // A shared prefix of ten pages an SM (13 where a sequence has several tiles of eight columns), counted for every such
     // tile, is read as own pages: it stays in L2, and two kernels do with it what four do. 4 sequences of 32 heads over 8
     // groups behind 16 pages 15 us against 19, 16 behind 8 pages 14 and 19, 8 of 4 rows behind 12 pages (1536) 17 and 21,
@@ -84,9 +121,7 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
     // In 8 bits 18 pages an SM: 16 sequences of 32 heads over 8 groups behind 16 pages (2048) 18 us and 22, 32 behind 16 (4096)
     // 31 and 25, 128 of 8 heads over 2 groups behind 16 (4096) 33 and 26.
     // (Idle sequences count too: their tables are looked at by the one block that lines up the rows.)
-    const long long readers = std::max<long long>(tiles, p.S);
-    const bool fold = !runs && readers * p.prefix * p.G <= (bytes ? 2800 : readers > p.S ? 2000 : 1500);
-    L.prefix = fold ? 0 : p.prefix;
+    L.prefix = folds && !runs ? 0 : p.prefix;
     if (runs) {
       L.run_rows = 256 / p.hg;
       L.runs = take((size_t)p.N * 16);
@@ -105,11 +140,21 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
       // 2,000; own pages: half of what the table holds), and the prefix has half of the SMs at least, lest a poor estimate
       // make it the longer one. 64 sequences behind 32K tokens with up to 2K of their own: 112 us one after the other,
       // 100 with two thirds, 94 with half, 102 with 0.35 of the SMs; 100 sequences with 2000 each: 67, 49, 48, 48. (In 8 bits
-      // 3,500 and 1,200 cycles: the first of these 95 -> 91 us.)
-      const double own = (double)tiles * p.G * (p.max_blocks - p.prefix + 1) / 2 * (bytes ? 1200 : 2000);
+      // 3,500 and 1,200 cycles: the first of these 95 -> 91 us; and 4,000 for each CTA that has any, which has to find its
+      // first page: 100 of one row x 64 heads behind 40 pages with one of their own 57 -> 53, 64 x 32 heads behind 100 pages
+      // 46 -> 42.)
+      const double own = (double)tiles * p.G * (own_pages + 1) / 2 * (bytes ? 1200 : 2000) +
+                         (bytes ? 4000.0 * std::min<long long>(tiles * p.G * L.splits, kCutSms) : 0);
       const double shared = (double)units * L.pairs * (bytes ? 3500 : 2750);
       const int sms = L.run_rows ? kCutSms : (int)(kCutSms * std::max(0.5, shared / (shared + own)));
       L.teams = std::min(units, std::max(1, sms / L.pairs));
+      if (bytes && runs) {
+        const bool both = (long long)p.N * p.hg > 128LL * p.S, even = p.G % 2 == 0;  // two tiles of rows; groups two at a time
+        const int streams = even ? 2 : 1, walks = even && both ? 2 : 1;
+        const double item = L.per_run * (walks > 1 ? 2 * 2.1 : 1.4 * streams) + 4 * walks;
+        L.teams = prefix_teams(L.teams, units, L.pairs, p.G,
+                               std::max<long long>(p.N / L.run_rows, std::min(p.S, p.N)) * L.rslots * p.G / streams, item);
+      }
       L.n_flags = std::max(L.n_flags, L.teams * L.pairs);
       for (int g = 0; g < p.G; ++g)
         L.pslots = std::max(L.pslots, team_of((g + 1) * p.prefix - 1, units, L.teams) -

@@ -56,8 +56,12 @@
 // (copied, converted, multiplied, and its place free again) needs. P is one bf16 for
 // own pages, too: that is below the codes' own rounding by far. What bounds is still
 // the chain above, beside which the conversion takes issue slots and shared memory:
-// the call of 128 x 2 rows x 32 heads behind 256 pages 156 us (155 without copies and
-// conversion, 132 in bf16), of 32 x 4 rows x 64 heads over 2000 tokens 69 us (64).
+// the call of 128 x 2 rows x 32 heads behind 256 pages 158 us (145 without the
+// conversion, 132 in bf16), of 32 x 4 rows x 64 heads over 2000 tokens 69 us (64), of
+// 23 drafts of 5 rows x 64 heads behind 64 pages, 700 tokens of their own, 64 us.
+// Both tiles' products go through one thread, in turn: two, one for each tile, let the
+// tiles run in step, each waiting for the tensor core and then both in the softmax
+// (the last of these behind 1000 pages 462 -> 530 us).
 #include "paged_fp8.cuh"
 #include "paged_rows.cuh"
 
@@ -109,9 +113,10 @@ struct PrefixShared {
   int flag;
   Run run[2];
   int odd[2][2 * kConverters];  // a run's V has infinities or NaN among the rows' own tokens (as each warp that looks finds it)
-  uint64_t run_full[2], run_empty[2], k_full[kStages], v_clean[kStages];  // (kRuns)
+  uint64_t run_full[2], run_empty[2], v_clean[kStages];  // (kRuns)
+  uint64_t k_full[kStages], kv_full[kStages];   // (kRuns: K;) a page's V (without kRuns with the next one's K)
   uint64_t q_full, q_empty;
-  uint64_t k0_full, kv_full[kStages];  // the first page's K; then a page's V with the next one's K
+  uint64_t k0_full;              // the first page's K
   uint64_t k_empty[kStages], v_empty[kStages];
   uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
   uint64_t pair[2][4];           // the two warps of a tile's 32 rows
@@ -181,15 +186,17 @@ __device__ __forceinline__ void st_global8(float* p, const float* v) {
 }
 
 // kShared: the call has a shared prefix. Without one every page is a sequence's own, and its P has both parts: told at run
-// time, as where there are both kinds, it costs 2 % (32 x 4 rows x 64 heads over 2000 tokens 63.3 -> 64.9 us). kBytes: the
-// call has nothing but a shared prefix, and no masks (what they and P's second part take of the registers costs 128 x 2 rows
-// behind 256 pages 287 -> 245 us, without being run).
+// time, as where there are both kinds, it costs 2 % (32 x 4 rows x 64 heads over 2000 tokens 63.3 -> 64.9 us). kBytes: with a
+// prefix K and V are converted by the same instructions. Two SMs share the cache that instructions come from, and a CTA in
+// the prefix whose neighbour does something else (own pages, another kernel) lost up to half of its speed to code that was
+// 3 KB longer (128 x 2 rows behind 256 pages 189 -> 159 us; without a prefix, where neighbours do the same, 32 x 4 rows x 64
+// heads over 2000 tokens would take 71 instead of 68).
 template <bool kRuns, bool kShared, bool kBytes>
 __global__ void __launch_bounds__(kThreads<kBytes>, 1)
     paged_prefix_kernel(PrefixArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v) {
   static_assert(kRuns || !kBytes, "8 bits: runs' descriptions always go round");
-  constexpr bool kOwn = kRuns && !(kBytes && kShared);  // there are sequences' own pages
+  constexpr bool kOwn = kRuns;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = kBytes ? smem_raw
                          : reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -310,7 +317,8 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
     };
     if constexpr (kRuns) {
       // The prefix's runs first, as below, then the sequences' own ones as they come. A run's first 32 pages are looked
-      // up ahead, one step a page: the number, the rows, the pages.
+      // up ahead, one step a page: the number, the rows, the pages; on the last pages of the run before, as what is taken
+      // earlier is not there for a CTA that is free.
       struct Ahead {
         Run run;
         int y;  // of this lane's page
@@ -324,11 +332,12 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
       auto step1 = [&]() {
         own_now = second || u >= u_end;
         if (!own_now || second) return;
-        if (++own > 0 && lane == 0) taken = atomicAdd(a.header + kRunNext, 1);
+        if ((a.prefix || ++own > 0) && lane == 0) taken = atomicAdd(a.header + kRunNext, 1);
       };
       auto step2 = [&]() {
         if (!own_now || second) return;
-        id = own ? gridDim.x + __shfl_sync(0xffffffffu, taken, 0) : blockIdx.x;
+        const int next = __shfl_sync(0xffffffffu, taken, 0);  // (behind a prefix the first one, too: whoever is free takes it)
+        id = a.prefix ? next : own ? gridDim.x + next : blockIdx.x;
         if (id < items) lead = ld_in(a.runs + id / (a.rslots * (a.G / pair_g)));
       };
       auto step3 = [&](Ahead& h) {
@@ -418,7 +427,7 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
           }
           __syncwarp();
           if constexpr (kBytes) load_codes(true, at);
-          if (step < 3) find(next, step++);
+          if (step < 3 && i + 4 >= now.run.pages * streams) find(next, step++);
         }
         ++n_run;
         for (; step < 3; ++step) find(next, step);
@@ -639,6 +648,9 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
       // key meet in no bank. (Addresses in shared memory, 32 bits, with what does not change added up before.)
       const int half = (warp - 20) / kConverters, key0 = half * kHalfKeys + (warp & (kConverters - 1)) * 4 + (lane >> 3);
       const int piece = lane & 7, up = piece >> 2, c0 = (((piece & 3) * 2 + up) ^ (key0 & 7)) << 4;
+      const uint8_t* const raw0 = smem + oRawK + key0 * 128 + piece * 16;
+      const uint8_t* const exps0 = smem + oExpK + key0;
+      uint8_t* const tile0 = smem + oK + up * kChunk + key0 * 128;
       uint32_t kc = 0;
       Run none;
       bool ok = true;
@@ -646,36 +658,36 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
         const Run& run = sh.run[(n_run - 1) & 1];
         const int tiles = run.twin ? run.pages * 2 : run.pages;
         bool odd = false;
-        // this half of the CTA's tile kc of K or V; keys from `behind` on become zeros, NaN among those from `own` on too
-        auto make_half = [&](auto of_values, int own, int behind) {
-          constexpr bool values = decltype(of_values)::value;
-          const int st = kc % kStages, bar = (values ? kRaw : 0) + half;
-          if (!mbar_wait(values ? &sh.v_empty[st] : &sh.k_empty[st], ((kc / kStages) & 1) ^ 1, err, values ? 1504 : 1503)) return false;
-          if (!mbar_wait(&sh.raw_full[bar], kc & 1, err, values ? 1509 : 1508)) return false;
-          const uint8_t* const raw = smem + (values ? oRawV : oRawK) + key0 * 128 + piece * 16;
-          const uint8_t* const exps = smem + (values ? oExpV : oExpK) + key0;
-          uint8_t* const tile = smem + (values ? oV : oK) + st * kTile + up * kChunk + key0 * 128;
+        // this half of the CTA's tile kc of K (v = 0) or V; keys from `behind` on become zeros, NaN among those from `own` on too
+        auto make_half = [&](auto v, int own, int behind) {
+          const int st = kc % kStages, bar = v * kRaw + half;
+          if (!mbar_wait(&sh.k_empty[st] + v * kStages, ((kc / kStages) & 1) ^ 1, err, 1503 + v)) return false;
+          if (!mbar_wait(&sh.raw_full[bar], kc & 1, err, 1508 + v)) return false;
+          const uint8_t* const raw = raw0 + v * (oRawV - oRawK);
+          const uint8_t* const exps = exps0 + v * (oExpV - oExpK);
+          uint8_t* const tile = tile0 + (v * kStages + st) * kTile;
 #pragma unroll
           for (int j = 0; j < kHalfKeys; j += 4 * kConverters) {
-            uint4 v = *reinterpret_cast<const uint4*>(raw + j * 128);
+            uint4 w = *reinterpret_cast<const uint4*>(raw + j * 128);
             uint32_t byte = exps[j];
             const int key = key0 + j;
-            if (kOwn && values && key >= own) {
+            if (v && key >= own) {
               // (0x7f, the only code that is not finite, plus 1 has the top bit)
               auto clean = [&](uint32_t& w) {
                 const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
                 odd |= nan != 0 && key < behind;
                 w = key < behind ? w & ~((nan >> 7) * 0xffu) : 0u;
               };
-              clean(v.x); clean(v.y); clean(v.z); clean(v.w);
+              clean(w.x); clean(w.y); clean(w.z); clean(w.w);
               if (key >= behind) byte = 0;
             }
             const float pow2 = exp_value(byte);
-            const uint2 first = up ? make_uint2(v.z, v.w) : make_uint2(v.x, v.y), second = up ? make_uint2(v.x, v.y) : make_uint2(v.z, v.w);
+            const uint2 first = up ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y),
+                        second = up ? make_uint2(w.x, w.y) : make_uint2(w.z, w.w);
             *reinterpret_cast<uint4*>(tile + j * 128 + c0) = eight_bf16(first, pow2);
             *reinterpret_cast<uint4*>(tile + j * 128 + (c0 ^ 16)) = eight_bf16(second, pow2);
           }
-          if (kOwn && values) {
+          if (v) {
             odd = __any_sync(0xffffffffu, odd);
             if (lane == 0) sh.odd[(n_run - 1) & 1][warp - 20] = odd;
           }
@@ -683,19 +695,25 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&sh.raw_empty[bar]);
-            mbar_arrive(values ? &sh.kv_full[st] : &sh.k_full[st]);
+            mbar_arrive(&sh.k_full[st] + v * kStages);
           }
           return true;
         };
         for (int i = 0; i < tiles && ok; ++i, ++kc) {
           const int page = run.twin ? i >> 1 : i;
           int own = 128, behind = 128;
-          if (kOwn && page >= run.masked) {
+          if (page >= run.masked) {
             const int token0 = (run.first + page) * 128;
             behind = min(128, max(0, run.pos + run.rows - token0));
             own = min(behind, max(0, run.pos + 1 - token0));
           }
-          ok = make_half(std::false_type(), 128, 128) && make_half(std::true_type(), own, behind);
+          if constexpr (kShared) {
+#pragma unroll 1
+            for (int v = 0; v < 2 && ok; ++v) ok = make_half(v, own, behind);
+          } else {
+            ok = make_half(std::integral_constant<int, 0>(), own, behind) &&
+                 make_half(std::integral_constant<int, 1>(), own, behind);
+          }
         }
         run_done(false);
       }
@@ -880,7 +898,7 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;  // (a run behind the row's end, or scores of -infinity)
       float* dst = a.part_o + at * 128 + half * 64;
-#pragma unroll
+#pragma unroll(kBytes && kShared ? 1 : 4)
       for (int z = 0; z < 4; ++z) {
         float o[16];
         tmem_ld16(o_at + z * 16, o);
@@ -979,8 +997,8 @@ cudaError_t launch_paged_prefix(const PagedProb& p, const PagedCachePtrs& c, con
   a.rslots = L.rslots;
   a.pslots = L.pslots;
   if (c.bytes())
-    return L.run_rows ? launch_prefix<true, false, true>(a, L.n_flags, mq, maps, st)
-                      : launch_prefix<true, true, true>(a, L.n_flags, mq, maps, st);
+    return L.prefix ? launch_prefix<true, true, true>(a, L.n_flags, mq, maps, st)
+                    : launch_prefix<true, false, true>(a, L.n_flags, mq, maps, st);
   if (!L.run_rows) return launch_prefix<false, true, false>(a, L.n_flags, mq, maps, st);
   if (L.prefix) return launch_prefix<true, true, false>(a, L.n_flags, mq, maps, st);
   return launch_prefix<true, false, false>(a, L.n_flags, mq, maps, st);
