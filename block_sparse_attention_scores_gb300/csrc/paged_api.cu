@@ -40,25 +40,27 @@ static void cut_pages(long long tiles, int pages, double extra, double join, int
   }
 }
 
-// (8 bits) Into how many runs to cut a shared prefix that sequences' own pages follow in the same kernel: `units` pages of a
-// group, each read by `pairs` CTAs, and `items` of `pages` pages with `streams` tiles of codes a page. What has no part of
-// the prefix starts with the items, the others go on with them, and an item is not cut, so that the last ones decide. Times
-// in us, as measured: a page of the prefix 2.1, of an item 1.4 a stream, a run's start and end 5 and 4; a run that passes
-// from a group to the next has two of these. 23 sequences of 5 rows x 64 heads behind 64 pages, 700 tokens of their own:
+// (8 bits) Time in us, as measured, of a shared prefix cut into n runs of equal length: `units` pages of a group, 2.1 each,
+// and `edge` for a run's start and end, 2 and up to 3 for its rows; a run that passes from a group to the next has two.
+static double prefix_time(int units, int G, int n, double edge) {
+  return (units + n - 1) / n * 2.1 + edge * (n % G == 0 ? 1 : n > G ? 2 : 1 + (G + n - 1) / n);
+}
+// Into how many runs to cut it where sequences' own pages follow in the same kernel, in `items` that take a CTA `item` us
+// each; `pairs` CTAs read a run. What has no part of the prefix starts with the items, the others go on with them, and an
+// item is not cut, so that the last ones decide. 23 sequences of 5 rows x 64 heads behind 64 pages, 700 tokens of their own:
 // 71 us with all CTAs in the prefix (38 runs), 65 with the 24 that this finds; 4 of 60 x 32 heads behind 12 pages 41 and 31.
-static int prefix_teams(int most, int units, int pairs, int G, long long items, double item) {
+static int prefix_teams(int most, int units, int pairs, int G, double edge, long long items, double item) {
   if (items > 8 * kCutSms) return most;
   double best = 0;
   int teams = most;
   for (int n = most; n >= 1 && n * pairs * 2 >= kCutSms; --n) {
-    const int busy = n * pairs, idle = kCutSms - busy;
-    const double T = (units + n - 1) / n * 2.1 + (n % G == 0 ? 5 : n > G ? 10 : 5 * (1 + (G + n - 1) / n));
+    const int idle = kCutSms - n * pairs;
+    const double T = prefix_time(units, G, n, edge);
     const long long before = (long long)(T / item);  // items of a CTA without prefix until then
     double t = T;
     if (idle * before < items) {
       const long long left = items - idle * before - 1, rounds = left / kCutSms;
-      t = rounds * item + (left % kCutSms < idle ? (before + 1) * item : T + item);
-      t = std::max(t, T);
+      t = std::max(T, rounds * item + (left % kCutSms < idle ? (before + 1) * item : T + item));
     }
     if (best == 0 || t < 0.97 * best) {
       best = t;
@@ -148,11 +150,16 @@ PagedWs paged_ws_layout(const PagedProb& p, int which) {
       const double shared = (double)units * L.pairs * (bytes ? 3500 : 2750);
       const int sms = L.run_rows ? kCutSms : (int)(kCutSms * std::max(0.5, shared / (shared + own)));
       L.teams = std::min(units, std::max(1, sms / L.pairs));
-      if (bytes && runs) {
+      const double edge = 2 + 3 * (double)p.N * p.hg / (L.pairs * 256.);
+      if (bytes && !runs) {
+        // a few runs less where they then pass from group to group less often (64 sequences behind 32K 84 -> 80: 94 -> 91 us)
+        for (int n = L.teams - 1, most = L.teams; n >= 1 && n * 8 >= most * 7; --n)
+          if (prefix_time(units, p.G, n, edge) < 0.97 * prefix_time(units, p.G, L.teams, edge)) L.teams = n;
+      } else if (bytes) {
         const bool both = (long long)p.N * p.hg > 128LL * p.S, even = p.G % 2 == 0;  // two tiles of rows; groups two at a time
         const int streams = even ? 2 : 1, walks = even && both ? 2 : 1;
         const double item = L.per_run * (walks > 1 ? 2 * 2.1 : 1.4 * streams) + 4 * walks;
-        L.teams = prefix_teams(L.teams, units, L.pairs, p.G,
+        L.teams = prefix_teams(L.teams, units, L.pairs, p.G, edge,
                                std::max<long long>(p.N / L.run_rows, std::min(p.S, p.N)) * L.rslots * p.G / streams, item);
       }
       L.n_flags = std::max(L.n_flags, L.teams * L.pairs);

@@ -130,6 +130,10 @@ struct PrefixShared {
 template <bool kBytes>
 constexpr int kSmem = kBytes ? oShared + (int)sizeof(PrefixShared) : oV + kStages * kTile + 1024;
 static_assert(kSmem<true> <= 232448, "shared memory of a block");
+// (K's and V's barriers lie side by side for the warps that make tiles of both)
+static_assert(offsetof(PrefixShared, kv_full) == offsetof(PrefixShared, k_full) + kStages * 8 &&
+                  offsetof(PrefixShared, v_empty) == offsetof(PrefixShared, k_empty) + kStages * 8,
+              "barriers of V behind those of K");
 
 template <bool kBytes>
 struct PrefixSharedOf {
@@ -196,7 +200,6 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
     paged_prefix_kernel(PrefixArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v) {
   static_assert(kRuns || !kBytes, "8 bits: runs' descriptions always go round");
-  constexpr bool kOwn = kRuns;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = kBytes ? smem_raw
                          : reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -759,7 +762,7 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
         tmem_ld32_max(s_at, *reinterpret_cast<float(*)[32]>(sv), mq[0]);
         tmem_ld32_max(s_at + 32, *reinterpret_cast<float(*)[32]>(sv + 32), mq[1]);
         tmem_wait_ld();
-        if (kOwn && c >= run.masked) {
+        if (kRuns && c >= run.masked) {
           const int seen = run.pos + in + 1 - (run.first + c) * 128 - half * 64;  // keys of this warp's before the row's end
           mq[0] = mq[1] = -INFINITY;
 #pragma unroll
@@ -891,7 +894,7 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
       const int group = run.g + (twin ? t : 0);
       const size_t at = ((size_t)run.slot * a.N + row) * a.Hq + group * a.hg + lrow % a.hg;
       bool odd = false;
-      if (kOwn && run.own) {
+      if (kRuns && run.own) {
         const int* found = sh.odd[(n_run - 1) & 1];
 #pragma unroll
         for (int i = 0; i < 2 * kConverters; ++i) odd |= found[i] != 0;
