@@ -17,7 +17,7 @@
 //
 // Measured: 32,764 rows of 32 + 2 x 8 heads (881 MB) 139 us, 6.3 TB/s, 0.93 of a
 // plain copy; one row 3 us in a graph, which is a launch's time. Into 8 bits 812 MB
-// in 164 us (0.73): twice the instructions for K and V, and what bounds is issuing
+// in 162 us (0.74): twice the instructions for K and V, and what bounds is issuing
 // them.
 //
 // Positions with several axes (kind of token: time, height, width): a pair turns
@@ -410,7 +410,7 @@ cudaError_t launch_paged_append(const PagedProb& p, const PagedCachePtrs& c, con
     if (e != cudaSuccess) return e;
   }
   // Blocks of 128 threads for many long rows, whose waits for one another are shorter then: 32,764 rows of 32 + 2 x 8 heads
-  // take 146 us with 256 threads and 139 with 128 in bf16, 176 and 164 in 8 bits; but 64 of them 4.0 and 5.0 us in a graph, and
+  // take 146 us with 256 threads and 139 with 128 in bf16, 176 and 162 in 8 bits; but 64 of them 4.0 and 5.0 us in a graph, and
   // 2,400 of 8 + 2 x 2 heads, of which a block has four, 8.4 and 10.4.
   const bool small = !a.report && a.items >= 256;
   if (c.bytes()) return small ? launch_append<true, 128>(p, a, st) : launch_append<true, 256>(p, a, st);

@@ -36,10 +36,18 @@ __device__ __forceinline__ float finite_max(float most, float x) {
   const float m = fabsf(x);
   return m < INFINITY ? fmaxf(most, m) : most;
 }
+// (a, b) *= m
+__device__ __forceinline__ void mul2(float& a, float& b, float m) {
+  asm("{\n\t.reg .b64 x, m;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 m, {%2, %2};\n\tmul.rn.f32x2 x, x, m;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(m));
+}
 // Four codes of x * scale (a power of two), rounded to nearest, ties to even; NaN stays NaN.
 __device__ __forceinline__ uint32_t four_codes(float a, float b, float c, float d, float scale) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a * scale, b * scale), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c * scale, d * scale), __NV_SATFINITE, __NV_E4M3);
+  mul2(a, b, scale);
+  mul2(c, d, scale);
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
   return lo | hi << 16;
 }
 
@@ -65,10 +73,9 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
 }
 // The bf16 pair of an fp16 pair of codes times 2^e, exactly.
 __device__ __forceinline__ uint32_t scaled_bf16(uint32_t f16x2, float pow2) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f16x2));
-  float a = f.x, b = f.y;
-  asm("{\n\t.reg .b64 x, m;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 m, {%2, %2};\n\tmul.rn.f32x2 x, x, m;\n\tmov.b64 {%0, %1}, x;\n\t}" : "+f"(a), "+f"(b) : "f"(pow2));
-  return pack_bf16(a, b);
+  float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f16x2));
+  mul2(f.x, f.y, pow2);
+  return pack_bf16(f.x, f.y);
 }
 // Eight codes as eight bf16.
 __device__ __forceinline__ uint4 eight_bf16(uint2 codes, float pow2) {

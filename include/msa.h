@@ -485,7 +485,8 @@ MSA_API msa_status msa_paged_append_axes(const msa_paged_shape *shape, const msa
  * are not supported.
  *
  * The calls below are the ones above over such a cache, their results those of the
- * values it stands for: same batches, limits, errors and NaN; workspaces are sized with the _FP8 values (the append: MSA_WS_PAGED_APPEND).
+ * values it stands for: same batches, limits, errors and NaN. Workspaces are sized
+ * with the _FP8 values (the append's with MSA_WS_PAGED_APPEND).
  * Powers of two of a query and a key (a value) whose product leaves fp32's range
  * may give infinities or zeros where the exact score would not.
  */
