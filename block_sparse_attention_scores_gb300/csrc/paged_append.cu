@@ -410,7 +410,7 @@ cudaError_t launch_paged_append(const PagedProb& p, const PagedCachePtrs& c, con
     if (e != cudaSuccess) return e;
   }
   // Blocks of 128 threads for many long rows, whose waits for one another are shorter then: 32,764 rows of 32 + 2 x 8 heads
-  // take 146 us with 256 threads and 139 with 128 in bf16, 176 and 162 in 8 bits; but 64 of them 4.0 and 5.0 us in a graph, and
+  // take 146 us with 256 threads and 139 with 128 in bf16, 170 and 162 in 8 bits; but 64 of them 4.0 and 5.0 us in a graph, and
   // 2,400 of 8 + 2 x 2 heads, of which a block has four, 8.4 and 10.4.
   const bool small = !a.report && a.items >= 256;
   if (c.bytes()) return small ? launch_append<true, 128>(p, a, st) : launch_append<true, 256>(p, a, st);
