@@ -28,15 +28,15 @@ struct ReadArgs {
   int* err;
 };
 
-// Place in the pools (page * 128 + slot) of row r of the result, which is one of sequence s or a later one; -1 behind the
-// last sequence, or where there is no such token (what is wrong: bad).
+// Place in the pools (page * 128 + slot) of row r of the result, which is one of sequence s or a later one; -1 before the
+// first sequence and behind the last one, or where there is no such token (what is wrong: bad).
 __device__ __forceinline__ int place_of(const ReadArgs& a, int s, int r, int& bad) {
   const auto start = [&](int i) { return __ldg(a.out_start + i); };
   bad = 0;
   if (r >= a.M || s >= a.S) return -1;
   if (start(s + 1) <= r) s = bisect_rows(start, a.S, r);
-  if (s >= a.S) return -1;
-  const long long token = (a.first ? (long long)__ldg(a.first + s) : 0) + (r - start(s));
+  if (s >= a.S || r < start(s)) return -1;  // (the searches take the first start for 0)
+  const long long token = (a.first ? (long long)__ldg(a.first + s) : 0LL) + r - start(s);
   if (token < 0 || token >= __ldg(a.seq_len + s) || token >= a.max_blocks * 128) {
     bad = 1221;
     return -1;

@@ -392,7 +392,7 @@ def msa_paged_dense_attn_fp8(shape, cache, Q, O, LSE, workspace, stream=None) ->
 def msa_paged_read_fp8(shape, cache, first, out_start, K_out, V_out, k_idx_out, workspace, stream=None) -> None:
     """Tokens of a PagedCacheFp8 as bf16: rows out_start[s] .. out_start[s + 1] - 1 of K_out, V_out [M, G, 128] and
     k_idx_out [M, 64] (or None) are the tokens from first[s] on of sequence s (first None: from its beginning).
-    first [S] and out_start [S + 1] are int32."""
+    first [S] and out_start [S + 1] are int32; rows before out_start[0] and from out_start[S] on are left alone."""
     _is(PagedCacheFp8, cache)
     cache.check(shape)
     dev, i32, M = cache._device, _torch.int32, K_out.shape[0]

@@ -510,8 +510,8 @@ MSA_API msa_status msa_paged_append_fp8(const msa_paged_shape *shape, const msa_
  * Tokens back as bf16, exactly the values that the cache stands for: row r of the
  * M rows, out_start[s] <= r < out_start[s+1], is token first[s] + r - out_start[s]
  * of sequence s (first NULL: from the first token on), K_out and V_out [M, G, d],
- * k_idx_out [M, d_idx] (NULL: not wanted), all bf16 and 32-byte aligned. Rows from
- * out_start[S] on are left alone. A token past seq_len[s] or a page outside the
+ * k_idx_out [M, d_idx] (NULL: not wanted), all bf16 and 32-byte aligned. Rows before
+ * out_start[0] and from out_start[S] on are left alone. A token past seq_len[s] or a page outside the
  * pools is reported in the error word and its row left alone. cache->row_start and
  * shape->N, Hq, k are not used. M <= 2^28. first and out_start [S], [S + 1] are
  * device memory.
