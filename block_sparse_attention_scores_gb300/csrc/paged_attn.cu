@@ -880,7 +880,7 @@ __global__ void __launch_bounds__(kMergeThreads, 6) paged_merge_kernel(MergeArgs
       acc.w = fmaf(w, v[j].w, acc.w);
     }
   }
-  const float inv = 1.f / den;
+  const float inv = den == 0.f ? 0.f : 1.f / den;  // (no part has a score above -infinity)
   const uint2 out = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
   reinterpret_cast<uint2*>(a.O + (size_t)item * 128)[lane] = out;
   if (lane == 0) a.LSE[item] = (m + log2f(den)) * 0.6931471805599453f;

@@ -4,9 +4,13 @@ import numpy as np
 import pytest
 
 import paged_fp8_ref as ref8
-from test_paged_fp8_gpu import msa  # noqa: F401
+import paged_ref as ref
+from test_paged_fp8_gpu import SCALES, _dense, msa  # noqa: F401
+from test_paged_gpu import _dense as _dense16
 
 pytestmark = pytest.mark.gpu
+
+INF = float("inf")
 
 
 # ----------------------------------------------------------------- reading back
@@ -38,3 +42,39 @@ def test_read_leaves_the_rows_before_the_first_sequence_alone(msa, start, count,
         page, slot = b.table[s, token // 128].long(), token % 128
         assert torch.equal(K[rows].cpu(), b.K[page, :, slot]) and torch.equal(V[rows].cpu(), b.V[page, :, slot])
         assert torch.equal(ki[rows].cpu(), b.k_idx[page, slot])
+
+
+# ----------------------------------------------------------------- scores
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("name", SCALES)
+def test_infinite_queries(msa, name, bits):  # noqa: F811
+    """Every score of such a head is an infinity: with all of them negative the row sees nothing (O = 0, LSE = -infinity), one
+    positive makes it NaN; keys far below 1 change nothing of that, and the other heads of the rows have the same bits."""
+    import torch
+
+    dense = _dense if bits == 8 else _dense16
+
+    def change(b):
+        b.K *= 2.0 ** -60
+        b.K[..., 5] = b.K[..., 5].abs() + 2.0 ** -61
+
+    if bits == 8:
+        b = ref8.Batch(seed=8, change=change, **SCALES[name])
+    else:
+        b = ref.Batch(seed=8, **SCALES[name])
+        change(b)
+    clean = dense(msa, b)
+    r = b.n - 1
+    page, slot = int(b.table[b.row_seq[r], b.row_pos[r] // 128]), b.row_pos[r] % 128
+    b.Q[r, 0] = 0.0
+    b.Q[r, 0, 5] = -INF
+    O, LSE = dense(msa, b)
+    assert bool((O[r, 0] == 0).all()) and float(LSE[r, 0]) == -INF
+    assert torch.equal(O[r, 1:], clean[0][r, 1:]) and torch.equal(O[:r], clean[0][:r]) and torch.equal(LSE[:r], clean[1][:r])
+    # the row's own token: its score is +infinity
+    if bits == 8:
+        b.K8.view(torch.uint8)[page, 0, slot, 5] |= 128
+    else:
+        b.K[page, 0, slot, 5] *= -1
+    O, LSE = dense(msa, b)
+    assert bool(O[r, 0].isnan().all()) and not bool(O[r, b.hg:].isnan().any())
