@@ -424,7 +424,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int ks = 0; ks < 8; ++ks) most = finite_max2(finite_max2(most, qb[ks][0]), qb[ks][1]);
 #pragma unroll
         for (int x = 1; x < 4; x <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
-        const uint32_t byte = query_scale_byte(most);
+        // a query with infinities has no other scores than infinities and NaN: no scale, which a key's power of two could
+        // take below fp32's range (0 times infinity)
+        bool infinite = false;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+          for (int z = 0; z < 2; ++z) infinite |= !(fabsf(lo_f(qb[ks][z])) < INFINITY) || !(fabsf(hi_f(qb[ks][z])) < INFINITY);
+        const uint32_t any = __ballot_sync(0xffffffffu, infinite) >> (lane & 28) & 15;
+        const uint32_t byte = any ? 127u : query_scale_byte(most);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
@@ -478,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float x[8], top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // s + f; the maxima of s, then of s + f
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            float v = sc[i] * exp_value(exps[8 * (i >> 1)]) * qscale[i & 1];
+            float v = sc[i] * (exp_value(exps[8 * (i >> 1)]) * qscale[i & 1]);  // (a sum times one of them may pass fp32)
             if (masked && token0 + r + (i >> 1) * 8 >= lim[i & 1]) v = -INFINITY;
             sc[i] = v;
             top[i & 1] = fmaxf(top[i & 1], v);

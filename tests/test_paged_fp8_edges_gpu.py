@@ -5,7 +5,7 @@ import pytest
 
 import paged_fp8_ref as ref8
 import paged_ref as ref
-from test_paged_fp8_gpu import SCALES, _dense, msa  # noqa: F401
+from test_paged_fp8_gpu import SCALES, _all, _check_padding, _dense, msa  # noqa: F401
 from test_paged_gpu import _dense as _dense16
 
 pytestmark = pytest.mark.gpu
@@ -45,6 +45,23 @@ def test_read_leaves_the_rows_before_the_first_sequence_alone(msa, start, count,
 
 
 # ----------------------------------------------------------------- scores
+@pytest.mark.parametrize("up,down", [(90, -90), (112, -98), (118, -103), (-90, 90), (-114, 114)])
+@pytest.mark.parametrize("name", SCALES)
+def test_scores_of_far_powers_of_two(msa, name, up, down):  # noqa: F811
+    """Keys of 2^up and queries of 2^down: their scores fit, whatever is multiplied first. One head's queries are smaller."""
+    def change(b):
+        b.K *= 2.0 ** up
+        b.Q *= 2.0 ** down
+        b.Q[:, 1] *= 2.0 ** -3
+
+    b = ref8.Batch(seed=7, change=change, **SCALES[name])
+    O, LSE = _dense(msa, b)
+    assert bool(LSE[:b.n].isfinite().all()) and bool(O[:b.n].isfinite().all())
+    rows = range(b.n) if b.n < 30 else range(0, b.n, 7)
+    ref8.check_attention(b, rows, range(0, b.Hq, 1 if b.Hq <= 8 else 5), O, LSE, _all(b), bf16_p=ref8.tiles(b))
+    _check_padding(b, O, LSE)
+
+
 @pytest.mark.parametrize("bits", [8, 16])
 @pytest.mark.parametrize("name", SCALES)
 def test_infinite_queries(msa, name, bits):  # noqa: F811
