@@ -18,7 +18,7 @@
 namespace msa {
 
 // Exponents are kept in [-117, 120]: 448 * 2^120 is above every bf16, and the smallest code, 2^-9, times 2^-117 is the
-// smallest normal number.
+// smallest normal number. (With 2^120, what rounds to 256 = 0x78 is 2^128: an infinity in bf16 and fp32.)
 constexpr int kLeastExp = 10, kMostExp = 247;
 
 // The byte of a vector whose largest finite magnitude is `most`.
@@ -71,7 +71,7 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 v = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// The bf16 pair of an fp16 pair of codes times 2^e, exactly.
+// The bf16 pair of an fp16 pair of codes times 2^e, exactly (2^128: an infinity).
 __device__ __forceinline__ uint32_t scaled_bf16(uint32_t f16x2, float pow2) {
   float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f16x2));
   mul2(f.x, f.y, pow2);

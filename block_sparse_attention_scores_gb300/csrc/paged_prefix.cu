@@ -661,7 +661,8 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
         const Run& run = sh.run[(n_run - 1) & 1];
         const int tiles = run.twin ? run.pages * 2 : run.pages;
         bool odd = false;
-        // this half of the CTA's tile kc of K (v = 0) or V; keys from `behind` on become zeros, NaN among those from `own` on too
+        // this half of the CTA's tile kc of K (v = 0) or V; keys from `behind` on become zeros, and what is not finite among
+        // those from `own` on
         auto make_half = [&](auto v, int own, int behind) {
           const int st = kc % kStages, bar = v * kRaw + half;
           if (!mbar_wait(&sh.k_empty[st] + v * kStages, ((kc / kStages) & 1) ^ 1, err, 1503 + v)) return false;
@@ -675,11 +676,13 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
             uint32_t byte = exps[j];
             const int key = key0 + j;
             if (v && key >= own) {
-              // (0x7f, the only code that is not finite, plus 1 has the top bit)
+              // What is not finite as bf16: code 0x7f (plus 1 it has the top bit), and with the largest power of two the codes
+              // from 0x78 = 256 on (plus 8).
+              const uint32_t plus = byte >= (uint32_t)kMostExp ? 0x08080808u : 0x01010101u;
               auto clean = [&](uint32_t& w) {
-                const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                odd |= nan != 0 && key < behind;
-                w = key < behind ? w & ~((nan >> 7) * 0xffu) : 0u;
+                const uint32_t wide = ((w & 0x7f7f7f7fu) + plus) & 0x80808080u;
+                odd |= wide != 0 && key < behind;
+                w = key < behind ? w & ~((wide >> 7) * 0xffu) : 0u;
               };
               clean(w.x); clean(w.y); clean(w.z); clean(w.w);
               if (key >= behind) byte = 0;
@@ -914,10 +917,11 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
             const int page = ld_in(a.page_table + (size_t)run.seq * a.max_blocks + k / 128);
             if (page < 0 || page >= a.num_pages) continue;
             const size_t at = (((size_t)page * a.G + group) * 128 + k % 128) * 128 + half * 64 + z * 16;
+            const uint32_t wide = kBytes && a.V_exp[at >> 7] >= kMostExp ? 0x78u : 0x7fu;  // (kBytes) the first such code
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               if constexpr (kBytes) {
-                if ((static_cast<const uint8_t*>(a.V)[at + i] & 0x7f) == 0x7f) o[i] = NAN;
+                if ((static_cast<const uint8_t*>(a.V)[at + i] & 0x7fu) >= wide) o[i] = NAN;
               } else {
                 const float x = __bfloat162float(static_cast<const __nv_bfloat16*>(a.V)[at + i]);
                 if (!(fabsf(x) < INFINITY)) o[i] += x;

@@ -481,8 +481,11 @@ MSA_API msa_status msa_paged_append_axes(const msa_paged_shape *shape, const msa
  *   code_i = x_i * 2^-e rounded to nearest, ties to even,
  * so a value is off by 2^-4 of itself at most (2^-10 * 2^e where that is more).
  * Values that are not finite become NaN (E4M3 has no infinity) and count for
- * nothing in e. The values are exact in bf16. Bytes other than 10 .. 247 (those e)
- * are not supported.
+ * nothing in e. The values are exact in bf16, but for magnitudes from 248 * 2^120 on
+ * (bf16 ends at 255 * 2^120): they round to 256 * 2^120 = 2^128, which is read back
+ * as an infinity. A row that sees such a key may have any result, one that sees
+ * such a value of V any in that dim; other rows and dims are not reached by it.
+ * Bytes other than 10 .. 247 (those e) are not supported.
  *
  * The calls below are the ones above over such a cache, their results those of the
  * values it stands for: same batches, limits, errors and NaN. Workspaces are sized

@@ -5,7 +5,7 @@ import pytest
 
 import paged_fp8_ref as ref8
 import paged_ref as ref
-from test_paged_fp8_gpu import SCALES, _all, _check_padding, _dense, msa  # noqa: F401
+from test_paged_fp8_gpu import SCALES, TILES, _all, _check_padding, _dense, msa  # noqa: F401
 from test_paged_gpu import _dense as _dense16
 
 pytestmark = pytest.mark.gpu
@@ -95,3 +95,52 @@ def test_infinite_queries(msa, name, bits):  # noqa: F811
         b.K[page, 0, slot, 5] *= -1
     O, LSE = dense(msa, b)
     assert bool(O[r, 0].isnan().all()) and not bool(O[r, b.hg:].isnan().any())
+
+# ----------------------------------------------------------------- the largest magnitudes
+@pytest.mark.parametrize("name", [*SCALES, *TILES])
+def test_codes_past_the_largest_number_reach_their_rows_alone(msa, name):  # noqa: F811
+    """The last token's V has a value that the format rounds to 2^128. The rows that see it may have any value in its dim;
+    everything else has the same bits as with a zero there."""
+    import torch
+
+    kw = {**SCALES, **TILES}[name]
+    b = ref8.Batch(seed=10, **kw)
+
+    def put(code, d):
+        for s in range(b.S):
+            t = b.lens[s] - 1
+            if b.counts[s]:
+                at = (int(b.table[s, t // 128]), slice(None), t % 128)
+                b.V_exp[at] = 247
+                b.V8.view(torch.uint8)[at] = 0
+                b.V8.view(torch.uint8)[(*at, d)] = code
+
+    put(0, 0)
+    clean = _dense(msa, b)
+    for code, d in ((0x78, 3), (0xfe, 77), (0x7b, 126)):
+        put(code, d)
+        O, LSE = _dense(msa, b)
+        assert torch.equal(LSE[:b.n], clean[1][:b.n])
+        other = torch.arange(128) != d
+        for r in range(b.n):
+            if b.row_pos[r] == b.lens[b.row_seq[r]] - 1:
+                assert torch.equal(O[r][:, other], clean[0][r][:, other]), r
+            else:
+                assert torch.equal(O[r], clean[0][r]), r
+
+
+def test_append_and_read_of_the_largest_magnitudes(msa):  # noqa: F811
+    """Up to where a code of 2^120 rounds to 256 a value comes back within 2^-4 of itself; from there on as an infinity."""
+    import torch
+
+    top = torch.arange(0x7f00, 0x7f80, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)  # 2^127 and more
+    x = torch.stack([top, -top])[:, None]
+    b = ref8.Batch(counts=[2], lens=[2], Hq=1, G=1)
+    shape, cache, t = b.gpu()
+    msa.paged_append_fp8(shape, cache, msa.Rope(), x.cuda(), x.cuda(), x[:, 0, :64].contiguous().cuda())
+    K, V, _ = msa.paged_read_fp8(shape, cache, torch.tensor([0, 2], dtype=torch.int32, device="cuda"), 2)
+    for got in (K.cpu().double(), V.cpu().double()):
+        y = x.double()
+        fits = y.abs() < 248 * 2.0 ** 120
+        assert bool(((got - y).abs() <= 2.0 ** -4 * y.abs())[fits].all())
+        assert bool((got[~fits] == y[~fits].sign() * INF).all()) and int((~fits).sum()) == 2 * 8
