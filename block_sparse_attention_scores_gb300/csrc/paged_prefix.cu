@@ -304,7 +304,6 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
 
   // (kBytes) The block starts with 72 registers a thread; the warps that make tiles give some of theirs to the softmax.
   static_assert(!kBytes || 512 * 88 + 128 * (72 + 2 * 40) <= 896 * 72, "registers of a block");
-  if (warp < 4) {
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
     tma_prefetch_desc(&map_q);
@@ -320,8 +319,9 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
     };
     if constexpr (kRuns) {
       // The prefix's runs first, as below, then the sequences' own ones as they come. A run's first 32 pages are looked
-      // up ahead, one step a page: the number, the rows, the pages; on the last pages of the run before, as what is taken
-      // earlier is not there for a CTA that is free.
+      // up ahead, one step a page: the number, the rows, the pages. Behind a prefix on the last pages of the run before, as
+      // what is taken earlier is not there for a CTA that is free; without one on its first pages (all CTAs take their
+      // runs at the same times: one sequence's 300 rows x 32 heads over 4 groups and 8000 tokens 64 us, 74 on the last).
       struct Ahead {
         Run run;
         int y;  // of this lane's page
@@ -335,12 +335,12 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
       auto step1 = [&]() {
         own_now = second || u >= u_end;
         if (!own_now || second) return;
-        if ((a.prefix || ++own > 0) && lane == 0) taken = atomicAdd(a.header + kRunNext, 1);
+        if (((kShared && a.prefix) || ++own > 0) && lane == 0) taken = atomicAdd(a.header + kRunNext, 1);
       };
       auto step2 = [&]() {
         if (!own_now || second) return;
         const int next = __shfl_sync(0xffffffffu, taken, 0);  // (behind a prefix the first one, too: whoever is free takes it)
-        id = a.prefix ? next : own ? gridDim.x + next : blockIdx.x;
+        id = kShared && a.prefix ? next : own ? gridDim.x + next : blockIdx.x;
         if (id < items) lead = ld_in(a.runs + id / (a.rslots * (a.G / pair_g)));
       };
       auto step3 = [&](Ahead& h) {
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
           }
           __syncwarp();
           if constexpr (kBytes) load_codes(true, at);
-          if (step < 3 && i + 4 >= now.run.pages * streams) find(next, step++);
+          if (step < 3 && (!kShared || i + 4 >= now.run.pages * streams)) find(next, step++);
         }
         ++n_run;
         for (; step < 3; ++step) find(next, step);
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
         }
       }
     }
-  } else {
+  } else if (warp < 4) {
     // ---------------------------------------------------------------- V of the sequences' own pages
     if constexpr (kRuns && !kBytes) {
       // Two warps for V. The first loads it; K has a producer of its own (and arrives a softmax earlier), so that neither
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
         const int streams = run.twin ? 2 : 1;
         int y = 0;
         if (warp == 2) y = table_row(run, lane);
-        else if (lane < 2 * kConverters) sh.odd[(n_run - 1) & 1][lane] = 0;
+        else if (lane == 0) sh.odd[(n_run - 1) & 1][0] = 0;
         __syncwarp();
         for (int i = 0; i < run.pages * streams; ++i, ++kc) {
           const int st = kc % kStages, page = run.twin ? i >> 1 : i, other = run.twin ? i & 1 : 0;
@@ -641,7 +641,6 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
         run_done(false);
       }
     }
-  }
   } else if (kBytes && warp >= 20) {
     // ---------------------------------------------------------------- codes to bf16 tiles
     if constexpr (kBytes) {
@@ -900,7 +899,7 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
       if (kRuns && run.own) {
         const int* found = sh.odd[(n_run - 1) & 1];
 #pragma unroll
-        for (int i = 0; i < 2 * kConverters; ++i) odd |= found[i] != 0;
+        for (int i = 0; i < (kBytes ? 2 * kConverters : 1); ++i) odd |= found[i] != 0;
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;  // (a run behind the row's end, or scores of -infinity)
       float* dst = a.part_o + at * 128 + half * 64;
