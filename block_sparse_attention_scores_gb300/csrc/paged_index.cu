@@ -318,13 +318,16 @@ __device__ __forceinline__ float from_key(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-// The index keys of a page: eight values, or two, of a key as bf16 (the codes' values are exact in it).
+// The index keys of a page: eight values, or two, of a key as bf16 (the codes' values are exact in it). The functions that
+// are calls of their own take its address (an object of this as argument cost the 1024-thread selection 28 bytes of spills).
 template <bool kBytes>
 struct PageKeys;
 template <>
 struct PageKeys<false> {
-  const __nv_bfloat16* page;
-  __device__ __forceinline__ PageKeys(const SelectArgs& a, int at) : page(static_cast<const __nv_bfloat16*>(a.k_idx) + (size_t)at * 128 * 64) {}
+  using Page = const __nv_bfloat16*;
+  Page page;
+  static __device__ __forceinline__ Page of(const SelectArgs& a, int at) { return static_cast<Page>(a.k_idx) + (size_t)at * 128 * 64; }
+  __device__ __forceinline__ explicit PageKeys(Page p) : page(p) {}
   __device__ __forceinline__ uint4 eight(int key, int c) const { return ld_in(reinterpret_cast<const uint4*>(page + key * 64) + c); }
   __device__ __forceinline__ uint32_t two(int key, int i) const {
     return ld_in(reinterpret_cast<const uint32_t*>(page + key * 64) + i);
@@ -332,9 +335,14 @@ struct PageKeys<false> {
 };
 template <>
 struct PageKeys<true> {
+  struct Page {
+    const uint8_t *codes, *exps;
+  };
   const uint8_t *page, *exps;
-  __device__ __forceinline__ PageKeys(const SelectArgs& a, int at)
-      : page(static_cast<const uint8_t*>(a.k_idx) + (size_t)at * 128 * 64), exps(a.k_exp + (size_t)at * 128) {}
+  static __device__ __forceinline__ Page of(const SelectArgs& a, int at) {
+    return {static_cast<const uint8_t*>(a.k_idx) + (size_t)at * 128 * 64, a.k_exp + (size_t)at * 128};
+  }
+  __device__ __forceinline__ explicit PageKeys(Page p) : page(p.codes), exps(p.exps) {}
   __device__ __forceinline__ uint4 eight(int key, int c) const {
     return eight_bf16(__ldcg(reinterpret_cast<const uint2*>(page + key * 64) + c), exp_value(__ldcg(exps + key)));
   }
@@ -362,7 +370,8 @@ struct Units {
 
 // The largest of a block's scores for a query (64 bf16 at q), by one warp, a key per lane. NaN where a product is cut.
 template <class Keys>
-__device__ __noinline__ double integer_max(Keys keys, const __nv_bfloat16* q, float most, int lane) {
+__device__ __noinline__ double integer_max(typename Keys::Page at, const __nv_bfloat16* q, float most, int lane) {
+  const Keys keys(at);
   const Units units(most);
   long long top = -0x7fffffffffffffffll;
   bool cut = false;
@@ -393,7 +402,8 @@ __device__ __forceinline__ void add_exactly(double& s, double& e, double t, doub
 
 // The largest score among the keys of `near` (of lane i: the keys 32 i + bit), by one warp, two dims per lane.
 template <class Keys>
-__device__ __noinline__ double double_max(Keys keys, uint32_t qq, unsigned near, int lane) {
+__device__ __noinline__ double double_max(typename Keys::Page at, uint32_t qq, unsigned near, int lane) {
+  const Keys keys(at);
   double top = -INFINITY;
 #pragma unroll 1
   for (int i = 0; i < 4; ++i)
@@ -422,7 +432,8 @@ __device__ __noinline__ double double_max(Keys keys, uint32_t qq, unsigned near,
 // additions lose. A score is the same number in whichever way: one that was
 // rounded in between could part equal keys.
 template <class Keys>
-__device__ __noinline__ double exact_max(Keys keys, const __nv_bfloat16* q, float margin, float qmax, float kmax, int lane) {
+__device__ __noinline__ double exact_max(typename Keys::Page at, const __nv_bfloat16* q, float margin, float qmax, float kmax, int lane) {
+  const Keys keys(at);
   float s32[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -459,7 +470,7 @@ __device__ __noinline__ double exact_max(Keys keys, const __nv_bfloat16* q, floa
   double t = NAN;
   if (most >= 0x1p-60f && most <= 0x1p90f) {
     if (many > 8) {
-      t = integer_max(keys, q, most, lane);
+      t = integer_max<Keys>(at, q, most, lane);
     } else {
       const Units units(most);
       long long top = -0x7fffffffffffffffll;
@@ -477,7 +488,7 @@ __device__ __noinline__ double exact_max(Keys keys, const __nv_bfloat16* q, floa
       if (!__any_sync(0xffffffffu, cut)) t = (double)top * units.unit;
     }
   }
-  return t == t ? t : double_max(keys, qq, near, lane);
+  return t == t ? t : double_max<Keys>(at, qq, near, lane);
 }
 
 // One block per (row, group). A thread keeps its blocks' lower bounds (as
@@ -641,7 +652,7 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(SelectArgs a) {
       double t = -INFINITY;
       if (page < 0 || page >= a.num_pages) t = -INFINITY;  // (reported)
       else if ((qmax == 0.f || top == 0.f) && qmax < INFINITY && top < INFINITY) t = 0.;  // nothing but zeros
-      else t = exact_max(PageKeys<kBytes>(a, page), q, margin, qmax, top, lane);
+      else t = exact_max<PageKeys<kBytes>>(PageKeys<kBytes>::of(a, page), q, margin, qmax, top, lane);
       if (lane == 0) score[i] = t;
     }
     __syncthreads();
