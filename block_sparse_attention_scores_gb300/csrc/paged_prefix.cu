@@ -154,20 +154,6 @@ __device__ __forceinline__ void set_registers() {
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCount) : "memory");
 }
 
-__device__ __forceinline__ uint32_t ld_shared1(uint32_t at) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 ld_shared2(uint32_t at) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
-  return v;
-}
-__device__ __forceinline__ void st_shared(uint32_t at, const uint4& v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
 // (x0, x1) * a + b, two at a time.
 __device__ __forceinline__ void fma2(float& x0, float& x1, float a, float b) {
   asm("{\n\t.reg .b64 x, m, n;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 m, {%2, %2};\n\tmov.b64 n, {%3, %3};\n\t"
@@ -647,7 +633,7 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
       set_registers<40, false>();
       // Eight threads a key, 16 codes each: a warp takes four keys at a time. A thread's two halves go into one of the
       // tile's 64-column chunks; the upper chunk's threads take theirs the other way round, so that the eight threads of a
-      // key meet in no bank. (Addresses in shared memory, 32 bits, with what does not change added up before.)
+      // key meet in no bank. (What does not change of the addresses is added up before.)
       const int half = (warp - 20) / kConverters, key0 = half * kHalfKeys + (warp & (kConverters - 1)) * 4 + (lane >> 3);
       const int piece = lane & 7, up = piece >> 2, c0 = (((piece & 3) * 2 + up) ^ (key0 & 7)) << 4;
       const uint8_t* const raw0 = smem + oRawK + key0 * 128 + piece * 16;
