@@ -399,8 +399,8 @@ static msa_status dense_attn(const msa_paged_shape* shape, const Cache* cache, i
   if ((s = check_device()) != MSA_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  PoolMaps maps;
-  if ((s = encode_pools(p, c, &maps)) != MSA_OK) return s;
+  PoolMaps maps{};  // (128-row tiles of codes have no use for them)
+  if (!(c.bytes() && L.run_rows) && (s = encode_pools(p, c, &maps)) != MSA_OK) return s;
   const bool parts = L.prefix || L.run_rows;
   if ((s = cuda_status(launch_paged_rows(p, c, w, L, st), "paged rows launch")) != MSA_OK) return s;
   if (parts && (s = cuda_status(launch_paged_prefix(p, c, maps, Q, w, L, st), "paged prefix launch")) != MSA_OK) return s;

@@ -293,8 +293,10 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
     tma_prefetch_desc(&map_q);
-    tma_prefetch_desc(&map_k);
-    tma_prefetch_desc(&map_v);
+    if constexpr (!kBytes) {  // (codes come by plain bulk copies)
+      tma_prefetch_desc(&map_k);
+      tma_prefetch_desc(&map_v);
+    }
     auto load_tile = [&](int at, const CUtensorMap* map, uint64_t* bar, int y) {
       tma_load_2d(smem + at, map, bar, 0, y);
       tma_load_2d(smem + at + kChunk, map, bar, 64, y);
