@@ -5,7 +5,8 @@ import pytest
 
 import paged_fp8_ref as ref8
 import paged_ref as ref
-from test_paged_fp8_gpu import SCALES, TILES, _all, _check_padding, _dense, msa  # noqa: F401
+from test_paged_fp8_gpu import (DENSE, SCALES, SPARSE, TILES, _all, _check_padding, _check_sparse, _dense, _sparse,  # noqa: F401
+                                msa)
 from test_paged_gpu import _dense as _dense16
 
 pytestmark = pytest.mark.gpu
@@ -144,3 +145,50 @@ def test_append_and_read_of_the_largest_magnitudes(msa):  # noqa: F811
         fits = y.abs() < 248 * 2.0 ** 120
         assert bool(((got - y).abs() <= 2.0 ** -4 * y.abs())[fits].all())
         assert bool((got[~fits] == y[~fits].sign() * INF).all()) and int((~fits).sum()) == 2 * 8
+
+
+# ----------------------------------------------------------------- probabilities
+@pytest.mark.parametrize("name", [*DENSE, *SCALES])
+def test_probabilities_by_eight_columns_have_eleven_bits(msa, name):  # noqa: F811
+    """Two launches: eight columns at a time, whatever the batch's shape, also where they read a small shared prefix."""
+    b = ref8.Batch(seed=6, **{**DENSE, **SCALES}[name])
+    before = msa.msa_kernel_launches()
+    O, LSE = _dense(msa, b)
+    if msa.msa_kernel_launches() - before > 2:
+        assert b.prefix or b.N * b.hg > 20 * b.S
+        pytest.skip("128-row tiles")
+    rows = range(b.n) if b.n < 30 else range(0, b.n, 7)
+    ref8.check_attention(b, rows, range(0, b.Hq, 1 if b.Hq <= 8 else 5), O, LSE, _all(b))
+    _check_padding(b, O, LSE)
+
+
+@pytest.mark.parametrize("rows", [2, 3])
+def test_up_to_twenty_columns_a_sequence_have_eleven_bits(msa, rows):  # noqa: F811
+    """Without a prefix 128-row tiles take batches of more than 20 columns (rows x heads of a group) a sequence alone."""
+    b = ref8.Batch(counts=[rows] * 20, lens=[1100 + 7 * i for i in range(20)], Hq=64, G=8, seed=6)
+    before = msa.msa_kernel_launches()
+    O, LSE = _dense(msa, b)
+    assert msa.msa_kernel_launches() - before == (2 if rows == 2 else 3)
+    ref8.check_attention(b, range(0, b.n, 7), range(0, 64, 5), O, LSE, _all(b), bf16_p=rows == 3)
+
+
+# ----------------------------------------------------------------- tables as wide as a serving program's
+@pytest.mark.parametrize("width", [200, 8192])
+@pytest.mark.parametrize("name", ["rows_hg2_idle", "g8_long", "runs_hg8", "tokens", "shared", "prefix", "hg8_one_tile", "drafts",
+                                  "two_rows"])
+def test_dense_over_wide_tables(msa, name, width):  # noqa: F811
+    """Columns past the sequences' ends (-1) change the cuts and nothing else."""
+    b = ref8.Batch(seed=6, max_blocks=width, **{**DENSE, **SCALES, **TILES}[name])
+    O, LSE = _dense(msa, b)
+    rows = range(b.n) if b.n < 30 else range(0, b.n, 7)
+    ref8.check_attention(b, rows, range(0, b.Hq, 1 if b.Hq <= 8 else 5), O, LSE, _all(b), bf16_p=ref8.tiles(b))
+    _check_padding(b, O, LSE)
+
+
+@pytest.mark.parametrize("width", [200, 8192])
+@pytest.mark.parametrize("name", ["first_token", "hg2_idle_padding", "hg8_rows", "many_rows"])
+def test_sparse_over_wide_tables(msa, name, width):  # noqa: F811
+    kw = dict(SPARSE[name])
+    k = kw.pop("k")
+    b = ref8.Batch(seed=3, max_blocks=width, **kw)
+    _check_sparse(b, k, *_sparse(msa, b, k))
