@@ -77,6 +77,16 @@ __device__ __forceinline__ uint4 eight_bf16(uint2 codes, float pow2) {
   return make_uint4(scaled_bf16(f16_lo(codes.x), pow2), scaled_bf16(f16_hi(codes.x), pow2),
                     scaled_bf16(f16_lo(codes.y), pow2), scaled_bf16(f16_hi(codes.y), pow2));
 }
+// Eight codes as eight fp16, times a pair of equal fp16 powers of two.
+__device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint4 eight_f16(uint2 codes, uint32_t pow2) {
+  return make_uint4(mul_f16(f16_lo(codes.x), pow2), mul_f16(f16_hi(codes.x), pow2), mul_f16(f16_lo(codes.y), pow2),
+                    mul_f16(f16_hi(codes.y), pow2));
+}
 
 // A query as fp16, for products with codes: times the power of two that brings its largest finite magnitude into
 // [2^14, 2^15), so that its values are exact down to 2^-28 of that and off by 2^-39 of it at most below (magnitudes under

@@ -51,14 +51,23 @@
 // A cache in 8 bits (kBytes, paged_fp8.cuh): the same products of the values that
 // the codes stand for, which bf16 holds exactly. Codes arrive by plain bulk copies,
 // half a tile at a time (a page's codes of a group lie in a row), and eight warps
-// turn them into the bf16 tiles that the tensor core reads, four a half, K's and then
-// V's of a page: a tile then takes them half of what four warps take, which V's way
-// (copied, converted, multiplied, and its place free again) needs. P is one bf16 for
-// own pages, too: that is below the codes' own rounding by far. What bounds is still
-// the chain above, beside which the conversion takes issue slots and shared memory:
-// the call of 128 x 2 rows x 32 heads behind 256 pages 158 us (145 without the
-// conversion, 132 in bf16), of 32 x 4 rows x 64 heads over 2000 tokens 69 us (64), of
-// 23 drafts of 5 rows x 64 heads behind 64 pages, 700 tokens of their own, 64 us.
+// turn them into the tiles that the tensor core reads, four a half, K's and then V's
+// of a page: a tile then takes them half of what four warps take, which V's way
+// (copied, converted, multiplied, and its place free again) needs. K is bf16, code
+// times power of two. P and V are fp16, which keeps eleven bits of P without a second
+// part (two bf16 parts of P, 32 x 4 rows x 64 heads over 2000 tokens: 85 us, one 68,
+// fp16 69; O's error against 64 bits 0.00165, 0.0023 and 0.00166 of its norm, of which
+// 0.00165 is its own rounding):
+//   V_j = code_j 2^(f_j - F),  P_j = exp2(s_j + F - o),  O_true = O 2^(o - m) / l
+// with f_j the exponent of token j's V, F the page's largest (so a V is exact down to
+// 2^-14 of it), and o a row's reference, which the largest s + F seen stays within 2^15
+// of. l = sum exp2(s_j - m) has a reference of its own. Where a page's f_j lie further
+// apart, V_j = code_j, and P_j = exp2(s_j + f_j - o) has each one's own: what a token adds
+// to O decides what its P may lose. A warp of its own looks at the pages' f_j ahead.
+// What bounds is still the chain above, beside which the conversion takes issue slots and
+// shared memory: the call of 128 x 2 rows x 32 heads behind 256 pages 166 us (131 in
+// bf16), of 32 x 4 rows x 64 heads over 2000 tokens 69 us (60), of 23 drafts of 5 rows x
+// 64 heads behind 64 pages, 700 tokens of their own, 69 us (66).
 // Both tiles' products go through one thread, in turn: two, one for each tile, let the
 // tiles run in step, each waiting for the tensor core and then both in the softmax
 // (the last of these behind 1000 pages 462 -> 530 us).
@@ -69,8 +78,9 @@ namespace msa {
 namespace {
 
 constexpr float kHeadroom = 8.f;  // P = exp2(s - m) stays <= 2^kHeadroom
+constexpr float kFarScore = 60.f; // (kBytes) how far (log2) a page's sum may be from what it is relative to
 // warp 0 TMA, warp 1 UMMA + TMEM, 2 and 3 V of own pages, 4-11 and 12-19 softmax of tiles 0 and 1
-// (kBytes: 20-23 and 24-27 make bf16 tiles of K's and V's codes; 2 and 3 have nothing to do)
+// (kBytes: 20-23 and 24-27 make tiles of K's and V's codes; 2 looks at V's powers of two, 3 has nothing to do)
 template <bool kBytes>
 constexpr int kThreads = kBytes ? 896 : 640;
 constexpr int kTile = 32768;      // 128 rows x 128 bf16, two 64-column SW128 chunks
@@ -83,6 +93,9 @@ constexpr int kHalfKeys = 64, kHalf = kHalfKeys * 128, kRaw = 2;  // halves in f
 constexpr int oRawK = oV + kStages * kTile, oRawV = oRawK + kRaw * kHalf;
 constexpr int oExpK = oRawV + kRaw * kHalf, oExpV = oExpK + kRaw * kHalfKeys;
 constexpr int oShared = oExpV + kRaw * kHalfKeys;                 // PrefixShared
+constexpr int kExps = 8;          // (kBytes) pages whose powers of two of V are known: more than are on their way
+constexpr int kSpread = 14;       // (kBytes) how far below a page's largest power of two of V others are held in fp16
+constexpr float kTopP = 7.f;      // (kBytes) log2 of a page's largest P where the reference is set; it may grow to 2^15
 
 // One run: pages of one group against up to two tiles of rows.
 struct Run {
@@ -94,6 +107,7 @@ struct Run {
   int seq, first;   // whose pages, from which block
   int pos;          // own: position of the first row
   int masked;       // the first page that not every row sees all of
+  int tiles;        // (kBytes) tiles of V before this run's
 };
 
 struct PrefixArgs {
@@ -123,6 +137,7 @@ struct PrefixShared {
   float row_max[2][2][128];      // [tile][half][row] of the page's scores (at the end: the row's sums)
   int raised[2][2][4];           // [tile][half][quarter] the page (counted from 1) at which this warp called the other
   uint64_t raw_full[2 * kRaw], raw_empty[2 * kRaw];  // (kBytes)
+  int v_exps[kExps];  // (kBytes) a page's largest byte of V, plus 256 where others are more than kSpread below it
   uint32_t tmem_base;
 };
 // 8 bits: everything in the dynamic part, which then begins at a multiple of 1024 bytes (there is no room left to align it;
@@ -175,12 +190,39 @@ __device__ __forceinline__ void st_global8(float* p, const float* v) {
                : "memory");
 }
 
+// (kBytes) For a page whose powers of two of V are far apart, a row's 64 scores at s_at: the sum of exp2(s - base) is
+// returned, and s + f - top_v put in their place (in units of the scores), f the exponent of each key's V. `seen` of them
+// count. (A function of its own: inline its code, which hardly ever runs, took the others' place in the instruction cache.)
+__device__ __noinline__ float weigh_scores(uint32_t s_at, float scale_log2, float m_run, float top_v, const uint8_t* exps,
+                                           int seen) {
+  const float base = m_run == -INFINITY ? 0.f : m_run, unit = 1.f / scale_log2;
+  float l = 0.f;
+#pragma unroll 1
+  for (int z = 0; z < 64; z += 8) {
+    float s[8];
+    uint32_t w[8];
+    tmem_ld8(s_at + z, s);
+    tmem_wait_ld();
+    const uint2 f = __ldg(reinterpret_cast<const uint2*>(exps + z));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool in = z + i < seen;
+      const float e = (float)((int)((i < 4 ? f.x : f.y) >> 8 * (i & 3) & 255) - 127);
+      if (in) l += fast_exp2(fmaf(s[i], scale_log2, -base));
+      w[i] = __float_as_uint(in ? fmaf(e - top_v, unit, s[i]) : -INFINITY);
+    }
+    tmem_st8(s_at + z, w);
+  }
+  tmem_wait_st();
+  return l;
+}
+
 // kShared: the call has a shared prefix. Without one every page is a sequence's own, and its P has both parts: told at run
-// time, as where there are both kinds, it costs 2 % (32 x 4 rows x 64 heads over 2000 tokens 63.3 -> 64.9 us). kBytes: with a
-// prefix K and V are converted by the same instructions. Two SMs share the cache that instructions come from, and a CTA in
-// the prefix whose neighbour does something else (own pages, another kernel) lost up to half of its speed to code that was
-// 3 KB longer (128 x 2 rows behind 256 pages 189 -> 159 us; without a prefix, where neighbours do the same, 32 x 4 rows x 64
-// heads over 2000 tokens would take 71 instead of 68).
+// time, as where there are both kinds, it costs 2 % (32 x 4 rows x 64 heads over 2000 tokens 63.3 -> 64.9 us). kBytes: the
+// conversion's code is kept short, K's for two keys at a time (behind a prefix one) and V's for one. Two SMs share the cache
+// that instructions come from, and a CTA in the prefix whose neighbour does something else (own pages, another kernel) loses
+// most: with four keys at a time 128 x 2 rows behind 256 pages take 220 us instead of 166, 23 x 5 rows x 64 heads behind 64
+// pages 83 instead of 71, 32 x 4 over 2000 tokens 74 instead of 69.
 template <bool kRuns, bool kShared, bool kBytes>
 __global__ void __launch_bounds__(kThreads<kBytes>, 1)
     paged_prefix_kernel(PrefixArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -219,14 +261,14 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
     if (kRuns) {
       for (int i = 0; i < 2; ++i) {
         mbar_init(&sh.run_full[i], 1);
-        mbar_init(&sh.run_empty[i], kBytes ? 17 + 2 * kConverters : 19);
+        mbar_init(&sh.run_empty[i], kBytes ? 18 + 2 * kConverters : 19);
         mbar_init(&sh.k_full[i], kBytes ? 2 * kConverters : 1);
         mbar_init(&sh.v_clean[i], 1);
       }
     }
     if (kBytes) {
       for (int i = 0; i < 2 * kRaw; ++i) {
-        mbar_init(&sh.raw_full[i], 1);
+        mbar_init(&sh.raw_full[i], i < kRaw ? 2 : 1);  // (K's: the codes, and what is known of the page's V)
         mbar_init(&sh.raw_empty[i], kConverters);
       }
     }
@@ -386,6 +428,7 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
         if (!mbar_wait(&sh.run_empty[slot], ((n_run >> 1) & 1) ^ 1, err, 1501)) break;
         if (lane == 0) {
           sh.run[slot] = now.run;
+          if (kBytes) sh.run[slot].tiles = kc;
           mbar_arrive(&sh.run_full[slot]);
         }
         __syncwarp();
@@ -483,7 +526,8 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
     // ---------------------------------------------------------------- UMMA issuer
     if (lane == 0) {
       constexpr uint32_t id_s = make_idesc_bf16(128, 128, false, false);  // Q, K both K-major
-      constexpr uint32_t id_o = make_idesc_bf16(128, 128, false, true);   // P from TMEM, V MN-major
+      constexpr uint32_t id_o = kBytes ? make_idesc_f16(128, 128, false, true)   // P from TMEM, V MN-major
+                                       : make_idesc_bf16(128, 128, false, true);
       // the operands' descriptors as 32-bit words: one add per instruction, so that the issuing thread keeps up
       constexpr uint32_t hi = sdesc_hi_sw128_sbo1024();
       const uint32_t q_lo = sdesc_lo(smem_u32(smem + oQ), 16), k_lo = sdesc_lo(smem_u32(smem + oK), 16);
@@ -629,8 +673,53 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
         run_done(false);
       }
     }
+    if constexpr (kBytes) {
+      // Looks at the powers of two of a page's V before anyone needs them; loaded three pages ahead.
+      uint32_t kc = 0;
+      Run none;
+      bool ok = warp == 2;
+      while (ok && next_run(none)) {
+        const Run& run = sh.run[(n_run - 1) & 1];
+        const int streams = run.twin ? 2 : 1, tiles = run.pages * streams;
+        int y = 0;
+        auto load = [&](int i) {
+          const int page = run.twin ? i >> 1 : i, other = run.twin ? i & 1 : 0;
+          if (!other && (page & 31) == 0) y = table_row(run, page + lane);
+          const int at = __shfl_sync(0xffffffffu, y, page & 31) + other * 128;
+          return i < tiles ? ld_in(reinterpret_cast<const uint32_t*>(a.V_exp + at) + lane) : 0u;
+        };
+        uint32_t four = load(0), four1 = load(1), four2 = load(2);
+        for (int i = 0; i < tiles; ++i, ++kc) {
+          const uint32_t four3 = load(i + 3);
+          const int page = run.twin ? i >> 1 : i;
+          const int behind = page >= run.masked ? run.pos + run.rows - (run.first + page) * 128 : 128;
+          uint32_t most = 0, least = 255;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const uint32_t byte = four >> 8 * b & 255;
+            if (lane * 4 + b >= behind) continue;
+            most = max(most, byte);
+            if (byte > kLeastExp) least = min(least, byte);  // (the least one is that of zeros)
+          }
+          most = __reduce_max_sync(0xffffffffu, most);
+          least = __reduce_min_sync(0xffffffffu, least);
+          // with K's codes, so that the converting warps know, and by way of K and its scores the softmax
+          for (int h = 0; h < kRaw && ok; ++h) ok = mbar_wait(&sh.raw_empty[h], (kc & 1) ^ 1, err, 1506);
+          if (!ok) break;
+          if (lane == 0) {
+            sh.v_exps[kc % kExps] = (int)most + (least + kSpread < most ? 256 : 0);
+            for (int h = 0; h < kRaw; ++h) mbar_arrive(&sh.raw_full[h]);
+          }
+          __syncwarp();
+          four = four1;
+          four1 = four2;
+          four2 = four3;
+        }
+        run_done(false);
+      }
+    }
   } else if (kBytes && warp >= 20) {
-    // ---------------------------------------------------------------- codes to bf16 tiles
+    // ---------------------------------------------------------------- codes to tiles
     if constexpr (kBytes) {
       set_registers<40, false>();
       // Eight threads a key, 16 codes each: a warp takes four keys at a time. A thread's two halves go into one of the
@@ -657,28 +746,38 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
           const uint8_t* const raw = raw0 + v * (oRawV - oRawK);
           const uint8_t* const exps = exps0 + v * (oExpV - oExpK);
           uint8_t* const tile = tile0 + (v * kStages + st) * kTile;
-#pragma unroll
+          const int most = v ? sh.v_exps[kc % kExps] : 0;
+#pragma unroll(v || kShared ? 1 : 2)
           for (int j = 0; j < kHalfKeys; j += 4 * kConverters) {
             uint4 w = *reinterpret_cast<const uint4*>(raw + j * 128);
-            uint32_t byte = exps[j];
+            const uint32_t byte = exps[j];
             const int key = key0 + j;
             if (v && key >= own) {
-              // What is not finite as bf16: code 0x7f (plus 1 it has the top bit), and with the largest power of two the codes
-              // from 0x78 = 256 on (plus 8).
-              const uint32_t plus = byte >= (uint32_t)kMostExp ? 0x08080808u : 0x01010101u;
+              // (0x7f, the only code that is not finite, plus 1 has the top bit)
               auto clean = [&](uint32_t& w) {
-                const uint32_t wide = ((w & 0x7f7f7f7fu) + plus) & 0x80808080u;
-                odd |= wide != 0 && key < behind;
-                w = key < behind ? w & ~((wide >> 7) * 0xffu) : 0u;
+                const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                odd |= nan != 0 && key < behind;
+                w = key < behind ? w & ~((nan >> 7) * 0xffu) : 0u;
               };
               clean(w.x); clean(w.y); clean(w.z); clean(w.w);
-              if (key >= behind) byte = 0;
             }
-            const float pow2 = exp_value(byte);
             const uint2 first = up ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y),
                         second = up ? make_uint2(w.x, w.y) : make_uint2(w.z, w.w);
-            *reinterpret_cast<uint4*>(tile + j * 128 + c0) = eight_bf16(first, pow2);
-            *reinterpret_cast<uint4*>(tile + j * 128 + (c0 ^ 16)) = eight_bf16(second, pow2);
+            uint4 x, y;
+            if (v) {
+              const int below = most - (int)byte;  // (of a page with a wide spread, P has the powers of two)
+              const uint32_t pow2 = most & 256                    ? 0x3c003c00u
+                                    : (uint32_t)below <= kSpread ? (uint32_t)(15 - below) * 0x04000400u
+                                                                 : 0u;
+              x = eight_f16(first, pow2);
+              y = eight_f16(second, pow2);
+            } else {
+              const float pow2 = exp_value(byte);
+              x = eight_bf16(first, pow2);
+              y = eight_bf16(second, pow2);
+            }
+            *reinterpret_cast<uint4*>(tile + j * 128 + c0) = x;
+            *reinterpret_cast<uint4*>(tile + j * 128 + (c0 ^ 16)) = y;
           }
           if (v) {
             odd = __any_sync(0xffffffffu, odd);
@@ -700,13 +799,8 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
             behind = min(128, max(0, run.pos + run.rows - token0));
             own = min(behind, max(0, run.pos + 1 - token0));
           }
-          if constexpr (kShared) {
-#pragma unroll 1
-            for (int v = 0; v < 2 && ok; ++v) ok = make_half(v, own, behind);
-          } else {
-            ok = make_half(std::integral_constant<int, 0>(), own, behind) &&
-                 make_half(std::integral_constant<int, 1>(), own, behind);
-          }
+          ok = make_half(std::integral_constant<int, 0>(), own, behind) &&
+               make_half(std::integral_constant<int, 1>(), own, behind);
         }
         run_done(false);
       }
@@ -745,12 +839,14 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
       const int in = (twin ? 0 : t * tile_rows) + lrow / a.hg, row = run.row0 + in;
       const int pages = run.pages;
       float m_run = -INFINITY, l_run = 0.f;  // the maximum is the row's, the sum that of this warp's keys
+      float o_run = -INFINITY;               // (kBytes) O is relative to 2^o_run
       if (!mbar_wait(&sh.s_full[t], kc & 1, err, 1522 + t)) { ok = false; break; }
       for (int c = 0; c < pages && ok; ++c, ++kc) {
         tc_fence_after();
         float sv[64], mq[2];
         tmem_ld32_max(s_at, *reinterpret_cast<float(*)[32]>(sv), mq[0]);
         tmem_ld32_max(s_at + 32, *reinterpret_cast<float(*)[32]>(sv + 32), mq[1]);
+        const int exps = kBytes ? sh.v_exps[(run.tiles + (twin ? 2 * c + t : c)) % kExps] : 0;  // (there before K was)
         tmem_wait_ld();
         if (kRuns && c >= run.masked) {
           const int seen = run.pos + in + 1 - (run.first + c) * 128 - half * 64;  // keys of this warp's before the row's end
@@ -761,13 +857,19 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
             mq[i & 1] = fmaxf(mq[i & 1], sv[i]);
           }
         }
-        const float m_blk = fmaxf(mq[0], mq[1]) * a.scale_log2;
+        float m_blk = fmaxf(mq[0], mq[1]) * a.scale_log2;
         sh.row_max[t][half][lrow] = m_blk;
-        bool mine = c == 0 || __any_sync(0xffffffffu, m_blk > m_run + kHeadroom);  // this warp calls the other
+        const float top_v = (float)((exps & 255) - 127);  // exponent of the page's largest power of two of V
+        const bool wide = kBytes && (exps & 256);         // and others are far below it
+        bool mine = c == 0 || wide ||  // this warp calls the other
+                    __any_sync(0xffffffffu, kBytes ? m_blk > m_run + kFarScore || m_blk + top_v > o_run + (kTopP + kHeadroom)
+                                                   : m_blk > m_run + kHeadroom);
         float l_add = 0.f;
         auto write_p = [&]() {
           float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
-          const float base = m_run == -INFINITY ? 0.f : m_run;  // (nothing but -infinity so far: exp2(-inf - 0) = 0)
+          // (kBytes: P 2^o_run = p 2^top_v, but no p of l is lost where V is far below what O has)
+          float base = kBytes ? fminf(o_run - top_v, m_blk + kFarScore) : m_run;
+          if ((kBytes ? m_blk : m_run) == -INFINITY) base = 0.f;  // (nothing but -infinity: exp2(-inf - 0) = 0)
           if (kRuns && !kBytes && (!kShared || run.own)) {
             // (stored by fours: both parts of eight pairs at a time do not fit the registers, 32 x 4 rows x 64 heads over 2000
             // tokens 63.5 us, 60)
@@ -800,12 +902,14 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
                 p1 = fast_exp2(p1);
                 if (z & 1) add2(t0, t1, p0, p1);
                 else add2(s0, s1, p0, p1);
-                pk[z] = pack_bf16(p0, p1);
+                pk[z] = kBytes ? pack_f16(p0, p1) : pack_bf16(p0, p1);
               }
               tmem_st8(s_at + 8 * h, pk);
             }
           }
-          l_add = (s0 + s1) + (t0 + t1);
+          const float sum = (s0 + s1) + (t0 + t1);
+          if (!kBytes) l_add = sum;
+          else if (!wide) l_add = sum * (m_blk == -INFINITY ? 0.f : fast_exp2(base - m_run));  // (NaN stays)
         };
         if (!mine) {
           write_p();
@@ -844,10 +948,41 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
         if (redo) {
           if (!warps_sync(&sh.pair[t][quarter], pair_ph, err, 1526 + t)) { ok = false; break; }
           const float m_new = fmaxf(m_blk, sh.row_max[t][half ^ 1][lrow]);
-          const bool need = m_new > m_run + kHeadroom;
-          const float alpha = need ? fast_exp2(m_run - m_new) : 1.f;
-          if (need) m_run = m_new;
-          l_run *= alpha;
+          float alpha;
+          if constexpr (kBytes) {
+            alpha = 1.f;
+            float o_new = m_new + top_v;
+            if (m_new > m_run) {
+              l_run *= fast_exp2(m_run - m_new);
+              m_run = m_new;
+            }
+            if (wide) {
+              // Each key's own power of two goes into its score, and l is summed before: what a token adds to O decides
+              // what its P may lose.
+              int page = ld_in(a.page_table + (size_t)run.seq * a.max_blocks + run.first + c);
+              if (page < 0 || page >= a.num_pages) page = 0;  // (reported)
+              l_add = weigh_scores(s_at, a.scale_log2, m_run, top_v,
+                                   a.V_exp + ((size_t)page * a.G + run.g + (twin ? t : 0)) * 128 + half * 64,
+                                   c >= run.masked ? run.pos + in + 1 - (run.first + c) * 128 - half * 64 : 64);
+              tmem_ld32_max(s_at, *reinterpret_cast<float(*)[32]>(sv), mq[0]);
+              tmem_ld32_max(s_at + 32, *reinterpret_cast<float(*)[32]>(sv + 32), mq[1]);
+              tmem_wait_ld();
+              m_blk = fmaxf(mq[0], mq[1]) * a.scale_log2;  // (now with V's power of two over the page's largest)
+              if (!warps_sync(&sh.pair[t][quarter], pair_ph, err, 1538 + t)) { ok = false; break; }
+              sh.row_max[t][half][lrow] = m_blk;
+              if (!warps_sync(&sh.pair[t][quarter], pair_ph, err, 1540 + t)) { ok = false; break; }
+              o_new = fmaxf(m_blk, sh.row_max[t][half ^ 1][lrow]) + top_v;
+            }
+            if (o_new > o_run + (kTopP + kHeadroom)) {
+              alpha = fast_exp2(o_run - (o_new - kTopP));
+              o_run = o_new - kTopP;
+            }
+          } else {
+            const bool need = m_new > m_run + kHeadroom;
+            alpha = need ? fast_exp2(m_run - m_new) : 1.f;
+            if (need) m_run = m_new;
+            l_run *= alpha;
+          }
           if (c > 0) {
             // O_t to the new maximum: PV_t of the previous page is done (it was issued before this page's S_t)
 #pragma unroll 1
@@ -892,25 +1027,25 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
         for (int i = 0; i < (kBytes ? 2 * kConverters : 1); ++i) odd |= found[i] != 0;
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;  // (a run behind the row's end, or scores of -infinity)
+      const float unit = kBytes && l != 0.f ? fast_exp2(o_run - m_run) : 1.f;
       float* dst = a.part_o + at * 128 + half * 64;
-#pragma unroll(kBytes && kShared ? 1 : 4)
+#pragma unroll(kBytes ? 1 : 4)
       for (int z = 0; z < 4; ++z) {
         float o[16];
         tmem_ld16(o_at + z * 16, o);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] *= inv;
+        for (int i = 0; i < 16; ++i) o[i] = kBytes ? o[i] * inv * unit : o[i] * inv;
         if (odd && valid) {  // infinities and NaN of the own tokens that this row sees, and of this run's
           const int begin = max(run.pos + 1, run.first * 128), end = min(run.pos + in + 1, (run.first + run.pages) * 128);
           for (int k = begin; k < end; ++k) {
             const int page = ld_in(a.page_table + (size_t)run.seq * a.max_blocks + k / 128);
             if (page < 0 || page >= a.num_pages) continue;
             const size_t at = (((size_t)page * a.G + group) * 128 + k % 128) * 128 + half * 64 + z * 16;
-            const uint32_t wide = kBytes && a.V_exp[at >> 7] >= kMostExp ? 0x78u : 0x7fu;  // (kBytes) the first such code
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               if constexpr (kBytes) {
-                if ((static_cast<const uint8_t*>(a.V)[at + i] & 0x7fu) >= wide) o[i] = NAN;
+                if ((static_cast<const uint8_t*>(a.V)[at + i] & 0x7f) == 0x7f) o[i] = NAN;
               } else {
                 const float x = __bfloat162float(static_cast<const __nv_bfloat16*>(a.V)[at + i]);
                 if (!(fabsf(x) < INFINITY)) o[i] += x;

@@ -383,6 +383,11 @@ __host__ __device__ constexpr uint32_t make_idesc_bf16(int M, int N, bool a_mn, 
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// The same with fp16 A/B.
+__host__ __device__ constexpr uint32_t make_idesc_f16(int M, int N, bool a_mn, bool b_mn) {
+  return make_idesc_bf16(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+
 // Instruction descriptor for kind::f8f6f4 with E4M3 A and B (format code 0),
 // K-major operands and an fp32 accumulator.
 __host__ __device__ constexpr uint32_t make_idesc_e4m3(int M, int N) {

@@ -529,9 +529,12 @@ MSA_API msa_status msa_paged_sparse_attn_fp8(const msa_paged_shape *shape, const
                                              const void *q_idx, int32_t *block_idx, void *O, float *LSE, void *workspace,
                                              size_t workspace_bytes, msa_stream_t stream);
 
-/* msa_paged_dense_attn. Made for tokens and few rows a sequence; where there are
- * more, or the prefix is shared by many, probabilities may be rounded to bf16 (O then
- * differs by up to 2^-8 of sum p |v|), which depends on the shape alone. */
+/* msa_paged_dense_attn. Probabilities are multiplied with V in fp16, whatever the
+ * batch's shape: each is off by 2^-11 of itself at most, or, times its page's
+ * largest power of two of V, by 2^-32 of the largest such product in its row where
+ * that is more (in a page whose powers of two lie more than 2^14 apart, times its
+ * own one). A vector of V with the least power of two, 2^-117, may count as zeros
+ * beside larger ones in its page. */
 MSA_API msa_status msa_paged_dense_attn_fp8(const msa_paged_shape *shape, const msa_paged_cache_fp8 *cache, const void *Q,
                                             void *O, float *LSE, void *workspace, size_t workspace_bytes,
                                             msa_stream_t stream);

@@ -1,17 +1,19 @@
 """Calls over a paged cache in 8 bits at the edges of what they take, on the GPU against their 64-bit forms (tests/paged_ref.py
 and tests/paged_fp8_ref.py, bounds derived there)."""
+import math
+
 import numpy as np
 import pytest
 
 import paged_fp8_ref as ref8
 import paged_ref as ref
-from test_paged_fp8_gpu import (DENSE, SCALES, SPARSE, TILES, _all, _check_padding, _check_sparse, _dense, _sparse,  # noqa: F401
+from test_paged_fp8_gpu import (DENSE, SCALES, SHARED, SPARSE, TILES, _all, _check_padding, _check_sparse, _dense, _sparse,  # noqa: F401
                                 msa)
 from test_paged_gpu import _dense as _dense16
 
 pytestmark = pytest.mark.gpu
 
-INF = float("inf")
+NAN, INF = float("nan"), float("inf")
 
 
 # ----------------------------------------------------------------- reading back
@@ -148,28 +150,80 @@ def test_append_and_read_of_the_largest_magnitudes(msa):  # noqa: F811
 
 
 # ----------------------------------------------------------------- probabilities
-@pytest.mark.parametrize("name", [*DENSE, *SCALES])
-def test_probabilities_by_eight_columns_have_eleven_bits(msa, name):  # noqa: F811
-    """Two launches: eight columns at a time, whatever the batch's shape, also where they read a small shared prefix."""
-    b = ref8.Batch(seed=6, **{**DENSE, **SCALES}[name])
-    before = msa.msa_kernel_launches()
+def _check_eleven_bits(b, O, LSE, rows, heads):
+    """ref8.check_attention's bounds, with P's own: fp16, 2^-11 of itself, or half of fp16's last step, 2^-25, in units that the
+    largest P of a row's page was 2^7 in when they were set (128-row tiles; eight columns: 2^15). There V stands relative to
+    its page's largest power of two 2^F, or, where a page's lie more than 2^14 apart, each vector to its own: for a token j
+    that is 2^-32 max(p 2^F) |v_j| / 2^F_j."""
+    import torch
+
+    for r in rows:
+        blocks = list(range(b.row_pos[r] // 128 + 1))
+        at = b.table[b.row_seq[r], blocks].long()
+        token = (torch.arange(len(blocks) * 128) <= b.row_pos[r])
+        own_end = b.row_pos[r] + b.counts[b.row_seq[r]]  # (a page's powers of two are those of all rows' tokens)
+        there = torch.arange(len(blocks) * 128).view(-1, 128) <= own_end
+        for h in heads:
+            g = h // b.hg
+            o, lse, tol, tol_lse = ref.attend(b, r, h, blocks)
+            k, v = (x[at, g].reshape(-1, 128)[token].double() for x in (b.K, b.V))
+            f = b.V_exp[at, g].double() - 127
+            largest = torch.where(there, f, -200.0).amax(1, keepdim=True).expand_as(f)
+            least = torch.where(there & (f > -117), f, 200.0).amin(1, keepdim=True)
+            unit = torch.where(largest - least > 14, f, largest).reshape(-1)[token]
+            p = (k @ b.Q[r, h].double() / math.sqrt(128) - lse).exp()
+            unit, top = torch.exp2(unit), float((p * torch.exp2(largest.reshape(-1)[token])).max())
+            tol = tol + 2.0 ** -11 * (p @ v.abs()) + 2.0 ** -32 * top * (v.abs() / unit[:, None]).sum(0)
+            err = (O[r, h].double() - o).abs()
+            assert bool((err <= tol + 1e-30).all()), (r, h, float((err / (tol + 1e-30)).max()))
+            assert abs(float(LSE[r, h]) - lse) <= tol_lse, (r, h)
+
+
+def _some(b):
+    return range(b.n) if b.n < 30 else range(0, b.n, 7), range(0, b.Hq, 1 if b.Hq <= 8 else 5)
+
+
+@pytest.mark.parametrize("name", [*DENSE, *SCALES, *TILES, *SHARED])
+def test_probabilities_have_eleven_bits(msa, name):  # noqa: F811
+    """By eight columns, by 128-row tiles, behind a prefix that is shared or read as own pages."""
+    b = ref8.Batch(seed=6, **{**DENSE, **SCALES, **TILES, **SHARED}[name])
     O, LSE = _dense(msa, b)
-    if msa.msa_kernel_launches() - before > 2:
-        assert b.prefix or b.N * b.hg > 20 * b.S
-        pytest.skip("128-row tiles")
-    rows = range(b.n) if b.n < 30 else range(0, b.n, 7)
-    ref8.check_attention(b, rows, range(0, b.Hq, 1 if b.Hq <= 8 else 5), O, LSE, _all(b))
+    _check_eleven_bits(b, O, LSE, *_some(b))
     _check_padding(b, O, LSE)
 
 
-@pytest.mark.parametrize("rows", [2, 3])
-def test_up_to_twenty_columns_a_sequence_have_eleven_bits(msa, rows):  # noqa: F811
-    """Without a prefix 128-row tiles take batches of more than 20 columns (rows x heads of a group) a sequence alone."""
-    b = ref8.Batch(counts=[rows] * 20, lens=[1100 + 7 * i for i in range(20)], Hq=64, G=8, seed=6)
-    before = msa.msa_kernel_launches()
+@pytest.mark.parametrize("what", ["spread", "spread a little", "pages", "rising pages", "falling pages", "zeros", "one large vector",
+                                  "half a page large"])
+@pytest.mark.parametrize("name", SCALES)
+def test_eleven_bits_of_values_of_any_powers_of_two(msa, name, what):  # noqa: F811
+    """V's powers of two differ from token to token and from page to page, by more and by less than fp16 holds."""
+    import torch
+
+    def change(b):
+        gen = torch.Generator().manual_seed(5)
+        some = lambda lo, hi, *shape: torch.exp2(torch.randint(lo, hi, shape, generator=gen).float())  # noqa: E731
+        V = b.V.float()
+        if what == "spread":
+            V = V * some(-20, 20, *V.shape[:-1], 1)
+        elif what == "spread a little":
+            V = V * some(-6, 7, *V.shape[:-1], 1)
+        elif what == "pages":
+            V = V * some(-40, 40, V.shape[0], V.shape[1], 1, 1)
+        elif what in ("rising pages", "falling pages"):
+            for s in range(b.S):
+                for c in range(b.prefix if s else 0, -(-b.lens[s] // 128)):
+                    V[int(b.table[s, c])] *= 2.0 ** ((c * 3 if what[0] == "r" else -c * 3) % 90)
+        elif what == "zeros":
+            V[:, :, ::3] = torch.where(V[:, :, ::3].isnan(), NAN, 0.0)
+        elif what == "one large vector":
+            V[:, :, 17] *= 2.0 ** 40
+        else:
+            V[:, :, 64:] *= 2.0 ** 15
+        b.V = V.to(torch.bfloat16)
+
+    b = ref8.Batch(seed=9, change=change, **SCALES[name])
     O, LSE = _dense(msa, b)
-    assert msa.msa_kernel_launches() - before == (2 if rows == 2 else 3)
-    ref8.check_attention(b, range(0, b.n, 7), range(0, 64, 5), O, LSE, _all(b), bf16_p=rows == 3)
+    _check_eleven_bits(b, O, LSE, *_some(b))
 
 
 # ----------------------------------------------------------------- tables as wide as a serving program's
