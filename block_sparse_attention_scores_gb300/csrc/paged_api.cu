@@ -20,8 +20,8 @@ static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // with two pages. 128-row tiles (3 and 0): 300 rows x 32 heads over 4 groups and
 // 8000 tokens 64 us, 84 with one and 93 with eight pages. In 8 bits, where the
 // mma.sync path joins (8 and 8: a page takes half as long, and the items cost less,
-// too): 16 sequences of up to 4099 tokens and 8 groups 26.4 us, 31.4 with six, 29.5
-// with two.
+// too): 16 sequences of up to 4099 tokens and 8 groups, in a graph, 26.4 us, 31.4 with
+// six, 29.5 with two.
 static void cut_pages(long long tiles, int pages, double extra, double join, int* per_split, int* n_splits) {
   tiles = std::max(1LL, tiles);
   pages = std::max(1, pages);

@@ -35,15 +35,17 @@
 //   O'  = sum_j fp16(2^15 exp2(s_j + f_j - w)) V_j',  w = max_j (s_j + f_j)
 //   O   = O' 2^(w - m - 15) / l
 // with e_j, f_j the exponents of token j's K and V. What is summed in O' is thus the
-// part that a token really has in it, at most 1 before the factor 2^15, which lets
-// fp16 hold it down to 2^-39 of the largest: all 2^20 tokens' roundings then stay
-// below 2^-19 of O. P needs no second part (fp16 has eleven bits), and V' no infinities.
+// part that a token really has in it, at most 1 before the factor 2^15. A token's P is
+// off by 2^-11 of itself at most, or by 2^-40 of max (p 2^f) where that is more (half of
+// fp16's last step), which its code, 448 at most, multiplies: O by 2^-11 sum p |v| and
+// 448 * 2^-40 max (p 2^f) for each token, in each dim. P needs no second part (fp16 has
+// eleven bits), and V' no infinities.
 // A page's codes are read as they lie: K by ldmatrix (a lane gets four neighbouring
 // codes of a key, the sum's order over d follows), V by 16-byte loads of four keys'
 // 16 neighbouring dims, paired by key with byte permutes, so that the fragments of
 // the transposed V come without another pass.
-// Measured: 64 rows over 8000 tokens of 8 groups, 729 MB in 120 us, 6.1 TB/s, 0.89
-// of a plain copy; 57 rows x 8 groups x 16 selected pages 46 us with the rows' kernel,
+// Measured: 64 rows over 8000 tokens of 8 groups, 1,057 MB in 171 us, 6.2 TB/s, 0.91
+// of a plain copy; 57 rows x 8 groups x 16 selected pages 44 us with the rows' kernel,
 // of which the memory takes 35 (k = 64: 149 and 142).
 #include "mma_sync.cuh"
 #include "paged_fp8.cuh"

@@ -44,9 +44,9 @@
 //
 // Measured: the shared part of 128 sequences x 2 rows x 32 heads over 128K tokens
 // 385 us on 136 SMs, 1430 TFLOP/s (0.74 of what a library product reaches on all);
-// own pages of 16 x 4 rows x 64 heads over 3000 tokens 50 us, 4.1 TB/s; the whole
-// call for 32 x 4 rows x 64 heads over 2000 tokens 63 us, for 300 rows x 32 heads
-// over 4 groups and 8000 tokens 64 us (610 TFLOP/s, P's second product not counted).
+// the whole call for 16 x 4 rows x 64 heads over 3000 tokens 48 us, 4.1 TB/s, for
+// 32 x 4 rows x 64 heads over 2000 tokens 60 us, for 300 rows x 32 heads over 4 groups
+// and 8000 tokens 62 us (630 TFLOP/s, P's second product not counted).
 //
 // A cache in 8 bits (kBytes, paged_fp8.cuh): the same products of the values that
 // the codes stand for, which bf16 holds exactly. Codes arrive by plain bulk copies,

@@ -330,7 +330,9 @@ MSA_API msa_status msa_dense_bwd(const msa_shape *shape, const void *Q, const vo
  * Values that are not finite, where a row sees them: an infinity in V gives
  * that infinity in O (both signs, or NaN, give NaN), in the dims that have it
  * alone, unless the token's probability is below 2^-100; a NaN score gives NaN
- * in the row's O and LSE.
+ * in the row's O and LSE. Scores s_j are expected below 2^30 in magnitude: full
+ * attention of several rows a sequence may lose rows with larger ones (NaN, or as
+ * if they saw nothing).
  */
 typedef struct msa_paged_shape {
   int32_t S;             /* sequences                                            */
@@ -471,7 +473,8 @@ MSA_API msa_status msa_paged_append_axes(const msa_paged_shape *shape, const msa
 
 /*
  * Serving from a cache in 8 bits: half the bytes of msa_paged_cache, so twice the
- * tokens, and half the time where the memory's speed is what counts.
+ * tokens, and less time for tokens and few rows over long contexts, where the
+ * memory's speed is what counts (full attention of many rows takes as long or longer).
  *
  * Each vector of the cache (a token's K or V of one group, a token's index key) is
  * held as E4M3 codes and one power of two, its exponent + 127 in a byte (E8M0); it
