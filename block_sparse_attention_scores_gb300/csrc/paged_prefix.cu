@@ -83,6 +83,7 @@ constexpr float kFarScore = 60.f; // (kBytes) how far (log2) a page's sum may be
 // (kBytes: 20-23 and 24-27 make tiles of K's and V's codes; 2 looks at V's powers of two, 3 has nothing to do)
 template <bool kBytes>
 constexpr int kThreads = kBytes ? 896 : 640;
+constexpr int kRegisters = 72;    // (kBytes) of a thread as the block starts, the most for so many
 constexpr int kTile = 32768;      // 128 rows x 128 bf16, two 64-column SW128 chunks
 constexpr int kChunk = 16384;
 constexpr int kStages = 2;        // K/V ring
@@ -330,8 +331,8 @@ __global__ void __launch_bounds__(kThreads<kBytes>, 1)
     return (page * a.G + run.g) * 128;
   };
 
-  // (kBytes) The block starts with 72 registers a thread; the warps that make tiles give some of theirs to the softmax.
-  static_assert(!kBytes || 512 * 88 + 128 * (72 + 2 * 40) <= 896 * 72, "registers of a block");
+  // (kBytes) The warps that make tiles give some of their registers to the softmax.
+  static_assert(!kBytes || 512 * 88 + 128 * (kRegisters + 2 * 40) <= 896 * kRegisters, "registers of a block");
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
     tma_prefetch_desc(&map_q);
@@ -1081,6 +1082,12 @@ cudaError_t launch_prefix(const PrefixArgs& a, int blocks, const CUtensorMap& mq
     cudaError_t e =
         cudaFuncSetAttribute(paged_prefix_kernel<kRuns, kShared, kBytes>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<kBytes>);
     if (e != cudaSuccess) return e;
+    if (kBytes) {  // (the softmax's share of the registers comes out of what the block starts with, and would be waited for)
+      cudaFuncAttributes made;
+      e = cudaFuncGetAttributes(&made, paged_prefix_kernel<kRuns, kShared, kBytes>);
+      if (e != cudaSuccess) return e;
+      if (made.numRegs < kRegisters) return cudaErrorInvalidKernelImage;
+    }
     attr[dslot] = true;
   }
   count_launches(1);
